@@ -71,6 +71,7 @@ typedef int ra_status;
 
 #define RA_F32 0
 #define RA_BF16 1
+#define RA_E4M3 2   /* of a key/value cache only: e4m3 values, one power-of-two scale per row */
 
 /* Kernel paths reported by ring_attn_fwd_path / ring_attn_bwd_path. */
 #define RA_PATH_SIMT 1      /* CUDA-core kernels: any shape, f32 or bf16 */
@@ -81,6 +82,7 @@ typedef int ra_status;
 /* Device status bits (ring_attn_device_status). */
 #define RA_DEVICE_TIMEOUT 1u  /* a bounded wait inside a kernel ran out; the kernel stopped */
 #define RA_DEVICE_LAYOUT 2u   /* a kernel found its shared memory misaligned and did nothing */
+#define RA_DEVICE_RANGE 4u    /* a kernel met a length or token count outside its range (see the calls) */
 
 /*
  * ring_attn_fwd -- the whole ring forward in one launch.
@@ -404,6 +406,94 @@ RA_API ra_status ring_attn_ulysses_bwd(const void* q, const void* k, const void*
 RA_API size_t ring_attn_ulysses_bwd_workspace_size(int B, int H, int Hkv, int L, int d, int n_shards, int dtype,
                                                    int grad_dtype);
 
+/*
+ * ring_attn_qk_norm_rope -- the norm of every query and key head, then the rotation by natural
+ * position (ring_attn_rope's), in one pass over both tensors: for a row x of d elements, w the weights
+ * of its kind,
+ *   r = 1 / sqrt(mean(x^2) + eps),   y = R(p) (x r w).
+ *   q [B][H][rows][d], k [B][Hkv][rows][d] (dtype): rows = L, the whole sequence in the layout's order
+ *   (shard = -1), or L / n_shards, one device's rows (shard in [0, n_shards), as ring_attn_block_rope).
+ *   q_strides, k_strides: HOST arrays of three element strides (batch, head, row), each a multiple of
+ *   16 bytes and >= 0 (0 repeats), or NULL for contiguous tensors: slices of a fused projection
+ *   [B][rows][H + 2 Hkv][d] are read where they lie.  d itself is contiguous.
+ *   wq, wk: [d] float32.   q_out, k_out: contiguous, dtype; each may be its own contiguous input.
+ *   positions: [B][rows] int32, 4-byte aligned: the natural position of every token (any int value),
+ *   in place of the layout's; or NULL.
+ *   base > 0 and finite; eps >= 0 and finite; H % Hkv == 0; L and layout as ring_attn_rope; d in {64, 128}.
+ *
+ * ring_attn_qk_norm_rope_bwd -- its gradients.  With g = R(-p) dy and u = g w:
+ *   dw = sum over rows of g x r (float32, summed in a fixed order),  dx = r (u - x r^2 mean(u x)).
+ *   dq_out, dk_out: the gradients of q_out, k_out; dq, dk: those of q, k; all contiguous, dtype (dq may
+ *   be dq_out, dk may be dk_out).  dwq, dwk: [d] float32.
+ *   workspace: DEVICE, 256-byte aligned, at least ring_attn_qk_norm_rope_bwd_workspace_size(d) bytes.
+ */
+RA_API ra_status ring_attn_qk_norm_rope(const void* q, const long long* q_strides, const void* k,
+                                        const long long* k_strides, const float* wq, const float* wk, void* q_out,
+                                        void* k_out, int B, int H, int Hkv, int L, int d, int n_shards, int shard,
+                                        int layout, int dtype, double base, double eps, const int* positions,
+                                        void* stream);
+RA_API ra_status ring_attn_qk_norm_rope_bwd(const void* q, const long long* q_strides, const void* k,
+                                            const long long* k_strides, const float* wq, const float* wk,
+                                            const void* dq_out, const void* dk_out, void* dq, void* dk, float* dwq,
+                                            float* dwk, void* workspace, size_t workspace_bytes, int B, int H, int Hkv,
+                                            int L, int d, int n_shards, int shard, int layout, int dtype, double base,
+                                            double eps, const int* positions, void* stream);
+RA_API size_t ring_attn_qk_norm_rope_bwd_workspace_size(int d);
+
+/*
+ * A key/value cache: k_cache, v_cache [B][Hkv][cap][d], cap rows per sequence and kv head, in the
+ * tensors' dtype (cache_dtype == dtype) or quantised (RA_E4M3).  A quantised row (one token of one kv
+ * head) has one scale 2^e, the smallest with e >= -126 that brings its largest magnitude to at most 448:
+ * element x is held as the e4m3 value nearest to x 2^-e (ties to even) and e as the byte e + 127 in
+ * k_exp, v_exp [B][Hkv][cap].  NaN is held as NaN; a row with an infinite element has e = 120, and its
+ * infinite elements read back as infinite (as do elements within an e4m3 rounding of float32's largest).
+ * k_exp, v_exp are not used, and may be NULL, when the cache is not quantised.
+ * The caller keeps the lengths; nothing in the calls changes them.
+ *
+ * ring_attn_cache_write -- tokens t < ntok[b] of k, v [B][Hkv][T][d] (dtype; strides as in
+ *   ring_attn_qk_norm_rope, NULL = contiguous) to the rows lens[b] + t of sequence b.  lens, ntok: DEVICE
+ *   int32 [B], 4-byte aligned; lens NULL: from row 0; ntok NULL: all T.  Rows that are not written keep
+ *   what they held.  A row outside [0, cap), and every row of a sequence with lens[b] < 0, is not
+ *   written, and RA_DEVICE_RANGE set in the status word; an ntok[b] outside [0, T] is taken as the nearer end of that range, and the bit set.
+ * ring_attn_cache_read -- rows [row0, row0 + rows) of every sequence and kv head to k, v
+ *   [B][Hkv][rows][d] (dtype, contiguous): the values the cache stands for, rounded once to dtype.
+ */
+RA_API ra_status ring_attn_cache_write(const void* k, const long long* k_strides, const void* v,
+                                       const long long* v_strides, void* k_cache, void* v_cache, void* k_exp,
+                                       void* v_exp, const int* lens, const int* ntok, int B, int Hkv, int T, int d,
+                                       int cap, int dtype, int cache_dtype, void* stream);
+RA_API ra_status ring_attn_cache_read(const void* k_cache, const void* v_cache, const void* k_exp, const void* v_exp,
+                                      void* k, void* v, int B, int Hkv, int row0, int rows, int d, int cap, int dtype,
+                                      int cache_dtype, void* stream);
+
+/*
+ * ring_attn_tree_fwd -- attention of T new (drafted) tokens per sequence over a cache: every query of
+ * sequence b sees the prefix, rows [0, lens[b]), and of the step's own tokens, whose keys and values are
+ * the rows lens[b] + j, j < ntok[b] (ring_attn_cache_write puts them there first), those that mask
+ * allows: token t sees token j where mask[b][t][j] != 0.  T = 1 without a mask is the decoding of single
+ * tokens; a tree of drafted tokens has the ancestors of t (itself among them) in row t of the mask.
+ *   q, out: [B][H][T][d]; q in dtype, out in out_dtype (dtype, or RA_F32: the output before rounding);
+ *   lse: [B][H][T] float32.  Query head h reads kv head h / (H / Hkv); the scale is 1/sqrt(d).
+ *   lens: DEVICE int32 [B];  ntok: DEVICE int32 [B], or NULL: T tokens each (both 4-byte aligned).
+ *   mask: DEVICE, [B][T][T] bytes (mask_batched != 0) or one [T][T] for all sequences (0); NULL: j <= t.
+ *   A row that sees nothing, and tokens t >= ntok[b], get out = 0 and lse = -infinity.  What a query does
+ *   not see has no part in its result, whatever it holds (NaN, infinities, rows never written).
+ *   The tokens have to fit: lens[b] + ntok[b] <= cap, both >= 0, ntok[b] <= T.  Otherwise lens[b] is taken
+ *   as the nearest value in [0, cap], then ntok[b] as the nearest in [0, min(T, cap - lens[b])], and
+ *   RA_DEVICE_RANGE is set in the status word.
+ *   Prefixes in parts (a cache sharded over devices): out in float32 and lse of each part fold together
+ *   with ring_attn_lse_merge; parts that do not hold the step's tokens take a mask of zeros.
+ *   workspace: DEVICE, 256-byte aligned, at least ring_attn_tree_fwd_workspace_size(...) bytes.  Its contents
+ *   do not matter; calls whose GPU work overlaps (other streams, two graphs at once) need one each.
+ *   The result does not vary from run to run.
+ */
+RA_API ra_status ring_attn_tree_fwd(const void* q, const void* k_cache, const void* v_cache, const void* k_exp,
+                                    const void* v_exp, const int* lens, const int* ntok, const unsigned char* mask,
+                                    int mask_batched, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                    int B, int H, int Hkv, int T, int d, int cap, int dtype, int cache_dtype,
+                                    int out_dtype, void* stream);
+RA_API size_t ring_attn_tree_fwd_workspace_size(int B, int H, int Hkv, int T, int d, int cap, int dtype, int cache_dtype);
+
 /* Which kernel path ring_attn_fwd / ring_attn_bwd take for these arguments (RA_PATH_*), written
  * to *path (HOST pointer).  Same argument checks as the calls themselves; no CUDA call. */
 RA_API ra_status ring_attn_fwd_path(int B, int H, int Hkv, int L, int d, int n_shards, int causal,
@@ -443,7 +533,8 @@ RA_API ra_status ring_attn_device_status(unsigned int* status, void* stream);
  * ring_attn_device_check -- ring_attn_device_status as a status code: synchronises `stream`, reads
  * and clears the word, and returns RA_ERR_TIMEOUT if a bounded wait inside a kernel ran out (that
  * kernel stopped early: its outputs are incomplete and must not be used), RA_ERR_CUDA if a kernel
- * found its shared memory misaligned and did nothing, RA_OK if the word was clear.
+ * found its shared memory misaligned and did nothing, RA_ERR_INVALID_ARG if a kernel met a length or
+ * token count outside its range, RA_OK if the word was clear.
  */
 RA_API ra_status ring_attn_device_check(void* stream);
 

@@ -6,8 +6,12 @@ call does, and fails loudly if the library has not been built (``python -c "impo
 __graft_entry__ as g; g.build()"``).
 """
 from .binding import (  # noqa: F401
+    KVCache,
     RingAttnError,
     bwd_workspace_size,
+    cache_alloc,
+    cache_read,
+    cache_write,
     device_check,
     device_status,
     fwd,
@@ -31,14 +35,18 @@ from .binding import (  # noqa: F401
     f32_zero,
     library,
     lse_merge,
+    qk_norm_rope,
+    qk_norm_rope_bwd,
     ring_step_fwd,
     ring_step_fwd_accumulate,
     rope,
     selftest_bounded_wait,
     shard_tiles,
+    tree_fwd,
+    tree_workspace_size,
     ulysses_a2a,
     ulysses_bwd,
     ulysses_fwd,
 )
-from .autograd import ring_attention  # noqa: F401
+from .autograd import ring_attention, ring_qk_norm_rope  # noqa: F401
 from .ring import RingAttention, ring_attention_distributed  # noqa: F401

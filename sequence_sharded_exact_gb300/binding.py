@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -20,6 +21,8 @@ LAYOUTS = {"contiguous": 0, "zigzag": 1, "striped": 2}
 PATHS = {1: "simt", 2: "tcgen05"}
 RA_DEVICE_TIMEOUT = 1
 RA_DEVICE_LAYOUT = 2
+RA_DEVICE_RANGE = 4
+RA_E4M3 = 2
 
 _lock = threading.Lock()
 _lib = None
@@ -36,7 +39,9 @@ EXPORTS = (
     "ring_attn_fwd_host_workspace_size", "ring_attn_selftest_bounded_wait", "ring_attn_device_check",
     "ring_attn_block_fwd", "ring_attn_block_bwd", "ring_attn_bwd_preprocess", "ring_attn_f32_zero",
     "ring_attn_f32_add", "ring_attn_f32_convert", "ring_attn_block_rope", "ring_attn_fwd_f32out",
-    "ring_attn_bwd_f32out", "ring_attn_bwd_preprocess_f32out",
+    "ring_attn_bwd_f32out", "ring_attn_bwd_preprocess_f32out", "ring_attn_qk_norm_rope",
+    "ring_attn_qk_norm_rope_bwd", "ring_attn_qk_norm_rope_bwd_workspace_size", "ring_attn_cache_write",
+    "ring_attn_cache_read", "ring_attn_tree_fwd", "ring_attn_tree_fwd_workspace_size",
 )
 
 
@@ -123,6 +128,21 @@ def library():
         lib.ring_attn_ring_step_fwd_accumulate.restype = ctypes.c_int
         lib.ring_attn_bwd_static_scratch_capacity.argtypes = []
         lib.ring_attn_bwd_static_scratch_capacity.restype = SZ
+        D = ctypes.c_double
+        lib.ring_attn_qk_norm_rope.argtypes = [P] * 8 + [I] * 9 + [D, D, P, P]
+        lib.ring_attn_qk_norm_rope.restype = ctypes.c_int
+        lib.ring_attn_qk_norm_rope_bwd.argtypes = [P] * 13 + [SZ] + [I] * 9 + [D, D, P, P]
+        lib.ring_attn_qk_norm_rope_bwd.restype = ctypes.c_int
+        lib.ring_attn_qk_norm_rope_bwd_workspace_size.argtypes = [I]
+        lib.ring_attn_qk_norm_rope_bwd_workspace_size.restype = SZ
+        lib.ring_attn_cache_write.argtypes = [P] * 10 + [I] * 7 + [P]
+        lib.ring_attn_cache_write.restype = ctypes.c_int
+        lib.ring_attn_cache_read.argtypes = [P] * 6 + [I] * 8 + [P]
+        lib.ring_attn_cache_read.restype = ctypes.c_int
+        lib.ring_attn_tree_fwd.argtypes = [P] * 8 + [I] + [P] * 3 + [SZ] + [I] * 9 + [P]
+        lib.ring_attn_tree_fwd.restype = ctypes.c_int
+        lib.ring_attn_tree_fwd_workspace_size.argtypes = [I] * 8
+        lib.ring_attn_tree_fwd_workspace_size.restype = SZ
         for name in EXPORTS:
             f = getattr(lib, name)
             if f.restype is ctypes.c_int or name in ("ring_attn_fwd", "ring_attn_ring_step_fwd",
@@ -703,3 +723,262 @@ def block_rope(x, n_shards, shard, layout="zigzag", base=10000.0, inverse=False,
                                           _dtype_code(x.dtype), float(base), int(bool(inverse)),
                                           _stream(stream, x.device)))
     return x
+
+
+# ------------------------------------------------------------------------------------------------
+# Norms and rotation of queries and keys, the key/value cache and the attention over it
+# ------------------------------------------------------------------------------------------------
+def _on(device, call, *args):
+    """Calls the library with `device` current: a kernel is launched on the device of its tensors."""
+    if torch.cuda.current_device() == device.index:
+        _check(call(*args))
+    else:
+        with torch.cuda.device(device):
+            _check(call(*args))
+
+
+def _need_rows(t, name, device, shape, dtype):
+    """A tensor read by strides: any [B, heads, rows, d] whose rows are contiguous and lie on 16-byte
+    boundaries.  Returns its (batch, head, row) element strides, or None if it is contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.is_contiguous():
+        return None
+    per = 16 // t.element_size()
+    strides = t.stride()
+    if strides[3] != 1 or any(n > 1 and s % per for n, s in zip(shape[:3], strides)):
+        raise ValueError(f"{name} must have contiguous rows on 16-byte boundaries")
+    return (ctypes.c_longlong * 3)(*strides[:3])
+
+
+def as_rows(t):
+    """t, or a contiguous copy if its rows cannot be read where they lie."""
+    per = 16 // t.element_size()
+    if t.dim() == 4 and t.stride(3) == 1 and not any(n > 1 and s % per for n, s in zip(t.shape, t.stride()[:3])) \
+            and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _rows_dims(q, k, name="q"):
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor):
+        raise TypeError("the inputs must be torch tensors")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"{name} must be [B, heads, rows, d]")
+    _dtype_code(q.dtype)
+    return tuple(q.shape) + (k.shape[1],)
+
+
+def _norm_rope_args(q, k, wq, wk, n_shards, layout, base, eps, shard, positions):
+    B, H, rows, d, Hkv = _rows_dims(q, k, "q and k")
+    dev = q.device
+    qs = _need_rows(q, "q", dev, (B, H, rows, d), q.dtype)
+    ks = _need_rows(k, "k", dev, (B, Hkv, rows, d), q.dtype)
+    _need(wq, "wq", dev, (d,), torch.float32)
+    _need(wk, "wk", dev, (d,), torch.float32)
+    n = int(n_shards)
+    if positions is not None:
+        _need(positions, "positions", dev, (B, rows), torch.int32)
+        if shard is not None or n != 1:
+            raise ValueError("positions stand in place of a layout: n_shards must be 1 and shard None")
+    if shard is not None and not 0 <= int(shard) < n:
+        raise ValueError("shard must lie in [0, n_shards)")
+    L = rows if shard is None else n * rows
+    tail = (B, H, Hkv, L, d, n, -1 if shard is None else int(shard),
+            LAYOUTS["contiguous"] if positions is not None else _layout(layout), _dtype_code(q.dtype), float(base), float(eps),
+            None if positions is None else positions.data_ptr())
+    return qs, ks, tail
+
+
+def qk_norm_rope(q, k, wq, wk, n_shards=1, layout="contiguous", base=10000.0, eps=1e-6, shard=None, positions=None,
+                 q_out=None, k_out=None, stream=None):
+    """ring_attn_qk_norm_rope: every head of q [B,H,rows,d] and k [B,Hkv,rows,d] divided by its root mean square
+    (eps added to the mean square), times wq or wk [d] float32, then rotated by its natural position -- the
+    layout's over n_shards shards, shard `shard`'s of them, or positions [B, rows] int32.  q and k may be
+    slices of a fused projection (rows contiguous, on 16-byte boundaries).  Returns (q_out, k_out), contiguous,
+    in q's dtype; q_out may be q and k_out may be k, where those are contiguous."""
+    qs, ks, tail = _norm_rope_args(q, k, wq, wk, n_shards, layout, base, eps, shard, positions)
+    dev = q.device
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    else:
+        _need(q_out, "q_out", dev, q.shape, q.dtype)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    else:
+        _need(k_out, "k_out", dev, k.shape, q.dtype)
+    _on(dev, library().ring_attn_qk_norm_rope, q.data_ptr(), qs, k.data_ptr(), ks, wq.data_ptr(), wk.data_ptr(),
+        q_out.data_ptr(), k_out.data_ptr(), *tail, _stream(stream, dev))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, wq, wk, dq_out, dk_out, n_shards=1, layout="contiguous", base=10000.0, eps=1e-6, shard=None,
+                     positions=None, dq=None, dk=None, workspace=None, stream=None):
+    """ring_attn_qk_norm_rope_bwd: the gradients of qk_norm_rope's inputs from those of its outputs (contiguous).
+    Returns (dq, dk) in q's dtype, contiguous (dq may be dq_out, dk may be dk_out), and (dwq, dwk) [d] float32."""
+    qs, ks, tail = _norm_rope_args(q, k, wq, wk, n_shards, layout, base, eps, shard, positions)
+    dev = q.device
+    _need(dq_out, "dq_out", dev, q.shape, q.dtype)
+    _need(dk_out, "dk_out", dev, k.shape, q.dtype)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    else:
+        _need(dq, "dq", dev, q.shape, q.dtype)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    else:
+        _need(dk, "dk", dev, k.shape, q.dtype)
+    d = q.shape[3]
+    dwq = torch.empty(d, dtype=torch.float32, device=dev)
+    dwk = torch.empty(d, dtype=torch.float32, device=dev)
+    need = int(library().ring_attn_qk_norm_rope_bwd_workspace_size(d))
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _need_workspace(workspace, need, dev)
+    _on(dev, library().ring_attn_qk_norm_rope_bwd, q.data_ptr(), qs, k.data_ptr(), ks, wq.data_ptr(), wk.data_ptr(),
+        dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dwq.data_ptr(), dwk.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), *tail, _stream(stream, dev))
+    return dq, dk, dwq, dwk
+
+
+class KVCache(NamedTuple):
+    """A key/value cache: k, v [B, Hkv, cap, d], bfloat16 or float32 like the tensors written to it, or
+    float8_e4m3fn with the rows' exponents + 127 in k_exp, v_exp [B, Hkv, cap] uint8 (an element stands for
+    its e4m3 value times 2^(byte - 127)).  The caller keeps the lengths."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_exp: Optional[torch.Tensor] = None
+    v_exp: Optional[torch.Tensor] = None
+
+
+def cache_alloc(B, Hkv, cap, d, dtype=torch.float8_e4m3fn, device=None):
+    """A KVCache of zeros: dtype float8_e4m3fn (quantised as it is written), bfloat16 or float32."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    _cache_code(dtype)
+    k, v = (torch.zeros((B, Hkv, cap, d), dtype=dtype, device=dev) for _ in range(2))
+    if dtype != torch.float8_e4m3fn:
+        return KVCache(k, v)
+    return KVCache(k, v, *(torch.zeros((B, Hkv, cap), dtype=torch.uint8, device=dev) for _ in range(2)))
+
+
+def _cache_code(dtype):
+    return RA_E4M3 if dtype == torch.float8_e4m3fn else _dtype_code(dtype)
+
+
+def _need_cache(cache, device, B, Hkv, d, dtype):
+    """Checks a cache against the tensors it is used with; returns its arguments (pointers) and (cap, code)."""
+    k, v, ke, ve = cache
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("the cache's k must be a [B, Hkv, cap, d] tensor")
+    cap = k.shape[2]
+    shape = (B, Hkv, cap, d)
+    code = _cache_code(k.dtype)
+    if code != RA_E4M3 and k.dtype != dtype:
+        raise ValueError(f"the cache must hold {dtype} or float8_e4m3fn, not {k.dtype}")
+    _need(k, "the cache's k", device, shape)
+    _need(v, "the cache's v", device, shape, k.dtype)
+    if code != RA_E4M3:
+        return (k.data_ptr(), v.data_ptr(), None, None), cap, code
+    _need(ke, "the cache's k_exp", device, shape[:3], torch.uint8)
+    _need(ve, "the cache's v_exp", device, shape[:3], torch.uint8)
+    return (k.data_ptr(), v.data_ptr(), ke.data_ptr(), ve.data_ptr()), cap, code
+
+
+def _need_lengths(t, name, device, B, optional=True):
+    if t is None:
+        if not optional:
+            raise ValueError(f"{name} is required")
+        return None
+    _need(t, name, device, (B,), torch.int32)
+    return t.data_ptr()
+
+
+def cache_write(cache, k, v, lens=None, ntok=None, stream=None):
+    """ring_attn_cache_write: tokens t < ntok[b] (all T without ntok) of k and v [B, Hkv, T, d] to the rows
+    lens[b] + t (t without lens) of the cache, quantised there if it is float8_e4m3fn.  lens, ntok: int32 [B] on
+    the device.  k and v may be slices of a fused projection.  Rows outside the cache are not written (the
+    device status word then has the range bit).  Returns the cache."""
+    B, Hkv, T, d, _ = _rows_dims(k, v, "k and v")
+    dev = k.device
+    ks = _need_rows(k, "k", dev, (B, Hkv, T, d), k.dtype)
+    vs = _need_rows(v, "v", dev, (B, Hkv, T, d), k.dtype)
+    ptrs, cap, code = _need_cache(cache, dev, B, Hkv, d, k.dtype)
+    _on(dev, library().ring_attn_cache_write, k.data_ptr(), ks, v.data_ptr(), vs, *ptrs, _need_lengths(lens, "lens", dev, B),
+        _need_lengths(ntok, "ntok", dev, B), B, Hkv, T, d, cap, _dtype_code(k.dtype), code, _stream(stream, dev))
+    return cache
+
+
+def cache_read(cache, rows, row0=0, dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """ring_attn_cache_read: rows [row0, row0 + rows) of every sequence and kv head as (k, v) [B, Hkv, rows, d] in
+    dtype: the values the cache stands for."""
+    if not isinstance(cache.k, torch.Tensor) or cache.k.dim() != 4:
+        raise ValueError("the cache's k must be a [B, Hkv, cap, d] tensor")
+    B, Hkv, _, d = cache.k.shape
+    dev = cache.k.device
+    code_out = _dtype_code(dtype)
+    ptrs, cap, code = _need_cache(cache, dev, B, Hkv, d, dtype)
+    rows, row0 = int(rows), int(row0)
+    if rows < 0 or row0 < 0 or row0 + rows > cap:
+        raise ValueError(f"rows [{row0}, {row0 + rows}) lie outside the cache ({cap} rows)")
+    shape = (B, Hkv, rows, d)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=dev)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=dev)
+    _need(k, "k", dev, shape, dtype)
+    _need(v, "v", dev, shape, dtype)
+    _on(dev, library().ring_attn_cache_read, *ptrs, k.data_ptr(), v.data_ptr(), B, Hkv, row0, rows, d, cap, code_out, code,
+        _stream(stream, dev))
+    return k, v
+
+
+def tree_workspace_size(B, H, Hkv, T, d, cap, dtype, cache_dtype):
+    return int(library().ring_attn_tree_fwd_workspace_size(B, H, Hkv, T, d, cap, _dtype_code(dtype), _cache_code(cache_dtype)))
+
+
+def tree_fwd(q, cache, lens, mask=None, ntok=None, out_dtype=None, out=None, lse=None, workspace=None, stream=None):
+    """ring_attn_tree_fwd: attention of T new tokens per sequence, q [B, H, T, d], over a cache that already holds
+    their keys and values in the rows lens[b] + t (cache_write): token t of sequence b sees the prefix, rows
+    [0, lens[b]), and the step's tokens j < ntok[b] with mask[b, t, j] ([B, T, T] or [T, T] bool; without a mask
+    j <= t).  lens, ntok: int32 [B] on the device.  Returns (out [B, H, T, d] in out_dtype -- q's, or float32 --
+    and lse [B, H, T] float32); a row that sees nothing, and tokens t >= ntok[b], have 0 and -infinity."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B, H, T, d] tensor")
+    if not isinstance(cache.k, torch.Tensor) or cache.k.dim() != 4:
+        raise ValueError("the cache's k must be a [B, Hkv, cap, d] tensor")
+    B, H, T, d = q.shape
+    Hkv, dev = cache.k.shape[1], q.device
+    _need(q, "q", dev)
+    code_q = _dtype_code(q.dtype)
+    ptrs, cap, code = _need_cache(cache, dev, B, Hkv, d, q.dtype)
+    out_dtype = q.dtype if out_dtype is None else out_dtype
+    if out_dtype not in (q.dtype, torch.float32):
+        raise ValueError("out_dtype must be q's dtype or float32")
+    mask_ptr, batched = None, 0
+    if mask is not None:
+        batched = int(isinstance(mask, torch.Tensor) and mask.dim() == 3)
+        _need(mask, "mask", dev, (B, T, T) if batched else (T, T), torch.bool)
+        mask_ptr = mask.data_ptr()
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+    else:
+        _need(out, "out", dev, q.shape, out_dtype)
+    if lse is None:
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=dev)
+    else:
+        _need(lse, "lse", dev, (B, H, T), torch.float32)
+    need = int(library().ring_attn_tree_fwd_workspace_size(B, H, Hkv, T, d, cap, code_q, code))
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    else:
+        _need_workspace(workspace, need, dev)
+    _on(dev, library().ring_attn_tree_fwd, q.data_ptr(), *ptrs, _need_lengths(lens, "lens", dev, B, optional=False),
+        _need_lengths(ntok, "ntok", dev, B), mask_ptr, batched, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), B, H, Hkv, T, d, cap, code_q, code, _dtype_code(out_dtype), _stream(stream, dev))
+    return out, lse

@@ -21,6 +21,8 @@ namespace {
 
 thread_local std::string g_last_error;
 
+}  // namespace
+
 ra_status fail(ra_status st, const char* fmt, ...)
 {
     char buf[512];
@@ -36,6 +38,8 @@ ra_status cuda_fail(cudaError_t e, const char* what)
 {
     return fail(RA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -53,6 +57,8 @@ int current_device()
     if (cudaGetDevice(&dev) != cudaSuccess) return -1;
     return dev;
 }
+
+}  // namespace
 
 // Device address of the status word for the current device (looked up once per device).
 unsigned int* status_word(cudaError_t* err)
@@ -119,6 +125,8 @@ ra_status check_ptrs(std::initializer_list<const void*> ptrs)
     }
     return RA_OK;
 }
+
+namespace {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -912,6 +920,8 @@ ra_status ring_attn_device_check(void* stream)
                     "incomplete (status word 0x%x)", st);
     if (st & RA_DEVICE_LAYOUT)
         return fail(RA_ERR_CUDA, "a kernel found its shared memory misaligned and did nothing (status word 0x%x)", st);
+    if (st & RA_DEVICE_RANGE)
+        return fail(RA_ERR_INVALID_ARG, "a kernel met a sequence length or token count outside its range (status word 0x%x)", st);
     return RA_OK;
 }
 

@@ -1,0 +1,299 @@
+// cache.cu -- the key/value cache: rows quantised as they are written, and read back (HBM-bound).
+//
+// A cache holds k and v as [B][Hkv][cap][d] in the model's dtype, or in e4m3 with one power-of-two
+// scale per row (one token of one kv head): the smallest 2^e, e >= -126, with amax <= 448 * 2^e (448
+// is e4m3's largest value), stored as the byte e + 127.  Element x is stored as the e4m3 value
+// nearest to x 2^-e (ties to even) and stands for that value times 2^e.  A power of two costs no
+// accuracy against amax / 448 as the scale (e4m3 is a floating-point format: only the range below
+// its smallest normal value moves, by less than a binade) and keeps the scaling and the reading back
+// exact: the row's rounding is the conversion to e4m3 alone, at most 2^-4 of an element that is a
+// normal e4m3 value after scaling.  amax passes over NaN, which is stored as NaN; an infinite amax
+// takes e = 120, under which 448 * 2^e reads back as infinity.
+//
+// What bounds it: each element is read once and written once.  d / 8 lanes hold a row (8 elements a
+// lane: 16 or 32 bytes in, 8 out, or the reverse), its largest magnitude is a shuffle reduction in
+// that group, and kUnroll rows are loaded before the first is used.
+#include <cuda_bf16.h>
+
+#include "ra_internal.h"
+#include "ra_ptx.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
+
+template <typename T>
+struct Eight {  // eight consecutive elements of T
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p)
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ void store(T* p) const
+    {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const;
+    __device__ __forceinline__ void set(const float (&f)[8]);
+};
+
+template <>
+__device__ __forceinline__ void Eight<float>::get(float (&f)[8]) const
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        f[4 * i] = __uint_as_float(v[i].x);
+        f[4 * i + 1] = __uint_as_float(v[i].y);
+        f[4 * i + 2] = __uint_as_float(v[i].z);
+        f[4 * i + 3] = __uint_as_float(v[i].w);
+    }
+}
+template <>
+__device__ __forceinline__ void Eight<float>::set(const float (&f)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        v[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
+                          __float_as_uint(f[4 * i + 3]));
+}
+template <>
+__device__ __forceinline__ void Eight<__nv_bfloat16>::get(float (&f)[8]) const
+{
+    const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+template <>
+__device__ __forceinline__ void Eight<__nv_bfloat16>::set(const float (&f)[8])
+{
+    v[0] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+// The row's exponent from its largest magnitude, by its bits: amax = 1.f * 2^E, 448 = 1.75 * 2^8.
+__device__ __forceinline__ int row_exponent(float amax)
+{
+    const uint32_t bits = __float_as_uint(amax);
+    const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return e < -126 ? -126 : (e > 120 ? 120 : e);
+}
+
+struct WriteArgs {
+    int B, Hkv, T, cap;
+    const void* x[2];                // k, v
+    long long s[2][3];               // their element strides: batch, head, row
+    void* values[2];
+    uint8_t* exps[2];                // null: the cache holds the inputs' dtype
+    const int *lens, *ntok;          // either may be null: 0, T
+    unsigned int* status;
+};
+
+// Where token t of sequence b goes, or -1: not one of its tokens, or outside the cache.
+__device__ __forceinline__ long long write_row(const WriteArgs& a, int b, int t)
+{
+    if (a.ntok) {
+        const int n = a.ntok[b];
+        if (t == 0 && (n < 0 || n > a.T)) atomicOr(a.status, kStatusRange);
+        if (t >= n) return -1;
+    }
+    const long long row = (a.lens ? a.lens[b] : 0) + (long long)t;
+    if (row >= t && row < a.cap) return row;
+    atomicOr(a.status, kStatusRange);
+    return -1;
+}
+
+template <typename T, int D, bool QUANT>
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteArgs a)
+{
+    constexpr int LPR = D / 8, kGroups = kThreads / LPR;
+    const int ch = threadIdx.x % LPR;
+    const unsigned mask = ((1u << LPR) - 1u) << (threadIdx.x & 31 & ~(LPR - 1));
+    const long long half = (long long)a.B * a.Hkv * a.T, total = 2 * half;
+    const long long step = (long long)gridDim.x * kGroups;
+    const long long first = (long long)blockIdx.x * kGroups + threadIdx.x / LPR;
+    for (long long base = first; base < total; base += step * kUnroll) {
+        Eight<T> x[kUnroll];
+        long long dst[kUnroll];  // cache row, all heads counted; -1: nothing to write
+        int kind[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const long long idx = base + u * step;
+            dst[u] = -1;
+            kind[u] = 0;
+            if (idx >= total) continue;
+            kind[u] = idx >= half;
+            const long long i = idx - (kind[u] ? half : 0);
+            const int t = (int)(i % a.T);
+            const long long bh = i / a.T;
+            const int b = (int)(bh / a.Hkv), h = (int)(bh % a.Hkv);
+            const long long row = write_row(a, b, t);
+            if (row < 0) continue;
+            dst[u] = bh * a.cap + row;
+            const long long* s = a.s[kind[u]];
+            x[u].load(static_cast<const T*>(a.x[kind[u]]) + b * s[0] + h * s[1] + t * s[2] + ch * 8);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (dst[u] < 0) continue;  // the same for every lane of a row
+            if constexpr (!QUANT) {
+                x[u].store(static_cast<T*>(a.values[kind[u]]) + dst[u] * D + ch * 8);
+            } else {
+                float f[8], m = 0.f;
+                x[u].get(f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
+                const int e = row_exponent(m);
+                const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
+                uint2 w;
+                w.x = (uint32_t)e4m3x2(f[0] * down, f[1] * down) | (uint32_t)e4m3x2(f[2] * down, f[3] * down) << 16;
+                w.y = (uint32_t)e4m3x2(f[4] * down, f[5] * down) | (uint32_t)e4m3x2(f[6] * down, f[7] * down) << 16;
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.values[kind[u]]) + dst[u] * D + ch * 8) = w;
+                if (ch == 0) a.exps[kind[u]][dst[u]] = (uint8_t)(e + 127);
+            }
+        }
+    }
+}
+
+struct ReadArgs {
+    int B, Hkv, cap, row0, rows;
+    const void* values[2];
+    const uint8_t* exps[2];
+    void* out[2];
+};
+
+template <typename T, int D, bool QUANT>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a)
+{
+    constexpr int LPR = D / 8, kGroups = kThreads / LPR;
+    const int ch = threadIdx.x % LPR;
+    const long long half = (long long)a.B * a.Hkv * a.rows, total = 2 * half;
+    const long long step = (long long)gridDim.x * kGroups;
+    const long long first = (long long)blockIdx.x * kGroups + threadIdx.x / LPR;
+    for (long long base = first; base < total; base += step * kUnroll) {
+        Eight<T> x[kUnroll];
+        uint2 w[kUnroll];
+        uint32_t e[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const long long idx = base + u * step;
+            if (idx >= total) continue;
+            const int kind = idx >= half;
+            const long long i = idx - (kind ? half : 0);
+            const long long src = i / a.rows * a.cap + a.row0 + i % a.rows;
+            if constexpr (QUANT) {
+                w[u] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.values[kind]) + src * D + ch * 8);
+                e[u] = a.exps[kind][src];
+            } else {
+                x[u].load(static_cast<const T*>(a.values[kind]) + src * D + ch * 8);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const long long idx = base + u * step;
+            if (idx >= total) continue;
+            const int kind = idx >= half;
+            const long long i = idx - (kind ? half : 0);
+            if constexpr (QUANT) {
+                const float up = __uint_as_float(e[u] << 23);  // 2^(byte - 127), byte 1 .. 247
+                float f[8];
+                e4m3x4_to_float(w[u].x, f[0], f[1], f[2], f[3]);
+                e4m3x4_to_float(w[u].y, f[4], f[5], f[6], f[7]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] *= up;
+                x[u].set(f);
+            }
+            x[u].store(static_cast<T*>(a.out[kind]) + i * D + ch * 8);
+        }
+    }
+}
+
+// Blocks for `rows` rows of d elements: enough for all, at most eight resident on every SM.
+unsigned cache_grid(long long rows, int d)
+{
+    const long long per = (long long)(kThreads / (d / 8)) * kUnroll;
+    const long long want = (rows + per - 1) / per, cap = (long long)device_sm_count() * 8;
+    return (unsigned)(want < cap ? (want < 1 ? 1 : want) : cap);
+}
+
+template <typename T, int D>
+void write_as(const WriteArgs& a, bool quant, unsigned grid, cudaStream_t s)
+{
+    if (quant)
+        cache_write_kernel<T, D, true><<<grid, kThreads, 0, s>>>(a);
+    else
+        cache_write_kernel<T, D, false><<<grid, kThreads, 0, s>>>(a);
+}
+
+template <typename T, int D>
+void read_as(const ReadArgs& a, bool quant, unsigned grid, cudaStream_t s)
+{
+    if (quant)
+        cache_read_kernel<T, D, true><<<grid, kThreads, 0, s>>>(a);
+    else
+        cache_read_kernel<T, D, false><<<grid, kThreads, 0, s>>>(a);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const Cache& c, int T, const void* k, const long long* ks, const void* v, const long long* vs,
+                               const int* lens, const int* ntok, int dtype, unsigned int* status, cudaStream_t s)
+{
+    WriteArgs a;
+    a.B = c.B;
+    a.Hkv = c.Hkv;
+    a.T = T;
+    a.cap = c.cap;
+    a.x[0] = k;
+    a.x[1] = v;
+    for (int i = 0; i < 3; ++i) {
+        a.s[0][i] = ks[i];
+        a.s[1][i] = vs[i];
+    }
+    a.values[0] = c.k;
+    a.values[1] = c.v;
+    a.exps[0] = c.k_exp;
+    a.exps[1] = c.v_exp;
+    a.lens = lens;
+    a.ntok = ntok;
+    a.status = status;
+    const bool quant = c.dtype != dtype;
+    const unsigned grid = cache_grid(2LL * c.B * c.Hkv * T, c.d);
+    if (dtype == 1)
+        c.d == 128 ? write_as<__nv_bfloat16, 128>(a, quant, grid, s) : write_as<__nv_bfloat16, 64>(a, quant, grid, s);
+    else
+        c.d == 128 ? write_as<float, 128>(a, quant, grid, s) : write_as<float, 64>(a, quant, grid, s);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_read(const Cache& c, int row0, int rows, void* k, void* v, int dtype, cudaStream_t s)
+{
+    ReadArgs a;
+    a.B = c.B;
+    a.Hkv = c.Hkv;
+    a.cap = c.cap;
+    a.row0 = row0;
+    a.rows = rows;
+    a.values[0] = c.k;
+    a.values[1] = c.v;
+    a.exps[0] = c.k_exp;
+    a.exps[1] = c.v_exp;
+    a.out[0] = k;
+    a.out[1] = v;
+    const bool quant = c.dtype != dtype;
+    const unsigned grid = cache_grid(2LL * c.B * c.Hkv * rows, c.d);
+    if (dtype == 1)
+        c.d == 128 ? read_as<__nv_bfloat16, 128>(a, quant, grid, s) : read_as<__nv_bfloat16, 64>(a, quant, grid, s);
+    else
+        c.d == 128 ? read_as<float, 128>(a, quant, grid, s) : read_as<float, 64>(a, quant, grid, s);
+    return cudaGetLastError();
+}
+
+}  // namespace ra

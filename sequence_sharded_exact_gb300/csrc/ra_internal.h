@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "ra_geometry.h"
 
 namespace ra {
@@ -22,6 +24,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // bits of the device status word (the ABI's RA_DEVICE_* values; api.cu checks they agree)
 constexpr unsigned kStatusTimeout = 1u;
 constexpr unsigned kStatusLayout = 2u;
+constexpr unsigned kStatusRange = 4u;
 
 // One device's block call (the per-device data path of the multi-device ring): the query rows are
 // those of shard q_shard alone and the keys those of shard kv_shard alone, each in a local buffer
@@ -75,6 +78,53 @@ cudaError_t launch_bwd_tc(const Problem& p, const void* q, const void* k, const 
 // Rotary position embedding by natural position, in place, of a [B][H][L][d] buffer (p.H heads),
 // or (shard >= 0) of one device's [B][H][L/n][d] buffer holding shard `shard`'s rows.
 cudaError_t launch_rope(const Problem& p, void* x, double base, int inverse, cudaStream_t s, int shard = -1);
+// theta_i / (2 pi) for theta_i = base^(-2i/d), i < d / 2, in units of 2^-64 turn (0 behind them).
+void rope_turns(double base, int d, unsigned long long (&turn)[64]);
+
+// Norm of every query and key head, then the rotation (dyq null), or the gradients of that.
+struct NormRope {
+    const void *q, *k;          // [B][heads][rows][d] by element strides (batch, head, row), d contiguous
+    long long q_strides[3], k_strides[3];
+    const float *wq, *wk;       // [d]
+    const void *dyq, *dyk;      // backward: gradients of the outputs, contiguous
+    void *out_q, *out_k;        // outputs, or dq and dk, contiguous
+    float *dwq, *dwk, *partial; // backward: [d] each; kNormRopeBwdBlocks * 2 * d floats of scratch
+    const int* positions;       // [B][rows], or null: natural positions of the layout
+    int shard;                  // -1: whole-sequence buffers; else one device's shard
+    double base, eps;
+};
+constexpr int kNormRopeBwdBlocks = 1216;  // 152 SMs x 8: the most blocks the backward launches
+cudaError_t launch_norm_rope(const Problem& p, const NormRope& n, cudaStream_t s);
+
+// A key/value cache: k, v [B][Hkv][cap][d] of `dtype` (a tensor dtype, or kCacheE4m3 with the rows'
+// exponents + 127 in k_exp, v_exp [B][Hkv][cap]).
+constexpr int kCacheE4m3 = 2;
+struct Cache {
+    int B, Hkv, cap, d, dtype;
+    void *k, *v;
+    uint8_t *k_exp, *v_exp;
+};
+// Tokens t < ntok[b] of k, v (element strides batch, head, row; d contiguous) to rows lens[b] + t.
+cudaError_t launch_cache_write(const Cache& c, int T, const void* k, const long long* ks, const void* v, const long long* vs,
+                               const int* lens, const int* ntok, int dtype, unsigned int* status, cudaStream_t s);
+// Rows [row0, row0 + rows) of every head to k, v [B][Hkv][rows][d] of `dtype`.
+cudaError_t launch_cache_read(const Cache& c, int row0, int rows, void* k, void* v, int dtype, cudaStream_t s);
+
+// Attention of T drafted tokens per sequence over the cache (tree.cuh).
+struct Tree {
+    int H, T, dtype, out_dtype;
+    const void* q;              // [B][H][T][d]
+    const int *lens, *ntok;     // [B]; ntok may be null
+    const uint8_t* mask;        // [B][T][T] or [T][T] truth values, or null: token t sees tokens <= t
+    int mask_batched;
+    void* out;                  // [B][H][T][d] out_dtype
+    float* lse;                 // [B][H][T]
+    void* workspace;
+    unsigned int* status;
+};
+size_t tree_workspace_size(const Cache& c, int H, int T, int dtype);
+cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s);
+
 // Ulysses all-to-all re-layout between the token split [n][B][S][H][row] and the head split
 // [n][B][H/n][L][row] (direction 0 token -> head, 1 back); row_bytes a multiple of 4.
 cudaError_t launch_ulysses_a2a(const Geometry& geo, int B, int H, int row_bytes, const void* src, void* dst,
@@ -97,6 +147,16 @@ cudaError_t launch_bounded_wait_selftest(unsigned int* status, unsigned long lon
 
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
+
+// Shared by the entry points (api.cu).  fail / cuda_fail record the message and return the status;
+// the checks return RA_OK or have failed.
+int fail(int status, const char* fmt, ...);
+int cuda_fail(cudaError_t e, const char* what);
+int check_device();
+int check_problem(const Problem& p);
+int check_ptrs(std::initializer_list<const void*> ptrs);
+// Device address of the status word of the current device, or null with *err set.
+unsigned int* status_word(cudaError_t* err);
 
 // Records `msg` as the calling thread's last error (ring_attn_last_error) and returns `status`.
 int set_last_error(int status, const char* msg);

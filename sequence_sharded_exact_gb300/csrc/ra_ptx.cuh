@@ -80,6 +80,26 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     return r;
 }
 
+// Two float32 to e4m3, nearest even, lo in the low byte; finite values beyond +-448 become +-448.
+__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Four packed e4m3 values to float32 (exact: every e4m3 value is a float16 value).
+__device__ __forceinline__ void e4m3x4_to_float(uint32_t w, float& a, float& b, float& c, float& d)
+{
+    asm("{\n\t.reg .b16 lo, hi, x0, x1, x2, x3;\n\t.reg .b32 p, q;\n\t"
+        "mov.b32 {lo, hi}, %4;\n\t"
+        "cvt.rn.f16x2.e4m3x2 p, lo;\n\tcvt.rn.f16x2.e4m3x2 q, hi;\n\t"
+        "mov.b32 {x0, x1}, p;\n\tmov.b32 {x2, x3}, q;\n\t"
+        "cvt.f32.f16 %0, x0;\n\tcvt.f32.f16 %1, x1;\n\tcvt.f32.f16 %2, x2;\n\tcvt.f32.f16 %3, x3;\n\t}"
+        : "=f"(a), "=f"(b), "=f"(c), "=f"(d)
+        : "r"(w));
+}
+
 __device__ __forceinline__ bool elect_one_lane()
 {
     return (threadIdx.x & 31) == 0;

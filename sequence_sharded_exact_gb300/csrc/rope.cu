@@ -122,6 +122,19 @@ unsigned rope_grid(long long items)
 
 }  // namespace
 
+void rope_turns(double base, int d, unsigned long long (&turn)[64])
+{
+    const double two_pi = 6.283185307179586476925;
+    for (int i = 0; i < 64; ++i) {
+        turn[i] = 0;
+        if (i < d / 2) {
+            double frac = pow(base, -2.0 * i / d) / two_pi;  // turns per position
+            frac -= floor(frac);                               // only the fraction of a turn matters
+            turn[i] = (unsigned long long)ldexp(frac, 64);
+        }
+    }
+}
+
 cudaError_t launch_rope(const Problem& p, void* x, double base, int inverse, cudaStream_t s, int shard)
 {
     RopeArgs a;
@@ -131,15 +144,7 @@ cudaError_t launch_rope(const Problem& p, void* x, double base, int inverse, cud
     a.rows = shard < 0 ? p.L : p.L / p.n;
     a.row_off = shard < 0 ? 0 : shard * (p.L / p.n);
     a.inverse = inverse ? 1 : 0;
-    const double two_pi = 6.283185307179586476925;
-    for (int i = 0; i < 64; ++i) {
-        a.turn[i] = 0;
-        if (i < p.d / 2) {
-            double frac = pow(base, -2.0 * i / p.d) / two_pi;  // turns per position
-            frac -= floor(frac);                                 // only the fraction of a turn matters
-            a.turn[i] = (unsigned long long)ldexp(frac, 64);
-        }
-    }
+    rope_turns(base, p.d, a.turn);
     const long long rows = (long long)p.B * a.rows;
     if (p.dtype == 1) {
         const long long items = rows * (p.d / 8);

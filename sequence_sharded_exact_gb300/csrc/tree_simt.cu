@@ -1,0 +1,244 @@
+// tree_simt.cu -- attention over a cache (tree.cuh) on the CUDA cores: float32 queries, any cache.
+//
+// Four warps work through the CTA's tiles in chunks of 32 cached rows, staged in shared memory as
+// float32.  Scores: lane = cached row, each warp takes kRows / 4 query rows, so a row's maximum and sum
+// are shuffles in its warp, which alone keeps that row's running (m, l).  Output: thread = column (two
+// threads share a column's query rows when d = 64), the weights come from shared memory.  Masked
+// weights are stored as -1 and left out by a comparison, so that a masked row's values never meet the sums.
+#include <cuda_bf16.h>
+
+#include "ra_internal.h"
+#include "ra_ptx.cuh"
+#include "tree.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kChunk = 32;
+constexpr int kCtasPerSm = 4;
+
+// 16 bytes of a cached row as float32.
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, float up, float* f);
+template <>
+__device__ __forceinline__ void load16<float>(const float* p, float, float* f)
+{
+    *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16* p, float, float* f)
+{
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+template <>
+__device__ __forceinline__ void load16<uint8_t>(const uint8_t* p, float up, float* f)
+{
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        e4m3x4_to_float(w[i], f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[4 * i + j] *= up;
+    }
+}
+
+template <typename TQ, typename TC, int D, int ROWS>
+__global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a)
+{
+    constexpr int RW = ROWS / 4;            // query rows per warp in the scores
+    constexpr int SPLIT = kThreads / D;     // threads per output column
+    constexpr int RC = ROWS / SPLIT;        // query rows per thread in the output
+    constexpr int kStride = D + 4;          // keys: consecutive rows fall into different banks
+    __shared__ __align__(16) float qs[ROWS][D];
+    __shared__ __align__(16) float ks[kChunk][kStride];
+    __shared__ __align__(16) float vs[kChunk][D];
+    __shared__ __align__(16) float ps[ROWS][kChunk];
+    __shared__ float al[ROWS];
+    __shared__ float ml[ROWS][2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int col = tid % D, part = tid / D;
+    TreeWalk w;
+    if (!w.begin(a, blockIdx.x)) return;
+    do {
+        const long long head = (long long)w.b * a.Hkv + w.g;
+        const TQ* q = static_cast<const TQ*>(a.q) + (head * a.R + (long long)w.r * a.rt) * D;
+        const int rows = a.R - w.r * a.rt < a.rt ? a.R - w.r * a.rt : a.rt;
+        __syncthreads();
+        for (int e = tid; e < ROWS * D; e += kThreads) {
+            const int x = e / D;
+            qs[x][e % D] = x < rows ? (float)q[(long long)e] * a.scale_log2 : 0.f;
+        }
+        float m[RW], l[RW], acc[RC];
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < RC; ++i) acc[i] = 0.f;
+        const int end = w.t1 * kTreeTile < w.s.end ? w.t1 * kTreeTile : w.s.end;
+        for (int k0 = w.t0 * kTreeTile; k0 < end; k0 += kChunk) {
+            constexpr int per = 16 / sizeof(TC);
+            __syncthreads();
+            for (int e = tid; e < kChunk * D / per; e += kThreads) {
+                const int j = e / (D / per), c = e % (D / per) * per;
+                float fk[per], fv[per];
+#pragma unroll
+                for (int i = 0; i < per; ++i) fk[i] = fv[i] = 0.f;
+                if (k0 + j < end) {
+                    const long long src = head * a.cap + k0 + j;
+                    float uk = 1.f, uv = 1.f;
+                    if (sizeof(TC) == 1) {
+                        uk = __uint_as_float((uint32_t)a.k_exp[src] << 23);
+                        uv = __uint_as_float((uint32_t)a.v_exp[src] << 23);
+                    }
+                    load16(static_cast<const TC*>(a.k) + src * D + c, uk, fk);
+                    load16(static_cast<const TC*>(a.v) + src * D + c, uv, fv);
+                }
+#pragma unroll
+                for (int i = 0; i < per; i += 4) {
+                    *reinterpret_cast<float4*>(&ks[j][c + i]) = make_float4(fk[i], fk[i + 1], fk[i + 2], fk[i + 3]);
+                    *reinterpret_cast<float4*>(&vs[j][c + i]) = make_float4(fv[i], fv[i + 1], fv[i + 2], fv[i + 3]);
+                }
+            }
+            __syncthreads();
+            float sc[RW];
+#pragma unroll
+            for (int i = 0; i < RW; ++i) sc[i] = 0.f;
+#pragma unroll 4
+            for (int c = 0; c < D; c += 4) {
+                const float4 kv = *reinterpret_cast<const float4*>(&ks[lane][c]);
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    const float4 qv = *reinterpret_cast<const float4*>(&qs[warp * RW + i][c]);
+                    sc[i] = fmaf(qv.x, kv.x, sc[i]);
+                    sc[i] = fmaf(qv.y, kv.y, sc[i]);
+                    sc[i] = fmaf(qv.z, kv.z, sc[i]);
+                    sc[i] = fmaf(qv.w, kv.w, sc[i]);
+                }
+            }
+            const int key = k0 + lane;
+            const bool drafted = k0 + kChunk > w.s.len;  // the chunk holds drafted tokens, or rows past the end
+#pragma unroll
+            for (int i = 0; i < RW; ++i) {
+                const int x = w.r * a.rt + warp * RW + i, t = x % a.T;
+                bool sees = key < end;
+                if (drafted && key >= w.s.len && sees) sees = t < w.s.cnt && x < a.R && tree_sees(a, w.b, t, key - w.s.len);
+                float mx = sees ? sc[i] : -INFINITY;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn;
+                const float p = sees ? ex2_approx(sc[i] - ref) : 0.f;
+                const float alpha = ex2_approx(m[i] - ref);
+                float sum = p;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                l[i] = l[i] * alpha + sum;
+                m[i] = mn;
+                ps[warp * RW + i][lane] = sees ? p : -1.f;
+                if (lane == 0) al[warp * RW + i] = alpha;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < RC; ++i) acc[i] *= al[part * RC + i];
+            if (!drafted) {
+#pragma unroll 2
+                for (int j = 0; j < kChunk; j += 4) {
+                    const float v0 = vs[j][col], v1 = vs[j + 1][col], v2 = vs[j + 2][col], v3 = vs[j + 3][col];
+#pragma unroll
+                    for (int i = 0; i < RC; ++i) {
+                        const float4 pv = *reinterpret_cast<const float4*>(&ps[part * RC + i][j]);
+                        acc[i] = fmaf(pv.x, v0, acc[i]);
+                        acc[i] = fmaf(pv.y, v1, acc[i]);
+                        acc[i] = fmaf(pv.z, v2, acc[i]);
+                        acc[i] = fmaf(pv.w, v3, acc[i]);
+                    }
+                }
+            } else {
+                for (int j = 0; j < kChunk; ++j) {
+                    const float v0 = vs[j][col];
+#pragma unroll
+                    for (int i = 0; i < RC; ++i) {
+                        const float p = ps[part * RC + i][j];
+                        if (!(p < 0.f)) acc[i] = fmaf(p, v0, acc[i]);  // NaN weights stay
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RW; ++i)
+            if (lane == 0) {
+                ml[warp * RW + i][0] = m[i];
+                ml[warp * RW + i][1] = l[i];
+            }
+        __syncthreads();
+        const bool whole = w.whole();
+        const long long slot = (long long)blockIdx.x * 2 + (w.first ? 0 : 1);
+#pragma unroll
+        for (int i = 0; i < RC; ++i) {
+            const int x = part * RC + i;
+            if (x >= rows || (w.r * a.rt + x) % a.T >= w.s.cnt) continue;
+            const float mm = ml[x][0], ll = ml[x][1];
+            if (whole) {
+                const bool none = mm == -INFINITY && ll == 0.f;
+                const float o = none ? 0.f : acc[i] / ll;
+                const long long dst = head * a.R + w.r * a.rt + x;
+                if (a.bf16_out)
+                    static_cast<__nv_bfloat16*>(a.out)[dst * D + col] = __float2bfloat16_rn(o);
+                else
+                    static_cast<float*>(a.out)[dst * D + col] = o;
+                if (col == 0) a.lse[dst] = none ? -INFINITY : (mm + log2f(ll)) * kLn2;
+            } else {
+                a.part_o[(slot * a.rt + x) * D + col] = acc[i];
+                if (col == 0) {
+                    a.part_ml[(slot * a.rt + x) * 2] = mm;
+                    a.part_ml[(slot * a.rt + x) * 2 + 1] = ll;
+                }
+            }
+        }
+    } while (w.next(a));
+}
+
+template <typename TQ, typename TC, int D>
+cudaError_t launch_rows(const TreeArgs& a, cudaStream_t s)
+{
+    if (a.rt == 4)
+        tree_simt_kernel<TQ, TC, D, 4><<<a.ctas, kThreads, 0, s>>>(a);
+    else
+        tree_simt_kernel<TQ, TC, D, 16><<<a.ctas, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename TQ, typename TC>
+cudaError_t launch_d(const TreeArgs& a, int d, cudaStream_t s)
+{
+    return d == 128 ? launch_rows<TQ, TC, 128>(a, s) : launch_rows<TQ, TC, 64>(a, s);
+}
+
+}  // namespace
+
+int tree_simt_rows(int R) { return R <= 4 ? 4 : 16; }
+
+cudaError_t launch_tree_simt(TreeArgs& a, int d, int dtype, int cache_dtype, cudaStream_t s)
+{
+    const long long most = (long long)a.B * a.Hkv * a.nrt * ((a.cap + kTreeTile - 1) / kTreeTile);
+    long long ctas = (long long)device_sm_count() * kCtasPerSm;
+    if (ctas > kTreeMaxCtas) ctas = kTreeMaxCtas;
+    a.ctas = (int)(ctas < most ? ctas : most);
+    cudaError_t e;
+    if (dtype == 1)
+        e = cache_dtype == kCacheE4m3 ? launch_d<__nv_bfloat16, uint8_t>(a, d, s) : launch_d<__nv_bfloat16, __nv_bfloat16>(a, d, s);
+    else
+        e = cache_dtype == kCacheE4m3 ? launch_d<float, uint8_t>(a, d, s) : launch_d<float, float>(a, d, s);
+    return e != cudaSuccess ? e : launch_tree_join(a, d, s);
+}
+
+}  // namespace ra
