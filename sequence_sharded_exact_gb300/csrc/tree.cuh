@@ -31,7 +31,8 @@
 namespace ra {
 
 constexpr int kTreeTile = 128;     // cached rows per tile of the work list
-constexpr int kTreeMaxCtas = 640;  // most CTAs of the first launch (bounds the workspace)
+constexpr int kTreeMaxCtas = 640;    // most CTAs of the first launch on the CUDA cores (bounds the workspace)
+constexpr int kTreeMaxTcCtas = 160;  // and on the tensor cores (one per SM)
 
 struct TreeArgs {
     int B, H, Hkv, G, T, R;  // R = G * T query rows per kv head, row x: head x / T of the group, token x % T
@@ -44,7 +45,7 @@ struct TreeArgs {
     const uint8_t *k_exp, *v_exp;
     void* out;
     float* lse;
-    float* part_ml;  // [ctas][2][rt][2]: m (log2 units), l
+    float* part_ml;  // [ctas][2][rt][4]: m (log2 units), l, the output's normaliser (l as the weights were rounded), 0
     float* part_o;   // [ctas][2][rt][d]
     unsigned int* status;
     float scale_log2;  // log2(e) / sqrt(d)
@@ -187,8 +188,13 @@ __host__ __device__ inline size_t tree_align(size_t x) { return (x + 255) & ~siz
 
 // Joins the partials of shared items and writes the rows that see nothing (tree_join.cu).
 cudaError_t launch_tree_join(const TreeArgs& a, int d, cudaStream_t s);
-// CUDA-core path: any dtype (tree_simt.cu).  Query rows per row tile and CTAs for R query rows per kv head.
+// CUDA-core path: float32 queries (tree_simt.cu).  Query rows per row tile for R query rows per kv head.
 int tree_simt_rows(int R);
-cudaError_t launch_tree_simt(TreeArgs& a, int d, int dtype, int cache_dtype, cudaStream_t s);
+constexpr int kTreeSimtCtasPerSm = 4;
+cudaError_t launch_tree_simt(const TreeArgs& a, int d, int cache_dtype, cudaStream_t s);
+
+// Tensor-core path: bf16 queries, bf16 or e4m3 cache (tree_tc_body.cuh).
+cudaError_t launch_tree_tc_d128(const TreeArgs& a, bool e4m3, cudaStream_t s);
+cudaError_t launch_tree_tc_d64(const TreeArgs& a, bool e4m3, cudaStream_t s);
 
 }  // namespace ra

@@ -5,8 +5,6 @@
 // are shuffles in its warp, which alone keeps that row's running (m, l).  Output: thread = column (two
 // threads share a column's query rows when d = 64), the weights come from shared memory.  Masked
 // weights are stored as -1 and left out by a comparison, so that a masked row's values never meet the sums.
-#include <cuda_bf16.h>
-
 #include "ra_internal.h"
 #include "ra_ptx.cuh"
 #include "tree.cuh"
@@ -16,7 +14,6 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kChunk = 32;
-constexpr int kCtasPerSm = 4;
 
 // 16 bytes of a cached row as float32.
 template <typename T>
@@ -25,17 +22,6 @@ template <>
 __device__ __forceinline__ void load16<float>(const float* p, float, float* f)
 {
     *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(p);
-}
-template <>
-__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16* p, float, float* f)
-{
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
 }
 template <>
 __device__ __forceinline__ void load16<uint8_t>(const uint8_t* p, float up, float* f)
@@ -50,7 +36,7 @@ __device__ __forceinline__ void load16<uint8_t>(const uint8_t* p, float up, floa
     }
 }
 
-template <typename TQ, typename TC, int D, int ROWS>
+template <typename TC, int D, int ROWS>
 __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a)
 {
     constexpr int RW = ROWS / 4;            // query rows per warp in the scores
@@ -69,12 +55,12 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a)
     if (!w.begin(a, blockIdx.x)) return;
     do {
         const long long head = (long long)w.b * a.Hkv + w.g;
-        const TQ* q = static_cast<const TQ*>(a.q) + (head * a.R + (long long)w.r * a.rt) * D;
+        const float* q = static_cast<const float*>(a.q) + (head * a.R + (long long)w.r * a.rt) * D;
         const int rows = a.R - w.r * a.rt < a.rt ? a.R - w.r * a.rt : a.rt;
         __syncthreads();
         for (int e = tid; e < ROWS * D; e += kThreads) {
             const int x = e / D;
-            qs[x][e % D] = x < rows ? (float)q[(long long)e] * a.scale_log2 : 0.f;
+            qs[x][e % D] = x < rows ? q[e] * a.scale_log2 : 0.f;
         }
         float m[RW], l[RW], acc[RC];
 #pragma unroll
@@ -191,54 +177,39 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a)
                 const bool none = mm == -INFINITY && ll == 0.f;
                 const float o = none ? 0.f : acc[i] / ll;
                 const long long dst = head * a.R + w.r * a.rt + x;
-                if (a.bf16_out)
-                    static_cast<__nv_bfloat16*>(a.out)[dst * D + col] = __float2bfloat16_rn(o);
-                else
-                    static_cast<float*>(a.out)[dst * D + col] = o;
+                static_cast<float*>(a.out)[dst * D + col] = o;
                 if (col == 0) a.lse[dst] = none ? -INFINITY : (mm + log2f(ll)) * kLn2;
             } else {
                 a.part_o[(slot * a.rt + x) * D + col] = acc[i];
-                if (col == 0) {
-                    a.part_ml[(slot * a.rt + x) * 2] = mm;
-                    a.part_ml[(slot * a.rt + x) * 2 + 1] = ll;
-                }
+                if (col == 0) *reinterpret_cast<float4*>(a.part_ml + (slot * a.rt + x) * 4) = make_float4(mm, ll, ll, 0.f);
             }
         }
     } while (w.next(a));
 }
 
-template <typename TQ, typename TC, int D>
+template <typename TC, int D>
 cudaError_t launch_rows(const TreeArgs& a, cudaStream_t s)
 {
     if (a.rt == 4)
-        tree_simt_kernel<TQ, TC, D, 4><<<a.ctas, kThreads, 0, s>>>(a);
+        tree_simt_kernel<TC, D, 4><<<a.ctas, kThreads, 0, s>>>(a);
     else
-        tree_simt_kernel<TQ, TC, D, 16><<<a.ctas, kThreads, 0, s>>>(a);
+        tree_simt_kernel<TC, D, 16><<<a.ctas, kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
-template <typename TQ, typename TC>
+template <typename TC>
 cudaError_t launch_d(const TreeArgs& a, int d, cudaStream_t s)
 {
-    return d == 128 ? launch_rows<TQ, TC, 128>(a, s) : launch_rows<TQ, TC, 64>(a, s);
+    return d == 128 ? launch_rows<TC, 128>(a, s) : launch_rows<TC, 64>(a, s);
 }
 
 }  // namespace
 
 int tree_simt_rows(int R) { return R <= 4 ? 4 : 16; }
 
-cudaError_t launch_tree_simt(TreeArgs& a, int d, int dtype, int cache_dtype, cudaStream_t s)
+cudaError_t launch_tree_simt(const TreeArgs& a, int d, int cache_dtype, cudaStream_t s)
 {
-    const long long most = (long long)a.B * a.Hkv * a.nrt * ((a.cap + kTreeTile - 1) / kTreeTile);
-    long long ctas = (long long)device_sm_count() * kCtasPerSm;
-    if (ctas > kTreeMaxCtas) ctas = kTreeMaxCtas;
-    a.ctas = (int)(ctas < most ? ctas : most);
-    cudaError_t e;
-    if (dtype == 1)
-        e = cache_dtype == kCacheE4m3 ? launch_d<__nv_bfloat16, uint8_t>(a, d, s) : launch_d<__nv_bfloat16, __nv_bfloat16>(a, d, s);
-    else
-        e = cache_dtype == kCacheE4m3 ? launch_d<float, uint8_t>(a, d, s) : launch_d<float, float>(a, d, s);
-    return e != cudaSuccess ? e : launch_tree_join(a, d, s);
+    return cache_dtype == kCacheE4m3 ? launch_d<uint8_t>(a, d, s) : launch_d<float>(a, d, s);
 }
 
 }  // namespace ra

@@ -1,0 +1,938 @@
+// tree_tc_body.cuh -- tensor-core path of the attention over a cache (tree.cuh) for bf16 queries and a bf16
+// or e4m3 cache, head dim RA_TREE_HD (128 or 64).  Compiled once per head dim (tree_tc.cu: 128,
+// tree_tc_d64.cu: 64); the including file names the host entry point through RA_TREE_LAUNCH.
+//
+// One CTA per SM walks its items (tree.cuh): one kv head's tile of query rows against its cached rows, 128
+// at a time.  For query rows X and cached rows K, V of a tile:
+//   S = X K^T (TMEM), P = 2^(S c - m) (bf16, over S's columns), O += P V (TMEM), the running m, l per row.
+// A query row is a TMEM lane and a thread, so its maximum and sum need no exchange between threads.
+//   * Up to 128 query rows (kNq = 1): the two softmax warpgroups take turns at the tiles, each with its own
+//     m, l and O, so that one tile's exponentials run beside the other's products; they join the two at the
+//     item's end (both read both O's: a warp of either group reaches the same TMEM lanes), half the
+//     columns each.
+//   * More (kNq = 2): 256 query rows as two 128-row tiles that share every K/V tile, a warpgroup each.
+//   * m follows the row maximum only when that grows by more than 2^8: O / l does not depend on the
+//     reference, and O in TMEM is then seldom rescaled.
+//   * Warps: 0-3 and 4-7 softmax; 8 loads the queries and K, 10 V (TMA, one thread each); 9 issues the MMAs;
+//     11 fetches the rows' scales (e4m3); 12-15 prepare V.
+// Rows that must not count: scores of unseen rows are set to -infinity before the maximum, but 0 * NaN in
+// P V would still be NaN, so warps 12-15 clear the rows of V behind the sequence, and non-finite elements
+// of drafted tokens' rows, in shared memory before the product; those elements are added afterwards to
+// the rows that do see them (rare, from global memory).
+// e4m3: K goes into the products as it is cached.  The queries are split into two e4m3 values,
+// x 2^-e = hi + lo with a power-of-two scale per row: hi takes four significant bits, the rest of a bf16's
+// eight is exact in lo (elements below 2^-10 of the row's largest lose what lies below 2^-18 of it), so S
+// is two e4m3 products at twice the rate, with float32 sums.  The row and column scales are applied to
+// S.  P keeps bf16 (an e4m3 P would lose weights below 2^-9 of the largest, which add up over a long
+// cache), so warps 12-15 turn V into bf16, exactly, scale included.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <mutex>
+
+#include "ra_internal.h"
+#include "ra_ptx.cuh"
+#include "tree.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kHd = RA_TREE_HD;
+static_assert(kHd == 128 || kHd == 64, "head dim");
+constexpr int kThreads = 512;
+constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;  // S_w at 128 w, O_w at 256 + 128 w
+constexpr uint64_t kWaitLimitNs = 4000000000ull;             // 4 s
+
+template <bool kE4, int kNq>
+struct Cfg {
+    static constexpr int kSlotsK = kE4 ? (kNq == 1 ? 4 : 3) : (kNq == 1 ? 3 : 2);
+    static constexpr int kSlotsL = kE4 ? (kNq == 1 ? 3 : 2) : 2;  // V as loaded
+    static constexpr int kSlotsP = 2;                             // V as prepared (e4m3; bf16 is prepared in place)
+    static_assert(kE4 || kSlotsP == kSlotsL, "bf16: a barrier per slot in place");
+    static constexpr int kSlotsX = kE4 ? 8 : 1;                   // rows' scales
+    static constexpr uint32_t kBytesK = 128 * kHd * (kE4 ? 1 : 2);
+    static constexpr uint32_t kBytesV = 128 * kHd * 2;
+    static constexpr uint32_t kBytesQ = 128 * kHd * 2;  // of one 128-row tile: bf16, or the hi and lo halves
+
+    static constexpr uint32_t kQ = 0;
+    static constexpr uint32_t kK = kQ + kNq * kBytesQ;
+    static constexpr uint32_t kL = kK + kSlotsK * kBytesK;  // slots of kBytesK: V is loaded in the cache's type
+    static constexpr uint32_t kP = kL + kSlotsL * kBytesK;
+    static constexpr uint32_t kX = kP + (kE4 ? kSlotsP * kBytesV : 0);  // [slots][2][128] float
+    static constexpr uint32_t kMl = kX + (kE4 ? kSlotsX * 1024 : 0);    // [2][128] float4 (kNq == 1)
+    static constexpr uint32_t kQs = kMl + (kNq == 1 ? 4096 : 0);        // [2][kNq * 128] float (e4m3)
+    static constexpr uint32_t kPoison = kQs + (kE4 ? 2 * kNq * 512 : 0);  // [8] int
+    static constexpr uint32_t kBar = kPoison + 32;
+
+    static constexpr int bQFull = 0, bQEmpty = 1, bS = 2, bP = 4, bO = 6, bEpi = 8, bDrain = 10;
+    static constexpr int bKFull = 11, bKEmpty = bKFull + kSlotsK;
+    static constexpr int bLFull = bKEmpty + kSlotsK, bLEmpty = bLFull + kSlotsL;
+    static constexpr int bPFull = bLEmpty + kSlotsL, bPEmpty = bPFull + kSlotsP;
+    static constexpr int bXFull = bPEmpty + kSlotsP, bXEmpty = bXFull + kSlotsX;
+    static constexpr int kBars = bXEmpty + kSlotsX;
+
+    static constexpr uint32_t kSlot = kBar + kBars * 8;
+    static constexpr uint32_t kAbort = kSlot + 8;
+    static constexpr uint32_t kSmem = kAbort + 8 + 1024;  // slack for the 1024-byte alignment of the base
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+// The whole warp's wait: every lane learns whether all of them saw the phase.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl& ctl)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl));
+}
+
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity)
+{
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (global_timer_ns() - t0 > 1000000000ull) return;
+    }
+}
+
+// Shared-memory descriptors.  K-major operands of bf16 and of 128-column e4m3 have 128-byte rows and that
+// swizzle; 64-column e4m3 rows are 64 bytes with the 64-byte swizzle (layout 4, 8-row groups of 512 bytes).
+template <bool kE4>
+constexpr bool kNarrow = kE4 && kHd == 64;
+template <bool kE4>
+__host__ __device__ constexpr uint32_t kmajor_hi()
+{
+    return kNarrow<kE4> ? (((512u >> 4) & 0x3FFFu) | (1u << 14) | (4u << 29)) : sdesc_sw128_hi(1024);
+}
+
+// kind::f8f6f4 (e4m3 operands, f32 accumulate): formats 0, the other fields as kind::f16's.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N)
+{
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// S_w = X K^T.
+template <bool kE4, int kNq>
+__device__ __forceinline__ void issue_s(uint32_t sbase, uint32_t tmem, int w, int slot)
+{
+    using C = Cfg<kE4, kNq>;
+    const uint32_t q = sdesc_sw128_lo(sbase + C::kQ + (kNq == 2 ? (uint32_t)w * C::kBytesQ : 0u), 16);
+    const uint32_t k = sdesc_sw128_lo(sbase + C::kK + (uint32_t)slot * C::kBytesK, 16);
+    const uint32_t d = tmem + kColS + (uint32_t)w * 128;
+    constexpr uint32_t hi = kmajor_hi<kE4>();
+    if constexpr (kE4) {
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int kk = 0; kk < kHd / 32; ++kk)
+                mma_ss_e4m3(d, sdesc_at(q, (uint32_t)part * 128 * kHd + (uint32_t)kk * 32, hi), sdesc_at(k, (uint32_t)kk * 32, hi),
+                            idesc_e4m3_f32(128, 128), part + kk > 0 ? 1u : 0u);
+    } else {
+#pragma unroll
+        for (int kk = 0; kk < kHd / 16; ++kk) {
+            const uint32_t off = (uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u;
+            mma_ss(d, sdesc_at(q, off, hi), sdesc_at(k, off, hi), idesc_bf16_f32(128, 128, false, false), kk > 0 ? 1u : 0u);
+        }
+    }
+}
+
+// O_w (+)= P_w V.
+__device__ __forceinline__ void issue_pv(uint32_t v_addr, uint32_t tmem, int w, bool accumulate)
+{
+    const uint32_t v = sdesc_sw128_lo(v_addr, 16384);
+    constexpr uint32_t hi = sdesc_sw128_hi(1024);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+        mma_ts(tmem + kColO + (uint32_t)w * 128, tmem + kColS + (uint32_t)w * 128 + (uint32_t)kk * 8,
+               sdesc_at(v, (uint32_t)kk * 2048u, hi), idesc_bf16_f32(128, kHd, false, true), kk > 0 || accumulate ? 1u : 0u);
+}
+
+// ------------------------------------------------------------------------------------------------
+// loads
+// ------------------------------------------------------------------------------------------------
+template <bool kE4, int kNq>
+__device__ __forceinline__ void load_qk_role(const TreeArgs& a, uint32_t sbase, const Maps& maps, TreeWalk w, const WaitCtl& ctl)
+{
+    using C = Cfg<kE4, kNq>;
+    auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
+    uint32_t kc = 0, item = 0;
+    bool ok = true;
+    do {
+        const int z = w.b * a.Hkv + w.g;
+        if constexpr (!kE4) {
+            if (item > 0 && !mbar_wait(bar(C::bQEmpty), (item - 1) & 1, ctl)) break;
+            mbar_arrive_expect_tx(bar(C::bQFull), kNq * C::kBytesQ);
+            for (int t = 0; t < kNq; ++t)
+                for (int h = 0; h < kHd / 64; ++h)
+                    tma_load_3d(sbase + C::kQ + (uint32_t)t * C::kBytesQ + (uint32_t)h * 16384u, &maps.q, bar(C::bQFull), h * 64,
+                                w.r * a.rt + t * 128, z);
+            ++item;
+        }
+        for (int t = w.t0; t < w.t1; ++t, ++kc) {
+            const int slot = (int)(kc % C::kSlotsK);
+            const uint32_t use = kc / C::kSlotsK;
+            if (use > 0 && !mbar_wait(bar(C::bKEmpty + slot), (use - 1) & 1, ctl)) { ok = false; break; }
+            mbar_arrive_expect_tx(bar(C::bKFull + slot), C::kBytesK);
+            const uint32_t dst = sbase + C::kK + (uint32_t)slot * C::kBytesK;
+            if constexpr (kE4) {
+                tma_load_3d(dst, &maps.k, bar(C::bKFull + slot), 0, t * kTreeTile, z);
+            } else {
+                for (int h = 0; h < kHd / 64; ++h)
+                    tma_load_3d(dst + (uint32_t)h * 16384u, &maps.k, bar(C::bKFull + slot), h * 64, t * kTreeTile, z);
+            }
+        }
+    } while (ok && w.next(a));
+    if (item > 0) drain_wait(bar(C::bQFull), (item - 1) & 1);
+    for (uint32_t s = 0; s < (uint32_t)C::kSlotsK && s < kc; ++s)
+        drain_wait(bar(C::bKFull + (int)((kc - 1 - s) % C::kSlotsK)), ((kc - 1 - s) / C::kSlotsK) & 1);
+}
+
+template <bool kE4, int kNq>
+__device__ __forceinline__ void load_v_role(const TreeArgs& a, uint32_t sbase, const Maps& maps, TreeWalk w, const WaitCtl& ctl)
+{
+    using C = Cfg<kE4, kNq>;
+    auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
+    uint32_t vc = 0;
+    bool ok = true;
+    do {
+        const int z = w.b * a.Hkv + w.g;
+        for (int t = w.t0; t < w.t1; ++t, ++vc) {
+            const int slot = (int)(vc % C::kSlotsL);
+            const uint32_t use = vc / C::kSlotsL;
+            if (use > 0 && !mbar_wait(bar(C::bLEmpty + slot), (use - 1) & 1, ctl)) { ok = false; break; }
+            const uint32_t dst = sbase + C::kL + (uint32_t)slot * C::kBytesK;
+            if constexpr (kE4) {
+                // rows are contiguous and V is not a product's operand here: one untiled copy, no row past the cache
+                const int rows = a.cap - t * kTreeTile < kTreeTile ? a.cap - t * kTreeTile : kTreeTile;
+                mbar_arrive_expect_tx(bar(C::bLFull + slot), (uint32_t)rows * kHd);
+                bulk_load_1d(dst, static_cast<const uint8_t*>(a.v) + ((long long)z * a.cap + (long long)t * kTreeTile) * kHd,
+                             (uint32_t)rows * kHd, bar(C::bLFull + slot));
+            } else {
+                mbar_arrive_expect_tx(bar(C::bLFull + slot), C::kBytesK);
+                for (int h = 0; h < kHd / 64; ++h)
+                    tma_load_3d(dst + (uint32_t)h * 16384u, &maps.v, bar(C::bLFull + slot), h * 64, t * kTreeTile, z);
+            }
+        }
+    } while (ok && w.next(a));
+    for (uint32_t s = 0; s < (uint32_t)C::kSlotsL && s < vc; ++s)
+        drain_wait(bar(C::bLFull + (int)((vc - 1 - s) % C::kSlotsL)), ((vc - 1 - s) / C::kSlotsL) & 1);
+}
+
+// The scales of a tile's rows, 2^e as float32, k's then v's; four tiles' bytes are in flight at a time.
+template <int kNq>
+__device__ __forceinline__ void scale_role(const TreeArgs& a, uint32_t sbase, uint8_t* smem, TreeWalk w, const WaitCtl& ctl)
+{
+    using C = Cfg<true, kNq>;
+    auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
+    const int lane = threadIdx.x & 31;
+    uint32_t xc = 0;
+    do {
+        const long long row0 = ((long long)w.b * a.Hkv + w.g) * a.cap;
+        for (int t = w.t0; t < w.t1;) {
+            const int n = w.t1 - t < 4 ? w.t1 - t : 4;
+            uint32_t raw[4][4];  // k's byte in bits 0-7, v's in 8-15
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = (t + u) * kTreeTile + i * 32 + lane;
+                    raw[u][i] = 0;
+                    if (u < n && row < w.s.end)
+                        raw[u][i] = (uint32_t)a.k_exp[row0 + row] | (uint32_t)a.v_exp[row0 + row] << 8;
+                }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (u >= n) break;
+                const int slot = (int)(xc % C::kSlotsX);
+                const uint32_t use = xc / C::kSlotsX;
+                if (use > 0 && !warp_wait(bar(C::bXEmpty + slot), (use - 1) & 1, ctl)) return;
+                float* x = reinterpret_cast<float*>(smem + C::kX + slot * 1024);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i * 32 + lane] = __uint_as_float((raw[u][i] & 0xffu) << 23);
+                    x[128 + i * 32 + lane] = __uint_as_float((raw[u][i] >> 8) << 23);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::bXFull + slot));
+                ++xc;
+            }
+            t += n;
+        }
+    } while (w.next(a));
+}
+
+// ------------------------------------------------------------------------------------------------
+// V (and, for e4m3, the queries) as the products take them
+// ------------------------------------------------------------------------------------------------
+// Clears the non-finite halves of a packed bf16 pair; true if there was one.
+__device__ __forceinline__ bool clear_nonfinite(uint32_t& w)
+{
+    bool hit = false;
+    if ((w & 0x7f80u) == 0x7f80u) {
+        w &= 0xffff0000u;
+        hit = true;
+    }
+    if ((w & 0x7f800000u) == 0x7f800000u) {
+        w &= 0x0000ffffu;
+        hit = true;
+    }
+    return hit;
+}
+
+// bf16: only the tiles that reach past the prefix are touched, in place; the others are passed on (a warp that
+// skipped a tile's phase could take the slot's previous phase for the one it waits for).
+template <int kNq>
+__device__ __forceinline__ void prep_bf16_role(const TreeArgs& a, uint32_t sbase, uint8_t* smem, TreeWalk w, const WaitCtl& ctl)
+{
+    using C = Cfg<false, kNq>;
+    auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
+    const int row = threadIdx.x & 127;
+    uint32_t vc = 0, item = 0;
+    do {
+        for (int t = w.t0; t < w.t1; ++t, ++vc) {
+            const int slot = (int)(vc % C::kSlotsL);
+            if (!warp_wait(bar(C::bLFull + slot), (vc / C::kSlotsL) & 1, ctl)) return;
+            if ((t + 1) * kTreeTile > w.s.len) {
+                uint8_t* v = smem + C::kL + (uint32_t)slot * C::kBytesK;
+                const int key = t * kTreeTile + row;
+                if (key >= w.s.len) {
+                    bool hit = false;
+                    for (int c = 0; c < kHd / 8; ++c) {
+                        uint4* p = reinterpret_cast<uint4*>(v + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+                        if (key >= w.s.end) {
+                            *p = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+                        uint4 x = *p;
+                        const bool bad = clear_nonfinite(x.x) | clear_nonfinite(x.y) | clear_nonfinite(x.z) | clear_nonfinite(x.w);
+                        if (bad) *p = x;
+                        hit |= bad;
+                    }
+                    if (hit) *reinterpret_cast<volatile int*>(smem + C::kPoison + (item & 7) * 4) = (int)item + 1;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(bar(C::bPFull + slot));
+        }
+        ++item;
+    } while (w.next(a));
+}
+
+__device__ __forceinline__ uint32_t qk_offset(int row, int c16)  // 16-byte chunk of a K-major e4m3 row
+{
+    return kHd == 128 ? (uint32_t)(row * 128 + ((c16 ^ (row & 7)) << 4)) : (uint32_t)(row * 64 + ((c16 ^ ((row >> 1) & 3)) << 4));
+}
+
+template <int kNq>
+__device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase, uint8_t* smem, TreeWalk w, const WaitCtl& ctl)
+{
+    using C = Cfg<true, kNq>;
+    auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
+    const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
+    uint32_t vc = 0, item = 0;
+    do {
+        // the item's queries: hi and lo e4m3 values and the row's scale
+        if (item > 0 && !warp_wait(bar(C::bQEmpty), (item - 1) & 1, ctl)) return;
+#pragma unroll 1
+        for (int qt = 0; qt < kNq; ++qt) {
+            const int x = w.r * a.rt + qt * 128 + row;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                              (((long long)w.b * a.Hkv + w.g) * a.R + x) * kHd);
+            uint8_t* q = smem + C::kQ + (uint32_t)qt * C::kBytesQ;
+            uint32_t big = 0;  // bits of the largest magnitude: bf16 in the upper half, ordered as integers
+            if (x < a.R) {
+#pragma unroll 4
+                for (int c = 0; c < kHd / 8; ++c) {
+                    const uint4 v = src[c];
+                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        big = max(big, u[i] << 16 & 0x7fff0000u);
+                        big = max(big, u[i] & 0x7fff0000u);
+                    }
+                }
+            }
+            const bool finite = big < 0x7f800000u;
+            int e = (int)(big >> 23) - 135 + ((big & 0x7fffffu) > 0x600000u ? 1 : 0);
+            e = !finite || e < -126 ? -126 : e;
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            reinterpret_cast<float*>(smem + C::kQs)[(item & 1) * kNq * 128 + qt * 128 + row] =
+                finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7fc00000u);
+#pragma unroll 1
+            for (int c = 0; c < kHd / 16; ++c) {
+                uint4 hi = make_uint4(0, 0, 0, 0), lo = make_uint4(0, 0, 0, 0);
+                if (x < a.R && finite) {
+                    const uint4 v0 = src[2 * c], v1 = src[2 * c + 1];
+                    const uint32_t u[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                    uint32_t ph[4], pl[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float f0 = __uint_as_float(u[2 * i] << 16) * down, f1 = __uint_as_float(u[2 * i] & 0xffff0000u) * down;
+                        const float f2 = __uint_as_float(u[2 * i + 1] << 16) * down, f3 = __uint_as_float(u[2 * i + 1] & 0xffff0000u) * down;
+                        ph[i] = (uint32_t)e4m3x2(f0, f1) | (uint32_t)e4m3x2(f2, f3) << 16;
+                        float h0, h1, h2, h3;
+                        e4m3x4_to_float(ph[i], h0, h1, h2, h3);
+                        pl[i] = (uint32_t)e4m3x2(f0 - h0, f1 - h1) | (uint32_t)e4m3x2(f2 - h2, f3 - h3) << 16;
+                    }
+                    hi = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+                    lo = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+                }
+                *reinterpret_cast<uint4*>(q + qk_offset(row, c)) = hi;
+                *reinterpret_cast<uint4*>(q + 128 * kHd + qk_offset(row, c)) = lo;
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::bQFull));
+
+        for (int t = w.t0; t < w.t1; ++t, ++vc) {
+            const int sl = (int)(vc % C::kSlotsL), sp = (int)(vc % C::kSlotsP), sx = (int)(vc % C::kSlotsX);
+            const uint32_t use = vc / C::kSlotsP;
+            if (!warp_wait(bar(C::bXFull + sx), (vc / C::kSlotsX) & 1, ctl)) return;
+            if (!warp_wait(bar(C::bLFull + sl), (vc / C::kSlotsL) & 1, ctl)) return;
+            if (use > 0 && !warp_wait(bar(C::bPEmpty + sp), (use - 1) & 1, ctl)) return;
+            const uint8_t* src = smem + C::kL + (uint32_t)sl * C::kBytesK;
+            uint8_t* dst = smem + C::kP + (uint32_t)sp * C::kBytesV;
+            const float up = reinterpret_cast<const float*>(smem + C::kX + sx * 1024)[128 + row];
+            const int key = t * kTreeTile + row;
+            const bool past = key >= w.s.end, drafted = key >= w.s.len;
+            bool hit = false;
+            // a thread has a row; starting each at another chunk keeps a warp's accesses in different banks
+#pragma unroll 4
+            for (int i = 0; i < kHd / 16; ++i) {
+                const int c = (i + row) & (kHd / 16 - 1);
+                const uint4 x = *reinterpret_cast<const uint4*>(src + row * kHd + c * 16);
+                const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float f0, f1, f2, f3;
+                    e4m3x4_to_float(u[j], f0, f1, f2, f3);
+                    o[2 * j] = pack_bf16x2(f0 * up, f1 * up);
+                    o[2 * j + 1] = pack_bf16x2(f2 * up, f3 * up);
+                }
+                if (drafted) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (past)
+                            o[j] = 0;
+                        else
+                            hit |= clear_nonfinite(o[j]);
+                    }
+                }
+                uint8_t* p = dst + (c >> 2) * 16384 + row * 128;
+                *reinterpret_cast<uint4*>(p + ((((2 * c) & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(p + ((((2 * c + 1) & 7) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            if (hit) *reinterpret_cast<volatile int*>(smem + C::kPoison + (item & 7) * 4) = (int)item + 1;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(C::bPFull + sp));
+                mbar_arrive(bar(C::bLEmpty + sl));
+            }
+        }
+        ++item;
+    } while (w.next(a));
+}
+
+// ------------------------------------------------------------------------------------------------
+// MMA issue (one thread)
+// ------------------------------------------------------------------------------------------------
+template <bool kE4, int kNq>
+__device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint32_t tmem, TreeWalk w, const WaitCtl& ctl)
+{
+    using C = Cfg<kE4, kNq>;
+    auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
+    uint32_t kc = 0, vc = 0, item = 0, pc[2] = {0, 0};
+    bool ok = true;
+
+    // S of the next K tile into S_w (kNq == 2: w = 0 waits for the tile, w = 1 releases it)
+    auto score = [&](int wg, bool last) {
+        const int slot = (int)(kc % C::kSlotsK);
+        if (kNq == 1 || wg == 0) {
+            if (!mbar_wait(bar(C::bKFull + slot), (kc / C::kSlotsK) & 1, ctl)) return false;
+            tc_fence_after_sync();
+        }
+        issue_s<kE4, kNq>(sbase, tmem, wg, slot);
+        tc_commit(bar(C::bS + wg));
+        if (kNq == 1 || wg == 1) {
+            tc_commit(bar(C::bKEmpty + slot));
+            if (last) tc_commit(bar(C::bQEmpty));
+            ++kc;
+        }
+        return true;
+    };
+    // the V tile of the current job as the product takes it
+    auto v_wait = [&]() { return mbar_wait(bar(C::bPFull + (int)(vc % C::kSlotsP)), (vc / C::kSlotsP) & 1, ctl); };
+    auto weigh = [&](int wg, bool accumulate) {
+        if (!mbar_wait(bar(C::bP + wg), pc[wg]++ & 1, ctl)) return false;
+        tc_fence_after_sync();
+        const uint32_t v = kE4 ? sbase + C::kP + (vc % C::kSlotsP) * C::kBytesV : sbase + C::kL + (vc % C::kSlotsL) * C::kBytesK;
+        issue_pv(v, tmem, wg, accumulate);
+        tc_commit(bar(C::bO + wg));
+        return true;
+    };
+    auto v_done = [&]() {
+        if constexpr (kE4) {
+            tc_commit(bar(C::bPEmpty + (int)(vc % C::kSlotsP)));
+            tc_commit(bar(C::bXEmpty + (int)(vc % C::kSlotsX)));
+        } else {
+            tc_commit(bar(C::bLEmpty + (int)(vc % C::kSlotsL)));
+        }
+        ++vc;
+    };
+
+    do {
+        if (!mbar_wait(bar(C::bQFull), item++ & 1, ctl)) break;
+        tc_fence_after_sync();
+        const int n = w.t1 - w.t0;
+        if constexpr (kNq == 1) {
+            ok = score(0, n == 1);
+            if (ok && n > 1) ok = score(1, n == 2);
+            for (int i = 0; ok && i < n; ++i) {
+                const int wg = i & 1;
+                ok = v_wait() && weigh(wg, i >= 2);
+                if (!ok) break;
+                v_done();
+                if (i + 2 < n) ok = score(wg, i + 2 == n - 1);
+            }
+        } else {
+            ok = score(0, false) && score(1, n == 1);
+            for (int i = 0; ok && i < n; ++i) {
+                const bool more = i + 1 < n;
+                ok = v_wait() && weigh(0, i > 0);
+                if (ok && more) ok = score(0, false);
+                ok = ok && weigh(1, i > 0);
+                if (!ok) break;
+                v_done();
+                if (more) ok = score(1, i + 1 == n - 1);
+            }
+        }
+    } while (ok && w.next(a));
+    tc_commit(bar(C::bDrain));
+    drain_wait(bar(C::bDrain), 0);
+}
+
+// ------------------------------------------------------------------------------------------------
+// softmax warpgroups
+// ------------------------------------------------------------------------------------------------
+// Which of the tile's 128 rows (from k0) query token t sees, one bit each; only for tiles that reach past the prefix.
+__device__ __forceinline__ void seen_bits(const TreeArgs& a, const TreeSeq& s, int b, int t, int k0, uint32_t (&bits)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int p = s.len - (k0 + i * 32);  // rows of this word in the prefix
+        bits[i] = p >= 32 ? 0xffffffffu : (p > 0 ? (1u << p) - 1u : 0u);
+    }
+    const int j0 = k0 > s.len ? k0 - s.len : 0;
+    const int j1 = k0 + kTreeTile - s.len < s.cnt ? k0 + kTreeTile - s.len : s.cnt;
+    if (t >= s.cnt) return;
+    const uint8_t* m = a.mask ? a.mask + ((a.mask_batched ? (long long)b * a.T : 0) + t) * a.T : nullptr;
+#pragma unroll 8
+    for (int j = j0; j < j1; ++j) {
+        const bool sees = m ? m[j] != 0 : j <= t;
+        const int c = s.len + j - k0;
+        const uint32_t one = sees ? 1u << (c & 31) : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c >> 5 == i) bits[i] |= one;
+    }
+}
+
+template <bool kE4, int kNq>
+__device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, uint8_t* smem, uint32_t tmem, TreeWalk w,
+                                             const WaitCtl& ctl)
+{
+    using C = Cfg<kE4, kNq>;
+    auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wg = warp >> 2;
+    const int rw = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + kColS + (uint32_t)wg * 128;
+    const uint32_t tO = tmem + lanes + kColO + (uint32_t)wg * 128;
+    uint32_t jobs[2] = {0, 0};  // S tiles of each warpgroup so far
+    uint32_t tiles = 0, item = 0;
+
+    do {
+        const int x = w.r * a.rt + (kNq == 2 ? wg * 128 : 0) + rw;  // query row of the kv head
+        const int tq = x % a.T;
+        const bool live = x < a.R && tq < w.s.cnt;
+        const bool any_live = __any_sync(0xffffffffu, live);
+        const int n = w.t1 - w.t0;
+        float m_run = -INFINITY, l_run = 0.f, c_run = 0.f, sl2 = a.scale_log2;
+        bool first = true;
+        for (int i = kNq == 1 ? wg : 0; i < n; i += kNq == 1 ? 2 : 1) {
+            const int k0 = (w.t0 + i) * kTreeTile;
+            const bool masked = k0 + kTreeTile > w.s.len;
+            uint32_t bits[4];
+            if (masked) seen_bits(a, w.s, w.b, tq, k0, bits);
+            const uint32_t job = jobs[wg]++;
+            if (!warp_wait(bar(C::bS + wg), job & 1, ctl)) return;
+            if (!any_live) {  // no query row in these lanes: what P holds there reaches no row that is read
+                if (lane == 0) mbar_arrive(bar(C::bP + wg));
+                continue;
+            }
+            tc_fence_after_sync();
+            const float* xs = nullptr;
+            if constexpr (kE4) {
+                const uint32_t xc = tiles + (uint32_t)i;
+                if (!warp_wait(bar(C::bXFull + (int)(xc % C::kSlotsX)), (xc / C::kSlotsX) & 1, ctl)) return;
+                xs = reinterpret_cast<const float*>(smem + C::kX + (xc % C::kSlotsX) * 1024);
+                if (first)
+                    sl2 = a.scale_log2 * reinterpret_cast<const float*>(smem + C::kQs)[(item & 1) * kNq * 128 + (kNq == 2 ? wg * 128 : 0) + rw];
+            }
+            uint32_t r[4][32];
+            float m8[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m8[e] = -INFINITY;
+            tmem_ld_32x32b_x32(tS + 0, r[0]);
+            tmem_ld_32x32b_x32(tS + 32, r[1]);
+            tmem_ld_wait(r[0]);
+            tmem_ld_wait(r[1]);
+            tmem_ld_32x32b_x32(tS + 64, r[2]);
+            tmem_ld_32x32b_x32(tS + 96, r[3]);
+#pragma unroll
+            for (int c4 = 0; c4 < 4; ++c4) {
+                if (c4 == 2) {
+                    tmem_ld_wait(r[2]);
+                    tmem_ld_wait(r[3]);
+                }
+                if constexpr (kE4) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 sc = *reinterpret_cast<const float4*>(xs + c4 * 32 + e);
+                        const float2 u0 = mul2(make_float2(__uint_as_float(r[c4][e]), __uint_as_float(r[c4][e + 1])), make_float2(sc.x, sc.y));
+                        const float2 u1 = mul2(make_float2(__uint_as_float(r[c4][e + 2]), __uint_as_float(r[c4][e + 3])), make_float2(sc.z, sc.w));
+                        r[c4][e] = __float_as_uint(u0.x);
+                        r[c4][e + 1] = __float_as_uint(u0.y);
+                        r[c4][e + 2] = __float_as_uint(u1.x);
+                        r[c4][e + 3] = __float_as_uint(u1.y);
+                    }
+                }
+                if (masked) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!(bits[c4] >> e & 1u)) r[c4][e] = __float_as_uint(-INFINITY);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 2)
+                    m8[(e >> 1) & 7] = max3f(m8[(e >> 1) & 7], __uint_as_float(r[c4][e]), __uint_as_float(r[c4][e + 1]));
+            }
+            const float mx = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+            const float m_tile = mx * sl2;
+            const float m_new = m_tile > m_run + 8.0f ? m_tile : m_run;
+            const float alpha = m_new == m_run ? 1.0f : ex2_approx(m_run - m_new);
+            const float ref = m_new == -INFINITY ? 0.f : m_new;
+            const float2 scale2 = make_float2(sl2, sl2), nref2 = make_float2(-ref, -ref);
+            float2 s4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s4[e] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc) {
+                    const int c4 = half * 2 + cc;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 x2 = fma2(make_float2(__uint_as_float(r[c4][e]), __uint_as_float(r[c4][e + 1])), scale2, nref2);
+                        const float2 p2 = make_float2(ex2_approx(x2.x), ex2_approx(x2.y));
+                        s4[(e >> 1) & 3] = add2(s4[(e >> 1) & 3], p2);
+                        pk[cc * 16 + e / 2] = pack_bf16x2(p2.x, p2.y);
+                    }
+                }
+                tmem_st_32x32b_x32(tS + half * 32, pk);
+            }
+            const float2 s2 = add2(add2(s4[0], s4[1]), add2(s4[2], s4[3]));
+            // the largest weight's rounding to bf16 goes into the normaliser, so that a row that one key
+            // dominates is divided by the weight that its V row got; lse keeps the unrounded sum
+            const float p_max = mx == -INFINITY ? 0.f : ex2_approx(fmaf(mx, sl2, -ref));
+            const float p_max_bf16 = __uint_as_float(pack_bf16x2(p_max, 0.f) << 16);
+            l_run = l_run * alpha + (s2.x + s2.y);
+            c_run = c_run * alpha + (p_max_bf16 - p_max);
+            tmem_st_wait();
+            if (__any_sync(0xffffffffu, !first && live && alpha != 1.0f)) {
+                if (!warp_wait(bar(C::bO + wg), (job - 1) & 1, ctl)) return;
+                tc_fence_after_sync();
+#pragma unroll 1
+                for (int c4 = 0; c4 < kHd / 32; ++c4) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(tO + c4 * 32, o);
+                    tmem_ld_wait(o);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 v = mul2(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), make_float2(alpha, alpha));
+                        o[e] = __float_as_uint(v.x);
+                        o[e + 1] = __float_as_uint(v.y);
+                    }
+                    tmem_st_32x32b_x32(tO + c4 * 32, o);
+                }
+                tmem_st_wait();
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::bP + wg));
+            m_run = m_new;
+            first = false;
+        }
+
+        // the item's rows: O of both warpgroups (kNq == 1), or of this one
+        float m = m_run, l = l_run, den = l_run + c_run, w0 = 1.f, w1 = 0.f;
+        const int n1 = kNq == 1 ? n >> 1 : 0;
+        if constexpr (kNq == 1) {
+            jobs[wg ^ 1] += (uint32_t)(wg == 0 ? n1 : n - n1);
+            float4* ml = reinterpret_cast<float4*>(smem + C::kMl);
+            ml[wg * 128 + rw] = make_float4(m, l, den, 0.f);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::bEpi));
+            if (!warp_wait(bar(C::bEpi), item & 1, ctl)) return;
+            const float4 a0 = ml[rw], a1 = ml[128 + rw];
+            m = fmaxf(a0.x, a1.x);
+            const float ref = m == -INFINITY ? 0.f : m;
+            w0 = ex2_approx(a0.x - ref);
+            w1 = ex2_approx(a1.x - ref);
+            l = a0.y * w0 + a1.y * w1;
+            den = a0.z * w0 + a1.z * w1;
+            if (a0.x == -INFINITY && a0.y != 0.f) l = den = a0.y;  // NaN scores alone leave no maximum
+            if (a1.x == -INFINITY && a1.y != 0.f) l = den = a1.y;
+            if (!warp_wait(bar(C::bO + 0), (jobs[0] - 1) & 1, ctl)) return;
+            if (n1 > 0 && !warp_wait(bar(C::bO + 1), (jobs[1] - 1) & 1, ctl)) return;
+        } else {
+            if (!warp_wait(bar(C::bO + wg), (jobs[wg] - 1) & 1, ctl)) return;
+        }
+        tc_fence_after_sync();
+        if (any_live) {
+            const bool whole = w.whole(), none = m == -INFINITY && l == 0.f;
+            const bool poison = *reinterpret_cast<volatile int*>(smem + C::kPoison + (item & 7) * 4) == (int)item + 1;
+            const float inv = whole ? (none ? 0.f : 1.0f / den) : 1.0f;
+            const long long grow = ((long long)w.b * a.Hkv + w.g) * a.R + x;
+            const long long prow = ((long long)blockIdx.x * 2 + (w.first ? 0 : 1)) * a.rt + (kNq == 2 ? wg * 128 : 0) + rw;
+            constexpr int kCols = kNq == 1 ? kHd / 2 : kHd;
+            const int col0 = kNq == 1 ? wg * kCols : 0;
+#pragma unroll 1
+            for (int c = col0; c < col0 + kCols; c += 32) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(tmem + lanes + kColO + (kNq == 2 ? (uint32_t)wg * 128u : 0u) + c, o);
+                tmem_ld_wait(o);
+                if constexpr (kNq == 1) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w0);
+                    if (n1 > 0) {
+                        uint32_t o1[32];
+                        tmem_ld_32x32b_x32(tmem + lanes + kColO + 128 + c, o1);
+                        tmem_ld_wait(o1);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), w1, __uint_as_float(o[e])));
+                    }
+                }
+                if (poison && live) {
+                    for (int j = 0; j < w.s.cnt; ++j) {
+                        const int key = w.s.len + j;
+                        if (key < w.t0 * kTreeTile || key >= w.t1 * kTreeTile || !tree_sees(a, w.b, tq, j)) continue;
+                        const long long src = ((long long)w.b * a.Hkv + w.g) * a.cap + key;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float v;
+                            if constexpr (kE4) {
+                                float z0, z1, z2;
+                                e4m3x4_to_float(static_cast<const uint8_t*>(a.v)[src * kHd + c + e], v, z0, z1, z2);
+                                v *= __uint_as_float((uint32_t)a.v_exp[src] << 23);
+                            } else {
+                                v = __bfloat162float(static_cast<const __nv_bfloat16*>(a.v)[src * kHd + c + e]);
+                            }
+                            if (!(fabsf(v) <= 3.3895314e38f)) o[e] = __float_as_uint(__uint_as_float(o[e]) + v);  // past bf16's largest
+                        }
+                    }
+                }
+                if (!live) continue;
+                if (whole && a.bf16_out) {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + grow * kHd + c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            pk[i] = none ? 0u
+                                         : pack_bf16x2(__uint_as_float(o[8 * e + 2 * i]) * inv, __uint_as_float(o[8 * e + 2 * i + 1]) * inv);
+                        dst[e] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(whole ? static_cast<float*>(a.out) + grow * kHd + c : a.part_o + prow * kHd + c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[e] = none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                      : make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                                    __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+                }
+            }
+            if (live && (kNq == 2 || wg == 0)) {
+                if (whole)
+                    a.lse[grow] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+                else
+                    *reinterpret_cast<float4*>(a.part_ml + prow * 4) = make_float4(m, l, den, 0.f);
+            }
+        }
+        if constexpr (kNq == 1) {  // the next item's products overwrite both O's
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::bEpi + 1));
+            if (!warp_wait(bar(C::bEpi + 1), item & 1, ctl)) return;
+            tc_fence_after_sync();
+        }
+        tiles += (uint32_t)n;
+        ++item;
+    } while (w.next(a));
+}
+
+template <bool kE4, int kNq>
+__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ Maps maps, const TreeArgs a)
+{
+    using C = Cfg<kE4, kNq>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kAbort);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kSlot);
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kBars; ++i) {
+            uint32_t cnt = 1;
+            if (i == C::bP || i == C::bP + 1) cnt = 4;                              // softmax warps of one group
+            if (i == C::bEpi || i == C::bEpi + 1) cnt = 8;                          // of both
+            if (i >= C::bPFull && i < C::bPEmpty) cnt = 4;                          // warps 12-15
+            if (kE4 && (i == C::bQFull || (i >= C::bLEmpty && i < C::bPFull))) cnt = 4;
+            mbar_init(sbase + C::kBar + 8u * (uint32_t)i, cnt);
+        }
+        for (int i = 0; i < 8; ++i) reinterpret_cast<int*>(smem + C::kPoison)[i] = 0;
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    TreeWalk w;
+    const bool work = w.begin(a, blockIdx.x);  // the same for every warp
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtl ctl{abort_flag, a.status, kWaitLimitNs};
+
+    // launched with 512 x 128 registers; 2 x 128 x 192 + 2 x 128 x 64 = 65536
+    if (warp < 8)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;" ::: "memory");
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
+
+    if (work) {
+        if (warp < 8) {
+            softmax_role<kE4, kNq>(a, sbase, smem, tmem, w, ctl);
+        } else if (warp == 8) {
+            if (lane == 0) load_qk_role<kE4, kNq>(a, sbase, maps, w, ctl);
+        } else if (warp == 9) {
+            if (lane == 0) mma_role<kE4, kNq>(a, sbase, tmem, w, ctl);
+        } else if (warp == 10) {
+            if (lane == 0) load_v_role<kE4, kNq>(a, sbase, maps, w, ctl);
+        } else if (warp == 11) {
+            if constexpr (kE4) scale_role<kNq>(a, sbase, smem, w, ctl);
+        } else {
+            if constexpr (kE4)
+                prep_e4m3_role<kNq>(a, sbase, smem, w, ctl);
+            else
+                prep_bf16_role<kNq>(a, sbase, smem, w, ctl);
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// host side
+// ------------------------------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// [heads][rows][kHd] of 1- or 2-byte elements, boxes of 128 rows and the swizzled row's columns (64 bf16, all e4m3).
+bool make_map(CUtensorMap* map, const void* base, long long rows, long long heads, bool bytes)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t es = bytes ? 1 : 2;
+    cuuint64_t dims[3] = {(cuuint64_t)kHd, (cuuint64_t)rows, (cuuint64_t)heads};
+    cuuint64_t strides[2] = {(cuuint64_t)kHd * es, (cuuint64_t)rows * kHd * es};
+    cuuint32_t box[3] = {bytes ? (cuuint32_t)kHd : 64u, 128u, 1u};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              bytes && kHd == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kE4, int kNq>
+cudaError_t launch(const TreeArgs& a, const Maps& maps, cudaStream_t s)
+{
+    using C = Cfg<kE4, kNq>;
+    static std::mutex mu;
+    static bool done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!done[dev]) {
+            e = cudaFuncSetAttribute(tree_tc_kernel<kE4, kNq>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+            if (e != cudaSuccess) return e;
+            done[dev] = true;
+        }
+    }
+    tree_tc_kernel<kE4, kNq><<<a.ctas, kThreads, C::kSmem, s>>>(maps, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t RA_TREE_LAUNCH(const TreeArgs& a, bool e4m3, cudaStream_t s)
+{
+    Maps maps;
+    const long long heads = (long long)a.B * a.Hkv;
+    if (!make_map(&maps.q, a.q, a.R, heads, false) || !make_map(&maps.k, a.k, a.cap, heads, e4m3) ||
+        !make_map(&maps.v, a.v, a.cap, heads, e4m3))
+        return cudaErrorInvalidValue;
+    if (a.rt == 128) return e4m3 ? launch<true, 1>(a, maps, s) : launch<false, 1>(a, maps, s);
+    return e4m3 ? launch<true, 2>(a, maps, s) : launch<false, 2>(a, maps, s);
+}
+
+}  // namespace ra

@@ -78,6 +78,24 @@ def test_against_float64(B, H, Hkv, T, d, cap, lens, ntok, tree, dtype, cdt):
 
 
 @pytest.mark.parametrize("dtype,cdt", TYPES)
+@pytest.mark.parametrize("B,H,Hkv,T,d,cap,lens", [
+    (1, 16, 4, 8, 128, 20000, [19000]),         # several tiles per CTA, the last with rows past the end
+    (1, 2, 1, 3, 64, 60000, [59001]),
+    (1, 32, 1, 5, 128, 30000, [29995]),         # two query tiles
+    (40, 4, 4, 2, 128, 700, [601 + b for b in range(40)]),  # several items per CTA
+    (16, 20, 2, 15, 64, 500, [30 * b for b in range(16)]),  # and two query tiles
+])
+def test_several_tiles_and_items_per_cta(B, H, Hkv, T, d, cap, lens, dtype, cdt):
+    cache = _cache(B, Hkv, cap, d, dtype, cdt, seed=cap)
+    q = _randn(B, H, T, d, seed=T, dtype=dtype)
+    first = _check(q, cache, lens, cu.random_tree(B, T, cap), None)
+    mask = cu.random_tree(B, T, cap).to(DEV)
+    for _ in range(20):
+        again = ra.tree_fwd(q, cache, _i32(lens), mask=mask)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@pytest.mark.parametrize("dtype,cdt", TYPES)
 def test_peaked_scores_and_a_maximum_that_grows(dtype, cdt):
     """Large keys: the running maximum grows over the tiles, by more than any rescale threshold; then one key far
     above all others, at the end, in the middle, at the start."""
