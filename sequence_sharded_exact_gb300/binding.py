@@ -54,6 +54,8 @@ class RingAttnError(RuntimeError):
 def library():
     """The loaded ctypes library (raises RingAttnError if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -728,33 +730,58 @@ def block_rope(x, n_shards, shard, layout="zigzag", base=10000.0, inverse=False,
 # ------------------------------------------------------------------------------------------------
 # Norms and rotation of queries and keys, the key/value cache and the attention over it
 # ------------------------------------------------------------------------------------------------
-def _on(device, call, *args):
-    """Calls the library with `device` current: a kernel is launched on the device of its tensors."""
-    if torch.cuda.current_device() == device.index:
-        _check(call(*args))
+# The calls of a serving step take a few microseconds on the GPU, so their checks are kept cheap: one expression
+# per tensor on the way that passes, and the checks that name what is wrong only where it fails.
+_Strides = ctypes.c_longlong * 3
+_E4M3 = torch.float8_e4m3fn
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_ptr(stream, index):
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _run(index, call, *args):
+    """Calls the library with device `index` current: a kernel is launched on the device of its tensors."""
+    if torch.cuda.current_device() == index:
+        st = call(*args)
     else:
-        with torch.cuda.device(device):
-            _check(call(*args))
+        with torch.cuda.device(index):
+            st = call(*args)
+    if st != RA_OK:
+        _check(st)
 
 
-def _need_rows(t, name, device, shape, dtype):
-    """A tensor read by strides: any [B, heads, rows, d] whose rows are contiguous and lie on 16-byte
-    boundaries.  Returns its (batch, head, row) element strides, or None if it is contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.dtype != dtype:
+def _fits(t, name, device, shape, dtype):
+    """A contiguous tensor of this device, shape and dtype; returns its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda
+            and t.is_contiguous()):
+        _need(t, name, device, shape, dtype)
+    return t.data_ptr()
+
+
+def _rows(t, name, device, shape, dtype):
+    """A tensor read by strides: any [B, heads, rows, d] whose rows are contiguous and lie on 16-byte boundaries.
+    Returns its address and its (batch, head, row) element strides, None if it is contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda or t.device != device:
+            raise ValueError(f"{name} must be a CUDA tensor on {device}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.is_contiguous():
-        return None
-    per = 16 // t.element_size()
-    strides = t.stride()
-    if strides[3] != 1 or any(n > 1 and s % per for n, s in zip(shape[:3], strides)):
-        raise ValueError(f"{name} must have contiguous rows on 16-byte boundaries")
-    return (ctypes.c_longlong * 3)(*strides[:3])
+        return t.data_ptr(), None
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1 or (s0 | s1 | s2) % (16 // t.element_size()):
+        per = 16 // t.element_size()
+        if s3 != 1 or any(n > 1 and s % per for n, s in zip(shape, (s0, s1, s2))):
+            raise ValueError(f"{name} must have contiguous rows on 16-byte boundaries")
+    return t.data_ptr(), _Strides(s0, s1, s2)
 
 
 def as_rows(t):
@@ -766,34 +793,35 @@ def as_rows(t):
     return t.clone(memory_format=torch.contiguous_format)
 
 
-def _rows_dims(q, k, name="q"):
+def _dims4(q, k, name):
+    """The shapes [B, heads, rows, d] of two tensors and q's dtype code."""
     if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor):
         raise TypeError("the inputs must be torch tensors")
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError(f"{name} must be [B, heads, rows, d]")
-    _dtype_code(q.dtype)
-    return tuple(q.shape) + (k.shape[1],)
+    code = _DTYPES.get(q.dtype)
+    return q.shape, k.shape, _dtype_code(q.dtype) if code is None else code
 
 
 def _norm_rope_args(q, k, wq, wk, n_shards, layout, base, eps, shard, positions):
-    B, H, rows, d, Hkv = _rows_dims(q, k, "q and k")
-    dev = q.device
-    qs = _need_rows(q, "q", dev, (B, H, rows, d), q.dtype)
-    ks = _need_rows(k, "k", dev, (B, Hkv, rows, d), q.dtype)
-    _need(wq, "wq", dev, (d,), torch.float32)
-    _need(wk, "wk", dev, (d,), torch.float32)
+    (B, H, rows, d), (_, Hkv, _, _), code = _dims4(q, k, "q and k")
+    dev, dt = q.device, q.dtype
+    qp, qs = _rows(q, "q", dev, (B, H, rows, d), dt)
+    kp, ks = _rows(k, "k", dev, (B, Hkv, rows, d), dt)
+    head = (qp, qs, kp, ks, _fits(wq, "wq", dev, (d,), torch.float32), _fits(wk, "wk", dev, (d,), torch.float32))
     n = int(n_shards)
+    L, which, pos = rows, -1, None
     if positions is not None:
-        _need(positions, "positions", dev, (B, rows), torch.int32)
+        pos = _fits(positions, "positions", dev, (B, rows), torch.int32)
         if shard is not None or n != 1:
             raise ValueError("positions stand in place of a layout: n_shards must be 1 and shard None")
-    if shard is not None and not 0 <= int(shard) < n:
-        raise ValueError("shard must lie in [0, n_shards)")
-    L = rows if shard is None else n * rows
-    tail = (B, H, Hkv, L, d, n, -1 if shard is None else int(shard),
-            LAYOUTS["contiguous"] if positions is not None else _layout(layout), _dtype_code(q.dtype), float(base), float(eps),
-            None if positions is None else positions.data_ptr())
-    return qs, ks, tail
+        layout = 0
+    elif shard is not None:
+        which = int(shard)
+        if not 0 <= which < n:
+            raise ValueError("shard must lie in [0, n_shards)")
+        L = n * rows
+    return head, (B, H, Hkv, L, d, n, which, _layout(layout), code, float(base), float(eps), pos)
 
 
 def qk_norm_rope(q, k, wq, wk, n_shards=1, layout="contiguous", base=10000.0, eps=1e-6, shard=None, positions=None,
@@ -803,18 +831,14 @@ def qk_norm_rope(q, k, wq, wk, n_shards=1, layout="contiguous", base=10000.0, ep
     layout's over n_shards shards, shard `shard`'s of them, or positions [B, rows] int32.  q and k may be
     slices of a fused projection (rows contiguous, on 16-byte boundaries).  Returns (q_out, k_out), contiguous,
     in q's dtype; q_out may be q and k_out may be k, where those are contiguous."""
-    qs, ks, tail = _norm_rope_args(q, k, wq, wk, n_shards, layout, base, eps, shard, positions)
-    dev = q.device
+    head, tail = _norm_rope_args(q, k, wq, wk, n_shards, layout, base, eps, shard, positions)
+    dev, dt = q.device, q.dtype
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    else:
-        _need(q_out, "q_out", dev, q.shape, q.dtype)
+        q_out = torch.empty(q.shape, dtype=dt, device=dev)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-    else:
-        _need(k_out, "k_out", dev, k.shape, q.dtype)
-    _on(dev, library().ring_attn_qk_norm_rope, q.data_ptr(), qs, k.data_ptr(), ks, wq.data_ptr(), wk.data_ptr(),
-        q_out.data_ptr(), k_out.data_ptr(), *tail, _stream(stream, dev))
+        k_out = torch.empty(k.shape, dtype=dt, device=dev)
+    _run(dev.index, library().ring_attn_qk_norm_rope, *head, _fits(q_out, "q_out", dev, q.shape, dt),
+         _fits(k_out, "k_out", dev, k.shape, dt), *tail, _stream_ptr(stream, dev.index))
     return q_out, k_out
 
 
@@ -822,28 +846,23 @@ def qk_norm_rope_bwd(q, k, wq, wk, dq_out, dk_out, n_shards=1, layout="contiguou
                      positions=None, dq=None, dk=None, workspace=None, stream=None):
     """ring_attn_qk_norm_rope_bwd: the gradients of qk_norm_rope's inputs from those of its outputs (contiguous).
     Returns (dq, dk) in q's dtype, contiguous (dq may be dq_out, dk may be dk_out), and (dwq, dwk) [d] float32."""
-    qs, ks, tail = _norm_rope_args(q, k, wq, wk, n_shards, layout, base, eps, shard, positions)
-    dev = q.device
-    _need(dq_out, "dq_out", dev, q.shape, q.dtype)
-    _need(dk_out, "dk_out", dev, k.shape, q.dtype)
+    head, tail = _norm_rope_args(q, k, wq, wk, n_shards, layout, base, eps, shard, positions)
+    dev, dt, d = q.device, q.dtype, q.shape[3]
+    gq, gk = _fits(dq_out, "dq_out", dev, q.shape, dt), _fits(dk_out, "dk_out", dev, k.shape, dt)
     if dq is None:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    else:
-        _need(dq, "dq", dev, q.shape, q.dtype)
+        dq = torch.empty(q.shape, dtype=dt, device=dev)
     if dk is None:
-        dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
-    else:
-        _need(dk, "dk", dev, k.shape, q.dtype)
-    d = q.shape[3]
-    dwq = torch.empty(d, dtype=torch.float32, device=dev)
-    dwk = torch.empty(d, dtype=torch.float32, device=dev)
-    need = int(library().ring_attn_qk_norm_rope_bwd_workspace_size(d))
+        dk = torch.empty(k.shape, dtype=dt, device=dev)
+    dwq, dwk = torch.empty(d, dtype=torch.float32, device=dev), torch.empty(d, dtype=torch.float32, device=dev)
+    lib = library()
+    need = lib.ring_attn_qk_norm_rope_bwd_workspace_size(d)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _need_workspace(workspace, need, dev)
-    _on(dev, library().ring_attn_qk_norm_rope_bwd, q.data_ptr(), qs, k.data_ptr(), ks, wq.data_ptr(), wk.data_ptr(),
-        dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dwq.data_ptr(), dwk.data_ptr(),
-        workspace.data_ptr(), workspace.numel(), *tail, _stream(stream, dev))
+    else:
+        _need_workspace(workspace, need, dev)
+    _run(dev.index, lib.ring_attn_qk_norm_rope_bwd, *head, gq, gk, _fits(dq, "dq", dev, q.shape, dt),
+         _fits(dk, "dk", dev, k.shape, dt), dwq.data_ptr(), dwk.data_ptr(), workspace.data_ptr(), workspace.numel(), *tail,
+         _stream_ptr(stream, dev.index))
     return dq, dk, dwq, dwk
 
 
@@ -857,46 +876,36 @@ class KVCache(NamedTuple):
     v_exp: Optional[torch.Tensor] = None
 
 
-def cache_alloc(B, Hkv, cap, d, dtype=torch.float8_e4m3fn, device=None):
+def cache_alloc(B, Hkv, cap, d, dtype=_E4M3, device=None):
     """A KVCache of zeros: dtype float8_e4m3fn (quantised as it is written), bfloat16 or float32."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     _cache_code(dtype)
     k, v = (torch.zeros((B, Hkv, cap, d), dtype=dtype, device=dev) for _ in range(2))
-    if dtype != torch.float8_e4m3fn:
+    if dtype != _E4M3:
         return KVCache(k, v)
     return KVCache(k, v, *(torch.zeros((B, Hkv, cap), dtype=torch.uint8, device=dev) for _ in range(2)))
 
 
 def _cache_code(dtype):
-    return RA_E4M3 if dtype == torch.float8_e4m3fn else _dtype_code(dtype)
+    return RA_E4M3 if dtype == _E4M3 else _dtype_code(dtype)
 
 
-def _need_cache(cache, device, B, Hkv, d, dtype):
-    """Checks a cache against the tensors it is used with; returns its arguments (pointers) and (cap, code)."""
+def _cache_args(cache, device, B, Hkv, d, dtype):
+    """Checks a cache against the tensors it is used with; returns its addresses, its rows and its dtype's code."""
     k, v, ke, ve = cache
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("the cache's k must be a [B, Hkv, cap, d] tensor")
-    cap = k.shape[2]
+    cap, kind = k.shape[2], k.dtype
     shape = (B, Hkv, cap, d)
-    code = _cache_code(k.dtype)
-    if code != RA_E4M3 and k.dtype != dtype:
-        raise ValueError(f"the cache must hold {dtype} or float8_e4m3fn, not {k.dtype}")
-    _need(k, "the cache's k", device, shape)
-    _need(v, "the cache's v", device, shape, k.dtype)
-    if code != RA_E4M3:
-        return (k.data_ptr(), v.data_ptr(), None, None), cap, code
-    _need(ke, "the cache's k_exp", device, shape[:3], torch.uint8)
-    _need(ve, "the cache's v_exp", device, shape[:3], torch.uint8)
-    return (k.data_ptr(), v.data_ptr(), ke.data_ptr(), ve.data_ptr()), cap, code
-
-
-def _need_lengths(t, name, device, B, optional=True):
-    if t is None:
-        if not optional:
-            raise ValueError(f"{name} is required")
-        return None
-    _need(t, name, device, (B,), torch.int32)
-    return t.data_ptr()
+    if kind is not _E4M3:
+        if kind is not dtype:
+            raise ValueError(f"the cache must hold {dtype} or float8_e4m3fn, not {kind}")
+        return (_fits(k, "the cache's k", device, shape, kind), _fits(v, "the cache's v", device, shape, kind), None, None), cap, \
+            _DTYPES[kind]
+    rows = shape[:3]
+    return (_fits(k, "the cache's k", device, shape, kind), _fits(v, "the cache's v", device, shape, kind),
+            _fits(ke, "the cache's k_exp", device, rows, torch.uint8), _fits(ve, "the cache's v_exp", device, rows, torch.uint8)), \
+        cap, RA_E4M3
 
 
 def cache_write(cache, k, v, lens=None, ntok=None, stream=None):
@@ -904,13 +913,16 @@ def cache_write(cache, k, v, lens=None, ntok=None, stream=None):
     lens[b] + t (t without lens) of the cache, quantised there if it is float8_e4m3fn.  lens, ntok: int32 [B] on
     the device.  k and v may be slices of a fused projection.  Rows outside the cache are not written (the
     device status word then has the range bit).  Returns the cache."""
-    B, Hkv, T, d, _ = _rows_dims(k, v, "k and v")
-    dev = k.device
-    ks = _need_rows(k, "k", dev, (B, Hkv, T, d), k.dtype)
-    vs = _need_rows(v, "v", dev, (B, Hkv, T, d), k.dtype)
-    ptrs, cap, code = _need_cache(cache, dev, B, Hkv, d, k.dtype)
-    _on(dev, library().ring_attn_cache_write, k.data_ptr(), ks, v.data_ptr(), vs, *ptrs, _need_lengths(lens, "lens", dev, B),
-        _need_lengths(ntok, "ntok", dev, B), B, Hkv, T, d, cap, _dtype_code(k.dtype), code, _stream(stream, dev))
+    shape, _, code = _dims4(k, v, "k and v")
+    B, Hkv, T, d = shape
+    dev, dt = k.device, k.dtype
+    kp, ks = _rows(k, "k", dev, shape, dt)
+    vp, vs = _rows(v, "v", dev, shape, dt)
+    ptrs, cap, kind = _cache_args(cache, dev, B, Hkv, d, dt)
+    _run(dev.index, library().ring_attn_cache_write, kp, ks, vp, vs, *ptrs,
+         None if lens is None else _fits(lens, "lens", dev, (B,), torch.int32),
+         None if ntok is None else _fits(ntok, "ntok", dev, (B,), torch.int32), B, Hkv, T, d, cap, code, kind,
+         _stream_ptr(stream, dev.index))
     return cache
 
 
@@ -921,8 +933,8 @@ def cache_read(cache, rows, row0=0, dtype=torch.bfloat16, k=None, v=None, stream
         raise ValueError("the cache's k must be a [B, Hkv, cap, d] tensor")
     B, Hkv, _, d = cache.k.shape
     dev = cache.k.device
-    code_out = _dtype_code(dtype)
-    ptrs, cap, code = _need_cache(cache, dev, B, Hkv, d, dtype)
+    code = _dtype_code(dtype)
+    ptrs, cap, kind = _cache_args(cache, dev, B, Hkv, d, dtype)
     rows, row0 = int(rows), int(row0)
     if rows < 0 or row0 < 0 or row0 + rows > cap:
         raise ValueError(f"rows [{row0}, {row0 + rows}) lie outside the cache ({cap} rows)")
@@ -931,10 +943,8 @@ def cache_read(cache, rows, row0=0, dtype=torch.bfloat16, k=None, v=None, stream
         k = torch.empty(shape, dtype=dtype, device=dev)
     if v is None:
         v = torch.empty(shape, dtype=dtype, device=dev)
-    _need(k, "k", dev, shape, dtype)
-    _need(v, "v", dev, shape, dtype)
-    _on(dev, library().ring_attn_cache_read, *ptrs, k.data_ptr(), v.data_ptr(), B, Hkv, row0, rows, d, cap, code_out, code,
-        _stream(stream, dev))
+    _run(dev.index, library().ring_attn_cache_read, *ptrs, _fits(k, "k", dev, shape, dtype), _fits(v, "v", dev, shape, dtype), B,
+         Hkv, row0, rows, d, cap, code, kind, _stream_ptr(stream, dev.index))
     return k, v
 
 
@@ -948,37 +958,32 @@ def tree_fwd(q, cache, lens, mask=None, ntok=None, out_dtype=None, out=None, lse
     [0, lens[b]), and the step's tokens j < ntok[b] with mask[b, t, j] ([B, T, T] or [T, T] bool; without a mask
     j <= t).  lens, ntok: int32 [B] on the device.  Returns (out [B, H, T, d] in out_dtype -- q's, or float32 --
     and lse [B, H, T] float32); a row that sees nothing, and tokens t >= ntok[b], have 0 and -infinity."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be a [B, H, T, d] tensor")
-    if not isinstance(cache.k, torch.Tensor) or cache.k.dim() != 4:
-        raise ValueError("the cache's k must be a [B, Hkv, cap, d] tensor")
-    B, H, T, d = q.shape
-    Hkv, dev = cache.k.shape[1], q.device
-    _need(q, "q", dev)
-    code_q = _dtype_code(q.dtype)
-    ptrs, cap, code = _need_cache(cache, dev, B, Hkv, d, q.dtype)
-    out_dtype = q.dtype if out_dtype is None else out_dtype
-    if out_dtype not in (q.dtype, torch.float32):
+    (B, H, T, d), kshape, code = _dims4(q, cache.k, "q and the cache's k")
+    Hkv, dev, dt = kshape[1], q.device, q.dtype
+    qp = _fits(q, "q", dev, q.shape, dt)
+    ptrs, cap, kind = _cache_args(cache, dev, B, Hkv, d, dt)
+    if out_dtype is None:
+        out_dtype = dt
+    elif out_dtype not in (dt, torch.float32):
         raise ValueError("out_dtype must be q's dtype or float32")
-    mask_ptr, batched = None, 0
+    if lens is None:
+        raise ValueError("lens is required")
+    mp, batched = None, 0
     if mask is not None:
         batched = int(isinstance(mask, torch.Tensor) and mask.dim() == 3)
-        _need(mask, "mask", dev, (B, T, T) if batched else (T, T), torch.bool)
-        mask_ptr = mask.data_ptr()
+        mp = _fits(mask, "mask", dev, (B, T, T) if batched else (T, T), torch.bool)
     if out is None:
         out = torch.empty(q.shape, dtype=out_dtype, device=dev)
-    else:
-        _need(out, "out", dev, q.shape, out_dtype)
     if lse is None:
         lse = torch.empty((B, H, T), dtype=torch.float32, device=dev)
-    else:
-        _need(lse, "lse", dev, (B, H, T), torch.float32)
-    need = int(library().ring_attn_tree_fwd_workspace_size(B, H, Hkv, T, d, cap, code_q, code))
+    lib = library()
+    need = lib.ring_attn_tree_fwd_workspace_size(B, H, Hkv, T, d, cap, code, kind)
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
     else:
         _need_workspace(workspace, need, dev)
-    _on(dev, library().ring_attn_tree_fwd, q.data_ptr(), *ptrs, _need_lengths(lens, "lens", dev, B, optional=False),
-        _need_lengths(ntok, "ntok", dev, B), mask_ptr, batched, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel(), B, H, Hkv, T, d, cap, code_q, code, _dtype_code(out_dtype), _stream(stream, dev))
+    _run(dev.index, lib.ring_attn_tree_fwd, qp, *ptrs, _fits(lens, "lens", dev, (B,), torch.int32),
+         None if ntok is None else _fits(ntok, "ntok", dev, (B,), torch.int32), mp, batched,
+         _fits(out, "out", dev, q.shape, out_dtype), _fits(lse, "lse", dev, (B, H, T), torch.float32), workspace.data_ptr(),
+         workspace.numel(), B, H, Hkv, T, d, cap, code, kind, _DTYPES[out_dtype], _stream_ptr(stream, dev.index))
     return out, lse

@@ -100,7 +100,7 @@ ra_status check_tree(const Cache& c, int H, int T)
 {
     if (H < 1 || T < 1) return fail(RA_ERR_INVALID_ARG, "H, T must be >= 1 (got %d %d)", H, T);
     if (H % c.Hkv != 0) return fail(RA_ERR_INVALID_ARG, "H (%d) must be a multiple of Hkv (%d)", H, c.Hkv);
-    if ((long long)H * T >= (1LL << 30) || (long long)c.B * H * T >= (1LL << 32))
+    if ((long long)H * T >= (1LL << 30) || (long long)c.B * H * T >= (1LL << 31))
         return fail(RA_ERR_UNSUPPORTED, "too many query rows");
     return RA_OK;
 }

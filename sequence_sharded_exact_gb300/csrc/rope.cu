@@ -19,6 +19,7 @@
 // shard (rows = S = L / n, row_off = shard * S: local row r is whole-sequence row r + row_off).
 #include <cuda_bf16.h>
 #include <math.h>
+#include <string.h>
 
 #include "ra_internal.h"
 
@@ -124,6 +125,14 @@ unsigned rope_grid(long long items)
 
 void rope_turns(double base, int d, unsigned long long (&turn)[64])
 {
+    // 64 powers take as long as a launch, and a program uses one base: each thread keeps its last table
+    thread_local double last_base = 0.0;  // no valid base
+    thread_local int last_d = 0;
+    thread_local unsigned long long last[64];
+    if (base == last_base && d == last_d) {
+        memcpy(turn, last, sizeof(last));
+        return;
+    }
     const double two_pi = 6.283185307179586476925;
     for (int i = 0; i < 64; ++i) {
         turn[i] = 0;
@@ -133,6 +142,9 @@ void rope_turns(double base, int d, unsigned long long (&turn)[64])
             turn[i] = (unsigned long long)ldexp(frac, 64);
         }
     }
+    memcpy(last, turn, sizeof(last));
+    last_base = base;
+    last_d = d;
 }
 
 cudaError_t launch_rope(const Problem& p, void* x, double base, int inverse, cudaStream_t s, int shard)

@@ -121,17 +121,26 @@ struct TreeWalk {
     // One warp calls it; the walk starts at tile `at` of `total`, `count` tiles long.
     __device__ __forceinline__ bool begin(const TreeArgs& a, int cta)
     {
+        // up to 32 sequences, the usual batch: their lengths are read once
+        const int lane = threadIdx.x & 31;
+        const int mine32 = lane < a.B ? tree_tiles(tree_seq(a, lane)) : 0;
         long long total, before;
-        tree_totals(a, 0, total, before);
+        if (a.B <= 32) {
+            int all = mine32;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+            total = (long long)all * a.Hkv * a.nrt;
+        } else {
+            tree_totals(a, 0, total, before);
+        }
         long long at = tree_first(a, total, cta);
         left = tree_first(a, total, cta + 1) - at;
         first = true;
         if (left <= 0) return false;
         // the sequence that holds tile `at`: a warp looks at 32 sequences at a time
-        const int lane = threadIdx.x & 31;
         const long long items = (long long)a.Hkv * a.nrt;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
-            const long long mine = b0 + lane < a.B ? tree_tiles(tree_seq(a, b0 + lane)) * items : 0;
+            const long long mine = (b0 == 0 ? mine32 : b0 + lane < a.B ? tree_tiles(tree_seq(a, b0 + lane)) : 0) * items;
             long long upto = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {

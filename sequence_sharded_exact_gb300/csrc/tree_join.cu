@@ -1,9 +1,12 @@
 // tree_join.cu -- second launch of the attention over a cache (tree.cuh): joins the partials of the
 // items that several CTAs share, and writes zeros and -infinity to the rows that see nothing.
 //
-// For the partials (m_c, l_c, o_c) of a row, M = max m_c:  out = sum 2^(m_c - M) o_c / sum 2^(m_c - M) l_c,
-// lse = (M + log2 sum) ln 2, in CTA order.  One warp per query row; the lanes hold d / 32 elements.
-// Bound by latency: the partials are a few hundred KB and still in L2.
+// For the partials (m_c, l_c, den_c, o_c) of a row, c in CTA order, M = max m_c and w_c = 2^(m_c - M):
+//   out = sum w_c o_c / sum w_c den_c,  lse = (M + log2 sum w_c l_c) ln 2.
+// What bounds it is latency: a row has up to kTreeMaxCtas partials of d floats, all still in L2, and few rows
+// leave few blocks.  A block has one row, its four warps every fourth partial, a lane d / 32 columns, and
+// each warp loads eight partials before it needs the first; the warps' sums meet in a fixed order.
+// (One warp per row, walking its partials one by one: decoding over 19 partials took 15 us of 100.)
 #include <cuda_bf16.h>
 
 #include "ra_internal.h"
@@ -13,69 +16,105 @@
 namespace ra {
 namespace {
 
-constexpr int kRowsPerBlock = 4;  // one warp each
+constexpr int kWarps = 4;
+
+template <int V>
+struct Cols {
+    float f[V];
+};
+__device__ __forceinline__ Cols<4> load_cols(const float* p, Cols<4>)
+{
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    return {{v.x, v.y, v.z, v.w}};
+}
+__device__ __forceinline__ Cols<2> load_cols(const float* p, Cols<2>)
+{
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    return {{v.x, v.y}};
+}
 
 template <int D>
-__global__ void __launch_bounds__(kRowsPerBlock * 32) tree_join_kernel(const TreeArgs a)
+__global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const TreeArgs a)
 {
     constexpr int V = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long rows = (long long)a.B * a.Hkv * a.R;
-    const long long x = (long long)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5);
-    if (x >= rows) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        return;
-    }
+    __shared__ float sums[kWarps][D + 2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long x = blockIdx.x;  // query row: sequence, kv head, row of the head's group
     const int row = (int)(x % a.R);
     const int g = (int)(x / a.R % a.Hkv), b = (int)(x / a.R / a.Hkv);
     const int r = row / a.rt, i = row % a.rt;
     const TreeSeq s = tree_seq(a, b);
-    if (s.bad && g == 0 && row == 0 && lane == 0) atomicOr(a.status, kStatusRange);
     const int nt = tree_tiles(s);
-    int c0 = 0, c1 = -1;
-    long long total = 0, first = 0;
+    int c0 = 0, c1 = -1, head = 0;
     if (nt && row % a.T < s.cnt) {
-        long long before;
+        long long total, before;
         tree_totals(a, b, total, before);
-        first = before + ((long long)g * a.nrt + r) * nt;
+        const long long first = before + ((long long)g * a.nrt + r) * nt;
         c0 = tree_owner(a, total, first);
         c1 = tree_owner(a, total, first + nt - 1);
+        head = tree_first(a, total, c0) < first ? 1 : 0;  // c0 comes to this item after another one
     }
     // the partials are the first launch's; everything above needed the lengths alone
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (s.bad && g == 0 && row == 0 && threadIdx.x == 0) atomicOr(a.status, kStatusRange);
     if (c0 == c1 && nt) return;  // written whole by that CTA
+    auto at = [&](int c) { return ((long long)c * 2 + (c == c0 ? head : 0)) * a.rt + i; };
     float m = -INFINITY;
-    for (int c = c0; c <= c1; ++c) {
-        const int slot = c == c0 && tree_first(a, total, c) < first ? 1 : 0;
-        m = fmaxf(m, a.part_ml[(((long long)c * 2 + slot) * a.rt + i) * 4]);
-    }
+    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, a.part_ml[at(c) * 4]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float ref = m == -INFINITY ? 0.f : m;
     float l = 0.f, den = 0.f, o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-        const int slot = c == c0 && tree_first(a, total, c) < first ? 1 : 0;
-        const long long at = ((long long)c * 2 + slot) * a.rt + i;
-        const float4 ml = *reinterpret_cast<const float4*>(a.part_ml + at * 4);
-        const float w = ex2_approx(ml.x - ref);
-        l = fmaf(ml.y, w, l);
-        den = fmaf(ml.z, w, den);
+    constexpr int U = 8;
+    for (int c = c0 + warp; c <= c1; c += kWarps * U) {
+        float4 ml[U];
+        Cols<V> p[U];
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = fmaf(a.part_o[at * D + lane * V + e], w, o[e]);
+        for (int u = 0; u < U; ++u) {
+            const long long k = at(c + u * kWarps <= c1 ? c + u * kWarps : c);
+            ml[u] = *reinterpret_cast<const float4*>(a.part_ml + k * 4);
+            p[u] = load_cols(a.part_o + k * D + lane * V, Cols<V>());
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (c + u * kWarps > c1) break;
+            const float w = ex2_approx(ml[u].x - ref);
+            l = fmaf(ml[u].y, w, l);
+            den = fmaf(ml[u].z, w, den);
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[e] = fmaf(p[u].f[e], w, o[e]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) sums[warp][lane * V + e] = o[e];
+    if (lane == 0) {
+        sums[warp][D] = l;
+        sums[warp][D + 1] = den;
+    }
+    __syncthreads();
+    l = den = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+        l += sums[k][D];
+        den += sums[k][D + 1];
     }
     const bool none = m == -INFINITY && l == 0.f;
     const float inv = none ? 0.f : 1.0f / den;
-    const long long dst = (((long long)b * a.Hkv + g) * a.R + row) * D + lane * V;
-    if (a.bf16_out) {
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + dst;
+    if (threadIdx.x < D / 2) {  // two columns each
+        float2 t = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < V; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-    } else {
-        float* out = static_cast<float*>(a.out) + dst;
-#pragma unroll
-        for (int e = 0; e < V; ++e) out[e] = o[e] * inv;
+        for (int k = 0; k < kWarps; ++k) {
+            t.x += sums[k][threadIdx.x * 2];
+            t.y += sums[k][threadIdx.x * 2 + 1];
+        }
+        if (a.bf16_out)
+            static_cast<uint32_t*>(a.out)[(x * D >> 1) + threadIdx.x] = none ? 0u : pack_bf16x2(t.x * inv, t.y * inv);
+        else
+            static_cast<float2*>(a.out)[(x * D >> 1) + threadIdx.x] = none ? make_float2(0.f, 0.f) : make_float2(t.x * inv, t.y * inv);
     }
-    if (lane == 0) a.lse[((long long)b * a.Hkv + g) * a.R + row] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (threadIdx.x == 0) a.lse[x] = none ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 }  // namespace
@@ -151,8 +190,8 @@ cudaError_t launch_tree_join(const TreeArgs& a, int d, cudaStream_t s)
 {
     const long long rows = (long long)a.B * a.Hkv * a.R;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((rows + kRowsPerBlock - 1) / kRowsPerBlock));
-    cfg.blockDim = dim3(kRowsPerBlock * 32);
+    cfg.gridDim = dim3((unsigned)rows);
+    cfg.blockDim = dim3(kWarps * 32);
     cfg.stream = s;
     // starts while the first launch runs; it waits for that one's results in the kernel
     cudaLaunchAttribute early;

@@ -343,54 +343,55 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
     const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
     uint32_t vc = 0, item = 0;
     do {
-        // the item's queries: hi and lo e4m3 values and the row's scale
+        // the item's queries: hi and lo e4m3 values and the row's scale; kHd / 8 lanes share a row.  Rows past the
+        // kv head's keep what they hold: it reaches no row of S that is read.
         if (item > 0 && !warp_wait(bar(C::bQEmpty), (item - 1) & 1, ctl)) return;
-#pragma unroll 1
-        for (int qt = 0; qt < kNq; ++qt) {
-            const int x = w.r * a.rt + qt * 128 + row;
+        {
+            constexpr int kLanes = kHd / 8, kStep = 128 / kLanes, kU = 4;
+            const int c = row % kLanes;
+            const int rows = a.R - w.r * a.rt < kNq * 128 ? a.R - w.r * a.rt : kNq * 128;
             const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                              (((long long)w.b * a.Hkv + w.g) * a.R + x) * kHd);
-            uint8_t* q = smem + C::kQ + (uint32_t)qt * C::kBytesQ;
-            uint32_t big = 0;  // bits of the largest magnitude: bf16 in the upper half, ordered as integers
-            if (x < a.R) {
-#pragma unroll 4
-                for (int c = 0; c < kHd / 8; ++c) {
-                    const uint4 v = src[c];
-                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        big = max(big, u[i] << 16 & 0x7fff0000u);
-                        big = max(big, u[i] & 0x7fff0000u);
-                    }
-                }
-            }
-            const bool finite = big < 0x7f800000u;
-            int e = (int)(big >> 23) - 135 + ((big & 0x7fffffu) > 0x600000u ? 1 : 0);
-            e = !finite || e < -126 ? -126 : e;
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-            reinterpret_cast<float*>(smem + C::kQs)[(item & 1) * kNq * 128 + qt * 128 + row] =
-                finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7fc00000u);
+                                                              (((long long)w.b * a.Hkv + w.g) * a.R + (long long)w.r * a.rt) * kHd) + c;
+            float* scale = reinterpret_cast<float*>(smem + C::kQs) + (item & 1) * kNq * 128;
 #pragma unroll 1
-            for (int c = 0; c < kHd / 16; ++c) {
-                uint4 hi = make_uint4(0, 0, 0, 0), lo = make_uint4(0, 0, 0, 0);
-                if (x < a.R && finite) {
-                    const uint4 v0 = src[2 * c], v1 = src[2 * c + 1];
-                    const uint32_t u[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-                    uint32_t ph[4], pl[4];
+            for (int x0 = row / kLanes; x0 < (rows + kStep * kU - 1) / (kStep * kU) * (kStep * kU); x0 += kStep * kU) {
+                uint4 v[kU];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float f0 = __uint_as_float(u[2 * i] << 16) * down, f1 = __uint_as_float(u[2 * i] & 0xffff0000u) * down;
-                        const float f2 = __uint_as_float(u[2 * i + 1] << 16) * down, f3 = __uint_as_float(u[2 * i + 1] & 0xffff0000u) * down;
+                for (int u = 0; u < kU; ++u) {
+                    const int x = x0 + u * kStep;
+                    v[u] = x < rows ? src[(long long)x * (kHd / 8)] : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int x = x0 + u * kStep;
+                    const uint32_t p[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                    uint32_t big = 0;  // bits of the largest magnitude: bf16 in the upper half, ordered as integers
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) big = max(big, max(p[i] << 16 & 0x7fff0000u, p[i] & 0x7fff0000u));
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+                    if (x >= rows) continue;
+                    const bool finite = big < 0x7f800000u;
+                    int e = (int)(big >> 23) - 135 + ((big & 0x7fffffu) > 0x600000u ? 1 : 0);
+                    e = !finite || e < -126 ? -126 : e;
+                    const float down = finite ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
+                    if (c == 0) scale[x] = finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7fc00000u);
+                    uint2 hi, lo;
+                    uint32_t* ph = &hi.x;
+                    uint32_t* pl = &lo.x;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float f0 = __uint_as_float(p[2 * i] << 16) * down, f1 = __uint_as_float(p[2 * i] & 0xffff0000u) * down;
+                        const float f2 = __uint_as_float(p[2 * i + 1] << 16) * down, f3 = __uint_as_float(p[2 * i + 1] & 0xffff0000u) * down;
                         ph[i] = (uint32_t)e4m3x2(f0, f1) | (uint32_t)e4m3x2(f2, f3) << 16;
                         float h0, h1, h2, h3;
                         e4m3x4_to_float(ph[i], h0, h1, h2, h3);
                         pl[i] = (uint32_t)e4m3x2(f0 - h0, f1 - h1) | (uint32_t)e4m3x2(f2 - h2, f3 - h3) << 16;
                     }
-                    hi = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-                    lo = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+                    uint8_t* q = smem + C::kQ + (uint32_t)(x >> 7) * C::kBytesQ + qk_offset(x & 127, c >> 1) + (c & 1) * 8;
+                    *reinterpret_cast<uint2*>(q) = hi;
+                    *reinterpret_cast<uint2*>(q + 128 * kHd) = lo;
                 }
-                *reinterpret_cast<uint4*>(q + qk_offset(row, c)) = hi;
-                *reinterpret_cast<uint4*>(q + 128 * kHd + qk_offset(row, c)) = lo;
             }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -410,12 +411,10 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
             const bool past = key >= w.s.end, drafted = key >= w.s.len;
             bool hit = false;
             // a thread has a row; starting each at another chunk keeps a warp's accesses in different banks
-#pragma unroll 4
-            for (int i = 0; i < kHd / 16; ++i) {
+            auto chunk = [&](int i, uint32_t (&o)[8]) {
                 const int c = (i + row) & (kHd / 16 - 1);
                 const uint4 x = *reinterpret_cast<const uint4*>(src + row * kHd + c * 16);
                 const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-                uint32_t o[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float f0, f1, f2, f3;
@@ -423,18 +422,36 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
                     o[2 * j] = pack_bf16x2(f0 * up, f1 * up);
                     o[2 * j + 1] = pack_bf16x2(f2 * up, f3 * up);
                 }
-                if (drafted) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        if (past)
-                            o[j] = 0;
-                        else
-                            hit |= clear_nonfinite(o[j]);
-                    }
-                }
+            };
+            auto store = [&](int i, const uint32_t (&o)[8]) {
+                const int c = (i + row) & (kHd / 16 - 1);
                 uint8_t* p = dst + (c >> 2) * 16384 + row * 128;
                 *reinterpret_cast<uint4*>(p + ((((2 * c) & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 *reinterpret_cast<uint4*>(p + ((((2 * c + 1) & 7) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            };
+            if ((t + 1) * kTreeTile <= w.s.len) {  // no branch inside: the chunks' conversions overlap
+#pragma unroll 2
+                for (int i = 0; i < kHd / 16; ++i) {
+                    uint32_t o[8];
+                    chunk(i, o);
+                    store(i, o);
+                }
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < kHd / 16; ++i) {
+                    uint32_t o[8];
+                    chunk(i, o);
+                    if (drafted) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            if (past)
+                                o[j] = 0;
+                            else
+                                hit |= clear_nonfinite(o[j]);
+                        }
+                    }
+                    store(i, o);
+                }
             }
             if (hit) *reinterpret_cast<volatile int*>(smem + C::kPoison + (item & 7) * 4) = (int)item + 1;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
