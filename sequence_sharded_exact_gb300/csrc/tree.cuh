@@ -46,7 +46,7 @@ struct TreeArgs {
     void* out;
     float* lse;
     float* part_ml;  // [ctas][2][rt][4]: m (log2 units), l, the output's normaliser (l as the weights were rounded), 0
-    float* part_o;   // [ctas][2][rt][d]
+    float* part_o;   // [ctas][2][d][rt]: a warp that holds consecutive rows writes whole lines
     unsigned int* status;
     float scale_log2;  // log2(e) / sqrt(d)
 };

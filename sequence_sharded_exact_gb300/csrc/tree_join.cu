@@ -4,8 +4,9 @@
 // For the partials (m_c, l_c, den_c, o_c) of a row, c in CTA order, M = max m_c and w_c = 2^(m_c - M):
 //   out = sum w_c o_c / sum w_c den_c,  lse = (M + log2 sum w_c l_c) ln 2.
 // What bounds it is latency: a row has up to kTreeMaxCtas partials of d floats, all still in L2, and few rows
-// leave few blocks.  A block has one row, its four warps every fourth partial, a lane d / 32 columns, and
-// each warp loads eight partials before it needs the first; the warps' sums meet in a fixed order.
+// leave few blocks.  A block has 32 rows (a lane each: the partials are stored column by column) and 16
+// columns; its eight warps take every eighth partial, three of them, 48 loads, at a time, keep a running
+// maximum of their own, and meet in shared memory in a fixed order.
 // (One warp per row, walking its partials one by one: decoding over 19 partials took 15 us of 100.)
 #include <cuda_bf16.h>
 
@@ -16,37 +17,23 @@
 namespace ra {
 namespace {
 
-constexpr int kWarps = 4;
-
-template <int V>
-struct Cols {
-    float f[V];
-};
-__device__ __forceinline__ Cols<4> load_cols(const float* p, Cols<4>)
-{
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    return {{v.x, v.y, v.z, v.w}};
-}
-__device__ __forceinline__ Cols<2> load_cols(const float* p, Cols<2>)
-{
-    const float2 v = *reinterpret_cast<const float2*>(p);
-    return {{v.x, v.y}};
-}
+constexpr int kWarps = 8, kCols = 16;
 
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const TreeArgs a)
 {
-    constexpr int V = D / 32;
-    __shared__ float sums[kWarps][D + 2];
+    __shared__ float so[kWarps][kCols][33];
+    __shared__ float sm[kWarps][3][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long x = blockIdx.x;  // query row: sequence, kv head, row of the head's group
-    const int row = (int)(x % a.R);
-    const int g = (int)(x / a.R % a.Hkv), b = (int)(x / a.R / a.Hkv);
-    const int r = row / a.rt, i = row % a.rt;
+    const int chunks = (a.rt + 31) / 32;
+    const long long it = blockIdx.x / chunks;  // sequence, kv head, row tile
+    const int i0 = (int)(blockIdx.x % chunks) * 32, i = i0 + lane;
+    const int r = (int)(it % a.nrt), g = (int)(it / a.nrt % a.Hkv), b = (int)(it / a.nrt / a.Hkv);
+    const int col0 = blockIdx.y * kCols;
     const TreeSeq s = tree_seq(a, b);
     const int nt = tree_tiles(s);
-    int c0 = 0, c1 = -1, head = 0;
-    if (nt && row % a.T < s.cnt) {
+    int c0 = 0, c1 = 0, head = 0;
+    if (nt) {
         long long total, before;
         tree_totals(a, b, total, before);
         const long long first = before + ((long long)g * a.nrt + r) * nt;
@@ -54,67 +41,83 @@ __global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const TreeArgs a
         c1 = tree_owner(a, total, first + nt - 1);
         head = tree_first(a, total, c0) < first ? 1 : 0;  // c0 comes to this item after another one
     }
+    const bool shared = c0 < c1;  // else written whole by one CTA
+    auto lives = [&](int k) { return k < a.rt && r * a.rt + k < a.R && nt && (r * a.rt + k) % a.T < s.cnt; };
+    const bool live = lives(i);
     // the partials are the first launch's; everything above needed the lengths alone
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (s.bad && g == 0 && row == 0 && threadIdx.x == 0) atomicOr(a.status, kStatusRange);
-    if (c0 == c1 && nt) return;  // written whole by that CTA
-    auto at = [&](int c) { return ((long long)c * 2 + (c == c0 ? head : 0)) * a.rt + i; };
-    float m = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, a.part_ml[at(c) * 4]);
+    if (s.bad && blockIdx.y == 0 && i0 == 0 && r == 0 && g == 0 && threadIdx.x == 0) atomicOr(a.status, kStatusRange);
+    float m = -INFINITY, l = 0.f, den = 0.f, o[kCols];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f, den = 0.f, o[V];
+    for (int e = 0; e < kCols; ++e) o[e] = 0.f;
+    if (shared && live) {
+        constexpr int U = 3;
+#pragma unroll 1
+        for (int c = c0 + warp; c <= c1; c += kWarps * U) {
+            float4 ml[U];
+            float p[U][kCols];
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = 0.f;
-    constexpr int U = 8;
-    for (int c = c0 + warp; c <= c1; c += kWarps * U) {
-        float4 ml[U];
-        Cols<V> p[U];
+            for (int u = 0; u < U; ++u) {
+                const int cc = c + u * kWarps;
+                if (cc > c1) break;
+                const long long slot = (long long)cc * 2 + (cc == c0 ? head : 0);
+                ml[u] = *reinterpret_cast<const float4*>(a.part_ml + (slot * a.rt + i) * 4);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long k = at(c + u * kWarps <= c1 ? c + u * kWarps : c);
-            ml[u] = *reinterpret_cast<const float4*>(a.part_ml + k * 4);
-            p[u] = load_cols(a.part_o + k * D + lane * V, Cols<V>());
-        }
+                for (int e = 0; e < kCols; ++e) p[u][e] = a.part_o[(slot * D + col0 + e) * a.rt + i];
+            }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (c + u * kWarps > c1) break;
-            const float w = ex2_approx(ml[u].x - ref);
-            l = fmaf(ml[u].y, w, l);
-            den = fmaf(ml[u].z, w, den);
+            for (int u = 0; u < U; ++u) {
+                if (c + u * kWarps > c1) break;
+                const float mn = fmaxf(m, ml[u].x), ref = mn == -INFINITY ? 0.f : mn;
+                const float keep = ex2_approx(m - ref), w = ex2_approx(ml[u].x - ref);
+                m = mn;
+                l = fmaf(ml[u].y, w, l * keep);
+                den = fmaf(ml[u].z, w, den * keep);
+                if (ml[u].x == -INFINITY && ml[u].y != 0.f) l = den = ml[u].y;  // NaN scores leave no maximum
 #pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = fmaf(p[u].f[e], w, o[e]);
+                for (int e = 0; e < kCols; ++e) o[e] = fmaf(p[u][e], w, o[e] * keep);
+            }
         }
     }
+    if (shared) {  // the same for the whole block
+        sm[warp][0][lane] = m;
+        sm[warp][1][lane] = l;
+        sm[warp][2][lane] = den;
 #pragma unroll
-    for (int e = 0; e < V; ++e) sums[warp][lane * V + e] = o[e];
-    if (lane == 0) {
-        sums[warp][D] = l;
-        sums[warp][D + 1] = den;
+        for (int e = 0; e < kCols; ++e) so[warp][e][lane] = o[e];
     }
     __syncthreads();
+    // 32 rows of 8 column pairs
+    const int k = threadIdx.x >> 3, pair = threadIdx.x & 7;
+    if (i0 + k >= a.rt || r * a.rt + i0 + k >= a.R) return;
+    const bool dead = !lives(i0 + k);
+    if (!dead && !shared) return;
+    float2 t = make_float2(0.f, 0.f);
+    m = -INFINITY;
     l = den = 0.f;
+    if (!dead) {
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-        l += sums[k][D];
-        den += sums[k][D + 1];
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm[w][0][k]);
+        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = ex2_approx(sm[w][0][k] - ref);
+            l = fmaf(sm[w][1][k], f, l);
+            den = fmaf(sm[w][2][k], f, den);
+            t.x = fmaf(so[w][2 * pair][k], f, t.x);
+            t.y = fmaf(so[w][2 * pair + 1][k], f, t.y);
+        }
     }
     const bool none = m == -INFINITY && l == 0.f;
-    const float inv = none ? 0.f : 1.0f / den;
-    if (threadIdx.x < D / 2) {  // two columns each
-        float2 t = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-            t.x += sums[k][threadIdx.x * 2];
-            t.y += sums[k][threadIdx.x * 2 + 1];
-        }
-        if (a.bf16_out)
-            static_cast<uint32_t*>(a.out)[(x * D >> 1) + threadIdx.x] = none ? 0u : pack_bf16x2(t.x * inv, t.y * inv);
-        else
-            static_cast<float2*>(a.out)[(x * D >> 1) + threadIdx.x] = none ? make_float2(0.f, 0.f) : make_float2(t.x * inv, t.y * inv);
-    }
-    if (threadIdx.x == 0) a.lse[x] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+    const float inv = 1.0f / den;
+    t = none ? make_float2(0.f, 0.f) : make_float2(t.x * inv, t.y * inv);
+    const long long x = ((long long)b * a.Hkv + g) * a.R + (long long)r * a.rt + i0 + k;
+    const long long at = (x * D + col0) / 2 + pair;
+    if (a.bf16_out)
+        static_cast<uint32_t*>(a.out)[at] = pack_bf16x2(t.x, t.y);
+    else
+        static_cast<float2*>(a.out)[at] = t;
+    if (pair == 0 && blockIdx.y == 0) a.lse[x] = none ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 }  // namespace
@@ -188,9 +191,9 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
 
 cudaError_t launch_tree_join(const TreeArgs& a, int d, cudaStream_t s)
 {
-    const long long rows = (long long)a.B * a.Hkv * a.R;
+    const long long items = (long long)a.B * a.Hkv * a.nrt;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)rows);
+    cfg.gridDim = dim3((unsigned)(items * ((a.rt + 31) / 32)), (unsigned)(d / kCols));
     cfg.blockDim = dim3(kWarps * 32);
     cfg.stream = s;
     // starts while the first launch runs; it waits for that one's results in the kernel

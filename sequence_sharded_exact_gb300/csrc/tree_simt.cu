@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a)
                 static_cast<float*>(a.out)[dst * D + col] = o;
                 if (col == 0) a.lse[dst] = none ? -INFINITY : (mm + log2f(ll)) * kLn2;
             } else {
-                a.part_o[(slot * a.rt + x) * D + col] = acc[i];
+                a.part_o[(slot * D + col) * a.rt + x] = acc[i];
                 if (col == 0) *reinterpret_cast<float4*>(a.part_ml + (slot * a.rt + x) * 4) = make_float4(mm, ll, ll, 0.f);
             }
         }

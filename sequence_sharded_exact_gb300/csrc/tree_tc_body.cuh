@@ -83,10 +83,20 @@ struct Maps {
     CUtensorMap q, k, v;
 };
 
-// The whole warp's wait: every lane learns whether all of them saw the phase.
+// Waits.  The part that polls is a function of its own: inlined at every wait it took the loops of the roles,
+// which run side by side, out of the instruction cache.
+__device__ __noinline__ bool poll(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int* status)
+{
+    return mbar_wait_slow(bar, parity, WaitCtl{abort, status, kWaitLimitNs});
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const WaitCtl& ctl)
+{
+    return mbar_try_wait(bar, parity) || poll(bar, parity, ctl.abort, ctl.status);
+}
+// The whole warp's: every lane learns whether all of them saw the phase.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl& ctl)
 {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl));
+    return __all_sync(0xffffffffu, wait(bar, parity, ctl));
 }
 
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity)
@@ -171,7 +181,7 @@ __device__ __forceinline__ void load_qk_role(const TreeArgs& a, uint32_t sbase, 
     do {
         const int z = w.b * a.Hkv + w.g;
         if constexpr (!kE4) {
-            if (item > 0 && !mbar_wait(bar(C::bQEmpty), (item - 1) & 1, ctl)) break;
+            if (item > 0 && !wait(bar(C::bQEmpty), (item - 1) & 1, ctl)) break;
             mbar_arrive_expect_tx(bar(C::bQFull), kNq * C::kBytesQ);
             for (int t = 0; t < kNq; ++t)
                 for (int h = 0; h < kHd / 64; ++h)
@@ -182,7 +192,7 @@ __device__ __forceinline__ void load_qk_role(const TreeArgs& a, uint32_t sbase, 
         for (int t = w.t0; t < w.t1; ++t, ++kc) {
             const int slot = (int)(kc % C::kSlotsK);
             const uint32_t use = kc / C::kSlotsK;
-            if (use > 0 && !mbar_wait(bar(C::bKEmpty + slot), (use - 1) & 1, ctl)) { ok = false; break; }
+            if (use > 0 && !wait(bar(C::bKEmpty + slot), (use - 1) & 1, ctl)) { ok = false; break; }
             mbar_arrive_expect_tx(bar(C::bKFull + slot), C::kBytesK);
             const uint32_t dst = sbase + C::kK + (uint32_t)slot * C::kBytesK;
             if constexpr (kE4) {
@@ -210,7 +220,7 @@ __device__ __forceinline__ void load_v_role(const TreeArgs& a, uint32_t sbase, c
         for (int t = w.t0; t < w.t1; ++t, ++vc) {
             const int slot = (int)(vc % C::kSlotsL);
             const uint32_t use = vc / C::kSlotsL;
-            if (use > 0 && !mbar_wait(bar(C::bLEmpty + slot), (use - 1) & 1, ctl)) { ok = false; break; }
+            if (use > 0 && !wait(bar(C::bLEmpty + slot), (use - 1) & 1, ctl)) { ok = false; break; }
             const uint32_t dst = sbase + C::kL + (uint32_t)slot * C::kBytesK;
             if constexpr (kE4) {
                 // rows are contiguous and V is not a product's operand here: one untiled copy, no row past the cache
@@ -347,7 +357,7 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
         // kv head's keep what they hold: it reaches no row of S that is read.
         if (item > 0 && !warp_wait(bar(C::bQEmpty), (item - 1) & 1, ctl)) return;
         {
-            constexpr int kLanes = kHd / 8, kStep = 128 / kLanes, kU = 4;
+            constexpr int kLanes = kHd / 8, kStep = 128 / kLanes, kU = 8;
             const int c = row % kLanes;
             const int rows = a.R - w.r * a.rt < kNq * 128 ? a.R - w.r * a.rt : kNq * 128;
             const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
@@ -468,74 +478,54 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
 // ------------------------------------------------------------------------------------------------
 // MMA issue (one thread)
 // ------------------------------------------------------------------------------------------------
+// An item's jobs, one S and one P V each: tile by tile, and (kNq == 2) warpgroup 0's query rows, then 1's.  Job j
+// belongs to warpgroup j & 1; its S is issued once P V of job j - 2, which reads the same TMEM columns, is.
 template <bool kE4, int kNq>
 __device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint32_t tmem, TreeWalk w, const WaitCtl& ctl)
 {
     using C = Cfg<kE4, kNq>;
     auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
-    uint32_t kc = 0, vc = 0, item = 0, pc[2] = {0, 0};
+    uint32_t kc = 0, vc = 0, item = 0, pc = 0;  // pc: a parity bit per warpgroup
     bool ok = true;
-
-    // S of the next K tile into S_w (kNq == 2: w = 0 waits for the tile, w = 1 releases it)
-    auto score = [&](int wg, bool last) {
-        const int slot = (int)(kc % C::kSlotsK);
-        if (kNq == 1 || wg == 0) {
-            if (!mbar_wait(bar(C::bKFull + slot), (kc / C::kSlotsK) & 1, ctl)) return false;
-            tc_fence_after_sync();
-        }
-        issue_s<kE4, kNq>(sbase, tmem, wg, slot);
-        tc_commit(bar(C::bS + wg));
-        if (kNq == 1 || wg == 1) {
-            tc_commit(bar(C::bKEmpty + slot));
-            if (last) tc_commit(bar(C::bQEmpty));
-            ++kc;
-        }
-        return true;
-    };
-    // the V tile of the current job as the product takes it
-    auto v_wait = [&]() { return mbar_wait(bar(C::bPFull + (int)(vc % C::kSlotsP)), (vc / C::kSlotsP) & 1, ctl); };
-    auto weigh = [&](int wg, bool accumulate) {
-        if (!mbar_wait(bar(C::bP + wg), pc[wg]++ & 1, ctl)) return false;
-        tc_fence_after_sync();
-        const uint32_t v = kE4 ? sbase + C::kP + (vc % C::kSlotsP) * C::kBytesV : sbase + C::kL + (vc % C::kSlotsL) * C::kBytesK;
-        issue_pv(v, tmem, wg, accumulate);
-        tc_commit(bar(C::bO + wg));
-        return true;
-    };
-    auto v_done = [&]() {
-        if constexpr (kE4) {
-            tc_commit(bar(C::bPEmpty + (int)(vc % C::kSlotsP)));
-            tc_commit(bar(C::bXEmpty + (int)(vc % C::kSlotsX)));
-        } else {
-            tc_commit(bar(C::bLEmpty + (int)(vc % C::kSlotsL)));
-        }
-        ++vc;
-    };
-
     do {
-        if (!mbar_wait(bar(C::bQFull), item++ & 1, ctl)) break;
+        if (!wait(bar(C::bQFull), item++ & 1, ctl)) break;
         tc_fence_after_sync();
-        const int n = w.t1 - w.t0;
-        if constexpr (kNq == 1) {
-            ok = score(0, n == 1);
-            if (ok && n > 1) ok = score(1, n == 2);
-            for (int i = 0; ok && i < n; ++i) {
-                const int wg = i & 1;
-                ok = v_wait() && weigh(wg, i >= 2);
+        const int n = (w.t1 - w.t0) * kNq;
+#pragma unroll 1
+        for (int j = 0; j < n + 2; ++j) {
+            const int wg = j & 1;
+            if (j >= 2) {
+                const int sp = (int)(vc % C::kSlotsP);
+                ok = wait(bar(C::bPFull + sp), (vc / C::kSlotsP) & 1, ctl) && wait(bar(C::bP + wg), pc >> wg & 1, ctl);
                 if (!ok) break;
-                v_done();
-                if (i + 2 < n) ok = score(wg, i + 2 == n - 1);
+                pc ^= 1u << wg;
+                tc_fence_after_sync();
+                issue_pv(sbase + (kE4 ? C::kP + (uint32_t)sp * C::kBytesV : C::kL + (uint32_t)sp * C::kBytesK), tmem, wg, j >= 4);
+                tc_commit(bar(C::bO + wg));
+                if (kNq == 1 || wg == 1) {
+                    if constexpr (kE4) {
+                        tc_commit(bar(C::bPEmpty + sp));
+                        tc_commit(bar(C::bXEmpty + (int)(vc % C::kSlotsX)));
+                    } else {
+                        tc_commit(bar(C::bLEmpty + sp));
+                    }
+                    ++vc;
+                }
             }
-        } else {
-            ok = score(0, false) && score(1, n == 1);
-            for (int i = 0; ok && i < n; ++i) {
-                const bool more = i + 1 < n;
-                ok = v_wait() && weigh(0, i > 0);
-                if (ok && more) ok = score(0, false);
-                ok = ok && weigh(1, i > 0);
-                if (!ok) break;
-                v_done();
-                if (more) ok = score(1, i + 1 == n - 1);
+            if (j < n) {
+                const int slot = (int)(kc % C::kSlotsK);
+                if (kNq == 1 || wg == 0) {
+                    ok = wait(bar(C::bKFull + slot), (kc / C::kSlotsK) & 1, ctl);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                }
+                issue_s<kE4, kNq>(sbase, tmem, wg, slot);
+                tc_commit(bar(C::bS + wg));
+                if (kNq == 1 || wg == 1) {
+                    tc_commit(bar(C::bKEmpty + slot));
+                    ++kc;
+                }
+                if (j == n - 1) tc_commit(bar(C::bQEmpty));
             }
         }
     } while (ok && w.next(a));
@@ -546,27 +536,29 @@ __device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint
 // ------------------------------------------------------------------------------------------------
 // softmax warpgroups
 // ------------------------------------------------------------------------------------------------
-// Which of the tile's 128 rows (from k0) query token t sees, one bit each; only for tiles that reach past the prefix.
-__device__ __forceinline__ void seen_bits(const TreeArgs& a, const TreeSeq& s, int b, int t, int k0, uint32_t (&bits)[4])
+// Which of the 64 rows from k0 query token t sees, one bit each; for tiles that reach past the prefix.
+__device__ __noinline__ unsigned long long seen_bits(const TreeArgs& a, const TreeSeq& s, int b, int t, int k0)
 {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int p = s.len - (k0 + i * 32);  // rows of this word in the prefix
-        bits[i] = p >= 32 ? 0xffffffffu : (p > 0 ? (1u << p) - 1u : 0u);
+    const int p = s.len - k0;  // rows of the prefix among them
+    unsigned long long bits = p >= 64 ? ~0ull : (p > 0 ? (1ull << p) - 1 : 0ull);
+    if (t >= s.cnt) return bits;
+    const int j0 = p < 0 ? -p : 0, j1 = 64 - p < s.cnt ? 64 - p : s.cnt;
+    if (!a.mask) {
+        const int n = (j1 < t + 1 ? j1 : t + 1) - j0;  // drafted tokens up to t
+        return n > 0 ? bits | (n >= 64 ? ~0ull : (1ull << n) - 1) << (p + j0) : bits;
     }
-    const int j0 = k0 > s.len ? k0 - s.len : 0;
-    const int j1 = k0 + kTreeTile - s.len < s.cnt ? k0 + kTreeTile - s.len : s.cnt;
-    if (t >= s.cnt) return;
-    const uint8_t* m = a.mask ? a.mask + ((a.mask_batched ? (long long)b * a.T : 0) + t) * a.T : nullptr;
-#pragma unroll 8
-    for (int j = j0; j < j1; ++j) {
-        const bool sees = m ? m[j] != 0 : j <= t;
-        const int c = s.len + j - k0;
-        const uint32_t one = sees ? 1u << (c & 31) : 0u;
+    const uint8_t* m = a.mask + ((a.mask_batched ? (long long)b * a.T : 0) + t) * a.T;
+#pragma unroll 1
+    for (int j = j0; j < j1; j += 16) {
+        uint8_t v[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (c >> 5 == i) bits[i] |= one;
+        for (int i = 0; i < 16; ++i) v[i] = j + i < j1 ? m[j + i] : (uint8_t)0;
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w |= v[i] ? 1u << i : 0u;
+        bits |= (unsigned long long)w << (p + j);
     }
+    return bits;
 }
 
 template <bool kE4, int kNq>
@@ -595,8 +587,11 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
         for (int i = kNq == 1 ? wg : 0; i < n; i += kNq == 1 ? 2 : 1) {
             const int k0 = (w.t0 + i) * kTreeTile;
             const bool masked = k0 + kTreeTile > w.s.len;
-            uint32_t bits[4];
-            if (masked) seen_bits(a, w.s, w.b, tq, k0, bits);
+            unsigned long long seen[2] = {~0ull, ~0ull};
+            if (masked && any_live) {
+                seen[0] = seen_bits(a, w.s, w.b, tq, k0);
+                seen[1] = seen_bits(a, w.s, w.b, tq, k0 + 64);
+            }
             const uint32_t job = jobs[wg]++;
             if (!warp_wait(bar(C::bS + wg), job & 1, ctl)) return;
             if (!any_live) {  // no query row in these lanes: what P holds there reaches no row that is read
@@ -604,77 +599,75 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
                 continue;
             }
             tc_fence_after_sync();
-            const float* xs = nullptr;
+            const float4* xs = nullptr;
             if constexpr (kE4) {
                 const uint32_t xc = tiles + (uint32_t)i;
                 if (!warp_wait(bar(C::bXFull + (int)(xc % C::kSlotsX)), (xc / C::kSlotsX) & 1, ctl)) return;
-                xs = reinterpret_cast<const float*>(smem + C::kX + (xc % C::kSlotsX) * 1024);
+                xs = reinterpret_cast<const float4*>(smem + C::kX + (xc % C::kSlotsX) * 1024);
                 if (first)
                     sl2 = a.scale_log2 * reinterpret_cast<const float*>(smem + C::kQs)[(item & 1) * kNq * 128 + (kNq == 2 ? wg * 128 : 0) + rw];
             }
-            uint32_t r[4][32];
-            float m8[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m8[e] = -INFINITY;
-            tmem_ld_32x32b_x32(tS + 0, r[0]);
-            tmem_ld_32x32b_x32(tS + 32, r[1]);
-            tmem_ld_wait(r[0]);
-            tmem_ld_wait(r[1]);
-            tmem_ld_32x32b_x32(tS + 64, r[2]);
-            tmem_ld_32x32b_x32(tS + 96, r[3]);
-#pragma unroll
-            for (int c4 = 0; c4 < 4; ++c4) {
-                if (c4 == 2) {
-                    tmem_ld_wait(r[2]);
-                    tmem_ld_wait(r[3]);
-                }
+            // S is read twice, 64 columns at a time in loops that are not unrolled: the maximum, then the weights.
+            // (Kept in registers in between, the 128 columns took a code of 24 KB a tile, and with the other
+            // warps' loops the instruction cache was what the kernel waited for.)
+            auto load = [&](int half, uint32_t (&r)[64]) {
+                tmem_ld_32x32b_x64(tS + half * 64, r);
+                tmem_ld_wait(r);
                 if constexpr (kE4) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 sc = *reinterpret_cast<const float4*>(xs + c4 * 32 + e);
-                        const float2 u0 = mul2(make_float2(__uint_as_float(r[c4][e]), __uint_as_float(r[c4][e + 1])), make_float2(sc.x, sc.y));
-                        const float2 u1 = mul2(make_float2(__uint_as_float(r[c4][e + 2]), __uint_as_float(r[c4][e + 3])), make_float2(sc.z, sc.w));
-                        r[c4][e] = __float_as_uint(u0.x);
-                        r[c4][e + 1] = __float_as_uint(u0.y);
-                        r[c4][e + 2] = __float_as_uint(u1.x);
-                        r[c4][e + 3] = __float_as_uint(u1.y);
+                    for (int e = 0; e < 64; e += 4) {
+                        const float4 sc = xs[half * 16 + e / 4];
+                        const float2 u0 = mul2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), make_float2(sc.x, sc.y));
+                        const float2 u1 = mul2(make_float2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), make_float2(sc.z, sc.w));
+                        r[e] = __float_as_uint(u0.x);
+                        r[e + 1] = __float_as_uint(u0.y);
+                        r[e + 2] = __float_as_uint(u1.x);
+                        r[e + 3] = __float_as_uint(u1.y);
                     }
                 }
                 if (masked) {
+                    const unsigned long long bits = half ? seen[1] : seen[0];
+                    const uint32_t lo = (uint32_t)bits, hi = (uint32_t)(bits >> 32);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!(bits[c4] >> e & 1u)) r[c4][e] = __float_as_uint(-INFINITY);
+                    for (int e = 0; e < 32; ++e) {
+                        if (!(lo & 1u << e)) r[e] = __float_as_uint(-INFINITY);
+                        if (!(hi & 1u << e)) r[32 + e] = __float_as_uint(-INFINITY);
+                    }
                 }
+            };
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                uint32_t r[64];
+                load(half, r);
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                    m8[(e >> 1) & 7] = max3f(m8[(e >> 1) & 7], __uint_as_float(r[c4][e]), __uint_as_float(r[c4][e + 1]));
+                for (int e = 0; e < 64; e += 2) m4[(e >> 1) & 3] = max3f(m4[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+                mx = max3f(mx, max3f(m4[0], m4[1], m4[2]), m4[3]);
             }
-            const float mx = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
             const float m_tile = mx * sl2;
             const float m_new = m_tile > m_run + 8.0f ? m_tile : m_run;
             const float alpha = m_new == m_run ? 1.0f : ex2_approx(m_run - m_new);
             const float ref = m_new == -INFINITY ? 0.f : m_new;
             const float2 scale2 = make_float2(sl2, sl2), nref2 = make_float2(-ref, -ref);
-            float2 s4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s4[e] = make_float2(0.f, 0.f);
-#pragma unroll
+            float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll 1
             for (int half = 0; half < 2; ++half) {
-                uint32_t pk[32];
+                uint32_t r[64], pk[32];
+                load(half, r);
+                float2 s4[4];
 #pragma unroll
-                for (int cc = 0; cc < 2; ++cc) {
-                    const int c4 = half * 2 + cc;
+                for (int e = 0; e < 4; ++e) s4[e] = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 x2 = fma2(make_float2(__uint_as_float(r[c4][e]), __uint_as_float(r[c4][e + 1])), scale2, nref2);
-                        const float2 p2 = make_float2(ex2_approx(x2.x), ex2_approx(x2.y));
-                        s4[(e >> 1) & 3] = add2(s4[(e >> 1) & 3], p2);
-                        pk[cc * 16 + e / 2] = pack_bf16x2(p2.x, p2.y);
-                    }
+                for (int e = 0; e < 64; e += 2) {
+                    const float2 x2 = fma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), scale2, nref2);
+                    const float2 p2 = make_float2(ex2_approx(x2.x), ex2_approx(x2.y));
+                    s4[(e >> 1) & 3] = add2(s4[(e >> 1) & 3], p2);
+                    pk[e / 2] = pack_bf16x2(p2.x, p2.y);
                 }
                 tmem_st_32x32b_x32(tS + half * 32, pk);
+                s2 = add2(s2, add2(add2(s4[0], s4[1]), add2(s4[2], s4[3])));
             }
-            const float2 s2 = add2(add2(s4[0], s4[1]), add2(s4[2], s4[3]));
             // the largest weight's rounding to bf16 goes into the normaliser, so that a row that one key
             // dominates is divided by the weight that its V row got; lse keeps the unrounded sum
             const float p_max = mx == -INFINITY ? 0.f : ex2_approx(fmaf(mx, sl2, -ref));
@@ -737,7 +730,8 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
             const bool poison = *reinterpret_cast<volatile int*>(smem + C::kPoison + (item & 7) * 4) == (int)item + 1;
             const float inv = whole ? (none ? 0.f : 1.0f / den) : 1.0f;
             const long long grow = ((long long)w.b * a.Hkv + w.g) * a.R + x;
-            const long long prow = ((long long)blockIdx.x * 2 + (w.first ? 0 : 1)) * a.rt + (kNq == 2 ? wg * 128 : 0) + rw;
+            const long long pslot = (long long)blockIdx.x * 2 + (w.first ? 0 : 1);
+            const int prow = (kNq == 2 ? wg * 128 : 0) + rw;
             constexpr int kCols = kNq == 1 ? kHd / 2 : kHd;
             const int col0 = kNq == 1 ? wg * kCols : 0;
 #pragma unroll 1
@@ -787,20 +781,24 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
                                          : pack_bf16x2(__uint_as_float(o[8 * e + 2 * i]) * inv, __uint_as_float(o[8 * e + 2 * i + 1]) * inv);
                         dst[e] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
-                } else {
-                    float4* dst = reinterpret_cast<float4*>(whole ? static_cast<float*>(a.out) + grow * kHd + c : a.part_o + prow * kHd + c);
+                } else if (whole) {
+                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + grow * kHd + c);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         dst[e] = none ? make_float4(0.f, 0.f, 0.f, 0.f)
                                       : make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
                                                     __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+                } else {  // column by column: a warp's rows lie side by side
+                    float* dst = a.part_o + (pslot * kHd + c) * a.rt + prow;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) dst[(long long)e * a.rt] = __uint_as_float(o[e]);
                 }
             }
             if (live && (kNq == 2 || wg == 0)) {
                 if (whole)
                     a.lse[grow] = none ? -INFINITY : (m + log2f(l)) * kLn2;
                 else
-                    *reinterpret_cast<float4*>(a.part_ml + prow * 4) = make_float4(m, l, den, 0.f);
+                    *reinterpret_cast<float4*>(a.part_ml + (pslot * a.rt + prow) * 4) = make_float4(m, l, den, 0.f);
             }
         }
         if constexpr (kNq == 1) {  // the next item's products overwrite both O's
@@ -851,12 +849,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const WaitCtl ctl{abort_flag, a.status, kWaitLimitNs};
-
-    // launched with 512 x 128 registers; 2 x 128 x 192 + 2 x 128 x 64 = 65536
-    if (warp < 8)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;" ::: "memory");
-    else
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory");
 
     if (work) {
         if (warp < 8) {
