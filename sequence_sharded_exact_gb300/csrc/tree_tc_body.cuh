@@ -380,12 +380,11 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
                     for (int i = 0; i < 4; ++i) big = max(big, max(p[i] << 16 & 0x7fff0000u, p[i] & 0x7fff0000u));
 #pragma unroll
                     for (int o = kLanes / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-                    if (x >= rows) continue;
                     const bool finite = big < 0x7f800000u;
                     int e = (int)(big >> 23) - 135 + ((big & 0x7fffffu) > 0x600000u ? 1 : 0);
                     e = !finite || e < -126 ? -126 : e;
                     const float down = finite ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
-                    if (c == 0) scale[x] = finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7fc00000u);
+                    if (c == 0 && x < rows) scale[x] = finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7fc00000u);
                     uint2 hi, lo;
                     uint32_t* ph = &hi.x;
                     uint32_t* pl = &lo.x;
@@ -399,8 +398,10 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
                         pl[i] = (uint32_t)e4m3x2(f0 - h0, f1 - h1) | (uint32_t)e4m3x2(f2 - h2, f3 - h3) << 16;
                     }
                     uint8_t* q = smem + C::kQ + (uint32_t)(x >> 7) * C::kBytesQ + qk_offset(x & 127, c >> 1) + (c & 1) * 8;
-                    *reinterpret_cast<uint2*>(q) = hi;
-                    *reinterpret_cast<uint2*>(q + 128 * kHd) = lo;
+                    if (x < rows) {
+                        *reinterpret_cast<uint2*>(q) = hi;
+                        *reinterpret_cast<uint2*>(q + 128 * kHd) = lo;
+                    }
                 }
             }
         }
@@ -417,13 +418,14 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
             const uint8_t* src = smem + C::kL + (uint32_t)sl * C::kBytesK;
             uint8_t* dst = smem + C::kP + (uint32_t)sp * C::kBytesV;
             const float up = reinterpret_cast<const float*>(smem + C::kX + sx * 1024)[128 + row];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::bXEmpty + sx));
             const int key = t * kTreeTile + row;
             const bool past = key >= w.s.end, drafted = key >= w.s.len;
             bool hit = false;
             // a thread has a row; starting each at another chunk keeps a warp's accesses in different banks
-            auto chunk = [&](int i, uint32_t (&o)[8]) {
-                const int c = (i + row) & (kHd / 16 - 1);
-                const uint4 x = *reinterpret_cast<const uint4*>(src + row * kHd + c * 16);
+            auto at = [&](int i) { return (i + row) & (kHd / 16 - 1); };
+            auto convert = [&](const uint4& x, uint32_t (&o)[8]) {
                 const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -433,24 +435,27 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
                     o[2 * j + 1] = pack_bf16x2(f2 * up, f3 * up);
                 }
             };
-            auto store = [&](int i, const uint32_t (&o)[8]) {
-                const int c = (i + row) & (kHd / 16 - 1);
+            auto store = [&](int c, const uint32_t (&o)[8]) {
                 uint8_t* p = dst + (c >> 2) * 16384 + row * 128;
                 *reinterpret_cast<uint4*>(p + ((((2 * c) & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 *reinterpret_cast<uint4*>(p + ((((2 * c + 1) & 7) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
             };
+            uint4 x[kHd / 16];
+#pragma unroll
+            for (int i = 0; i < kHd / 16; ++i) x[i] = *reinterpret_cast<const uint4*>(src + row * kHd + at(i) * 16);
             if ((t + 1) * kTreeTile <= w.s.len) {  // no branch inside: the chunks' conversions overlap
-#pragma unroll 2
+#pragma unroll
                 for (int i = 0; i < kHd / 16; ++i) {
                     uint32_t o[8];
-                    chunk(i, o);
-                    store(i, o);
+                    convert(x[i], o);
+                    store(at(i), o);
                 }
             } else {
 #pragma unroll 1
                 for (int i = 0; i < kHd / 16; ++i) {
+                    const int c = at(i);
                     uint32_t o[8];
-                    chunk(i, o);
+                    convert(*reinterpret_cast<const uint4*>(src + row * kHd + c * 16), o);
                     if (drafted) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
@@ -460,7 +465,7 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
                                 hit |= clear_nonfinite(o[j]);
                         }
                     }
-                    store(i, o);
+                    store(c, o);
                 }
             }
             if (hit) *reinterpret_cast<volatile int*>(smem + C::kPoison + (item & 7) * 4) = (int)item + 1;
@@ -479,7 +484,9 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
 // MMA issue (one thread)
 // ------------------------------------------------------------------------------------------------
 // An item's jobs, one S and one P V each: tile by tile, and (kNq == 2) warpgroup 0's query rows, then 1's.  Job j
-// belongs to warpgroup j & 1; its S is issued once P V of job j - 2, which reads the same TMEM columns, is.
+// belongs to warpgroup j & 1; its S is issued once P V of job j - 2, which reads the same TMEM columns, is.  A
+// commit costs the issuing thread over 100 cycles, so there are two per job: S is ready (which also says that P V
+// of job j - 2 is done, and that K has been read), and V has been read.
 template <bool kE4, int kNq>
 __device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint32_t tmem, TreeWalk w, const WaitCtl& ctl)
 {
@@ -501,16 +508,8 @@ __device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint
                 pc ^= 1u << wg;
                 tc_fence_after_sync();
                 issue_pv(sbase + (kE4 ? C::kP + (uint32_t)sp * C::kBytesV : C::kL + (uint32_t)sp * C::kBytesK), tmem, wg, j >= 4);
-                tc_commit(bar(C::bO + wg));
-                if (kNq == 1 || wg == 1) {
-                    if constexpr (kE4) {
-                        tc_commit(bar(C::bPEmpty + sp));
-                        tc_commit(bar(C::bXEmpty + (int)(vc % C::kSlotsX)));
-                    } else {
-                        tc_commit(bar(C::bLEmpty + sp));
-                    }
-                    ++vc;
-                }
+                if (j >= n) tc_commit(bar(C::bO + wg));  // the warpgroup's last job of the item
+                if (kNq == 1 || wg == 1) tc_commit(bar((kE4 ? C::bPEmpty : C::bLEmpty) + (int)(vc++ % C::kSlotsP)));
             }
             if (j < n) {
                 const int slot = (int)(kc % C::kSlotsK);
@@ -520,11 +519,8 @@ __device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint
                     tc_fence_after_sync();
                 }
                 issue_s<kE4, kNq>(sbase, tmem, wg, slot);
-                tc_commit(bar(C::bS + wg));
-                if (kNq == 1 || wg == 1) {
-                    tc_commit(bar(C::bKEmpty + slot));
-                    ++kc;
-                }
+                tc_commit(bar(C::bS + wg));  // the softmax warps release K
+                if (kNq == 1 || wg == 1) ++kc;
                 if (j == n - 1) tc_commit(bar(C::bQEmpty));
             }
         }
@@ -573,8 +569,8 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + kColS + (uint32_t)wg * 128;
     const uint32_t tO = tmem + lanes + kColO + (uint32_t)wg * 128;
-    uint32_t jobs[2] = {0, 0};  // S tiles of each warpgroup so far
-    uint32_t tiles = 0, item = 0;
+    uint32_t jobs = 0, tiles = 0, item = 0;  // this warpgroup's jobs, all tiles, items so far
+    uint32_t pairs = 0;                      // items that both warpgroups had jobs of (kNq == 1)
 
     do {
         const int x = w.r * a.rt + (kNq == 2 ? wg * 128 : 0) + rw;  // query row of the kv head
@@ -592,10 +588,16 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
                 seen[0] = seen_bits(a, w.s, w.b, tq, k0);
                 seen[1] = seen_bits(a, w.s, w.b, tq, k0 + 64);
             }
-            const uint32_t job = jobs[wg]++;
+            const uint32_t job = jobs++;
             if (!warp_wait(bar(C::bS + wg), job & 1, ctl)) return;
+            if (lane == 0 && (warp & 3) == 0 && (kNq == 1 || wg == 1)) {  // S of both warpgroups is in job order
+                mbar_arrive(bar(C::bKEmpty + (int)((tiles + (uint32_t)i) % C::kSlotsK)));
+            }
             if (!any_live) {  // no query row in these lanes: what P holds there reaches no row that is read
-                if (lane == 0) mbar_arrive(bar(C::bP + wg));
+                if (lane == 0) {
+                    if constexpr (kE4) mbar_arrive(bar(C::bXEmpty + (int)((tiles + (uint32_t)i) % C::kSlotsX)));
+                    mbar_arrive(bar(C::bP + wg));
+                }
                 continue;
             }
             tc_fence_after_sync();
@@ -607,44 +609,48 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
                 if (first)
                     sl2 = a.scale_log2 * reinterpret_cast<const float*>(smem + C::kQs)[(item & 1) * kNq * 128 + (kNq == 2 ? wg * 128 : 0) + rw];
             }
-            // S is read twice, 64 columns at a time in loops that are not unrolled: the maximum, then the weights.
-            // (Kept in registers in between, the 128 columns took a code of 24 KB a tile, and with the other
-            // warps' loops the instruction cache was what the kernel waited for.)
-            auto load = [&](int half, uint32_t (&r)[64]) {
-                tmem_ld_32x32b_x64(tS + half * 64, r);
+            // S is read twice in loops that are not unrolled: scaled, masked (and then stored again) for the
+            // maximum, then for the weights.  (Kept in registers in between, the 128 columns took a code of
+            // 24 KB a tile, and with the other warps' loops the instruction cache was what the kernel waited for.)
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t r[32];
+                float4 sc[kE4 ? 8 : 1];
+                if constexpr (kE4) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sc[e] = xs[c / 4 + e];
+                }
+                tmem_ld_32x32b_x32(tS + c, r);
                 tmem_ld_wait(r);
                 if constexpr (kE4) {
 #pragma unroll
-                    for (int e = 0; e < 64; e += 4) {
-                        const float4 sc = xs[half * 16 + e / 4];
-                        const float2 u0 = mul2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), make_float2(sc.x, sc.y));
-                        const float2 u1 = mul2(make_float2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), make_float2(sc.z, sc.w));
-                        r[e] = __float_as_uint(u0.x);
-                        r[e + 1] = __float_as_uint(u0.y);
-                        r[e + 2] = __float_as_uint(u1.x);
-                        r[e + 3] = __float_as_uint(u1.y);
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 u0 = mul2(make_float2(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1])), make_float2(sc[e].x, sc[e].y));
+                        const float2 u1 = mul2(make_float2(__uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3])), make_float2(sc[e].z, sc[e].w));
+                        r[4 * e] = __float_as_uint(u0.x);
+                        r[4 * e + 1] = __float_as_uint(u0.y);
+                        r[4 * e + 2] = __float_as_uint(u1.x);
+                        r[4 * e + 3] = __float_as_uint(u1.y);
                     }
                 }
                 if (masked) {
-                    const unsigned long long bits = half ? seen[1] : seen[0];
-                    const uint32_t lo = (uint32_t)bits, hi = (uint32_t)(bits >> 32);
+                    const uint32_t bits = (uint32_t)((c < 64 ? seen[0] : seen[1]) >> (c & 32));
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        if (!(lo & 1u << e)) r[e] = __float_as_uint(-INFINITY);
-                        if (!(hi & 1u << e)) r[32 + e] = __float_as_uint(-INFINITY);
-                    }
+                    for (int e = 0; e < 32; ++e)
+                        if (!(bits & 1u << e)) r[e] = __float_as_uint(-INFINITY);
                 }
-            };
-            float mx = -INFINITY;
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                uint32_t r[64];
-                load(half, r);
+                if (kE4 || masked) tmem_st_32x32b_x32(tS + c, r);
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < 64; e += 2) m4[(e >> 1) & 3] = max3f(m4[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+                for (int e = 0; e < 32; e += 2) m4[(e >> 1) & 3] = max3f(m4[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
                 mx = max3f(mx, max3f(m4[0], m4[1], m4[2]), m4[3]);
             }
+            if constexpr (kE4) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::bXEmpty + (int)((tiles + (uint32_t)i) % C::kSlotsX)));
+            }
+            if (kE4 || masked) tmem_st_wait();
             const float m_tile = mx * sl2;
             const float m_new = m_tile > m_run + 8.0f ? m_tile : m_run;
             const float alpha = m_new == m_run ? 1.0f : ex2_approx(m_run - m_new);
@@ -654,7 +660,8 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 uint32_t r[64], pk[32];
-                load(half, r);
+                tmem_ld_32x32b_x64(tS + half * 64, r);
+                tmem_ld_wait(r);
                 float2 s4[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s4[e] = make_float2(0.f, 0.f);
@@ -676,8 +683,7 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
             c_run = c_run * alpha + (p_max_bf16 - p_max);
             tmem_st_wait();
             if (__any_sync(0xffffffffu, !first && live && alpha != 1.0f)) {
-                if (!warp_wait(bar(C::bO + wg), (job - 1) & 1, ctl)) return;
-                tc_fence_after_sync();
+                // (the previous job's P V is done: S of this one was committed after it)
 #pragma unroll 1
                 for (int c4 = 0; c4 < kHd / 32; ++c4) {
                     uint32_t o[32];
@@ -704,7 +710,6 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
         float m = m_run, l = l_run, den = l_run + c_run, w0 = 1.f, w1 = 0.f;
         const int n1 = kNq == 1 ? n >> 1 : 0;
         if constexpr (kNq == 1) {
-            jobs[wg ^ 1] += (uint32_t)(wg == 0 ? n1 : n - n1);
             float4* ml = reinterpret_cast<float4*>(smem + C::kMl);
             ml[wg * 128 + rw] = make_float4(m, l, den, 0.f);
             __syncwarp();
@@ -719,10 +724,10 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
             den = a0.z * w0 + a1.z * w1;
             if (a0.x == -INFINITY && a0.y != 0.f) l = den = a0.y;  // NaN scores alone leave no maximum
             if (a1.x == -INFINITY && a1.y != 0.f) l = den = a1.y;
-            if (!warp_wait(bar(C::bO + 0), (jobs[0] - 1) & 1, ctl)) return;
-            if (n1 > 0 && !warp_wait(bar(C::bO + 1), (jobs[1] - 1) & 1, ctl)) return;
+            if (!warp_wait(bar(C::bO + 0), item & 1, ctl)) return;
+            if (n1 > 0 && !warp_wait(bar(C::bO + 1), pairs++ & 1, ctl)) return;
         } else {
-            if (!warp_wait(bar(C::bO + wg), (jobs[wg] - 1) & 1, ctl)) return;
+            if (!warp_wait(bar(C::bO + wg), item & 1, ctl)) return;
         }
         tc_fence_after_sync();
         if (any_live) {
@@ -832,6 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             if (i == C::bEpi || i == C::bEpi + 1) cnt = 8;                          // of both
             if (i >= C::bPFull && i < C::bPEmpty) cnt = 4;                          // warps 12-15
             if (kE4 && (i == C::bQFull || (i >= C::bLEmpty && i < C::bPFull))) cnt = 4;
+            if (kE4 && i >= C::bXEmpty) cnt = 4 * kNq + 4;                          // the warps that read a tile's scales
             mbar_init(sbase + C::kBar + 8u * (uint32_t)i, cnt);
         }
         for (int i = 0; i < 8; ++i) reinterpret_cast<int*>(smem + C::kPoison)[i] = 0;
