@@ -12,7 +12,7 @@
 //     columns each.
 //   * More (kNq = 2): 256 query rows as two 128-row tiles that share every K/V tile, a warpgroup each.
 //   * m follows the row maximum only when that grows by more than 2^8: O / l does not depend on the
-//     reference, and O in TMEM is then seldom rescaled.
+//     reference, O in TMEM is then seldom rescaled, and S is read once.
 //   * Warps: 0-3 and 4-7 softmax; 8 loads the queries and K, 10 V (TMA, one thread each); 9 issues the MMAs;
 //     11 fetches the rows' scales (e4m3); 12-15 prepare V.
 // Rows that must not count: scores of unseen rows are set to -infinity before the maximum, but 0 * NaN in
@@ -43,7 +43,7 @@ constexpr int kHd = RA_TREE_HD;
 static_assert(kHd == 128 || kHd == 64, "head dim");
 constexpr int kThreads = 512;
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;  // S_w at 128 w, O_w at 256 + 128 w
-constexpr uint64_t kWaitLimitNs = 4000000000ull;             // 4 s
+constexpr long long kWaitLimit = 10000000000ll;
 
 template <bool kE4, int kNq>
 struct Cfg {
@@ -83,15 +83,21 @@ struct Maps {
     CUtensorMap q, k, v;
 };
 
-// Waits.  The part that polls is a function of its own: inlined at every wait it took the loops of the roles,
-// which run side by side, out of the instruction cache.
-__device__ __noinline__ bool poll(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int* status)
-{
-    return mbar_wait_slow(bar, parity, WaitCtl{abort, status, kWaitLimitNs});
-}
+// A bounded wait, short enough to be inlined at every use: the loops of the roles run side by side and have to
+// stay in the instruction cache together.  Gives up after kWaitLimit cycles (over 4 s at the highest clock), or
+// when another warp has.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const WaitCtl& ctl)
 {
-    return mbar_try_wait(bar, parity) || poll(bar, parity, ctl.abort, ctl.status);
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*ctl.abort) return false;
+        if (clock64() - t0 > kWaitLimit) {
+            *ctl.abort = 1;
+            atomicOr(ctl.status, kStatusTimeout);
+            return false;
+        }
+    }
+    return true;
 }
 // The whole warp's: every lane learns whether all of them saw the phase.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl& ctl)
@@ -417,7 +423,7 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
             if (use > 0 && !warp_wait(bar(C::bPEmpty + sp), (use - 1) & 1, ctl)) return;
             const uint8_t* src = smem + C::kL + (uint32_t)sl * C::kBytesK;
             uint8_t* dst = smem + C::kP + (uint32_t)sp * C::kBytesV;
-            const float up = reinterpret_cast<const float*>(smem + C::kX + sx * 1024)[128 + row];
+            const __nv_bfloat162 up = __float2bfloat162_rn(reinterpret_cast<const float*>(smem + C::kX + sx * 1024)[128 + row]);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::bXEmpty + sx));
             const int key = t * kTreeTile + row;
@@ -431,8 +437,9 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
                 for (int j = 0; j < 4; ++j) {
                     float f0, f1, f2, f3;
                     e4m3x4_to_float(u[j], f0, f1, f2, f3);
-                    o[2 * j] = pack_bf16x2(f0 * up, f1 * up);
-                    o[2 * j + 1] = pack_bf16x2(f2 * up, f3 * up);
+                    __nv_bfloat162 p0 = __hmul2(__floats2bfloat162_rn(f0, f1), up), p1 = __hmul2(__floats2bfloat162_rn(f2, f3), up);
+                    o[2 * j] = *reinterpret_cast<const uint32_t*>(&p0);
+                    o[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&p1);
                 }
             };
             auto store = [&](int c, const uint32_t (&o)[8]) {
@@ -440,15 +447,20 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
                 *reinterpret_cast<uint4*>(p + ((((2 * c) & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 *reinterpret_cast<uint4*>(p + ((((2 * c + 1) & 7) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
             };
-            uint4 x[kHd / 16];
-#pragma unroll
-            for (int i = 0; i < kHd / 16; ++i) x[i] = *reinterpret_cast<const uint4*>(src + row * kHd + at(i) * 16);
             if ((t + 1) * kTreeTile <= w.s.len) {  // no branch inside: the chunks' conversions overlap
-#pragma unroll
-                for (int i = 0; i < kHd / 16; ++i) {
-                    uint32_t o[8];
-                    convert(x[i], o);
+                uint4 x0 = *reinterpret_cast<const uint4*>(src + row * kHd + at(0) * 16);
+                uint4 x1 = *reinterpret_cast<const uint4*>(src + row * kHd + at(1) * 16);
+#pragma unroll 1
+                for (int i = 0; i < kHd / 16; i += 2) {
+                    const uint4 n0 = *reinterpret_cast<const uint4*>(src + row * kHd + at(i + 2) * 16);
+                    const uint4 n1 = *reinterpret_cast<const uint4*>(src + row * kHd + at(i + 3) * 16);
+                    uint32_t o[8], p[8];
+                    convert(x0, o);
+                    convert(x1, p);
                     store(at(i), o);
+                    store(at(i + 1), p);
+                    x0 = n0;
+                    x1 = n1;
                 }
             } else {
 #pragma unroll 1
@@ -533,7 +545,7 @@ __device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint
 // softmax warpgroups
 // ------------------------------------------------------------------------------------------------
 // Which of the 64 rows from k0 query token t sees, one bit each; for tiles that reach past the prefix.
-__device__ __noinline__ unsigned long long seen_bits(const TreeArgs& a, const TreeSeq& s, int b, int t, int k0)
+__device__ __forceinline__ unsigned long long seen_bits(const TreeArgs& a, const TreeSeq& s, int b, int t, int k0)
 {
     const int p = s.len - k0;  // rows of the prefix among them
     unsigned long long bits = p >= 64 ? ~0ull : (p > 0 ? (1ull << p) - 1 : 0ull);
@@ -585,8 +597,12 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
             const bool masked = k0 + kTreeTile > w.s.len;
             unsigned long long seen[2] = {~0ull, ~0ull};
             if (masked && any_live) {
-                seen[0] = seen_bits(a, w.s, w.b, tq, k0);
-                seen[1] = seen_bits(a, w.s, w.b, tq, k0 + 64);
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const unsigned long long v = seen_bits(a, w.s, w.b, tq, k0 + 64 * h);
+                    seen[0] = h ? seen[0] : v;
+                    seen[1] = v;
+                }
             }
             const uint32_t job = jobs++;
             if (!warp_wait(bar(C::bS + wg), job & 1, ctl)) return;
@@ -609,25 +625,21 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
                 if (first)
                     sl2 = a.scale_log2 * reinterpret_cast<const float*>(smem + C::kQs)[(item & 1) * kNq * 128 + (kNq == 2 ? wg * 128 : 0) + rw];
             }
-            // S is read twice in loops that are not unrolled: scaled, masked (and then stored again) for the
-            // maximum, then for the weights.  (Kept in registers in between, the 128 columns took a code of
-            // 24 KB a tile, and with the other warps' loops the instruction cache was what the kernel waited for.)
-            float mx = -INFINITY;
+            // 32 columns of S at a time, their weights written over S as it is read.  The loop is not unrolled:
+            // the roles' loops run side by side and wait for the instruction cache when they do not fit it.
+            float m_tile = -INFINITY;
+            float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
+            for (int c = 0; c < 4; ++c) {
                 uint32_t r[32];
-                float4 sc[kE4 ? 8 : 1];
-                if constexpr (kE4) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sc[e] = xs[c / 4 + e];
-                }
-                tmem_ld_32x32b_x32(tS + c, r);
+                tmem_ld_32x32b_x32(tS + 32 * c, r);
                 tmem_ld_wait(r);
                 if constexpr (kE4) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float2 u0 = mul2(make_float2(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1])), make_float2(sc[e].x, sc[e].y));
-                        const float2 u1 = mul2(make_float2(__uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3])), make_float2(sc[e].z, sc[e].w));
+                        const float4 sc = xs[8 * c + e];
+                        const float2 u0 = mul2(make_float2(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1])), make_float2(sc.x, sc.y));
+                        const float2 u1 = mul2(make_float2(__uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3])), make_float2(sc.z, sc.w));
                         r[4 * e] = __float_as_uint(u0.x);
                         r[4 * e + 1] = __float_as_uint(u0.y);
                         r[4 * e + 2] = __float_as_uint(u1.x);
@@ -635,74 +647,77 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
                     }
                 }
                 if (masked) {
-                    const uint32_t bits = (uint32_t)((c < 64 ? seen[0] : seen[1]) >> (c & 32));
+                    const uint32_t bits = (uint32_t)((c < 2 ? seen[0] : seen[1]) >> (32 * (c & 1)));
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (!(bits & 1u << e)) r[e] = __float_as_uint(-INFINITY);
                 }
-                if (kE4 || masked) tmem_st_32x32b_x32(tS + c, r);
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) m4[(e >> 1) & 3] = max3f(m4[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
-                mx = max3f(mx, max3f(m4[0], m4[1], m4[2]), m4[3]);
-            }
-            if constexpr (kE4) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::bXEmpty + (int)((tiles + (uint32_t)i) % C::kSlotsX)));
-            }
-            if (kE4 || masked) tmem_st_wait();
-            const float m_tile = mx * sl2;
-            const float m_new = m_tile > m_run + 8.0f ? m_tile : m_run;
-            const float alpha = m_new == m_run ? 1.0f : ex2_approx(m_run - m_new);
-            const float ref = m_new == -INFINITY ? 0.f : m_new;
-            const float2 scale2 = make_float2(sl2, sl2), nref2 = make_float2(-ref, -ref);
-            float2 s2 = make_float2(0.f, 0.f);
+                const float m_new = max3f(max3f(m4[0], m4[1], m4[2]), m4[3], -INFINITY) * sl2;
+                m_tile = fmaxf(m_tile, m_new);
+                const bool raise = live && m_new > m_run + 8.0f;
+                if (__any_sync(0xffffffffu, raise)) {
+                    // The reference goes up, by a whole number of binades once there is one, and with it go the
+                    // sums, O (the previous job's P V is done: S of this one was committed after it), and the
+                    // weights of this tile's columns so far, which a power of two leaves as they are rounded.
+                    const float to = raise ? (m_run == -INFINITY ? m_new : m_run + ceilf(m_new - m_run)) : m_run;
+                    const float alpha = to == m_run ? 1.0f : ex2_approx(m_run - to);
+                    l_run *= alpha;
+                    c_run *= alpha;
+                    s2 = mul2(s2, make_float2(alpha, alpha));
+                    m_run = to;
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                uint32_t r[64], pk[32];
-                tmem_ld_32x32b_x64(tS + half * 64, r);
-                tmem_ld_wait(r);
-                float2 s4[4];
+                    for (int k = first ? 0 : kHd / 16; k > 0; --k) {
+                        uint32_t o[16];
+                        tmem_ld_32x32b_x16(tO + 16 * (k - 1), o);
+                        tmem_ld_wait(o);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s4[e] = make_float2(0.f, 0.f);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st_32x32b_x16(tO + 16 * (k - 1), o);
+                    }
+                    const __nv_bfloat162 a2 = __float2bfloat162_rn(alpha);
+#pragma unroll 1
+                    for (int k = 0; k < c; ++k) {
+                        uint32_t o[16];
+                        tmem_st_wait();
+                        tmem_ld_32x32b_x16(tS + 16 * k, o);
+                        tmem_ld_wait(o);
 #pragma unroll
-                for (int e = 0; e < 64; e += 2) {
+                        for (int e = 0; e < 16; ++e) {
+                            __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o[e]), a2);
+                            o[e] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                        tmem_st_32x32b_x16(tS + 16 * k, o);
+                    }
+                }
+                const float ref = m_run == -INFINITY ? 0.f : m_run;
+                const float2 scale2 = make_float2(sl2, sl2), nref2 = make_float2(-ref, -ref);
+                float2 s4[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
                     const float2 x2 = fma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), scale2, nref2);
                     const float2 p2 = make_float2(ex2_approx(x2.x), ex2_approx(x2.y));
-                    s4[(e >> 1) & 3] = add2(s4[(e >> 1) & 3], p2);
+                    s4[(e >> 1) & 1] = add2(s4[(e >> 1) & 1], p2);
                     pk[e / 2] = pack_bf16x2(p2.x, p2.y);
                 }
-                tmem_st_32x32b_x32(tS + half * 32, pk);
-                s2 = add2(s2, add2(add2(s4[0], s4[1]), add2(s4[2], s4[3])));
+                tmem_st_32x32b_x16(tS + 16 * c, pk);
+                s2 = add2(s2, add2(s4[0], s4[1]));
+            }
+            if constexpr (kE4) {
+                if (lane == 0) mbar_arrive(bar(C::bXEmpty + (int)((tiles + (uint32_t)i) % C::kSlotsX)));
             }
             // the largest weight's rounding to bf16 goes into the normaliser, so that a row that one key
             // dominates is divided by the weight that its V row got; lse keeps the unrounded sum
-            const float p_max = mx == -INFINITY ? 0.f : ex2_approx(fmaf(mx, sl2, -ref));
-            const float p_max_bf16 = __uint_as_float(pack_bf16x2(p_max, 0.f) << 16);
-            l_run = l_run * alpha + (s2.x + s2.y);
-            c_run = c_run * alpha + (p_max_bf16 - p_max);
+            const float p_max = m_tile == -INFINITY ? 0.f : ex2_approx(m_tile - m_run);
+            l_run += s2.x + s2.y;
+            c_run += __uint_as_float(pack_bf16x2(p_max, 0.f) << 16) - p_max;
             tmem_st_wait();
-            if (__any_sync(0xffffffffu, !first && live && alpha != 1.0f)) {
-                // (the previous job's P V is done: S of this one was committed after it)
-#pragma unroll 1
-                for (int c4 = 0; c4 < kHd / 32; ++c4) {
-                    uint32_t o[32];
-                    tmem_ld_32x32b_x32(tO + c4 * 32, o);
-                    tmem_ld_wait(o);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 v = mul2(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), make_float2(alpha, alpha));
-                        o[e] = __float_as_uint(v.x);
-                        o[e + 1] = __float_as_uint(v.y);
-                    }
-                    tmem_st_32x32b_x32(tO + c4 * 32, o);
-                }
-                tmem_st_wait();
-            }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::bP + wg));
-            m_run = m_new;
             first = false;
         }
 
@@ -854,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const WaitCtl ctl{abort_flag, a.status, kWaitLimitNs};
+    const WaitCtl ctl{abort_flag, a.status, 0};
 
     if (work) {
         if (warp < 8) {
