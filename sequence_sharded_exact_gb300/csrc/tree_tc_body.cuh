@@ -88,6 +88,7 @@ struct Maps {
 // when another warp has.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const WaitCtl& ctl)
 {
+    if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (!mbar_try_wait(bar, parity)) {
         if (*ctl.abort) return false;
@@ -112,6 +113,22 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity)
         if (global_timer_ns() - t0 > 1000000000ull) return;
     }
 }
+
+// A place in a ring of kSlots slots and the parity of its use: full barriers are waited for with `par`, empty ones
+// (which the first round finds free) with `par ^ 1`.
+template <int kSlots>
+struct Ring {
+    int slot = 0;
+    uint32_t par = 0, round = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++slot == kSlots) {
+            slot = 0;
+            par ^= 1;
+            round = 1;
+        }
+    }
+};
 
 // Shared-memory descriptors.  K-major operands of bf16 and of 128-column e4m3 have 128-byte rows and that
 // swizzle; 64-column e4m3 rows are 64 bytes with the 64-byte swizzle (layout 4, 8-row groups of 512 bytes).
@@ -351,76 +368,78 @@ __device__ __forceinline__ uint32_t qk_offset(int row, int c16)  // 16-byte chun
     return kHd == 128 ? (uint32_t)(row * 128 + ((c16 ^ (row & 7)) << 4)) : (uint32_t)(row * 64 + ((c16 ^ ((row >> 1) & 3)) << 4));
 }
 
+// An item's queries as hi and lo e4m3 values with the row's scale, by the softmax warps; kHd / 8 lanes share a row.  Rows
+// past the kv head's keep what they hold: it reaches no row of S that is read.
+template <int kNq>
+__device__ __forceinline__ void split_queries(const TreeArgs& a, uint8_t* smem, const TreeWalk& w, uint32_t item)
+{
+    using C = Cfg<true, kNq>;
+    constexpr int kLanes = kHd / 8, kStep = 256 / kLanes, kU = 8;
+    const int tid = threadIdx.x, c = tid % kLanes;
+    const int rows = a.R - w.r * a.rt < kNq * 128 ? a.R - w.r * a.rt : kNq * 128;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                      (((long long)w.b * a.Hkv + w.g) * a.R + (long long)w.r * a.rt) * kHd) + c;
+    const int rows_up = (rows + kStep * kU - 1) / (kStep * kU) * (kStep * kU);  // the same for a whole warp
+    float* scale = reinterpret_cast<float*>(smem + C::kQs) + (item & 1) * kNq * 128;
+#pragma unroll 1
+    for (int x0 = tid / kLanes; x0 < rows_up; x0 += kStep * kU) {
+        uint4 v[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int x = x0 + u * kStep;
+            v[u] = x < rows ? src[(long long)x * (kHd / 8)] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int x = x0 + u * kStep;
+            const uint32_t p[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+            uint32_t big = 0;  // bits of the largest magnitude: bf16 in the upper half, ordered as integers
+#pragma unroll
+            for (int i = 0; i < 4; ++i) big = max(big, max(p[i] << 16 & 0x7fff0000u, p[i] & 0x7fff0000u));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+            const bool finite = big < 0x7f800000u;
+            int e = (int)(big >> 23) - 135 + ((big & 0x7fffffu) > 0x600000u ? 1 : 0);
+            e = !finite || e < -126 ? -126 : e;
+            const float down = finite ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
+            if (c == 0 && x < rows) scale[x] = finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7fc00000u);
+            uint2 hi, lo;
+            uint32_t* ph = &hi.x;
+            uint32_t* pl = &lo.x;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float f0 = __uint_as_float(p[2 * i] << 16) * down, f1 = __uint_as_float(p[2 * i] & 0xffff0000u) * down;
+                const float f2 = __uint_as_float(p[2 * i + 1] << 16) * down, f3 = __uint_as_float(p[2 * i + 1] & 0xffff0000u) * down;
+                ph[i] = (uint32_t)e4m3x2(f0, f1) | (uint32_t)e4m3x2(f2, f3) << 16;
+                float h0, h1, h2, h3;
+                e4m3x4_to_float(ph[i], h0, h1, h2, h3);
+                pl[i] = (uint32_t)e4m3x2(f0 - h0, f1 - h1) | (uint32_t)e4m3x2(f2 - h2, f3 - h3) << 16;
+            }
+            uint8_t* q = smem + C::kQ + (uint32_t)(x >> 7) * C::kBytesQ + qk_offset(x & 127, c >> 1) + (c & 1) * 8;
+            if (x < rows) {
+                *reinterpret_cast<uint2*>(q) = hi;
+                *reinterpret_cast<uint2*>(q + 128 * kHd) = lo;
+            }
+        }
+    }
+}
+
 template <int kNq>
 __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase, uint8_t* smem, TreeWalk w, const WaitCtl& ctl)
 {
     using C = Cfg<true, kNq>;
     auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
     const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
-    uint32_t vc = 0, item = 0;
+    Ring<C::kSlotsL> rl;
+    Ring<C::kSlotsP> rp;
+    Ring<C::kSlotsX> rx;
+    uint32_t item = 0;
     do {
-        // the item's queries: hi and lo e4m3 values and the row's scale; kHd / 8 lanes share a row.  Rows past the
-        // kv head's keep what they hold: it reaches no row of S that is read.
-        if (item > 0 && !warp_wait(bar(C::bQEmpty), (item - 1) & 1, ctl)) return;
-        {
-            constexpr int kLanes = kHd / 8, kStep = 128 / kLanes, kU = 8;
-            const int c = row % kLanes;
-            const int rows = a.R - w.r * a.rt < kNq * 128 ? a.R - w.r * a.rt : kNq * 128;
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                              (((long long)w.b * a.Hkv + w.g) * a.R + (long long)w.r * a.rt) * kHd) + c;
-            float* scale = reinterpret_cast<float*>(smem + C::kQs) + (item & 1) * kNq * 128;
-#pragma unroll 1
-            for (int x0 = row / kLanes; x0 < (rows + kStep * kU - 1) / (kStep * kU) * (kStep * kU); x0 += kStep * kU) {
-                uint4 v[kU];
-#pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    const int x = x0 + u * kStep;
-                    v[u] = x < rows ? src[(long long)x * (kHd / 8)] : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    const int x = x0 + u * kStep;
-                    const uint32_t p[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-                    uint32_t big = 0;  // bits of the largest magnitude: bf16 in the upper half, ordered as integers
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) big = max(big, max(p[i] << 16 & 0x7fff0000u, p[i] & 0x7fff0000u));
-#pragma unroll
-                    for (int o = kLanes / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-                    const bool finite = big < 0x7f800000u;
-                    int e = (int)(big >> 23) - 135 + ((big & 0x7fffffu) > 0x600000u ? 1 : 0);
-                    e = !finite || e < -126 ? -126 : e;
-                    const float down = finite ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
-                    if (c == 0 && x < rows) scale[x] = finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7fc00000u);
-                    uint2 hi, lo;
-                    uint32_t* ph = &hi.x;
-                    uint32_t* pl = &lo.x;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float f0 = __uint_as_float(p[2 * i] << 16) * down, f1 = __uint_as_float(p[2 * i] & 0xffff0000u) * down;
-                        const float f2 = __uint_as_float(p[2 * i + 1] << 16) * down, f3 = __uint_as_float(p[2 * i + 1] & 0xffff0000u) * down;
-                        ph[i] = (uint32_t)e4m3x2(f0, f1) | (uint32_t)e4m3x2(f2, f3) << 16;
-                        float h0, h1, h2, h3;
-                        e4m3x4_to_float(ph[i], h0, h1, h2, h3);
-                        pl[i] = (uint32_t)e4m3x2(f0 - h0, f1 - h1) | (uint32_t)e4m3x2(f2 - h2, f3 - h3) << 16;
-                    }
-                    uint8_t* q = smem + C::kQ + (uint32_t)(x >> 7) * C::kBytesQ + qk_offset(x & 127, c >> 1) + (c & 1) * 8;
-                    if (x < rows) {
-                        *reinterpret_cast<uint2*>(q) = hi;
-                        *reinterpret_cast<uint2*>(q + 128 * kHd) = lo;
-                    }
-                }
-            }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::bQFull));
-
-        for (int t = w.t0; t < w.t1; ++t, ++vc) {
-            const int sl = (int)(vc % C::kSlotsL), sp = (int)(vc % C::kSlotsP), sx = (int)(vc % C::kSlotsX);
-            const uint32_t use = vc / C::kSlotsP;
-            if (!warp_wait(bar(C::bXFull + sx), (vc / C::kSlotsX) & 1, ctl)) return;
-            if (!warp_wait(bar(C::bLFull + sl), (vc / C::kSlotsL) & 1, ctl)) return;
-            if (use > 0 && !warp_wait(bar(C::bPEmpty + sp), (use - 1) & 1, ctl)) return;
+        for (int t = w.t0; t < w.t1; ++t, rl.next(), rp.next(), rx.next()) {
+            const int sl = rl.slot, sp = rp.slot, sx = rx.slot;
+            if (!warp_wait(bar(C::bXFull + sx), rx.par, ctl)) return;
+            if (!warp_wait(bar(C::bLFull + sl), rl.par, ctl)) return;
+            if (rp.round && !warp_wait(bar(C::bPEmpty + sp), rp.par ^ 1, ctl)) return;
             const uint8_t* src = smem + C::kL + (uint32_t)sl * C::kBytesK;
             uint8_t* dst = smem + C::kP + (uint32_t)sp * C::kBytesV;
             const __nv_bfloat162 up = __float2bfloat162_rn(reinterpret_cast<const float*>(smem + C::kX + sx * 1024)[128 + row]);
@@ -504,7 +523,9 @@ __device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint
 {
     using C = Cfg<kE4, kNq>;
     auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
-    uint32_t kc = 0, vc = 0, item = 0, pc = 0;  // pc: a parity bit per warpgroup
+    Ring<C::kSlotsK> rk;
+    Ring<C::kSlotsP> rv;
+    uint32_t item = 0, pc = 0;  // pc: a parity bit per warpgroup
     bool ok = true;
     do {
         if (!wait(bar(C::bQFull), item++ & 1, ctl)) break;
@@ -514,25 +535,26 @@ __device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint
         for (int j = 0; j < n + 2; ++j) {
             const int wg = j & 1;
             if (j >= 2) {
-                const int sp = (int)(vc % C::kSlotsP);
-                ok = wait(bar(C::bPFull + sp), (vc / C::kSlotsP) & 1, ctl) && wait(bar(C::bP + wg), pc >> wg & 1, ctl);
+                ok = wait(bar(C::bPFull + rv.slot), rv.par, ctl) && wait(bar(C::bP + wg), pc >> wg & 1, ctl);
                 if (!ok) break;
                 pc ^= 1u << wg;
                 tc_fence_after_sync();
-                issue_pv(sbase + (kE4 ? C::kP + (uint32_t)sp * C::kBytesV : C::kL + (uint32_t)sp * C::kBytesK), tmem, wg, j >= 4);
+                issue_pv(sbase + (kE4 ? C::kP + (uint32_t)rv.slot * C::kBytesV : C::kL + (uint32_t)rv.slot * C::kBytesK), tmem, wg, j >= 4);
                 if (j >= n) tc_commit(bar(C::bO + wg));  // the warpgroup's last job of the item
-                if (kNq == 1 || wg == 1) tc_commit(bar((kE4 ? C::bPEmpty : C::bLEmpty) + (int)(vc++ % C::kSlotsP)));
+                if (kNq == 1 || wg == 1) {
+                    tc_commit(bar((kE4 ? C::bPEmpty : C::bLEmpty) + rv.slot));
+                    rv.next();
+                }
             }
             if (j < n) {
-                const int slot = (int)(kc % C::kSlotsK);
                 if (kNq == 1 || wg == 0) {
-                    ok = wait(bar(C::bKFull + slot), (kc / C::kSlotsK) & 1, ctl);
+                    ok = wait(bar(C::bKFull + rk.slot), rk.par, ctl);
                     if (!ok) break;
                     tc_fence_after_sync();
                 }
-                issue_s<kE4, kNq>(sbase, tmem, wg, slot);
+                issue_s<kE4, kNq>(sbase, tmem, wg, rk.slot);
                 tc_commit(bar(C::bS + wg));  // the softmax warps release K
-                if (kNq == 1 || wg == 1) ++kc;
+                if (kNq == 1 || wg == 1) rk.next();
                 if (j == n - 1) tc_commit(bar(C::bQEmpty));
             }
         }
@@ -590,6 +612,13 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
         const bool live = x < a.R && tq < w.s.cnt;
         const bool any_live = __any_sync(0xffffffffu, live);
         const int n = w.t1 - w.t0;
+        if constexpr (kE4) {
+            if (item > 0 && !warp_wait(bar(C::bQEmpty), (item - 1) & 1, ctl)) return;
+            split_queries<kNq>(a, smem, w, item);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::bQFull));
+        }
         float m_run = -INFINITY, l_run = 0.f, c_run = 0.f, sl2 = a.scale_log2;
         bool first = true;
         for (int i = kNq == 1 ? wg : 0; i < n; i += kNq == 1 ? 2 : 1) {
@@ -606,12 +635,13 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
             }
             const uint32_t job = jobs++;
             if (!warp_wait(bar(C::bS + wg), job & 1, ctl)) return;
-            if (lane == 0 && (warp & 3) == 0 && (kNq == 1 || wg == 1)) {  // S of both warpgroups is in job order
-                mbar_arrive(bar(C::bKEmpty + (int)((tiles + (uint32_t)i) % C::kSlotsK)));
-            }
+            const uint32_t tile = tiles + (uint32_t)i;  // of all this CTA's
+            if (lane == 0 && (warp & 3) == 0 && (kNq == 1 || wg == 1))  // S of both warpgroups is in job order
+                mbar_arrive(bar(C::bKEmpty + (int)(tile % C::kSlotsK)));
+            const int sx = (int)(tile % C::kSlotsX);
             if (!any_live) {  // no query row in these lanes: what P holds there reaches no row that is read
                 if (lane == 0) {
-                    if constexpr (kE4) mbar_arrive(bar(C::bXEmpty + (int)((tiles + (uint32_t)i) % C::kSlotsX)));
+                    if constexpr (kE4) mbar_arrive(bar(C::bXEmpty + sx));
                     mbar_arrive(bar(C::bP + wg));
                 }
                 continue;
@@ -619,9 +649,8 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
             tc_fence_after_sync();
             const float4* xs = nullptr;
             if constexpr (kE4) {
-                const uint32_t xc = tiles + (uint32_t)i;
-                if (!warp_wait(bar(C::bXFull + (int)(xc % C::kSlotsX)), (xc / C::kSlotsX) & 1, ctl)) return;
-                xs = reinterpret_cast<const float4*>(smem + C::kX + (xc % C::kSlotsX) * 1024);
+                if (!warp_wait(bar(C::bXFull + sx), (tile / C::kSlotsX) & 1, ctl)) return;
+                xs = reinterpret_cast<const float4*>(smem + C::kX + sx * 1024);
                 if (first)
                     sl2 = a.scale_log2 * reinterpret_cast<const float*>(smem + C::kQs)[(item & 1) * kNq * 128 + (kNq == 2 ? wg * 128 : 0) + rw];
             }
@@ -632,14 +661,18 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t r[32];
+                float4 sc[kE4 ? 8 : 1];
+                if constexpr (kE4) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sc[e] = xs[8 * c + e];
+                }
                 tmem_ld_32x32b_x32(tS + 32 * c, r);
                 tmem_ld_wait(r);
                 if constexpr (kE4) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float4 sc = xs[8 * c + e];
-                        const float2 u0 = mul2(make_float2(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1])), make_float2(sc.x, sc.y));
-                        const float2 u1 = mul2(make_float2(__uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3])), make_float2(sc.z, sc.w));
+                        const float2 u0 = mul2(make_float2(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1])), make_float2(sc[e].x, sc[e].y));
+                        const float2 u1 = mul2(make_float2(__uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3])), make_float2(sc[e].z, sc[e].w));
                         r[4 * e] = __float_as_uint(u0.x);
                         r[4 * e + 1] = __float_as_uint(u0.y);
                         r[4 * e + 2] = __float_as_uint(u1.x);
@@ -707,7 +740,7 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
                 s2 = add2(s2, add2(s4[0], s4[1]));
             }
             if constexpr (kE4) {
-                if (lane == 0) mbar_arrive(bar(C::bXEmpty + (int)((tiles + (uint32_t)i) % C::kSlotsX)));
+                if (lane == 0) mbar_arrive(bar(C::bXEmpty + sx));
             }
             // the largest weight's rounding to bf16 goes into the normaliser, so that a row that one key
             // dominates is divided by the weight that its V row got; lse keeps the unrounded sum
@@ -851,7 +884,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             if (i == C::bP || i == C::bP + 1) cnt = 4;                              // softmax warps of one group
             if (i == C::bEpi || i == C::bEpi + 1) cnt = 8;                          // of both
             if (i >= C::bPFull && i < C::bPEmpty) cnt = 4;                          // warps 12-15
-            if (kE4 && (i == C::bQFull || (i >= C::bLEmpty && i < C::bPFull))) cnt = 4;
+            if (kE4 && i == C::bQFull) cnt = 8;                                     // softmax warps
+            if (kE4 && i >= C::bLEmpty && i < C::bPFull) cnt = 4;
             if (kE4 && i >= C::bXEmpty) cnt = 4 * kNq + 4;                          // the warps that read a tile's scales
             mbar_init(sbase + C::kBar + 8u * (uint32_t)i, cnt);
         }
