@@ -86,145 +86,126 @@ __device__ __forceinline__ int row_exponent(float amax)
 
 struct WriteArgs {
     int B, Hkv, T, cap;
-    const void* x[2];                // k, v
-    long long s[2][3];               // their element strides: batch, head, row
-    void* values[2];
-    uint8_t* exps[2];                // null: the cache holds the inputs' dtype
-    const int *lens, *ntok;          // either may be null: 0, T
+    const void *k, *v;
+    long long ks[3], vs[3];  // element strides: batch, head, row
+    void *k_out, *v_out;
+    uint8_t *k_exp, *v_exp;  // null: the cache holds the inputs' dtype
+    const int *lens, *ntok;  // either may be null: 0, T
     unsigned int* status;
 };
 
-// Where token t of sequence b goes, or -1: not one of its tokens, or outside the cache.
-__device__ __forceinline__ long long write_row(const WriteArgs& a, int b, int t)
-{
-    if (a.ntok) {
-        const int n = a.ntok[b];
-        if (t == 0 && (n < 0 || n > a.T)) atomicOr(a.status, kStatusRange);
-        if (t >= n) return -1;
-    }
-    const long long row = (a.lens ? a.lens[b] : 0) + (long long)t;
-    if (row >= t && row < a.cap) return row;
-    atomicOr(a.status, kStatusRange);
-    return -1;
-}
-
+// Grid: blocks of rows, heads of all sequences, k or v.  A block stays with one head, so that a row costs no division.
 template <typename T, int D, bool QUANT>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteArgs a)
 {
     constexpr int LPR = D / 8, kGroups = kThreads / LPR;
-    const int ch = threadIdx.x % LPR;
+    const int ch = threadIdx.x % LPR, grp = threadIdx.x / LPR;
     const unsigned mask = ((1u << LPR) - 1u) << (threadIdx.x & 31 & ~(LPR - 1));
-    const long long half = (long long)a.B * a.Hkv * a.T, total = 2 * half;
-    const long long step = (long long)gridDim.x * kGroups;
-    const long long first = (long long)blockIdx.x * kGroups + threadIdx.x / LPR;
-    for (long long base = first; base < total; base += step * kUnroll) {
-        Eight<T> x[kUnroll];
-        long long dst[kUnroll];  // cache row, all heads counted; -1: nothing to write
-        int kind[kUnroll];
+    const bool is_v = blockIdx.z != 0;
+    const long long s0 = is_v ? a.vs[0] : a.ks[0], s1 = is_v ? a.vs[1] : a.ks[1], s2 = is_v ? a.vs[2] : a.ks[2];
+    for (int bh = blockIdx.y; bh < a.B * a.Hkv; bh += gridDim.y) {
+        const int b = bh / a.Hkv, h = bh - b * a.Hkv;
+        const int len = a.lens ? a.lens[b] : 0, given = a.ntok ? a.ntok[b] : a.T;
+        int n = given < 0 ? 0 : (given > a.T ? a.T : given);
+        const int fit = len < 0 || len > a.cap ? 0 : (n < a.cap - len ? n : a.cap - len);
+        if ((n != given || fit != n) && blockIdx.x == 0 && h == 0 && !is_v && threadIdx.x == 0) atomicOr(a.status, kStatusRange);
+        n = fit;
+        const T* src = static_cast<const T*>(is_v ? a.v : a.k) + b * s0 + h * s1 + ch * 8;
+        const long long row0 = (long long)bh * a.cap + len;
+        for (int t0 = blockIdx.x * (kGroups * kUnroll) + grp; t0 < n; t0 += gridDim.x * (kGroups * kUnroll)) {
+            Eight<T> x[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const long long idx = base + u * step;
-            dst[u] = -1;
-            kind[u] = 0;
-            if (idx >= total) continue;
-            kind[u] = idx >= half;
-            const long long i = idx - (kind[u] ? half : 0);
-            const int t = (int)(i % a.T);
-            const long long bh = i / a.T;
-            const int b = (int)(bh / a.Hkv), h = (int)(bh % a.Hkv);
-            const long long row = write_row(a, b, t);
-            if (row < 0) continue;
-            dst[u] = bh * a.cap + row;
-            const long long* s = a.s[kind[u]];
-            x[u].load(static_cast<const T*>(a.x[kind[u]]) + b * s[0] + h * s[1] + t * s[2] + ch * 8);
-        }
+            for (int u = 0; u < kUnroll; ++u)
+                if (t0 + u * kGroups < n) x[u].load(src + (long long)(t0 + u * kGroups) * s2);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            if (dst[u] < 0) continue;  // the same for every lane of a row
-            if constexpr (!QUANT) {
-                x[u].store(static_cast<T*>(a.values[kind[u]]) + dst[u] * D + ch * 8);
-            } else {
-                float f[8], m = 0.f;
-                x[u].get(f);
+            for (int u = 0; u < kUnroll; ++u) {
+                if (t0 + u * kGroups >= n) break;  // the same for every lane of a row
+                const long long dst = row0 + t0 + u * kGroups;
+                if constexpr (!QUANT) {
+                    x[u].store(static_cast<T*>(is_v ? a.v_out : a.k_out) + dst * D + ch * 8);
+                } else {
+                    float f[8], m = 0.f;
+                    x[u].get(f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+                    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
 #pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
-                const int e = row_exponent(m);
-                const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
-                uint2 w;
-                w.x = (uint32_t)e4m3x2(f[0] * down, f[1] * down) | (uint32_t)e4m3x2(f[2] * down, f[3] * down) << 16;
-                w.y = (uint32_t)e4m3x2(f[4] * down, f[5] * down) | (uint32_t)e4m3x2(f[6] * down, f[7] * down) << 16;
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.values[kind[u]]) + dst[u] * D + ch * 8) = w;
-                if (ch == 0) a.exps[kind[u]][dst[u]] = (uint8_t)(e + 127);
+                    for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
+                    const int e = row_exponent(m);
+                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
+                    uint2 w;
+                    w.x = (uint32_t)e4m3x2(f[0] * down, f[1] * down) | (uint32_t)e4m3x2(f[2] * down, f[3] * down) << 16;
+                    w.y = (uint32_t)e4m3x2(f[4] * down, f[5] * down) | (uint32_t)e4m3x2(f[6] * down, f[7] * down) << 16;
+                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.v_out : a.k_out) + dst * D + ch * 8) = w;
+                    if (ch == 0) (is_v ? a.v_exp : a.k_exp)[dst] = (uint8_t)(e + 127);
+                }
             }
         }
     }
 }
 
 struct ReadArgs {
-    int B, Hkv, cap, row0, rows;
-    const void* values[2];
-    const uint8_t* exps[2];
-    void* out[2];
+    int heads, cap, row0, rows;  // heads of all sequences
+    const void *k, *v;
+    const uint8_t *k_exp, *v_exp;
+    void *k_out, *v_out;
 };
 
 template <typename T, int D, bool QUANT>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a)
 {
     constexpr int LPR = D / 8, kGroups = kThreads / LPR;
-    const int ch = threadIdx.x % LPR;
-    const long long half = (long long)a.B * a.Hkv * a.rows, total = 2 * half;
-    const long long step = (long long)gridDim.x * kGroups;
-    const long long first = (long long)blockIdx.x * kGroups + threadIdx.x / LPR;
-    for (long long base = first; base < total; base += step * kUnroll) {
-        Eight<T> x[kUnroll];
-        uint2 w[kUnroll];
-        uint32_t e[kUnroll];
+    const int ch = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+    const bool is_v = blockIdx.z != 0;
+    for (int bh = blockIdx.y; bh < a.heads; bh += gridDim.y) {
+        const long long in0 = (long long)bh * a.cap + a.row0, out0 = (long long)bh * a.rows;
+        const uint8_t* exps = is_v ? a.v_exp : a.k_exp;
+        T* out = static_cast<T*>(is_v ? a.v_out : a.k_out) + out0 * D + ch * 8;
+        for (int t0 = blockIdx.x * (kGroups * kUnroll) + grp; t0 < a.rows; t0 += gridDim.x * (kGroups * kUnroll)) {
+            Eight<T> x[kUnroll];
+            uint2 w[kUnroll];
+            uint32_t e[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const long long idx = base + u * step;
-            if (idx >= total) continue;
-            const int kind = idx >= half;
-            const long long i = idx - (kind ? half : 0);
-            const long long src = i / a.rows * a.cap + a.row0 + i % a.rows;
-            if constexpr (QUANT) {
-                w[u] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.values[kind]) + src * D + ch * 8);
-                e[u] = a.exps[kind][src];
-            } else {
-                x[u].load(static_cast<const T*>(a.values[kind]) + src * D + ch * 8);
+            for (int u = 0; u < kUnroll; ++u) {
+                if (t0 + u * kGroups >= a.rows) break;
+                const long long src = in0 + t0 + u * kGroups;
+                if constexpr (QUANT) {
+                    w[u] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(is_v ? a.v : a.k) + src * D + ch * 8);
+                    e[u] = exps[src];
+                } else {
+                    x[u].load(static_cast<const T*>(is_v ? a.v : a.k) + src * D + ch * 8);
+                }
             }
-        }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const long long idx = base + u * step;
-            if (idx >= total) continue;
-            const int kind = idx >= half;
-            const long long i = idx - (kind ? half : 0);
-            if constexpr (QUANT) {
-                const float up = __uint_as_float(e[u] << 23);  // 2^(byte - 127), byte 1 .. 247
-                float f[8];
-                e4m3x4_to_float(w[u].x, f[0], f[1], f[2], f[3]);
-                e4m3x4_to_float(w[u].y, f[4], f[5], f[6], f[7]);
+            for (int u = 0; u < kUnroll; ++u) {
+                if (t0 + u * kGroups >= a.rows) break;
+                if constexpr (QUANT) {
+                    const float up = __uint_as_float(e[u] << 23);  // 2^(byte - 127), byte 1 .. 247
+                    float f[8];
+                    e4m3x4_to_float(w[u].x, f[0], f[1], f[2], f[3]);
+                    e4m3x4_to_float(w[u].y, f[4], f[5], f[6], f[7]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] *= up;
-                x[u].set(f);
+                    for (int j = 0; j < 8; ++j) f[j] *= up;
+                    x[u].set(f);
+                }
+                x[u].store(out + (long long)(t0 + u * kGroups) * D);
             }
-            x[u].store(static_cast<T*>(a.out[kind]) + i * D + ch * 8);
         }
     }
 }
 
-// Blocks for `rows` rows of d elements: enough for all, at most eight resident on every SM.
-unsigned cache_grid(long long rows, int d)
+// Blocks for `rows` rows of every head: enough for all of them, at most eight per SM over k and v and the heads.
+dim3 cache_grid(long long heads, long long rows, int d)
 {
     const long long per = (long long)(kThreads / (d / 8)) * kUnroll;
-    const long long want = (rows + per - 1) / per, cap = (long long)device_sm_count() * 8;
-    return (unsigned)(want < cap ? (want < 1 ? 1 : want) : cap);
+    const long long y = heads < 65535 ? heads : 65535;
+    long long most = (long long)device_sm_count() * 8 / (2 * y);
+    if (most < 1) most = 1;
+    const long long x = (rows + per - 1) / per;
+    return dim3((unsigned)(x < most ? x : most), (unsigned)y, 2);
 }
 
 template <typename T, int D>
-void write_as(const WriteArgs& a, bool quant, unsigned grid, cudaStream_t s)
+void write_as(const WriteArgs& a, bool quant, dim3 grid, cudaStream_t s)
 {
     if (quant)
         cache_write_kernel<T, D, true><<<grid, kThreads, 0, s>>>(a);
@@ -233,7 +214,7 @@ void write_as(const WriteArgs& a, bool quant, unsigned grid, cudaStream_t s)
 }
 
 template <typename T, int D>
-void read_as(const ReadArgs& a, bool quant, unsigned grid, cudaStream_t s)
+void read_as(const ReadArgs& a, bool quant, dim3 grid, cudaStream_t s)
 {
     if (quant)
         cache_read_kernel<T, D, true><<<grid, kThreads, 0, s>>>(a);
@@ -251,21 +232,21 @@ cudaError_t launch_cache_write(const Cache& c, int T, const void* k, const long 
     a.Hkv = c.Hkv;
     a.T = T;
     a.cap = c.cap;
-    a.x[0] = k;
-    a.x[1] = v;
+    a.k = k;
+    a.v = v;
     for (int i = 0; i < 3; ++i) {
-        a.s[0][i] = ks[i];
-        a.s[1][i] = vs[i];
+        a.ks[i] = ks[i];
+        a.vs[i] = vs[i];
     }
-    a.values[0] = c.k;
-    a.values[1] = c.v;
-    a.exps[0] = c.k_exp;
-    a.exps[1] = c.v_exp;
+    a.k_out = c.k;
+    a.v_out = c.v;
+    a.k_exp = c.k_exp;
+    a.v_exp = c.v_exp;
     a.lens = lens;
     a.ntok = ntok;
     a.status = status;
     const bool quant = c.dtype != dtype;
-    const unsigned grid = cache_grid(2LL * c.B * c.Hkv * T, c.d);
+    const dim3 grid = cache_grid((long long)c.B * c.Hkv, T, c.d);
     if (dtype == 1)
         c.d == 128 ? write_as<__nv_bfloat16, 128>(a, quant, grid, s) : write_as<__nv_bfloat16, 64>(a, quant, grid, s);
     else
@@ -276,19 +257,18 @@ cudaError_t launch_cache_write(const Cache& c, int T, const void* k, const long 
 cudaError_t launch_cache_read(const Cache& c, int row0, int rows, void* k, void* v, int dtype, cudaStream_t s)
 {
     ReadArgs a;
-    a.B = c.B;
-    a.Hkv = c.Hkv;
+    a.heads = c.B * c.Hkv;
     a.cap = c.cap;
     a.row0 = row0;
     a.rows = rows;
-    a.values[0] = c.k;
-    a.values[1] = c.v;
-    a.exps[0] = c.k_exp;
-    a.exps[1] = c.v_exp;
-    a.out[0] = k;
-    a.out[1] = v;
+    a.k = c.k;
+    a.v = c.v;
+    a.k_exp = c.k_exp;
+    a.v_exp = c.v_exp;
+    a.k_out = k;
+    a.v_out = v;
     const bool quant = c.dtype != dtype;
-    const unsigned grid = cache_grid(2LL * c.B * c.Hkv * rows, c.d);
+    const dim3 grid = cache_grid((long long)c.B * c.Hkv, rows, c.d);
     if (dtype == 1)
         c.d == 128 ? read_as<__nv_bfloat16, 128>(a, quant, grid, s) : read_as<__nv_bfloat16, 64>(a, quant, grid, s);
     else
