@@ -22,7 +22,8 @@ namespace ra {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 4;      // rows per group and turn, written
+constexpr int kUnrollRead = 8;  // and read back: 8 bytes a lane and row come in
 
 template <typename T>
 struct Eight {  // eight consecutive elements of T
@@ -160,12 +161,12 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a)
         const long long in0 = (long long)bh * a.cap + a.row0, out0 = (long long)bh * a.rows;
         const uint8_t* exps = is_v ? a.v_exp : a.k_exp;
         T* out = static_cast<T*>(is_v ? a.v_out : a.k_out) + out0 * D + ch * 8;
-        for (int t0 = blockIdx.x * (kGroups * kUnroll) + grp; t0 < a.rows; t0 += gridDim.x * (kGroups * kUnroll)) {
-            Eight<T> x[kUnroll];
-            uint2 w[kUnroll];
-            uint32_t e[kUnroll];
+        for (int t0 = blockIdx.x * (kGroups * kUnrollRead) + grp; t0 < a.rows; t0 += gridDim.x * (kGroups * kUnrollRead)) {
+            Eight<T> x[kUnrollRead];
+            uint2 w[kUnrollRead];
+            uint32_t e[kUnrollRead];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
+            for (int u = 0; u < kUnrollRead; ++u) {
                 if (t0 + u * kGroups >= a.rows) break;
                 const long long src = in0 + t0 + u * kGroups;
                 if constexpr (QUANT) {
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a)
                 }
             }
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
+            for (int u = 0; u < kUnrollRead; ++u) {
                 if (t0 + u * kGroups >= a.rows) break;
                 if constexpr (QUANT) {
                     const float up = __uint_as_float(e[u] << 23);  // 2^(byte - 127), byte 1 .. 247
@@ -194,9 +195,9 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a)
 }
 
 // Blocks for `rows` rows of every head: enough for all of them, at most eight per SM over k and v and the heads.
-dim3 cache_grid(long long heads, long long rows, int d)
+dim3 cache_grid(long long heads, long long rows, int d, int unroll)
 {
-    const long long per = (long long)(kThreads / (d / 8)) * kUnroll;
+    const long long per = (long long)(kThreads / (d / 8)) * unroll;
     const long long y = heads < 65535 ? heads : 65535;
     long long most = (long long)device_sm_count() * 8 / (2 * y);
     if (most < 1) most = 1;
@@ -246,7 +247,7 @@ cudaError_t launch_cache_write(const Cache& c, int T, const void* k, const long 
     a.ntok = ntok;
     a.status = status;
     const bool quant = c.dtype != dtype;
-    const dim3 grid = cache_grid((long long)c.B * c.Hkv, T, c.d);
+    const dim3 grid = cache_grid((long long)c.B * c.Hkv, T, c.d, kUnroll);
     if (dtype == 1)
         c.d == 128 ? write_as<__nv_bfloat16, 128>(a, quant, grid, s) : write_as<__nv_bfloat16, 64>(a, quant, grid, s);
     else
@@ -268,7 +269,7 @@ cudaError_t launch_cache_read(const Cache& c, int row0, int rows, void* k, void*
     a.k_out = k;
     a.v_out = v;
     const bool quant = c.dtype != dtype;
-    const dim3 grid = cache_grid((long long)c.B * c.Hkv, rows, c.d);
+    const dim3 grid = cache_grid((long long)c.B * c.Hkv, rows, c.d, kUnrollRead);
     if (dtype == 1)
         c.d == 128 ? read_as<__nv_bfloat16, 128>(a, quant, grid, s) : read_as<__nv_bfloat16, 64>(a, quant, grid, s);
     else
