@@ -763,6 +763,14 @@ def _fits(t, name, device, shape, dtype):
     return t.data_ptr()
 
 
+def _output(t, name, device, shape, dtype):
+    """The caller's output, checked, or a new one; and its address."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _fits(t, name, device, shape, dtype)
+
+
 def _rows(t, name, device, shape, dtype):
     """A tensor read by strides: any [B, heads, rows, d] whose rows are contiguous and lie on 16-byte boundaries.
     Returns its address and its (batch, head, row) element strides, None if it is contiguous."""
@@ -833,12 +841,9 @@ def qk_norm_rope(q, k, wq, wk, n_shards=1, layout="contiguous", base=10000.0, ep
     in q's dtype; q_out may be q and k_out may be k, where those are contiguous."""
     head, tail = _norm_rope_args(q, k, wq, wk, n_shards, layout, base, eps, shard, positions)
     dev, dt = q.device, q.dtype
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=dev)
-    if k_out is None:
-        k_out = torch.empty(k.shape, dtype=dt, device=dev)
-    _run(dev.index, library().ring_attn_qk_norm_rope, *head, _fits(q_out, "q_out", dev, q.shape, dt),
-         _fits(k_out, "k_out", dev, k.shape, dt), *tail, _stream_ptr(stream, dev.index))
+    q_out, qo = _output(q_out, "q_out", dev, q.shape, dt)
+    k_out, ko = _output(k_out, "k_out", dev, k.shape, dt)
+    _run(dev.index, library().ring_attn_qk_norm_rope, *head, qo, ko, *tail, _stream_ptr(stream, dev.index))
     return q_out, k_out
 
 
@@ -849,10 +854,8 @@ def qk_norm_rope_bwd(q, k, wq, wk, dq_out, dk_out, n_shards=1, layout="contiguou
     head, tail = _norm_rope_args(q, k, wq, wk, n_shards, layout, base, eps, shard, positions)
     dev, dt, d = q.device, q.dtype, q.shape[3]
     gq, gk = _fits(dq_out, "dq_out", dev, q.shape, dt), _fits(dk_out, "dk_out", dev, k.shape, dt)
-    if dq is None:
-        dq = torch.empty(q.shape, dtype=dt, device=dev)
-    if dk is None:
-        dk = torch.empty(k.shape, dtype=dt, device=dev)
+    dq, dqp = _output(dq, "dq", dev, q.shape, dt)
+    dk, dkp = _output(dk, "dk", dev, k.shape, dt)
     dwq, dwk = torch.empty(d, dtype=torch.float32, device=dev), torch.empty(d, dtype=torch.float32, device=dev)
     lib = library()
     need = lib.ring_attn_qk_norm_rope_bwd_workspace_size(d)
@@ -860,9 +863,8 @@ def qk_norm_rope_bwd(q, k, wq, wk, dq_out, dk_out, n_shards=1, layout="contiguou
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         _need_workspace(workspace, need, dev)
-    _run(dev.index, lib.ring_attn_qk_norm_rope_bwd, *head, gq, gk, _fits(dq, "dq", dev, q.shape, dt),
-         _fits(dk, "dk", dev, k.shape, dt), dwq.data_ptr(), dwk.data_ptr(), workspace.data_ptr(), workspace.numel(), *tail,
-         _stream_ptr(stream, dev.index))
+    _run(dev.index, lib.ring_attn_qk_norm_rope_bwd, *head, gq, gk, dqp, dkp, dwq.data_ptr(), dwk.data_ptr(),
+         workspace.data_ptr(), workspace.numel(), *tail, _stream_ptr(stream, dev.index))
     return dq, dk, dwq, dwk
 
 
@@ -939,12 +941,10 @@ def cache_read(cache, rows, row0=0, dtype=torch.bfloat16, k=None, v=None, stream
     if rows < 0 or row0 < 0 or row0 + rows > cap:
         raise ValueError(f"rows [{row0}, {row0 + rows}) lie outside the cache ({cap} rows)")
     shape = (B, Hkv, rows, d)
-    if k is None:
-        k = torch.empty(shape, dtype=dtype, device=dev)
-    if v is None:
-        v = torch.empty(shape, dtype=dtype, device=dev)
-    _run(dev.index, library().ring_attn_cache_read, *ptrs, _fits(k, "k", dev, shape, dtype), _fits(v, "v", dev, shape, dtype), B,
-         Hkv, row0, rows, d, cap, code, kind, _stream_ptr(stream, dev.index))
+    k, kp = _output(k, "k", dev, shape, dtype)
+    v, vp = _output(v, "v", dev, shape, dtype)
+    _run(dev.index, library().ring_attn_cache_read, *ptrs, kp, vp, B, Hkv, row0, rows, d, cap, code, kind,
+         _stream_ptr(stream, dev.index))
     return k, v
 
 
@@ -972,10 +972,8 @@ def tree_fwd(q, cache, lens, mask=None, ntok=None, out_dtype=None, out=None, lse
     if mask is not None:
         batched = int(isinstance(mask, torch.Tensor) and mask.dim() == 3)
         mp = _fits(mask, "mask", dev, (B, T, T) if batched else (T, T), torch.bool)
-    if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=dev)
-    if lse is None:
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=dev)
+    out, op = _output(out, "out", dev, q.shape, out_dtype)
+    lse, lp = _output(lse, "lse", dev, (B, H, T), torch.float32)
     lib = library()
     need = lib.ring_attn_tree_fwd_workspace_size(B, H, Hkv, T, d, cap, code, kind)
     if workspace is None:
@@ -983,7 +981,6 @@ def tree_fwd(q, cache, lens, mask=None, ntok=None, out_dtype=None, out=None, lse
     else:
         _need_workspace(workspace, need, dev)
     _run(dev.index, lib.ring_attn_tree_fwd, qp, *ptrs, _fits(lens, "lens", dev, (B,), torch.int32),
-         None if ntok is None else _fits(ntok, "ntok", dev, (B,), torch.int32), mp, batched,
-         _fits(out, "out", dev, q.shape, out_dtype), _fits(lse, "lse", dev, (B, H, T), torch.float32), workspace.data_ptr(),
-         workspace.numel(), B, H, Hkv, T, d, cap, code, kind, _DTYPES[out_dtype], _stream_ptr(stream, dev.index))
+         None if ntok is None else _fits(ntok, "ntok", dev, (B,), torch.int32), mp, batched, op, lp,
+         workspace.data_ptr(), workspace.numel(), B, H, Hkv, T, d, cap, code, kind, _DTYPES[out_dtype], _stream_ptr(stream, dev.index))
     return out, lse

@@ -21,7 +21,8 @@
 // kv head's tile of query rows) that it holds whole; of one that it shares it writes the partial
 // (m, l, unnormalised output) to the workspace, in slot 0 if the item is the first it works on and
 // slot 1 otherwise, and a second launch joins the partials in CTA order: the result does not vary
-// from run to run.  That launch also writes the rows that see nothing.
+// from run to run.  That launch takes the items that go over a border between CTAs from a list that
+// the first one leaves, whatever the batch, and also writes the rows of sequences that have no tokens.
 #pragma once
 
 #include <math.h>
@@ -47,6 +48,8 @@ struct TreeArgs {
     float* lse;
     float* part_ml;  // [ctas][2][rt][4]: m (log2 units), l, the output's normaliser (l as the weights were rounded), 0
     float* part_o;   // [ctas][2][d][rt]: a warp that holds consecutive rows writes whole lines
+    int4* border;    // [ctas]: the item that starts in this CTA and goes on in the next: sequence (-1: none),
+                     // head * nrt + row tile, its last CTA, its slot here
     unsigned int* status;
     float scale_log2;  // log2(e) / sqrt(d)
 };
@@ -70,27 +73,6 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b)
 
 __device__ __forceinline__ int tree_tiles(const TreeSeq& s) { return (s.end + kTreeTile - 1) / kTreeTile; }
 
-// One warp: the tiles of all sequences, and of those before sequence b.
-__device__ __forceinline__ void tree_totals(const TreeArgs& a, int b, long long& total, long long& before)
-{
-    total = before = 0;
-    const int lane = threadIdx.x & 31;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int mine = b0 + lane < a.B ? tree_tiles(tree_seq(a, b0 + lane)) : 0;
-        int all = mine, pre = b0 + lane < b ? mine : 0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            all += __shfl_xor_sync(0xffffffffu, all, o);
-            pre += __shfl_xor_sync(0xffffffffu, pre, o);
-        }
-        total += all;
-        before += pre;
-    }
-    const long long items = (long long)a.Hkv * a.nrt;
-    total *= items;
-    before *= items;
-}
-
 // First tile of CTA c, and the CTA that holds tile x.  With fewer tiles than CTAs the first `total` CTAs take
 // one each, so that every CTA between an item's first and last has written a partial of it.
 __device__ __forceinline__ long long tree_first(const TreeArgs& a, long long total, int c)
@@ -107,37 +89,57 @@ __device__ __forceinline__ int tree_owner(const TreeArgs& a, long long total, lo
 // A CTA's walk over its items: (b, kv head g, row tile r) and the tiles [t0, t1) of it.
 struct TreeWalk {
     long long left;  // tiles still to do, the current item's included
+    long long total; // of all CTAs
     int b, g, r, t0, t1, nt;
     bool first;
     TreeSeq s;
 
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
+    // Starts here and goes on in the next CTA.
+    __device__ __forceinline__ bool goes_on() const { return t0 == 0 && t1 < nt; }
+    // What one thread writes for the second launch about the item.  The tiles that are left lie in the CTAs behind.
+    __device__ __forceinline__ int4 border(const TreeArgs& a, int cta) const
+    {
+        const long long end = tree_first(a, total, cta + 1) + (nt - t1);
+        return make_int4(b, g * a.nrt + r, tree_owner(a, total, end - 1), first ? 0 : 1);
+    }
 
     __device__ __forceinline__ void take()
     {
         const long long n = nt - t0;
         t1 = n < left ? nt : t0 + (int)left;
     }
-    // One warp calls it; the walk starts at tile `at` of `total`, `count` tiles long.
+    // One warp calls these.  The walk of CTA `cta`; false if it has no tiles.
     __device__ __forceinline__ bool begin(const TreeArgs& a, int cta)
     {
-        // up to 32 sequences, the usual batch: their lengths are read once
-        const int lane = threadIdx.x & 31;
-        const int mine32 = lane < a.B ? tree_tiles(tree_seq(a, lane)) : 0;
-        long long total, before;
-        if (a.B <= 32) {
-            int all = mine32;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-            total = (long long)all * a.Hkv * a.nrt;
-        } else {
-            tree_totals(a, 0, total, before);
-        }
-        long long at = tree_first(a, total, cta);
+        const int mine = lengths(a);
+        const long long at = tree_first(a, total, cta);
         left = tree_first(a, total, cta + 1) - at;
         first = true;
         if (left <= 0) return false;
-        // the sequence that holds tile `at`: a warp looks at 32 sequences at a time
+        locate(a, at, mine);
+        take();
+        return true;
+    }
+    // All tiles, and this lane's sequence's among the first 32 (the usual batch has no more: its lengths are read once).
+    __device__ __forceinline__ int lengths(const TreeArgs& a)
+    {
+        const int lane = threadIdx.x & 31;
+        const int mine = lane < a.B ? tree_tiles(tree_seq(a, lane)) : 0;
+        long long all = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            int n = b0 == 0 ? mine : b0 + lane < a.B ? tree_tiles(tree_seq(a, b0 + lane)) : 0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+            all += n;
+        }
+        total = all * a.Hkv * a.nrt;
+        return mine;
+    }
+    // The item that holds tile `at` of the list, and where in it.
+    __device__ __forceinline__ void locate(const TreeArgs& a, long long at, int mine32)
+    {
+        const int lane = threadIdx.x & 31;
         const long long items = (long long)a.Hkv * a.nrt;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
             const long long mine = (b0 == 0 ? mine32 : b0 + lane < a.B ? tree_tiles(tree_seq(a, b0 + lane)) : 0) * items;
@@ -162,8 +164,6 @@ struct TreeWalk {
         t0 = (int)(at % nt);
         g = item / a.nrt;
         r = item % a.nrt;
-        take();
-        return true;
     }
     __device__ __forceinline__ bool next(const TreeArgs& a)
     {
@@ -192,6 +192,9 @@ __device__ __forceinline__ bool tree_sees(const TreeArgs& a, int b, int t, int j
     if (!a.mask) return j <= t;
     return a.mask[((a.mask_batched ? (long long)b * a.T : 0) + t) * a.T + j] != 0;
 }
+
+// Query rows of an item: a row tile's, or all of a kv head's where they are fewer.
+__host__ __device__ inline int tree_item_rows(const TreeArgs& a) { return a.R < a.rt ? a.R : a.rt; }
 
 __host__ __device__ inline size_t tree_align(size_t x) { return (x + 255) & ~size_t(255); }
 

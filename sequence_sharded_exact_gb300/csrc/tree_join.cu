@@ -1,10 +1,10 @@
 // tree_join.cu -- second launch of the attention over a cache (tree.cuh): joins the partials of the
-// items that several CTAs share, and writes zeros and -infinity to the rows that see nothing.
+// items that several CTAs share, and writes zeros and -infinity to the rows of sequences without tokens.
 //
 // For the partials (m_c, l_c, den_c, o_c) of a row, c in CTA order, M = max m_c and w_c = 2^(m_c - M):
 //   out = sum w_c o_c / sum w_c den_c,  lse = (M + log2 sum w_c l_c) ln 2.
 // What bounds it is latency: a row has up to kTreeMaxCtas partials of d floats, all still in L2, and few rows
-// leave few blocks.  A block has 32 rows (a lane each: the partials are stored column by column) and 16
+// leave few blocks.  A block takes 32 rows (a lane each: the partials are stored column by column) and 16
 // columns; its eight warps take every eighth partial, three of them, 48 loads, at a time, keep a running
 // maximum of their own, and meet in shared memory in a fixed order.
 // (One warp per row, walking its partials one by one: decoding over 19 partials took 15 us of 100.)
@@ -19,38 +19,20 @@ namespace {
 
 constexpr int kWarps = 8, kCols = 16;
 
+// 32 rows from i0 and 16 columns from col0 of one item.
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const TreeArgs a)
+__device__ __forceinline__ void join_unit(const TreeArgs& a, int c0, const int4& item, int i0, int col0, float (&so)[kWarps][kCols][33],
+                                          float (&sm)[kWarps][3][32])
 {
-    __shared__ float so[kWarps][kCols][33];
-    __shared__ float sm[kWarps][3][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int chunks = (a.rt + 31) / 32;
-    const long long it = blockIdx.x / chunks;  // sequence, kv head, row tile
-    const int i0 = (int)(blockIdx.x % chunks) * 32, i = i0 + lane;
-    const int r = (int)(it % a.nrt), g = (int)(it / a.nrt % a.Hkv), b = (int)(it / a.nrt / a.Hkv);
-    const int col0 = blockIdx.y * kCols;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = i0 + lane;
+    const int b = item.x, g = item.y / a.nrt, r = item.y % a.nrt, c1 = item.z, head = item.w;
     const TreeSeq s = tree_seq(a, b);
-    const int nt = tree_tiles(s);
-    int c0 = 0, c1 = 0, head = 0;
-    if (nt) {
-        long long total, before;
-        tree_totals(a, b, total, before);
-        const long long first = before + ((long long)g * a.nrt + r) * nt;
-        c0 = tree_owner(a, total, first);
-        c1 = tree_owner(a, total, first + nt - 1);
-        head = tree_first(a, total, c0) < first ? 1 : 0;  // c0 comes to this item after another one
-    }
-    const bool shared = c0 < c1;  // else written whole by one CTA
-    auto lives = [&](int k) { return k < a.rt && r * a.rt + k < a.R && nt && (r * a.rt + k) % a.T < s.cnt; };
+    auto lives = [&](int k) { return k < a.rt && r * a.rt + k < a.R && (r * a.rt + k) % a.T < s.cnt; };
     const bool live = lives(i);
-    // the partials are the first launch's; everything above needed the lengths alone
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (s.bad && blockIdx.y == 0 && i0 == 0 && r == 0 && g == 0 && threadIdx.x == 0) atomicOr(a.status, kStatusRange);
     float m = -INFINITY, l = 0.f, den = 0.f, o[kCols];
 #pragma unroll
     for (int e = 0; e < kCols; ++e) o[e] = 0.f;
-    if (shared && live) {
+    if (live) {
         constexpr int U = 3;
 #pragma unroll 1
         for (int c = c0 + warp; c <= c1; c += kWarps * U) {
@@ -79,19 +61,16 @@ __global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const TreeArgs a
             }
         }
     }
-    if (shared) {  // the same for the whole block
-        sm[warp][0][lane] = m;
-        sm[warp][1][lane] = l;
-        sm[warp][2][lane] = den;
+    sm[warp][0][lane] = m;
+    sm[warp][1][lane] = l;
+    sm[warp][2][lane] = den;
 #pragma unroll
-        for (int e = 0; e < kCols; ++e) so[warp][e][lane] = o[e];
-    }
+    for (int e = 0; e < kCols; ++e) so[warp][e][lane] = o[e];
     __syncthreads();
     // 32 rows of 8 column pairs
     const int k = threadIdx.x >> 3, pair = threadIdx.x & 7;
     if (i0 + k >= a.rt || r * a.rt + i0 + k >= a.R) return;
     const bool dead = !lives(i0 + k);
-    if (!dead && !shared) return;
     float2 t = make_float2(0.f, 0.f);
     m = -INFINITY;
     l = den = 0.f;
@@ -112,12 +91,61 @@ __global__ void __launch_bounds__(kWarps * 32) tree_join_kernel(const TreeArgs a
     const float inv = 1.0f / den;
     t = none ? make_float2(0.f, 0.f) : make_float2(t.x * inv, t.y * inv);
     const long long x = ((long long)b * a.Hkv + g) * a.R + (long long)r * a.rt + i0 + k;
-    const long long at = (x * D + col0) / 2 + pair;
+    const long long dst = (x * D + col0) / 2 + pair;
     if (a.bf16_out)
-        static_cast<uint32_t*>(a.out)[at] = pack_bf16x2(t.x, t.y);
+        static_cast<uint32_t*>(a.out)[dst] = pack_bf16x2(t.x, t.y);
     else
-        static_cast<float2*>(a.out)[at] = t;
-    if (pair == 0 && blockIdx.y == 0) a.lse[x] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+        static_cast<float2*>(a.out)[dst] = t;
+    if (pair == 0 && col0 == 0) a.lse[x] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32, 2) tree_join_kernel(const TreeArgs a)
+{
+    __shared__ float so[kWarps][kCols][33];
+    __shared__ float sm[kWarps][3][32];
+    __shared__ short list[kTreeMaxCtas];
+    __shared__ int count[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int chunks = (tree_item_rows(a) + 31) / 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for the first launch's results
+    // sequences without tokens, and lengths outside their ranges: a turn for every block
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const TreeSeq s = tree_seq(a, b);
+        if (s.bad && threadIdx.x == 0) atomicOr(a.status, kStatusRange);
+        if (s.end) continue;
+        const long long rows = (long long)a.Hkv * a.R, row0 = b * rows;
+        for (long long e = threadIdx.x; e < rows * D / 2; e += blockDim.x) {
+            if (a.bf16_out)
+                static_cast<uint32_t*>(a.out)[row0 * D / 2 + e] = 0u;
+            else
+                static_cast<float2*>(a.out)[row0 * D / 2 + e] = make_float2(0.f, 0.f);
+        }
+        for (long long e = threadIdx.x; e < rows; e += blockDim.x) a.lse[row0 + e] = -INFINITY;
+    }
+    // the borders that an item goes over, in order
+    int n = 0;
+    for (int c = 0; c < a.ctas; c += kWarps * 32) {
+        const int mine = c + (int)threadIdx.x;
+        const bool has = mine < a.ctas && a.border[mine].x >= 0;
+        const unsigned votes = __ballot_sync(0xffffffffu, has);
+        if (lane == 0) count[warp] = __popc(votes);
+        __syncthreads();
+        int before = n;
+        for (int k = 0; k < kWarps; ++k) {
+            if (k < warp) before += count[k];
+            n += count[k];
+        }
+        if (has) list[before + __popc(votes & ((1u << lane) - 1u))] = (short)mine;
+        __syncthreads();
+    }
+    const int units = n * chunks * (D / kCols);
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        const int c0 = list[u / (chunks * (D / kCols))];
+        const int4 item = a.border[c0];
+        join_unit<D>(a, c0, item, u / (D / kCols) % chunks * 32, u % (D / kCols) * kCols, so, sm);
+        __syncthreads();
+    }
 }
 
 }  // namespace
@@ -142,12 +170,13 @@ static Cut cut_of(const Cache& c, int H, int T, int dtype)
     return u;
 }
 
+static size_t border_bytes(const Cut& u) { return tree_align((size_t)u.ctas * sizeof(int4)); }
 static size_t ml_bytes(const Cut& u) { return tree_align((size_t)u.ctas * 2 * u.rt * 4 * sizeof(float)); }
 
 size_t tree_workspace_size(const Cache& c, int H, int T, int dtype)
 {
     const Cut u = cut_of(c, H, T, dtype);
-    return ml_bytes(u) + tree_align((size_t)u.ctas * 2 * u.rt * c.d * sizeof(float));
+    return border_bytes(u) + ml_bytes(u) + tree_align((size_t)u.ctas * 2 * u.rt * c.d * sizeof(float));
 }
 
 cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
@@ -179,8 +208,10 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
     a.lse = t.lse;
     a.status = t.status;
     a.scale_log2 = kLog2e / sqrtf((float)c.d);
-    a.part_ml = static_cast<float*>(t.workspace);
-    a.part_o = reinterpret_cast<float*>(static_cast<char*>(t.workspace) + ml_bytes(u));
+    char* ws = static_cast<char*>(t.workspace);
+    a.border = reinterpret_cast<int4*>(ws);
+    a.part_ml = reinterpret_cast<float*>(ws + border_bytes(u));
+    a.part_o = reinterpret_cast<float*>(ws + border_bytes(u) + ml_bytes(u));
     cudaError_t e;
     if (u.tc)
         e = c.d == 128 ? launch_tree_tc_d128(a, c.dtype == kCacheE4m3, s) : launch_tree_tc_d64(a, c.dtype == kCacheE4m3, s);
@@ -191,9 +222,10 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
 
 cudaError_t launch_tree_join(const TreeArgs& a, int d, cudaStream_t s)
 {
-    const long long items = (long long)a.B * a.Hkv * a.nrt;
+    const long long most = (long long)(a.ctas > 1 ? a.ctas - 1 : 1) * ((tree_item_rows(a) + 31) / 32) * (d / kCols);
+    const long long resident = (long long)device_sm_count() * 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items * ((a.rt + 31) / 32)), (unsigned)(d / kCols));
+    cfg.gridDim = dim3((unsigned)(most < resident ? most : resident));
     cfg.blockDim = dim3(kWarps * 32);
     cfg.stream = s;
     // starts while the first launch runs; it waits for that one's results in the kernel

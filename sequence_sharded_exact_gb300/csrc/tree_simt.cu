@@ -52,8 +52,13 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int col = tid % D, part = tid / D;
     TreeWalk w;
-    if (!w.begin(a, blockIdx.x)) return;
+    int4 border = make_int4(-1, 0, 0, 0);
+    if (!w.begin(a, blockIdx.x)) {
+        if (tid == 0) a.border[blockIdx.x] = border;
+        return;
+    }
     do {
+        if (w.goes_on()) border = w.border(a, blockIdx.x);
         const long long head = (long long)w.b * a.Hkv + w.g;
         const float* q = static_cast<const float*>(a.q) + (head * a.R + (long long)w.r * a.rt) * D;
         const int rows = a.R - w.r * a.rt < a.rt ? a.R - w.r * a.rt : a.rt;
@@ -171,10 +176,10 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a)
 #pragma unroll
         for (int i = 0; i < RC; ++i) {
             const int x = part * RC + i;
-            if (x >= rows || (w.r * a.rt + x) % a.T >= w.s.cnt) continue;
+            if (x >= rows) continue;
             const float mm = ml[x][0], ll = ml[x][1];
             if (whole) {
-                const bool none = mm == -INFINITY && ll == 0.f;
+                const bool none = (mm == -INFINITY && ll == 0.f) || (w.r * a.rt + x) % a.T >= w.s.cnt;
                 const float o = none ? 0.f : acc[i] / ll;
                 const long long dst = head * a.R + w.r * a.rt + x;
                 static_cast<float*>(a.out)[dst * D + col] = o;
@@ -185,6 +190,7 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a)
             }
         }
     } while (w.next(a));
+    if (tid == 0) a.border[blockIdx.x] = border;
 }
 
 template <typename TC, int D>

@@ -202,6 +202,7 @@ __device__ __forceinline__ void load_qk_role(const TreeArgs& a, uint32_t sbase, 
     uint32_t kc = 0, item = 0;
     bool ok = true;
     do {
+        if (w.goes_on()) a.border[blockIdx.x] = w.border(a, blockIdx.x);
         const int z = w.b * a.Hkv + w.g;
         if constexpr (!kE4) {
             if (item > 0 && !wait(bar(C::bQEmpty), (item - 1) & 1, ctl)) break;
@@ -778,8 +779,9 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
             if (!warp_wait(bar(C::bO + wg), item & 1, ctl)) return;
         }
         tc_fence_after_sync();
-        if (any_live) {
-            const bool whole = w.whole(), none = m == -INFINITY && l == 0.f;
+        const bool row = x < a.R;  // a query row of the kv head, if not of a token that the sequence has
+        if (__any_sync(0xffffffffu, row)) {
+            const bool whole = w.whole(), none = !live || (m == -INFINITY && l == 0.f);
             const bool poison = *reinterpret_cast<volatile int*>(smem + C::kPoison + (item & 7) * 4) == (int)item + 1;
             const float inv = whole ? (none ? 0.f : 1.0f / den) : 1.0f;
             const long long grow = ((long long)w.b * a.Hkv + w.g) * a.R + x;
@@ -822,7 +824,7 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
                         }
                     }
                 }
-                if (!live) continue;
+                if (!row) continue;
                 if (whole && a.bf16_out) {
                     uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + grow * kHd + c);
 #pragma unroll
@@ -847,7 +849,7 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
                     for (int e = 0; e < 32; ++e) dst[(long long)e * a.rt] = __uint_as_float(o[e]);
                 }
             }
-            if (live && (kNq == 2 || wg == 0)) {
+            if (row && (kNq == 2 || wg == 0)) {
                 if (whole)
                     a.lse[grow] = none ? -INFINITY : (m + log2f(l)) * kLn2;
                 else
@@ -909,6 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         if (warp < 8) {
             softmax_role<kE4, kNq>(a, sbase, smem, tmem, w, ctl);
         } else if (warp == 8) {
+            if (lane == 0) a.border[blockIdx.x].x = -1;  // (the walk's last item may say otherwise)
             if (lane == 0) load_qk_role<kE4, kNq>(a, sbase, maps, w, ctl);
         } else if (warp == 9) {
             if (lane == 0) mma_role<kE4, kNq>(a, sbase, tmem, w, ctl);
@@ -923,6 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
                 prep_bf16_role<kNq>(a, sbase, smem, w, ctl);
         }
     }
+    if (!work && threadIdx.x == 0) a.border[blockIdx.x] = make_int4(-1, 0, 0, 0);
     tc_fence_before_sync();
     __syncthreads();
     if (warp == 9) {
