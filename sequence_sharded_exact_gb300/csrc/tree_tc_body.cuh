@@ -13,8 +13,8 @@
 //   * More (kNq = 2): 256 query rows as two 128-row tiles that share every K/V tile, a warpgroup each.
 //   * m follows the row maximum only when that grows by more than 2^8: O / l does not depend on the
 //     reference, O in TMEM is then seldom rescaled, and S is read once.
-//   * Warps: 0-3 and 4-7 softmax; 8 loads the queries and K, 10 V (TMA, one thread each); 9 issues the MMAs;
-//     11 fetches the rows' scales (e4m3); 12-15 prepare V.
+//   * Warps: 0-3 and 4-7 softmax; 8 loads the queries and K, 10 V (TMA, one thread each); 9 issues the MMAs; 11
+//     fetches the rows' scales (e4m3); 12-15 prepare V.
 // Rows that must not count: scores of unseen rows are set to -infinity before the maximum, but 0 * NaN in
 // P V would still be NaN, so warps 12-15 clear the rows of V behind the sequence, and non-finite elements
 // of drafted tokens' rows, in shared memory before the product; those elements are added afterwards to
@@ -140,24 +140,59 @@ __host__ __device__ constexpr uint32_t kmajor_hi()
     return kNarrow<kE4> ? (((512u >> 4) & 0x3FFFu) | (1u << 14) | (4u << 29)) : sdesc_sw128_hi(1024);
 }
 
+// The issuing warp runs as a whole, so that descriptors and addresses are the same in every lane and stay in uniform
+// registers; one elected lane (`lead`) issues.
+__device__ __forceinline__ uint32_t elect()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void lead_mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, l;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void lead_mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, l;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void lead_commit(uint32_t lead, uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %1, 0;\n\t"
+        "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead)
+        : "memory");
+}
+
 // kind::f8f6f4 (e4m3 operands, f32 accumulate): formats 0, the other fields as kind::f16's.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N)
 {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void lead_mma_ss_e4m3(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, l;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
         : "memory");
 }
 
 // S_w = X K^T.
 template <bool kE4, int kNq>
-__device__ __forceinline__ void issue_s(uint32_t sbase, uint32_t tmem, int w, int slot)
+__device__ __forceinline__ void issue_s(uint32_t lead, uint32_t sbase, uint32_t tmem, int w, int slot)
 {
     using C = Cfg<kE4, kNq>;
     const uint32_t q = sdesc_sw128_lo(sbase + C::kQ + (kNq == 2 ? (uint32_t)w * C::kBytesQ : 0u), 16);
@@ -169,25 +204,25 @@ __device__ __forceinline__ void issue_s(uint32_t sbase, uint32_t tmem, int w, in
         for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int kk = 0; kk < kHd / 32; ++kk)
-                mma_ss_e4m3(d, sdesc_at(q, (uint32_t)part * 128 * kHd + (uint32_t)kk * 32, hi), sdesc_at(k, (uint32_t)kk * 32, hi),
+                lead_mma_ss_e4m3(lead, d, sdesc_at(q, (uint32_t)part * 128 * kHd + (uint32_t)kk * 32, hi), sdesc_at(k, (uint32_t)kk * 32, hi),
                             idesc_e4m3_f32(128, 128), part + kk > 0 ? 1u : 0u);
     } else {
 #pragma unroll
         for (int kk = 0; kk < kHd / 16; ++kk) {
             const uint32_t off = (uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u;
-            mma_ss(d, sdesc_at(q, off, hi), sdesc_at(k, off, hi), idesc_bf16_f32(128, 128, false, false), kk > 0 ? 1u : 0u);
+            lead_mma_ss(lead, d, sdesc_at(q, off, hi), sdesc_at(k, off, hi), idesc_bf16_f32(128, 128, false, false), kk > 0 ? 1u : 0u);
         }
     }
 }
 
 // O_w (+)= P_w V.
-__device__ __forceinline__ void issue_pv(uint32_t v_addr, uint32_t tmem, int w, bool accumulate)
+__device__ __forceinline__ void issue_pv(uint32_t lead, uint32_t v_addr, uint32_t tmem, int w, bool accumulate)
 {
     const uint32_t v = sdesc_sw128_lo(v_addr, 16384);
     constexpr uint32_t hi = sdesc_sw128_hi(1024);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
-        mma_ts(tmem + kColO + (uint32_t)w * 128, tmem + kColS + (uint32_t)w * 128 + (uint32_t)kk * 8,
+        lead_mma_ts(lead, tmem + kColO + (uint32_t)w * 128, tmem + kColS + (uint32_t)w * 128 + (uint32_t)kk * 8,
                sdesc_at(v, (uint32_t)kk * 2048u, hi), idesc_bf16_f32(128, kHd, false, true), kk > 0 || accumulate ? 1u : 0u);
 }
 
@@ -527,40 +562,42 @@ __device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint
     Ring<C::kSlotsK> rk;
     Ring<C::kSlotsP> rv;
     uint32_t item = 0, pc = 0;  // pc: a parity bit per warpgroup
+    const uint32_t lead = elect();
+    tmem = __shfl_sync(0xffffffffu, tmem, 0);
     bool ok = true;
     do {
-        if (!wait(bar(C::bQFull), item++ & 1, ctl)) break;
+        if (!warp_wait(bar(C::bQFull), item++ & 1, ctl)) break;
         tc_fence_after_sync();
-        const int n = (w.t1 - w.t0) * kNq;
+        const int n = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0) * kNq;
 #pragma unroll 1
         for (int j = 0; j < n + 2; ++j) {
             const int wg = j & 1;
             if (j >= 2) {
-                ok = wait(bar(C::bPFull + rv.slot), rv.par, ctl) && wait(bar(C::bP + wg), pc >> wg & 1, ctl);
+                ok = warp_wait(bar(C::bPFull + rv.slot), rv.par, ctl) && warp_wait(bar(C::bP + wg), pc >> wg & 1, ctl);
                 if (!ok) break;
                 pc ^= 1u << wg;
                 tc_fence_after_sync();
-                issue_pv(sbase + (kE4 ? C::kP + (uint32_t)rv.slot * C::kBytesV : C::kL + (uint32_t)rv.slot * C::kBytesK), tmem, wg, j >= 4);
-                if (j >= n) tc_commit(bar(C::bO + wg));  // the warpgroup's last job of the item
+                issue_pv(lead, sbase + (kE4 ? C::kP + (uint32_t)rv.slot * C::kBytesV : C::kL + (uint32_t)rv.slot * C::kBytesK), tmem, wg, j >= 4);
+                if (j >= n) lead_commit(lead, bar(C::bO + wg));  // the warpgroup's last job of the item
                 if (kNq == 1 || wg == 1) {
-                    tc_commit(bar((kE4 ? C::bPEmpty : C::bLEmpty) + rv.slot));
+                    lead_commit(lead, bar((kE4 ? C::bPEmpty : C::bLEmpty) + rv.slot));
                     rv.next();
                 }
             }
             if (j < n) {
                 if (kNq == 1 || wg == 0) {
-                    ok = wait(bar(C::bKFull + rk.slot), rk.par, ctl);
+                    ok = warp_wait(bar(C::bKFull + rk.slot), rk.par, ctl);
                     if (!ok) break;
                     tc_fence_after_sync();
                 }
-                issue_s<kE4, kNq>(sbase, tmem, wg, rk.slot);
-                tc_commit(bar(C::bS + wg));  // the softmax warps release K
+                issue_s<kE4, kNq>(lead, sbase, tmem, wg, rk.slot);
+                lead_commit(lead, bar(C::bS + wg));  // the softmax warps release K
                 if (kNq == 1 || wg == 1) rk.next();
-                if (j == n - 1) tc_commit(bar(C::bQEmpty));
+                if (j == n - 1) lead_commit(lead, bar(C::bQEmpty));
             }
         }
     } while (ok && w.next(a));
-    tc_commit(bar(C::bDrain));
+    lead_commit(lead, bar(C::bDrain));
     drain_wait(bar(C::bDrain), 0);
 }
 
@@ -914,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
             if (lane == 0) a.border[blockIdx.x].x = -1;  // (the walk's last item may say otherwise)
             if (lane == 0) load_qk_role<kE4, kNq>(a, sbase, maps, w, ctl);
         } else if (warp == 9) {
-            if (lane == 0) mma_role<kE4, kNq>(a, sbase, tmem, w, ctl);
+            mma_role<kE4, kNq>(a, sbase, tmem, w, ctl);
         } else if (warp == 10) {
             if (lane == 0) load_v_role<kE4, kNq>(a, sbase, maps, w, ctl);
         } else if (warp == 11) {
