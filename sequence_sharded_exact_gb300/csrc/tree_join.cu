@@ -5,8 +5,9 @@
 //   out = sum w_c o_c / sum w_c den_c,  lse = (M + log2 sum w_c l_c) ln 2.
 // What bounds it is latency: a row has up to kTreeMaxCtas partials of d floats, all still in L2, and few rows
 // leave few blocks.  A block takes 32 rows (a lane each: the partials are stored column by column) and 16
-// columns; its eight warps take every eighth partial, three of them, 48 loads, at a time, keep a running
-// maximum of their own, and meet in shared memory in a fixed order.
+// columns: a unit, whose partials its eight warps take in turn, three of them, 48 loads, at a time; each keeps a
+// running maximum of its own, and they meet in shared memory in a fixed order.  With more units than blocks the
+// warps of a block work in groups of four, two or one on units of their own.
 // (One warp per row, walking its partials one by one: decoding over 19 partials took 15 us of 100.)
 #include <cuda_bf16.h>
 
@@ -19,14 +20,17 @@ namespace {
 
 constexpr int kWarps = 8, kCols = 16;
 
-// 32 rows from i0 and 16 columns from col0 of one item.
+// 32 rows from i0 and 16 columns from col0 of one item, by `group` warps of which this is number `part`; every warp of
+// the block calls this at the same time, those without a unit with has = false.
 template <int D>
-__device__ __forceinline__ void join_unit(const TreeArgs& a, int c0, const int4& item, int i0, int col0, float (&so)[kWarps][kCols][33],
-                                          float (&sm)[kWarps][3][32])
+__device__ __forceinline__ void join_unit(const TreeArgs& a, bool has, int c0, const int4& item, int i0, int col0, int group, int part,
+                                          float (&so)[kWarps][kCols][33], float (&sm)[kWarps][3][32])
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = i0 + lane;
     const int b = item.x, g = item.y / a.nrt, r = item.y % a.nrt, c1 = item.z, head = item.w;
-    const TreeSeq s = tree_seq(a, b);
+    TreeSeq s;
+    s.cnt = 0;
+    if (has) s = tree_seq(a, b);
     auto lives = [&](int k) { return k < a.rt && r * a.rt + k < a.R && (r * a.rt + k) % a.T < s.cnt; };
     const bool live = lives(i);
     float m = -INFINITY, l = 0.f, den = 0.f, o[kCols];
@@ -35,12 +39,12 @@ __device__ __forceinline__ void join_unit(const TreeArgs& a, int c0, const int4&
     if (live) {
         constexpr int U = 3;
 #pragma unroll 1
-        for (int c = c0 + warp; c <= c1; c += kWarps * U) {
+        for (int c = c0 + part; c <= c1; c += group * U) {
             float4 ml[U];
             float p[U][kCols];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int cc = c + u * kWarps;
+                const int cc = c + u * group;
                 if (cc > c1) break;
                 const long long slot = (long long)cc * 2 + (cc == c0 ? head : 0);
                 ml[u] = *reinterpret_cast<const float4*>(a.part_ml + (slot * a.rt + i) * 4);
@@ -49,7 +53,7 @@ __device__ __forceinline__ void join_unit(const TreeArgs& a, int c0, const int4&
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (c + u * kWarps > c1) break;
+                if (c + u * group > c1) break;
                 const float mn = fmaxf(m, ml[u].x), ref = mn == -INFINITY ? 0.f : mn;
                 const float keep = ex2_approx(m - ref), w = ex2_approx(ml[u].x - ref);
                 m = mn;
@@ -68,35 +72,37 @@ __device__ __forceinline__ void join_unit(const TreeArgs& a, int c0, const int4&
     for (int e = 0; e < kCols; ++e) so[warp][e][lane] = o[e];
     __syncthreads();
     // 32 rows of 8 column pairs
-    const int k = threadIdx.x >> 3, pair = threadIdx.x & 7;
-    if (i0 + k >= a.rt || r * a.rt + i0 + k >= a.R) return;
-    const bool dead = !lives(i0 + k);
-    float2 t = make_float2(0.f, 0.f);
-    m = -INFINITY;
-    l = den = 0.f;
-    if (!dead) {
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm[w][0][k]);
-        const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2_approx(sm[w][0][k] - ref);
-            l = fmaf(sm[w][1][k], f, l);
-            den = fmaf(sm[w][2][k], f, den);
-            t.x = fmaf(so[w][2 * pair][k], f, t.x);
-            t.y = fmaf(so[w][2 * pair + 1][k], f, t.y);
+    const int w0 = warp - part;
+#pragma unroll 1
+    for (int t0 = part * 32 + lane; has && t0 < 256; t0 += group * 32) {
+        const int k = t0 >> 3, pair = t0 & 7;
+        if (i0 + k >= a.rt || r * a.rt + i0 + k >= a.R) break;
+        const bool dead = !lives(i0 + k);
+        float2 t = make_float2(0.f, 0.f);
+        m = -INFINITY;
+        l = den = 0.f;
+        if (!dead) {
+            for (int w = w0; w < w0 + group; ++w) m = fmaxf(m, sm[w][0][k]);
+            const float ref = m == -INFINITY ? 0.f : m;
+            for (int w = w0; w < w0 + group; ++w) {
+                const float f = ex2_approx(sm[w][0][k] - ref);
+                l = fmaf(sm[w][1][k], f, l);
+                den = fmaf(sm[w][2][k], f, den);
+                t.x = fmaf(so[w][2 * pair][k], f, t.x);
+                t.y = fmaf(so[w][2 * pair + 1][k], f, t.y);
+            }
         }
+        const bool none = m == -INFINITY && l == 0.f;
+        const float inv = 1.0f / den;
+        t = none ? make_float2(0.f, 0.f) : make_float2(t.x * inv, t.y * inv);
+        const long long x = ((long long)b * a.Hkv + g) * a.R + (long long)r * a.rt + i0 + k;
+        const long long dst = (x * D + col0) / 2 + pair;
+        if (a.bf16_out)
+            static_cast<uint32_t*>(a.out)[dst] = pack_bf16x2(t.x, t.y);
+        else
+            static_cast<float2*>(a.out)[dst] = t;
+        if (pair == 0 && col0 == 0) a.lse[x] = none ? -INFINITY : (m + log2f(l)) * kLn2;
     }
-    const bool none = m == -INFINITY && l == 0.f;
-    const float inv = 1.0f / den;
-    t = none ? make_float2(0.f, 0.f) : make_float2(t.x * inv, t.y * inv);
-    const long long x = ((long long)b * a.Hkv + g) * a.R + (long long)r * a.rt + i0 + k;
-    const long long dst = (x * D + col0) / 2 + pair;
-    if (a.bf16_out)
-        static_cast<uint32_t*>(a.out)[dst] = pack_bf16x2(t.x, t.y);
-    else
-        static_cast<float2*>(a.out)[dst] = t;
-    if (pair == 0 && col0 == 0) a.lse[x] = none ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <int D>
@@ -140,10 +146,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) tree_join_kernel(const TreeArg
         __syncthreads();
     }
     const int units = n * chunks * (D / kCols);
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-        const int c0 = list[u / (chunks * (D / kCols))];
-        const int4 item = a.border[c0];
-        join_unit<D>(a, c0, item, u / (D / kCols) % chunks * 32, u % (D / kCols) * kCols, so, sm);
+    // few units: all the block's warps share one; many: a warp has its own, and the loads of eight are in flight
+    int group = kWarps;
+    while (group > 1 && units > (int)gridDim.x * (kWarps / group)) group >>= 1;
+    for (int u0 = blockIdx.x; u0 < units; u0 += gridDim.x * (kWarps / group)) {
+        const int u = u0 + warp / group * (int)gridDim.x;
+        const bool has = u < units;
+        const int c0 = has ? list[u / (chunks * (D / kCols))] : 0;
+        const int4 item = has ? a.border[c0] : make_int4(0, 0, 0, 0);
+        join_unit<D>(a, has, c0, item, u / (D / kCols) % chunks * 32, u % (D / kCols) * kCols, group, warp % group, so, sm);
         __syncthreads();
     }
 }

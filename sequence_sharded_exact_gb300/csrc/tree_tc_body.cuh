@@ -616,15 +616,29 @@ __device__ __forceinline__ unsigned long long seen_bits(const TreeArgs& a, const
         return n > 0 ? bits | (n >= 64 ? ~0ull : (1ull << n) - 1) << (p + j0) : bits;
     }
     const uint8_t* m = a.mask + ((a.mask_batched ? (long long)b * a.T : 0) + t) * a.T;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.mask) & 15) == 0 && a.T % 16 == 0;  // rows of whole 16-byte words
 #pragma unroll 1
-    for (int j = j0; j < j1; j += 16) {
-        uint8_t v[16];
+    for (int j = j0 & ~15; j < j1; j += 16) {
+        uint32_t w = 0;  // drafted tokens j .. j + 15, one bit each
+        if (wide) {
+            const uint4 v = *reinterpret_cast<const uint4*>(m + j);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = j + i < j1 ? m[j + i] : (uint8_t)0;
-        uint32_t w = 0;
+            for (int i = 0; i < 4; ++i) {  // a byte's bit 7 says that it is not 0; the product gathers the four
+                const uint32_t y = ((u[i] & 0x7f7f7f7fu) + 0x7f7f7f7fu | u[i]) >> 7 & 0x01010101u;
+                w |= (y * 0x01020408u >> 24 & 15u) << 4 * i;
+            }
+        } else {
+            uint8_t v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w |= v[i] ? 1u << i : 0u;
-        bits |= (unsigned long long)w << (p + j);
+            for (int i = 0; i < 16; ++i) v[i] = j + i < j1 ? m[j + i] : (uint8_t)0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w |= v[i] ? 1u << i : 0u;
+        }
+        if (j < j0) w &= ~0u << (j0 - j);
+        if (j + 16 > j1) w &= (1u << (j1 - j)) - 1;
+        const int to = p + j;  // the first of them among the 64 rows; below 0 only bits that j0 has cleared
+        bits |= to < 0 ? (unsigned long long)(w >> -to) : (unsigned long long)w << to;
     }
     return bits;
 }
