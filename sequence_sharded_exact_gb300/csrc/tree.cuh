@@ -14,7 +14,7 @@
 // the least traffic is the live part of the cache, and the operations are 4 d G T per row and kv head:
 // below about 128 query rows per kv head it is the memory's time, above that the products'.  A long
 // cache and few sequences leave only B * Hkv independent pieces, far fewer than SMs, so the token
-// axis is split: the tiles (128 cached rows of one kv head against one tile of query rows) of all
+// axis is split: the tiles (128 or 32 cached rows of one kv head against one tile of query rows) of all
 // sequences form one list, and CTA c of n takes the tiles [c total / n, (c + 1) total / n) whatever
 // sequences they belong to.  Every SM gets the same work to within one tile for any mix of lengths,
 // and the lengths stay on the device (a captured graph replays with new ones).  A CTA writes an item (one
@@ -31,13 +31,15 @@
 
 namespace ra {
 
-constexpr int kTreeTile = 128;     // cached rows per tile of the work list
+constexpr int kTreeTile = 128;       // cached rows per tile of the work list on the tensor cores
+constexpr int kTreeSimtTile = 32;    // and on the CUDA cores
 constexpr int kTreeMaxCtas = 640;    // most CTAs of the first launch on the CUDA cores (bounds the workspace)
 constexpr int kTreeMaxTcCtas = 160;  // and on the tensor cores (one per SM)
 
 struct TreeArgs {
     int B, H, Hkv, G, T, R;  // R = G * T query rows per kv head, row x: head x / T of the group, token x % T
     int cap, rt, nrt;        // cache rows; query rows per row tile; row tiles per kv head
+    int tile;                // cached rows per tile
     int ctas;                // CTAs of the first launch
     int mask_batched, bf16_out;
     const int *lens, *ntok;
@@ -71,7 +73,10 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b)
     return s;
 }
 
-__device__ __forceinline__ int tree_tiles(const TreeSeq& s) { return (s.end + kTreeTile - 1) / kTreeTile; }
+__device__ __forceinline__ int tree_tiles(const TreeArgs& a, const TreeSeq& s)
+{
+    return a.tile == kTreeTile ? (s.end + kTreeTile - 1) / kTreeTile : (s.end + kTreeSimtTile - 1) / kTreeSimtTile;
+}
 
 // First tile of CTA c, and the CTA that holds tile x.  With fewer tiles than CTAs the first `total` CTAs take
 // one each, so that every CTA between an item's first and last has written a partial of it.
@@ -125,10 +130,10 @@ struct TreeWalk {
     __device__ __forceinline__ int lengths(const TreeArgs& a)
     {
         const int lane = threadIdx.x & 31;
-        const int mine = lane < a.B ? tree_tiles(tree_seq(a, lane)) : 0;
+        const int mine = lane < a.B ? tree_tiles(a, tree_seq(a, lane)) : 0;
         long long all = 0;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
-            int n = b0 == 0 ? mine : b0 + lane < a.B ? tree_tiles(tree_seq(a, b0 + lane)) : 0;
+            int n = b0 == 0 ? mine : b0 + lane < a.B ? tree_tiles(a, tree_seq(a, b0 + lane)) : 0;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
             all += n;
@@ -142,7 +147,7 @@ struct TreeWalk {
         const int lane = threadIdx.x & 31;
         const long long items = (long long)a.Hkv * a.nrt;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
-            const long long mine = (b0 == 0 ? mine32 : b0 + lane < a.B ? tree_tiles(tree_seq(a, b0 + lane)) : 0) * items;
+            const long long mine = (b0 == 0 ? mine32 : b0 + lane < a.B ? tree_tiles(a, tree_seq(a, b0 + lane)) : 0) * items;
             long long upto = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -159,7 +164,7 @@ struct TreeWalk {
             at -= __shfl_sync(0xffffffffu, upto, 31);
         }
         s = tree_seq(a, b);
-        nt = tree_tiles(s);
+        nt = tree_tiles(a, s);
         const int item = (int)(at / nt);
         t0 = (int)(at % nt);
         g = item / a.nrt;
@@ -177,7 +182,7 @@ struct TreeWalk {
                 g = 0;
                 do {
                     s = tree_seq(a, ++b);
-                    nt = tree_tiles(s);
+                    nt = tree_tiles(a, s);
                 } while (nt == 0);  // `left` says that a later sequence has tiles
             }
         }

@@ -3,12 +3,13 @@
 //
 // For the partials (m_c, l_c, den_c, o_c) of a row, c in CTA order, M = max m_c and w_c = 2^(m_c - M):
 //   out = sum w_c o_c / sum w_c den_c,  lse = (M + log2 sum w_c l_c) ln 2.
-// What bounds it is latency: a row has up to kTreeMaxCtas partials of d floats, all still in L2, and few rows
-// leave few blocks.  A block takes 32 rows (a lane each: the partials are stored column by column) and 16
-// columns: a unit, whose partials its eight warps take in turn, three of them, 48 loads, at a time; each keeps a
-// running maximum of its own, and they meet in shared memory in a fixed order.  With more units than blocks the
-// warps of a block work in groups of four, two or one on units of their own.
-// (One warp per row, walking its partials one by one: decoding over 19 partials took 15 us of 100.)
+// What bounds it is latency: a row has up to kTreeMaxCtas partials of d floats, all still in L2.  A unit is 32
+// rows (a lane each: the partials are stored column by column) and 4 or 16 columns.  With few units a block's
+// eight warps share one of 4 columns and take its partials in turn, eight each, 32 loads, at a time; each keeps a
+// running maximum of its own, and they meet in shared memory in a fixed order.  With more units than blocks a
+// unit has 16 columns and three partials are loaded at a time, by as few warps as keep all of them busy: four,
+// two or one.  (One warp per row, walking its partials one by one: decoding over 19 partials took 15 us of 100;
+// eight warps per unit whatever the number: 18.5 us in place of FIGURE for 64 items of 128 rows.)
 #include <cuda_bf16.h>
 
 #include "ra_internal.h"
@@ -18,13 +19,13 @@
 namespace ra {
 namespace {
 
-constexpr int kWarps = 8, kCols = 16;
+constexpr int kWarps = 8, kMaxCols = 16;
 
-// 32 rows from i0 and 16 columns from col0 of one item, by `group` warps of which this is number `part`; every warp of
+// 32 rows from i0 and kCols columns from col0 of one item, U partials at a time, by `group` warps of which this is number `part`; every warp of
 // the block calls this at the same time, those without a unit with has = false.
-template <int D>
+template <int D, int kCols, int U>
 __device__ __forceinline__ void join_unit(const TreeArgs& a, bool has, int c0, const int4& item, int i0, int col0, int group, int part,
-                                          float (&so)[kWarps][kCols][33], float (&sm)[kWarps][3][32])
+                                          float (&so)[kWarps][kMaxCols][33], float (&sm)[kWarps][3][32])
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = i0 + lane;
     const int b = item.x, g = item.y / a.nrt, r = item.y % a.nrt, c1 = item.z, head = item.w;
@@ -37,7 +38,6 @@ __device__ __forceinline__ void join_unit(const TreeArgs& a, bool has, int c0, c
 #pragma unroll
     for (int e = 0; e < kCols; ++e) o[e] = 0.f;
     if (live) {
-        constexpr int U = 3;
 #pragma unroll 1
         for (int c = c0 + part; c <= c1; c += group * U) {
             float4 ml[U];
@@ -71,11 +71,12 @@ __device__ __forceinline__ void join_unit(const TreeArgs& a, bool has, int c0, c
 #pragma unroll
     for (int e = 0; e < kCols; ++e) so[warp][e][lane] = o[e];
     __syncthreads();
-    // 32 rows of 8 column pairs
+    // 32 rows of column pairs
+    constexpr int kPairs = kCols / 2;
     const int w0 = warp - part;
 #pragma unroll 1
-    for (int t0 = part * 32 + lane; has && t0 < 256; t0 += group * 32) {
-        const int k = t0 >> 3, pair = t0 & 7;
+    for (int t0 = part * 32 + lane; has && t0 < 32 * kPairs; t0 += group * 32) {
+        const int k = t0 / kPairs, pair = t0 % kPairs;
         if (i0 + k >= a.rt || r * a.rt + i0 + k >= a.R) break;
         const bool dead = !lives(i0 + k);
         float2 t = make_float2(0.f, 0.f);
@@ -105,10 +106,27 @@ __device__ __forceinline__ void join_unit(const TreeArgs& a, bool has, int c0, c
     }
 }
 
+template <int D, int kCols, int U>
+__device__ __forceinline__ void join_units(const TreeArgs& a, int n, int chunks, const short* list, float (&so)[kWarps][kMaxCols][33],
+                                           float (&sm)[kWarps][3][32])
+{
+    const int warp = threadIdx.x >> 5, units = n * chunks * (D / kCols);
+    int group = kWarps;
+    while (group > 1 && units > (int)gridDim.x * (kWarps / group)) group >>= 1;
+    for (int u0 = blockIdx.x; u0 < units; u0 += gridDim.x * (kWarps / group)) {
+        const int u = u0 + warp / group * (int)gridDim.x;
+        const bool has = u < units;
+        const int c0 = has ? list[u / (chunks * (D / kCols))] : 0;
+        const int4 item = has ? a.border[c0] : make_int4(0, 0, 0, 0);
+        join_unit<D, kCols, U>(a, has, c0, item, u / (D / kCols) % chunks * 32, u % (D / kCols) * kCols, group, warp % group, so, sm);
+        __syncthreads();
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32, 2) tree_join_kernel(const TreeArgs a)
 {
-    __shared__ float so[kWarps][kCols][33];
+    __shared__ float so[kWarps][kMaxCols][33];
     __shared__ float sm[kWarps][3][32];
     __shared__ short list[kTreeMaxCtas];
     __shared__ int count[kWarps];
@@ -145,18 +163,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) tree_join_kernel(const TreeArg
         if (has) list[before + __popc(votes & ((1u << lane) - 1u))] = (short)mine;
         __syncthreads();
     }
-    const int units = n * chunks * (D / kCols);
-    // few units: all the block's warps share one; many: a warp has its own, and the loads of eight are in flight
-    int group = kWarps;
-    while (group > 1 && units > (int)gridDim.x * (kWarps / group)) group >>= 1;
-    for (int u0 = blockIdx.x; u0 < units; u0 += gridDim.x * (kWarps / group)) {
-        const int u = u0 + warp / group * (int)gridDim.x;
-        const bool has = u < units;
-        const int c0 = has ? list[u / (chunks * (D / kCols))] : 0;
-        const int4 item = has ? a.border[c0] : make_int4(0, 0, 0, 0);
-        join_unit<D>(a, has, c0, item, u / (D / kCols) % chunks * 32, u % (D / kCols) * kCols, group, warp % group, so, sm);
-        __syncthreads();
-    }
+    if (n * chunks * (D / 4) <= (int)gridDim.x)
+        join_units<D, 4, 8>(a, n, chunks, list, so, sm);
+    else
+        join_units<D, 16, 3>(a, n, chunks, list, so, sm);
 }
 
 }  // namespace
@@ -165,7 +175,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) tree_join_kernel(const TreeArg
 // device (the workspace is sized by it).
 struct Cut {
     bool tc;
-    int rt, nrt, ctas;
+    int tile, rt, nrt, ctas;
 };
 
 static Cut cut_of(const Cache& c, int H, int T, int dtype)
@@ -173,9 +183,10 @@ static Cut cut_of(const Cache& c, int H, int T, int dtype)
     Cut u;
     const int R = H / c.Hkv * T;
     u.tc = dtype == 1;
+    u.tile = u.tc ? kTreeTile : kTreeSimtTile;
     u.rt = u.tc ? (R <= 128 ? 128 : 256) : tree_simt_rows(R);
     u.nrt = (R + u.rt - 1) / u.rt;
-    const long long most = (long long)c.B * c.Hkv * u.nrt * ((c.cap + kTreeTile - 1) / kTreeTile);
+    const long long most = (long long)c.B * c.Hkv * u.nrt * ((c.cap + u.tile - 1) / u.tile);
     const int cap = u.tc ? kTreeMaxTcCtas : kTreeMaxCtas;
     u.ctas = (int)(most < cap ? most : cap);
     return u;
@@ -201,6 +212,7 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
     a.T = t.T;
     a.R = a.G * t.T;
     a.cap = c.cap;
+    a.tile = u.tile;
     a.rt = u.rt;
     a.nrt = u.nrt;
     const int resident = device_sm_count() * (u.tc ? 1 : kTreeSimtCtasPerSm);
@@ -233,7 +245,7 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
 
 cudaError_t launch_tree_join(const TreeArgs& a, int d, cudaStream_t s)
 {
-    const long long most = (long long)(a.ctas > 1 ? a.ctas - 1 : 1) * ((tree_item_rows(a) + 31) / 32) * (d / kCols);
+    const long long most = (long long)(a.ctas > 1 ? a.ctas - 1 : 1) * ((tree_item_rows(a) + 31) / 32) * (d / 4);
     const long long resident = (long long)device_sm_count() * 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(most < resident ? most : resident));

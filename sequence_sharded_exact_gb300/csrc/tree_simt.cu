@@ -14,19 +14,22 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kChunk = 32;
+static_assert(kTreeSimtTile % kChunk == 0, "a tile is whole chunks");
 
 // 16 bytes of a cached row as float32.
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float up, float* f);
+__device__ __forceinline__ void spread16(const uint4& v, float up, float* f);
 template <>
-__device__ __forceinline__ void load16<float>(const float* p, float, float* f)
+__device__ __forceinline__ void spread16<float>(const uint4& v, float, float* f)
 {
-    *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(p);
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
 }
 template <>
-__device__ __forceinline__ void load16<uint8_t>(const uint8_t* p, float up, float* f)
+__device__ __forceinline__ void spread16<uint8_t>(const uint4& v, float up, float* f)
 {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -36,8 +39,50 @@ __device__ __forceinline__ void load16<uint8_t>(const uint8_t* p, float up, floa
     }
 }
 
+// A thread's part of a chunk's keys and values as they are cached, on their way from memory while the chunk before
+// is worked on; rows from `end` on are zeros.
+template <typename TC, int D>
+struct Chunk {
+    static constexpr int kPer = 16 / sizeof(TC), kN = kChunk * D / kPer / kThreads;
+    uint4 k[kN], v[kN];
+    float uk[kN], uv[kN];
+    __device__ __forceinline__ void load(const TreeArgs& a, long long row0, int k0, int end)
+    {
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            const int e = threadIdx.x + n * kThreads, j = e / (D / kPer), c = e % (D / kPer) * kPer;
+            k[n] = v[n] = make_uint4(0, 0, 0, 0);
+            uk[n] = uv[n] = 1.f;
+            if (k0 + j >= end) continue;
+            const long long src = row0 + k0 + j;
+            if (sizeof(TC) == 1) {
+                uk[n] = __uint_as_float((uint32_t)a.k_exp[src] << 23);
+                uv[n] = __uint_as_float((uint32_t)a.v_exp[src] << 23);
+            }
+            k[n] = *reinterpret_cast<const uint4*>(static_cast<const TC*>(a.k) + src * D + c);
+            v[n] = *reinterpret_cast<const uint4*>(static_cast<const TC*>(a.v) + src * D + c);
+        }
+    }
+    template <int kStride>
+    __device__ __forceinline__ void store(float (*ks)[kStride], float (*vs)[D]) const
+    {
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            const int e = threadIdx.x + n * kThreads, j = e / (D / kPer), c = e % (D / kPer) * kPer;
+            float fk[kPer], fv[kPer];
+            spread16<TC>(k[n], uk[n], fk);
+            spread16<TC>(v[n], uv[n], fv);
+#pragma unroll
+            for (int i = 0; i < kPer; i += 4) {
+                *reinterpret_cast<float4*>(&ks[j][c + i]) = make_float4(fk[i], fk[i + 1], fk[i + 2], fk[i + 3]);
+                *reinterpret_cast<float4*>(&vs[j][c + i]) = make_float4(fv[i], fv[i + 1], fv[i + 2], fv[i + 3]);
+            }
+        }
+    }
+};
+
 template <typename TC, int D, int ROWS>
-__global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a)
+__global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel(const TreeArgs a)
 {
     constexpr int RW = ROWS / 4;            // query rows per warp in the scores
     constexpr int SPLIT = kThreads / D;     // threads per output column
@@ -75,31 +120,13 @@ __global__ void __launch_bounds__(kThreads) tree_simt_kernel(const TreeArgs a)
         }
 #pragma unroll
         for (int i = 0; i < RC; ++i) acc[i] = 0.f;
-        const int end = w.t1 * kTreeTile < w.s.end ? w.t1 * kTreeTile : w.s.end;
-        for (int k0 = w.t0 * kTreeTile; k0 < end; k0 += kChunk) {
-            constexpr int per = 16 / sizeof(TC);
+        const int end = w.t1 * kTreeSimtTile < w.s.end ? w.t1 * kTreeSimtTile : w.s.end;
+        Chunk<TC, D> next;
+        next.load(a, head * a.cap, w.t0 * kTreeSimtTile, end);
+        for (int k0 = w.t0 * kTreeSimtTile; k0 < end; k0 += kChunk) {
             __syncthreads();
-            for (int e = tid; e < kChunk * D / per; e += kThreads) {
-                const int j = e / (D / per), c = e % (D / per) * per;
-                float fk[per], fv[per];
-#pragma unroll
-                for (int i = 0; i < per; ++i) fk[i] = fv[i] = 0.f;
-                if (k0 + j < end) {
-                    const long long src = head * a.cap + k0 + j;
-                    float uk = 1.f, uv = 1.f;
-                    if (sizeof(TC) == 1) {
-                        uk = __uint_as_float((uint32_t)a.k_exp[src] << 23);
-                        uv = __uint_as_float((uint32_t)a.v_exp[src] << 23);
-                    }
-                    load16(static_cast<const TC*>(a.k) + src * D + c, uk, fk);
-                    load16(static_cast<const TC*>(a.v) + src * D + c, uv, fv);
-                }
-#pragma unroll
-                for (int i = 0; i < per; i += 4) {
-                    *reinterpret_cast<float4*>(&ks[j][c + i]) = make_float4(fk[i], fk[i + 1], fk[i + 2], fk[i + 3]);
-                    *reinterpret_cast<float4*>(&vs[j][c + i]) = make_float4(fv[i], fv[i + 1], fv[i + 2], fv[i + 3]);
-                }
-            }
+            next.store(ks, vs);
+            if (k0 + kChunk < end) next.load(a, head * a.cap, k0 + kChunk, end);
             __syncthreads();
             float sc[RW];
 #pragma unroll
