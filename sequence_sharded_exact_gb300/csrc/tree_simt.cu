@@ -223,10 +223,12 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
 template <typename TC, int D>
 cudaError_t launch_rows(const TreeArgs& a, cudaStream_t s)
 {
-    if (a.rt == 4)
-        tree_simt_kernel<TC, D, 4><<<a.ctas, kThreads, 0, s>>>(a);
-    else
-        tree_simt_kernel<TC, D, 16><<<a.ctas, kThreads, 0, s>>>(a);
+    switch (a.rt) {
+        case 4: tree_simt_kernel<TC, D, 4><<<a.ctas, kThreads, 0, s>>>(a); break;
+        case 8: tree_simt_kernel<TC, D, 8><<<a.ctas, kThreads, 0, s>>>(a); break;
+        case 12: tree_simt_kernel<TC, D, 12><<<a.ctas, kThreads, 0, s>>>(a); break;
+        default: tree_simt_kernel<TC, D, 16><<<a.ctas, kThreads, 0, s>>>(a);
+    }
     return cudaGetLastError();
 }
 
@@ -238,7 +240,12 @@ cudaError_t launch_d(const TreeArgs& a, int d, cudaStream_t s)
 
 }  // namespace
 
-int tree_simt_rows(int R) { return R <= 4 ? 4 : 16; }
+// Query rows per tile, a multiple of 4 (the warps): as few tiles as 16 rows each allow, and as even.
+int tree_simt_rows(int R)
+{
+    const int tiles = (R + 15) / 16, rows = (R + tiles - 1) / tiles;
+    return (rows + 3) / 4 * 4;
+}
 
 cudaError_t launch_tree_simt(const TreeArgs& a, int d, int cache_dtype, cudaStream_t s)
 {
