@@ -173,8 +173,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) tree_join_kernel(const TreeArg
 
 // How a problem is cut: its path, query rows per row tile, and the most CTAs of the first launch, known without a
 // device (the workspace is sized by it).
+enum class Path { kSimt, kMma, kTc };
+
 struct Cut {
-    bool tc;
+    Path path;
     int tile, rt, nrt, ctas;
 };
 
@@ -182,12 +184,12 @@ static Cut cut_of(const Cache& c, int H, int T, int dtype)
 {
     Cut u;
     const int R = H / c.Hkv * T;
-    u.tc = dtype == 1;
-    u.tile = u.tc ? kTreeTile : kTreeSimtTile;
-    u.rt = u.tc ? (R <= 128 ? 128 : 256) : tree_simt_rows(R);
+    u.path = dtype != 1 ? Path::kSimt : c.dtype == kCacheE4m3 && R <= kTreeMmaRows ? Path::kMma : Path::kTc;
+    u.tile = u.path == Path::kSimt ? kTreeSimtTile : kTreeTile;
+    u.rt = u.path == Path::kSimt ? tree_simt_rows(R) : u.path == Path::kMma ? kTreeMmaRows : R <= 128 ? 128 : 256;
     u.nrt = (R + u.rt - 1) / u.rt;
     const long long most = (long long)c.B * c.Hkv * u.nrt * ((c.cap + u.tile - 1) / u.tile);
-    const int cap = u.tc ? kTreeMaxTcCtas : kTreeMaxCtas;
+    const int cap = u.path == Path::kSimt ? kTreeMaxCtas : u.path == Path::kMma ? kTreeMaxMmaCtas : kTreeMaxTcCtas;
     u.ctas = (int)(most < cap ? most : cap);
     return u;
 }
@@ -215,7 +217,7 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
     a.tile = u.tile;
     a.rt = u.rt;
     a.nrt = u.nrt;
-    const int resident = device_sm_count() * (u.tc ? 1 : kTreeSimtCtasPerSm);
+    const int resident = device_sm_count() * (u.path == Path::kSimt ? kTreeSimtCtasPerSm : u.path == Path::kMma ? kTreeMmaCtasPerSm : 1);
     a.ctas = u.ctas < resident ? u.ctas : resident;
     a.mask_batched = t.mask_batched;
     a.bf16_out = t.out_dtype == 1;
@@ -236,7 +238,9 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
     a.part_ml = reinterpret_cast<float*>(ws + border_bytes(u));
     a.part_o = reinterpret_cast<float*>(ws + border_bytes(u) + ml_bytes(u));
     cudaError_t e;
-    if (u.tc)
+    if (u.path == Path::kMma)
+        e = launch_tree_mma(a, c.d, s);
+    else if (u.path == Path::kTc)
         e = c.d == 128 ? launch_tree_tc_d128(a, c.dtype == kCacheE4m3, s) : launch_tree_tc_d64(a, c.dtype == kCacheE4m3, s);
     else
         e = launch_tree_simt(a, c.d, c.dtype, s);

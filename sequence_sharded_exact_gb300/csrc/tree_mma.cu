@@ -1,0 +1,505 @@
+// tree_mma.cu -- attention over an e4m3 cache (tree.cuh) for bf16 queries, up to 8 query rows per kv head.
+//
+// So few rows leave the 128-row products of tree_tc_body.cuh nearly empty, and what bounds that path over an e4m3
+// cache is V's way through shared memory as bf16.  Here a warp works on 16 cached rows by itself, in products whose
+// 16 rows are cached rows or columns of V and whose 8 columns are queries (mma.m16n8k16, f16, float32 sums):
+//   S^T = K Q^T,  O^T += V^T P^T,
+// with operands that a thread puts together in registers: every e4m3 value is an f16, by one conversion per two of
+// them, and nothing goes back to shared memory.  The order of a product's contraction and of its rows is free: thread
+// (t, g) of a warp (t = lane % 4, g = lane / 4) takes d / 4 neighbouring elements of K's rows g and g + 8, and of V's rows
+// 2t, 2t + 1, 2t + 8, 2t + 9 the d / 8 from d / 8 g on, whose bytes it pairs up.  S^T's weights become P^T's operand by
+// a transposition of 8 x 8 within the warp.
+//   * Queries: x 2^-e in f16, e such that the row's largest lies in [2^14, 2^15): a bf16's eight bits are exact down
+//     to 2^-28 of it.  The scales of rows and keys are applied to S.
+//   * Weights: p 2^(ev_j - E + 7) in f16, ev_j the exponent of key j's V row, E the largest so far of the rows that the
+//     query sees: eleven bits down to 2^-21 of weight 1 at E, weight and scale together.  The sum l takes p itself.
+//     The reference of p follows the row maximum only when that grows by more than 2^8, so O is seldom rescaled.
+//   * A CTA's eight warps take 16 rows of every tile each, with rings of their own that the TMA fills; m, l, E and O are
+//     a warp's own until the item's end, where they meet in the rings' memory, in warp order.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <mutex>
+
+#include "ra_internal.h"
+#include "ra_ptx.cuh"
+#include "tree.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps, kKeys = 16, kStages = 2;
+static_assert(kWarps * kKeys == kTreeTile, "a warp's rows of a tile");
+constexpr long long kWaitLimit = 10000000000ll;
+
+template <int D>
+struct Cfg {
+    static constexpr uint32_t kHalf = kKeys * D;                          // bytes of 16 rows
+    static constexpr uint32_t kRings = kWarps * kStages * 2 * kHalf;      // [warps][stages][k, v]
+    static constexpr uint32_t kMl = kRings;                               // [warps][8] m, l, E's bits, 0
+    static constexpr uint32_t kBar = kMl + kWarps * 8 * 16;
+    static constexpr uint32_t kAbort = kBar + kWarps * kStages * 8;
+    static constexpr uint32_t kSmem = kAbort + 8 + 1024;  // slack for the 1024-byte alignment of the base
+    static_assert(kWarps * 32 * D <= kRings, "the warps' O meet in the rings");
+    static_assert(kSmem * kTreeMmaCtasPerSm <= 229376, "shared memory");
+};
+
+struct Maps {
+    CUtensorMap k, v;
+};
+
+// A bounded wait by the whole warp.  After one has given up (or another warp's) every further wait returns at once, and
+// the caller goes on to its end with whatever is there: the status word says that the results do not count.
+__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, const WaitCtl& ctl)
+{
+    if (!mbar_try_wait(bar, parity)) {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar, parity)) {
+            if (*ctl.abort) break;
+            if (clock64() - t0 > kWaitLimit) {
+                *ctl.abort = 1;
+                atomicOr(ctl.status, kStatusTimeout);
+                break;
+            }
+        }
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity)
+{
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (global_timer_ns() - t0 > 1000000000ull) return;
+    }
+}
+
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
+{
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Rows g of an 8 x 8 matrix of f16, two columns 2t, 2t + 1 per thread: its transpose in the same places.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// A V byte that stands for no finite float32 at its row's scale: NaN, and from kHuge on the values that pass 2^128.
+constexpr int kHuge = 247;
+__device__ __forceinline__ bool not_finite(uint32_t x, int scale)
+{
+    const uint32_t mag = x & 127u;
+    return mag == 127u || (scale >= kHuge && (scale == 255 || mag >= (uint32_t)(262 - scale) << 3));
+}
+
+// 2^n, 0 below the smallest normal number; n <= 127.
+__device__ __forceinline__ float pow2(int n) { return __uint_as_float((uint32_t)max(127 + n, 0) << 23); }
+
+// Byte offset of 16-byte chunk c of row r in the TMA's 128- (d = 128) or 64-byte swizzle.
+template <int D>
+__device__ __forceinline__ uint32_t at16(int r, int c)
+{
+    return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// Query row x as the operand of S^T's k steps, two registers each: elements (D / 4) t + 4 s .. + 3 of step s.  Returns the
+// row's scale times the scores'.
+template <int D>
+__device__ __forceinline__ float load_query(const TreeArgs& a, long long head, int x, uint32_t (&f)[D / 8])
+{
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (head * a.R + x) * D) + (threadIdx.x & 3) * (D / 32);
+    uint32_t big = 0;  // bits of the largest magnitude: bf16 in the upper half, ordered as integers
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        const uint4 v = x < a.R ? src[c] : make_uint4(0, 0, 0, 0);
+        f[4 * c] = v.x, f[4 * c + 1] = v.y, f[4 * c + 2] = v.z, f[4 * c + 3] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) big = max(big, max(f[i] << 16 & 0x7fff0000u, f[i] & 0x7fff0000u));
+    big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    const bool finite = big < 0x7f800000u;
+    int e = (int)(big >> 23) - 127 - 14;
+    e = e < -126 ? -126 : e;
+    const float down = pow2(-e);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+        f[i] = finite ? pack_f16x2(__uint_as_float(f[i] << 16) * down, __uint_as_float(f[i] & 0xffff0000u) * down) : 0u;
+    return finite ? pow2(e) * a.scale_log2 : __uint_as_float(0x7fc00000u);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, kTreeMmaCtasPerSm) tree_mma_kernel(const __grid_constant__ Maps maps, const TreeArgs a)
+{
+    using C = Cfg<D>;
+    constexpr int kTiles = D / 16;  // 16-row tiles of O^T
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t4 = lane & 3, g8 = lane >> 2;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kAbort);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWarps * kStages; ++i) mbar_init(sbase + C::kBar + 8u * (uint32_t)i, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    TreeWalk w;
+    if (!w.begin(a, blockIdx.x)) {  // the same for every warp
+        if (threadIdx.x == 0) a.border[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        return;
+    }
+    const WaitCtl ctl{abort_flag, a.status, 0};
+    const uint32_t ring_at = (uint32_t)warp * kStages * 2 * C::kHalf, bars = sbase + C::kBar + 8u * (uint32_t)(warp * kStages);
+    int4 border = make_int4(-1, 0, 0, 0);
+    uint32_t used = 0, sent = 0;  // of the ring (sent: lane 0's)
+
+    do {
+        if (w.goes_on()) border = w.border(a, blockIdx.x);
+        const int z = w.b * a.Hkv + w.g;
+        const int row0 = w.t0 * kTreeTile + warp * kKeys;  // this warp's rows: row0, row0 + 128, ...
+        const int n = w.t1 - w.t0 - ((w.t1 - 1) * kTreeTile + warp * kKeys >= w.s.end ? 1 : 0);
+        auto send = [&](int i) {  // rows of the warp's i-th group
+            if (lane == 0 && !*abort_flag) {
+                const uint32_t slot = sent % kStages, bar = bars + 8u * slot, dst = sbase + ring_at + slot * 2 * C::kHalf;
+                mbar_arrive_expect_tx(bar, 2 * C::kHalf);
+                tma_load_3d(dst, &maps.k, bar, 0, row0 + i * kTreeTile, z);
+                tma_load_3d(dst + C::kHalf, &maps.v, bar, 0, row0 + i * kTreeTile, z);
+                ++sent;
+            }
+        };
+        // lane's key's scale byte of group i: K's of key lane, V's of key lane - 16; four groups' in use, four on their
+        // way (a register that is moved on is waited for)
+        const uint8_t* exps = (lane < kKeys ? a.k_exp : a.v_exp) + (long long)z * a.cap;
+        auto scale_byte = [&](int i) {
+            const int row = row0 + i * kTreeTile + (lane & 15);
+            return i < n && row < w.s.end ? (uint32_t)exps[row] : 0u;
+        };
+        uint32_t bytes = 0, coming[4];
+        for (int i = 0; i < kStages && i < n; ++i) send(i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) coming[e] = scale_byte(e);
+
+        uint32_t qr[D / 8];
+        const float scale = load_query<D>(a, z, g8, qr);
+        float o[kTiles][4], m[2], l[2], sl[2];  // queries 2t + u
+        int big_e[2];                           // E as the scale's byte
+        bool live[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int x = 2 * t4 + u;
+            sl[u] = __shfl_sync(0xffffffffu, scale, x * 4);
+            m[u] = -INFINITY;
+            l[u] = 0.f;
+            big_e[u] = 0;
+            live[u] = x < a.R && x % a.T < w.s.cnt;
+        }
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+        auto sees = [&](int u, int key) {
+            return key < w.s.len || (key < w.s.end && live[u] && tree_sees(a, w.b, (2 * t4 + u) % a.T, key - w.s.len));
+        };
+
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const uint32_t slot = used % kStages;
+            const uint8_t* kp = smem + ring_at + slot * 2 * C::kHalf;
+            if ((i & 3) == 0) {
+                bytes = coming[0] | coming[1] << 8 | coming[2] << 16 | coming[3] << 24;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) coming[e] = scale_byte(i + 4 + e);
+            }
+            const uint32_t byte = bytes & 255u;
+            bytes >>= 8;
+            // keys g and g + 8: scales of K, exponents of V
+            const float ks[2] = {__uint_as_float(__shfl_sync(0xffffffffu, byte, g8) << 23), __uint_as_float(__shfl_sync(0xffffffffu, byte, g8 + 8) << 23)};
+            const int ve[2] = {(int)__shfl_sync(0xffffffffu, byte, g8 + 16), (int)__shfl_sync(0xffffffffu, byte, g8 + 24)};
+            const int group_e = (int)__reduce_max_sync(0xffffffffu, lane < kKeys ? 0u : byte);
+            warp_wait(bars + 8u * slot, (used / kStages) & 1, ctl);
+            ++used;
+
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {  // 16 bytes of each key at a time: four k steps
+                const uint4 x0 = *reinterpret_cast<const uint4*>(kp + at16<D>(g8, D == 128 ? 2 * t4 + c : t4));
+                const uint4 x1 = *reinterpret_cast<const uint4*>(kp + at16<D>(g8 + 8, D == 128 ? 2 * t4 + c : t4));
+                const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+                for (int st = 0; st < 4; ++st) {
+                    uint32_t a0, a1, a2, a3;
+                    e4m3x4_to_f16(w0[st], a0, a2);
+                    e4m3x4_to_f16(w1[st], a1, a3);
+                    mma16(s, a0, a1, a2, a3, qr[2 * (4 * c + st)], qr[2 * (4 * c + st) + 1]);
+                }
+            }
+
+            const int k0 = row0 + i * kTreeTile;
+            const bool masked = k0 + kKeys > w.s.len;
+            bool raise = false;
+            float alpha[2], p[2][2];  // p: [key][query]
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float x0 = s[u] * ks[0], x1 = s[2 + u] * ks[1];
+                int new_e = group_e;
+                if (masked) {
+                    const bool s0 = sees(u, k0 + g8), s1 = sees(u, k0 + g8 + 8);
+                    if (!s0) x0 = -INFINITY;
+                    if (!s1) x1 = -INFINITY;
+                    new_e = max(s0 ? ve[0] : 0, s1 ? ve[1] : 0);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) new_e = max(new_e, __shfl_xor_sync(0xffffffffu, new_e, d));
+                }
+                new_e = max(new_e, big_e[u]);
+                float mx = fmaxf(x0, x1);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                mx *= sl[u];
+                const float to = mx > m[u] + 8.f ? mx : m[u], ref = to == -INFINITY ? 0.f : to;
+                alpha[u] = 1.f;
+                if (to != m[u] || new_e != big_e[u]) {
+                    const float keep = ex2_approx(m[u] - ref);
+                    l[u] *= keep;
+                    alpha[u] = keep * pow2(big_e[u] - new_e);
+                    m[u] = to;
+                    big_e[u] = new_e;
+                    raise = true;
+                }
+                p[0][u] = ex2_approx(fmaf(x0, sl[u], -ref));
+                p[1][u] = ex2_approx(fmaf(x1, sl[u], -ref));
+                l[u] += p[0][u] + p[1][u];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) p[e][u] *= pow2(min(ve[e] - new_e, 0) + 7);  // (above E: not seen, p = 0)
+            }
+            const uint32_t pb[2] = {transpose8(pack_f16x2(p[0][0], p[0][1])), transpose8(pack_f16x2(p[1][0], p[1][1]))};
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[j][e] *= alpha[e & 1];
+            }
+
+            // V: rows 2t, 2t + 1, 2t + 8, 2t + 9, eight of the thread's d / 8 columns at a time
+            const uint8_t* vp = kp + C::kHalf;
+#pragma unroll
+            for (int part = 0; part < D / 64; ++part) {
+                uint32_t vw[4][2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = 2 * t4 + (e & 1) + 8 * (e >> 1);
+                    const uint2 v = *reinterpret_cast<const uint2*>(vp + (D == 128 ? at16<D>(r, g8) + part * 8 : at16<D>(r, g8 >> 1) + (g8 & 1) * 8));
+                    vw[e][0] = v.x, vw[e][1] = v.y;
+                }
+                // Rows behind the sequence count as zeros.  NaN, and values whose scale takes them past float32, are
+                // cleared and added to the queries that see them: a weight of 0 would not hide them from the others.
+                if (masked || group_e >= kHuge) {
+                    bool odd = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = 2 * t4 + (e & 1) + 8 * (e >> 1), er = (int)__shfl_sync(0xffffffffu, byte, r + 16);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            if (k0 + r >= w.s.end) vw[e][q] = 0;
+#pragma unroll 1
+                            for (int sh = 0; sh < 32; sh += 8)
+                                if (not_finite(vw[e][q] >> sh & 255u, er)) {
+                                    vw[e][q] &= ~(255u << sh);
+                                    odd |= k0 + r < w.s.end;
+                                }
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+                        for (int r = 0; r < kKeys; ++r) {
+                            const int er = (int)__shfl_sync(0xffffffffu, byte, r + 16);
+                            if (k0 + r >= w.s.end) continue;
+                            const bool s0 = sees(0, k0 + r), s1 = sees(1, k0 + r);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const int d = g8 * (D / 8) + part * 8 + j;
+                                const uint32_t x = vp[at16<D>(r, d >> 4) + (d & 15)];
+                                if (!not_finite(x, er)) continue;
+                                float v, y0, y1, y2;
+                                e4m3x4_to_float(x, v, y0, y1, y2);
+                                v *= __uint_as_float((uint32_t)er << 23);
+                                if (s0) o[part * 4 + j / 2][2 * (j & 1)] += v;
+                                if (s1) o[part * 4 + j / 2][2 * (j & 1) + 1] += v;
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // columns 4q + 2h, + 1 of the eight
+                        uint32_t a0, a1, a2, a3;
+                        e4m3x4_to_f16(__byte_perm(vw[0][q], vw[1][q], h ? 0x7362 : 0x5140), a0, a1);
+                        e4m3x4_to_f16(__byte_perm(vw[2][q], vw[3][q], h ? 0x7362 : 0x5140), a2, a3);
+                        mma16(o[part * 4 + 2 * q + h], a0, a1, a2, a3, pb[0], pb[1]);
+                    }
+            }
+            __syncwarp();  // all lanes have read the slot
+            if (i + kStages < n) send(i + kStages);
+        }
+
+        // the item's rows: the eight warps' m, l, E and O, in warp order
+        float4* ml = reinterpret_cast<float4*>(smem + C::kMl);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[u] += __shfl_xor_sync(0xffffffffu, l[u], d);
+            if (g8 == 0) ml[warp * 8 + 2 * t4 + u] = make_float4(m[u], l[u], __int_as_float(big_e[u]), 0.f);
+        }
+        __syncthreads();  // (and every warp's ring is free)
+        float4* xs = reinterpret_cast<float4*>(smem);
+        constexpr int kFours = D / 32, kVecs = 2 * kFours;  // float4 per thread: [u][fours of its d / 8 columns]
+        auto join = [&](int x, float& top, float& sum, int& top_e) {
+            top = -INFINITY;
+            top_e = 0;
+            for (int k = 0; k < kWarps; ++k) {
+                const float4 v = ml[k * 8 + x];
+                top = fmaxf(top, v.x);
+                top_e = max(top_e, __float_as_int(v.z));
+            }
+            const float ref = top == -INFINITY ? 0.f : top;
+            sum = 0.f;
+            for (int k = 0; k < kWarps; ++k) {
+                const float4 v = ml[k * 8 + x];
+                // NaN scores alone leave no maximum
+                sum = v.x == -INFINITY && v.y != 0.f ? v.y : fmaf(v.y, ex2_approx(v.x - ref), sum);
+            }
+        };
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            float top, sum;
+            int top_e;
+            join(2 * t4 + u, top, sum, top_e);
+            const float f = ex2_approx(m[u] - (top == -INFINITY ? 0.f : top)) * pow2(big_e[u] - top_e);
+#pragma unroll
+            for (int c = 0; c < kFours; ++c)
+                xs[(warp * kVecs + u * kFours + c) * 32 + lane] =
+                    make_float4(o[2 * c][u] * f, o[2 * c][2 + u] * f, o[2 * c + 1][u] * f, o[2 * c + 1][2 + u] * f);
+        }
+        __syncthreads();
+        const bool whole = w.whole();
+        const long long pslot = (long long)blockIdx.x * 2 + (w.first ? 0 : 1);
+        const int row = 2 * t4 + warp / kFours, d = g8 * (D / 8) + warp % kFours * 4;  // warp k: vector k (d = 64: the first four)
+        if (warp < kVecs && row < a.R) {
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const float4 y = xs[(k * kVecs + warp) * 32 + lane];
+                sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+            }
+            float mr, lr;
+            int top_e;
+            join(row, mr, lr, top_e);
+            const bool none = row % a.T >= w.s.cnt || (mr == -INFINITY && lr == 0.f);
+            const long long grow = (long long)z * a.R + row;
+            const float inv = whole ? 1.0f / lr : 1.0f, up = __uint_as_float((uint32_t)top_e << 23);
+            float* ps = &sum.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ps[e] = none ? 0.f : ps[e] * 0x1p-7f * up * inv;
+            if (whole) {
+                if (a.bf16_out)
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + grow * D + d) =
+                        make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+                else
+                    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + grow * D + d) = sum;
+                if (d == 0) a.lse[grow] = none ? -INFINITY : (mr + log2f(lr)) * kLn2;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a.part_o[(pslot * D + d + e) * a.rt + row] = ps[e];
+                if (d == 0) *reinterpret_cast<float4*>(a.part_ml + (pslot * a.rt + row) * 4) = make_float4(mr, lr, lr, 0.f);
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the rings are filled again
+        __syncthreads();
+    } while (w.next(a));
+    if (threadIdx.x == 0) a.border[blockIdx.x] = border;
+    if (lane == 0) {  // after a wait that gave up, copies may still be on their way
+        for (uint32_t k = 1; k <= (uint32_t)kStages && k <= sent; ++k)
+            drain_wait(bars + 8u * ((sent - k) % kStages), ((sent - k) / kStages) & 1);
+    }
+}
+
+// [heads][cap][D] bytes, boxes of 16 rows, in the swizzle of a whole row.
+template <int D>
+bool make_map(CUtensorMap* map, const void* base, long long rows, long long heads)
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)heads};
+    cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)rows * D};
+    cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)kKeys, 1u};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const TreeArgs& a, cudaStream_t s)
+{
+    using C = Cfg<D>;
+    Maps maps;
+    const long long heads = (long long)a.B * a.Hkv;
+    if (!make_map<D>(&maps.k, a.k, a.cap, heads) || !make_map<D>(&maps.v, a.v, a.cap, heads)) return cudaErrorInvalidValue;
+    static std::mutex mu;
+    static bool done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!done[dev]) {
+            e = cudaFuncSetAttribute(tree_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+            if (e != cudaSuccess) return e;
+            done[dev] = true;
+        }
+    }
+    tree_mma_kernel<D><<<a.ctas, kThreads, C::kSmem, s>>>(maps, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tree_mma(const TreeArgs& a, int d, cudaStream_t s)
+{
+    return d == 128 ? launch<128>(a, s) : launch<64>(a, s);
+}
+
+}  // namespace ra
