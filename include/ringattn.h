@@ -419,6 +419,7 @@ RA_API size_t ring_attn_ulysses_bwd_workspace_size(int B, int H, int Hkv, int L,
  *   wq, wk: [d] float32.   q_out, k_out: contiguous, dtype; each may be its own contiguous input.
  *   positions: [B][rows] int32, 4-byte aligned: the natural position of every token (any int value),
  *   in place of the layout's; or NULL.
+ *   All sums are float32 (x^2 has to fit it).
  *   base > 0 and finite; eps >= 0 and finite; H % Hkv == 0; L and layout as ring_attn_rope; d in {64, 128}.
  *
  * ring_attn_qk_norm_rope_bwd -- its gradients.  With g = R(-p) dy and u = g w:
@@ -454,7 +455,8 @@ RA_API size_t ring_attn_qk_norm_rope_bwd_workspace_size(int d);
  *   ring_attn_qk_norm_rope, NULL = contiguous) to the rows lens[b] + t of sequence b.  lens, ntok: DEVICE
  *   int32 [B], 4-byte aligned; lens NULL: from row 0; ntok NULL: all T.  Rows that are not written keep
  *   what they held.  A row outside [0, cap), and every row of a sequence with lens[b] < 0, is not
- *   written, and RA_DEVICE_RANGE set in the status word; an ntok[b] outside [0, T] is taken as the nearer end of that range, and the bit set.
+ *   written, and RA_DEVICE_RANGE set in the status word; an ntok[b] outside [0, T] is taken as the nearer
+ *   end of that range, and the bit set.
  * ring_attn_cache_read -- rows [row0, row0 + rows) of every sequence and kv head to k, v
  *   [B][Hkv][rows][d] (dtype, contiguous): the values the cache stands for, rounded once to dtype.
  */

@@ -744,6 +744,14 @@ def _stream_ptr(stream, index):
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
+def _hold(stream, *tensors):
+    """Memory that a call allocated belongs to the current stream: the caller's other stream has to be done with it
+    before it is given out again."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def _run(index, call, *args):
     """Calls the library with device `index` current: a kernel is launched on the device of its tensors."""
     if torch.cuda.current_device() == index:
@@ -844,6 +852,7 @@ def qk_norm_rope(q, k, wq, wk, n_shards=1, layout="contiguous", base=10000.0, ep
     q_out, qo = _output(q_out, "q_out", dev, q.shape, dt)
     k_out, ko = _output(k_out, "k_out", dev, k.shape, dt)
     _run(dev.index, library().ring_attn_qk_norm_rope, *head, qo, ko, *tail, _stream_ptr(stream, dev.index))
+    _hold(stream, q_out, k_out)
     return q_out, k_out
 
 
@@ -865,13 +874,14 @@ def qk_norm_rope_bwd(q, k, wq, wk, dq_out, dk_out, n_shards=1, layout="contiguou
         _need_workspace(workspace, need, dev)
     _run(dev.index, lib.ring_attn_qk_norm_rope_bwd, *head, gq, gk, dqp, dkp, dwq.data_ptr(), dwk.data_ptr(),
          workspace.data_ptr(), workspace.numel(), *tail, _stream_ptr(stream, dev.index))
+    _hold(stream, dq, dk, dwq, dwk, workspace)
     return dq, dk, dwq, dwk
 
 
 class KVCache(NamedTuple):
     """A key/value cache: k, v [B, Hkv, cap, d], bfloat16 or float32 like the tensors written to it, or
     float8_e4m3fn with the rows' exponents + 127 in k_exp, v_exp [B, Hkv, cap] uint8 (an element stands for
-    its e4m3 value times 2^(byte - 127)).  The caller keeps the lengths."""
+    its e4m3 value times 2^(byte - 127), byte 1 to 247).  The caller keeps the lengths."""
     k: torch.Tensor
     v: torch.Tensor
     k_exp: Optional[torch.Tensor] = None
@@ -945,6 +955,7 @@ def cache_read(cache, rows, row0=0, dtype=torch.bfloat16, k=None, v=None, stream
     v, vp = _output(v, "v", dev, shape, dtype)
     _run(dev.index, library().ring_attn_cache_read, *ptrs, kp, vp, B, Hkv, row0, rows, d, cap, code, kind,
          _stream_ptr(stream, dev.index))
+    _hold(stream, k, v)
     return k, v
 
 
@@ -983,4 +994,5 @@ def tree_fwd(q, cache, lens, mask=None, ntok=None, out_dtype=None, out=None, lse
     _run(dev.index, lib.ring_attn_tree_fwd, qp, *ptrs, _fits(lens, "lens", dev, (B,), torch.int32),
          None if ntok is None else _fits(ntok, "ntok", dev, (B,), torch.int32), mp, batched, op, lp,
          workspace.data_ptr(), workspace.numel(), B, H, Hkv, T, d, cap, code, kind, _DTYPES[out_dtype], _stream_ptr(stream, dev.index))
+    _hold(stream, out, lse, workspace)
     return out, lse

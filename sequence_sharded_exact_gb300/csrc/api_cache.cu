@@ -82,7 +82,7 @@ ra_status check_cache(const Cache& c, int dtype)
     if (c.dtype != dtype && c.dtype != RA_E4M3)
         return fail(RA_ERR_INVALID_ARG, "cache dtype %d is neither the tensors' dtype %d nor RA_E4M3", c.dtype, dtype);
     if (c.d != 64 && c.d != 128) return fail(RA_ERR_UNSUPPORTED, "head dim %d not supported (64 or 128)", c.d);
-    if ((long long)c.B * c.Hkv >= (1LL << 31) || (long long)c.B * c.Hkv * c.cap >= (1LL << 40) / c.d)
+    if ((long long)c.B * c.Hkv >= (1LL << 30) || c.cap >= (1 << 30) || (long long)c.B * c.Hkv * c.cap >= (1LL << 40) / c.d)
         return fail(RA_ERR_UNSUPPORTED, "cache too large");
     ra_status st = check_ptrs({c.k, c.v});
     if (st != RA_OK) return st;
@@ -169,7 +169,7 @@ ra_status ring_attn_cache_write(const void* k, const long long* k_strides, const
     ra_status st = check_cache(c, dtype);
     if (st != RA_OK) return st;
     if (T < 1) return fail(RA_ERR_INVALID_ARG, "T must be >= 1 (got %d)", T);
-    if ((long long)B * Hkv * T >= (1LL << 40) / d) return fail(RA_ERR_UNSUPPORTED, "too many rows");
+    if (T >= (1 << 30) || (long long)B * Hkv * T >= (1LL << 40) / d) return fail(RA_ERR_UNSUPPORTED, "too many rows");
     if (!lens && T > cap) return fail(RA_ERR_INVALID_ARG, "T (%d) rows from row 0 do not fit the cache (%d rows)", T, cap);
     if ((st = check_ptrs({k, v})) != RA_OK) return st;
     if ((st = check_ints("lens", lens, true)) != RA_OK || (st = check_ints("ntok", ntok, true)) != RA_OK) return st;

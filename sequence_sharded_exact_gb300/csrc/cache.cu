@@ -13,6 +13,10 @@
 // What bounds it: each element is read once and written once.  d / 8 lanes hold a row (8 elements a
 // lane: 16 or 32 bytes in, 8 out, or the reverse), its largest magnitude is a shuffle reduction in
 // that group, and kUnroll rows are loaded before the first is used.
+//
+// Measured, 131072 rows of 8 kv heads of 128 between bf16 and e4m3 (0.81 GB): written in 123 us (6.55 TB/s, 0.96 of the
+// copy rate), read back in 134 us (6.0 TB/s, 0.89).  With one division per row, in a grid over all rows, it
+// was 236 and 152 us.  Four rows ahead on reading back, in place of eight: 138 us.
 #include <cuda_bf16.h>
 
 #include "ra_internal.h"

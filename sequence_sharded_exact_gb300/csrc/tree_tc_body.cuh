@@ -25,6 +25,20 @@
 // is two e4m3 products at twice the rate, with float32 sums.  The row and column scales are applied to
 // S.  P keeps bf16 (an e4m3 P would lose weights below 2^-9 of the largest, which add up over a long
 // cache), so warps 12-15 turn V into bf16, exactly, scale included.
+//
+// What bounds it, per tile of 128 cached rows on each of 152 SMs, d = 128 (launches apart):
+//   * bf16, up to 128 query rows: 1.38 us for 64 KB, 7.2 TB/s: the memory.  One token over 131072 rows of 8 kv heads
+//     takes 89 us, the second launch included.
+//   * bf16, 256 rows: 1.67 us.  The products take 1.06 of them; S, the softmax and P V of a warpgroup's query rows follow
+//     one another on one S, whose columns P takes (TMEM is full: two S, two O).
+//   * e4m3, up to 128 rows: 1.45 us for 32 KB.  Shared memory serves 1600 of the 2500 cycles at 128 bytes each: copies
+//     256, S 512 (hi and lo), V to bf16 450, P V 256, scales 130; the rest is the same chain.  Up to 8 rows take
+//     tree_mma.cu (0.9 us).  256 rows: 2.5 us.
+// What did not help: S in halves of 64 columns, two per warpgroup (256 rows: 2.29 us: twice the issue and waits);
+// warpgroups that take half of each tile's keys (e4m3 1.58); V's e4m3 to bf16 by moving bits (its instructions are not
+// what takes the time); loading a whole row of V ahead; the e4m3 queries split by warps 12-15 (later at the start, no
+// earlier at an item's end); one thread of a diverged warp issuing (256 rows 1.90 in place of 1.67 us: descriptors then
+// are not uniform registers).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -548,11 +562,11 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
 }
 
 // ------------------------------------------------------------------------------------------------
-// MMA issue (one thread)
+// MMA issue (one warp, one lane of it)
 // ------------------------------------------------------------------------------------------------
 // An item's jobs, one S and one P V each: tile by tile, and (kNq == 2) warpgroup 0's query rows, then 1's.  Job j
 // belongs to warpgroup j & 1; its S is issued once P V of job j - 2, which reads the same TMEM columns, is.  A
-// commit costs the issuing thread over 100 cycles, so there are two per job: S is ready (which also says that P V
+// commit costs the issuing warp 50 to 180 cycles, so there are two per job: S is ready (which also says that P V
 // of job j - 2 is done, and that K has been read), and V has been read.
 template <bool kE4, int kNq>
 __device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint32_t tmem, TreeWalk w, const WaitCtl& ctl)

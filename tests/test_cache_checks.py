@@ -187,3 +187,11 @@ def test_device_tensors_that_do_not_fit_are_refused():
         ra.tree_fwd(z(B, 3, T, d), cache, lens)
     torch.cuda.synchronize()
     assert ra.device_status() == 0
+
+
+@pytest.mark.parametrize("call,kw", [
+    ("write", dict(B=1, Hkv=1, T=1 << 30, cap=1 << 29)), ("write", dict(B=1, Hkv=1, cap=1 << 30)), ("read", dict(B=1, Hkv=1, cap=1 << 30)),
+    ("read", dict(B=1 << 15, Hkv=1 << 15, cap=10)), ("tree", dict(B=1, Hkv=1, cap=1 << 30)),
+])
+def test_row_counts_that_an_int_could_not_step_over(lib, call, kw):
+    assert {"write": _write, "read": _read, "tree": _tree}[call](lib, **kw) == UNS

@@ -215,3 +215,24 @@ def test_nothing_is_written_around_rotated_heads_and_their_gradients(B, H, Hkv, 
     got = ra.qk_norm_rope_bwd(q, k, wq, wk, dq, dk, dq=grads[0][0], dk=grads[1][0], workspace=ws)
     assert all(torch.equal(x, y) for x, y in zip(got, ref))
     assert ws_ok() and all(ok() for _, ok in grads)
+
+
+def test_scratch_stays_with_the_stream_that_uses_it():
+    """Given another stream than the current one, the call's own workspace is not given out again while that stream works."""
+    B, H, Hkv, T, d, cap = 1, 4, 1, 64, 128, 2000
+    cache = _cache_of(_randn(B, Hkv, cap, d, seed=1), _randn(B, Hkv, cap, d, seed=2), BF, BF)
+    q, lens = _randn(B, H, T, d, seed=3, dtype=BF), _i32([1900])
+    ref = ra.tree_fwd(q, cache, lens)
+    need = ra.tree_workspace_size(B, H, Hkv, T, d, cap, BF, BF)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    at = torch.empty(need, dtype=torch.uint8, device=DEV).data_ptr()
+    assert torch.empty(need, dtype=torch.uint8, device=DEV).data_ptr() == at  # a free block is given out again
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)
+    out = ra.tree_fwd(q, cache, lens, stream=s)
+    after = torch.empty(need, dtype=torch.uint8, device=DEV).data_ptr()
+    assert s.query() or after != at
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(out, ref))
