@@ -51,7 +51,7 @@ struct TreeArgs {
     float* part_ml;  // [ctas][2][rt][4]: m (log2 units), l, the output's normaliser (l as the weights were rounded), 0
     float* part_o;   // [ctas][2][d][rt]: a warp that holds consecutive rows writes whole lines
     int4* border;    // [ctas]: the item that starts in this CTA and goes on in the next: sequence (-1: none),
-                     // head * nrt + row tile, its last CTA, its slot here
+                     // head * nrt + row tile, its last CTA, its slot here + 2 * its sequence's drafted tokens
     unsigned int* status;
     float scale_log2;  // log2(e) / sqrt(d)
 };
@@ -106,7 +106,7 @@ struct TreeWalk {
     __device__ __forceinline__ int4 border(const TreeArgs& a, int cta) const
     {
         const long long end = tree_first(a, total, cta + 1) + (nt - t1);
-        return make_int4(b, g * a.nrt + r, tree_owner(a, total, end - 1), first ? 0 : 1);
+        return make_int4(b, g * a.nrt + r, tree_owner(a, total, end - 1), (first ? 0 : 1) + 2 * s.cnt);
     }
 
     __device__ __forceinline__ void take()

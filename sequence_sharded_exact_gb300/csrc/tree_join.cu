@@ -29,11 +29,8 @@ __device__ __forceinline__ void join_unit(const TreeArgs& a, bool has, int c0, c
                                           float (&so)[kWarps][kMaxCols][33], float (&sm)[kWarps][3][32])
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = i0 + lane;
-    const int b = item.x, g = item.y / a.nrt, r = item.y % a.nrt, c1 = item.z, head = item.w;
-    TreeSeq s;
-    s.cnt = 0;
-    if (has) s = tree_seq(a, b);
-    auto lives = [&](int k) { return k < a.rt && r * a.rt + k < a.R && (r * a.rt + k) % a.T < s.cnt; };
+    const int b = item.x, g = item.y / a.nrt, r = item.y % a.nrt, c1 = item.z, head = item.w & 1, cnt = has ? item.w >> 1 : 0;
+    auto lives = [&](int k) { return k < a.rt && r * a.rt + k < a.R && (r * a.rt + k) % a.T < cnt; };
     const bool live = lives(i);
     float m = -INFINITY, l = 0.f, den = 0.f, o[kCols];
 #pragma unroll
@@ -108,7 +105,7 @@ __device__ __forceinline__ void join_unit(const TreeArgs& a, bool has, int c0, c
 }
 
 template <int D, int kCols, int U>
-__device__ __forceinline__ void join_units(const TreeArgs& a, int n, int chunks, const short* list, float (&so)[kWarps][kMaxCols][33],
+__device__ __forceinline__ void join_units(const TreeArgs& a, int n, int chunks, const int4* items, const short* list, float (&so)[kWarps][kMaxCols][33],
                                            float (&sm)[kWarps][3][32])
 {
     const int warp = threadIdx.x >> 5, units = n * chunks * (D / kCols);
@@ -118,7 +115,7 @@ __device__ __forceinline__ void join_units(const TreeArgs& a, int n, int chunks,
         const int u = u0 + warp / group * (int)gridDim.x;
         const bool has = u < units;
         const int c0 = has ? list[u / (chunks * (D / kCols))] : 0;
-        const int4 item = has ? a.border[c0] : make_int4(0, 0, 0, 0);
+        const int4 item = has ? items[u / (chunks * (D / kCols))] : make_int4(0, 0, 0, 0);
         join_unit<D, kCols, U>(a, has, c0, item, u / (D / kCols) % chunks * 32, u % (D / kCols) * kCols, group, warp % group, so, sm);
         __syncthreads();
     }
@@ -129,12 +126,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) tree_join_kernel(const TreeArg
 {
     __shared__ float so[kWarps][kMaxCols][33];
     __shared__ float sm[kWarps][3][32];
+    __shared__ int4 items[kTreeMaxCtas];
     __shared__ short list[kTreeMaxCtas];
     __shared__ int count[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int chunks = (tree_item_rows(a) + 31) / 32;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // for the first launch's results
-    // sequences without tokens, and lengths outside their ranges: a turn for every block
+    // sequences without tokens, and lengths outside their ranges: a turn for every block (nothing here depends on the
+    // first launch, which leaves their rows alone)
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         const TreeSeq s = tree_seq(a, b);
         if (s.bad && threadIdx.x == 0) atomicOr(a.status, kStatusRange);
@@ -148,26 +146,38 @@ __global__ void __launch_bounds__(kWarps * 32, 2) tree_join_kernel(const TreeArg
         }
         for (long long e = threadIdx.x; e < rows; e += blockDim.x) a.lse[row0 + e] = -INFINITY;
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for the first launch's results
     // the borders that an item goes over, in order
+    constexpr int kRounds = (kTreeMaxCtas + kWarps * 32 - 1) / (kWarps * 32);
+    int4 mine[kRounds];
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+        const int c = k * kWarps * 32 + (int)threadIdx.x;
+        mine[k] = c < a.ctas ? a.border[c] : make_int4(-1, 0, 0, 0);
+    }
     int n = 0;
-    for (int c = 0; c < a.ctas; c += kWarps * 32) {
-        const int mine = c + (int)threadIdx.x;
-        const bool has = mine < a.ctas && a.border[mine].x >= 0;
-        const unsigned votes = __ballot_sync(0xffffffffu, has);
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+        if (k * kWarps * 32 >= a.ctas) break;
+        const unsigned votes = __ballot_sync(0xffffffffu, mine[k].x >= 0);
         if (lane == 0) count[warp] = __popc(votes);
         __syncthreads();
         int before = n;
-        for (int k = 0; k < kWarps; ++k) {
-            if (k < warp) before += count[k];
-            n += count[k];
+        for (int j = 0; j < kWarps; ++j) {
+            if (j < warp) before += count[j];
+            n += count[j];
         }
-        if (has) list[before + __popc(votes & ((1u << lane) - 1u))] = (short)mine;
+        if (mine[k].x >= 0) {
+            const int at = before + __popc(votes & ((1u << lane) - 1u));
+            items[at] = mine[k];
+            list[at] = (short)(k * kWarps * 32 + (int)threadIdx.x);
+        }
         __syncthreads();
     }
     if (n * chunks * (D / 4) <= (int)gridDim.x)
-        join_units<D, 4, 8>(a, n, chunks, list, so, sm);
+        join_units<D, 4, 8>(a, n, chunks, items, list, so, sm);
     else
-        join_units<D, 16, 3>(a, n, chunks, list, so, sm);
+        join_units<D, 16, 3>(a, n, chunks, items, list, so, sm);
 }
 
 }  // namespace
