@@ -421,15 +421,15 @@ __device__ __forceinline__ uint32_t qk_offset(int row, int c16)  // 16-byte chun
 // An item's queries as hi and lo e4m3 values with the row's scale, by the softmax warps; kHd / 8 lanes share a row.  Rows
 // past the kv head's keep what they hold: it reaches no row of S that is read.
 template <int kNq>
-__device__ __forceinline__ void split_queries(const TreeArgs& a, uint8_t* smem, const TreeWalk& w, uint32_t item)
+__device__ __forceinline__ void split_queries(const TreeArgs& a, uint8_t* smem, int b, int g, int r, uint32_t item)
 {
     using C = Cfg<true, kNq>;
     constexpr int kLanes = kHd / 8, kStep = 256 / kLanes, kU = 8;
     const int tid = threadIdx.x, c = tid % kLanes;
-    const int rows = a.R - w.r * a.rt < kNq * 128 ? a.R - w.r * a.rt : kNq * 128;
+    const int rows = a.R - r * a.rt < kNq * 128 ? a.R - r * a.rt : kNq * 128;
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                      (((long long)w.b * a.Hkv + w.g) * a.R + (long long)w.r * a.rt) * kHd) + c;
-    const int rows_up = (rows + kStep * kU - 1) / (kStep * kU) * (kStep * kU);  // the same for a whole warp
+                                                      (((long long)b * a.Hkv + g) * a.R + (long long)r * a.rt) * kHd) + c;
+    const int rows_up = (rows + kStep - 1) / kStep * kStep;  // the same for a whole warp
     float* scale = reinterpret_cast<float*>(smem + C::kQs) + (item & 1) * kNq * 128;
 #pragma unroll 1
     for (int x0 = tid / kLanes; x0 < rows_up; x0 += kStep * kU) {
@@ -442,6 +442,7 @@ __device__ __forceinline__ void split_queries(const TreeArgs& a, uint8_t* smem, 
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int x = x0 + u * kStep;
+            if (x >= rows_up) break;
             const uint32_t p[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
             uint32_t big = 0;  // bits of the largest magnitude: bf16 in the upper half, ordered as integers
 #pragma unroll
@@ -672,19 +673,19 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
     uint32_t jobs = 0, tiles = 0, item = 0;  // this warpgroup's jobs, all tiles, items so far
     uint32_t pairs = 0;                      // items that both warpgroups had jobs of (kNq == 1)
 
+    auto split = [&](int b, int g, int r, uint32_t it) {
+        split_queries<kNq>(a, smem, b, g, r, it);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::bQFull));
+    };
+    if constexpr (kE4) split(w.b, w.g, w.r, 0);
     do {
         const int x = w.r * a.rt + (kNq == 2 ? wg * 128 : 0) + rw;  // query row of the kv head
         const int tq = x % a.T;
         const bool live = x < a.R && tq < w.s.cnt;
         const bool any_live = __any_sync(0xffffffffu, live);
         const int n = w.t1 - w.t0;
-        if constexpr (kE4) {
-            if (item > 0 && !warp_wait(bar(C::bQEmpty), (item - 1) & 1, ctl)) return;
-            split_queries<kNq>(a, smem, w, item);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::bQFull));
-        }
         float m_run = -INFINITY, l_run = 0.f, c_run = 0.f, sl2 = a.scale_log2;
         bool first = true;
         for (int i = kNq == 1 ? wg : 0; i < n; i += kNq == 1 ? 2 : 1) {
@@ -818,6 +819,14 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::bP + wg));
             first = false;
+        }
+
+        if constexpr (kE4) {  // the next item's queries, while the last products run
+            TreeWalk next = w;
+            if (next.next(a)) {
+                if (!warp_wait(bar(C::bQEmpty), item & 1, ctl)) return;
+                split(next.b, next.g, next.r, item + 1);
+            }
         }
 
         // the item's rows: O of both warpgroups (kNq == 1), or of this one
