@@ -7,6 +7,7 @@ call raises RingAttnError (there is no fallback of any kind).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -960,7 +961,12 @@ def cache_read(cache, rows, row0=0, dtype=torch.bfloat16, k=None, v=None, stream
 
 
 def tree_workspace_size(B, H, Hkv, T, d, cap, dtype, cache_dtype):
-    return int(library().ring_attn_tree_fwd_workspace_size(B, H, Hkv, T, d, cap, _dtype_code(dtype), _cache_code(cache_dtype)))
+    return _tree_workspace(B, H, Hkv, T, d, cap, _dtype_code(dtype), _cache_code(cache_dtype))
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_workspace(*sizes):
+    return int(library().ring_attn_tree_fwd_workspace_size(*sizes))
 
 
 def tree_fwd(q, cache, lens, mask=None, ntok=None, out_dtype=None, out=None, lse=None, workspace=None, stream=None):
@@ -986,7 +992,7 @@ def tree_fwd(q, cache, lens, mask=None, ntok=None, out_dtype=None, out=None, lse
     out, op = _output(out, "out", dev, q.shape, out_dtype)
     lse, lp = _output(lse, "lse", dev, (B, H, T), torch.float32)
     lib = library()
-    need = lib.ring_attn_tree_fwd_workspace_size(B, H, Hkv, T, d, cap, code, kind)
+    need = _tree_workspace(B, H, Hkv, T, d, cap, code, kind)
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
     else:
