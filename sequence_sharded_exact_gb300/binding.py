@@ -8,6 +8,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -27,6 +29,7 @@ RA_E4M3 = 2
 
 _lock = threading.Lock()
 _lib = None
+_calls = None
 
 EXPORTS = (
     "ring_attn_fwd", "ring_attn_ring_step_fwd", "ring_attn_lse_merge", "ring_attn_fwd_stepwise",
@@ -155,8 +158,27 @@ def library():
                                                      "ring_attn_device_status",
                                                      "ring_attn_abi_version"):
                 f.restype = ctypes.c_int
+        _load_calls(lib)
         _lib = lib
         return lib
+
+
+def _load_calls(lib):
+    """The compiled form of the calls below that have one (csrc/calls.cpp), if it was built for this Python and torch."""
+    global _calls
+    from .build_lib import calls_path
+
+    path = calls_path()
+    if not os.path.exists(path):
+        return
+    name = __package__ + "._calls"
+    loader = importlib.machinery.ExtensionFileLoader(name, path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(lib, "ring_attn_" + f), ctypes.c_void_p).value for f in (
+        "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size", "cache_write", "cache_read", "tree_fwd",
+        "tree_fwd_workspace_size")))
+    _calls = module
 
 
 def _check(status):
@@ -731,8 +753,10 @@ def block_rope(x, n_shards, shard, layout="zigzag", base=10000.0, inverse=False,
 # ------------------------------------------------------------------------------------------------
 # Norms and rotation of queries and keys, the key/value cache and the attention over it
 # ------------------------------------------------------------------------------------------------
-# The calls of a serving step take a few microseconds on the GPU, so their checks are kept cheap: one expression
-# per tensor on the way that passes, and the checks that name what is wrong only where it fails.
+# The calls of a serving step take a few microseconds on the GPU, so on the current stream they go through their compiled
+# form (csrc/calls.cpp: 24 -> 10 us for the attention over a short cache), which answers None to whatever it does not take:
+# then, and where it was not built, the Python form runs, which says what is wrong.  Its checks are kept cheap too: one
+# expression per tensor on the way that passes, and the checks that name what is wrong only where it fails.
 _Strides = ctypes.c_longlong * 3
 _E4M3 = torch.float8_e4m3fn
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
@@ -848,6 +872,10 @@ def qk_norm_rope(q, k, wq, wk, n_shards=1, layout="contiguous", base=10000.0, ep
     layout's over n_shards shards, shard `shard`'s of them, or positions [B, rows] int32.  q and k may be
     slices of a fused projection (rows contiguous, on 16-byte boundaries).  Returns (q_out, k_out), contiguous,
     in q's dtype; q_out may be q and k_out may be k, where those are contiguous."""
+    if _calls is not None and stream is None:
+        done = _calls.qk_norm_rope(q, k, wq, wk, n_shards, layout, base, eps, shard, positions, q_out, k_out)
+        if done is not None:
+            return done
     head, tail = _norm_rope_args(q, k, wq, wk, n_shards, layout, base, eps, shard, positions)
     dev, dt = q.device, q.dtype
     q_out, qo = _output(q_out, "q_out", dev, q.shape, dt)
@@ -861,6 +889,11 @@ def qk_norm_rope_bwd(q, k, wq, wk, dq_out, dk_out, n_shards=1, layout="contiguou
                      positions=None, dq=None, dk=None, workspace=None, stream=None):
     """ring_attn_qk_norm_rope_bwd: the gradients of qk_norm_rope's inputs from those of its outputs (contiguous).
     Returns (dq, dk) in q's dtype, contiguous (dq may be dq_out, dk may be dk_out), and (dwq, dwk) [d] float32."""
+    if _calls is not None and stream is None:
+        done = _calls.qk_norm_rope_bwd(q, k, wq, wk, dq_out, dk_out, n_shards, layout, base, eps, shard, positions, dq, dk,
+                                       workspace)
+        if done is not None:
+            return done
     head, tail = _norm_rope_args(q, k, wq, wk, n_shards, layout, base, eps, shard, positions)
     dev, dt, d = q.device, q.dtype, q.shape[3]
     gq, gk = _fits(dq_out, "dq_out", dev, q.shape, dt), _fits(dk_out, "dk_out", dev, k.shape, dt)
@@ -926,6 +959,10 @@ def cache_write(cache, k, v, lens=None, ntok=None, stream=None):
     lens[b] + t (t without lens) of the cache, quantised there if it is float8_e4m3fn.  lens, ntok: int32 [B] on
     the device.  k and v may be slices of a fused projection.  Rows outside the cache are not written (the
     device status word then has the range bit).  Returns the cache."""
+    if _calls is not None and stream is None:
+        done = _calls.cache_write(cache, k, v, lens, ntok)
+        if done is not None:
+            return cache
     shape, _, code = _dims4(k, v, "k and v")
     B, Hkv, T, d = shape
     dev, dt = k.device, k.dtype
@@ -942,6 +979,10 @@ def cache_write(cache, k, v, lens=None, ntok=None, stream=None):
 def cache_read(cache, rows, row0=0, dtype=torch.bfloat16, k=None, v=None, stream=None):
     """ring_attn_cache_read: rows [row0, row0 + rows) of every sequence and kv head as (k, v) [B, Hkv, rows, d] in
     dtype: the values the cache stands for."""
+    if _calls is not None and stream is None:
+        done = _calls.cache_read(cache, rows, row0, dtype, k, v)
+        if done is not None:
+            return done
     if not isinstance(cache.k, torch.Tensor) or cache.k.dim() != 4:
         raise ValueError("the cache's k must be a [B, Hkv, cap, d] tensor")
     B, Hkv, _, d = cache.k.shape
@@ -975,6 +1016,10 @@ def tree_fwd(q, cache, lens, mask=None, ntok=None, out_dtype=None, out=None, lse
     [0, lens[b]), and the step's tokens j < ntok[b] with mask[b, t, j] ([B, T, T] or [T, T] bool; without a mask
     j <= t).  lens, ntok: int32 [B] on the device.  Returns (out [B, H, T, d] in out_dtype -- q's, or float32 --
     and lse [B, H, T] float32); a row that sees nothing, and tokens t >= ntok[b], have 0 and -infinity."""
+    if _calls is not None and stream is None:
+        done = _calls.tree_fwd(q, cache, lens, mask, ntok, out_dtype, out, lse, workspace)
+        if done is not None:
+            return done
     (B, H, T, d), kshape, code = _dims4(q, cache.k, "q and the cache's k")
     Hkv, dev, dt = kshape[1], q.device, q.dtype
     qp = _fits(q, "q", dev, q.shape, dt)

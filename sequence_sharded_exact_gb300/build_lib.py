@@ -1,4 +1,5 @@
-"""Builds libringattn.so in-tree: every csrc/*.cu compiled for sm_103a in parallel, then linked.
+"""Builds libringattn.so in-tree: every csrc/*.cu compiled for sm_103a in parallel, then linked; and beside it the
+binding's compiled calls (csrc/calls.cpp, against the installed torch).
 
 Usage: python -m sequence_sharded_exact_gb300.build_lib [--force]
 The CUDA runtime is linked statically and the driver API is reached through the runtime's entry
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -35,7 +37,7 @@ def _sources():
 
 
 def _deps():
-    return [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "ringattn.h"),
+    return [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != "calls.cpp"] + [os.path.join(INCLUDE, "ringattn.h"),
                                                               os.path.abspath(__file__)]
 
 
@@ -46,11 +48,39 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def calls_path() -> str:
+    """Where the compiled calls for this Python and torch lie."""
+    import torch
+
+    return os.path.join(HERE, f"_calls-py{sys.version_info[0]}.{sys.version_info[1]}-torch{torch.__version__}.so")
+
+
+def build_calls(nvcc, force: bool = False) -> str:
+    import torch
+
+    target, src = calls_path(), os.path.join(CSRC, "calls.cpp")
+    if not force and not _stale(target, [src, os.path.join(INCLUDE, "ringattn.h"), os.path.abspath(__file__)]):
+        return target
+    root = os.path.dirname(torch.__file__)
+    include = [os.path.join(root, "include"), sysconfig.get_paths()["include"],
+               os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")]
+    tmp = target + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in include), src, "-o", tmp,
+           "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling calls.cpp failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, target)
+    return target
+
+
 def build(force: bool = False, verbose: bool = False, extra=None) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     deps = _deps()
     if not force and not _stale(LIB, deps):
+        build_calls(nvcc)
         return LIB
     flags = NVCC_FLAGS + list(extra or [])
 
@@ -65,8 +95,10 @@ def build(force: bool = False, verbose: bool = False, extra=None) -> str:
         return obj
 
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        calls = ex.submit(build_calls, nvcc, force)
         objs = list(ex.map(compile_one, srcs))
+        calls.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -195,3 +195,19 @@ def test_device_tensors_that_do_not_fit_are_refused():
 ])
 def test_row_counts_that_an_int_could_not_step_over(lib, call, kw):
     assert {"write": _write, "read": _read, "tree": _tree}[call](lib, **kw) == UNS
+
+
+def test_the_compiled_calls_are_there_and_leave_what_they_do_not_take(lib):
+    """Built beside the library for this Python and torch; host tensors and odd arguments are left to the Python form."""
+    calls = binding._calls
+    assert calls is not None
+    x = torch.zeros(1, 1, 1, 64)
+    cache = binding.KVCache(x, x)
+    assert calls.tree_fwd(x, cache, None, None, None, None, None, None, None) is None
+    assert calls.cache_write(cache, x, x, None, None) is None
+    assert calls.cache_read(cache, 1, 0, torch.float32, None, None) is None
+    assert calls.cache_read(None, "1", 0, 3, None, None) is None
+    assert calls.qk_norm_rope(x, x, x, x, 1, "zigzag", 1.0, 0.0, None, None, None, None) is None
+    assert calls.qk_norm_rope_bwd(1, None, x, x, x, x, 1, 2, 1.0, 0.0, None, None, None, None, None) is None
+    with pytest.raises(TypeError):
+        calls.tree_fwd(x)
