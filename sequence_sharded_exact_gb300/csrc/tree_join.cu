@@ -10,7 +10,7 @@
 // unit has 16 columns and three partials are loaded at a time, by as few warps as keep all of them busy: four,
 // two or one.  (One warp per row, walking its partials one by one: decoding over 19 partials took 15 us of 100;
 // eight warps per unit whatever the number: 18.5 us in place of 13 for 64 items of 128 rows over 152 CTAs,
-// 15.5 in place of 11.5 for 16 items of 256.  Of those 13 us about 4 are the launch and its first loads.)
+// 15.5 in place of 11.5 for 16 items of 256.)
 #include <cuda_bf16.h>
 
 #include "ra_internal.h"
