@@ -11,12 +11,13 @@
 // takes e = 120, under which 448 * 2^e reads back as infinity.
 //
 // What bounds it: each element is read once and written once.  d / 8 lanes hold a row (8 elements a
-// lane: 16 or 32 bytes in, 8 out, or the reverse), its largest magnitude is a shuffle reduction in
-// that group, and kUnroll rows are loaded before the first is used.
+// lane: 16 or 32 bytes in, 8 out; read back 16 elements), its largest magnitude is a shuffle
+// reduction in that group, and kUnroll rows are loaded before the first is used.
 //
 // Measured, 131072 rows of 8 kv heads of 128 between bf16 and e4m3 (0.81 GB): written in 123 us (6.55 TB/s, 0.96 of the
-// copy rate), read back in 134 us (6.0 TB/s, 0.89).  With one division per row, in a grid over all rows, it
-// was 236 and 152 us.  Four rows ahead on reading back, in place of eight: 138 us.
+// copy rate), read back in 128 us (6.3 TB/s, 0.93).  With one division per row, in a grid over all rows, it
+// was 236 and 152 us.  Reading back with 8 bytes a lane and row: 134 us; with two or eight rows ahead, in place of four:
+// 140, 130.
 #include <cuda_bf16.h>
 
 #include "ra_internal.h"
@@ -27,7 +28,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;      // rows per group and turn, written
-constexpr int kUnrollRead = 8;  // and read back: 8 bytes a lane and row come in
+constexpr int kUnrollRead = 4;  // and read back: 16 bytes a lane and row come in
 
 template <typename T>
 struct Eight {  // eight consecutive elements of T
@@ -148,60 +149,89 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteArgs a
     }
 }
 
+// 32 bytes at p, in one store where p allows it (`wide`: a 32-byte boundary).
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8], bool wide)
+{
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                     "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+
 struct ReadArgs {
+    bool wide;                   // the outputs lie on 32-byte boundaries
     int heads, cap, row0, rows;  // heads of all sequences
     const void *k, *v;
     const uint8_t *k_exp, *v_exp;
     void *k_out, *v_out;
 };
 
+// Quantised rows: 16 elements a lane, 16 bytes in and 32 (bf16) or 64 out.  Rows in the outputs' dtype are copied, 16
+// bytes a lane.
 template <typename T, int D, bool QUANT>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a)
 {
-    constexpr int LPR = D / 8, kGroups = kThreads / LPR;
+    constexpr int E = QUANT ? 16 : 16 / sizeof(T), LPR = D / E, kGroups = kThreads / LPR;
     const int ch = threadIdx.x % LPR, grp = threadIdx.x / LPR;
     const bool is_v = blockIdx.z != 0;
     for (int bh = blockIdx.y; bh < a.heads; bh += gridDim.y) {
         const long long in0 = (long long)bh * a.cap + a.row0, out0 = (long long)bh * a.rows;
         const uint8_t* exps = is_v ? a.v_exp : a.k_exp;
-        T* out = static_cast<T*>(is_v ? a.v_out : a.k_out) + out0 * D + ch * 8;
+        const uint8_t* in = static_cast<const uint8_t*>(is_v ? a.v : a.k) + ch * 16;
+        T* out = static_cast<T*>(is_v ? a.v_out : a.k_out) + out0 * D + ch * E;
         for (int t0 = blockIdx.x * (kGroups * kUnrollRead) + grp; t0 < a.rows; t0 += gridDim.x * (kGroups * kUnrollRead)) {
-            Eight<T> x[kUnrollRead];
-            uint2 w[kUnrollRead];
+            uint4 w[kUnrollRead];
             uint32_t e[kUnrollRead];
 #pragma unroll
             for (int u = 0; u < kUnrollRead; ++u) {
                 if (t0 + u * kGroups >= a.rows) break;
                 const long long src = in0 + t0 + u * kGroups;
-                if constexpr (QUANT) {
-                    w[u] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(is_v ? a.v : a.k) + src * D + ch * 8);
-                    e[u] = exps[src];
-                } else {
-                    x[u].load(static_cast<const T*>(is_v ? a.v : a.k) + src * D + ch * 8);
-                }
+                w[u] = *reinterpret_cast<const uint4*>(in + src * (D / E * 16));
+                if constexpr (QUANT) e[u] = exps[src];
             }
 #pragma unroll
             for (int u = 0; u < kUnrollRead; ++u) {
                 if (t0 + u * kGroups >= a.rows) break;
+                T* dst = out + (long long)(t0 + u * kGroups) * D;
                 if constexpr (QUANT) {
                     const float up = __uint_as_float(e[u] << 23);  // 2^(byte - 127), byte 1 .. 247
-                    float f[8];
-                    e4m3x4_to_float(w[u].x, f[0], f[1], f[2], f[3]);
-                    e4m3x4_to_float(w[u].y, f[4], f[5], f[6], f[7]);
+                    const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+                    uint32_t o[4 * sizeof(T)];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] *= up;
-                    x[u].set(f);
+                    for (int j = 0; j < 4; ++j) {
+                        float f[4];
+                        e4m3x4_to_float(x[j], f[0], f[1], f[2], f[3]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[i] *= up;
+                        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[4 * j + i] = __float_as_uint(f[i]);
+                        } else {
+                            o[2 * j] = pack_bf16x2(f[0], f[1]);
+                            o[2 * j + 1] = pack_bf16x2(f[2], f[3]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+                        const uint32_t part[8] = {o[8 * i], o[8 * i + 1], o[8 * i + 2], o[8 * i + 3], o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]};
+                        store32(reinterpret_cast<uint8_t*>(dst) + 32 * i, part, a.wide);
+                    }
+                } else {
+                    *reinterpret_cast<uint4*>(dst) = w[u];
                 }
-                x[u].store(out + (long long)(t0 + u * kGroups) * D);
             }
         }
     }
 }
 
 // Blocks for `rows` rows of every head: enough for all of them, at most eight per SM over k and v and the heads.
-dim3 cache_grid(long long heads, long long rows, int d, int unroll)
+dim3 cache_grid(long long heads, long long rows, int lanes, int unroll)
 {
-    const long long per = (long long)(kThreads / (d / 8)) * unroll;
+    const long long per = (long long)(kThreads / lanes) * unroll;
     const long long y = heads < 65535 ? heads : 65535;
     long long most = (long long)device_sm_count() * 8 / (2 * y);
     if (most < 1) most = 1;
@@ -251,7 +281,7 @@ cudaError_t launch_cache_write(const Cache& c, int T, const void* k, const long 
     a.ntok = ntok;
     a.status = status;
     const bool quant = c.dtype != dtype;
-    const dim3 grid = cache_grid((long long)c.B * c.Hkv, T, c.d, kUnroll);
+    const dim3 grid = cache_grid((long long)c.B * c.Hkv, T, c.d / 8, kUnroll);
     if (dtype == 1)
         c.d == 128 ? write_as<__nv_bfloat16, 128>(a, quant, grid, s) : write_as<__nv_bfloat16, 64>(a, quant, grid, s);
     else
@@ -262,6 +292,7 @@ cudaError_t launch_cache_write(const Cache& c, int T, const void* k, const long 
 cudaError_t launch_cache_read(const Cache& c, int row0, int rows, void* k, void* v, int dtype, cudaStream_t s)
 {
     ReadArgs a;
+    a.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31) == 0;
     a.heads = c.B * c.Hkv;
     a.cap = c.cap;
     a.row0 = row0;
@@ -273,7 +304,7 @@ cudaError_t launch_cache_read(const Cache& c, int row0, int rows, void* k, void*
     a.k_out = k;
     a.v_out = v;
     const bool quant = c.dtype != dtype;
-    const dim3 grid = cache_grid((long long)c.B * c.Hkv, rows, c.d, kUnrollRead);
+    const dim3 grid = cache_grid((long long)c.B * c.Hkv, rows, quant || dtype == 1 ? c.d / (quant ? 16 : 8) : c.d / 4, kUnrollRead);
     if (dtype == 1)
         c.d == 128 ? read_as<__nv_bfloat16, 128>(a, quant, grid, s) : read_as<__nv_bfloat16, 64>(a, quant, grid, s);
     else
