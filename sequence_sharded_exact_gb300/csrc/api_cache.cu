@@ -55,6 +55,7 @@ ra_status norm_rope_impl(Problem p, NormRope n, const long long* qs, const long 
 {
     ra_status st = check_problem(p);
     if (st != RA_OK) return st;
+    if ((long long)p.H + p.Hkv >= (1LL << 30)) return fail(RA_ERR_UNSUPPORTED, "too many heads");
     if (n.shard < -1 || n.shard >= p.n) return fail(RA_ERR_INVALID_ARG, "shard %d outside [-1, n_shards)", n.shard);
     if (!(n.base > 0.0) || !isfinite(n.base)) return fail(RA_ERR_INVALID_ARG, "base must be positive and finite");
     if (!(n.eps >= 0.0) || !isfinite(n.eps)) return fail(RA_ERR_INVALID_ARG, "eps must be >= 0 and finite");

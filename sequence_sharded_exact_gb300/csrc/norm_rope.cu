@@ -14,15 +14,17 @@
 // lanes per row, so a row's sums are shuffles inside the group that holds it.  A group owns one
 // (batch, position) and walks heads: the angles (64-bit fixed-point turns, as in rope.cu) are
 // computed once for all the heads it walks, which counts: with 8 heads per group in place of 40 the
-// forward of 64K positions took 258 us in place of 214.  Loads of four heads are issued before the
+// forward of 64K positions took 258 us in place of 214 (as it was then).  Loads of four heads are issued before the
 // first is used (two or eight: 240, 232 us).  All sums are float32; the output is rounded once.
 //
 // With few tokens one group per position would leave most SMs idle, so the heads of a position are
 // then split over several groups, which repeat the angles.
 //
-// Measured, 64K positions of 32 + 8 heads of 128 in bf16: forward 214 us (6.27 TB/s, 0.92 of the copy
-// rate), backward 330 us (6.10 TB/s, 0.90).  What is left are the shuffles and the products between
-// loads: more heads in flight cost registers and so the other blocks that hide them.
+// Measured, 64K positions of 32 + 8 heads of 128 in bf16: forward 208 us (6.45 TB/s, 0.95 of the copy
+// rate), backward 320 us (6.30 TB/s, 0.93).  What is left are the shuffles and the products between
+// loads: more heads in flight cost registers and so the other blocks that hide them.  32 bytes a lane in
+// place of 16 took the forward 6 us further and the backward 14 back, and would need rows on 32-byte
+// boundaries.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -122,16 +124,25 @@ struct Item {
     long long p;
 };
 
+// kFew: the heads of a position are shared out, and all counts fit 32 bits (a 64-bit division is a hundred instructions:
+// of 5.4 us that 128 tokens took 0.6).
+template <bool kFew>
 __device__ __forceinline__ Item item_of(const NormRopeArgs& a, long long idx)
 {
     Item it;
-    it.r = (int)(idx % a.rows);
-    const long long rest = idx / a.rows;
-    const int c = (int)(rest % a.splits);
-    it.b = (int)(rest / a.splits);
-    const int heads = a.H + a.Hkv;
-    it.h0 = (int)((long long)c * heads / a.splits);
-    it.h1 = (int)((long long)(c + 1) * heads / a.splits);
+    if constexpr (kFew) {
+        const unsigned i = (unsigned)idx, rows = (unsigned)a.rows, n = (unsigned)a.splits, heads = (unsigned)(a.H + a.Hkv);
+        const unsigned rest = i / rows, b = rest / n, c = rest - b * n;
+        it.r = (int)(i - rest * rows);
+        it.b = (int)b;
+        it.h0 = (int)(c * heads / n);
+        it.h1 = (int)((c + 1) * heads / n);
+    } else {
+        it.r = (int)(idx % a.rows);
+        it.b = (int)(idx / a.rows);
+        it.h0 = 0;
+        it.h1 = a.H + a.Hkv;
+    }
     it.p = a.pos ? a.pos[(long long)it.b * a.rows + it.r] : natural_position(a.geo, it.r + a.row_off);
     return it;
 }
@@ -166,7 +177,7 @@ __device__ __forceinline__ void fwd_heads(const T* x, long long xs, T* y, long l
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kFew>
 __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const NormRopeArgs a)
 {
     constexpr int V = Pack<T>::kElems, LPR = D / V, U = 4;
@@ -181,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const NormRopeAr
         wk[e] = a.wk[ch * V + e];
     }
     for (long long idx = (long long)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR; idx < total; idx += step) {
-        const Item it = item_of(a, idx);
+        const Item it = item_of<kFew>(a, idx);
         float c[V / 2], s[V / 2];
         angles<V / 2>(a, ch, it.p, c, s);
         const long long ys = (long long)a.rows * D;
@@ -249,11 +260,12 @@ __device__ __forceinline__ void bwd_heads(const T* x, long long xs, const T* dy,
 
 // dw is summed per lane over the rows it meets, then over the block's groups, in a fixed order;
 // norm_rope_dw_kernel adds the blocks' sums in block order, so the result does not vary from run to run.
-template <typename T, int D>
+template <typename T, int D, bool kFew>
 __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_rope_bwd_kernel(const NormRopeArgs a)
 {
     constexpr int V = Pack<T>::kElems, LPR = D / V, U = 4, kGroups = kThreads / LPR;
     __shared__ float sums[kGroups][2 * D];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int ch = threadIdx.x % LPR, grp = threadIdx.x / LPR;
     const unsigned mask = group_mask<LPR>();
     const long long total = (long long)a.B * a.rows * a.splits;
@@ -266,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_rope_bwd_kerne
         dq[e] = dk[e] = 0.f;
     }
     for (long long idx = (long long)blockIdx.x * kGroups + grp; idx < total; idx += step) {
-        const Item it = item_of(a, idx);
+        const Item it = item_of<kFew>(a, idx);
         float c[V / 2], s[V / 2];
         angles<V / 2>(a, ch, it.p, c, s);
         const long long ys = (long long)a.rows * D;
@@ -304,6 +316,7 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* partial
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + tx;  // d is 64 or 128: 2 d columns in whole warps
     float t = 0.f;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for the partial sums
 #pragma unroll 4
     for (int b = ty; b < blocks; b += 32) t += partial[(long long)b * 2 * d + col];
     part[ty][tx] = t;
@@ -328,22 +341,39 @@ cudaError_t launch(NormRopeArgs& a, bool backward, float* dwq, float* dwk, cudaS
     const long long want = (long long)device_sm_count() * 1024 / LPR;
     long long splits = (want + tokens - 1) / tokens;
     if (splits > a.H + a.Hkv) splits = a.H + a.Hkv;
-    a.splits = splits < 1 ? 1 : (int)splits;
+    const long long heads = (long long)a.H + a.Hkv;
+    const bool few = splits > 1 && heads * heads <= 0x7fffffffLL && tokens * splits <= 0x7fffffffLL;
+    a.splits = few ? (int)splits : 1;
     long long grid = (tokens * a.splits + kGroups - 1) / kGroups;
     if (!backward) {  // a block per group of positions: the last ones fill the SMs evenly
         if (grid > 0x7fffffffLL) grid = 0x7fffffffLL;
-        norm_rope_kernel<T, D><<<(unsigned)grid, kThreads, 0, s>>>(a);
+        if (few)
+            norm_rope_kernel<T, D, true><<<(unsigned)grid, kThreads, 0, s>>>(a);
+        else
+            norm_rope_kernel<T, D, false><<<(unsigned)grid, kThreads, 0, s>>>(a);
         return cudaGetLastError();
     }
     // as many blocks as are resident, which take the positions in turns: their dw leave a partial sum each
     const long long most = (long long)device_sm_count() * kBwdBlocksPerSm;
     if (grid > most) grid = most;
     if (grid > kNormRopeBwdBlocks) grid = kNormRopeBwdBlocks;
-    norm_rope_bwd_kernel<T, D><<<(unsigned)grid, kThreads, 0, s>>>(a);
+    if (few)
+        norm_rope_bwd_kernel<T, D, true><<<(unsigned)grid, kThreads, 0, s>>>(a);
+    else
+        norm_rope_bwd_kernel<T, D, false><<<(unsigned)grid, kThreads, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    norm_rope_dw_kernel<<<2 * D / 32, 1024, 0, s>>>(a.partial, (int)grid, D, dwq, dwk);
-    return cudaGetLastError();
+    // starts while the first launch runs and waits for its results in the kernel
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * D / 32);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, static_cast<const float*>(a.partial), (int)grid, D, dwq, dwk);
 }
 
 }  // namespace
