@@ -15,7 +15,8 @@
 //     query sees: eleven bits down to 2^-21 of weight 1 at E, weight and scale together.  The sum l takes p itself.
 //     The reference of p follows the row maximum only when that grows by more than 2^8, so O is seldom rescaled.
 //   * A CTA's eight warps take 16 rows of every tile each, with rings of their own that the TMA fills; m, l, E and O are
-//     a warp's own until the item's end, where they meet in the rings' memory, in warp order.
+//     a warp's own until the item's end, where they meet in shared memory, in warp order.  The next item's first rows
+//     and its queries are on their way meanwhile.
 //
 // What bounds it: the memory, nearly.  A tile of 128 rows of 8 kv heads' e4m3 cache (d = 128) costs each of 152 SMs
 // 0.88 us, 5.6 TB/s (tree_tc_body.cuh: 1.46), one token over 131072 rows 56 us with both launches (it: 91).  A group of 16
@@ -46,11 +47,11 @@ template <int D>
 struct Cfg {
     static constexpr uint32_t kHalf = kKeys * D;                          // bytes of 16 rows
     static constexpr uint32_t kRings = kWarps * kStages * 2 * kHalf;      // [warps][stages][k, v]
-    static constexpr uint32_t kMl = kRings;                               // [warps][8] m, l, E's bits, 0
-    static constexpr uint32_t kBar = kMl + kWarps * 8 * 16;
+    static constexpr uint32_t kX = kRings;                                // exchange: [warps][D / 16][lanes] float4
+    static constexpr uint32_t kMl = kX + kWarps * 32 * D;                 // [2 items][warps][8] m, l, E's bits, 0
+    static constexpr uint32_t kBar = kMl + 2 * kWarps * 8 * 16;
     static constexpr uint32_t kAbort = kBar + kWarps * kStages * 8;
     static constexpr uint32_t kSmem = kAbort + 8 + 1024;  // slack for the 1024-byte alignment of the base
-    static_assert(kWarps * 32 * D <= kRings, "the warps' O meet in the rings");
     static_assert(kSmem * kTreeMmaCtasPerSm <= 229376, "shared memory");
 };
 
@@ -131,18 +132,24 @@ __device__ __forceinline__ uint32_t at16(int r, int c)
     return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-// Query row x as the operand of S^T's k steps, two registers each: elements (D / 4) t + 4 s .. + 3 of step s.  Returns the
-// row's scale times the scores'.
+// Query row x of a kv head, elements (D / 4) t .. of thread t of its quad.
 template <int D>
-__device__ __forceinline__ float load_query(const TreeArgs& a, long long head, int x, uint32_t (&f)[D / 8])
+__device__ __forceinline__ void load_query(const TreeArgs& a, long long head, int x, uint32_t (&f)[D / 8])
 {
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (head * a.R + x) * D) + (threadIdx.x & 3) * (D / 32);
-    uint32_t big = 0;  // bits of the largest magnitude: bf16 in the upper half, ordered as integers
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
         const uint4 v = x < a.R ? src[c] : make_uint4(0, 0, 0, 0);
         f[4 * c] = v.x, f[4 * c + 1] = v.y, f[4 * c + 2] = v.z, f[4 * c + 3] = v.w;
     }
+}
+
+// It as the operand of S^T's k steps, two registers each: elements (D / 4) t + 4 s .. + 3 of step s.  Returns the row's
+// scale times the scores'.
+template <int D>
+__device__ __forceinline__ float convert_query(const TreeArgs& a, uint32_t (&f)[D / 8])
+{
+    uint32_t big = 0;  // bits of the largest magnitude: bf16 in the upper half, ordered as integers
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) big = max(big, max(f[i] << 16 & 0x7fff0000u, f[i] & 0x7fff0000u));
     big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
@@ -184,34 +191,39 @@ __global__ void __launch_bounds__(kThreads, kTreeMmaCtasPerSm) tree_mma_kernel(c
     int4 border = make_int4(-1, 0, 0, 0);
     uint32_t used = 0, sent = 0;  // of the ring (sent: lane 0's)
 
+    uint32_t bytes = 0, coming[4], qr[D / 8], item = 0;
+    // An item's first rows, scales and queries set out.
+    auto group_row = [&](const TreeWalk& w) { return w.t0 * kTreeTile + warp * kKeys; };  // the warp's rows: these, + 128, ...
+    auto groups = [&](const TreeWalk& w) { return w.t1 - w.t0 - ((w.t1 - 1) * kTreeTile + warp * kKeys >= w.s.end ? 1 : 0); };
+    auto send = [&](const TreeWalk& w, int i) {  // rows of the warp's i-th group
+        if (lane == 0 && !*abort_flag) {
+            const uint32_t slot = sent % kStages, bar = bars + 8u * slot, dst = sbase + ring_at + slot * 2 * C::kHalf;
+            mbar_arrive_expect_tx(bar, 2 * C::kHalf);
+            tma_load_3d(dst, &maps.k, bar, 0, group_row(w) + i * kTreeTile, w.b * a.Hkv + w.g);
+            tma_load_3d(dst + C::kHalf, &maps.v, bar, 0, group_row(w) + i * kTreeTile, w.b * a.Hkv + w.g);
+            ++sent;
+        }
+    };
+    // lane's key's scale byte of group i: K's of key lane, V's of key lane - 16; four groups' in use, four on their
+    // way (a register that is moved on is waited for)
+    auto scale_byte = [&](const TreeWalk& w, int i) {
+        const int row = group_row(w) + i * kTreeTile + (lane & 15);
+        const uint8_t* exps = (lane < kKeys ? a.k_exp : a.v_exp) + ((long long)w.b * a.Hkv + w.g) * a.cap;
+        return i < groups(w) && row < w.s.end ? (uint32_t)exps[row] : 0u;
+    };
+    auto set_out = [&](const TreeWalk& w) {
+        for (int i = 0; i < kStages && i < groups(w); ++i) send(w, i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) coming[e] = scale_byte(w, e);
+        load_query<D>(a, (long long)w.b * a.Hkv + w.g, g8, qr);
+    };
+    set_out(w);
+
+    bool more;
     do {
         if (w.goes_on()) border = w.border(a, blockIdx.x);
-        const int z = w.b * a.Hkv + w.g;
-        const int row0 = w.t0 * kTreeTile + warp * kKeys;  // this warp's rows: row0, row0 + 128, ...
-        const int n = w.t1 - w.t0 - ((w.t1 - 1) * kTreeTile + warp * kKeys >= w.s.end ? 1 : 0);
-        auto send = [&](int i) {  // rows of the warp's i-th group
-            if (lane == 0 && !*abort_flag) {
-                const uint32_t slot = sent % kStages, bar = bars + 8u * slot, dst = sbase + ring_at + slot * 2 * C::kHalf;
-                mbar_arrive_expect_tx(bar, 2 * C::kHalf);
-                tma_load_3d(dst, &maps.k, bar, 0, row0 + i * kTreeTile, z);
-                tma_load_3d(dst + C::kHalf, &maps.v, bar, 0, row0 + i * kTreeTile, z);
-                ++sent;
-            }
-        };
-        // lane's key's scale byte of group i: K's of key lane, V's of key lane - 16; four groups' in use, four on their
-        // way (a register that is moved on is waited for)
-        const uint8_t* exps = (lane < kKeys ? a.k_exp : a.v_exp) + (long long)z * a.cap;
-        auto scale_byte = [&](int i) {
-            const int row = row0 + i * kTreeTile + (lane & 15);
-            return i < n && row < w.s.end ? (uint32_t)exps[row] : 0u;
-        };
-        uint32_t bytes = 0, coming[4];
-        for (int i = 0; i < kStages && i < n; ++i) send(i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) coming[e] = scale_byte(e);
-
-        uint32_t qr[D / 8];
-        const float scale = load_query<D>(a, z, g8, qr);
+        const int row0 = group_row(w), n = groups(w);
+        const float scale = convert_query<D>(a, qr);
         float o[kTiles][4], m[2], l[2], sl[2];  // queries 2t + u
         int big_e[2];                           // E as the scale's byte
         bool live[2];
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, kTreeMmaCtasPerSm) tree_mma_kernel(c
             if ((i & 3) == 0) {
                 bytes = coming[0] | coming[1] << 8 | coming[2] << 16 | coming[3] << 24;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) coming[e] = scale_byte(i + 4 + e);
+                for (int e = 0; e < 4; ++e) coming[e] = scale_byte(w, i + 4 + e);
             }
             const uint32_t byte = bytes & 255u;
             bytes >>= 8;
@@ -324,22 +336,24 @@ __global__ void __launch_bounds__(kThreads, kTreeMmaCtasPerSm) tree_mma_kernel(c
                 // Rows behind the sequence count as zeros.  NaN, and values whose scale takes them past float32, are
                 // cleared and added to the queries that see them: a weight of 0 would not hide them from the others.
                 if (masked || group_e >= kHuge) {
-                    bool odd = false;
+                    bool odd = group_e >= kHuge;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = 2 * t4 + (e & 1) + 8 * (e >> 1), er = (int)__shfl_sync(0xffffffffu, byte, r + 16);
+                    for (int e = 0; e < 4; ++e)
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            if (k0 + r >= w.s.end) vw[e][q] = 0;
-#pragma unroll 1
-                            for (int sh = 0; sh < 32; sh += 8)
-                                if (not_finite(vw[e][q] >> sh & 255u, er)) {
-                                    vw[e][q] &= ~(255u << sh);
-                                    odd |= k0 + r < w.s.end;
-                                }
+                            if (k0 + 2 * t4 + (e & 1) + 8 * (e >> 1) >= w.s.end) vw[e][q] = 0;
+                            odd |= (((vw[e][q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;  // a byte of NaN
                         }
-                    }
                     if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int er = (int)__shfl_sync(0xffffffffu, byte, 2 * t4 + (e & 1) + 8 * (e >> 1) + 16);
+#pragma unroll
+                            for (int q = 0; q < 2; ++q)
+#pragma unroll 1
+                                for (int sh = 0; sh < 32; sh += 8)
+                                    if (not_finite(vw[e][q] >> sh & 255u, er)) vw[e][q] &= ~(255u << sh);
+                        }
 #pragma unroll 1
                         for (int r = 0; r < kKeys; ++r) {
                             const int er = (int)__shfl_sync(0xffffffffu, byte, r + 16);
@@ -370,19 +384,26 @@ __global__ void __launch_bounds__(kThreads, kTreeMmaCtasPerSm) tree_mma_kernel(c
                     }
             }
             __syncwarp();  // all lanes have read the slot
-            if (i + kStages < n) send(i + kStages);
+            if (i + kStages < n) send(w, i + kStages);
         }
 
-        // the item's rows: the eight warps' m, l, E and O, in warp order
-        float4* ml = reinterpret_cast<float4*>(smem + C::kMl);
+        const bool whole = w.whole();
+        const int z = w.b * a.Hkv + w.g, cnt = w.s.cnt;
+        const long long pslot = (long long)blockIdx.x * 2 + (w.first ? 0 : 1);
+        more = w.next(a);
+        if (more) set_out(w);
+
+        // the item's rows: the eight warps' m, l, E and O, in warp order (the next item's m, l come elsewhere: some warps
+        // may still read these; its O are written behind the next barrier)
+        float4* ml = reinterpret_cast<float4*>(smem + C::kMl) + (item++ & 1) * kWarps * 8;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) l[u] += __shfl_xor_sync(0xffffffffu, l[u], d);
             if (g8 == 0) ml[warp * 8 + 2 * t4 + u] = make_float4(m[u], l[u], __int_as_float(big_e[u]), 0.f);
         }
-        __syncthreads();  // (and every warp's ring is free)
-        float4* xs = reinterpret_cast<float4*>(smem);
+        __syncthreads();
+        float4* xs = reinterpret_cast<float4*>(smem + C::kX);
         constexpr int kFours = D / 32, kVecs = 2 * kFours;  // float4 per thread: [u][fours of its d / 8 columns]
         auto join = [&](int x, float& top, float& sum, int& top_e) {
             top = -INFINITY;
@@ -412,8 +433,6 @@ __global__ void __launch_bounds__(kThreads, kTreeMmaCtasPerSm) tree_mma_kernel(c
                     make_float4(o[2 * c][u] * f, o[2 * c][2 + u] * f, o[2 * c + 1][u] * f, o[2 * c + 1][2 + u] * f);
         }
         __syncthreads();
-        const bool whole = w.whole();
-        const long long pslot = (long long)blockIdx.x * 2 + (w.first ? 0 : 1);
         const int row = 2 * t4 + warp / kFours, d = g8 * (D / 8) + warp % kFours * 4;  // warp k: vector k (d = 64: the first four)
         if (warp < kVecs && row < a.R) {
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -425,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, kTreeMmaCtasPerSm) tree_mma_kernel(c
             float mr, lr;
             int top_e;
             join(row, mr, lr, top_e);
-            const bool none = row % a.T >= w.s.cnt || (mr == -INFINITY && lr == 0.f);
+            const bool none = row % a.T >= cnt || (mr == -INFINITY && lr == 0.f);
             const long long grow = (long long)z * a.R + row;
             const float inv = whole ? 1.0f / lr : 1.0f, up = __uint_as_float((uint32_t)top_e << 23);
             float* ps = &sum.x;
@@ -444,9 +463,7 @@ __global__ void __launch_bounds__(kThreads, kTreeMmaCtasPerSm) tree_mma_kernel(c
                 if (d == 0) *reinterpret_cast<float4*>(a.part_ml + (pslot * a.rt + row) * 4) = make_float4(mr, lr, lr, 0.f);
             }
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the rings are filled again
-        __syncthreads();
-    } while (w.next(a));
+    } while (more);
     if (threadIdx.x == 0) a.border[blockIdx.x] = border;
     if (lane == 0) {  // after a wait that gave up, copies may still be on their way
         for (uint32_t k = 1; k <= (uint32_t)kStages && k <= sent; ++k)
