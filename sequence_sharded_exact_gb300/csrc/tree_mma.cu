@@ -19,7 +19,7 @@
 //     and its queries are on their way meanwhile.
 //
 // What bounds it: the memory, nearly.  A tile of 128 rows of 8 kv heads' e4m3 cache (d = 128) costs each of 152 SMs
-// 0.88 us, 5.6 TB/s (tree_tc_body.cuh: 1.46), one token over 131072 rows 56 us with both launches (it: 91).  A group of 16
+// 0.88 us, 5.6 TB/s (tree_tc_body.cuh: 1.46), one token over 131072 rows 54 us with both launches (it: 91).  A group of 16
 // rows is about 440 instructions, issued in 0.54 of the cycles: latency, which 16 warps per SM hide; 24 do not fit the
 // registers (80 each: spills, 60 us at 32 tiles per SM in place of 39), a third stage per ring changes nothing.  With query
 // rows as the products' 16 rows there are twice as many products and registers (65 us).  With 16 query rows it
