@@ -210,11 +210,13 @@ int tree_simt_rows(int R);
 constexpr int kTreeSimtCtasPerSm = 4;
 cudaError_t launch_tree_simt(const TreeArgs& a, int d, int cache_dtype, cudaStream_t s);
 
-// bf16 queries over an e4m3 cache, up to kTreeMmaRows query rows per kv head: one row tile (tree_mma.cu).
+// bf16 queries, up to kTreeMmaRows query rows per kv head: one row tile; an e4m3 cache (tree_mma.cu) or a bf16 one
+// (tree_mma_bf16.cu).
 constexpr int kTreeMmaRows = 8;
 constexpr int kTreeMmaCtasPerSm = 2;
 constexpr int kTreeMaxMmaCtas = 320;
 cudaError_t launch_tree_mma(const TreeArgs& a, int d, cudaStream_t s);
+cudaError_t launch_tree_mma_bf16(const TreeArgs& a, int d, cudaStream_t s);
 
 // Tensor-core path: bf16 queries, bf16 or e4m3 cache (tree_tc_body.cuh).
 cudaError_t launch_tree_tc_d128(const TreeArgs& a, bool e4m3, cudaStream_t s);

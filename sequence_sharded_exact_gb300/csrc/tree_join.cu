@@ -195,7 +195,7 @@ static Cut cut_of(const Cache& c, int H, int T, int dtype)
 {
     Cut u;
     const int R = H / c.Hkv * T;
-    u.path = dtype != 1 ? Path::kSimt : c.dtype == kCacheE4m3 && R <= kTreeMmaRows ? Path::kMma : Path::kTc;
+    u.path = dtype != 1 ? Path::kSimt : R <= kTreeMmaRows ? Path::kMma : Path::kTc;
     u.tile = u.path == Path::kSimt ? kTreeSimtTile : kTreeTile;
     u.rt = u.path == Path::kSimt ? tree_simt_rows(R) : u.path == Path::kMma ? kTreeMmaRows : R <= 128 ? 128 : 256;
     u.nrt = (R + u.rt - 1) / u.rt;
@@ -250,7 +250,7 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
     a.part_o = reinterpret_cast<float*>(ws + border_bytes(u) + ml_bytes(u));
     cudaError_t e;
     if (u.path == Path::kMma)
-        e = launch_tree_mma(a, c.d, s);
+        e = c.dtype == kCacheE4m3 ? launch_tree_mma(a, c.d, s) : launch_tree_mma_bf16(a, c.d, s);
     else if (u.path == Path::kTc)
         e = c.d == 128 ? launch_tree_tc_d128(a, c.dtype == kCacheE4m3, s) : launch_tree_tc_d64(a, c.dtype == kCacheE4m3, s);
     else

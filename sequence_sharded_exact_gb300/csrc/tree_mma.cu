@@ -24,24 +24,17 @@
 // registers (80 each: spills, 60 us at 32 tiles per SM in place of 39), a third stage per ring changes nothing.  With query
 // rows as the products' 16 rows there are twice as many products and registers (65 us).  With 16 query rows it
 // spills (64 us against 61 there), so more than 8 take the tcgen05 path.
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cudaTypedefs.h>
 #include <math.h>
 
-#include <mutex>
-
-#include "ra_internal.h"
-#include "ra_ptx.cuh"
-#include "tree.cuh"
+#include "tree_mma.cuh"
 
 namespace ra {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps, kKeys = 16, kStages = 2;
+constexpr int kWarps = 8, kThreads = 32 * kWarps, kStages = 2;
 static_assert(kWarps * kKeys == kTreeTile, "a warp's rows of a tile");
-constexpr long long kWaitLimit = 10000000000ll;
 
 template <int D>
 struct Cfg {
@@ -54,36 +47,6 @@ struct Cfg {
     static constexpr uint32_t kSmem = kAbort + 8 + 1024;  // slack for the 1024-byte alignment of the base
     static_assert(kSmem * kTreeMmaCtasPerSm <= 229376, "shared memory");
 };
-
-struct Maps {
-    CUtensorMap k, v;
-};
-
-// A bounded wait by the whole warp.  After one has given up (or another warp's) every further wait returns at once, and
-// the caller goes on to its end with whatever is there: the status word says that the results do not count.
-__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, const WaitCtl& ctl)
-{
-    if (!mbar_try_wait(bar, parity)) {
-        const long long t0 = clock64();
-        while (!mbar_try_wait(bar, parity)) {
-            if (*ctl.abort) break;
-            if (clock64() - t0 > kWaitLimit) {
-                *ctl.abort = 1;
-                atomicOr(ctl.status, kStatusTimeout);
-                break;
-            }
-        }
-    }
-    __syncwarp();
-}
-
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity)
-{
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (global_timer_ns() - t0 > 1000000000ull) return;
-    }
-}
 
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
 {
@@ -104,14 +67,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b)
 {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Rows g of an 8 x 8 matrix of f16, two columns 2t, 2t + 1 per thread: its transpose in the same places.
-__device__ __forceinline__ uint32_t transpose8(uint32_t x)
-{
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
 }
 
 // A V byte that stands for no finite float32 at its row's scale: NaN, and from kHuge on the values that pass 2^128.
@@ -475,15 +430,7 @@ __global__ void __launch_bounds__(kThreads, kTreeMmaCtasPerSm) tree_mma_kernel(c
 template <int D>
 bool make_map(CUtensorMap* map, const void* base, long long rows, long long heads)
 {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
+    auto fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)heads};
     cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)rows * D};
@@ -503,18 +450,8 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t s)
     if (!make_map<D>(&maps.k, a.k, a.cap, heads) || !make_map<D>(&maps.v, a.v, a.cap, heads)) return cudaErrorInvalidValue;
     static std::mutex mu;
     static bool done[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = allow_smem(tree_mma_kernel<D>, (int)C::kSmem, mu, done);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    {
-        std::lock_guard<std::mutex> lk(mu);
-        if (!done[dev]) {
-            e = cudaFuncSetAttribute(tree_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
-            if (e != cudaSuccess) return e;
-            done[dev] = true;
-        }
-    }
     tree_mma_kernel<D><<<a.ctas, kThreads, C::kSmem, s>>>(maps, a);
     return cudaGetLastError();
 }
