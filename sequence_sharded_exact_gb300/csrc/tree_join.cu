@@ -228,7 +228,9 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
     a.tile = u.tile;
     a.rt = u.rt;
     a.nrt = u.nrt;
-    const int resident = device_sm_count() * (u.path == Path::kSimt ? kTreeSimtCtasPerSm : u.path == Path::kMma ? kTreeMmaCtasPerSm : 1);
+    const int sms = device_sm_count();
+    const bool e4m3 = c.dtype == kCacheE4m3, many = (long long)c.B * c.Hkv >= (long long)kTreeMmaManyItems * sms;
+    const int resident = sms * (u.path == Path::kSimt ? kTreeSimtCtasPerSm : u.path == Path::kTc ? 1 : e4m3 ? (many ? 4 : 2) : many ? 3 : 2);
     a.ctas = u.ctas < resident ? u.ctas : resident;
     a.mask_batched = t.mask_batched;
     a.bf16_out = t.out_dtype == 1;
@@ -250,9 +252,9 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
     a.part_o = reinterpret_cast<float*>(ws + border_bytes(u) + ml_bytes(u));
     cudaError_t e;
     if (u.path == Path::kMma)
-        e = c.dtype == kCacheE4m3 ? launch_tree_mma(a, c.d, s) : launch_tree_mma_bf16(a, c.d, s);
+        e = e4m3 ? launch_tree_mma(a, c.d, many ? 4 : 8, s) : launch_tree_mma_bf16(a, c.d, s);
     else if (u.path == Path::kTc)
-        e = c.d == 128 ? launch_tree_tc_d128(a, c.dtype == kCacheE4m3, s) : launch_tree_tc_d64(a, c.dtype == kCacheE4m3, s);
+        e = c.d == 128 ? launch_tree_tc_d128(a, e4m3, s) : launch_tree_tc_d64(a, e4m3, s);
     else
         e = launch_tree_simt(a, c.d, c.dtype, s);
     return e != cudaSuccess ? e : launch_tree_join(a, c.d, s);

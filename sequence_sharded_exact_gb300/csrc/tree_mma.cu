@@ -14,14 +14,14 @@
 //   * Weights: p 2^(ev_j - E + 7) in f16, ev_j the exponent of key j's V row, E the largest so far of the rows that the
 //     query sees: eleven bits down to 2^-21 of weight 1 at E, weight and scale together.  The sum l takes p itself.
 //     The reference of p follows the row maximum only when that grows by more than 2^8, so O is seldom rescaled.
-//   * A CTA's eight warps take 16 rows of every tile each, with rings of their own that the TMA fills; m, l, E and O are
+//   * A CTA's warps take 16 rows in turn, with rings of their own that the TMA fills; m, l, E and O are
 //     a warp's own until the item's end, where they meet in shared memory, in warp order.  The next item's first rows
 //     and its queries are on their way meanwhile.
 //
 // What bounds it: the memory, nearly.  A tile of 128 rows of 8 kv heads' e4m3 cache (d = 128) costs each of 152 SMs
-// 0.88 us, 5.6 TB/s (tree_tc_body.cuh: 1.46), one token over 131072 rows 54 us with both launches (it: 91).  A group of 16
+// 0.90 us, 5.5 TB/s (tree_tc_body.cuh: 1.46), one token over 131072 rows 53 us with both launches (it: 91).  A group of 16
 // rows is about 440 instructions, issued in 0.54 of the cycles: latency, which 16 warps per SM hide; 24 do not fit the
-// registers (80 each: spills, 60 us at 32 tiles per SM in place of 39), a third stage per ring changes nothing.  With query
+// registers (80 each: spills, 60 us at 32 tiles per SM in place of 38), a third stage per ring changes nothing.  With query
 // rows as the products' 16 rows there are twice as many products and registers (65 us).  With 16 query rows it
 // spills (64 us against 61 there), so more than 8 take the tcgen05 path.
 #include <cuda_bf16.h>
@@ -33,10 +33,9 @@
 namespace ra {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps, kStages = 2;
-static_assert(kWarps * kKeys == kTreeTile, "a warp's rows of a tile");
+constexpr int kStages = 2;
 
-template <int D>
+template <int D, int kWarps>
 struct Cfg {
     static constexpr uint32_t kHalf = kKeys * D;                          // bytes of 16 rows
     static constexpr uint32_t kRings = kWarps * kStages * 2 * kHalf;      // [warps][stages][k, v]
@@ -45,7 +44,7 @@ struct Cfg {
     static constexpr uint32_t kBar = kMl + 2 * kWarps * 8 * 16;
     static constexpr uint32_t kAbort = kBar + kWarps * kStages * 8;
     static constexpr uint32_t kSmem = kAbort + 8 + 1024;  // slack for the 1024-byte alignment of the base
-    static_assert(kSmem * kTreeMmaCtasPerSm <= 229376, "shared memory");
+    static_assert((kSmem + 1024) * (kTreeMmaWarps / kWarps) <= 233472, "shared memory");
 };
 
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
@@ -119,10 +118,10 @@ __device__ __forceinline__ float convert_query(const TreeArgs& a, uint32_t (&f)[
     return finite ? pow2(e) * a.scale_log2 : __uint_as_float(0x7fc00000u);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, kTreeMmaCtasPerSm) tree_mma_kernel(const __grid_constant__ Maps maps, const TreeArgs a)
+template <int D, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kTreeMmaWarps / kWarps) tree_mma_kernel(const __grid_constant__ Maps maps, const TreeArgs a)
 {
-    using C = Cfg<D>;
+    using C = Cfg<D, kWarps>;
     constexpr int kTiles = D / 16;  // 16-row tiles of O^T
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -148,21 +147,25 @@ __global__ void __launch_bounds__(kThreads, kTreeMmaCtasPerSm) tree_mma_kernel(c
 
     uint32_t bytes = 0, coming[4], qr[D / 8], item = 0;
     // An item's first rows, scales and queries set out.
-    auto group_row = [&](const TreeWalk& w) { return w.t0 * kTreeTile + warp * kKeys; };  // the warp's rows: these, + 128, ...
-    auto groups = [&](const TreeWalk& w) { return w.t1 - w.t0 - ((w.t1 - 1) * kTreeTile + warp * kKeys >= w.s.end ? 1 : 0); };
+    constexpr int kStep = kWarps * kKeys;  // the warp's 16-row groups of an item: from group_row on, every kWarps-th
+    auto group_row = [&](const TreeWalk& w) { return w.t0 * kTreeTile + warp * kKeys; };
+    auto groups = [&](const TreeWalk& w) {
+        const int end = w.t1 * kTreeTile < w.s.end ? w.t1 * kTreeTile : w.s.end, all = (end - w.t0 * kTreeTile + kKeys - 1) / kKeys;
+        return all > warp ? (all - warp + kWarps - 1) / kWarps : 0;
+    };
     auto send = [&](const TreeWalk& w, int i) {  // rows of the warp's i-th group
         if (lane == 0 && !*abort_flag) {
             const uint32_t slot = sent % kStages, bar = bars + 8u * slot, dst = sbase + ring_at + slot * 2 * C::kHalf;
             mbar_arrive_expect_tx(bar, 2 * C::kHalf);
-            tma_load_3d(dst, &maps.k, bar, 0, group_row(w) + i * kTreeTile, w.b * a.Hkv + w.g);
-            tma_load_3d(dst + C::kHalf, &maps.v, bar, 0, group_row(w) + i * kTreeTile, w.b * a.Hkv + w.g);
+            tma_load_3d(dst, &maps.k, bar, 0, group_row(w) + i * kStep, w.b * a.Hkv + w.g);
+            tma_load_3d(dst + C::kHalf, &maps.v, bar, 0, group_row(w) + i * kStep, w.b * a.Hkv + w.g);
             ++sent;
         }
     };
     // lane's key's scale byte of group i: K's of key lane, V's of key lane - 16; four groups' in use, four on their
     // way (a register that is moved on is waited for)
     auto scale_byte = [&](const TreeWalk& w, int i) {
-        const int row = group_row(w) + i * kTreeTile + (lane & 15);
+        const int row = group_row(w) + i * kStep + (lane & 15);
         const uint8_t* exps = (lane < kKeys ? a.k_exp : a.v_exp) + ((long long)w.b * a.Hkv + w.g) * a.cap;
         return i < groups(w) && row < w.s.end ? (uint32_t)exps[row] : 0u;
     };
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, kTreeMmaCtasPerSm) tree_mma_kernel(c
                 }
             }
 
-            const int k0 = row0 + i * kTreeTile;
+            const int k0 = row0 + i * kStep;
             const bool masked = k0 + kKeys > w.s.len;
             bool raise = false;
             float alpha[2], p[2][2];  // p: [key][query]
@@ -388,12 +391,14 @@ __global__ void __launch_bounds__(kThreads, kTreeMmaCtasPerSm) tree_mma_kernel(c
                     make_float4(o[2 * c][u] * f, o[2 * c][2 + u] * f, o[2 * c + 1][u] * f, o[2 * c + 1][2 + u] * f);
         }
         __syncthreads();
-        const int row = 2 * t4 + warp / kFours, d = g8 * (D / 8) + warp % kFours * 4;  // warp k: vector k (d = 64: the first four)
-        if (warp < kVecs && row < a.R) {
+#pragma unroll 1
+        for (int v = warp; v < kVecs; v += kWarps) {  // vector v of every warp
+            const int row = 2 * t4 + v / kFours, d = g8 * (D / 8) + v % kFours * 4;
+            if (row >= a.R) continue;
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
-                const float4 y = xs[(k * kVecs + warp) * 32 + lane];
+                const float4 y = xs[(k * kVecs + v) * 32 + lane];
                 sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
             }
             float mr, lr;
@@ -441,26 +446,27 @@ bool make_map(CUtensorMap* map, const void* base, long long rows, long long head
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, int kWarps>
 cudaError_t launch(const TreeArgs& a, cudaStream_t s)
 {
-    using C = Cfg<D>;
+    using C = Cfg<D, kWarps>;
     Maps maps;
     const long long heads = (long long)a.B * a.Hkv;
     if (!make_map<D>(&maps.k, a.k, a.cap, heads) || !make_map<D>(&maps.v, a.v, a.cap, heads)) return cudaErrorInvalidValue;
     static std::mutex mu;
     static bool done[64];
-    const cudaError_t e = allow_smem(tree_mma_kernel<D>, (int)C::kSmem, mu, done);
+    const cudaError_t e = allow_smem(tree_mma_kernel<D, kWarps>, (int)C::kSmem, mu, done);
     if (e != cudaSuccess) return e;
-    tree_mma_kernel<D><<<a.ctas, kThreads, C::kSmem, s>>>(maps, a);
+    tree_mma_kernel<D, kWarps><<<a.ctas, 32 * kWarps, C::kSmem, s>>>(maps, a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_tree_mma(const TreeArgs& a, int d, cudaStream_t s)
+cudaError_t launch_tree_mma(const TreeArgs& a, int d, int warps, cudaStream_t s)
 {
-    return d == 128 ? launch<128>(a, s) : launch<64>(a, s);
+    if (warps == 8) return d == 128 ? launch<128, 8>(a, s) : launch<64, 8>(a, s);
+    return d == 128 ? launch<128, 4>(a, s) : launch<64, 4>(a, s);
 }
 
 }  // namespace ra

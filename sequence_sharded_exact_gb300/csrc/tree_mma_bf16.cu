@@ -3,8 +3,13 @@
 // The products of tree_mma.cu, S^T = K Q^T and O^T += V^T P^T with 16 cached rows, or columns of V, against 8 queries
 // (mma.m16n8k16, bf16, float32 sums), a warp by itself with 16 cached rows at a time; K and V are operands as they
 // are cached, V by transposing loads (ldmatrix).  P is bf16, as on the tcgen05 path, and so is the correction of the
-// normaliser for the largest weight's rounding.  A CTA has four warps, two CTAs an SM: while one joins its warps'
-// results at an item's end the other streams.
+// normaliser for the largest weight's rounding.  A CTA has four warps, two or three CTAs run on an SM: while one joins its
+// warps' results at an item's end the others stream.
+//
+// What bounds it: the memory.  A tile of 128 rows of 8 kv heads (d = 128, 64 KB) costs each of 152 SMs 1.30 us, 7.6
+// TB/s; one token over 131072 rows takes 85 us with both launches (tree_tc_body.cuh: 88), one over 19 tiles, a tile
+// an SM, 11.5 (12.7), 512 sequences of 129 rows 72 (120): no 128 query rows to fill, and no pipeline of
+// warps with different parts to drain at every item's end.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -19,13 +24,14 @@ template <int D>
 struct Cfg {
     static constexpr uint32_t kHalf = kKeys * D * 2;                      // bytes of 16 rows
     static constexpr uint32_t kRings = kWarps * kStages * 2 * kHalf;      // [warps][stages][k, v], 64 columns after 64
-    static constexpr int kXRow = D + 4;                                   // floats: queries' rows fall into different banks
+    static constexpr int kXRow = 64 + 4;                                  // floats: queries' rows fall into different banks
     static constexpr uint32_t kX = kRings;                                // exchange: [warps][8][kXRow] float
     static constexpr uint32_t kMl = kX + kWarps * 8 * kXRow * 4;          // [2 items][warps][8] m, l, normaliser, 0
     static constexpr uint32_t kBar = kMl + 2 * kWarps * 8 * 16;
     static constexpr uint32_t kAbort = kBar + kWarps * kStages * 8;
     static constexpr uint32_t kSmem = kAbort + 8 + 1024;  // slack for the 1024-byte alignment of the base
-    static_assert((kSmem + 1024) * kTreeMmaCtasPerSm <= 232448, "shared memory");
+    static_assert(kThreads == 8 * 16, "a thread per row and four of 64 columns");
+    static_assert((kSmem + 1024) * 3 <= 233472, "shared memory");
 };
 
 __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -57,7 +63,7 @@ __device__ __forceinline__ uint32_t at16(int r, int c) { return (uint32_t)((c >>
 __device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7f80u) == 0x7f80u; }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, kTreeMmaCtasPerSm) tree_mma_bf16_kernel(const __grid_constant__ Maps maps, const TreeArgs a)
+__global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid_constant__ Maps maps, const TreeArgs a)
 {
     using C = Cfg<D>;
     constexpr int kTiles = D / 16;  // k steps of S^T, 16-row tiles of O^T
@@ -255,40 +261,47 @@ __global__ void __launch_bounds__(kThreads, kTreeMmaCtasPerSm) tree_mma_bf16_ker
         }
         __syncthreads();
         float* xs = reinterpret_cast<float*>(smem + C::kX);
+        float f[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             float top = -INFINITY;
             for (int k = 0; k < kWarps; ++k) top = fmaxf(top, ml[k * 8 + 2 * t4 + u].x);
-            const float f = ex2_approx(m[u] - (top == -INFINITY ? 0.f : top));
-            float* x = xs + (warp * 8 + 2 * t4 + u) * C::kXRow + g8;
-#pragma unroll
-            for (int j = 0; j < 2 * kTiles; ++j) x[8 * j] = o[j >> 1][2 * (j & 1) + u] * f;
+            f[u] = ex2_approx(m[u] - (top == -INFINITY ? 0.f : top));
         }
-        __syncthreads();
-#pragma unroll 1
-        for (int v = threadIdx.x; v < 8 * (D / 4); v += kThreads) {
-            const int row = v / (D / 4), d = v % (D / 4) * 4;
-            if (row >= a.R) break;
+        // a thread sums four columns of one row, 64 columns of all rows at a time
+        const int row = threadIdx.x >> 4;
+        float top = -INFINITY, lr = 0.f, den = 0.f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, ml[k * 8 + row].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            const float4 y = ml[k * 8 + row];
+            const float g = ex2_approx(y.x - ref);
+            const bool nan = y.x == -INFINITY && y.y != 0.f;  // NaN scores alone leave no maximum
+            lr = nan ? y.y : fmaf(y.y, g, lr);
+            den = nan ? y.y : fmaf(y.z, g, den);
+        }
+        const bool none = row % a.T >= cnt || (top == -INFINITY && lr == 0.f);
+        const long long grow = (long long)z * a.R + row;
+        const float inv = whole ? 1.0f / den : 1.0f;
+#pragma unroll
+        for (int part = 0; part < D / 64; ++part) {
+            if (part) __syncthreads();
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    xs[(warp * 8 + 2 * t4 + u) * C::kXRow + 8 * j + g8] = o[part * 4 + (j >> 1)][2 * (j & 1) + u] * f[u];
+            __syncthreads();
+            if (row >= a.R) continue;
+            const int at = (threadIdx.x & 15) * 4, d = part * 64 + at;
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-            float top = -INFINITY, lr = 0.f, den = 0.f;
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
-                const float4 y = *reinterpret_cast<const float4*>(xs + (k * 8 + row) * C::kXRow + d);
+                const float4 y = *reinterpret_cast<const float4*>(xs + (k * 8 + row) * C::kXRow + at);
                 sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
-                top = fmaxf(top, ml[k * 8 + row].x);
             }
-            const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                const float4 y = ml[k * 8 + row];
-                const float f = ex2_approx(y.x - ref);
-                const bool nan = y.x == -INFINITY && y.y != 0.f;  // NaN scores alone leave no maximum
-                lr = nan ? y.y : fmaf(y.y, f, lr);
-                den = nan ? y.y : fmaf(y.z, f, den);
-            }
-            const bool none = row % a.T >= cnt || (top == -INFINITY && lr == 0.f);
-            const long long grow = (long long)z * a.R + row;
-            const float inv = whole ? 1.0f / den : 1.0f;
             float* ps = &sum.x;
 #pragma unroll
             for (int e = 0; e < 4; ++e) ps[e] = none ? 0.f : ps[e] * inv;

@@ -27,8 +27,7 @@
 // cache), so warps 12-15 turn V into bf16, exactly, scale included.
 //
 // What bounds it, per tile of 128 cached rows on each of 152 SMs, d = 128 (launches apart):
-//   * bf16, up to 128 query rows: 1.38 us for 64 KB, 7.2 TB/s: the memory.  One token over 131072 rows of 8 kv heads
-//     takes 89 us, the second launch included.
+//   * bf16, up to 128 query rows: 1.38 us for 64 KB, 7.2 TB/s: the memory.  (Up to 8 rows take tree_mma_bf16.cu.)
 //   * bf16, 256 rows: 1.67 us.  The products take 1.06 of them; S, the softmax and P V of a warpgroup's query rows follow
 //     one another on one S, whose columns P takes (TMEM is full: two S, two O).
 //   * e4m3, up to 128 rows: 1.45 us for 32 KB.  Shared memory serves 1600 of the 2500 cycles at 128 bytes each: copies

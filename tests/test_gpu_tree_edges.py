@@ -236,3 +236,19 @@ def test_scratch_stays_with_the_stream_that_uses_it():
     assert s.query() or after != at
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(out, ref))
+
+
+@pytest.mark.parametrize("cdt", [BF, E4M3])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [1, 2])
+def test_many_short_sequences(T, d, cdt):
+    """More (sequence, kv head) pairs than CTAs, of up to two tiles; some without tokens, some without a prefix."""
+    B, H, Hkv, cap = 500, 4, 2, 150
+    k, v, q = _randn(B, Hkv, cap, d, seed=101), _randn(B, Hkv, cap, d, seed=102), _randn(B, H, T, d, seed=103, dtype=BF)
+    cache = _cache_of(k, v, BF, cdt)
+    lens, ntok = [(37 * b) % (cap - T + 1) for b in range(B)], [T if b % 7 else b % 2 for b in range(B)]
+    got = ra.tree_fwd(q, cache, _i32(lens), ntok=_i32(ntok))
+    kk, vv = cu.cache_values(cache)
+    cu.check_tree(got, cu.tree(q, kk, vv, lens, None, ntok), 2.0 ** -8, BF)
+    again = ra.tree_fwd(q, cache, _i32(lens), ntok=_i32(ntok))
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
