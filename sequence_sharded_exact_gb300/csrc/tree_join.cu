@@ -195,9 +195,9 @@ static Cut cut_of(const Cache& c, int H, int T, int dtype)
 {
     Cut u;
     const int R = H / c.Hkv * T;
-    u.path = dtype != 1 ? Path::kSimt : R <= kTreeMmaRows ? Path::kMma : Path::kTc;
+    u.path = dtype != 1 ? Path::kSimt : R <= (c.dtype == kCacheE4m3 ? kTreeMmaE4m3Rows : kTreeMmaRows) ? Path::kMma : Path::kTc;
     u.tile = u.path == Path::kSimt ? kTreeSimtTile : kTreeTile;
-    u.rt = u.path == Path::kSimt ? tree_simt_rows(R) : u.path == Path::kMma ? kTreeMmaRows : R <= 128 ? 128 : 256;
+    u.rt = u.path == Path::kSimt ? tree_simt_rows(R) : u.path == Path::kMma ? (R <= kTreeMmaRows ? kTreeMmaRows : kTreeMmaE4m3Rows) : R <= 128 ? 128 : 256;
     u.nrt = (R + u.rt - 1) / u.rt;
     const long long most = (long long)c.B * c.Hkv * u.nrt * ((c.cap + u.tile - 1) / u.tile);
     const int cap = u.path == Path::kSimt ? kTreeMaxCtas : u.path == Path::kMma ? kTreeMaxMmaCtas : kTreeMaxTcCtas;
@@ -230,7 +230,7 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
     a.nrt = u.nrt;
     const int sms = device_sm_count();
     const bool e4m3 = c.dtype == kCacheE4m3, many = (long long)c.B * c.Hkv >= (long long)kTreeMmaManyItems * sms;
-    const int resident = sms * (u.path == Path::kSimt ? kTreeSimtCtasPerSm : u.path == Path::kTc ? 1 : e4m3 ? (many ? 4 : 2) : many ? 3 : 2);
+    const int resident = sms * (u.path == Path::kSimt ? kTreeSimtCtasPerSm : u.path == Path::kTc ? 1 : u.rt == kTreeMmaE4m3Rows ? tree_mma16_ctas_per_sm(c.d) : e4m3 ? (many ? 4 : 2) : many ? 3 : 2);
     a.ctas = u.ctas < resident ? u.ctas : resident;
     a.mask_batched = t.mask_batched;
     a.bf16_out = t.out_dtype == 1;

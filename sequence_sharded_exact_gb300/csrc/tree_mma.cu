@@ -1,9 +1,9 @@
-// tree_mma.cu -- attention over an e4m3 cache (tree.cuh) for bf16 queries, up to 8 query rows per kv head.
+// tree_mma.cu -- attention over an e4m3 cache (tree.cuh) for bf16 queries, up to 16 query rows per kv head.
 //
 // So few rows leave the 128-row products of tree_tc_body.cuh nearly empty, and what bounds that path over an e4m3
 // cache is V's way through shared memory as bf16.  Here a warp works on 16 cached rows by itself, in products whose
 // 16 rows are cached rows or columns of V and whose 8 columns are queries (mma.m16n8k16, f16, float32 sums):
-//   S^T = K Q^T,  O^T += V^T P^T,
+//   S^T = K Q^T,  O^T += V^T P^T  (twice, with one set of operands, for 9 to 16 rows),
 // with operands that a thread puts together in registers: every e4m3 value is an f16, by one conversion per two of
 // them, and nothing goes back to shared memory.  The order of a product's contraction and of its rows is free: thread
 // (t, g) of a warp (t = lane % 4, g = lane / 4) takes d / 4 neighbouring elements of K's rows g and g + 8, and of V's rows
@@ -22,8 +22,8 @@
 // 0.90 us, 5.5 TB/s (tree_tc_body.cuh: 1.46), one token over 131072 rows 53 us with both launches (it: 91).  A group of 16
 // rows is about 440 instructions, issued in 0.54 of the cycles: latency, which 16 warps per SM hide; 24 do not fit the
 // registers (80 each: spills, 60 us at 32 tiles per SM in place of 38), a third stage per ring changes nothing.  With query
-// rows as the products' 16 rows there are twice as many products and registers (65 us).  With 16 query rows it
-// spills (64 us against 61 there), so more than 8 take the tcgen05 path.
+// rows as the products' 16 rows there are twice as many products and registers (65 us).  9 to 16 query rows: 131072 rows in
+// 77 us in place of 88 there, 64 sequences of 1000 rows in 58 in place of 83 (d = 64: 52 for 73, 37 for 64).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -33,18 +33,20 @@
 namespace ra {
 namespace {
 
+
 constexpr int kStages = 2;
 
-template <int D, int kWarps>
+template <int D, int kWarps, int N>  // N: query rows in eights
 struct Cfg {
+    static constexpr int kPerSm = N == 1 ? kTreeMmaWarps / kWarps : tree_mma16_ctas_per_sm(D);
     static constexpr uint32_t kHalf = kKeys * D;                          // bytes of 16 rows
     static constexpr uint32_t kRings = kWarps * kStages * 2 * kHalf;      // [warps][stages][k, v]
-    static constexpr uint32_t kX = kRings;                                // exchange: [warps][D / 16][lanes] float4
-    static constexpr uint32_t kMl = kX + kWarps * 32 * D;                 // [2 items][warps][8] m, l, E's bits, 0
-    static constexpr uint32_t kBar = kMl + 2 * kWarps * 8 * 16;
+    static constexpr uint32_t kX = kRings;                                // exchange: [warps][N D / 16][lanes] float4
+    static constexpr uint32_t kMl = kX + kWarps * N * 32 * D;             // [2 items][warps][8 N] m, l, E's bits, 0
+    static constexpr uint32_t kBar = kMl + 2 * kWarps * 8 * N * 16;
     static constexpr uint32_t kAbort = kBar + kWarps * kStages * 8;
     static constexpr uint32_t kSmem = kAbort + 8 + 1024;  // slack for the 1024-byte alignment of the base
-    static_assert((kSmem + 1024) * (kTreeMmaWarps / kWarps) <= 233472, "shared memory");
+    static_assert((kSmem + 1024) * kPerSm <= 233472, "shared memory");
 };
 
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
@@ -118,10 +120,10 @@ __device__ __forceinline__ float convert_query(const TreeArgs& a, uint32_t (&f)[
     return finite ? pow2(e) * a.scale_log2 : __uint_as_float(0x7fc00000u);
 }
 
-template <int D, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, kTreeMmaWarps / kWarps) tree_mma_kernel(const __grid_constant__ Maps maps, const TreeArgs a)
+template <int D, int kWarps, int N>
+__global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_mma_kernel(const __grid_constant__ Maps maps, const TreeArgs a)
 {
-    using C = Cfg<D, kWarps>;
+    using C = Cfg<D, kWarps, N>;
     constexpr int kTiles = D / 16;  // 16-row tiles of O^T
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(32 * kWarps, kTreeMmaWarps / kWarps) tree_mma_
     int4 border = make_int4(-1, 0, 0, 0);
     uint32_t used = 0, sent = 0;  // of the ring (sent: lane 0's)
 
-    uint32_t bytes = 0, coming[4], qr[D / 8], item = 0;
+    uint32_t bytes = 0, coming[4], qr[N][D / 8], item = 0;
     // An item's first rows, scales and queries set out.
     constexpr int kStep = kWarps * kKeys;  // the warp's 16-row groups of an item: from group_row on, every kWarps-th
     auto group_row = [&](const TreeWalk& w) { return w.t0 * kTreeTile + warp * kKeys; };
@@ -173,7 +175,8 @@ __global__ void __launch_bounds__(32 * kWarps, kTreeMmaWarps / kWarps) tree_mma_
         for (int i = 0; i < kStages && i < groups(w); ++i) send(w, i);
 #pragma unroll
         for (int e = 0; e < 4; ++e) coming[e] = scale_byte(w, e);
-        load_query<D>(a, (long long)w.b * a.Hkv + w.g, g8, qr);
+#pragma unroll
+        for (int c = 0; c < N; ++c) load_query<D>(a, (long long)w.b * a.Hkv + w.g, 8 * c + g8, qr[c]);
     };
     set_out(w);
 
@@ -181,25 +184,29 @@ __global__ void __launch_bounds__(32 * kWarps, kTreeMmaWarps / kWarps) tree_mma_
     do {
         if (w.goes_on()) border = w.border(a, blockIdx.x);
         const int row0 = group_row(w), n = groups(w);
-        const float scale = convert_query<D>(a, qr);
-        float o[kTiles][4], m[2], l[2], sl[2];  // queries 2t + u
-        int big_e[2];                           // E as the scale's byte
-        bool live[2];
+        float o[N][kTiles][4], m[N][2], l[N][2], sl[N][2];  // queries 8 c + 2t + u
+        int big_e[N][2];                                    // E as the scale's byte
+        uint32_t live = 0;                                  // bit 2 c + u
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int x = 2 * t4 + u;
-            sl[u] = __shfl_sync(0xffffffffu, scale, x * 4);
-            m[u] = -INFINITY;
-            l[u] = 0.f;
-            big_e[u] = 0;
-            live[u] = x < a.R && x % a.T < w.s.cnt;
+        for (int c = 0; c < N; ++c) {
+            const float scale = convert_query<D>(a, qr[c]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int x = 8 * c + 2 * t4 + u;
+                sl[c][u] = __shfl_sync(0xffffffffu, scale, (2 * t4 + u) * 4);
+                m[c][u] = -INFINITY;
+                l[c][u] = 0.f;
+                big_e[c][u] = 0;
+                if (x < a.R && x % a.T < w.s.cnt) live |= 1u << (2 * c + u);
+            }
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[c][j][e] = 0.f;
         }
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-        auto sees = [&](int u, int key) {
-            return key < w.s.len || (key < w.s.end && live[u] && tree_sees(a, w.b, (2 * t4 + u) % a.T, key - w.s.len));
+        auto sees = [&](int c, int u, int key) {
+            return key < w.s.len ||
+                   (key < w.s.end && (live >> (2 * c + u) & 1) && tree_sees(a, w.b, (8 * c + 2 * t4 + u) % a.T, key - w.s.len));
         };
 
 #pragma unroll 1
@@ -220,64 +227,77 @@ __global__ void __launch_bounds__(32 * kWarps, kTreeMmaWarps / kWarps) tree_mma_
             warp_wait(bars + 8u * slot, (used / kStages) & 1, ctl);
             ++used;
 
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            float s[N][4];
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {  // 16 bytes of each key at a time: four k steps
-                const uint4 x0 = *reinterpret_cast<const uint4*>(kp + at16<D>(g8, D == 128 ? 2 * t4 + c : t4));
-                const uint4 x1 = *reinterpret_cast<const uint4*>(kp + at16<D>(g8 + 8, D == 128 ? 2 * t4 + c : t4));
+            for (int c = 0; c < N; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[c][e] = 0.f;
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {  // 16 bytes of each key at a time: four k steps
+                const uint4 x0 = *reinterpret_cast<const uint4*>(kp + at16<D>(g8, D == 128 ? 2 * t4 + h : t4));
+                const uint4 x1 = *reinterpret_cast<const uint4*>(kp + at16<D>(g8 + 8, D == 128 ? 2 * t4 + h : t4));
                 const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
                 for (int st = 0; st < 4; ++st) {
                     uint32_t a0, a1, a2, a3;
                     e4m3x4_to_f16(w0[st], a0, a2);
                     e4m3x4_to_f16(w1[st], a1, a3);
-                    mma16(s, a0, a1, a2, a3, qr[2 * (4 * c + st)], qr[2 * (4 * c + st) + 1]);
+#pragma unroll
+                    for (int c = 0; c < N; ++c) mma16(s[c], a0, a1, a2, a3, qr[c][2 * (4 * h + st)], qr[c][2 * (4 * h + st) + 1]);
                 }
             }
 
             const int k0 = row0 + i * kStep;
             const bool masked = k0 + kKeys > w.s.len;
             bool raise = false;
-            float alpha[2], p[2][2];  // p: [key][query]
+            float alpha[N][2];
+            uint32_t pb[N][2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float x0 = s[u] * ks[0], x1 = s[2 + u] * ks[1];
-                int new_e = group_e;
-                if (masked) {
-                    const bool s0 = sees(u, k0 + g8), s1 = sees(u, k0 + g8 + 8);
-                    if (!s0) x0 = -INFINITY;
-                    if (!s1) x1 = -INFINITY;
-                    new_e = max(s0 ? ve[0] : 0, s1 ? ve[1] : 0);
+            for (int c = 0; c < N; ++c) {
+                float p[2][2];  // [key][query]
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) new_e = max(new_e, __shfl_xor_sync(0xffffffffu, new_e, d));
+                for (int u = 0; u < 2; ++u) {
+                    float x0 = s[c][u] * ks[0], x1 = s[c][2 + u] * ks[1];
+                    int new_e = group_e;
+                    if (masked) {
+                        const bool s0 = sees(c, u, k0 + g8), s1 = sees(c, u, k0 + g8 + 8);
+                        if (!s0) x0 = -INFINITY;
+                        if (!s1) x1 = -INFINITY;
+                        new_e = max(s0 ? ve[0] : 0, s1 ? ve[1] : 0);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) new_e = max(new_e, __shfl_xor_sync(0xffffffffu, new_e, d));
+                    }
+                    new_e = max(new_e, big_e[c][u]);
+                    float mx = fmaxf(x0, x1);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    mx *= sl[c][u];
+                    const float to = mx > m[c][u] + 8.f ? mx : m[c][u], ref = to == -INFINITY ? 0.f : to;
+                    alpha[c][u] = 1.f;
+                    if (to != m[c][u] || new_e != big_e[c][u]) {
+                        const float keep = ex2_approx(m[c][u] - ref);
+                        l[c][u] *= keep;
+                        alpha[c][u] = keep * pow2(big_e[c][u] - new_e);
+                        m[c][u] = to;
+                        big_e[c][u] = new_e;
+                        raise = true;
+                    }
+                    p[0][u] = ex2_approx(fmaf(x0, sl[c][u], -ref));
+                    p[1][u] = ex2_approx(fmaf(x1, sl[c][u], -ref));
+                    l[c][u] += p[0][u] + p[1][u];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) p[e][u] *= pow2(min(ve[e] - new_e, 0) + 7);  // (above E: not seen, p = 0)
                 }
-                new_e = max(new_e, big_e[u]);
-                float mx = fmaxf(x0, x1);
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                mx *= sl[u];
-                const float to = mx > m[u] + 8.f ? mx : m[u], ref = to == -INFINITY ? 0.f : to;
-                alpha[u] = 1.f;
-                if (to != m[u] || new_e != big_e[u]) {
-                    const float keep = ex2_approx(m[u] - ref);
-                    l[u] *= keep;
-                    alpha[u] = keep * pow2(big_e[u] - new_e);
-                    m[u] = to;
-                    big_e[u] = new_e;
-                    raise = true;
-                }
-                p[0][u] = ex2_approx(fmaf(x0, sl[u], -ref));
-                p[1][u] = ex2_approx(fmaf(x1, sl[u], -ref));
-                l[u] += p[0][u] + p[1][u];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) p[e][u] *= pow2(min(ve[e] - new_e, 0) + 7);  // (above E: not seen, p = 0)
+                for (int e = 0; e < 2; ++e) pb[c][e] = transpose8(pack_f16x2(p[e][0], p[e][1]));
             }
-            const uint32_t pb[2] = {transpose8(pack_f16x2(p[0][0], p[0][1])), transpose8(pack_f16x2(p[1][0], p[1][1]))};
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-                for (int j = 0; j < kTiles; ++j)
+                for (int c = 0; c < N; ++c)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[j][e] *= alpha[e & 1];
+                    for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[c][j][e] *= alpha[c][e & 1];
             }
 
             // V: rows 2t, 2t + 1, 2t + 8, 2t + 9, eight of the thread's d / 8 columns at a time
@@ -316,17 +336,20 @@ __global__ void __launch_bounds__(32 * kWarps, kTreeMmaWarps / kWarps) tree_mma_
                         for (int r = 0; r < kKeys; ++r) {
                             const int er = (int)__shfl_sync(0xffffffffu, byte, r + 16);
                             if (k0 + r >= w.s.end) continue;
-                            const bool s0 = sees(0, k0 + r), s1 = sees(1, k0 + r);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const int d = g8 * (D / 8) + part * 8 + j;
-                                const uint32_t x = vp[at16<D>(r, d >> 4) + (d & 15)];
-                                if (!not_finite(x, er)) continue;
-                                float v, y0, y1, y2;
-                                e4m3x4_to_float(x, v, y0, y1, y2);
-                                v *= __uint_as_float((uint32_t)er << 23);
-                                if (s0) o[part * 4 + j / 2][2 * (j & 1)] += v;
-                                if (s1) o[part * 4 + j / 2][2 * (j & 1) + 1] += v;
+                            for (int c = 0; c < N; ++c) {
+                                const bool s0 = sees(c, 0, k0 + r), s1 = sees(c, 1, k0 + r);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const int d = g8 * (D / 8) + part * 8 + j;
+                                    const uint32_t x = vp[at16<D>(r, d >> 4) + (d & 15)];
+                                    if (!not_finite(x, er)) continue;
+                                    float v, y0, y1, y2;
+                                    e4m3x4_to_float(x, v, y0, y1, y2);
+                                    v *= __uint_as_float((uint32_t)er << 23);
+                                    if (s0) o[c][part * 4 + j / 2][2 * (j & 1)] += v;
+                                    if (s1) o[c][part * 4 + j / 2][2 * (j & 1) + 1] += v;
+                                }
                             }
                         }
                     }
@@ -338,7 +361,8 @@ __global__ void __launch_bounds__(32 * kWarps, kTreeMmaWarps / kWarps) tree_mma_
                         uint32_t a0, a1, a2, a3;
                         e4m3x4_to_f16(__byte_perm(vw[0][q], vw[1][q], h ? 0x7362 : 0x5140), a0, a1);
                         e4m3x4_to_f16(__byte_perm(vw[2][q], vw[3][q], h ? 0x7362 : 0x5140), a2, a3);
-                        mma16(o[part * 4 + 2 * q + h], a0, a1, a2, a3, pb[0], pb[1]);
+#pragma unroll
+                        for (int c = 0; c < N; ++c) mma16(o[c][part * 4 + 2 * q + h], a0, a1, a2, a3, pb[c][0], pb[c][1]);
                     }
             }
             __syncwarp();  // all lanes have read the slot
@@ -353,47 +377,51 @@ __global__ void __launch_bounds__(32 * kWarps, kTreeMmaWarps / kWarps) tree_mma_
 
         // the item's rows: the eight warps' m, l, E and O, in warp order (the next item's m, l come elsewhere: some warps
         // may still read these; its O are written behind the next barrier)
-        float4* ml = reinterpret_cast<float4*>(smem + C::kMl) + (item++ & 1) * kWarps * 8;
+        float4* ml = reinterpret_cast<float4*>(smem + C::kMl) + (item++ & 1) * kWarps * 8 * N;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int c = 0; c < N; ++c)
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) l[u] += __shfl_xor_sync(0xffffffffu, l[u], d);
-            if (g8 == 0) ml[warp * 8 + 2 * t4 + u] = make_float4(m[u], l[u], __int_as_float(big_e[u]), 0.f);
-        }
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[c][u] += __shfl_xor_sync(0xffffffffu, l[c][u], d);
+                if (g8 == 0) ml[(warp * N + c) * 8 + 2 * t4 + u] = make_float4(m[c][u], l[c][u], __int_as_float(big_e[c][u]), 0.f);
+            }
         __syncthreads();
         float4* xs = reinterpret_cast<float4*>(smem + C::kX);
-        constexpr int kFours = D / 32, kVecs = 2 * kFours;  // float4 per thread: [u][fours of its d / 8 columns]
+        constexpr int kFours = D / 32, kVecs = 2 * N * kFours;  // float4 per thread: [c][u][fours of its d / 8 columns]
         auto join = [&](int x, float& top, float& sum, int& top_e) {
             top = -INFINITY;
             top_e = 0;
             for (int k = 0; k < kWarps; ++k) {
-                const float4 v = ml[k * 8 + x];
+                const float4 v = ml[k * 8 * N + x];
                 top = fmaxf(top, v.x);
                 top_e = max(top_e, __float_as_int(v.z));
             }
             const float ref = top == -INFINITY ? 0.f : top;
             sum = 0.f;
             for (int k = 0; k < kWarps; ++k) {
-                const float4 v = ml[k * 8 + x];
+                const float4 v = ml[k * 8 * N + x];
                 // NaN scores alone leave no maximum
                 sum = v.x == -INFINITY && v.y != 0.f ? v.y : fmaf(v.y, ex2_approx(v.x - ref), sum);
             }
         };
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float top, sum;
-            int top_e;
-            join(2 * t4 + u, top, sum, top_e);
-            const float f = ex2_approx(m[u] - (top == -INFINITY ? 0.f : top)) * pow2(big_e[u] - top_e);
+        for (int c = 0; c < N; ++c)
 #pragma unroll
-            for (int c = 0; c < kFours; ++c)
-                xs[(warp * kVecs + u * kFours + c) * 32 + lane] =
-                    make_float4(o[2 * c][u] * f, o[2 * c][2 + u] * f, o[2 * c + 1][u] * f, o[2 * c + 1][2 + u] * f);
-        }
+            for (int u = 0; u < 2; ++u) {
+                float top, sum;
+                int top_e;
+                join(8 * c + 2 * t4 + u, top, sum, top_e);
+                const float f = ex2_approx(m[c][u] - (top == -INFINITY ? 0.f : top)) * pow2(big_e[c][u] - top_e);
+#pragma unroll
+                for (int k = 0; k < kFours; ++k)
+                    xs[(warp * kVecs + (2 * c + u) * kFours + k) * 32 + lane] =
+                        make_float4(o[c][2 * k][u] * f, o[c][2 * k][2 + u] * f, o[c][2 * k + 1][u] * f, o[c][2 * k + 1][2 + u] * f);
+            }
         __syncthreads();
 #pragma unroll 1
         for (int v = warp; v < kVecs; v += kWarps) {  // vector v of every warp
-            const int row = 2 * t4 + v / kFours, d = g8 * (D / 8) + v % kFours * 4;
+            const int row = v / (2 * kFours) * 8 + 2 * t4 + v / kFours % 2, d = g8 * (D / 8) + v % kFours * 4;
             if (row >= a.R) continue;
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -446,18 +474,18 @@ bool make_map(CUtensorMap* map, const void* base, long long rows, long long head
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int kWarps>
+template <int D, int kWarps, int N>
 cudaError_t launch(const TreeArgs& a, cudaStream_t s)
 {
-    using C = Cfg<D, kWarps>;
+    using C = Cfg<D, kWarps, N>;
     Maps maps;
     const long long heads = (long long)a.B * a.Hkv;
     if (!make_map<D>(&maps.k, a.k, a.cap, heads) || !make_map<D>(&maps.v, a.v, a.cap, heads)) return cudaErrorInvalidValue;
     static std::mutex mu;
     static bool done[64];
-    const cudaError_t e = allow_smem(tree_mma_kernel<D, kWarps>, (int)C::kSmem, mu, done);
+    const cudaError_t e = allow_smem(tree_mma_kernel<D, kWarps, N>, (int)C::kSmem, mu, done);
     if (e != cudaSuccess) return e;
-    tree_mma_kernel<D, kWarps><<<a.ctas, 32 * kWarps, C::kSmem, s>>>(maps, a);
+    tree_mma_kernel<D, kWarps, N><<<a.ctas, 32 * kWarps, C::kSmem, s>>>(maps, a);
     return cudaGetLastError();
 }
 
@@ -465,8 +493,9 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t s)
 
 cudaError_t launch_tree_mma(const TreeArgs& a, int d, int warps, cudaStream_t s)
 {
-    if (warps == 8) return d == 128 ? launch<128, 8>(a, s) : launch<64, 8>(a, s);
-    return d == 128 ? launch<128, 4>(a, s) : launch<64, 4>(a, s);
+    if (a.rt == kTreeMmaE4m3Rows) return d == 128 ? launch<128, 4, 2>(a, s) : launch<64, 4, 2>(a, s);
+    if (warps == 8) return d == 128 ? launch<128, 8, 1>(a, s) : launch<64, 8, 1>(a, s);
+    return d == 128 ? launch<128, 4, 1>(a, s) : launch<64, 4, 1>(a, s);
 }
 
 }  // namespace ra

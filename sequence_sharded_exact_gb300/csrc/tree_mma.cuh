@@ -1,4 +1,4 @@
-// tree_mma.cuh -- what the kernels for up to 8 query rows per kv head (tree_mma.cu, tree_mma_bf16.cu) share.
+// tree_mma.cuh -- what the kernels for few query rows per kv head (tree_mma.cu, tree_mma_bf16.cu) share.
 #pragma once
 
 #include <cuda.h>
