@@ -11,19 +11,19 @@
 // a transposition of 8 x 8 within the warp.
 //   * Queries: x 2^-e in f16, e such that the row's largest lies in [2^14, 2^15): a bf16's eight bits are exact down
 //     to 2^-28 of it.  The scales of rows and keys are applied to S.
-//   * Weights: p 2^(ev_j - E + 7) in f16, ev_j the exponent of key j's V row, E the largest so far of the rows that the
-//     query sees: eleven bits down to 2^-21 of weight 1 at E, weight and scale together.  The sum l takes p itself.
-//     The reference of p follows the row maximum only when that grows by more than 2^8, so O is seldom rescaled.
-//   * A CTA's warps take 16 rows in turn, with rings of their own that the TMA fills; m, l, E and O are
+//   * Weights: p 2^ev_j in f16, ev_j the exponent of key j's V row, 2^7 at a reference M of their own: eleven bits down to
+//     2^-21 of the largest, weight and scale together.  The sum l takes p itself, at its reference m.  Both follow the
+//     query's maximum only when that grows by more than 2^8: a vote per 16 rows, and reductions only where it says so.
+//   * A CTA's warps take 16 rows in turn, with rings of their own that the TMA fills; m, l, M and O are
 //     a warp's own until the item's end, where they meet in shared memory, in warp order.  The next item's first rows
 //     and its queries are on their way meanwhile.
 //
 // What bounds it: the memory, nearly.  A tile of 128 rows of 8 kv heads' e4m3 cache (d = 128) costs each of 152 SMs
-// 0.90 us, 5.5 TB/s (tree_tc_body.cuh: 1.46), one token over 131072 rows 53 us with both launches (it: 91).  A group of 16
-// rows is about 440 instructions, issued in 0.54 of the cycles: latency, which 16 warps per SM hide; 24 do not fit the
+// 0.95 us, 5.2 TB/s (tree_tc_body.cuh: 1.46), one token over 131072 rows 53 us with both launches (it: 91).  A group of 16
+// rows is some 400 instructions, issued in about half of the cycles: latency, which 16 warps per SM hide; 24 do not fit the
 // registers (80 each: spills, 60 us at 32 tiles per SM in place of 38), a third stage per ring changes nothing.  With query
 // rows as the products' 16 rows there are twice as many products and registers (65 us).  9 to 16 query rows: 131072 rows in
-// 77 us in place of 88 there, 64 sequences of 1000 rows in 58 in place of 83 (d = 64: 52 for 73, 37 for 64).
+// 82 us in place of 88 there, 64 sequences of 1000 rows in 60 in place of 83 (d = 64: 52 for 73, 37 for 64).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -42,7 +42,7 @@ struct Cfg {
     static constexpr uint32_t kHalf = kKeys * D;                          // bytes of 16 rows
     static constexpr uint32_t kRings = kWarps * kStages * 2 * kHalf;      // [warps][stages][k, v]
     static constexpr uint32_t kX = kRings;                                // exchange: [warps][N D / 16][lanes] float4
-    static constexpr uint32_t kMl = kX + kWarps * N * 32 * D;             // [2 items][warps][8 N] m, l, E's bits, 0
+    static constexpr uint32_t kMl = kX + kWarps * N * 32 * D;             // [2 items][warps][8 N] m, l, M, 0
     static constexpr uint32_t kBar = kMl + 2 * kWarps * 8 * N * 16;
     static constexpr uint32_t kAbort = kBar + kWarps * kStages * 8;
     static constexpr uint32_t kSmem = kAbort + 8 + 1024;  // slack for the 1024-byte alignment of the base
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
         if (w.goes_on()) border = w.border(a, blockIdx.x);
         const int row0 = group_row(w), n = groups(w);
         float o[N][kTiles][4], m[N][2], l[N][2], sl[N][2];  // queries 8 c + 2t + u
-        int big_e[N][2];                                    // E as the scale's byte
+        float top[N][2];                                    // M
         uint32_t live = 0;                                  // bit 2 c + u
 #pragma unroll
         for (int c = 0; c < N; ++c) {
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
                 sl[c][u] = __shfl_sync(0xffffffffu, scale, (2 * t4 + u) * 4);
                 m[c][u] = -INFINITY;
                 l[c][u] = 0.f;
-                big_e[c][u] = 0;
+                top[c][u] = -INFINITY;
                 if (x < a.R && x % a.T < w.s.cnt) live |= 1u << (2 * c + u);
             }
 #pragma unroll
@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
             bytes >>= 8;
             // keys g and g + 8: scales of K, exponents of V
             const float ks[2] = {__uint_as_float(__shfl_sync(0xffffffffu, byte, g8) << 23), __uint_as_float(__shfl_sync(0xffffffffu, byte, g8 + 8) << 23)};
-            const int ve[2] = {(int)__shfl_sync(0xffffffffu, byte, g8 + 16), (int)__shfl_sync(0xffffffffu, byte, g8 + 24)};
-            const int group_e = (int)__reduce_max_sync(0xffffffffu, lane < kKeys ? 0u : byte);
+            const float ve[2] = {(float)(int)__shfl_sync(0xffffffffu, byte, g8 + 16) - 127.f, (float)(int)__shfl_sync(0xffffffffu, byte, g8 + 24) - 127.f};
+            const bool huge = __any_sync(0xffffffffu, lane >= kKeys && byte >= (uint32_t)kHuge);
             warp_wait(bars + 8u * slot, (used / kStages) & 1, ctl);
             ++used;
 
@@ -250,54 +250,58 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
             const int k0 = row0 + i * kStep;
             const bool masked = k0 + kKeys > w.s.len;
             bool raise = false;
-            float alpha[N][2];
+            float y[N][2][2];  // scores: [query][key]
+#pragma unroll
+            for (int c = 0; c < N; ++c)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        y[c][u][e] = s[c][2 * e + u] * ks[e] * sl[c][u];
+                        if (masked && !sees(c, u, k0 + g8 + 8 * e)) y[c][u][e] = -INFINITY;
+                        raise |= y[c][u][e] > m[c][u] + 8.f || y[c][u][e] + ve[e] > top[c][u] + 8.f;
+                    }
+                }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int c = 0; c < N; ++c)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float my = fmaxf(y[c][u][0], y[c][u][1]), mz = fmaxf(y[c][u][0] + ve[0], y[c][u][1] + ve[1]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) {
+                            my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, d));
+                            mz = fmaxf(mz, __shfl_xor_sync(0xffffffffu, mz, d));
+                        }
+                        if (my > m[c][u] + 8.f) {
+                            l[c][u] *= ex2_approx(m[c][u] - my);
+                            m[c][u] = my;
+                        }
+                        float alpha = 1.f;
+                        if (mz > top[c][u] + 8.f) {
+                            alpha = ex2_approx(top[c][u] - mz);
+                            top[c][u] = mz;
+                        }
+#pragma unroll
+                        for (int j = 0; j < kTiles; ++j) {
+                            o[c][j][u] *= alpha;
+                            o[c][j][2 + u] *= alpha;
+                        }
+                    }
+            }
             uint32_t pb[N][2];
 #pragma unroll
             for (int c = 0; c < N; ++c) {
                 float p[2][2];  // [key][query]
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    float x0 = s[c][u] * ks[0], x1 = s[c][2 + u] * ks[1];
-                    int new_e = group_e;
-                    if (masked) {
-                        const bool s0 = sees(c, u, k0 + g8), s1 = sees(c, u, k0 + g8 + 8);
-                        if (!s0) x0 = -INFINITY;
-                        if (!s1) x1 = -INFINITY;
-                        new_e = max(s0 ? ve[0] : 0, s1 ? ve[1] : 0);
+                    const float ref = m[c][u] == -INFINITY ? 0.f : m[c][u], at = top[c][u] == -INFINITY ? 0.f : top[c][u] - 7.f;
+                    l[c][u] += ex2_approx(y[c][u][0] - ref) + ex2_approx(y[c][u][1] - ref);
 #pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) new_e = max(new_e, __shfl_xor_sync(0xffffffffu, new_e, d));
-                    }
-                    new_e = max(new_e, big_e[c][u]);
-                    float mx = fmaxf(x0, x1);
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                    mx *= sl[c][u];
-                    const float to = mx > m[c][u] + 8.f ? mx : m[c][u], ref = to == -INFINITY ? 0.f : to;
-                    alpha[c][u] = 1.f;
-                    if (to != m[c][u] || new_e != big_e[c][u]) {
-                        const float keep = ex2_approx(m[c][u] - ref);
-                        l[c][u] *= keep;
-                        alpha[c][u] = keep * pow2(big_e[c][u] - new_e);
-                        m[c][u] = to;
-                        big_e[c][u] = new_e;
-                        raise = true;
-                    }
-                    p[0][u] = ex2_approx(fmaf(x0, sl[c][u], -ref));
-                    p[1][u] = ex2_approx(fmaf(x1, sl[c][u], -ref));
-                    l[c][u] += p[0][u] + p[1][u];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) p[e][u] *= pow2(min(ve[e] - new_e, 0) + 7);  // (above E: not seen, p = 0)
+                    for (int e = 0; e < 2; ++e) p[e][u] = ex2_approx(y[c][u][e] + (ve[e] - at));
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) pb[c][e] = transpose8(pack_f16x2(p[e][0], p[e][1]));
-            }
-            if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-                for (int c = 0; c < N; ++c)
-#pragma unroll
-                    for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[c][j][e] *= alpha[c][e & 1];
             }
 
             // V: rows 2t, 2t + 1, 2t + 8, 2t + 9, eight of the thread's d / 8 columns at a time
@@ -313,8 +317,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
                 }
                 // Rows behind the sequence count as zeros.  NaN, and values whose scale takes them past float32, are
                 // cleared and added to the queries that see them: a weight of 0 would not hide them from the others.
-                if (masked || group_e >= kHuge) {
-                    bool odd = group_e >= kHuge;
+                if (masked || huge) {
+                    bool odd = huge;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -384,35 +388,33 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[c][u] += __shfl_xor_sync(0xffffffffu, l[c][u], d);
-                if (g8 == 0) ml[(warp * N + c) * 8 + 2 * t4 + u] = make_float4(m[c][u], l[c][u], __int_as_float(big_e[c][u]), 0.f);
+                if (g8 == 0) ml[(warp * N + c) * 8 + 2 * t4 + u] = make_float4(m[c][u], l[c][u], top[c][u], 0.f);
             }
         __syncthreads();
         float4* xs = reinterpret_cast<float4*>(smem + C::kX);
         constexpr int kFours = D / 32, kVecs = 2 * N * kFours;  // float4 per thread: [c][u][fours of its d / 8 columns]
-        auto join = [&](int x, float& top, float& sum, int& top_e) {
-            top = -INFINITY;
-            top_e = 0;
+        auto join = [&](int x, float& mr, float& lr, float& tr) {  // m, l and M of all
+            mr = tr = -INFINITY;
             for (int k = 0; k < kWarps; ++k) {
                 const float4 v = ml[k * 8 * N + x];
-                top = fmaxf(top, v.x);
-                top_e = max(top_e, __float_as_int(v.z));
+                mr = fmaxf(mr, v.x);
+                tr = fmaxf(tr, v.z);
             }
-            const float ref = top == -INFINITY ? 0.f : top;
-            sum = 0.f;
+            const float ref = mr == -INFINITY ? 0.f : mr;
+            lr = 0.f;
             for (int k = 0; k < kWarps; ++k) {
                 const float4 v = ml[k * 8 * N + x];
                 // NaN scores alone leave no maximum
-                sum = v.x == -INFINITY && v.y != 0.f ? v.y : fmaf(v.y, ex2_approx(v.x - ref), sum);
+                lr = v.x == -INFINITY && v.y != 0.f ? v.y : fmaf(v.y, ex2_approx(v.x - ref), lr);
             }
         };
 #pragma unroll
         for (int c = 0; c < N; ++c)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                float top, sum;
-                int top_e;
-                join(8 * c + 2 * t4 + u, top, sum, top_e);
-                const float f = ex2_approx(m[c][u] - (top == -INFINITY ? 0.f : top)) * pow2(big_e[c][u] - top_e);
+                float mr, lr, tr;
+                join(8 * c + 2 * t4 + u, mr, lr, tr);
+                const float f = ex2_approx(top[c][u] - (tr == -INFINITY ? 0.f : tr));
 #pragma unroll
                 for (int k = 0; k < kFours; ++k)
                     xs[(warp * kVecs + (2 * c + u) * kFours + k) * 32 + lane] =
@@ -429,15 +431,15 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
                 const float4 y = xs[(k * kVecs + v) * 32 + lane];
                 sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
             }
-            float mr, lr;
-            int top_e;
-            join(row, mr, lr, top_e);
+            float mr, lr, tr;
+            join(row, mr, lr, tr);
             const bool none = row % a.T >= cnt || (mr == -INFINITY && lr == 0.f);
             const long long grow = (long long)z * a.R + row;
-            const float inv = whole ? 1.0f / lr : 1.0f, up = __uint_as_float((uint32_t)top_e << 23);
+            // from M's reference to m's, in two steps: one could pass float32's range where the result does not
+            const float inv = whole ? 1.0f / lr : 1.0f, up = ex2_approx(0.5f * (tr - 7.f - (mr == -INFINITY ? 0.f : mr)));
             float* ps = &sum.x;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) ps[e] = none ? 0.f : ps[e] * 0x1p-7f * up * inv;
+            for (int e = 0; e < 4; ++e) ps[e] = none ? 0.f : ps[e] * up * inv * up;
             if (whole) {
                 if (a.bf16_out)
                     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + grow * D + d) =

@@ -2,8 +2,9 @@
 //
 // The products of tree_mma.cu, S^T = K Q^T and O^T += V^T P^T with 16 cached rows, or columns of V, against 8 queries
 // (mma.m16n8k16, bf16, float32 sums), a warp by itself with 16 cached rows at a time; K and V are operands as they
-// are cached, V by transposing loads (ldmatrix).  P is bf16, as on the tcgen05 path, and so is the correction of the
-// normaliser for the largest weight's rounding.  A CTA has four warps, two or three CTAs run on an SM: while one joins its
+// are cached, V by transposing loads (ldmatrix).  P is bf16, and the normaliser the sum of the weights as they were
+// rounded (lse takes them unrounded); their reference follows the maximum only when that grows by more than 2^8: a vote per
+// 16 rows, and reductions only where it says so.  A CTA has four warps, two or three CTAs run on an SM: while one joins its
 // warps' results at an item's end the others stream.
 //
 // What bounds it: the memory.  A tile of 128 rows of 8 kv heads (d = 128, 64 KB) costs each of 152 SMs 1.30 us, 7.6
@@ -126,13 +127,13 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
     do {
         if (w.goes_on()) border = w.border(a, blockIdx.x);
         const int row0 = group_row(w), n = groups(w);
-        float o[kTiles][4], m[2], l[2], fix[2];  // queries 2t + u; fix: what the largest weights' rounding adds to l
+        float o[kTiles][4], m[2], l[2], den[2];  // queries 2t + u; den: the sum of the rounded weights
         bool live[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int x = 2 * t4 + u;
             m[u] = -INFINITY;
-            l[u] = fix[u] = 0.f;
+            l[u] = den[u] = 0.f;
             live[u] = x < a.R && x % a.T < w.s.cnt;
         }
 #pragma unroll
@@ -158,39 +159,51 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
             const int k0 = row0 + i * kWarps * kKeys;
             const bool masked = k0 + kKeys > w.s.len;
             bool raise = false;
-            float alpha[2], p[2][2];  // p: [key][query]
+            float y[2][2];  // scores: [query][key]
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float x0 = s[u], x1 = s[2 + u];  // keys g and g + 8
-                if (masked) {
-                    if (!sees(u, k0 + g8)) x0 = -INFINITY;
-                    if (!sees(u, k0 + g8 + 8)) x1 = -INFINITY;
-                }
-                float mx = fmaxf(x0, x1);
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                mx *= a.scale_log2;
-                const float to = mx > m[u] + 8.f ? mx : m[u], ref = to == -INFINITY ? 0.f : to;
-                alpha[u] = 1.f;
-                if (to != m[u]) {
-                    alpha[u] = ex2_approx(m[u] - ref);
-                    l[u] *= alpha[u];
-                    fix[u] *= alpha[u];
-                    m[u] = to;
-                    raise = true;
+                for (int e = 0; e < 2; ++e) {
+                    y[u][e] = s[2 * e + u] * a.scale_log2;
+                    if (masked && !sees(u, k0 + g8 + 8 * e)) y[u][e] = -INFINITY;
+                    raise |= y[u][e] > m[u] + 8.f;
                 }
-                p[0][u] = ex2_approx(fmaf(x0, a.scale_log2, -ref));
-                p[1][u] = ex2_approx(fmaf(x1, a.scale_log2, -ref));
-                l[u] += p[0][u] + p[1][u];
-                const float top = ex2_approx(mx - ref);
-                fix[u] += __uint_as_float(pack_bf16x2(top, 0.f) << 16) - top;
-            }
-            const uint32_t pb[2] = {transpose8(pack_bf16x2(p[0][0], p[0][1])), transpose8(pack_bf16x2(p[1][0], p[1][1]))};
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-                for (int j = 0; j < kTiles; ++j)
+                for (int u = 0; u < 2; ++u) {
+                    float my = fmaxf(y[u][0], y[u][1]), alpha = 1.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[j][e] *= alpha[e & 1];
+                    for (int d = 4; d < 32; d <<= 1) my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, d));
+                    if (my > m[u] + 8.f) {
+                        alpha = ex2_approx(m[u] - my);
+                        m[u] = my;
+                    }
+                    l[u] *= alpha;
+                    den[u] *= alpha;
+#pragma unroll
+                    for (int j = 0; j < kTiles; ++j) {
+                        o[j][u] *= alpha;
+                        o[j][2 + u] *= alpha;
+                    }
+                }
+            }
+            uint32_t pb[2];
+            {
+                float p[2][2];  // [key][query]
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float ref = m[u] == -INFINITY ? 0.f : m[u];
+                    p[0][u] = ex2_approx(y[u][0] - ref);
+                    p[1][u] = ex2_approx(y[u][1] - ref);
+                    l[u] += p[0][u] + p[1][u];
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t w2 = pack_bf16x2(p[e][0], p[e][1]);
+                    den[0] += __uint_as_float(w2 << 16);
+                    den[1] += __uint_as_float(w2 & 0xffff0000u);
+                    pb[e] = transpose8(w2);
+                }
             }
             // Rows of V behind the sequence count as zeros, and what is not finite in drafted tokens' rows is cleared and
             // added to the queries that see it: a weight of 0 would not hide it from the others.
@@ -256,8 +269,11 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) l[u] += __shfl_xor_sync(0xffffffffu, l[u], d);
-            if (g8 == 0) ml[warp * 8 + 2 * t4 + u] = make_float4(m[u], l[u], l[u] + fix[u], 0.f);
+            for (int d = 4; d < 32; d <<= 1) {
+                l[u] += __shfl_xor_sync(0xffffffffu, l[u], d);
+                den[u] += __shfl_xor_sync(0xffffffffu, den[u], d);
+            }
+            if (g8 == 0) ml[warp * 8 + 2 * t4 + u] = make_float4(m[u], l[u], den[u], 0.f);
         }
         __syncthreads();
         float* xs = reinterpret_cast<float*>(smem + C::kX);
@@ -270,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
         }
         // a thread sums four columns of one row, 64 columns of all rows at a time
         const int row = threadIdx.x >> 4;
-        float top = -INFINITY, lr = 0.f, den = 0.f;
+        float top = -INFINITY, lr = 0.f, dr = 0.f;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) top = fmaxf(top, ml[k * 8 + row].x);
         const float ref = top == -INFINITY ? 0.f : top;
@@ -280,11 +296,11 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
             const float g = ex2_approx(y.x - ref);
             const bool nan = y.x == -INFINITY && y.y != 0.f;  // NaN scores alone leave no maximum
             lr = nan ? y.y : fmaf(y.y, g, lr);
-            den = nan ? y.y : fmaf(y.z, g, den);
+            dr = nan ? y.y : fmaf(y.z, g, dr);
         }
         const bool none = row % a.T >= cnt || (top == -INFINITY && lr == 0.f);
         const long long grow = (long long)z * a.R + row;
-        const float inv = whole ? 1.0f / den : 1.0f;
+        const float inv = whole ? 1.0f / dr : 1.0f;
 #pragma unroll
         for (int part = 0; part < D / 64; ++part) {
             if (part) __syncthreads();
@@ -315,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) a.part_o[(pslot * D + d + e) * a.rt + row] = ps[e];
-                if (d == 0) *reinterpret_cast<float4*>(a.part_ml + (pslot * a.rt + row) * 4) = make_float4(top, lr, den, 0.f);
+                if (d == 0) *reinterpret_cast<float4*>(a.part_ml + (pslot * a.rt + row) * 4) = make_float4(top, lr, dr, 0.f);
             }
         }
     } while (more);

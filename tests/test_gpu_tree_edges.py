@@ -253,3 +253,19 @@ def test_many_short_sequences(T, d, cdt):
     cu.check_tree(got, cu.tree(q, kk, vv, lens, None, ntok), 2.0 ** -8, BF)
     again = ra.tree_fwd(q, cache, _i32(lens), ntok=_i32(ntok))
     assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("H,Hkv,T,d", ROWS)
+@pytest.mark.parametrize("at", [0, 130, 419])
+def test_a_row_of_huge_values_that_hardly_counts(H, Hkv, T, d, dtype, at):
+    """One row of v is 2^40 times the others and weighs e^-50 or less of them (2^-72: its contribution is 2^-32 of theirs):
+    the others keep their precision, wherever it lies."""
+    B, n = 1, 420
+    cap = n + T
+    u = torch.ones(d, device=DEV)
+    k, v = 0.3 * _randn(B, Hkv, cap, d, seed=111), _randn(B, Hkv, cap, d, seed=112)
+    k[:, :, at] = -60 / d ** 0.5 * u
+    v[:, :, at] *= 2.0 ** 40
+    q = (u + 0.05 * _randn(B, H, T, d, seed=113)).to(dtype)
+    _check(q, _cache_of(k, v, dtype, E4M3), [n], None)
