@@ -59,6 +59,8 @@ def build_calls(nvcc, force: bool = False) -> str:
     import torch
 
     target, src = calls_path(), os.path.join(CSRC, "calls.cpp")
+    if torch.version.cuda is None:  # a torch without CUDA has nothing to call it with
+        return target
     if not force and not _stale(target, [src, os.path.join(INCLUDE, "ringattn.h"), os.path.abspath(__file__)]):
         return target
     root = os.path.dirname(torch.__file__)
