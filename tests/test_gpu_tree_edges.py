@@ -269,3 +269,25 @@ def test_a_row_of_huge_values_that_hardly_counts(H, Hkv, T, d, dtype, at):
     v[:, :, at] *= 2.0 ** 40
     q = (u + 0.05 * _randn(B, H, T, d, seed=113)).to(dtype)
     _check(q, _cache_of(k, v, dtype, E4M3), [n], None)
+
+
+@pytest.mark.parametrize("cdt,T,cap", [(E4M3, 2, 1 << 22), (E4M3, 6, 1 << 22), (E4M3, 20, 1 << 22), (BF, 20, 1 << 21)])
+def test_the_far_end_of_a_cache_of_more_than_32_bits(cdt, T, cap):
+    """The last sequence of a cache of more than 2^32 bytes per tensor, its prefix all zeros (each weighs 1) up to the
+    last T rows; 4, 12 and 40 query rows per kv head."""
+    B, H, Hkv, d = 5, 4, 2, 128
+    cache = ra.cache_alloc(B, Hkv, cap, d, cdt)
+    k, v, q = _randn(B, Hkv, T, d, seed=121, dtype=BF), _randn(B, Hkv, T, d, seed=122, dtype=BF), _randn(B, H, T, d, seed=123, dtype=BF)
+    lens = _i32([0, 0, 0, 0, cap - T])
+    ra.cache_write(cache, k, v, lens)
+    out, lse = ra.tree_fwd(q, cache, lens)
+    kk, vv = (x[4].double() for x in ra.cache_read(cache, T, row0=cap - T))
+    s = torch.einsum("hgtd,hjd->hgtj", q[4].view(Hkv, H // Hkv, T, d).double(), kk) / d ** 0.5
+    e = s.exp() * torch.ones(T, T, device=DEV).tril().double()
+    total = e.sum(-1) + cap - T
+    assert float((lse[4].view(Hkv, H // Hkv, T).double() - total.log()).abs().max()) <= 1e-4
+    ref = torch.einsum("hgtj,hjd->hgtd", e, vv) / total.unsqueeze(-1)
+    mag = torch.einsum("hgtj,hjd->hgtd", e, vv.abs()) / total.unsqueeze(-1)
+    # a weight's rounding to bfloat16 and the output's, 2^-8 each of the sum of magnitudes, and 2^-12 for the rest
+    assert float(((out[4].view(Hkv, H // Hkv, T, d).double() - ref).abs() - (2.0 ** -7 + 2.0 ** -12) * mag).max()) <= 0
+    assert torch.isfinite(out[:4]).all()
