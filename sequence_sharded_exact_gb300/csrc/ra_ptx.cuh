@@ -80,6 +80,13 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     return r;
 }
 
+// d + the two bf16 values of w, each to its own float32 sum.
+__device__ __forceinline__ float2 add_bf16x2(float2 d, uint32_t w)
+{
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.f32.bf16 %0, l, %0;\n\tadd.f32.bf16 %1, h, %1;\n\t}" : "+f"(d.x), "+f"(d.y) : "r"(w));
+    return d;
+}
+
 // Two float32 to e4m3, nearest even, lo in the low byte; finite values beyond +-448 become +-448.
 __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi)
 {

@@ -685,7 +685,7 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
         const bool live = x < a.R && tq < w.s.cnt;
         const bool any_live = __any_sync(0xffffffffu, live);
         const int n = w.t1 - w.t0;
-        float m_run = -INFINITY, l_run = 0.f, c_run = 0.f, sl2 = a.scale_log2;
+        float m_run = -INFINITY, l_run = 0.f, den_run = 0.f, sl2 = a.scale_log2;
         bool first = true;
         for (int i = kNq == 1 ? wg : 0; i < n; i += kNq == 1 ? 2 : 1) {
             const int k0 = (w.t0 + i) * kTreeTile;
@@ -722,8 +722,7 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
             }
             // 32 columns of S at a time, their weights written over S as it is read.  The loop is not unrolled:
             // the roles' loops run side by side and wait for the instruction cache when they do not fit it.
-            float m_tile = -INFINITY;
-            float2 s2 = make_float2(0.f, 0.f);
+            float2 s2 = make_float2(0.f, 0.f), d2 = make_float2(0.f, 0.f);  // of the weights, and of the weights as rounded
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t r[32];
@@ -755,7 +754,6 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) m4[(e >> 1) & 3] = max3f(m4[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
                 const float m_new = max3f(max3f(m4[0], m4[1], m4[2]), m4[3], -INFINITY) * sl2;
-                m_tile = fmaxf(m_tile, m_new);
                 const bool raise = live && m_new > m_run + 8.0f;
                 if (__any_sync(0xffffffffu, raise)) {
                     // The reference goes up, by a whole number of binades once there is one, and with it go the
@@ -764,8 +762,9 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
                     const float to = raise ? (m_run == -INFINITY ? m_new : m_run + ceilf(m_new - m_run)) : m_run;
                     const float alpha = to == m_run ? 1.0f : ex2_approx(m_run - to);
                     l_run *= alpha;
-                    c_run *= alpha;
+                    den_run *= alpha;
                     s2 = mul2(s2, make_float2(alpha, alpha));
+                    d2 = mul2(d2, make_float2(alpha, alpha));
                     m_run = to;
 #pragma unroll 1
                     for (int k = first ? 0 : kHd / 16; k > 0; --k) {
@@ -793,26 +792,29 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
                 }
                 const float ref = m_run == -INFINITY ? 0.f : m_run;
                 const float2 scale2 = make_float2(sl2, sl2), nref2 = make_float2(-ref, -ref);
-                float2 s4[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                float2 s4[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, d4[2] = {s4[0], s4[0]};
                 uint32_t pk[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                     const float2 x2 = fma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), scale2, nref2);
                     const float2 p2 = make_float2(ex2_approx(x2.x), ex2_approx(x2.y));
                     s4[(e >> 1) & 1] = add2(s4[(e >> 1) & 1], p2);
-                    pk[e / 2] = pack_bf16x2(p2.x, p2.y);
+                    const uint32_t w2 = pack_bf16x2(p2.x, p2.y);
+                    d4[(e >> 1) & 1] = add_bf16x2(d4[(e >> 1) & 1], w2);
+                    pk[e / 2] = w2;
                 }
                 tmem_st_32x32b_x16(tS + 16 * c, pk);
                 s2 = add2(s2, add2(s4[0], s4[1]));
+                d2 = add2(d2, add2(d4[0], d4[1]));
             }
             if constexpr (kE4) {
                 if (lane == 0) mbar_arrive(bar(C::bXEmpty + sx));
             }
-            // the largest weight's rounding to bf16 goes into the normaliser, so that a row that one key
-            // dominates is divided by the weight that its V row got; lse keeps the unrounded sum
-            const float p_max = m_tile == -INFINITY ? 0.f : ex2_approx(m_tile - m_run);
+            // The normaliser is the sum of the weights as the product gets them: where many keys share a weight their
+            // roundings go the same way, and a row that one key dominates is divided by that key's.  lse takes the
+            // unrounded sum.
             l_run += s2.x + s2.y;
-            c_run += __uint_as_float(pack_bf16x2(p_max, 0.f) << 16) - p_max;
+            den_run += d2.x + d2.y;
             tmem_st_wait();
             tc_fence_before_sync();
             __syncwarp();
@@ -829,7 +831,7 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
         }
 
         // the item's rows: O of both warpgroups (kNq == 1), or of this one
-        float m = m_run, l = l_run, den = l_run + c_run, w0 = 1.f, w1 = 0.f;
+        float m = m_run, l = l_run, den = den_run, w0 = 1.f, w1 = 0.f;
         const int n1 = kNq == 1 ? n >> 1 : 0;
         if constexpr (kNq == 1) {
             float4* ml = reinterpret_cast<float4*>(smem + C::kMl);
