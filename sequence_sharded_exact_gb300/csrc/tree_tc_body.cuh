@@ -452,7 +452,9 @@ __device__ __forceinline__ void split_queries(const TreeArgs& a, uint8_t* smem, 
             int e = (int)(big >> 23) - 135 + ((big & 0x7fffffu) > 0x600000u ? 1 : 0);
             e = !finite || e < -126 ? -126 : e;
             const float down = finite ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
-            if (c == 0 && x < rows) scale[x] = finite ? __uint_as_float((uint32_t)(127 + e) << 23) : __uint_as_float(0x7fc00000u);
+            // a row that is not finite: its elements that are not become NaN below (times 0), and with them its scores, of which
+            // the mask still hides what it hides
+            if (c == 0 && x < rows) scale[x] = __uint_as_float((uint32_t)(127 + e) << 23);
             uint2 hi, lo;
             uint32_t* ph = &hi.x;
             uint32_t* pl = &lo.x;
