@@ -95,6 +95,14 @@ __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi)
     return r;
 }
 
+// Two float32 to e5m2 (three significant bits, down to 2^-16), nearest even.
+__device__ __forceinline__ uint16_t e5m2x2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Four packed e4m3 values to float32 (exact: every e4m3 value is a float16 value).
 __device__ __forceinline__ void e4m3x4_to_float(uint32_t w, float& a, float& b, float& c, float& d)
 {

@@ -19,10 +19,12 @@
 // P V would still be NaN, so warps 12-15 clear the rows of V behind the sequence, and non-finite elements
 // of drafted tokens' rows, in shared memory before the product; those elements are added afterwards to
 // the rows that do see them (rare, from global memory).
-// e4m3: K goes into the products as it is cached.  The queries are split into two e4m3 values,
-// x 2^-e = hi + lo with a power-of-two scale per row: hi takes four significant bits, the rest of a bf16's
-// eight is exact in lo (elements below 2^-10 of the row's largest lose what lies below 2^-18 of it), so S
-// is two e4m3 products at twice the rate, with float32 sums.  The row and column scales are applied to
+// e4m3: K goes into the products as it is cached.  The queries are split into two 8-bit parts, x 2^-e = hi + lo with
+// a power-of-two scale per row that brings its largest element to 224 or more: hi in e4m3 takes four significant bits, lo
+// in e5m2 the other four of a bf16, exactly (they are at most 8 units of its last place), down to elements of 2^-6, 2^-13 of
+// the row's largest; what is smaller is off by at most 2^-14, 2^-21 of the largest (lo in e4m3, whose steps end at 2^-9,
+// was exact down to 2^-2 and off by up to 2^-10).  So S is two 8-bit products at twice the rate, with float32
+// sums.  The row and column scales are applied to
 // S.  P keeps bf16 (an e4m3 P would lose weights below 2^-9 of the largest, which add up over a long
 // cache), so warps 12-15 turn V into bf16, exactly, scale included.
 //
@@ -187,12 +189,12 @@ __device__ __forceinline__ void lead_commit(uint32_t lead, uint32_t bar)
         : "memory");
 }
 
-// kind::f8f6f4 (e4m3 operands, f32 accumulate): formats 0, the other fields as kind::f16's.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N)
+// kind::f8f6f4 (f32 accumulate): B in e4m3 (format 0), A in e4m3 or e5m2 (format 1); the other fields as kind::f16's.
+__host__ __device__ constexpr uint32_t idesc_8bit_f32(int M, int N, bool a_e5m2)
 {
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+    return (1u << 4) | (a_e5m2 ? 1u << 7 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void lead_mma_ss_e4m3(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void lead_mma_ss_8bit(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                                  uint32_t accumulate)
 {
     asm volatile(
@@ -217,8 +219,8 @@ __device__ __forceinline__ void issue_s(uint32_t lead, uint32_t sbase, uint32_t 
         for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int kk = 0; kk < kHd / 32; ++kk)
-                lead_mma_ss_e4m3(lead, d, sdesc_at(q, (uint32_t)part * 128 * kHd + (uint32_t)kk * 32, hi), sdesc_at(k, (uint32_t)kk * 32, hi),
-                            idesc_e4m3_f32(128, 128), part + kk > 0 ? 1u : 0u);
+                lead_mma_ss_8bit(lead, d, sdesc_at(q, (uint32_t)part * 128 * kHd + (uint32_t)kk * 32, hi), sdesc_at(k, (uint32_t)kk * 32, hi),
+                            idesc_8bit_f32(128, 128, part == 1), part + kk > 0 ? 1u : 0u);
     } else {
 #pragma unroll
         for (int kk = 0; kk < kHd / 16; ++kk) {
@@ -417,7 +419,7 @@ __device__ __forceinline__ uint32_t qk_offset(int row, int c16)  // 16-byte chun
     return kHd == 128 ? (uint32_t)(row * 128 + ((c16 ^ (row & 7)) << 4)) : (uint32_t)(row * 64 + ((c16 ^ ((row >> 1) & 3)) << 4));
 }
 
-// An item's queries as hi and lo e4m3 values with the row's scale, by the softmax warps; kHd / 8 lanes share a row.  Rows
+// An item's queries as hi (e4m3) and lo (e5m2) with the row's scale, by the softmax warps; kHd / 8 lanes share a row.  Rows
 // past the kv head's keep what they hold: it reaches no row of S that is read.
 template <int kNq>
 __device__ __forceinline__ void split_queries(const TreeArgs& a, uint8_t* smem, int b, int g, int r, uint32_t item)
@@ -465,7 +467,7 @@ __device__ __forceinline__ void split_queries(const TreeArgs& a, uint8_t* smem, 
                 ph[i] = (uint32_t)e4m3x2(f0, f1) | (uint32_t)e4m3x2(f2, f3) << 16;
                 float h0, h1, h2, h3;
                 e4m3x4_to_float(ph[i], h0, h1, h2, h3);
-                pl[i] = (uint32_t)e4m3x2(f0 - h0, f1 - h1) | (uint32_t)e4m3x2(f2 - h2, f3 - h3) << 16;
+                pl[i] = (uint32_t)e5m2x2(f0 - h0, f1 - h1) | (uint32_t)e5m2x2(f2 - h2, f3 - h3) << 16;
             }
             uint8_t* q = smem + C::kQ + (uint32_t)(x >> 7) * C::kBytesQ + qk_offset(x & 127, c >> 1) + (c & 1) * 8;
             if (x < rows) {

@@ -1,8 +1,9 @@
 """Queries of the attention over a cache that ask much of their form in the products: not finite in a row that sees
-nothing."""
+nothing, or with one element far above the others."""
 import pytest
 import torch
 
+import cache_util as cu
 import sequence_sharded_exact_gb300 as ra
 
 pytestmark = pytest.mark.gpu
@@ -50,3 +51,36 @@ def test_a_row_that_sees_nothing_is_empty_whatever_its_query_holds(H, Hkv, T, d,
     assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
     assert bool((out[1, 0, 0] == 0).all()) and float(lse[1, 0, 0]) == -float("inf")
     assert bool((out[0, :, T - 1] == 0).all()) and bool((lse[0, :, T - 1] == -float("inf")).all())
+
+
+@pytest.mark.parametrize("dtype,cdt", TYPES)
+@pytest.mark.parametrize("H,Hkv,T,d", ROWS)
+def test_a_query_with_one_element_far_above_the_others(H, Hkv, T, d, dtype, cdt):
+    """Element 0 of every query is 2^12 times the others' size, and the keys have 0 there: the scores are the other
+    elements'.  One to three keys, so that lse, which no rounding of weights touches, shows a score's error.
+
+    bfloat16 queries of more than 16 rows per kv head over e4m3 are two 8-bit parts: exact down to 2^-13 of the row's
+    largest, below that off by at most 2^-21 of it, so a score is off by sum_i e_i |k_i| / sqrt(d) with e_i that for the small
+    elements alone.  Everything else holds them exactly."""
+    B = 3
+    k, v = _randn(B, Hkv, T + 3, d, seed=11), _randn(B, Hkv, T + 3, d, seed=12)
+    k[..., 0] = 0
+    cache = _cache_of(k, v, dtype, cdt)
+    q = _randn(B, H, T, d, seed=13)
+    q[..., 0] = 2.0 ** 12
+    q = q.to(dtype)
+    lens, mask = [1, 2, 3], torch.zeros(T, T, dtype=torch.bool)
+    out, lse = ra.tree_fwd(q.to(DEV), cache, torch.tensor(lens, dtype=torch.int32, device=DEV), mask=mask.to(DEV), out_dtype=F32)
+    kk, vv = cu.cache_values(cache)
+    ref, ref_lse, mag, big = cu.tree(q, kk, vv, lens, mask, None)
+    split = dtype == BF and cdt == E4M3 and H // Hkv * T > 16
+    a = q.double().abs()
+    top = a.amax(-1, keepdim=True)
+    e = torch.where(a < 2.0 ** -13 * top, 2.0 ** -21 * top, torch.zeros_like(top)) if split else torch.zeros_like(a)
+    most = kk.abs()[:, :, :3].amax(2).repeat_interleave(H // Hkv, 1).unsqueeze(2)  # of the (at most three) keys, per element
+    s_err = (e * most).sum(-1) / d ** 0.5 + 2.0 ** -18 * (1 + big)
+    over = (lse.cpu().double() - ref_lse).abs() - s_err - 2.0 ** -22 * ref_lse.abs()
+    assert float(over.max()) <= 0, f"lse off by {float(over.max()):.3e} beyond its bound"
+    weight_eps = 2.0 ** -8 if dtype == BF else 0.0
+    over = (out.cpu().double() - ref).abs() - mag * (weight_eps + 2 * (s_err + 2.0 ** -20)).unsqueeze(-1) - 2.0 ** -23 * ref.abs()
+    assert float(over.max()) <= 0, f"out off by {float(over.max()):.3e} beyond its bound"
