@@ -12,6 +12,7 @@ import importlib.machinery
 import importlib.util
 import os
 import threading
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
@@ -172,12 +173,16 @@ def _load_calls(lib):
     if not os.path.exists(path):
         return
     name = __package__ + "._calls"
-    loader = importlib.machinery.ExtensionFileLoader(name, path)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
-    loader.exec_module(module)
-    module.bind(*(ctypes.cast(getattr(lib, "ring_attn_" + f), ctypes.c_void_p).value for f in (
-        "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size", "cache_write", "cache_read", "tree_fwd",
-        "tree_fwd_workspace_size")))
+    try:
+        loader = importlib.machinery.ExtensionFileLoader(name, path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
+        loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(lib, "ring_attn_" + f), ctypes.c_void_p).value for f in (
+            "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size", "cache_write", "cache_read", "tree_fwd",
+            "tree_fwd_workspace_size")))
+    except (ImportError, OSError, AttributeError, TypeError, ValueError) as e:
+        warnings.warn(f"the compiled calls in {path} do not load, calls go through Python: {e}", RuntimeWarning)
+        return
     _calls = module
 
 

@@ -14,6 +14,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -56,6 +57,8 @@ def calls_path() -> str:
 
 
 def build_calls(nvcc, force: bool = False) -> str:
+    """Builds the compiled calls if they are stale.  They only save the host's time: where they do not compile (no C++
+    compiler, no Python headers) this warns, leaves none behind, and the binding's Python form of them runs."""
     import torch
 
     target, src = calls_path(), os.path.join(CSRC, "calls.cpp")
@@ -70,9 +73,16 @@ def build_calls(nvcc, force: bool = False) -> str:
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in include), src, "-o", tmp,
            "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"compiling calls.cpp failed:\n{r.stdout}\n{r.stderr}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = "" if r.returncode == 0 else f"{r.stdout}\n{r.stderr}" or f"status {r.returncode}"
+    except OSError as e:
+        failed = str(e)
+    if failed:
+        if os.path.exists(target):
+            os.remove(target)
+        warnings.warn(f"compiling calls.cpp failed, calls go through Python:\n{failed}", RuntimeWarning)
+        return target
     os.replace(tmp, target)
     return target
 
