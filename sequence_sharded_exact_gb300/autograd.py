@@ -47,12 +47,17 @@ def ring_attention(q, k, v, n_shards, causal=True, layout="zigzag", f32_out=Fals
     return _RingAttention.apply(q, k, v, n_shards, causal, layout, f32_out)
 
 
+def _dense(t):
+    """t, or a contiguous copy if it is not contiguous or off a 16-byte boundary (a view into a larger tensor)."""
+    return t if t.is_contiguous() and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
 class _QkNormRope(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, wq, wk, n_shards, layout, base, eps, shard, positions):
         q, k = binding.as_rows(q), binding.as_rows(k)
         cfg = dict(n_shards=n_shards, layout=layout, base=base, eps=eps, shard=shard)
-        q_out, k_out = binding.qk_norm_rope(q, k, wq.float().contiguous(), wk.float().contiguous(), positions=positions, **cfg)
+        q_out, k_out = binding.qk_norm_rope(q, k, _dense(wq.float()), _dense(wk.float()), positions=positions, **cfg)
         ctx.save_for_backward(q, k, wq, wk, positions)
         ctx.cfg = cfg
         return q_out, k_out
@@ -61,14 +66,14 @@ class _QkNormRope(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, wq, wk, positions = ctx.saved_tensors
-        dq, dk, dwq, dwk = binding.qk_norm_rope_bwd(q, k, wq.float().contiguous(), wk.float().contiguous(),
-                                                    dq_out.contiguous(), dk_out.contiguous(), positions=positions, **ctx.cfg)
+        dq, dk, dwq, dwk = binding.qk_norm_rope_bwd(q, k, _dense(wq.float()), _dense(wk.float()),
+                                                    _dense(dq_out), _dense(dk_out), positions=positions, **ctx.cfg)
         return dq, dk, dwq.to(wq.dtype), dwk.to(wk.dtype), None, None, None, None, None, None
 
 
 def ring_qk_norm_rope(q, k, wq, wk, n_shards=1, layout="contiguous", base=10000.0, eps=1e-6, shard=None, positions=None):
     """Norms of every query and key head and the rotation by natural position in one pass, in front of
     ring_attention (or, with `shard`, of one device's ring): differentiable with respect to q [B,H,rows,d],
-    k [B,Hkv,rows,d] and the weights wq, wk [d] (any float dtype).  See qk_norm_rope for the arguments; q and k
-    that it cannot read where they lie are copied."""
+    k [B,Hkv,rows,d] and the weights wq, wk [d] (any float dtype).  See qk_norm_rope for the arguments; q, k, the
+    weights and the outputs' gradients are copied where the calls cannot read them as they lie."""
     return _QkNormRope.apply(q, k, wq, wk, n_shards, layout, base, eps, shard, positions)
