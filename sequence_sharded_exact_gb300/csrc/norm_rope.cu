@@ -114,7 +114,8 @@ __device__ __forceinline__ void angles(const NormRopeArgs& a, int ch, long long 
 #pragma unroll
     for (int j = 0; j < PAIRS; ++j) {
         const unsigned long long u = (unsigned long long)p * a.turn[ch * PAIRS + j];
-        sincospif(2.0f * ((float)(unsigned)(u >> 32) * 2.3283064365386963e-10f), &s[j], &c[j]);  // 2^-32
+        // as a signed fraction, [-1/2, 1/2) turn: a small angle of either sign keeps a float32's precision
+        sincospif(2.0f * ((float)(int)(unsigned)(u >> 32) * 2.3283064365386963e-10f), &s[j], &c[j]);  // 2^-32
     }
 }
 
