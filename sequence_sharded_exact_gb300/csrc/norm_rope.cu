@@ -34,7 +34,6 @@ namespace ra {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBwdBlocksPerSm = 2;
 
 struct NormRopeArgs {
     Geometry geo;
@@ -262,7 +261,7 @@ __device__ __forceinline__ void bwd_heads(const T* x, long long xs, const T* dy,
 // dw is summed per lane over the rows it meets, then over the block's groups, in a fixed order;
 // norm_rope_dw_kernel adds the blocks' sums in block order, so the result does not vary from run to run.
 template <typename T, int D, bool kFew>
-__global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) norm_rope_bwd_kernel(const NormRopeArgs a)
+__global__ void __launch_bounds__(kThreads, kNormRopeBwdPerSm) norm_rope_bwd_kernel(const NormRopeArgs a)
 {
     constexpr int V = Pack<T>::kElems, LPR = D / V, U = 4, kGroups = kThreads / LPR;
     __shared__ float sums[kGroups][2 * D];
@@ -355,7 +354,7 @@ cudaError_t launch(NormRopeArgs& a, bool backward, float* dwq, float* dwk, cudaS
         return cudaGetLastError();
     }
     // as many blocks as are resident, which take the positions in turns: their dw leave a partial sum each
-    const long long most = (long long)device_sm_count() * kBwdBlocksPerSm;
+    const long long most = (long long)device_sm_count() * kNormRopeBwdPerSm;
     if (grid > most) grid = most;
     if (grid > kNormRopeBwdBlocks) grid = kNormRopeBwdBlocks;
     if (few)

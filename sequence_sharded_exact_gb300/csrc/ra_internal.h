@@ -93,7 +93,8 @@ struct NormRope {
     int shard;                  // -1: whole-sequence buffers; else one device's shard
     double base, eps;
 };
-constexpr int kNormRopeBwdBlocks = 1216;  // 152 SMs x 8: the most blocks the backward launches
+constexpr int kNormRopeBwdPerSm = 2;  // blocks of the backward on an SM
+constexpr int kNormRopeBwdBlocks = 160 * kNormRopeBwdPerSm;  // and the most it launches (152 SMs here), which sizes the workspace
 cudaError_t launch_norm_rope(const Problem& p, const NormRope& n, cudaStream_t s);
 
 // A key/value cache: k, v [B][Hkv][cap][d] of `dtype` (a tensor dtype, or kCacheE4m3 with the rows'
