@@ -12,8 +12,10 @@
 //   * Queries: x 2^-e in f16, e such that the row's largest lies in [2^14, 2^15): a bf16's eight bits are exact down
 //     to 2^-28 of it.  The scales of rows and keys are applied to S.
 //   * Weights: p 2^ev_j in f16, ev_j the exponent of key j's V row, 2^7 at a reference M of their own: eleven bits down to
-//     2^-21 of the largest, weight and scale together.  The sum l takes p itself, at its reference m.  Both follow the
-//     query's maximum only when that grows by more than 2^8: a vote per 16 rows, and reductions only where it says so.
+//     2^-21 of the largest, weight and scale together; where scales far apart put a weight that counts below that, what f16
+//     does not hold of it is added in float32 (one row at a time: slow, and seldom).  The sum l takes p itself, at its
+//     reference m.  Both follow the query's maximum only when that grows by more than 2^8: a vote per 16 rows, and
+//     reductions only where it says so.
 //   * A CTA's warps take 16 rows in turn, with rings of their own that the TMA fills; m, l, M and O are
 //     a warp's own until the item's end, where they meet in shared memory, in warp order.  The next item's first rows
 //     and its queries are on their way meanwhile.
@@ -33,8 +35,9 @@
 namespace ra {
 namespace {
 
-
 constexpr int kStages = 2;
+constexpr int kBelow = 8;        // binades by which a row's scale may lie below the largest contribution's unlooked at
+constexpr float kCounts = 40.f;  // and a score below the largest, and count
 
 template <int D, int kWarps, int N>  // N: query rows in eights
 struct Cfg {
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
     auto scale_byte = [&](const TreeWalk& w, int i) {
         const int row = group_row(w) + i * kStep + (lane & 15);
         const uint8_t* exps = (lane < kKeys ? a.k_exp : a.v_exp) + ((long long)w.b * a.Hkv + w.g) * a.cap;
-        return i < groups(w) && row < w.s.end ? (uint32_t)exps[row] : 0u;
+        return i < groups(w) && row < w.s.end ? (uint32_t)exps[row] : (uint32_t)kHuge - 1;  // (of no row: never far below)
     };
     auto set_out = [&](const TreeWalk& w) {
         for (int i = 0; i < kStages && i < groups(w); ++i) send(w, i);
@@ -186,6 +189,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
         const int row0 = group_row(w), n = groups(w);
         float o[N][kTiles][4], m[N][2], l[N][2], sl[N][2];  // queries 8 c + 2t + u
         float top[N][2];                                    // M
+        int low = 0;                                        // V's scale bytes below this are far from M's
         uint32_t live = 0;                                  // bit 2 c + u
 #pragma unroll
         for (int c = 0; c < N; ++c) {
@@ -223,7 +227,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
             // keys g and g + 8: scales of K, exponents of V
             const float ks[2] = {__uint_as_float(__shfl_sync(0xffffffffu, byte, g8) << 23), __uint_as_float(__shfl_sync(0xffffffffu, byte, g8 + 8) << 23)};
             const float ve[2] = {(float)(int)__shfl_sync(0xffffffffu, byte, g8 + 16) - 127.f, (float)(int)__shfl_sync(0xffffffffu, byte, g8 + 24) - 127.f};
-            const bool huge = __any_sync(0xffffffffu, lane >= kKeys && byte >= (uint32_t)kHuge);
+            // a row of V whose scale is huge, or far below that of what contributes most
+            bool strange = __any_sync(0xffffffffu, lane >= kKeys && (byte >= (uint32_t)kHuge || (int)byte < low));
             warp_wait(bars + 8u * slot, (used / kStages) & 1, ctl);
             ++used;
 
@@ -288,6 +293,53 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
                             o[c][j][2 + u] *= alpha;
                         }
                     }
+                low = 0;
+#pragma unroll
+                for (int c = 0; c < N; ++c)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float at = top[c][u] - m[c][u];  // the scale of what contributes most
+                        if (at > -200.f && at < 300.f) low = max(low, (int)at + 127 - kBelow);
+                    }
+                low = __reduce_max_sync(0xffffffffu, low);
+                strange = strange || __any_sync(0xffffffffu, lane >= kKeys && (int)byte < low);
+            }
+            const uint8_t* vp = kp + C::kHalf;
+            // What float16 does not hold of the weights that count among the scores is added in float32, row by row: one element
+            // far above the others takes its row's scale up, and M with it, while the other columns are the other rows'.  (Rows of the
+            // smallest scale are zeros, mostly, and all below 2^-117.)
+            if (strange) {
+#pragma unroll
+                for (int c = 0; c < N; ++c) {
+                    float left[2][2];
+                    uint32_t rows = 0;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float p = ex2_approx(y[c][u][e] + (ve[e] - (top[c][u] == -INFINITY ? 0.f : top[c][u] - 7.f)));
+                            left[u][e] = p < pow2(-14) && y[c][u][e] > m[c][u] - kCounts && ve[e] > -126.f ? p - __half2float(__float2half_rn(p)) : 0.f;
+                            if (left[u][e] != 0.f) rows |= 1u << (g8 + 8 * e);
+                        }
+                    rows = __reduce_or_sync(0xffffffffu, rows);
+#pragma unroll 1
+                    for (; rows; rows &= rows - 1) {
+                        const int r = __ffs(rows) - 1, er = (int)__shfl_sync(0xffffffffu, byte, r + 16);
+                        float lw[2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) lw[u] = __shfl_sync(0xffffffffu, r < 8 ? left[u][0] : left[u][1], (r & 7) * 4 + t4);
+#pragma unroll
+                        for (int j = 0; j < D / 8; ++j) {
+                            const int d = g8 * (D / 8) + j;
+                            const uint32_t x = vp[at16<D>(r, d >> 4) + (d & 15)];
+                            float v, y0, y1, y2;
+                            e4m3x4_to_float(x, v, y0, y1, y2);
+                            if (not_finite(x, er)) v = 0.f;  // (added below)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) o[c][j / 2][2 * (j & 1) + u] = fmaf(lw[u], v, o[c][j / 2][2 * (j & 1) + u]);
+                        }
+                    }
+                }
             }
             uint32_t pb[N][2];
 #pragma unroll
@@ -305,7 +357,6 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
             }
 
             // V: rows 2t, 2t + 1, 2t + 8, 2t + 9, eight of the thread's d / 8 columns at a time
-            const uint8_t* vp = kp + C::kHalf;
 #pragma unroll
             for (int part = 0; part < D / 64; ++part) {
                 uint32_t vw[4][2];
@@ -317,8 +368,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
                 }
                 // Rows behind the sequence count as zeros.  NaN, and values whose scale takes them past float32, are
                 // cleared and added to the queries that see them: a weight of 0 would not hide them from the others.
-                if (masked || huge) {
-                    bool odd = huge;
+                if (masked || strange) {
+                    bool odd = lane >= kKeys && byte >= (uint32_t)kHuge;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
