@@ -774,12 +774,23 @@ def _stream_ptr(stream, index):
     return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-def _hold(stream, *tensors):
-    """Memory that a call allocated belongs to the current stream: the caller's other stream has to be done with it
-    before it is given out again."""
-    if stream is not None:
-        for t in tensors:
+def _hand_over(stream, index, *tensors):
+    """Memory that a call allocates (given: None, new: a tensor) comes from the current stream.  The caller's other stream waits
+    for what that one still has to do with it, and has to be done with it before it is given out again."""
+    new = [t for given, t in tensors if given is None]
+    if stream is None or not new:
+        return
+    current = torch.cuda.current_stream(index)
+    if stream != current:
+        if _capturing(stream) == _capturing(current):  # (what a capture records waits for nothing outside it)
+            stream.wait_stream(current)
+        for t in new:
             t.record_stream(stream)
+
+
+def _capturing(stream):
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def _run(index, call, *args):
@@ -883,10 +894,11 @@ def qk_norm_rope(q, k, wq, wk, n_shards=1, layout="contiguous", base=10000.0, ep
             return done
     head, tail = _norm_rope_args(q, k, wq, wk, n_shards, layout, base, eps, shard, positions)
     dev, dt = q.device, q.dtype
+    given = q_out, k_out
     q_out, qo = _output(q_out, "q_out", dev, q.shape, dt)
     k_out, ko = _output(k_out, "k_out", dev, k.shape, dt)
+    _hand_over(stream, dev.index, (given[0], q_out), (given[1], k_out))
     _run(dev.index, library().ring_attn_qk_norm_rope, *head, qo, ko, *tail, _stream_ptr(stream, dev.index))
-    _hold(stream, q_out, k_out)
     return q_out, k_out
 
 
@@ -902,6 +914,7 @@ def qk_norm_rope_bwd(q, k, wq, wk, dq_out, dk_out, n_shards=1, layout="contiguou
     head, tail = _norm_rope_args(q, k, wq, wk, n_shards, layout, base, eps, shard, positions)
     dev, dt, d = q.device, q.dtype, q.shape[3]
     gq, gk = _fits(dq_out, "dq_out", dev, q.shape, dt), _fits(dk_out, "dk_out", dev, k.shape, dt)
+    given = dq, dk, workspace
     dq, dqp = _output(dq, "dq", dev, q.shape, dt)
     dk, dkp = _output(dk, "dk", dev, k.shape, dt)
     dwq, dwk = torch.empty(d, dtype=torch.float32, device=dev), torch.empty(d, dtype=torch.float32, device=dev)
@@ -911,9 +924,9 @@ def qk_norm_rope_bwd(q, k, wq, wk, dq_out, dk_out, n_shards=1, layout="contiguou
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         _need_workspace(workspace, need, dev)
+    _hand_over(stream, dev.index, (given[0], dq), (given[1], dk), (None, dwq), (None, dwk), (given[2], workspace))
     _run(dev.index, lib.ring_attn_qk_norm_rope_bwd, *head, gq, gk, dqp, dkp, dwq.data_ptr(), dwk.data_ptr(),
          workspace.data_ptr(), workspace.numel(), *tail, _stream_ptr(stream, dev.index))
-    _hold(stream, dq, dk, dwq, dwk, workspace)
     return dq, dk, dwq, dwk
 
 
@@ -998,11 +1011,12 @@ def cache_read(cache, rows, row0=0, dtype=torch.bfloat16, k=None, v=None, stream
     if rows < 0 or row0 < 0 or row0 + rows > cap:
         raise ValueError(f"rows [{row0}, {row0 + rows}) lie outside the cache ({cap} rows)")
     shape = (B, Hkv, rows, d)
+    given = k, v
     k, kp = _output(k, "k", dev, shape, dtype)
     v, vp = _output(v, "v", dev, shape, dtype)
+    _hand_over(stream, dev.index, (given[0], k), (given[1], v))
     _run(dev.index, library().ring_attn_cache_read, *ptrs, kp, vp, B, Hkv, row0, rows, d, cap, code, kind,
          _stream_ptr(stream, dev.index))
-    _hold(stream, k, v)
     return k, v
 
 
@@ -1039,6 +1053,7 @@ def tree_fwd(q, cache, lens, mask=None, ntok=None, out_dtype=None, out=None, lse
     if mask is not None:
         batched = int(isinstance(mask, torch.Tensor) and mask.dim() == 3)
         mp = _fits(mask, "mask", dev, (B, T, T) if batched else (T, T), torch.bool)
+    given = out, lse, workspace
     out, op = _output(out, "out", dev, q.shape, out_dtype)
     lse, lp = _output(lse, "lse", dev, (B, H, T), torch.float32)
     lib = library()
@@ -1047,8 +1062,8 @@ def tree_fwd(q, cache, lens, mask=None, ntok=None, out_dtype=None, out=None, lse
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
     else:
         _need_workspace(workspace, need, dev)
+    _hand_over(stream, dev.index, (given[0], out), (given[1], lse), (given[2], workspace))
     _run(dev.index, lib.ring_attn_tree_fwd, qp, *ptrs, _fits(lens, "lens", dev, (B,), torch.int32),
          None if ntok is None else _fits(ntok, "ntok", dev, (B,), torch.int32), mp, batched, op, lp,
          workspace.data_ptr(), workspace.numel(), B, H, Hkv, T, d, cap, code, kind, _DTYPES[out_dtype], _stream_ptr(stream, dev.index))
-    _hold(stream, out, lse, workspace)
     return out, lse
