@@ -84,3 +84,20 @@ def test_a_query_with_one_element_far_above_the_others(H, Hkv, T, d, dtype, cdt)
     weight_eps = 2.0 ** -8 if dtype == BF else 0.0
     over = (out.cpu().double() - ref).abs() - mag * (weight_eps + 2 * (s_err + 2.0 ** -20)).unsqueeze(-1) - 2.0 ** -23 * ref.abs()
     assert float(over.max()) <= 0, f"out off by {float(over.max()):.3e} beyond its bound"
+
+
+@pytest.mark.parametrize("dtype,cdt", TYPES)
+@pytest.mark.parametrize("H,Hkv,T,d", [r for r in ROWS if r[2] > 1])
+def test_queries_of_tokens_that_a_sequence_does_not_have(H, Hkv, T, d, dtype, cdt):
+    """Rows behind ntok[b] of a padded batch hold NaN: they come back empty, the others as ever."""
+    B, cap = 3, 300 + T
+    cache = _cache_of(_randn(B, Hkv, cap, d, seed=31), _randn(B, Hkv, cap, d, seed=32), dtype, cdt)
+    q = _randn(B, H, T, d, seed=33).to(dtype).to(DEV)
+    lens, ntok = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([300, 17, 0], [1, T - 1, T // 2]))
+    ref, ref_lse = ra.tree_fwd(q, cache, lens, ntok=ntok)
+    for b in range(B):
+        q[b, :, int(ntok[b]):] = float("nan")
+    out, lse = ra.tree_fwd(q, cache, lens, ntok=ntok)
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse) and bool(torch.isfinite(out.float()).all())
+    for b in range(B):
+        assert bool((out[b, :, int(ntok[b]):] == 0).all()) and bool((lse[b, :, int(ntok[b]):] == -float("inf")).all())
