@@ -80,6 +80,19 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     return r;
 }
 
+// Two weights p as two bf16 values each: the upper half, cut off, and the rest of p (1 + 2^-20), rounded, off by at most
+// 2^-15 p.  The rest is above 0 wherever p is, so that an infinite value times it keeps its sign; a normaliser takes the
+// factor back.
+constexpr float kWeightUp = 1.f + 9.5367431640625e-07f;
+__device__ __forceinline__ void split_weights(float2 p, uint32_t& hi, uint32_t& lo)
+{
+    const uint32_t x = __float_as_uint(p.x), y = __float_as_uint(p.y);
+    hi = __byte_perm(x, y, 0x7632);
+    const float2 rest = fma2(p, make_float2(kWeightUp, kWeightUp),
+                             make_float2(__uint_as_float((x & 0xffff0000u) | 0x80000000u), __uint_as_float((y & 0xffff0000u) | 0x80000000u)));
+    lo = pack_bf16x2(rest.x, rest.y);
+}
+
 // d + the two bf16 values of w, each to its own float32 sum.
 __device__ __forceinline__ float2 add_bf16x2(float2 d, uint32_t w)
 {

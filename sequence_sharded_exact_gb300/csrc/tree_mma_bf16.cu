@@ -2,9 +2,9 @@
 //
 // The products of tree_mma.cu, S^T = K Q^T and O^T += V^T P^T with 16 cached rows, or columns of V, against 8 queries
 // (mma.m16n8k16, bf16, float32 sums), a warp by itself with 16 cached rows at a time; K and V are operands as they
-// are cached, V by transposing loads (ldmatrix).  P is bf16, and the normaliser the sum of the weights as they were
-// rounded (lse takes them unrounded); their reference follows the maximum only when that grows by more than 2^8: a vote per
-// 16 rows, and reductions only where it says so.  A CTA has four warps, two or three CTAs run on an SM: while one joins its
+// are cached, V by transposing loads (ldmatrix).  P is two bf16 parts, two products in place of one at no cost here; its
+// reference follows the maximum only when that grows by more than 2^8: a vote per 16 rows, and reductions only where it
+// says so.  A CTA has four warps, two or three CTAs run on an SM: while one joins its
 // warps' results at an item's end the others stream.
 //
 // What bounds it: the memory.  A tile of 128 rows of 8 kv heads (d = 128, 64 KB) costs each of 152 SMs 1.30 us, 7.6
@@ -127,13 +127,13 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
     do {
         if (w.goes_on()) border = w.border(a, blockIdx.x);
         const int row0 = group_row(w), n = groups(w);
-        float o[kTiles][4], m[2], l[2], den[2];  // queries 2t + u; den: the sum of the rounded weights
+        float o[kTiles][4], m[2], l[2];  // queries 2t + u
         bool live[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int x = 2 * t4 + u;
             m[u] = -INFINITY;
-            l[u] = den[u] = 0.f;
+            l[u] = 0.f;
             live[u] = x < a.R && x % a.T < w.s.cnt;
         }
 #pragma unroll
@@ -179,7 +179,6 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
                         m[u] = my;
                     }
                     l[u] *= alpha;
-                    den[u] *= alpha;
 #pragma unroll
                     for (int j = 0; j < kTiles; ++j) {
                         o[j][u] *= alpha;
@@ -187,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
                     }
                 }
             }
-            uint32_t pb[2];
+            uint32_t pb[2], pl[2];
             {
                 float p[2][2];  // [key][query]
 #pragma unroll
@@ -199,10 +198,10 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const uint32_t w2 = pack_bf16x2(p[e][0], p[e][1]);
-                    den[0] += __uint_as_float(w2 << 16);
-                    den[1] += __uint_as_float(w2 & 0xffff0000u);
-                    pb[e] = transpose8(w2);
+                    uint32_t hi, lo;
+                    split_weights(make_float2(p[e][0], p[e][1]), hi, lo);
+                    pb[e] = transpose8(hi);
+                    pl[e] = transpose8(lo);
                 }
             }
             // Rows of V behind the sequence count as zeros, and what is not finite in drafted tokens' rows is cleared and
@@ -252,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
                 uint32_t v[4];
                 load_matrices_transposed(v, v_at + at16(vr, 2 * j + vc));
                 mma16(o[j], v, pb[0], pb[1]);
+                mma16(o[j], v, pl[0], pl[1]);
             }
             __syncwarp();  // all lanes have read the slot
             if (i + kStages < n) send(w, i + kStages);
@@ -271,9 +271,8 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
                 l[u] += __shfl_xor_sync(0xffffffffu, l[u], d);
-                den[u] += __shfl_xor_sync(0xffffffffu, den[u], d);
             }
-            if (g8 == 0) ml[warp * 8 + 2 * t4 + u] = make_float4(m[u], l[u], den[u], 0.f);
+            if (g8 == 0) ml[warp * 8 + 2 * t4 + u] = make_float4(m[u], l[u], l[u] * kWeightUp, 0.f);
         }
         __syncthreads();
         float* xs = reinterpret_cast<float*>(smem + C::kX);

@@ -5,6 +5,11 @@
 // One CTA per SM walks its items (tree.cuh): one kv head's tile of query rows against its cached rows, 128
 // at a time.  For query rows X and cached rows K, V of a tile:
 //   S = X K^T (TMEM), P = 2^(S c - m) (bf16, over S's columns), O += P V (TMEM), the running m, l per row.
+// A weight goes into P V as two bf16 values (kExact), off by 2^-15 of itself, where the memory bounds the kernel, which
+// hardly feels it (a bf16 cache, up to 128 query rows: 1.49 us per tile in place of 1.44), and where the output is
+// float32: the output before rounding, or a part that others are to be folded into.  Otherwise as one, off by up to 2^-8 of
+// itself: the output's relative error is then 0.0023, where its own rounding to bf16 makes 0.0017.  Two would take ragged e4m3
+// caches from 131 to 140 us and 256 query rows from 72 to 80.
 // A query row is a TMEM lane and a thread, so its maximum and sum need no exchange between threads.
 //   * Up to 128 query rows (kNq = 1): the two softmax warpgroups take turns at the tiles, each with its own
 //     m, l and O, so that one tile's exponentials run beside the other's products; they join the two at the
@@ -230,15 +235,19 @@ __device__ __forceinline__ void issue_s(uint32_t lead, uint32_t sbase, uint32_t 
     }
 }
 
-// O_w (+)= P_w V.
+// O_w (+)= P_w V.  (kExact: of each 32 keys' columns of S the first 16 hold P's upper parts, the others what is left.)
+template <bool kExact>
 __device__ __forceinline__ void issue_pv(uint32_t lead, uint32_t v_addr, uint32_t tmem, int w, bool accumulate)
 {
     const uint32_t v = sdesc_sw128_lo(v_addr, 16384);
     constexpr uint32_t hi = sdesc_sw128_hi(1024);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
-        lead_mma_ts(lead, tmem + kColO + (uint32_t)w * 128, tmem + kColS + (uint32_t)w * 128 + (uint32_t)kk * 8,
-               sdesc_at(v, (uint32_t)kk * 2048u, hi), idesc_bf16_f32(128, kHd, false, true), kk > 0 || accumulate ? 1u : 0u);
+#pragma unroll
+        for (int part = 0; part < (kExact ? 2 : 1); ++part)
+            lead_mma_ts(lead, tmem + kColO + (uint32_t)w * 128,
+                        tmem + kColS + (uint32_t)w * 128 + (uint32_t)(kExact ? (kk >> 1) * 32 + part * 16 + (kk & 1) * 8 : kk * 8),
+                        sdesc_at(v, (uint32_t)kk * 2048u, hi), idesc_bf16_f32(128, kHd, false, true), part + kk > 0 || accumulate ? 1u : 0u);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -572,7 +581,7 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
 // belongs to warpgroup j & 1; its S is issued once P V of job j - 2, which reads the same TMEM columns, is.  A
 // commit costs the issuing warp 50 to 180 cycles, so there are two per job: S is ready (which also says that P V
 // of job j - 2 is done, and that K has been read), and V has been read.
-template <bool kE4, int kNq>
+template <bool kE4, int kNq, bool kExact>
 __device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint32_t tmem, TreeWalk w, const WaitCtl& ctl)
 {
     using C = Cfg<kE4, kNq>;
@@ -595,7 +604,7 @@ __device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint
                 if (!ok) break;
                 pc ^= 1u << wg;
                 tc_fence_after_sync();
-                issue_pv(lead, sbase + (kE4 ? C::kP + (uint32_t)rv.slot * C::kBytesV : C::kL + (uint32_t)rv.slot * C::kBytesK), tmem, wg, j >= 4);
+                issue_pv<kExact>(lead, sbase + (kE4 ? C::kP + (uint32_t)rv.slot * C::kBytesV : C::kL + (uint32_t)rv.slot * C::kBytesK), tmem, wg, j >= 4);
                 if (j >= n) lead_commit(lead, bar(C::bO + wg));  // the warpgroup's last job of the item
                 if (kNq == 1 || wg == 1) {
                     lead_commit(lead, bar((kE4 ? C::bPEmpty : C::bLEmpty) + rv.slot));
@@ -661,7 +670,7 @@ __device__ __forceinline__ unsigned long long seen_bits(const TreeArgs& a, const
     return bits;
 }
 
-template <bool kE4, int kNq>
+template <bool kE4, int kNq, bool kExact>
 __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, uint8_t* smem, uint32_t tmem, TreeWalk w,
                                              const WaitCtl& ctl)
 {
@@ -781,7 +790,7 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
                     }
                     const __nv_bfloat162 a2 = __float2bfloat162_rn(alpha);
 #pragma unroll 1
-                    for (int k = 0; k < c; ++k) {
+                    for (int k = 0; k < (kExact ? 2 * c : c); ++k) {
                         uint32_t o[16];
                         tmem_st_wait();
                         tmem_ld_32x32b_x16(tS + 16 * k, o);
@@ -797,17 +806,23 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
                 const float ref = m_run == -INFINITY ? 0.f : m_run;
                 const float2 scale2 = make_float2(sl2, sl2), nref2 = make_float2(-ref, -ref);
                 float2 s4[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, d4[2] = {s4[0], s4[0]};
-                uint32_t pk[16];
+                uint32_t pk[kExact ? 32 : 16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                     const float2 x2 = fma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), scale2, nref2);
                     const float2 p2 = make_float2(ex2_approx(x2.x), ex2_approx(x2.y));
                     s4[(e >> 1) & 1] = add2(s4[(e >> 1) & 1], p2);
-                    const uint32_t w2 = pack_bf16x2(p2.x, p2.y);
-                    d4[(e >> 1) & 1] = add_bf16x2(d4[(e >> 1) & 1], w2);
-                    pk[e / 2] = w2;
+                    if constexpr (kExact) {
+                        split_weights(p2, pk[e / 2], pk[16 + e / 2]);
+                    } else {
+                        pk[e / 2] = pack_bf16x2(p2.x, p2.y);
+                        d4[(e >> 1) & 1] = add_bf16x2(d4[(e >> 1) & 1], pk[e / 2]);
+                    }
                 }
-                tmem_st_32x32b_x16(tS + 16 * c, pk);
+                if constexpr (kExact)
+                    tmem_st_32x32b_x32(tS + 32 * c, pk);
+                else
+                    tmem_st_32x32b_x16(tS + 16 * c, pk);
                 s2 = add2(s2, add2(s4[0], s4[1]));
                 d2 = add2(d2, add2(d4[0], d4[1]));
             }
@@ -835,7 +850,7 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
         }
 
         // the item's rows: O of both warpgroups (kNq == 1), or of this one
-        float m = m_run, l = l_run, den = den_run, w0 = 1.f, w1 = 0.f;
+        float m = m_run, l = l_run, den = kExact ? l_run * kWeightUp : den_run, w0 = 1.f, w1 = 0.f;
         const int n1 = kNq == 1 ? n >> 1 : 0;
         if constexpr (kNq == 1) {
             float4* ml = reinterpret_cast<float4*>(smem + C::kMl);
@@ -947,7 +962,7 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
     } while (w.next(a));
 }
 
-template <bool kE4, int kNq>
+template <bool kE4, int kNq, bool kExact>
 __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ Maps maps, const TreeArgs a)
 {
     using C = Cfg<kE4, kNq>;
@@ -988,12 +1003,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
 
     if (work) {
         if (warp < 8) {
-            softmax_role<kE4, kNq>(a, sbase, smem, tmem, w, ctl);
+            softmax_role<kE4, kNq, kExact>(a, sbase, smem, tmem, w, ctl);
         } else if (warp == 8) {
             if (lane == 0) a.border[blockIdx.x].x = -1;  // (the walk's last item may say otherwise)
             if (lane == 0) load_qk_role<kE4, kNq>(a, sbase, maps, w, ctl);
         } else if (warp == 9) {
-            mma_role<kE4, kNq>(a, sbase, tmem, w, ctl);
+            mma_role<kE4, kNq, kExact>(a, sbase, tmem, w, ctl);
         } else if (warp == 10) {
             if (lane == 0) load_v_role<kE4, kNq>(a, sbase, maps, w, ctl);
         } else if (warp == 11) {
@@ -1047,7 +1062,7 @@ bool make_map(CUtensorMap* map, const void* base, long long rows, long long head
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kE4, int kNq>
+template <bool kE4, int kNq, bool kExact>
 cudaError_t launch(const TreeArgs& a, const Maps& maps, cudaStream_t s)
 {
     using C = Cfg<kE4, kNq>;
@@ -1060,12 +1075,12 @@ cudaError_t launch(const TreeArgs& a, const Maps& maps, cudaStream_t s)
     {
         std::lock_guard<std::mutex> lk(mu);
         if (!done[dev]) {
-            e = cudaFuncSetAttribute(tree_tc_kernel<kE4, kNq>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+            e = cudaFuncSetAttribute(tree_tc_kernel<kE4, kNq, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
             if (e != cudaSuccess) return e;
             done[dev] = true;
         }
     }
-    tree_tc_kernel<kE4, kNq><<<a.ctas, kThreads, C::kSmem, s>>>(maps, a);
+    tree_tc_kernel<kE4, kNq, kExact><<<a.ctas, kThreads, C::kSmem, s>>>(maps, a);
     return cudaGetLastError();
 }
 
@@ -1078,8 +1093,9 @@ cudaError_t RA_TREE_LAUNCH(const TreeArgs& a, bool e4m3, cudaStream_t s)
     if (!make_map(&maps.q, a.q, a.R, heads, false) || !make_map(&maps.k, a.k, a.cap, heads, e4m3) ||
         !make_map(&maps.v, a.v, a.cap, heads, e4m3))
         return cudaErrorInvalidValue;
-    if (a.rt == 128) return e4m3 ? launch<true, 1>(a, maps, s) : launch<false, 1>(a, maps, s);
-    return e4m3 ? launch<true, 2>(a, maps, s) : launch<false, 2>(a, maps, s);
+    if (a.rt == 128) return !e4m3 ? launch<false, 1, true>(a, maps, s) : a.bf16_out ? launch<true, 1, false>(a, maps, s) : launch<true, 1, true>(a, maps, s);
+    if (a.bf16_out) return e4m3 ? launch<true, 2, false>(a, maps, s) : launch<false, 2, false>(a, maps, s);
+    return e4m3 ? launch<true, 2, true>(a, maps, s) : launch<false, 2, true>(a, maps, s);
 }
 
 }  // namespace ra

@@ -51,3 +51,21 @@ def test_keys_that_share_a_weight_are_averaged(H, Hkv, T, d, n, cdt):
     tol = (1.02 * 2.0 ** -7 + 2 * (s_err[0].unsqueeze(-1) + 2.0 ** -20)) * apart + 2 * n * 2.0 ** -24 * mag[0]
     over = (out[0].cpu().double() - ref[0]).abs() - tol
     assert float(over.max()) <= 0, f"off by {float(over.max()):.3e} beyond its bound ({float(tol.max()):.3e})"
+
+
+@pytest.mark.parametrize("cdt", [BF, E4M3])
+@pytest.mark.parametrize("H,Hkv,T,d", [(2, 1, 1, 128), (4, 2, 4, 64), (8, 2, 4, 128), (8, 2, 5, 128), (4, 1, 32, 64), (4, 1, 32, 128),
+                                       (4, 1, 64, 128), (4, 1, 64, 64)])
+@pytest.mark.parametrize("n", [90, 1500])
+def test_float32_output_is_as_exact_as_its_sums(H, Hkv, T, d, n, cdt):
+    """bfloat16 queries, output in float32: the weights go into the product as two bfloat16 parts, off by at most 2^-15 of
+    themselves (over an e4m3 cache with up to 16 query rows per kv head as one float16, 2^-11), and the sums of n terms
+    are float32's, (n / 16 + 16) 2^-23 of sum w |v|.  One bfloat16 weight would be off by up to 2^-8 of itself."""
+    cap = n + T
+    cache = ra.cache_alloc(1, Hkv, cap, d, cdt)
+    g = torch.Generator().manual_seed(n)
+    ra.cache_write(cache, *(torch.randn((1, Hkv, cap, d), generator=g).to(BF).to(DEV) for _ in range(2)))
+    q, mask = torch.randn((1, H, T, d), generator=g).to(BF).to(DEV), cu.random_tree(1, T, 5)
+    got = ra.tree_fwd(q, cache, torch.tensor([n], dtype=torch.int32, device=DEV), mask=mask.to(DEV), out_dtype=F32)
+    weight_eps = 2.0 ** -11 if cdt == E4M3 and H // Hkv * T <= 16 else 2.0 ** -15
+    cu.check_tree(got, cu.tree(q, *cu.cache_values(cache), [n], mask, None), weight_eps + (n / 16 + 16) * 2.0 ** -23, F32)
