@@ -419,7 +419,7 @@ RA_API size_t ring_attn_ulysses_bwd_workspace_size(int B, int H, int Hkv, int L,
  *   wq, wk: [d] float32.   q_out, k_out: contiguous, dtype; each may be its own contiguous input.
  *   positions: [B][rows] int32, 4-byte aligned: the natural position of every token (any int value),
  *   in place of the layout's; or NULL.
- *   All sums are float32 (x^2 has to fit it).
+ *   All sums are float32 (x^2 has to fit it).  Angles are exact to 2^-32 of a turn, then a float32 in [-1/2, 1/2) turn.
  *   base > 0 and finite; eps >= 0 and finite; H % Hkv == 0; L and layout as ring_attn_rope; d in {64, 128}.
  *
  * ring_attn_qk_norm_rope_bwd -- its gradients.  With g = R(-p) dy and u = g w:
@@ -474,7 +474,7 @@ RA_API ra_status ring_attn_cache_read(const void* k_cache, const void* v_cache, 
  * the rows lens[b] + j, j < ntok[b] (ring_attn_cache_write puts them there first), those that mask
  * allows: token t sees token j where mask[b][t][j] != 0.  T = 1 without a mask is the decoding of single
  * tokens; a tree of drafted tokens has the ancestors of t (itself among them) in row t of the mask.
- *   q, out: [B][H][T][d]; q in dtype, out in out_dtype (dtype, or RA_F32: the output before rounding);
+ *   q, out: [B][H][T][d]; q in dtype, out in out_dtype (dtype, or RA_F32: see the accuracy below);
  *   lse: [B][H][T] float32.  Query head h reads kv head h / (H / Hkv); the scale is 1/sqrt(d).
  *   lens: DEVICE int32 [B];  ntok: DEVICE int32 [B], or NULL: T tokens each (both 4-byte aligned).
  *   mask: DEVICE, [B][T][T] bytes (mask_batched != 0) or one [T][T] for all sequences (0); NULL: j <= t.
@@ -488,6 +488,15 @@ RA_API ra_status ring_attn_cache_read(const void* k_cache, const void* v_cache, 
  *   workspace: DEVICE, 256-byte aligned, at least ring_attn_tree_fwd_workspace_size(...) bytes.  Its contents
  *   do not matter; calls whose GPU work overlaps (other streams, two graphs at once) need one each.
  *   The result does not vary from run to run.
+ *   Accuracy: scores, maxima, sums, lse and the output before its rounding are float32's.  With float32 q the weights
+ *   exp(s - m) are too.  With bf16 q, R = H / Hkv * T query rows per kv head, a weight goes into the product with v
+ *     as two bf16 values, off by up to 2^-15 of itself, over a bf16 cache with R <= 128 and wherever out is float32
+ *       (but for the next case);
+ *     as one float16, off by up to 2^-11, over an RA_E4M3 cache with R <= 16 (weights below 2^-40 of a row's largest, and
+ *       values below 2^-117, may be left out);
+ *     as one bf16 value, off by up to 2^-8, otherwise; the normaliser is the sum of those.
+ *   Over an RA_E4M3 cache with R > 16 the elements of q below 2^-13 of their row's largest are held to 2^-21 of that, all
+ *   others exactly; a row of q with an element that is not finite counts as NaN.
  */
 RA_API ra_status ring_attn_tree_fwd(const void* q, const void* k_cache, const void* v_cache, const void* k_exp,
                                     const void* v_exp, const int* lens, const int* ntok, const unsigned char* mask,

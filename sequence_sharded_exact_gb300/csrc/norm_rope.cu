@@ -22,8 +22,8 @@
 //
 // Measured, 64K positions of 32 + 8 heads of 128 in bf16: forward 208 us (6.45 TB/s, 0.95 of the copy
 // rate), backward 320 us (6.30 TB/s, 0.93).  What is left are the shuffles and the products between
-// loads: more heads in flight cost registers and so the other blocks that hide them.  32 bytes a lane in
-// place of 16 took the forward 6 us further and the backward 14 back, and would need rows on 32-byte
+// loads: more heads in flight cost registers and so the other blocks that hide them (the bf16 forward spills 40 bytes as
+// it is, to keep four blocks on an SM).  32 bytes a lane in place of 16 took the forward 6 us further and the backward 14 back, and would need rows on 32-byte
 // boundaries.
 #include <cuda_bf16.h>
 #include <math.h>

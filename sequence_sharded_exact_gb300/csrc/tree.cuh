@@ -48,7 +48,7 @@ struct TreeArgs {
     const uint8_t *k_exp, *v_exp;
     void* out;
     float* lse;
-    float* part_ml;  // [ctas][2][rt][4]: m (log2 units), l, the output's normaliser (l as the weights were rounded), 0
+    float* part_ml;  // [ctas][2][rt][4]: m (log2 units), l, the output's normaliser, 0
     float* part_o;   // [ctas][2][d][rt]: a warp that holds consecutive rows writes whole lines
     int4* border;    // [ctas]: the item that starts in this CTA and goes on in the next: sequence (-1: none),
                      // head * nrt + row tile, its last CTA, its slot here + 2 * its sequence's drafted tokens
@@ -213,8 +213,8 @@ cudaError_t launch_tree_simt(const TreeArgs& a, int d, int cache_dtype, cudaStre
 // bf16 queries, up to kTreeMmaRows query rows per kv head: one row tile; an e4m3 cache (tree_mma.cu) or a bf16 one
 // (tree_mma_bf16.cu).
 constexpr int kTreeMmaRows = 8, kTreeMmaE4m3Rows = 16;
-// 9 to 16 rows (e4m3): CTAs of four warps per SM; at d = 128 a third would leave too few registers (85 us for one
-// sequence of 131072 rows in place of 77, when that was measured).
+// 9 to 16 rows (e4m3): CTAs of four warps per SM; at d = 128 a third would leave too few registers (one sequence of 131072
+// rows, 87 us, took a tenth longer).
 __host__ __device__ constexpr int tree_mma16_ctas_per_sm(int d) { return d == 128 ? 2 : 3; }
 // With many items (sequences times kv heads) per SM their ends cost more than the join of more CTAs' partials, so there are
 // more CTAs.  e4m3: four of four warps per SM in place of two of eight; bf16: three of four warps in place of two.

@@ -21,11 +21,12 @@
 //     and its queries are on their way meanwhile.
 //
 // What bounds it: the memory, nearly.  A tile of 128 rows of 8 kv heads' e4m3 cache (d = 128) costs each of 152 SMs
-// 0.95 us, 5.2 TB/s (tree_tc_body.cuh: 1.46), one token over 131072 rows 53 us with both launches (it: 91).  A group of 16
+// 0.95 us, 5.2 TB/s (tree_tc_body.cuh: 1.57), one token over 131072 rows 53 us with both launches (it: 91).  A group of 16
 // rows is some 400 instructions, issued in about half of the cycles: latency, which 16 warps per SM hide; 24 do not fit the
 // registers (80 each: spills, 60 us at 32 tiles per SM in place of 38), a third stage per ring changes nothing.  With query
 // rows as the products' 16 rows there are twice as many products and registers (65 us).  9 to 16 query rows: 131072 rows in
-// 82 us in place of 88 there, 64 sequences of 1000 rows in 60 in place of 83 (d = 64: 52 for 73, 37 for 64).
+// 87 us (88 there, before it summed its weights as they are rounded), 64 sequences of 1000 rows in 62 in place of 83
+// (d = 64: 54 for 73, 38 for 64).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>

@@ -7,7 +7,7 @@
 // says so.  A CTA has four warps, two or three CTAs run on an SM: while one joins its
 // warps' results at an item's end the others stream.
 //
-// What bounds it: the memory.  A tile of 128 rows of 8 kv heads (d = 128, 64 KB) costs each of 152 SMs 1.30 us, 7.6
+// What bounds it: the memory.  A tile of 128 rows of 8 kv heads (d = 128, 64 KB) costs each of 152 SMs 1.32 us, 7.5
 // TB/s; one token over 131072 rows takes 85 us with both launches (tree_tc_body.cuh: 88), one over 19 tiles, a tile
 // an SM, 11.5 (12.7), 512 sequences of 129 rows 72 (120): no 128 query rows to fill, and no pipeline of
 // warps with different parts to drain at every item's end.

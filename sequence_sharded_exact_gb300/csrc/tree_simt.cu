@@ -6,8 +6,10 @@
 // threads share a column's query rows when d = 64), the weights come from shared memory.  Masked
 // weights are stored as -1 and left out by a comparison, so that a masked row's values never meet the sums.
 //
-// What bounds it: issue.  A chunk of 16 query rows is 512 fused multiply-adds and about 200 loads from shared memory per
-// thread; each of the next chunk's loads from memory is under way meanwhile.  128 rows of d = 64 against 20 query rows (two
+// What bounds it: shared memory, which every product is fed from (the most frequent stall; an instruction is issued in 0.39
+// of the cycles).  A chunk of 16 query rows is 512 fused multiply-adds and about 200 loads from shared memory per
+// thread; each of the next chunk's loads from memory is under way meanwhile.  Four CTAs on an SM leave 128 registers a
+// thread: 12 rows spill 28 bytes of them at d = 64 and 88 at d = 128.  128 rows of d = 64 against 20 query rows (two
 // tiles of 12) cost an SM 6.9 us; with two tiles of 16 and loads that are waited for at once 11.5.  Tiles are 32 rows, a
 // chunk, so that short caches spread over all SMs: one sequence of 9000 rows and 20 query rows 19 + 9 us (both
 // launches) in place of 25 + 12.

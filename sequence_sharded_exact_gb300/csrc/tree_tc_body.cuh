@@ -34,12 +34,16 @@
 // cache), so warps 12-15 turn V into bf16, exactly, scale included.
 //
 // What bounds it, per tile of 128 cached rows on each of 152 SMs, d = 128 (launches apart):
-//   * bf16, up to 128 query rows: 1.38 us for 64 KB, 7.2 TB/s: the memory.  (Up to 8 rows take tree_mma_bf16.cu.)
-//   * bf16, 256 rows: 1.67 us.  The products take 1.06 of them; S, the softmax and P V of a warpgroup's query rows follow
-//     one another on one S, whose columns P takes (TMEM is full: two S, two O).
-//   * e4m3, up to 128 rows: 1.45 us for 32 KB.  Shared memory serves 1600 of the 2500 cycles at 128 bytes each: copies
-//     256, S 512 (hi and lo), V to bf16 450, P V 256, scales 130; the rest is the same chain.  Up to 16 rows
-//     take tree_mma.cu (0.9 us up to 8).  256 rows: 2.5 us.
+//   * bf16, up to 128 query rows: 1.43 to 1.47 us for 64 KB, 6.8 to 7.0 TB/s: the memory.  (Up to 8 rows take
+//     tree_mma_bf16.cu.)
+//   * bf16, 256 rows: 1.80 us.  The products take 1.06 of them; S, the softmax and P V of a warpgroup's query rows follow
+//     one another on one S, whose columns P takes (at d = 128 TMEM is full: two S, two O; at d = 64 half of O's is free,
+//     and kept so).
+//   * e4m3, up to 128 rows: 1.57 to 1.63 us for 32 KB.  Shared memory serves 1600 of some 2800 cycles at 128 bytes each:
+//     copies 256, S 512 (hi and lo), V to bf16 450, P V 256, scales 130; the rest is the same chain.  Up to 16 rows
+//     take tree_mma.cu (0.95 us up to 8).  256 rows: 2.7 us.
+// The sum of the weights as they are rounded, for one bf16 value each, takes 0.12 us of a tile's (an uncorrected sum shifts
+// a row whose keys share a weight by up to 2^-8).
 // What did not help: S in halves of 64 columns, two per warpgroup (256 rows: 2.29 us: twice the issue and waits);
 // warpgroups that take half of each tile's keys (e4m3 1.58); V's e4m3 to bf16 by moving bits (its instructions are not
 // what takes the time); loading a whole row of V ahead; the e4m3 queries split by warps 12-15 (later at the start, no
