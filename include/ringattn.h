@@ -442,6 +442,33 @@ RA_API ra_status ring_attn_qk_norm_rope_bwd(const void* q, const long long* q_st
 RA_API size_t ring_attn_qk_norm_rope_bwd_workspace_size(int d);
 
 /*
+ * Attention of whole sequences through a sliding window, with a few first tokens that stay visible (sinks).
+ * With natural positions p (query) and j (key), from the layout:
+ *   causal = 1:  p sees j  iff  j <= p and (p - j < window or j < sinks);
+ *   causal = 0:  p sees j  iff  |p - j| < window or j < sinks.
+ * window >= 1 and sinks >= 0; past L they act as L.  window >= L is the attention without a window.
+ *
+ * ring_attn_window_fwd -- out and lse as ring_attn_fwd's, over the keys that each row sees.  Buffers as there, in the
+ *   layout's order; any L that the layout allows (there are no tile sizes to keep to), d in {64, 128}.
+ *   out in out_dtype: dtype, or RA_F32 (ring_attn_fwd_f32out).
+ *   workspace: DEVICE, 256-byte aligned, at least ring_attn_window_fwd_workspace_size(...) bytes, which may be 0 (the
+ *   pointer is then not used).  Contents on entry do not matter; calls whose GPU work overlaps need one each.
+ * ring_attn_window_bwd -- the gradients of sum(out * dout), as ring_attn_bwd's: out (out_dtype) and lse from the forward,
+ *   dout in dtype, dq, dk, dv in grad_dtype.  dk and dv do not vary from run to run, nor does dq with float32 inputs; with
+ *   bf16 inputs dq is summed by float32 atomics, in an order that varies.
+ */
+RA_API ra_status ring_attn_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse, void* workspace,
+                                      size_t workspace_bytes, int B, int H, int Hkv, int L, int d, int n_shards, int window,
+                                      int sinks, int causal, int layout, int dtype, int out_dtype, void* stream);
+RA_API size_t ring_attn_window_fwd_workspace_size(int B, int H, int Hkv, int L, int d, int n_shards, int layout, int dtype);
+RA_API ra_status ring_attn_window_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse,
+                                      const void* dout, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                                      int B, int H, int Hkv, int L, int d, int n_shards, int window, int sinks, int causal,
+                                      int layout, int dtype, int out_dtype, int grad_dtype, void* stream);
+RA_API size_t ring_attn_window_bwd_workspace_size(int B, int H, int Hkv, int L, int d, int n_shards, int window, int sinks,
+                                                  int causal, int layout, int dtype);
+
+/*
  * A key/value cache: k_cache, v_cache [B][Hkv][cap][d], cap rows per sequence and kv head, in the
  * tensors' dtype (cache_dtype == dtype) or quantised (RA_E4M3).  A quantised row (one token of one kv
  * head) has one scale 2^e, the smallest with e >= -126 that brings its largest magnitude to at most 448:

@@ -47,6 +47,8 @@ from .binding import (  # noqa: F401
     ulysses_a2a,
     ulysses_bwd,
     ulysses_fwd,
+    window_bwd,
+    window_fwd,
 )
 from .autograd import ring_attention, ring_qk_norm_rope  # noqa: F401
 from .ring import RingAttention, ring_attention_distributed  # noqa: F401

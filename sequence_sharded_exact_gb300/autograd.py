@@ -18,33 +18,46 @@ from . import binding
 
 class _RingAttention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, n_shards, causal, layout, f32_out):
+    def forward(ctx, q, k, v, n_shards, causal, layout, f32_out, window, sinks):
         q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
         f32_out = bool(f32_out) and q.dtype != torch.float32
-        if f32_out:
+        if window is not None:
+            q, k, v = _dense(q), _dense(k), _dense(v)
+            saved, lse = binding.window_fwd(q, k, v, n_shards, window, sinks, causal, layout,
+                                            out_dtype=torch.float32 if f32_out else None)
+            out = binding.f32_convert(saved, q.dtype) if f32_out else saved
+        elif f32_out:
             saved, lse = binding.fwd_f32out(q, k, v, n_shards, causal, layout)
             out = binding.f32_convert(saved, q.dtype)
         else:
             out, lse = binding.fwd(q, k, v, n_shards, causal, layout)
             saved = out
         ctx.save_for_backward(q, k, v, saved, lse)
-        ctx.cfg = (n_shards, causal, layout, f32_out)
+        ctx.cfg = (n_shards, causal, layout, f32_out, window, sinks)
         return out
 
     @staticmethod
     def backward(ctx, dout):
         q, k, v, saved, lse = ctx.saved_tensors
-        n_shards, causal, layout, f32_out = ctx.cfg
+        n_shards, causal, layout, f32_out, window, sinks = ctx.cfg
+        if window is not None:
+            dq, dk, dv = binding.window_bwd(q, k, v, saved, lse, _dense(dout), n_shards, window, sinks, causal, layout,
+                                            grad_dtype=q.dtype)
+            return dq, dk, dv, None, None, None, None, None, None
         call = binding.bwd_f32out if f32_out else binding.bwd
         dq, dk, dv = call(q, k, v, saved, lse, dout.contiguous(), n_shards, causal, layout, grad_dtype=q.dtype)
-        return dq, dk, dv, None, None, None, None
+        return dq, dk, dv, None, None, None, None, None, None
 
 
-def ring_attention(q, k, v, n_shards, causal=True, layout="zigzag", f32_out=False):
+def ring_attention(q, k, v, n_shards, causal=True, layout="zigzag", f32_out=False, window=None, sinks=0):
     """Exact attention of q [B,H,L,d] over k, v [B,Hkv,L,d] (sequence axis in the layout's order),
     computed as the ring over n_shards shards; differentiable with respect to q, k and v.
-    f32_out: keep the forward's output in float32 for the backward's D (see the module notes)."""
-    return _RingAttention.apply(q, k, v, n_shards, causal, layout, f32_out)
+    f32_out: keep the forward's output in float32 for the backward's D (see the module notes).
+    window, sinks: every token sees the `window` last tokens (itself among them) and the first `sinks` ones alone
+    (window_fwd); without a window all that `causal` allows, and `sinks` has to be 0."""
+    if window is None and sinks:
+        raise ValueError("sinks are the first tokens that a window leaves visible: they need a window")
+    return _RingAttention.apply(q, k, v, n_shards, causal, layout, f32_out, window, sinks)
 
 
 def _dense(t):

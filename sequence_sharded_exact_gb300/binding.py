@@ -10,6 +10,7 @@ import ctypes
 import functools
 import importlib.machinery
 import importlib.util
+import operator
 import os
 import threading
 import warnings
@@ -47,6 +48,8 @@ EXPORTS = (
     "ring_attn_bwd_f32out", "ring_attn_bwd_preprocess_f32out", "ring_attn_qk_norm_rope",
     "ring_attn_qk_norm_rope_bwd", "ring_attn_qk_norm_rope_bwd_workspace_size", "ring_attn_cache_write",
     "ring_attn_cache_read", "ring_attn_tree_fwd", "ring_attn_tree_fwd_workspace_size",
+    "ring_attn_window_fwd", "ring_attn_window_fwd_workspace_size", "ring_attn_window_bwd",
+    "ring_attn_window_bwd_workspace_size",
 )
 
 
@@ -150,6 +153,14 @@ def library():
         lib.ring_attn_tree_fwd.restype = ctypes.c_int
         lib.ring_attn_tree_fwd_workspace_size.argtypes = [I] * 8
         lib.ring_attn_tree_fwd_workspace_size.restype = SZ
+        lib.ring_attn_window_fwd.argtypes = [P] * 6 + [SZ] + [I] * 12 + [P]
+        lib.ring_attn_window_fwd.restype = ctypes.c_int
+        lib.ring_attn_window_fwd_workspace_size.argtypes = [I] * 8
+        lib.ring_attn_window_fwd_workspace_size.restype = SZ
+        lib.ring_attn_window_bwd.argtypes = [P] * 10 + [SZ] + [I] * 13 + [P]
+        lib.ring_attn_window_bwd.restype = ctypes.c_int
+        lib.ring_attn_window_bwd_workspace_size.argtypes = [I] * 11
+        lib.ring_attn_window_bwd_workspace_size.restype = SZ
         for name in EXPORTS:
             f = getattr(lib, name)
             if f.restype is ctypes.c_int or name in ("ring_attn_fwd", "ring_attn_ring_step_fwd",
@@ -928,6 +939,72 @@ def qk_norm_rope_bwd(q, k, wq, wk, dq_out, dk_out, n_shards=1, layout="contiguou
     _run(dev.index, lib.ring_attn_qk_norm_rope_bwd, *head, gq, gk, dqp, dkp, dwq.data_ptr(), dwk.data_ptr(),
          workspace.data_ptr(), workspace.numel(), *tail, _stream_ptr(stream, dev.index))
     return dq, dk, dwq, dwk
+
+
+def _whole(x, name):
+    """An integer argument that the library takes as a C int."""
+    x = operator.index(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} does not fit 32 bits")
+    return x
+
+
+def window_fwd(q, k, v, n_shards, window, sinks=0, causal=True, layout="zigzag", out_dtype=None, out=None, lse=None,
+               workspace=None, stream=None):
+    """ring_attn_window_fwd: attention of whole sequences, q [B,H,L,d], k and v [B,Hkv,L,d] in the layout's order, where
+    the token at natural position p sees the tokens j <= p with p - j < window, and the first `sinks` ones (causal=False:
+    |p - j| < window, and the first ones).  Returns (out [B,H,L,d] in out_dtype -- q's, or float32 -- and lse [B,H,L]
+    float32)."""
+    B, H, Hkv, L, d = _need_qkv(q, k, v)
+    dev, lib = q.device, library()
+    if out_dtype is None:
+        out_dtype = q.dtype
+    elif out_dtype not in (q.dtype, torch.float32):
+        raise ValueError("out_dtype must be q's dtype or float32")
+    n, window, sinks = _whole(n_shards, "n_shards"), _whole(window, "window"), _whole(sinks, "sinks")
+    code, lay = _dtype_code(q.dtype), _layout(layout)
+    given = out, lse, workspace
+    out, op = _output(out, "out", dev, q.shape, out_dtype)
+    lse, lp = _output(lse, "lse", dev, (B, H, L), torch.float32)
+    need = int(lib.ring_attn_window_fwd_workspace_size(B, H, Hkv, L, d, n, lay, code))
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _need_workspace(workspace, need, dev)
+    _hand_over(stream, dev.index, (given[0], out), (given[1], lse), (given[2], workspace))
+    _run(dev.index, lib.ring_attn_window_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), op, lp, workspace.data_ptr(),
+         workspace.numel(), B, H, Hkv, L, d, n, window, sinks, int(bool(causal)), lay, code, _DTYPES[out_dtype],
+         _stream_ptr(stream, dev.index))
+    return out, lse
+
+
+def window_bwd(q, k, v, out, lse, dout, n_shards, window, sinks=0, causal=True, layout="zigzag", grad_dtype=torch.float32,
+               dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """ring_attn_window_bwd: the gradients of window_fwd's inputs from that of its output, dout (q's dtype), with the
+    forward's out (q's dtype or float32) and lse.  Returns (dq, dk, dv) in grad_dtype."""
+    B, H, Hkv, L, d = _need_qkv(q, k, v)
+    dev, lib = q.device, library()
+    _need(out, "out", dev, q.shape)
+    if out.dtype not in (q.dtype, torch.float32):
+        raise ValueError("out must be in q's dtype or float32")
+    _need(lse, "lse", dev, (B, H, L), torch.float32)
+    _need(dout, "dout", dev, q.shape, q.dtype)
+    n, window, sinks = _whole(n_shards, "n_shards"), _whole(window, "window"), _whole(sinks, "sinks")
+    code, gcode, lay, causal = _dtype_code(q.dtype), _dtype_code(grad_dtype), _layout(layout), int(bool(causal))
+    given = dq, dk, dv, workspace
+    dq, dqp = _output(dq, "dq", dev, q.shape, grad_dtype)
+    dk, dkp = _output(dk, "dk", dev, k.shape, grad_dtype)
+    dv, dvp = _output(dv, "dv", dev, k.shape, grad_dtype)
+    need = int(lib.ring_attn_window_bwd_workspace_size(B, H, Hkv, L, d, n, window, sinks, causal, lay, code))
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _need_workspace(workspace, need, dev)
+    _hand_over(stream, dev.index, (given[0], dq), (given[1], dk), (given[2], dv), (given[3], workspace))
+    _run(dev.index, lib.ring_attn_window_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+         dout.data_ptr(), dqp, dkp, dvp, workspace.data_ptr(), workspace.numel(), B, H, Hkv, L, d, n, window, sinks, causal,
+         lay, code, _DTYPES[out.dtype], gcode, _stream_ptr(stream, dev.index))
+    return dq, dk, dv
 
 
 class KVCache(NamedTuple):

@@ -1,0 +1,105 @@
+// window.cuh -- attention of a whole sequence through a sliding window, with a few first tokens that stay visible
+// (sinks): what its kernels share.
+//
+// Natural positions p (query) and j (key) of a sequence of L tokens, window W >= 1, S sinks:
+//   causal:  p sees j  iff  j <= p and (p - j < W or j < S);      otherwise:  iff  |p - j| < W or j < S.
+//   s = q k / sqrt(d),  out = sum_j exp(s_j - lse) v_j,  lse = ln sum_j exp(s_j);
+//   D = dout . out,  P = exp(s - lse),  dS = P (dout . v - D) / sqrt(d),  dq = dS k,  dk = dS^T q,  dv = P^T dout,
+// dk and dv summed over the query heads that share a kv head.  Every row sees itself.
+//
+// The kernels work in natural order whatever the layout: a tile is a run of consecutive positions, so that a query tile
+// meets W / tile + 1 key tiles and the sinks' in every layout (in the striped one's buffer order a tile of 128 rows spans
+// 128 n positions, and most of what it meets would lie outside the window).  Only loads and stores know the layout.
+#pragma once
+
+#include "ra_internal.h"
+
+namespace ra {
+
+// Clamped to the sequence: 1 <= W <= L, 0 <= S <= L.
+struct Band {
+    int L, W, S, causal;
+};
+
+RA_HD bool band_sees(const Band& b, int p, int j)
+{
+    if (b.causal) return j <= p && (p - j < b.W || j < b.S);
+    return (p - j < b.W && j - p < b.W) || j < b.S;
+}
+
+// Do all of the queries [q0, q0 + nq) see all of the keys [k0, k0 + nk), every one of them in the sequence?
+RA_HD bool band_tile_whole(const Band& b, int q0, int nq, int k0, int nk)
+{
+    const int q1 = q0 + nq - 1, k1 = k0 + nk - 1;
+    if (q1 >= b.L || k1 >= b.L || (b.causal && k1 > q0)) return false;
+    return k1 < b.S || (q1 - k0 < b.W && (b.causal || k1 - q0 < b.W));
+}
+
+// The key tiles (of `tile` positions) that queries [q0, q0 + rows) meet: [0, sinks) and [first, last).
+struct TileRun {
+    int sinks, first, last;
+    RA_HD int count() const { return sinks + last - first; }
+    RA_HD int at(int i) const { return i < sinks ? i : first + (i - sinks); }
+};
+
+RA_HD TileRun key_tiles(const Band& b, int q0, int rows, int tile)
+{
+    const int q1 = q0 + rows < b.L ? q0 + rows : b.L;  // one past the last query
+    const int lo = q0 - b.W + 1 > 0 ? q0 - b.W + 1 : 0;
+    const int hi = b.causal || b.W > b.L - q1 ? (b.causal ? q1 : b.L) : q1 + b.W - 1;  // one past the last key of a window
+    TileRun r;
+    r.first = lo / tile;
+    r.last = (hi + tile - 1) / tile;
+    const int limit = b.causal && b.S > q1 ? q1 : b.S;  // one past the last sink that a query sees
+    const int st = (limit + tile - 1) / tile;
+    if (st >= r.first) {  // the sinks' tiles run into the window's: one run
+        r.first = 0;
+        r.sinks = 0;
+        if (st > r.last) r.last = st;
+    } else {
+        r.sinks = st;
+    }
+    return r;
+}
+
+// The query tiles that keys [k0, k0 + rows) meet through the window, and from which of them on (causal: any; otherwise
+// those before too) they are met as sinks alone.
+struct QueryRun {
+    int first, last;
+};
+
+RA_HD QueryRun query_tiles(const Band& b, int k0, int rows, int tile)
+{
+    const int k1 = k0 + rows < b.L ? k0 + rows : b.L;
+    QueryRun r;
+    if (k0 < b.S) {  // sinks: every query, or (causal) every later one
+        r.first = b.causal ? k0 / tile : 0;
+        r.last = (b.L + tile - 1) / tile;
+        return r;
+    }
+    const int lo = b.causal ? k0 : (k0 - b.W + 1 > 0 ? k0 - b.W + 1 : 0);
+    const int hi = b.W > b.L - k1 ? b.L : k1 + b.W - 1;
+    r.first = lo / tile;
+    r.last = (hi + tile - 1) / tile;
+    return r;
+}
+
+struct WindowArgs {
+    Geometry geo;
+    Band band;
+    int B, H, Hkv, G;
+    const void *q, *k, *v;
+    const void *out, *dout;  // backward
+    void* o;                 // forward
+    const float* D;          // backward: [B][H][L], natural order
+    float* lse;
+    void *dq, *dk, *dv;
+    float scale, scale_log2;
+    int out_dtype, grad_dtype, saved_dtype;
+};
+
+// CUDA-core path (window_simt.cu).
+cudaError_t launch_window_fwd_simt(const WindowArgs& a, int d, int dtype, cudaStream_t s);
+cudaError_t launch_window_bwd_simt(const WindowArgs& a, float* D, int d, int dtype, cudaStream_t s);
+
+}  // namespace ra

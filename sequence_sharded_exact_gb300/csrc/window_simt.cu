@@ -1,0 +1,400 @@
+// window_simt.cu -- attention through a window (window.cuh) on the CUDA cores: any dtype, layout and length.
+//
+// A block of 256 threads takes 64 consecutive positions of one head (queries, or keys in the dK/dV kernel) and walks the
+// tiles of 64 that they meet.  Every operand lies transposed in shared memory, [d][64], as float32: the products over the
+// head dimension (scores, dout . v) read four values of both operands with two 16-byte loads for 16 multiply-adds, and
+// the products over positions (P V, dS K, P^T dO, dS^T Q) read four consecutive positions of a column likewise.
+// Backward: one kernel over query tiles for dQ, one over key tiles for dK and dV, both recompute P = exp(s - lse): seven
+// products in place of five, and no sum whose order varies.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include <mutex>
+
+#include "window.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kT = 64, kStride = kT + 4, kThreads = 256;
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+__device__ __forceinline__ void load4(const float* p, float (&f)[4])
+{
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&f)[4])
+{
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xffff0000u);
+    f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store1(void* p, long long i, float v, int dtype)
+{
+    if (dtype == 1)
+        static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+    else
+        static_cast<float*>(p)[i] = v;
+}
+
+// 64 positions from p0 of one head's rows, transposed to [D][kStride]; positions past the sequence are zeros.
+template <typename T, int D>
+__device__ __forceinline__ void load_tile(const Geometry& g, const T* head, int p0, float* dst, float scale = 1.f)
+{
+    const int row = threadIdx.x % kT, p = p0 + row;
+    const T* src = p < g.L ? head + (long long)buffer_row(g, p) * D : nullptr;
+#pragma unroll 4
+    for (int c = threadIdx.x / kT * 4; c < D; c += kThreads / kT * 4) {
+        float f[4] = {0.f, 0.f, 0.f, 0.f};
+        if (src) load4(src + c, f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[(c + i) * kStride + row] = f[i] * scale;
+    }
+}
+
+// acc[i][j] += sum_c a[c][4 ty + i] b[c][4 tx + j].
+template <int D>
+__device__ __forceinline__ void dot_tile(const float* a, const float* b, float (&acc)[4][4])
+{
+    const float* pa = a + threadIdx.x / 16 * 4;
+    const float* pb = b + threadIdx.x % 16 * 4;
+#pragma unroll 8
+    for (int c = 0; c < D; ++c) {
+        float x[4], y[4];
+        load4(pa + c * kStride, x);
+        load4(pb + c * kStride, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+    }
+}
+
+// acc[i][k] += sum_j w[4 ty + i][j] b[tx + 16 k][j].  Hidden terms, marked by a weight below 0 (kNegative: P) or of 0
+// (kZero: dS), are left out, so that what is not finite in a hidden row stays out of the sums.
+enum Hidden { kNone, kNegative, kZero };
+template <int D, Hidden kHow>
+__device__ __forceinline__ void apply_rows(const float* w, const float* b, float (&acc)[4][D / 16])
+{
+    const float* pw = w + threadIdx.x / 16 * 4 * kStride;
+    const float* pb = b + threadIdx.x % 16 * kStride;
+#pragma unroll 2
+    for (int j = 0; j < kT; j += 4) {
+        float x[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load4(pw + i * kStride + j, x[i]);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            float y[4];
+            load4(pb + 16 * k * kStride + j, y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (kHow == kNone || (kHow == kNegative ? !(x[i][e] < 0.f) : x[i][e] != 0.f)) acc[i][k] = fmaf(x[i][e], y[e], acc[i][k]);
+        }
+    }
+}
+template <int D, Hidden kHow>
+__device__ __forceinline__ void apply_tile(bool whole, const float* w, const float* b, float (&acc)[4][D / 16])
+{
+    if (whole)
+        apply_rows<D, kNone>(w, b, acc);
+    else
+        apply_rows<D, kHow>(w, b, acc);
+}
+
+__device__ __forceinline__ void put4(float* w, const float (&x)[4][4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4*>(w + (threadIdx.x / 16 * 4 + i) * kStride + threadIdx.x % 16 * 4) =
+            make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+}
+
+__device__ __forceinline__ float max16(float v)
+{
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float sum16(float v)
+{
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(const WindowArgs a)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *sq = sm, *sk = sq + D * kStride, *sv = sk + D * kStride, *sp = sv + D * kStride;
+    const int tiles = (a.band.L + kT - 1) / kT;
+    const int q0 = (int)(blockIdx.x % tiles) * kT, zq = (int)(blockIdx.x / tiles), zk = zq / a.G;  // (b H + h) / G = b Hkv + g
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const long long per = (long long)a.band.L * D;
+    load_tile<T, D>(a.geo, static_cast<const T*>(a.q) + zq * per, q0, sq, a.scale_log2);
+    float m[4], l[4], o[4][D / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) o[i][k] = 0.f;
+    }
+    const TileRun run = key_tiles(a.band, q0, kT, kT);
+    for (int t = 0; t < run.count(); ++t) {
+        const int k0 = run.at(t) * kT;
+        __syncthreads();
+        load_tile<T, D>(a.geo, static_cast<const T*>(a.k) + zk * per, k0, sk);
+        load_tile<T, D>(a.geo, static_cast<const T*>(a.v) + zk * per, k0, sv);
+        __syncthreads();
+        float s[4][4] = {};
+        dot_tile<D>(sq, sk, s);
+        const bool whole = band_tile_whole(a.band, q0, kT, k0, kT);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = q0 + 4 * ty + i;
+            float mx = -INFINITY, sum = 0.f;
+            unsigned hidden = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = k0 + 4 * tx + j;
+                if (!whole && (key >= a.band.L || !band_sees(a.band, p, key))) hidden |= 1u << j;
+                if (!(hidden >> j & 1u)) mx = fmaxf(mx, s[i][j]);
+            }
+            const float mn = fmaxf(m[i], max16(mx)), ref = mn == -INFINITY ? 0.f : mn, alpha = exp2f(m[i] - ref);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = hidden >> j & 1u ? -1.f : exp2f(s[i][j] - ref);
+                if (!(hidden >> j & 1u)) sum += s[i][j];
+            }
+            l[i] = l[i] * alpha + sum16(sum);
+            m[i] = mn;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) o[i][k] *= alpha;
+        }
+        put4(sp, s);
+        __syncthreads();
+        apply_tile<D, kNegative>(whole, sp, sv, o);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int p = q0 + 4 * ty + i;
+        if (p >= a.band.L) continue;
+        const long long row = (long long)zq * a.band.L + buffer_row(a.geo, p);
+        const float inv = 1.f / l[i];
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) store1(a.o, row * D + tx + 16 * k, o[i][k] * inv, a.out_dtype);
+        if (tx == 0) a.lse[row] = (m[i] + log2f(l[i])) * kLn2;
+    }
+}
+
+// P (-1 where hidden) and dS (0) of a tile whose rows are queries, or keys, from the scores and dout . v.
+template <bool kKeyRows>
+__device__ __forceinline__ void weights(const WindowArgs& a, int r0, int c0, const float (&lse2)[4], const float (&Dv)[4], float (&s)[4][4],
+                                        float (&dp)[4][4])
+{
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = r0 + 4 * ty + i, c = c0 + 4 * tx + j, p = kKeyRows ? c : r, key = kKeyRows ? r : c;
+            const bool sees = p < a.band.L && key < a.band.L && band_sees(a.band, p, key);
+            s[i][j] = sees ? exp2f(s[i][j] - lse2[kKeyRows ? j : i]) : -1.f;
+            dp[i][j] = sees ? s[i][j] * (dp[i][j] - Dv[kKeyRows ? j : i]) * a.scale : 0.f;
+        }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) window_bwd_dq_simt_kernel(const WindowArgs a)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *sq = sm, *sd = sq + D * kStride, *sk = sd + D * kStride, *sv = sk + D * kStride, *sp = sv + D * kStride;
+    const int tiles = (a.band.L + kT - 1) / kT;
+    const int q0 = (int)(blockIdx.x % tiles) * kT, zq = (int)(blockIdx.x / tiles), zk = zq / a.G;
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const long long per = (long long)a.band.L * D;
+    load_tile<T, D>(a.geo, static_cast<const T*>(a.q) + zq * per, q0, sq, a.scale_log2);
+    load_tile<T, D>(a.geo, static_cast<const T*>(a.dout) + zq * per, q0, sd);
+    float lse2[4], Dv[4], acc[4][D / 16] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int p = q0 + 4 * ty + i;
+        const bool has = p < a.band.L;
+        lse2[i] = has ? a.lse[(long long)zq * a.band.L + buffer_row(a.geo, p)] * kLog2e : 0.f;
+        Dv[i] = has ? a.D[(long long)zq * a.band.L + p] : 0.f;
+    }
+    const TileRun run = key_tiles(a.band, q0, kT, kT);
+    for (int t = 0; t < run.count(); ++t) {
+        const int k0 = run.at(t) * kT;
+        __syncthreads();
+        load_tile<T, D>(a.geo, static_cast<const T*>(a.k) + zk * per, k0, sk);
+        load_tile<T, D>(a.geo, static_cast<const T*>(a.v) + zk * per, k0, sv);
+        __syncthreads();
+        float s[4][4] = {}, dp[4][4] = {};
+        dot_tile<D>(sq, sk, s);
+        dot_tile<D>(sd, sv, dp);
+        weights<false>(a, q0, k0, lse2, Dv, s, dp);
+        put4(sp, dp);
+        __syncthreads();
+        apply_tile<D, kZero>(band_tile_whole(a.band, q0, kT, k0, kT), sp, sk, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int p = q0 + 4 * ty + i;
+        if (p >= a.band.L) continue;
+        const long long row = (long long)zq * a.band.L + buffer_row(a.geo, p);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) store1(a.dq, row * D + tx + 16 * k, acc[i][k], a.grad_dtype);
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) window_bwd_dkv_simt_kernel(const WindowArgs a)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *sk = sm, *sv = sk + D * kStride, *sq = sv + D * kStride, *sd = sq + D * kStride, *sp = sd + D * kStride, *ss = sp + kT * kStride;
+    const int tiles = (a.band.L + kT - 1) / kT;
+    const int k0 = (int)(blockIdx.x % tiles) * kT, zk = (int)(blockIdx.x / tiles);
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const long long per = (long long)a.band.L * D;
+    load_tile<T, D>(a.geo, static_cast<const T*>(a.k) + zk * per, k0, sk, a.scale_log2);
+    load_tile<T, D>(a.geo, static_cast<const T*>(a.v) + zk * per, k0, sv);
+    float dk[4][D / 16] = {}, dv[4][D / 16] = {};
+    const QueryRun run = query_tiles(a.band, k0, kT, kT);
+    for (int h = 0; h < a.G; ++h) {
+        const int zq = zk * a.G + h;
+        for (int t = run.first; t < run.last; ++t) {
+            const int q0 = t * kT;
+            __syncthreads();
+            load_tile<T, D>(a.geo, static_cast<const T*>(a.q) + zq * per, q0, sq);
+            load_tile<T, D>(a.geo, static_cast<const T*>(a.dout) + zq * per, q0, sd);
+            float lse2[4], Dv[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int p = q0 + 4 * tx + j;
+                const bool has = p < a.band.L;
+                lse2[j] = has ? a.lse[(long long)zq * a.band.L + buffer_row(a.geo, p)] * kLog2e : 0.f;
+                Dv[j] = has ? a.D[(long long)zq * a.band.L + p] : 0.f;
+            }
+            __syncthreads();
+            float s[4][4] = {}, dp[4][4] = {};
+            dot_tile<D>(sk, sq, s);
+            dot_tile<D>(sv, sd, dp);
+            weights<true>(a, k0, q0, lse2, Dv, s, dp);
+            put4(sp, s);
+            put4(ss, dp);
+            __syncthreads();
+            const bool whole = band_tile_whole(a.band, q0, kT, k0, kT);
+            apply_tile<D, kNegative>(whole, sp, sd, dv);
+            apply_tile<D, kZero>(whole, ss, sq, dk);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int p = k0 + 4 * ty + i;
+        if (p >= a.band.L) continue;
+        const long long row = (long long)zk * a.band.L + buffer_row(a.geo, p);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            store1(a.dk, row * D + tx + 16 * k, dk[i][k], a.grad_dtype);
+            store1(a.dv, row * D + tx + 16 * k, dv[i][k], a.grad_dtype);
+        }
+    }
+}
+
+// D = dout . out per row, in natural order: a warp per row.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) window_rowdot_kernel(const WindowArgs a, float* Dv)
+{
+    const long long rows = (long long)a.B * a.H * a.band.L;
+    const int lane = threadIdx.x & 31;
+    for (long long x = (long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; x < rows; x += (long long)gridDim.x * (kThreads / 32)) {
+        const long long z = x / a.band.L, row = z * a.band.L + buffer_row(a.geo, (int)(x - z * a.band.L));
+        float sum = 0.f;
+        for (int c = lane; c < D; c += 32) {
+            const float o = a.saved_dtype == 1 ? to_f(static_cast<const __nv_bfloat16*>(a.out)[row * D + c])
+                                               : static_cast<const float*>(a.out)[row * D + c];
+            sum = fmaf(o, to_f(static_cast<const T*>(a.dout)[row * D + c]), sum);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) Dv[x] = sum;
+    }
+}
+
+constexpr size_t tile_bytes(int d) { return (size_t)d * kStride * sizeof(float); }
+constexpr size_t kWeightBytes = (size_t)kT * kStride * sizeof(float);
+
+template <typename K>
+cudaError_t allow(K kernel, size_t smem, std::mutex& mu, bool (&done)[64])
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lk(mu);
+    if (!done[dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        done[dev] = true;
+    }
+    return cudaSuccess;
+}
+
+template <typename T, int D>
+cudaError_t fwd(const WindowArgs& a, cudaStream_t s)
+{
+    static std::mutex mu;
+    static bool done[64];
+    constexpr size_t smem = 3 * tile_bytes(D) + kWeightBytes;
+    cudaError_t e = allow(window_fwd_simt_kernel<T, D>, smem, mu, done);
+    if (e != cudaSuccess) return e;
+    const long long blocks = (long long)a.B * a.H * ((a.band.L + kT - 1) / kT);
+    window_fwd_simt_kernel<T, D><<<(unsigned)blocks, kThreads, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t bwd(const WindowArgs& a, float* Dv, cudaStream_t s)
+{
+    static std::mutex mu;
+    static bool done_q[64], done_k[64];
+    constexpr size_t smem_q = 4 * tile_bytes(D) + kWeightBytes, smem_k = 4 * tile_bytes(D) + 2 * kWeightBytes;
+    cudaError_t e = allow(window_bwd_dq_simt_kernel<T, D>, smem_q, mu, done_q);
+    if (e == cudaSuccess) e = allow(window_bwd_dkv_simt_kernel<T, D>, smem_k, mu, done_k);
+    if (e != cudaSuccess) return e;
+    const long long rows = (long long)a.B * a.H * a.band.L, need = (rows + kThreads / 32 - 1) / (kThreads / 32);
+    const long long most = (long long)device_sm_count() * 8;
+    window_rowdot_kernel<T, D><<<(unsigned)(need < most ? need : most), kThreads, 0, s>>>(a, Dv);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const long long tiles = (a.band.L + kT - 1) / kT;
+    window_bwd_dq_simt_kernel<T, D><<<(unsigned)(a.B * (long long)a.H * tiles), kThreads, smem_q, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    window_bwd_dkv_simt_kernel<T, D><<<(unsigned)(a.B * (long long)a.Hkv * tiles), kThreads, smem_k, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_fwd_simt(const WindowArgs& a, int d, int dtype, cudaStream_t s)
+{
+    if (dtype == 1) return d == 128 ? fwd<__nv_bfloat16, 128>(a, s) : fwd<__nv_bfloat16, 64>(a, s);
+    return d == 128 ? fwd<float, 128>(a, s) : fwd<float, 64>(a, s);
+}
+
+cudaError_t launch_window_bwd_simt(const WindowArgs& args, float* D, int d, int dtype, cudaStream_t s)
+{
+    WindowArgs a = args;
+    a.D = D;
+    if (dtype == 1) return d == 128 ? bwd<__nv_bfloat16, 128>(a, D, s) : bwd<__nv_bfloat16, 64>(a, D, s);
+    return d == 128 ? bwd<float, 128>(a, D, s) : bwd<float, 64>(a, D, s);
+}
+
+}  // namespace ra
