@@ -69,6 +69,9 @@ typedef int ra_status;
 #define RA_LAYOUT_ZIGZAG 1
 #define RA_LAYOUT_STRIPED 2
 
+#define RA_SPECTRUM_WHOLE 0  /* of positions with several axes: pair i of a head has the frequency base^(-2i/d) */
+#define RA_SPECTRUM_AXIS 1   /* pair u of an axis with m pairs has base^(-u/m) */
+
 #define RA_F32 0
 #define RA_BF16 1
 #define RA_E4M3 2   /* of a key/value cache only: e4m3 values, one power-of-two scale per row */
@@ -440,6 +443,32 @@ RA_API ra_status ring_attn_qk_norm_rope_bwd(const void* q, const long long* q_st
                                             int L, int d, int n_shards, int shard, int layout, int dtype, double base,
                                             double eps, const int* positions, void* stream);
 RA_API size_t ring_attn_qk_norm_rope_bwd_workspace_size(int d);
+
+/*
+ * ring_attn_qk_rope_axes -- the rotation by positions with several axes (time, height and width of images and video),
+ * after the norm of every head or alone: the d/2 pairs of a head are dealt out to the axes in order, sections[0] pairs to
+ * axis 0 and so on, and pair i of axis a turns by positions[a] of its token times its frequency:
+ *   RA_SPECTRUM_WHOLE: base^(-2i/d), i the pair's place in the head;   RA_SPECTRUM_AXIS: base^(-u/m), u its place among
+ *   the m pairs of its axis.
+ *   axes: 1 to 4;  sections: HOST array of `axes` pair counts >= 0, d/2 in all;  positions: DEVICE int32 [axes][B][rows],
+ *   4-byte aligned, any int values, in the order of the buffers' rows.
+ *   wq, wk: as ring_attn_qk_norm_rope, or both NULL: the rotation alone (eps is then not used).
+ *   q [B][H][rows][d], k [B][Hkv][rows][d]: any rows >= 1 (a whole sequence, one device's shard, a step's tokens).
+ *   Everything else as ring_attn_qk_norm_rope.
+ *
+ * ring_attn_qk_rope_axes_bwd -- its gradients, as ring_attn_qk_norm_rope_bwd's (same workspace).  Without weights dq and
+ *   dk are dq_out and dk_out turned back; q, k, their strides, dwq, dwk and the workspace are then not used and may be NULL.
+ */
+RA_API ra_status ring_attn_qk_rope_axes(const void* q, const long long* q_strides, const void* k, const long long* k_strides,
+                                        const float* wq, const float* wk, void* q_out, void* k_out, int B, int H, int Hkv,
+                                        int rows, int d, int axes, const int* sections, int spectrum, int dtype, double base,
+                                        double eps, const int* positions, void* stream);
+RA_API ra_status ring_attn_qk_rope_axes_bwd(const void* q, const long long* q_strides, const void* k,
+                                            const long long* k_strides, const float* wq, const float* wk, const void* dq_out,
+                                            const void* dk_out, void* dq, void* dk, float* dwq, float* dwk, void* workspace,
+                                            size_t workspace_bytes, int B, int H, int Hkv, int rows, int d, int axes,
+                                            const int* sections, int spectrum, int dtype, double base, double eps,
+                                            const int* positions, void* stream);
 
 /*
  * Attention of whole sequences through a sliding window, with a few first tokens that stay visible (sinks).

@@ -37,6 +37,8 @@ from .binding import (  # noqa: F401
     lse_merge,
     qk_norm_rope,
     qk_norm_rope_bwd,
+    qk_rope_axes,
+    qk_rope_axes_bwd,
     ring_step_fwd,
     ring_step_fwd_accumulate,
     rope,
@@ -50,5 +52,5 @@ from .binding import (  # noqa: F401
     window_bwd,
     window_fwd,
 )
-from .autograd import ring_attention, ring_qk_norm_rope  # noqa: F401
+from .autograd import ring_attention, ring_qk_norm_rope, ring_qk_rope_axes  # noqa: F401
 from .ring import RingAttention, ring_attention_distributed  # noqa: F401

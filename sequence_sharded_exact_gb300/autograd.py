@@ -90,3 +90,38 @@ def ring_qk_norm_rope(q, k, wq, wk, n_shards=1, layout="contiguous", base=10000.
     k [B,Hkv,rows,d] and the weights wq, wk [d] (any float dtype).  See qk_norm_rope for the arguments; q, k, the
     weights and the outputs' gradients are copied where the calls cannot read them as they lie."""
     return _QkNormRope.apply(q, k, wq, wk, n_shards, layout, base, eps, shard, positions)
+
+
+class _QkRopeAxes(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, positions, sections, base, eps, spectrum):
+        q, k, norm = binding.as_rows(q), binding.as_rows(k), wq is not None
+        cfg = dict(base=base, eps=eps, spectrum=spectrum)
+        w = (_dense(wq.float()), _dense(wk.float())) if norm else (None, None)
+        q_out, k_out = binding.qk_rope_axes(q, k, positions, sections, *w, **cfg)
+        ctx.save_for_backward(positions, *((q, k, wq, wk) if norm else ()))
+        ctx.cfg, ctx.sections = cfg, sections
+        return q_out, k_out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        positions, *saved = ctx.saved_tensors
+        how = dict(ctx.cfg)
+        if saved:
+            q, k, wq, wk = saved
+            how.update(q=q, k=k, wq=_dense(wq.float()), wk=_dense(wk.float()))
+        dq, dk, dwq, dwk = binding.qk_rope_axes_bwd(_dense(dq_out), _dense(dk_out), positions, ctx.sections, **how)
+        if saved:
+            dwq, dwk = dwq.to(wq.dtype), dwk.to(wk.dtype)
+        return dq, dk, dwq, dwk, None, None, None, None, None
+
+
+def ring_qk_rope_axes(q, k, positions, sections, wq=None, wk=None, base=10000.0, eps=1e-6, spectrum="whole"):
+    """The rotation of q [B,H,rows,d] and k [B,Hkv,rows,d] by positions with several axes [axes, B, rows] int32, after the
+    norms of the heads where their weights wq, wk [d] (any float dtype) are given: differentiable with respect to q, k
+    and the weights.  See qk_rope_axes for the arguments; q, k, the weights and the outputs' gradients are copied where the
+    calls cannot read them as they lie."""
+    if (wq is None) != (wk is None):
+        raise ValueError("wq and wk must both be given, or neither")
+    return _QkRopeAxes.apply(q, k, wq, wk, positions, tuple(sections), base, eps, spectrum)

@@ -22,6 +22,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libringattn.so")
 
 RA_OK, RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_CUDA, RA_ERR_NO_DEVICE, RA_ERR_TIMEOUT = range(6)
+SPECTRA = {"whole": 0, "axis": 1}
 LAYOUTS = {"contiguous": 0, "zigzag": 1, "striped": 2}
 PATHS = {1: "simt", 2: "tcgen05"}
 RA_DEVICE_TIMEOUT = 1
@@ -49,7 +50,7 @@ EXPORTS = (
     "ring_attn_qk_norm_rope_bwd", "ring_attn_qk_norm_rope_bwd_workspace_size", "ring_attn_cache_write",
     "ring_attn_cache_read", "ring_attn_tree_fwd", "ring_attn_tree_fwd_workspace_size",
     "ring_attn_window_fwd", "ring_attn_window_fwd_workspace_size", "ring_attn_window_bwd",
-    "ring_attn_window_bwd_workspace_size",
+    "ring_attn_window_bwd_workspace_size", "ring_attn_qk_rope_axes", "ring_attn_qk_rope_axes_bwd",
 )
 
 
@@ -153,6 +154,10 @@ def library():
         lib.ring_attn_tree_fwd.restype = ctypes.c_int
         lib.ring_attn_tree_fwd_workspace_size.argtypes = [I] * 8
         lib.ring_attn_tree_fwd_workspace_size.restype = SZ
+        lib.ring_attn_qk_rope_axes.argtypes = [P] * 8 + [I] * 6 + [P, I, I, D, D, P, P]
+        lib.ring_attn_qk_rope_axes.restype = ctypes.c_int
+        lib.ring_attn_qk_rope_axes_bwd.argtypes = [P] * 13 + [SZ] + [I] * 6 + [P, I, I, D, D, P, P]
+        lib.ring_attn_qk_rope_axes_bwd.restype = ctypes.c_int
         lib.ring_attn_window_fwd.argtypes = [P] * 6 + [SZ] + [I] * 12 + [P]
         lib.ring_attn_window_fwd.restype = ctypes.c_int
         lib.ring_attn_window_fwd_workspace_size.argtypes = [I] * 8
@@ -190,7 +195,7 @@ def _load_calls(lib):
         loader.exec_module(module)
         module.bind(*(ctypes.cast(getattr(lib, "ring_attn_" + f), ctypes.c_void_p).value for f in (
             "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size", "cache_write", "cache_read", "tree_fwd",
-            "tree_fwd_workspace_size")))
+            "tree_fwd_workspace_size", "qk_rope_axes")))
     except (ImportError, OSError, AttributeError, TypeError, ValueError) as e:
         warnings.warn(f"the compiled calls in {path} do not load, calls go through Python: {e}", RuntimeWarning)
         return
@@ -938,6 +943,82 @@ def qk_norm_rope_bwd(q, k, wq, wk, dq_out, dk_out, n_shards=1, layout="contiguou
     _hand_over(stream, dev.index, (given[0], dq), (given[1], dk), (None, dwq), (None, dwk), (given[2], workspace))
     _run(dev.index, lib.ring_attn_qk_norm_rope_bwd, *head, gq, gk, dqp, dkp, dwq.data_ptr(), dwk.data_ptr(),
          workspace.data_ptr(), workspace.numel(), *tail, _stream_ptr(stream, dev.index))
+    return dq, dk, dwq, dwk
+
+
+def _axes_args(dev, B, rows, d, positions, sections, spectrum, wq, wk):
+    """(address of the positions, number of axes, the sections as a C array, the spectrum's code, addresses of the weights)"""
+    sections = [_whole(x, "a section") for x in sections]
+    if not 1 <= len(sections) <= 4:
+        raise ValueError("sections must name 1 to 4 axes")
+    if spectrum not in SPECTRA:
+        raise ValueError(f"spectrum must be one of {tuple(SPECTRA)}")
+    pos = _fits(positions, "positions", dev, (len(sections), B, rows), torch.int32)
+    if (wq is None) != (wk is None):
+        raise ValueError("wq and wk must both be given, or neither")
+    w = (None, None) if wq is None else (_fits(wq, "wq", dev, (d,), torch.float32), _fits(wk, "wk", dev, (d,), torch.float32))
+    return pos, len(sections), (ctypes.c_int * len(sections))(*sections), SPECTRA[spectrum], w
+
+
+def qk_rope_axes(q, k, positions, sections, wq=None, wk=None, base=10000.0, eps=1e-6, spectrum="whole", q_out=None, k_out=None,
+                 stream=None):
+    """ring_attn_qk_rope_axes: every head of q [B,H,rows,d] and k [B,Hkv,rows,d] rotated by positions with several axes,
+    positions [axes, B, rows] int32: the first sections[0] pairs of a head by its token's position along axis 0, the next
+    sections[1] by axis 1 and so on (d/2 pairs in all).  spectrum "whole": pair i of the head has the frequency
+    base^(-2i/d); "axis": pair u of an axis's m has base^(-u/m).  With weights wq, wk [d] float32 the heads are normed
+    first, as in qk_norm_rope.  q and k may be slices of a fused projection.  Returns (q_out, k_out), contiguous, in q's
+    dtype."""
+    if _calls is not None and stream is None:
+        done = _calls.qk_rope_axes(q, k, positions, sections, wq, wk, base, eps, spectrum, q_out, k_out)
+        if done is not None:
+            return done
+    (B, H, rows, d), (_, Hkv, _, _), code = _dims4(q, k, "q and k")
+    dev, dt = q.device, q.dtype
+    qp, qs = _rows(q, "q", dev, (B, H, rows, d), dt)
+    kp, ks = _rows(k, "k", dev, (B, Hkv, rows, d), dt)
+    pos, axes, sec, spec, w = _axes_args(dev, B, rows, d, positions, sections, spectrum, wq, wk)
+    given = q_out, k_out
+    q_out, qo = _output(q_out, "q_out", dev, q.shape, dt)
+    k_out, ko = _output(k_out, "k_out", dev, k.shape, dt)
+    _hand_over(stream, dev.index, (given[0], q_out), (given[1], k_out))
+    _run(dev.index, library().ring_attn_qk_rope_axes, qp, qs, kp, ks, *w, qo, ko, B, H, Hkv, rows, d, axes, sec, spec, code,
+         float(base), float(eps), pos, _stream_ptr(stream, dev.index))
+    return q_out, k_out
+
+
+def qk_rope_axes_bwd(dq_out, dk_out, positions, sections, q=None, k=None, wq=None, wk=None, base=10000.0, eps=1e-6,
+                     spectrum="whole", dq=None, dk=None, workspace=None, stream=None):
+    """ring_attn_qk_rope_axes_bwd: the gradients of qk_rope_axes' inputs from those of its outputs, dq_out [B,H,rows,d] and
+    dk_out [B,Hkv,rows,d] (contiguous).  With the norm's weights q and k are needed too.  Returns (dq, dk, dwq, dwk), the
+    last two None without weights; dq may be dq_out, dk may be dk_out."""
+    (B, H, rows, d), (_, Hkv, _, _), code = _dims4(dq_out, dk_out, "dq_out and dk_out")
+    dev, dt = dq_out.device, dq_out.dtype
+    gq, gk = _fits(dq_out, "dq_out", dev, (B, H, rows, d), dt), _fits(dk_out, "dk_out", dev, (B, Hkv, rows, d), dt)
+    pos, axes, sec, spec, w = _axes_args(dev, B, rows, d, positions, sections, spectrum, wq, wk)
+    lib, given = library(), (dq, dk, workspace)
+    qp = qs = kp = ks = dwq = dwk = None
+    new = []
+    if wq is None:
+        if q is not None or k is not None:
+            raise ValueError("q and k are the norm's inputs: they need its weights")
+        ws, ws_bytes = None, 0
+    else:
+        qp, qs = _rows(q, "q", dev, (B, H, rows, d), dt)
+        kp, ks = _rows(k, "k", dev, (B, Hkv, rows, d), dt)
+        dwq, dwk = torch.empty(d, dtype=torch.float32, device=dev), torch.empty(d, dtype=torch.float32, device=dev)
+        need = lib.ring_attn_qk_norm_rope_bwd_workspace_size(d)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _need_workspace(workspace, need, dev)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel()
+        new = [(None, dwq), (None, dwk), (given[2], workspace)]
+    dq, dqp = _output(dq, "dq", dev, (B, H, rows, d), dt)
+    dk, dkp = _output(dk, "dk", dev, (B, Hkv, rows, d), dt)
+    _hand_over(stream, dev.index, (given[0], dq), (given[1], dk), *new)
+    _run(dev.index, lib.ring_attn_qk_rope_axes_bwd, qp, qs, kp, ks, *w, gq, gk, dqp, dkp,
+         None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(), ws, ws_bytes, B, H, Hkv, rows, d, axes,
+         sec, spec, code, float(base), float(eps), pos, _stream_ptr(stream, dev.index))
     return dq, dk, dwq, dwk
 
 

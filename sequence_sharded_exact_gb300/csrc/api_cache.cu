@@ -59,19 +59,42 @@ ra_status norm_rope_impl(Problem p, NormRope n, const long long* qs, const long 
     if (n.shard < -1 || n.shard >= p.n) return fail(RA_ERR_INVALID_ARG, "shard %d outside [-1, n_shards)", n.shard);
     if (!(n.base > 0.0) || !isfinite(n.base)) return fail(RA_ERR_INVALID_ARG, "base must be positive and finite");
     if (!(n.eps >= 0.0) || !isfinite(n.eps)) return fail(RA_ERR_INVALID_ARG, "eps must be >= 0 and finite");
-    if ((st = check_ptrs({n.q, n.k, n.wq, n.wk, n.out_q, n.out_k})) != RA_OK) return st;
-    if ((st = check_ints("positions", n.positions, true)) != RA_OK) return st;
+    const bool axes = n.axes.count > 0, alone = axes && !n.wq && !n.wk;  // the rotation alone
+    if ((st = check_ptrs({n.out_q, n.out_k})) != RA_OK) return st;
+    if (!alone && (st = check_ptrs({n.wq, n.wk})) != RA_OK) return st;
+    if (!(alone && backward) && (st = check_ptrs({n.q, n.k})) != RA_OK) return st;
+    if ((st = check_ints("positions", n.positions, !axes)) != RA_OK) return st;
     const long long rows = n.shard < 0 ? p.L : p.L / p.n;
     if ((st = take_strides("q", qs, p.B, p.H, rows, p.d, p.dtype, n.q_strides)) != RA_OK) return st;
     if ((st = take_strides("k", ks, p.B, p.Hkv, rows, p.d, p.dtype, n.k_strides)) != RA_OK) return st;
-    if (backward) {
-        if ((st = check_ptrs({n.dyq, n.dyk, n.dwq, n.dwk})) != RA_OK) return st;
+    if (backward && (st = check_ptrs({n.dyq, n.dyk})) != RA_OK) return st;
+    if (backward && !alone) {
+        if ((st = check_ptrs({n.dwq, n.dwk})) != RA_OK) return st;
         if ((st = check_workspace(workspace, workspace_bytes, ring_attn_qk_norm_rope_bwd_workspace_size(p.d))) != RA_OK) return st;
         n.partial = static_cast<float*>(workspace);
     }
     if ((st = check_device()) != RA_OK) return st;
     cudaError_t e = launch_norm_rope(p, n, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail(e, backward ? "ring_attn_qk_norm_rope_bwd launch" : "ring_attn_qk_norm_rope launch");
+    if (e != cudaSuccess) return cuda_fail(e, axes ? (backward ? "ring_attn_qk_rope_axes_bwd launch" : "ring_attn_qk_rope_axes launch")
+                                               : backward ? "ring_attn_qk_norm_rope_bwd launch" : "ring_attn_qk_norm_rope launch");
+    return RA_OK;
+}
+
+ra_status take_axes(int d, int axes, const int* sections, int spectrum, RopeAxes& out)
+{
+    if (axes < 1 || axes > kMaxAxes) return fail(RA_ERR_INVALID_ARG, "axes must lie in [1, %d] (got %d)", kMaxAxes, axes);
+    if (!sections) return fail(RA_ERR_INVALID_ARG, "sections is NULL");
+    if (spectrum != RA_SPECTRUM_WHOLE && spectrum != RA_SPECTRUM_AXIS) return fail(RA_ERR_INVALID_ARG, "unknown spectrum %d", spectrum);
+    out = RopeAxes{};
+    out.count = axes;
+    out.own_spectrum = spectrum == RA_SPECTRUM_AXIS;
+    long long sum = 0;
+    for (int i = 0; i < axes; ++i) {
+        if (sections[i] < 0) return fail(RA_ERR_INVALID_ARG, "section %d is negative", i);
+        out.sections[i] = sections[i];
+        sum += sections[i];
+    }
+    if (sum != d / 2) return fail(RA_ERR_INVALID_ARG, "the sections must have d / 2 = %d pairs in all (got %lld)", d / 2, sum);
     return RA_OK;
 }
 
@@ -159,6 +182,55 @@ ra_status ring_attn_qk_norm_rope_bwd(const void* q, const long long* q_strides, 
     n.base = base;
     n.eps = eps;
     return norm_rope_impl(Problem{B, H, Hkv, L, d, n_shards, 1, layout, dtype}, n, q_strides, k_strides, true, workspace_bytes,
+                          workspace, stream);
+}
+
+ra_status ring_attn_qk_rope_axes(const void* q, const long long* q_strides, const void* k, const long long* k_strides,
+                                 const float* wq, const float* wk, void* q_out, void* k_out, int B, int H, int Hkv, int rows, int d,
+                                 int axes, const int* sections, int spectrum, int dtype, double base, double eps,
+                                 const int* positions, void* stream)
+{
+    NormRope n = {};
+    n.q = q;
+    n.k = k;
+    n.wq = wq;
+    n.wk = wk;
+    n.out_q = q_out;
+    n.out_k = k_out;
+    n.positions = positions;
+    n.shard = -1;
+    n.base = base;
+    n.eps = eps;
+    const ra_status st = take_axes(d, axes, sections, spectrum, n.axes);
+    if (st != RA_OK) return st;
+    return norm_rope_impl(Problem{B, H, Hkv, rows, d, 1, 1, RA_LAYOUT_CONTIGUOUS, dtype}, n, q_strides, k_strides, false, 0, nullptr, stream);
+}
+
+ra_status ring_attn_qk_rope_axes_bwd(const void* q, const long long* q_strides, const void* k, const long long* k_strides,
+                                     const float* wq, const float* wk, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                                     float* dwq, float* dwk, void* workspace, size_t workspace_bytes, int B, int H, int Hkv, int rows,
+                                     int d, int axes, const int* sections, int spectrum, int dtype, double base, double eps,
+                                     const int* positions, void* stream)
+{
+    NormRope n = {};
+    n.q = q;
+    n.k = k;
+    n.wq = wq;
+    n.wk = wk;
+    n.dyq = dq_out;
+    n.dyk = dk_out;
+    n.out_q = dq;
+    n.out_k = dk;
+    n.dwq = dwq;
+    n.dwk = dwk;
+    n.positions = positions;
+    n.shard = -1;
+    n.base = base;
+    n.eps = eps;
+    ra_status st = take_axes(d, axes, sections, spectrum, n.axes);
+    if (st != RA_OK) return st;
+    if (!dq_out) return fail(RA_ERR_INVALID_ARG, "dq_out is NULL");  // (what tells the backward from the forward)
+    return norm_rope_impl(Problem{B, H, Hkv, rows, d, 1, 1, RA_LAYOUT_CONTIGUOUS, dtype}, n, q_strides, k_strides, true, workspace_bytes,
                           workspace, stream);
 }
 

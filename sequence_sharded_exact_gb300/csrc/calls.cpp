@@ -26,6 +26,7 @@ decltype(&ring_attn_cache_write) write_cache = nullptr;
 decltype(&ring_attn_cache_read) read_cache = nullptr;
 decltype(&ring_attn_tree_fwd) tree = nullptr;
 decltype(&ring_attn_tree_fwd_workspace_size) tree_workspace = nullptr;
+decltype(&ring_attn_qk_rope_axes) rope_axes = nullptr;
 
 using at::ScalarType;
 using at::Tensor;
@@ -353,14 +354,47 @@ PyObject* py_norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// q, k, positions, sections, wq, wk, base, eps, spectrum, q_out, k_out
+PyObject* py_rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return answer(n, 11, [&]() -> PyObject* {
+        const Tensor &q = tensor(a[0]), &k = tensor(a[1]);
+        four(q);
+        four(k);
+        const Call c(q);
+        const int64_t B = q.size(0), H = q.size(1), rows = q.size(2), d = q.size(3), Hkv = k.size(1);
+        const ScalarType dt = q.scalar_type();
+        const int code = code_of(dt);
+        const Call::Rows qr = c.rows(q, {B, H, rows, d}, dt), kr = c.rows(k, {B, Hkv, rows, d}, dt);
+        if (!PyTuple_CheckExact(a[3])) throw Misfit{};
+        const Py_ssize_t axes = PyTuple_GET_SIZE(a[3]);
+        if (axes < 1 || axes > 4) throw Misfit{};
+        int sections[4];
+        for (Py_ssize_t i = 0; i < axes; ++i) sections[i] = whole_number(PyTuple_GET_ITEM(a[3], i));
+        const auto* pos = static_cast<const int*>(c.dense(a[2], {axes, B, rows}, at::kInt));
+        const auto* wq = static_cast<const float*>(c.optional(a[4], {d}, at::kFloat));
+        const auto* wk = static_cast<const float*>(c.optional(a[5], {d}, at::kFloat));
+        if ((wq == nullptr) != (wk == nullptr)) throw Misfit{};
+        const double base = real_number(a[6]), eps = real_number(a[7]);
+        if (!PyUnicode_CheckExact(a[8])) throw Misfit{};
+        const bool whole = PyUnicode_CompareWithASCIIString(a[8], "whole") == 0;
+        if (!whole && PyUnicode_CompareWithASCIIString(a[8], "axis") != 0) throw Misfit{};
+        Tensor qo = c.output(a[9], {B, H, rows, d}, dt), ko = c.output(a[10], {B, Hkv, rows, d}, dt);
+        accept(rope_axes(qr.p, qr.given(), kr.p, kr.given(), wq, wk, qo.data_ptr(), ko.data_ptr(), small(B), small(H), small(Hkv), small(rows),
+                         small(d), (int)axes, sections, whole ? RA_SPECTRUM_WHOLE : RA_SPECTRUM_AXIS, code, base, eps, pos, c.stream()));
+        return pair_of(std::move(qo), std::move(ko));
+    });
+}
+
 // bind(address, ...): the library's functions, in the order of the pointers above.
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     void** to[] = {reinterpret_cast<void**>(&norm_rope), reinterpret_cast<void**>(&norm_rope_bwd),
                    reinterpret_cast<void**>(&norm_rope_bwd_workspace), reinterpret_cast<void**>(&write_cache),
-                   reinterpret_cast<void**>(&read_cache), reinterpret_cast<void**>(&tree), reinterpret_cast<void**>(&tree_workspace)};
+                   reinterpret_cast<void**>(&read_cache), reinterpret_cast<void**>(&tree), reinterpret_cast<void**>(&tree_workspace),
+                   reinterpret_cast<void**>(&rope_axes)};
     if (n != (Py_ssize_t)(sizeof(to) / sizeof(to[0]))) {
-        PyErr_SetString(PyExc_TypeError, "seven addresses");
+        PyErr_SetString(PyExc_TypeError, "one address for each function");
         return nullptr;
     }
     for (Py_ssize_t i = 0; i < n; ++i) {
@@ -381,6 +415,7 @@ PyMethodDef methods[] = {{"bind", FAST(py_bind), nullptr},
                          {"cache_read", FAST(py_cache_read), nullptr},
                          {"qk_norm_rope", FAST(py_norm_rope), nullptr},
                          {"qk_norm_rope_bwd", FAST(py_norm_rope_bwd), nullptr},
+                         {"qk_rope_axes", FAST(py_rope_axes), nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -17,6 +17,10 @@
 // forward of 64K positions took 258 us in place of 214 (as it was then).  Loads of four heads are issued before the
 // first is used (two or eight: 240, 232 us).  All sums are float32; the output is rounded once.
 //
+// Positions with several axes (time, height, width of images and video): each pair of a head takes the position along
+// its axis, read once per group; everything else is as above.  Without weights the rotation alone, whose gradient is
+// the rotation back.
+//
 // With few tokens one group per position would leave most SMs idle, so the heads of a position are
 // then split over several groups, which repeat the angles.
 //
@@ -27,6 +31,7 @@
 // boundaries.
 #include <cuda_bf16.h>
 #include <math.h>
+#include <string.h>
 
 #include "ra_internal.h"
 
@@ -48,7 +53,14 @@ struct NormRopeArgs {
     float* partial;                // backward: [gridDim.x][2][d] sums of dw
     float eps;
     unsigned long long turn[64];   // theta_i / (2 pi) in units of 2^-64 turn
+    long long axis_step;           // with axes: positions of one axis, B * rows
+    float sign;                    // rotation alone: -1 turns back
+    uint8_t axis[64];              // each pair's axis
 };
+
+// What a kernel is compiled for: the norm with the rotation by one position, by a position along each pair's axis, or
+// that rotation alone.
+enum class Kind { kNatural, kAxes, kAxesAlone };
 
 template <typename T>
 struct Pack;
@@ -107,14 +119,18 @@ __device__ __forceinline__ float group_sum(float v, unsigned mask)
 }
 
 // cos and sin of this lane's pairs at natural position p.
-template <int PAIRS>
+template <int PAIRS, Kind kKind>
 __device__ __forceinline__ void angles(const NormRopeArgs& a, int ch, long long p, float (&c)[PAIRS], float (&s)[PAIRS])
 {
+    long long along[PAIRS];  // with axes p is the token's place in an axis's positions
+#pragma unroll
+    for (int j = 0; j < PAIRS; ++j) along[j] = kKind == Kind::kNatural ? p : a.pos[a.axis[ch * PAIRS + j] * a.axis_step + p];
 #pragma unroll
     for (int j = 0; j < PAIRS; ++j) {
-        const unsigned long long u = (unsigned long long)p * a.turn[ch * PAIRS + j];
+        const unsigned long long u = (unsigned long long)along[j] * a.turn[ch * PAIRS + j];
         // as a signed fraction, [-1/2, 1/2) turn: a small angle of either sign keeps a float32's precision
         sincospif(2.0f * ((float)(int)(unsigned)(u >> 32) * 2.3283064365386963e-10f), &s[j], &c[j]);  // 2^-32
+        if (kKind == Kind::kAxesAlone) s[j] *= a.sign;
     }
 }
 
@@ -126,7 +142,7 @@ struct Item {
 
 // kFew: the heads of a position are shared out, and all counts fit 32 bits (a 64-bit division is a hundred instructions:
 // of 5.4 us that 128 tokens took 0.6).
-template <bool kFew>
+template <bool kFew, Kind kKind>
 __device__ __forceinline__ Item item_of(const NormRopeArgs& a, long long idx)
 {
     Item it;
@@ -143,11 +159,14 @@ __device__ __forceinline__ Item item_of(const NormRopeArgs& a, long long idx)
         it.h0 = 0;
         it.h1 = a.H + a.Hkv;
     }
-    it.p = a.pos ? a.pos[(long long)it.b * a.rows + it.r] : natural_position(a.geo, it.r + a.row_off);
+    if constexpr (kKind != Kind::kNatural)
+        it.p = (long long)it.b * a.rows + it.r;
+    else
+        it.p = a.pos ? a.pos[(long long)it.b * a.rows + it.r] : natural_position(a.geo, it.r + a.row_off);
     return it;
 }
 
-template <typename T, int D, int U>
+template <typename T, int D, int U, bool kNorm>
 __device__ __forceinline__ void fwd_heads(const T* x, long long xs, T* y, long long ys, int count, const float* w,
                                           const float* c, const float* s, float eps, unsigned mask)
 {
@@ -161,14 +180,17 @@ __device__ __forceinline__ void fwd_heads(const T* x, long long xs, T* y, long l
             if (h + u >= count) break;
             float f[V];
             Pack<T>::unpack(raw[u], f);
-            float ss = 0.f;
+            float r = 1.f;
+            if constexpr (kNorm) {
+                float ss = 0.f;
 #pragma unroll
-            for (int e = 0; e < V; ++e) ss = fmaf(f[e], f[e], ss);
-            ss = group_sum<LPR>(ss, mask);
-            const float r = rsqrtf(ss * (1.0f / D) + eps);
+                for (int e = 0; e < V; ++e) ss = fmaf(f[e], f[e], ss);
+                ss = group_sum<LPR>(ss, mask);
+                r = rsqrtf(ss * (1.0f / D) + eps);
+            }
 #pragma unroll
             for (int j = 0; j < V / 2; ++j) {
-                const float a0 = f[2 * j] * r * w[2 * j], a1 = f[2 * j + 1] * r * w[2 * j + 1];
+                const float a0 = kNorm ? f[2 * j] * r * w[2 * j] : f[2 * j], a1 = kNorm ? f[2 * j + 1] * r * w[2 * j + 1] : f[2 * j + 1];
                 f[2 * j] = a0 * c[j] - a1 * s[j];
                 f[2 * j + 1] = a0 * s[j] + a1 * c[j];
             }
@@ -177,10 +199,11 @@ __device__ __forceinline__ void fwd_heads(const T* x, long long xs, T* y, long l
     }
 }
 
-template <typename T, int D, bool kFew>
+template <typename T, int D, bool kFew, Kind kKind>
 __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const NormRopeArgs a)
 {
     constexpr int V = Pack<T>::kElems, LPR = D / V, U = 4;
+    constexpr bool kNorm = kKind != Kind::kAxesAlone;
     const int ch = threadIdx.x % LPR;
     const unsigned mask = group_mask<LPR>();
     const long long total = (long long)a.B * a.rows * a.splits;
@@ -188,21 +211,21 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const NormRopeAr
     float wq[V], wk[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        wq[e] = a.wq[ch * V + e];
-        wk[e] = a.wk[ch * V + e];
+        wq[e] = kNorm ? a.wq[ch * V + e] : 1.f;
+        wk[e] = kNorm ? a.wk[ch * V + e] : 1.f;
     }
     for (long long idx = (long long)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR; idx < total; idx += step) {
-        const Item it = item_of<kFew>(a, idx);
+        const Item it = item_of<kFew, kKind>(a, idx);
         float c[V / 2], s[V / 2];
-        angles<V / 2>(a, ch, it.p, c, s);
+        angles<V / 2, kKind>(a, ch, it.p, c, s);
         const long long ys = (long long)a.rows * D;
         const int q1 = it.h1 < a.H ? it.h1 : a.H, k0 = it.h0 > a.H ? it.h0 : a.H;
         if (it.h0 < q1)
-            fwd_heads<T, D, U>(static_cast<const T*>(a.q) + it.b * a.qs[0] + it.h0 * a.qs[1] + it.r * a.qs[2] + ch * V, a.qs[1],
+            fwd_heads<T, D, U, kNorm>(static_cast<const T*>(a.q) + it.b * a.qs[0] + it.h0 * a.qs[1] + it.r * a.qs[2] + ch * V, a.qs[1],
                                static_cast<T*>(a.oq) + ((long long)it.b * a.H + it.h0) * ys + (long long)it.r * D + ch * V, ys,
                                q1 - it.h0, wq, c, s, a.eps, mask);
         if (k0 < it.h1)
-            fwd_heads<T, D, U>(static_cast<const T*>(a.k) + it.b * a.ks[0] + (k0 - a.H) * a.ks[1] + it.r * a.ks[2] + ch * V, a.ks[1],
+            fwd_heads<T, D, U, kNorm>(static_cast<const T*>(a.k) + it.b * a.ks[0] + (k0 - a.H) * a.ks[1] + it.r * a.ks[2] + ch * V, a.ks[1],
                                static_cast<T*>(a.ok) + ((long long)it.b * a.Hkv + k0 - a.H) * ys + (long long)it.r * D + ch * V, ys,
                                it.h1 - k0, wk, c, s, a.eps, mask);
     }
@@ -260,7 +283,7 @@ __device__ __forceinline__ void bwd_heads(const T* x, long long xs, const T* dy,
 
 // dw is summed per lane over the rows it meets, then over the block's groups, in a fixed order;
 // norm_rope_dw_kernel adds the blocks' sums in block order, so the result does not vary from run to run.
-template <typename T, int D, bool kFew>
+template <typename T, int D, bool kFew, Kind kKind>
 __global__ void __launch_bounds__(kThreads, kNormRopeBwdPerSm) norm_rope_bwd_kernel(const NormRopeArgs a)
 {
     constexpr int V = Pack<T>::kElems, LPR = D / V, U = 4, kGroups = kThreads / LPR;
@@ -278,9 +301,9 @@ __global__ void __launch_bounds__(kThreads, kNormRopeBwdPerSm) norm_rope_bwd_ker
         dq[e] = dk[e] = 0.f;
     }
     for (long long idx = (long long)blockIdx.x * kGroups + grp; idx < total; idx += step) {
-        const Item it = item_of<kFew>(a, idx);
+        const Item it = item_of<kFew, kKind>(a, idx);
         float c[V / 2], s[V / 2];
-        angles<V / 2>(a, ch, it.p, c, s);
+        angles<V / 2, kKind>(a, ch, it.p, c, s);
         const long long ys = (long long)a.rows * D;
         const int q1 = it.h1 < a.H ? it.h1 : a.H, k0 = it.h0 > a.H ? it.h0 : a.H;
         if (it.h0 < q1) {
@@ -332,8 +355,8 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* partial
     }
 }
 
-template <typename T, int D>
-cudaError_t launch(NormRopeArgs& a, bool backward, float* dwq, float* dwk, cudaStream_t s)
+template <typename T, int D, Kind kKind>
+cudaError_t launch_kind(NormRopeArgs& a, bool backward, float* dwq, float* dwk, cudaStream_t s)
 {
     constexpr int LPR = D / Pack<T>::kElems, kGroups = kThreads / LPR;
     // Groups enough for 1024 threads on every SM, as long as a position has heads to share out.
@@ -348,32 +371,46 @@ cudaError_t launch(NormRopeArgs& a, bool backward, float* dwq, float* dwk, cudaS
     if (!backward) {  // a block per group of positions: the last ones fill the SMs evenly
         if (grid > 0x7fffffffLL) grid = 0x7fffffffLL;
         if (few)
-            norm_rope_kernel<T, D, true><<<(unsigned)grid, kThreads, 0, s>>>(a);
+            norm_rope_kernel<T, D, true, kKind><<<(unsigned)grid, kThreads, 0, s>>>(a);
         else
-            norm_rope_kernel<T, D, false><<<(unsigned)grid, kThreads, 0, s>>>(a);
+            norm_rope_kernel<T, D, false, kKind><<<(unsigned)grid, kThreads, 0, s>>>(a);
         return cudaGetLastError();
     }
-    // as many blocks as are resident, which take the positions in turns: their dw leave a partial sum each
-    const long long most = (long long)device_sm_count() * kNormRopeBwdPerSm;
-    if (grid > most) grid = most;
-    if (grid > kNormRopeBwdBlocks) grid = kNormRopeBwdBlocks;
-    if (few)
-        norm_rope_bwd_kernel<T, D, true><<<(unsigned)grid, kThreads, 0, s>>>(a);
-    else
-        norm_rope_bwd_kernel<T, D, false><<<(unsigned)grid, kThreads, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    // starts while the first launch runs and waits for its results in the kernel
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * D / 32);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = s;
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, static_cast<const float*>(a.partial), (int)grid, D, dwq, dwk);
+    if constexpr (kKind == Kind::kAxesAlone) {
+        return cudaErrorInvalidValue;  // (a rotation's gradient is a rotation)
+    } else {
+        // as many blocks as are resident, which take the positions in turns: their dw leave a partial sum each
+        const long long most = (long long)device_sm_count() * kNormRopeBwdPerSm;
+        if (grid > most) grid = most;
+        if (grid > kNormRopeBwdBlocks) grid = kNormRopeBwdBlocks;
+        if (few)
+            norm_rope_bwd_kernel<T, D, true, kKind><<<(unsigned)grid, kThreads, 0, s>>>(a);
+        else
+            norm_rope_bwd_kernel<T, D, false, kKind><<<(unsigned)grid, kThreads, 0, s>>>(a);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        // starts while the first launch runs and waits for its results in the kernel
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * D / 32);
+        cfg.blockDim = dim3(1024);
+        cfg.stream = s;
+        cudaLaunchAttribute early;
+        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        early.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &early;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, static_cast<const float*>(a.partial), (int)grid, D, dwq, dwk);
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch(NormRopeArgs& a, Kind kind, bool backward, float* dwq, float* dwk, cudaStream_t s)
+{
+    switch (kind) {
+        case Kind::kAxes: return launch_kind<T, D, Kind::kAxes>(a, backward, dwq, dwk, s);
+        case Kind::kAxesAlone: return launch_kind<T, D, Kind::kAxesAlone>(a, backward, dwq, dwk, s);
+        default: return launch_kind<T, D, Kind::kNatural>(a, backward, dwq, dwk, s);
+    }
 }
 
 }  // namespace
@@ -402,12 +439,33 @@ cudaError_t launch_norm_rope(const Problem& p, const NormRope& n, cudaStream_t s
     a.ok = n.out_k;
     a.partial = n.partial;
     a.eps = (float)n.eps;
-    rope_turns(n.base, p.d, a.turn);
-    const bool backward = n.dyq != nullptr;
+    bool backward = n.dyq != nullptr;
+    Kind kind = Kind::kNatural;
+    a.axis_step = 0;
+    a.sign = 1.f;
+    memset(a.axis, 0, sizeof(a.axis));
+    if (n.axes.count == 0) {
+        rope_turns(n.base, p.d, a.turn);
+    } else {
+        rope_axes_turns(n.base, p.d, n.axes, a.turn);
+        a.axis_step = (long long)p.B * a.rows;
+        for (int x = 0, i = 0; x < n.axes.count; ++x)
+            for (int u = 0; u < n.axes.sections[x]; ++u, ++i) a.axis[i] = (uint8_t)x;
+        kind = n.wq ? Kind::kAxes : Kind::kAxesAlone;
+    }
+    if (kind == Kind::kAxesAlone && backward) {  // the gradients, turned back
+        a.q = n.dyq;
+        a.k = n.dyk;
+        a.sign = -1.f;
+        const long long row = p.d, head = (long long)a.rows * p.d;
+        a.qs[0] = p.H * head, a.qs[1] = head, a.qs[2] = row;
+        a.ks[0] = p.Hkv * head, a.ks[1] = head, a.ks[2] = row;
+        backward = false;
+    }
     if (p.dtype == 1)
-        return p.d == 128 ? launch<__nv_bfloat16, 128>(a, backward, n.dwq, n.dwk, s)
-                          : launch<__nv_bfloat16, 64>(a, backward, n.dwq, n.dwk, s);
-    return p.d == 128 ? launch<float, 128>(a, backward, n.dwq, n.dwk, s) : launch<float, 64>(a, backward, n.dwq, n.dwk, s);
+        return p.d == 128 ? launch<__nv_bfloat16, 128>(a, kind, backward, n.dwq, n.dwk, s)
+                          : launch<__nv_bfloat16, 64>(a, kind, backward, n.dwq, n.dwk, s);
+    return p.d == 128 ? launch<float, 128>(a, kind, backward, n.dwq, n.dwk, s) : launch<float, 64>(a, kind, backward, n.dwq, n.dwk, s);
 }
 
 }  // namespace ra

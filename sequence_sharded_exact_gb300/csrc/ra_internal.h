@@ -81,6 +81,17 @@ cudaError_t launch_rope(const Problem& p, void* x, double base, int inverse, cud
 // theta_i / (2 pi) for theta_i = base^(-2i/d), i < d / 2, in units of 2^-64 turn (0 behind them).
 void rope_turns(double base, int d, unsigned long long (&turn)[64]);
 
+// Positions with several axes: pair i of a head turns by the position along its axis, the first sections[0] pairs by axis 0
+// and so on (0 behind the last axis).
+constexpr int kMaxAxes = 4;
+struct RopeAxes {
+    int count;               // 0: one axis, NormRope::positions or the layout's
+    int sections[kMaxAxes];  // pairs of each axis, d / 2 in all
+    int own_spectrum;        // 0: pair i has theta_i; 1: pair u of an axis with m pairs has base^(-u / m)
+};
+// Their frequencies, as rope_turns.
+void rope_axes_turns(double base, int d, const RopeAxes& axes, unsigned long long (&turn)[64]);
+
 // Norm of every query and key head, then the rotation (dyq null), or the gradients of that.
 struct NormRope {
     const void *q, *k;          // [B][heads][rows][d] by element strides (batch, head, row), d contiguous
@@ -89,7 +100,8 @@ struct NormRope {
     const void *dyq, *dyk;      // backward: gradients of the outputs, contiguous
     void *out_q, *out_k;        // outputs, or dq and dk, contiguous
     float *dwq, *dwk, *partial; // backward: [d] each; kNormRopeBwdBlocks * 2 * d floats of scratch
-    const int* positions;       // [B][rows], or null: natural positions of the layout
+    const int* positions;       // [B][rows], or null: natural positions of the layout; with axes [axes.count][B][rows]
+    RopeAxes axes;              // with axes wq and wk may be null: the rotation alone (backward: of dyq, dyk alone)
     int shard;                  // -1: whole-sequence buffers; else one device's shard
     double base, eps;
 };

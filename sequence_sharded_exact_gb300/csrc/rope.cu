@@ -147,6 +147,31 @@ void rope_turns(double base, int d, unsigned long long (&turn)[64])
     last_d = d;
 }
 
+void rope_axes_turns(double base, int d, const RopeAxes& axes, unsigned long long (&turn)[64])
+{
+    if (!axes.own_spectrum) {  // pair i has the frequency that it has without axes
+        rope_turns(base, d, turn);
+        return;
+    }
+    thread_local double last_base = 0.0;
+    thread_local int last_sections[kMaxAxes];
+    thread_local unsigned long long last[64];
+    if (base != last_base || memcmp(last_sections, axes.sections, sizeof(last_sections)) != 0) {
+        const double two_pi = 6.283185307179586476925;
+        int i = 0;
+        for (int x = 0; x < kMaxAxes; ++x)
+            for (int u = 0; u < axes.sections[x] && i < 64; ++u, ++i) {
+                double frac = pow(base, -(double)u / axes.sections[x]) / two_pi;
+                frac -= floor(frac);
+                last[i] = (unsigned long long)ldexp(frac, 64);
+            }
+        for (; i < 64; ++i) last[i] = 0;
+        last_base = base;
+        memcpy(last_sections, axes.sections, sizeof(last_sections));
+    }
+    memcpy(turn, last, sizeof(last));
+}
+
 cudaError_t launch_rope(const Problem& p, void* x, double base, int inverse, cudaStream_t s, int shard)
 {
     RopeArgs a;
