@@ -3,7 +3,7 @@
 
 #include "../../include/ringattn.h"
 #include "ra_internal.h"
-#include "window.cuh"
+#include "window_tc.cuh"
 
 namespace ra {
 namespace {
@@ -77,7 +77,15 @@ ra_status ring_attn_window_fwd(const void* q, const void* k, const void* v, void
     a.o = out;
     a.lse = lse;
     a.out_dtype = out_dtype;
-    const cudaError_t e = launch_window_fwd_simt(a, d, dtype, static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (dtype == RA_BF16 && window_tma_reads(a.geo)) {
+        unsigned int* sw = status_word(&e);
+        if (!sw) return cuda_fail(e, "status word");
+        e = d == 128 ? launch_window_fwd_tc_d128(a, sw, s) : launch_window_fwd_tc_d64(a, sw, s);
+    } else {
+        e = launch_window_fwd_simt(a, d, dtype, s);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "ring_attn_window_fwd launch");
     return RA_OK;
 }

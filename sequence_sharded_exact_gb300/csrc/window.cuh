@@ -102,4 +102,9 @@ struct WindowArgs {
 cudaError_t launch_window_fwd_simt(const WindowArgs& a, int d, int dtype, cudaStream_t s);
 cudaError_t launch_window_bwd_simt(const WindowArgs& a, float* D, int d, int dtype, cudaStream_t s);
 
+
+// Tensor-core path, bf16, layouts that window_tma_reads (window_tc.cuh).
+cudaError_t launch_window_fwd_tc_d128(const WindowArgs& a, unsigned int* status, cudaStream_t s);
+cudaError_t launch_window_fwd_tc_d64(const WindowArgs& a, unsigned int* status, cudaStream_t s);
+
 }  // namespace ra
