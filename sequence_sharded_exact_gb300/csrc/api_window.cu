@@ -34,7 +34,7 @@ ra_status check_space(const void* ws, size_t have, size_t need)
 WindowArgs args_of(const Problem& p, int window, int sinks)
 {
     WindowArgs a = {};
-    a.geo = p.geo();
+    a.geo = a.store_geo = p.geo();
     a.band = Band{p.L, window < p.L ? window : p.L, sinks < p.L ? sinks : p.L, p.causal};
     a.B = p.B;
     a.H = p.H;
@@ -45,6 +45,24 @@ WindowArgs args_of(const Problem& p, int window, int sinks)
     return a;
 }
 
+// bf16 inputs that TMA cannot read in natural order are copied into it, one after another from `at` in the workspace.
+bool copies(const Problem& p) { return p.dtype == RA_BF16 && !window_tma_reads(p.geo()); }
+size_t copy_bytes(const Problem& p, int heads) { return up256((size_t)p.B * heads * p.L * p.d * 2); }
+
+struct Copier {
+    const Problem& p;
+    char* at;
+    cudaStream_t s;
+    cudaError_t e = cudaSuccess;
+    const void* operator()(const void* src, int heads)
+    {
+        void* dst = at;
+        at += copy_bytes(p, heads);
+        if (e == cudaSuccess) e = launch_window_gather(p.geo(), src, dst, (long long)p.B * heads, p.d, s);
+        return dst;
+    }
+};
+
 }  // namespace
 }  // namespace ra
 
@@ -54,8 +72,9 @@ extern "C" {
 
 size_t ring_attn_window_fwd_workspace_size(int B, int H, int Hkv, int L, int d, int n_shards, int layout, int dtype)
 {
-    (void)B, (void)H, (void)Hkv, (void)L, (void)d, (void)n_shards, (void)layout, (void)dtype;
-    return 0;
+    const Problem p{B, H, Hkv, L, d, n_shards, 1, layout, dtype};
+    if (check_window(p, 1, 0) != RA_OK || !copies(p)) return 0;
+    return copy_bytes(p, H) + 2 * copy_bytes(p, Hkv);
 }
 
 ra_status ring_attn_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse, void* workspace,
@@ -79,12 +98,20 @@ ra_status ring_attn_window_fwd(const void* q, const void* k, const void* v, void
     a.out_dtype = out_dtype;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (dtype == RA_BF16 && window_tma_reads(a.geo)) {
+    if (dtype == RA_BF16) {
         unsigned int* sw = status_word(&e);
         if (!sw) return cuda_fail(e, "status word");
+        if (copies(p)) {
+            Copier copy{p, static_cast<char*>(workspace), s};
+            a.q = copy(q, H);
+            a.k = copy(k, Hkv);
+            a.v = copy(v, Hkv);
+            if (copy.e != cudaSuccess) return cuda_fail(copy.e, "ring_attn_window_fwd copies");
+            a.geo = make_geometry(L, 1, RA_LAYOUT_CONTIGUOUS, causal);
+        }
         e = d == 128 ? launch_window_fwd_tc_d128(a, sw, s) : launch_window_fwd_tc_d64(a, sw, s);
     } else {
-        e = launch_window_fwd_simt(a, d, dtype, s);
+        e = launch_window_fwd_simt(a, d, s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "ring_attn_window_fwd launch");
     return RA_OK;
@@ -93,8 +120,11 @@ ra_status ring_attn_window_fwd(const void* q, const void* k, const void* v, void
 size_t ring_attn_window_bwd_workspace_size(int B, int H, int Hkv, int L, int d, int n_shards, int window, int sinks, int causal,
                                            int layout, int dtype)
 {
-    if (check_window(Problem{B, H, Hkv, L, d, n_shards, causal, layout, dtype}, window, sinks) != RA_OK) return 0;
-    return up256((size_t)B * H * L * sizeof(float));
+    const Problem p{B, H, Hkv, L, d, n_shards, causal, layout, dtype};
+    if (check_window(p, window, sinks) != RA_OK) return 0;
+    if (dtype == RA_F32) return up256((size_t)B * H * L * sizeof(float));  // D
+    return window_bwd_plan(args_of(p, window, sinks).band, B, H, Hkv, d).bytes +
+           (copies(p) ? 2 * copy_bytes(p, H) + 2 * copy_bytes(p, Hkv) : 0);
 }
 
 ra_status ring_attn_window_bwd(const void* q, const void* k, const void* v, const void* out, const float* lse, const void* dout,
@@ -123,7 +153,32 @@ ra_status ring_attn_window_bwd(const void* q, const void* k, const void* v, cons
     a.dv = dv;
     a.saved_dtype = out_dtype;
     a.grad_dtype = grad_dtype;
-    const cudaError_t e = launch_window_bwd_simt(a, static_cast<float*>(workspace), d, dtype, static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (dtype == RA_BF16) {
+        unsigned int* sw = status_word(&e);
+        if (!sw) return cuda_fail(e, "status word");
+        char* ws = static_cast<char*>(workspace);
+        WindowBwdPlan plan = window_bwd_plan(a.band, B, H, Hkv, d);
+        plan.lse2 = reinterpret_cast<float*>(ws + plan.lse_at);
+        plan.D = reinterpret_cast<float*>(ws + plan.D_at);
+        plan.dq = reinterpret_cast<float*>(ws + plan.dq_at);
+        plan.part = reinterpret_cast<float*>(ws + plan.part_at);
+        if (copies(p)) {
+            Copier copy{p, ws + plan.bytes, s};
+            a.q = copy(q, H);
+            a.k = copy(k, Hkv);
+            a.v = copy(v, Hkv);
+            a.dout = copy(dout, H);
+            if (copy.e != cudaSuccess) return cuda_fail(copy.e, "ring_attn_window_bwd copies");
+            a.geo = make_geometry(L, 1, RA_LAYOUT_CONTIGUOUS, causal);
+        }
+        e = launch_window_bwd_before(a, plan, d, s);
+        if (e == cudaSuccess) e = d == 128 ? launch_window_bwd_tc_d128(a, plan, sw, s) : launch_window_bwd_tc_d64(a, plan, sw, s);
+        if (e == cudaSuccess) e = launch_window_bwd_after(a, plan, d, s);
+    } else {
+        e = launch_window_bwd_simt(a, static_cast<float*>(workspace), d, s);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "ring_attn_window_bwd launch");
     return RA_OK;
 }

@@ -85,7 +85,8 @@ RA_HD QueryRun query_tiles(const Band& b, int k0, int rows, int tile)
 }
 
 struct WindowArgs {
-    Geometry geo;
+    Geometry geo;        // of the inputs (out and lse apart)
+    Geometry store_geo;  // of all others
     Band band;
     int B, H, Hkv, G;
     const void *q, *k, *v;
@@ -98,13 +99,30 @@ struct WindowArgs {
     int out_dtype, grad_dtype, saved_dtype;
 };
 
-// CUDA-core path (window_simt.cu).
-cudaError_t launch_window_fwd_simt(const WindowArgs& a, int d, int dtype, cudaStream_t s);
-cudaError_t launch_window_bwd_simt(const WindowArgs& a, float* D, int d, int dtype, cudaStream_t s);
+// CUDA-core path: float32 (window_simt.cu).
+cudaError_t launch_window_fwd_simt(const WindowArgs& a, int d, cudaStream_t s);
+cudaError_t launch_window_bwd_simt(const WindowArgs& a, float* D, int d, cudaStream_t s);
 
 
 // Tensor-core path, bf16, layouts that window_tma_reads (window_tc.cuh).
 cudaError_t launch_window_fwd_tc_d128(const WindowArgs& a, unsigned int* status, cudaStream_t s);
 cudaError_t launch_window_fwd_tc_d64(const WindowArgs& a, unsigned int* status, cudaStream_t s);
+
+// The backward's cut and its workspace.
+constexpr int kWindowTile = 128;
+struct WindowBwdPlan {
+    int tiles, sink_tiles, segs;  // tiles of the sequence and with sinks; segments of each of the latter
+    long long sink_items;         // segments in all (0: no sinks)
+    size_t lse_at, D_at, dq_at, part_at, bytes;
+    float *lse2, *D, *dq, *part;
+};
+WindowBwdPlan window_bwd_plan(const Band& b, int B, int H, int Hkv, int d);
+cudaError_t launch_window_bwd_tc_d128(const WindowArgs& a, const WindowBwdPlan& p, unsigned int* status, cudaStream_t s);
+cudaError_t launch_window_bwd_tc_d64(const WindowArgs& a, const WindowBwdPlan& p, unsigned int* status, cudaStream_t s);
+// What comes before and after them (window_aux.cu): D, lse2 and a cleared dq; dq and the sinks' dk and dv.
+cudaError_t launch_window_bwd_before(const WindowArgs& a, const WindowBwdPlan& p, int d, cudaStream_t s);
+cudaError_t launch_window_bwd_after(const WindowArgs& a, const WindowBwdPlan& p, int d, cudaStream_t s);
+// Rows of [heads][L][d] bf16 in natural order.
+cudaError_t launch_window_gather(const Geometry& g, const void* src, void* dst, long long heads, int d, cudaStream_t s);
 
 }  // namespace ra

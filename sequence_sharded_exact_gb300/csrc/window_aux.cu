@@ -1,0 +1,221 @@
+// window_aux.cu -- what the tensor-core kernels of the attention through a window need before and after them (HBM-bound).
+//
+// Before the backward: D = dout . out per row, lse in log2 units and the float32 accumulator of dQ cleared, all in natural
+// order and padded to whole tiles of 128 positions (rows behind the sequence: -lse2 = -infinity, which makes their P 0).
+// After it: dQ from the accumulator to the layout's rows, and the sinks' dK and dV, added over their segments in order.
+// Layouts that TMA cannot read in natural order with one box (window_tc.cuh) are copied into it first.
+// A group of d / 8 lanes has a row, 8 elements (16 bytes of bf16) each.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "ra_internal.h"
+#include "ra_ptx.cuh"
+#include "window.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ void load8(const void* p, long long i, bool bf16, float (&f)[8])
+{
+    if (bf16) {
+        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            f[2 * e] = __uint_as_float(w[e] << 16);
+            f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
+    } else {
+        const float4* v = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        const float4 a = v[0], b = v[1];
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    }
+}
+__device__ __forceinline__ void store8(void* p, long long i, bool bf16, const float (&f)[8])
+{
+    if (bf16) {
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) =
+            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    } else {
+        float4* v = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+        v[0] = make_float4(f[0], f[1], f[2], f[3]);
+        v[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+}
+
+// Row `x` of a padded natural-order array -> its head, position and (if in the sequence) row in the layout's buffers.
+struct Row {
+    int z, p;
+    bool in;
+    long long at;
+};
+__device__ __forceinline__ Row row_of(const Geometry& g, int padded, long long x)
+{
+    Row r;
+    r.z = (int)(x / padded);
+    r.p = (int)(x - (long long)r.z * padded);
+    r.in = r.p < g.L;
+    r.at = r.in ? (long long)r.z * g.L + buffer_row(g, r.p) : 0;
+    return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) before_kernel(const Geometry og, const Geometry dg, const void* out, bool out_bf16, const void* dout,
+                                                          const float* lse, float* lse2, float* Dv, float* dq, int padded, long long rows)
+{
+    constexpr int kLanes = D / 8;
+    const int c = threadIdx.x % kLanes * 8;
+    const long long step = (long long)gridDim.x * (kThreads / kLanes), up = (rows + 31) / 32 * 32;
+    for (long long x = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes; x < up; x += step) {
+        const bool has = x < rows;
+        const Row o = row_of(og, padded, has ? x : 0), g = row_of(dg, padded, has ? x : 0);
+        float sum = 0.f;
+        if (has && o.in) {
+            float a[8], b[8];
+            load8(out, o.at * D + c, out_bf16, a);
+            load8(dout, g.at * D + c, true, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = fmaf(a[e], b[e], sum);
+        }
+#pragma unroll
+        for (int s = kLanes / 2; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        if (!has) continue;
+        const float zero[8] = {};
+        store8(dq, x * D + c, false, zero);
+        if (c == 0) {
+            Dv[x] = sum;
+            lse2[x] = o.in ? -kLog2e * lse[o.at] : -INFINITY;
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) dq_kernel(const Geometry g, const float* acc, void* dq, bool bf16, long long rows, int padded)
+{
+    constexpr int kLanes = D / 8;
+    const int c = threadIdx.x % kLanes * 8;
+    const long long step = (long long)gridDim.x * (kThreads / kLanes);
+    for (long long x = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes; x < rows; x += step) {
+        const int z = (int)(x / g.L), r = (int)(x - (long long)z * g.L);  // the buffers' rows in their order
+        float f[8];
+        load8(acc, ((long long)z * padded + natural_position(g, r)) * D + c, false, f);
+        store8(dq, x * D + c, bf16, f);
+    }
+}
+
+// dK and dV of the sinks' tiles: segments [2][128][D] added in order.
+template <int D>
+__global__ void __launch_bounds__(kThreads) sinks_kernel(const Geometry g, const Band band, const float* part, void* dk, void* dv, bool bf16,
+                                                         int sink_tiles, int segs, long long rows)
+{
+    constexpr int kLanes = D / 8;
+    const int c = threadIdx.x % kLanes * 8;
+    const long long step = (long long)gridDim.x * (kThreads / kLanes);
+    for (long long x = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes; x < rows; x += step) {
+        const int r = (int)(x % kWindowTile), which = (int)(x / kWindowTile % 2);
+        const long long rest = x / (2 * kWindowTile);
+        const int tile = (int)(rest % sink_tiles), z = (int)(rest / sink_tiles), p = tile * kWindowTile + r;
+        if (p >= g.L) continue;
+        const QueryRun q = query_tiles(band, tile * kWindowTile, kWindowTile, kWindowTile);
+        const int n = q.last - q.first;
+        float sum[8] = {};
+        for (int s = 0; s < segs; ++s) {
+            if ((long long)n * s / segs == (long long)n * (s + 1) / segs) continue;  // an empty segment leaves nothing
+            float f[8];
+            load8(part, ((((long long)z * sink_tiles + tile) * segs + s) * 2 * kWindowTile + which * kWindowTile + r) * D + c, false, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += f[e];
+        }
+        store8(which ? dv : dk, ((long long)z * g.L + buffer_row(g, p)) * D + c, bf16, sum);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) gather_kernel(const Geometry g, const uint4* src, uint4* dst, long long rows)
+{
+    constexpr int kLanes = D / 8;
+    const int c = threadIdx.x % kLanes;
+    const long long step = (long long)gridDim.x * (kThreads / kLanes);
+    for (long long x = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes; x < rows; x += step) {
+        const long long z = x / g.L;
+        dst[x * kLanes + c] = src[(z * g.L + buffer_row(g, (int)(x - z * g.L))) * kLanes + c];
+    }
+}
+
+unsigned blocks(long long rows, int d)
+{
+    const long long per = kThreads / (d / 8), want = (rows + per - 1) / per, most = (long long)device_sm_count() * 16;
+    return (unsigned)(want < most ? want : most);
+}
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+}  // namespace
+
+WindowBwdPlan window_bwd_plan(const Band& b, int B, int H, int Hkv, int d)
+{
+    WindowBwdPlan p = {};
+    p.tiles = (b.L + kWindowTile - 1) / kWindowTile;
+    p.sink_tiles = (b.S + kWindowTile - 1) / kWindowTile;
+    p.segs = 1;
+    if (p.sink_tiles > 0) {
+        // segments about as long as the other units, but no more than a few for every SM of any GPU in all
+        const long long near = ((long long)b.W + kWindowTile - 1) / kWindowTile + 1, unit = b.causal ? near : 2 * near - 1;
+        const long long most = 640 / ((long long)B * Hkv * p.sink_tiles);
+        long long segs = (p.tiles + unit - 1) / unit;
+        if (segs > most) segs = most;
+        p.segs = segs < 1 ? 1 : (int)segs;
+        p.sink_items = (long long)B * Hkv * p.sink_tiles * p.segs;
+    }
+    const size_t rows = (size_t)B * H * p.tiles * kWindowTile;
+    p.lse_at = 0;
+    p.D_at = p.lse_at + up256(rows * sizeof(float));
+    p.dq_at = p.D_at + up256(rows * sizeof(float));
+    p.part_at = p.dq_at + up256(rows * d * sizeof(float));
+    p.bytes = p.part_at + (p.segs > 1 ? up256((size_t)p.sink_items * 2 * kWindowTile * d * sizeof(float)) : 0);
+    return p;
+}
+
+cudaError_t launch_window_bwd_before(const WindowArgs& a, const WindowBwdPlan& p, int d, cudaStream_t s)
+{
+    const int padded = p.tiles * kWindowTile;
+    const long long rows = (long long)a.B * a.H * padded;
+    if (d == 128)
+        before_kernel<128><<<blocks(rows, d), kThreads, 0, s>>>(a.store_geo, a.geo, a.out, a.saved_dtype == 1, a.dout, a.lse, p.lse2, p.D, p.dq, padded, rows);
+    else
+        before_kernel<64><<<blocks(rows, d), kThreads, 0, s>>>(a.store_geo, a.geo, a.out, a.saved_dtype == 1, a.dout, a.lse, p.lse2, p.D, p.dq, padded, rows);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_window_bwd_after(const WindowArgs& a, const WindowBwdPlan& p, int d, cudaStream_t s)
+{
+    const long long rows = (long long)a.B * a.H * a.band.L;
+    const bool bf16 = a.grad_dtype == 1;
+    const int padded = p.tiles * kWindowTile;
+    if (d == 128)
+        dq_kernel<128><<<blocks(rows, d), kThreads, 0, s>>>(a.store_geo, p.dq, a.dq, bf16, rows, padded);
+    else
+        dq_kernel<64><<<blocks(rows, d), kThreads, 0, s>>>(a.store_geo, p.dq, a.dq, bf16, rows, padded);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || p.segs == 1) return e;
+    const long long sinks = (long long)a.B * a.Hkv * p.sink_tiles * 2 * kWindowTile;
+    if (d == 128)
+        sinks_kernel<128><<<blocks(sinks, d), kThreads, 0, s>>>(a.store_geo, a.band, p.part, a.dk, a.dv, bf16, p.sink_tiles, p.segs, sinks);
+    else
+        sinks_kernel<64><<<blocks(sinks, d), kThreads, 0, s>>>(a.store_geo, a.band, p.part, a.dk, a.dv, bf16, p.sink_tiles, p.segs, sinks);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_window_gather(const Geometry& g, const void* src, void* dst, long long heads, int d, cudaStream_t s)
+{
+    const long long rows = heads * g.L;
+    if (d == 128)
+        gather_kernel<128><<<blocks(rows, d), kThreads, 0, s>>>(g, static_cast<const uint4*>(src), static_cast<uint4*>(dst), rows);
+    else
+        gather_kernel<64><<<blocks(rows, d), kThreads, 0, s>>>(g, static_cast<const uint4*>(src), static_cast<uint4*>(dst), rows);
+    return cudaGetLastError();
+}
+
+}  // namespace ra

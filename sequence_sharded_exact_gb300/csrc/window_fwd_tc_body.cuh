@@ -66,7 +66,7 @@ constexpr uint32_t kColS0 = 0, kColO0 = 256;
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 
 struct FwdArgs {
-    Geometry geo;
+    Geometry geo, store_geo;  // of the loads; of out and lse
     Band band;
     int H, Hkv, G;
     int pair;         // 1: a unit is two heads at 128 positions; 0: 256 positions of one head
@@ -229,7 +229,7 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, uint32_t sbase, u
         __syncwarp();
         const float inv = 1.0f / (l_run + c_run);
         const bool row = p < a.band.L;
-        const long long row_g = (long long)(w ? u.zq1 : u.zq) * a.band.L + (row ? buffer_row(a.geo, p) : 0);
+        const long long row_g = (long long)(w ? u.zq1 : u.zq) * a.band.L + (row ? buffer_row(a.store_geo, p) : 0);
         const bool poison = *reinterpret_cast<volatile int*>(smem + kSmemPoison + (ucount & 7) * 4) == (int)ucount + 1;
 #pragma unroll 1
         for (int c = 0; c < kHd; c += 32) {
@@ -539,6 +539,7 @@ cudaError_t RA_WIN_FWD_LAUNCH(const WindowArgs& w, unsigned int* status, cudaStr
         return cudaErrorInvalidValue;
     FwdArgs a;
     a.geo = w.geo;
+    a.store_geo = w.store_geo;
     a.band = w.band;
     a.H = w.H;
     a.Hkv = w.Hkv;

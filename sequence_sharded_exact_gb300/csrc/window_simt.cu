@@ -1,4 +1,4 @@
-// window_simt.cu -- attention through a window (window.cuh) on the CUDA cores: any dtype, layout and length.
+// window_simt.cu -- attention through a window (window.cuh) on the CUDA cores: float32, any layout and length.
 //
 // A block of 256 threads takes 64 consecutive positions of one head (queries, or keys in the dK/dV kernel) and walks the
 // tiles of 64 that they meet.  Every operand lies transposed in shared memory, [d][64], as float32: the products over the
@@ -18,19 +18,10 @@ namespace {
 
 constexpr int kT = 64, kStride = kT + 4, kThreads = 256;
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-
 __device__ __forceinline__ void load4(const float* p, float (&f)[4])
 {
     const float4 v = *reinterpret_cast<const float4*>(p);
     f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&f)[4])
-{
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xffff0000u);
 }
 __device__ __forceinline__ void store1(void* p, long long i, float v, int dtype)
 {
@@ -41,11 +32,11 @@ __device__ __forceinline__ void store1(void* p, long long i, float v, int dtype)
 }
 
 // 64 positions from p0 of one head's rows, transposed to [D][kStride]; positions past the sequence are zeros.
-template <typename T, int D>
-__device__ __forceinline__ void load_tile(const Geometry& g, const T* head, int p0, float* dst, float scale = 1.f)
+template <int D>
+__device__ __forceinline__ void load_tile(const Geometry& g, const float* head, int p0, float* dst, float scale = 1.f)
 {
     const int row = threadIdx.x % kT, p = p0 + row;
-    const T* src = p < g.L ? head + (long long)buffer_row(g, p) * D : nullptr;
+    const float* src = p < g.L ? head + (long long)buffer_row(g, p) * D : nullptr;
 #pragma unroll 4
     for (int c = threadIdx.x / kT * 4; c < D; c += kThreads / kT * 4) {
         float f[4] = {0.f, 0.f, 0.f, 0.f};
@@ -128,7 +119,7 @@ __device__ __forceinline__ float sum16(float v)
     return v;
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(const WindowArgs a)
 {
     extern __shared__ __align__(16) float sm[];
@@ -137,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(const WindowA
     const int q0 = (int)(blockIdx.x % tiles) * kT, zq = (int)(blockIdx.x / tiles), zk = zq / a.G;  // (b H + h) / G = b Hkv + g
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const long long per = (long long)a.band.L * D;
-    load_tile<T, D>(a.geo, static_cast<const T*>(a.q) + zq * per, q0, sq, a.scale_log2);
+    load_tile<D>(a.geo, static_cast<const float*>(a.q) + zq * per, q0, sq, a.scale_log2);
     float m[4], l[4], o[4][D / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -150,8 +141,8 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(const WindowA
     for (int t = 0; t < run.count(); ++t) {
         const int k0 = run.at(t) * kT;
         __syncthreads();
-        load_tile<T, D>(a.geo, static_cast<const T*>(a.k) + zk * per, k0, sk);
-        load_tile<T, D>(a.geo, static_cast<const T*>(a.v) + zk * per, k0, sv);
+        load_tile<D>(a.geo, static_cast<const float*>(a.k) + zk * per, k0, sk);
+        load_tile<D>(a.geo, static_cast<const float*>(a.v) + zk * per, k0, sv);
         __syncthreads();
         float s[4][4] = {};
         dot_tile<D>(sq, sk, s);
@@ -189,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(const WindowA
         const long long row = (long long)zq * a.band.L + buffer_row(a.geo, p);
         const float inv = 1.f / l[i];
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) store1(a.o, row * D + tx + 16 * k, o[i][k] * inv, a.out_dtype);
+        for (int k = 0; k < D / 16; ++k) static_cast<float*>(a.o)[row * D + tx + 16 * k] = o[i][k] * inv;
         if (tx == 0) a.lse[row] = (m[i] + log2f(l[i])) * kLn2;
     }
 }
@@ -211,7 +202,7 @@ __device__ __forceinline__ void weights(const WindowArgs& a, int r0, int c0, con
         }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) window_bwd_dq_simt_kernel(const WindowArgs a)
 {
     extern __shared__ __align__(16) float sm[];
@@ -220,8 +211,8 @@ __global__ void __launch_bounds__(kThreads) window_bwd_dq_simt_kernel(const Wind
     const int q0 = (int)(blockIdx.x % tiles) * kT, zq = (int)(blockIdx.x / tiles), zk = zq / a.G;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const long long per = (long long)a.band.L * D;
-    load_tile<T, D>(a.geo, static_cast<const T*>(a.q) + zq * per, q0, sq, a.scale_log2);
-    load_tile<T, D>(a.geo, static_cast<const T*>(a.dout) + zq * per, q0, sd);
+    load_tile<D>(a.geo, static_cast<const float*>(a.q) + zq * per, q0, sq, a.scale_log2);
+    load_tile<D>(a.geo, static_cast<const float*>(a.dout) + zq * per, q0, sd);
     float lse2[4], Dv[4], acc[4][D / 16] = {};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -234,8 +225,8 @@ __global__ void __launch_bounds__(kThreads) window_bwd_dq_simt_kernel(const Wind
     for (int t = 0; t < run.count(); ++t) {
         const int k0 = run.at(t) * kT;
         __syncthreads();
-        load_tile<T, D>(a.geo, static_cast<const T*>(a.k) + zk * per, k0, sk);
-        load_tile<T, D>(a.geo, static_cast<const T*>(a.v) + zk * per, k0, sv);
+        load_tile<D>(a.geo, static_cast<const float*>(a.k) + zk * per, k0, sk);
+        load_tile<D>(a.geo, static_cast<const float*>(a.v) + zk * per, k0, sv);
         __syncthreads();
         float s[4][4] = {}, dp[4][4] = {};
         dot_tile<D>(sq, sk, s);
@@ -255,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) window_bwd_dq_simt_kernel(const Wind
     }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) window_bwd_dkv_simt_kernel(const WindowArgs a)
 {
     extern __shared__ __align__(16) float sm[];
@@ -264,8 +255,8 @@ __global__ void __launch_bounds__(kThreads) window_bwd_dkv_simt_kernel(const Win
     const int k0 = (int)(blockIdx.x % tiles) * kT, zk = (int)(blockIdx.x / tiles);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const long long per = (long long)a.band.L * D;
-    load_tile<T, D>(a.geo, static_cast<const T*>(a.k) + zk * per, k0, sk, a.scale_log2);
-    load_tile<T, D>(a.geo, static_cast<const T*>(a.v) + zk * per, k0, sv);
+    load_tile<D>(a.geo, static_cast<const float*>(a.k) + zk * per, k0, sk, a.scale_log2);
+    load_tile<D>(a.geo, static_cast<const float*>(a.v) + zk * per, k0, sv);
     float dk[4][D / 16] = {}, dv[4][D / 16] = {};
     const QueryRun run = query_tiles(a.band, k0, kT, kT);
     for (int h = 0; h < a.G; ++h) {
@@ -273,8 +264,8 @@ __global__ void __launch_bounds__(kThreads) window_bwd_dkv_simt_kernel(const Win
         for (int t = run.first; t < run.last; ++t) {
             const int q0 = t * kT;
             __syncthreads();
-            load_tile<T, D>(a.geo, static_cast<const T*>(a.q) + zq * per, q0, sq);
-            load_tile<T, D>(a.geo, static_cast<const T*>(a.dout) + zq * per, q0, sd);
+            load_tile<D>(a.geo, static_cast<const float*>(a.q) + zq * per, q0, sq);
+            load_tile<D>(a.geo, static_cast<const float*>(a.dout) + zq * per, q0, sd);
             float lse2[4], Dv[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -310,7 +301,7 @@ __global__ void __launch_bounds__(kThreads) window_bwd_dkv_simt_kernel(const Win
 }
 
 // D = dout . out per row, in natural order: a warp per row.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) window_rowdot_kernel(const WindowArgs a, float* Dv)
 {
     const long long rows = (long long)a.B * a.H * a.band.L;
@@ -319,9 +310,7 @@ __global__ void __launch_bounds__(kThreads) window_rowdot_kernel(const WindowArg
         const long long z = x / a.band.L, row = z * a.band.L + buffer_row(a.geo, (int)(x - z * a.band.L));
         float sum = 0.f;
         for (int c = lane; c < D; c += 32) {
-            const float o = a.saved_dtype == 1 ? to_f(static_cast<const __nv_bfloat16*>(a.out)[row * D + c])
-                                               : static_cast<const float*>(a.out)[row * D + c];
-            sum = fmaf(o, to_f(static_cast<const T*>(a.dout)[row * D + c]), sum);
+            sum = fmaf(static_cast<const float*>(a.out)[row * D + c], static_cast<const float*>(a.dout)[row * D + c], sum);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -348,53 +337,51 @@ cudaError_t allow(K kernel, size_t smem, std::mutex& mu, bool (&done)[64])
     return cudaSuccess;
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t fwd(const WindowArgs& a, cudaStream_t s)
 {
     static std::mutex mu;
     static bool done[64];
     constexpr size_t smem = 3 * tile_bytes(D) + kWeightBytes;
-    cudaError_t e = allow(window_fwd_simt_kernel<T, D>, smem, mu, done);
+    cudaError_t e = allow(window_fwd_simt_kernel<D>, smem, mu, done);
     if (e != cudaSuccess) return e;
     const long long blocks = (long long)a.B * a.H * ((a.band.L + kT - 1) / kT);
-    window_fwd_simt_kernel<T, D><<<(unsigned)blocks, kThreads, smem, s>>>(a);
+    window_fwd_simt_kernel<D><<<(unsigned)blocks, kThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t bwd(const WindowArgs& a, float* Dv, cudaStream_t s)
 {
     static std::mutex mu;
     static bool done_q[64], done_k[64];
     constexpr size_t smem_q = 4 * tile_bytes(D) + kWeightBytes, smem_k = 4 * tile_bytes(D) + 2 * kWeightBytes;
-    cudaError_t e = allow(window_bwd_dq_simt_kernel<T, D>, smem_q, mu, done_q);
-    if (e == cudaSuccess) e = allow(window_bwd_dkv_simt_kernel<T, D>, smem_k, mu, done_k);
+    cudaError_t e = allow(window_bwd_dq_simt_kernel<D>, smem_q, mu, done_q);
+    if (e == cudaSuccess) e = allow(window_bwd_dkv_simt_kernel<D>, smem_k, mu, done_k);
     if (e != cudaSuccess) return e;
     const long long rows = (long long)a.B * a.H * a.band.L, need = (rows + kThreads / 32 - 1) / (kThreads / 32);
     const long long most = (long long)device_sm_count() * 8;
-    window_rowdot_kernel<T, D><<<(unsigned)(need < most ? need : most), kThreads, 0, s>>>(a, Dv);
+    window_rowdot_kernel<D><<<(unsigned)(need < most ? need : most), kThreads, 0, s>>>(a, Dv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long long tiles = (a.band.L + kT - 1) / kT;
-    window_bwd_dq_simt_kernel<T, D><<<(unsigned)(a.B * (long long)a.H * tiles), kThreads, smem_q, s>>>(a);
+    window_bwd_dq_simt_kernel<D><<<(unsigned)(a.B * (long long)a.H * tiles), kThreads, smem_q, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    window_bwd_dkv_simt_kernel<T, D><<<(unsigned)(a.B * (long long)a.Hkv * tiles), kThreads, smem_k, s>>>(a);
+    window_bwd_dkv_simt_kernel<D><<<(unsigned)(a.B * (long long)a.Hkv * tiles), kThreads, smem_k, s>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_window_fwd_simt(const WindowArgs& a, int d, int dtype, cudaStream_t s)
+cudaError_t launch_window_fwd_simt(const WindowArgs& a, int d, cudaStream_t s)
 {
-    if (dtype == 1) return d == 128 ? fwd<__nv_bfloat16, 128>(a, s) : fwd<__nv_bfloat16, 64>(a, s);
-    return d == 128 ? fwd<float, 128>(a, s) : fwd<float, 64>(a, s);
+    return d == 128 ? fwd<128>(a, s) : fwd<64>(a, s);
 }
 
-cudaError_t launch_window_bwd_simt(const WindowArgs& args, float* D, int d, int dtype, cudaStream_t s)
+cudaError_t launch_window_bwd_simt(const WindowArgs& args, float* D, int d, cudaStream_t s)
 {
     WindowArgs a = args;
     a.D = D;
-    if (dtype == 1) return d == 128 ? bwd<__nv_bfloat16, 128>(a, D, s) : bwd<__nv_bfloat16, 64>(a, D, s);
-    return d == 128 ? bwd<float, 128>(a, D, s) : bwd<float, 64>(a, D, s);
+    return d == 128 ? bwd<128>(a, D, s) : bwd<64>(a, D, s);
 }
 
 }  // namespace ra

@@ -13,7 +13,7 @@
 
 namespace ra {
 
-constexpr int kWinTile = 128;  // positions of a tile
+constexpr int kWinTile = kWindowTile;  // positions of a tile
 
 // Can TMA read 128 consecutive positions of this layout with one box?  Contiguous: always; zigzag: chunks of whole tiles;
 // striped: a box of n shards by 128 / n rows, whose shard index runs fastest, is a run of positions.
