@@ -485,6 +485,8 @@ RA_API ra_status ring_attn_qk_rope_axes_bwd(const void* q, const long long* q_st
  * ring_attn_window_bwd -- the gradients of sum(out * dout), as ring_attn_bwd's: out (out_dtype) and lse from the forward,
  *   dout in dtype, dq, dk, dv in grad_dtype.  dk and dv do not vary from run to run, nor does dq with float32 inputs; with
  *   bf16 inputs dq is summed by float32 atomics, in an order that varies.
+ * What a row of the forward does not see has no part in its result, whatever it holds (NaN, infinities).  The backward takes
+ * finite inputs: what is not may reach the gradients of all positions within 127 of those that see it.
  */
 RA_API ra_status ring_attn_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse, void* workspace,
                                       size_t workspace_bytes, int B, int H, int Hkv, int L, int d, int n_shards, int window,
@@ -560,6 +562,24 @@ RA_API ra_status ring_attn_tree_fwd(const void* q, const void* k_cache, const vo
                                     int B, int H, int Hkv, int T, int d, int cap, int dtype, int cache_dtype,
                                     int out_dtype, void* stream);
 RA_API size_t ring_attn_tree_fwd_workspace_size(int B, int H, int Hkv, int T, int d, int cap, int dtype, int cache_dtype);
+
+/*
+ * ring_attn_tree_window_fwd -- ring_attn_tree_fwd through a sliding window, with a few first tokens that stay visible
+ * (sinks): token t of sequence b, at position p_t, sees the rows j of the prefix with p_t - j < window or j < sinks.  Only
+ * the part of the cache that some token sees is read.
+ *   window >= 1, sinks >= 0 (any values: past the cache they reach all of it).
+ *   With a mask it says which of the step's tokens t sees, whatever their distance, and positions, DEVICE int32 [B][T],
+ *   4-byte aligned, gives p_t (for a tree of drafted tokens lens[b] + t's depth; a value outside [lens[b], lens[b] + T) counts
+ *   as the nearer end).  Without positions p_t = lens[b] + t.  Without a mask t sees the step's tokens j <= t with t - j < window,
+ *   and positions have to be NULL.
+ *   The prefix is the whole one: parts of a cache that is sharded over devices do not fold together through a window.
+ *   Everything else as ring_attn_tree_fwd, its workspace and its accuracy among it.
+ */
+RA_API ra_status ring_attn_tree_window_fwd(const void* q, const void* k_cache, const void* v_cache, const void* k_exp,
+                                           const void* v_exp, const int* lens, const int* ntok, const unsigned char* mask,
+                                           int mask_batched, const int* positions, void* out, float* lse, void* workspace,
+                                           size_t workspace_bytes, int B, int H, int Hkv, int T, int d, int cap, int window,
+                                           int sinks, int dtype, int cache_dtype, int out_dtype, void* stream);
 
 /* Which kernel path ring_attn_fwd / ring_attn_bwd take for these arguments (RA_PATH_*), written
  * to *path (HOST pointer).  Same argument checks as the calls themselves; no CUDA call. */

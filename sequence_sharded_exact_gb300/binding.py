@@ -51,6 +51,7 @@ EXPORTS = (
     "ring_attn_cache_read", "ring_attn_tree_fwd", "ring_attn_tree_fwd_workspace_size",
     "ring_attn_window_fwd", "ring_attn_window_fwd_workspace_size", "ring_attn_window_bwd",
     "ring_attn_window_bwd_workspace_size", "ring_attn_qk_rope_axes", "ring_attn_qk_rope_axes_bwd",
+    "ring_attn_tree_window_fwd",
 )
 
 
@@ -154,6 +155,8 @@ def library():
         lib.ring_attn_tree_fwd.restype = ctypes.c_int
         lib.ring_attn_tree_fwd_workspace_size.argtypes = [I] * 8
         lib.ring_attn_tree_fwd_workspace_size.restype = SZ
+        lib.ring_attn_tree_window_fwd.argtypes = [P] * 8 + [I] + [P] * 4 + [SZ] + [I] * 11 + [P]
+        lib.ring_attn_tree_window_fwd.restype = ctypes.c_int
         lib.ring_attn_qk_rope_axes.argtypes = [P] * 8 + [I] * 6 + [P, I, I, D, D, P, P]
         lib.ring_attn_qk_rope_axes.restype = ctypes.c_int
         lib.ring_attn_qk_rope_axes_bwd.argtypes = [P] * 13 + [SZ] + [I] * 6 + [P, I, I, D, D, P, P]
@@ -195,7 +198,7 @@ def _load_calls(lib):
         loader.exec_module(module)
         module.bind(*(ctypes.cast(getattr(lib, "ring_attn_" + f), ctypes.c_void_p).value for f in (
             "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size", "cache_write", "cache_read", "tree_fwd",
-            "tree_fwd_workspace_size", "qk_rope_axes")))
+            "tree_fwd_workspace_size", "qk_rope_axes", "tree_window_fwd")))
     except (ImportError, OSError, AttributeError, TypeError, ValueError) as e:
         warnings.warn(f"the compiled calls in {path} do not load, calls go through Python: {e}", RuntimeWarning)
         return
@@ -1187,14 +1190,22 @@ def _tree_workspace(*sizes):
     return int(library().ring_attn_tree_fwd_workspace_size(*sizes))
 
 
-def tree_fwd(q, cache, lens, mask=None, ntok=None, out_dtype=None, out=None, lse=None, workspace=None, stream=None):
+def tree_fwd(q, cache, lens, mask=None, ntok=None, out_dtype=None, out=None, lse=None, workspace=None, stream=None, window=None,
+             sinks=0, positions=None):
     """ring_attn_tree_fwd: attention of T new tokens per sequence, q [B, H, T, d], over a cache that already holds
     their keys and values in the rows lens[b] + t (cache_write): token t of sequence b sees the prefix, rows
     [0, lens[b]), and the step's tokens j < ntok[b] with mask[b, t, j] ([B, T, T] or [T, T] bool; without a mask
     j <= t).  lens, ntok: int32 [B] on the device.  Returns (out [B, H, T, d] in out_dtype -- q's, or float32 --
-    and lse [B, H, T] float32); a row that sees nothing, and tokens t >= ntok[b], have 0 and -infinity."""
+    and lse [B, H, T] float32); a row that sees nothing, and tokens t >= ntok[b], have 0 and -infinity.
+    window, sinks (ring_attn_tree_window_fwd): of the prefix a token at position p sees the rows j > p - window and the
+    first `sinks` ones alone.  positions [B, T] int32: the tokens' positions where a mask says which of the step's tokens
+    they see (lens[b] + depth in a tree); without them, and without a mask, token t is at lens[b] + t, and without a mask
+    it sees the step's tokens j <= t with t - j < window."""
     if _calls is not None and stream is None:
-        done = _calls.tree_fwd(q, cache, lens, mask, ntok, out_dtype, out, lse, workspace)
+        if window is None and not sinks and positions is None:
+            done = _calls.tree_fwd(q, cache, lens, mask, ntok, out_dtype, out, lse, workspace)
+        else:
+            done = _calls.tree_window_fwd(q, cache, lens, mask, ntok, out_dtype, out, lse, workspace, window, sinks, positions)
         if done is not None:
             return done
     (B, H, T, d), kshape, code = _dims4(q, cache.k, "q and the cache's k")
@@ -1207,6 +1218,8 @@ def tree_fwd(q, cache, lens, mask=None, ntok=None, out_dtype=None, out=None, lse
         raise ValueError("out_dtype must be q's dtype or float32")
     if lens is None:
         raise ValueError("lens is required")
+    if window is None and (sinks or positions is not None):
+        raise ValueError("sinks and positions need a window")
     mp, batched = None, 0
     if mask is not None:
         batched = int(isinstance(mask, torch.Tensor) and mask.dim() == 3)
@@ -1221,7 +1234,13 @@ def tree_fwd(q, cache, lens, mask=None, ntok=None, out_dtype=None, out=None, lse
     else:
         _need_workspace(workspace, need, dev)
     _hand_over(stream, dev.index, (given[0], out), (given[1], lse), (given[2], workspace))
-    _run(dev.index, lib.ring_attn_tree_fwd, qp, *ptrs, _fits(lens, "lens", dev, (B,), torch.int32),
-         None if ntok is None else _fits(ntok, "ntok", dev, (B,), torch.int32), mp, batched, op, lp,
-         workspace.data_ptr(), workspace.numel(), B, H, Hkv, T, d, cap, code, kind, _DTYPES[out_dtype], _stream_ptr(stream, dev.index))
+    head = (qp, *ptrs, _fits(lens, "lens", dev, (B,), torch.int32),
+            None if ntok is None else _fits(ntok, "ntok", dev, (B,), torch.int32), mp, batched)
+    tail = (op, lp, workspace.data_ptr(), workspace.numel(), B, H, Hkv, T, d, cap)
+    types = (code, kind, _DTYPES[out_dtype], _stream_ptr(stream, dev.index))
+    if window is None:
+        _run(dev.index, lib.ring_attn_tree_fwd, *head, *tail, *types)
+    else:
+        pos = None if positions is None else _fits(positions, "positions", dev, (B, T), torch.int32)
+        _run(dev.index, lib.ring_attn_tree_window_fwd, *head, pos, *tail, _whole(window, "window"), _whole(sinks, "sinks"), *types)
     return out, lse

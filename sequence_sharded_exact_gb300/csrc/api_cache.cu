@@ -129,6 +129,26 @@ ra_status check_tree(const Cache& c, int H, int T)
     return RA_OK;
 }
 
+ra_status tree_impl(const Cache& c, Tree t, size_t workspace_bytes, void* stream, const char* what)
+{
+    ra_status st = check_cache(c, t.dtype);
+    if (st != RA_OK) return st;
+    if ((st = check_tree(c, t.H, t.T)) != RA_OK) return st;
+    if (t.out_dtype != t.dtype && t.out_dtype != RA_F32) return fail(RA_ERR_INVALID_ARG, "out_dtype must be the dtype of q or RA_F32");
+    if ((st = check_ptrs({t.q, t.out, t.lse})) != RA_OK) return st;
+    if ((st = check_ints("lens", t.lens, false)) != RA_OK || (st = check_ints("ntok", t.ntok, true)) != RA_OK) return st;
+    if ((st = check_workspace(t.workspace, workspace_bytes,
+                              ring_attn_tree_fwd_workspace_size(c.B, t.H, c.Hkv, t.T, c.d, c.cap, t.dtype, c.dtype))) != RA_OK)
+        return st;
+    if ((st = check_device()) != RA_OK) return st;
+    cudaError_t e;
+    t.status = status_word(&e);
+    if (!t.status) return cuda_fail(e, "status word");
+    e = launch_tree(c, t, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    return RA_OK;
+}
+
 }  // namespace
 }  // namespace ra
 
@@ -286,23 +306,24 @@ ra_status ring_attn_tree_fwd(const void* q, const void* k_cache, const void* v_c
                              int cache_dtype, int out_dtype, void* stream)
 {
     const Cache c = cache_of(k_cache, v_cache, k_exp, v_exp, B, Hkv, cap, d, cache_dtype);
-    ra_status st = check_cache(c, dtype);
+    return tree_impl(c, Tree{H, T, dtype, out_dtype, q, lens, ntok, mask, mask_batched ? 1 : 0, out, lse, workspace, nullptr, 0, 0, nullptr},
+                     workspace_bytes, stream, "ring_attn_tree_fwd launch");
+}
+
+ra_status ring_attn_tree_window_fwd(const void* q, const void* k_cache, const void* v_cache, const void* k_exp, const void* v_exp,
+                                    const int* lens, const int* ntok, const unsigned char* mask, int mask_batched,
+                                    const int* positions, void* out, float* lse, void* workspace, size_t workspace_bytes, int B, int H,
+                                    int Hkv, int T, int d, int cap, int window, int sinks, int dtype, int cache_dtype, int out_dtype,
+                                    void* stream)
+{
+    const Cache c = cache_of(k_cache, v_cache, k_exp, v_exp, B, Hkv, cap, d, cache_dtype);
+    if (window < 1) return fail(RA_ERR_INVALID_ARG, "window must be >= 1 (got %d)", window);
+    if (sinks < 0) return fail(RA_ERR_INVALID_ARG, "sinks must be >= 0 (got %d)", sinks);
+    if (positions && !mask) return fail(RA_ERR_INVALID_ARG, "positions need a mask: without one token t is at lens + t");
+    ra_status st = check_ints("positions", positions, true);
     if (st != RA_OK) return st;
-    if ((st = check_tree(c, H, T)) != RA_OK) return st;
-    if (out_dtype != dtype && out_dtype != RA_F32) return fail(RA_ERR_INVALID_ARG, "out_dtype must be the dtype of q or RA_F32");
-    if ((st = check_ptrs({q, out, lse})) != RA_OK) return st;
-    if ((st = check_ints("lens", lens, false)) != RA_OK || (st = check_ints("ntok", ntok, true)) != RA_OK) return st;
-    if ((st = check_workspace(workspace, workspace_bytes,
-                              ring_attn_tree_fwd_workspace_size(B, H, Hkv, T, d, cap, dtype, cache_dtype))) != RA_OK)
-        return st;
-    if ((st = check_device()) != RA_OK) return st;
-    cudaError_t e;
-    unsigned int* sw = status_word(&e);
-    if (!sw) return cuda_fail(e, "status word");
-    const Tree t{H, T, dtype, out_dtype, q, lens, ntok, mask, mask_batched ? 1 : 0, out, lse, workspace, sw};
-    e = launch_tree(c, t, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail(e, "ring_attn_tree_fwd launch");
-    return RA_OK;
+    return tree_impl(c, Tree{H, T, dtype, out_dtype, q, lens, ntok, mask, mask_batched ? 1 : 0, out, lse, workspace, nullptr, window, sinks, positions},
+                     workspace_bytes, stream, "ring_attn_tree_window_fwd launch");
 }
 
 }  // extern "C"

@@ -27,6 +27,7 @@ decltype(&ring_attn_cache_read) read_cache = nullptr;
 decltype(&ring_attn_tree_fwd) tree = nullptr;
 decltype(&ring_attn_tree_fwd_workspace_size) tree_workspace = nullptr;
 decltype(&ring_attn_qk_rope_axes) rope_axes = nullptr;
+decltype(&ring_attn_tree_window_fwd) tree_window = nullptr;
 
 using at::ScalarType;
 using at::Tensor;
@@ -193,10 +194,10 @@ PyObject* answer(Py_ssize_t given, Py_ssize_t expected, F f)
     Py_RETURN_NONE;
 }
 
-// q, cache, lens, mask, ntok, out_dtype, out, lse, workspace
-PyObject* py_tree_fwd(PyObject*, PyObject* const* a, Py_ssize_t n)
+// q, cache, lens, mask, ntok, out_dtype, out, lse, workspace, and through a window: window, sinks, positions
+PyObject* attend(PyObject* const* a, Py_ssize_t n, Py_ssize_t expected)
 {
-    return answer(n, 9, [&]() -> PyObject* {
+    return answer(n, expected, [&]() -> PyObject* {
         const Tensor& q = tensor(a[0]);
         four(q);
         const Call c(q);
@@ -229,11 +230,21 @@ PyObject* py_tree_fwd(PyObject*, PyObject* const* a, Py_ssize_t n)
         if (need == 0) throw Misfit{};
         Tensor out = c.output(a[6], {B, H, T, d}, odt), lse = c.output(a[7], {B, H, T}, at::kFloat);
         const Tensor ws = c.workspace(a[8], (int64_t)need);
-        accept(tree(qp, cache.k, cache.v, cache.ke, cache.ve, lens, ntok, mask, batched, out.data_ptr(), static_cast<float*>(lse.data_ptr()),
-                    ws.data_ptr(), (size_t)ws.numel(), b, h, hk, t, dd, cache.cap, code, cache.code, code_of(odt), c.stream()));
+        if (expected == 9) {
+            accept(tree(qp, cache.k, cache.v, cache.ke, cache.ve, lens, ntok, mask, batched, out.data_ptr(), static_cast<float*>(lse.data_ptr()),
+                        ws.data_ptr(), (size_t)ws.numel(), b, h, hk, t, dd, cache.cap, code, cache.code, code_of(odt), c.stream()));
+        } else {
+            const auto* pos = static_cast<const int*>(c.optional(a[11], {B, T}, at::kInt));
+            accept(tree_window(qp, cache.k, cache.v, cache.ke, cache.ve, lens, ntok, mask, batched, pos, out.data_ptr(),
+                               static_cast<float*>(lse.data_ptr()), ws.data_ptr(), (size_t)ws.numel(), b, h, hk, t, dd, cache.cap,
+                               whole_number(a[9]), whole_number(a[10]), code, cache.code, code_of(odt), c.stream()));
+        }
         return pair_of(std::move(out), std::move(lse));
     });
 }
+
+PyObject* py_tree_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) { return attend(a, n, 9); }
+PyObject* py_tree_window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) { return attend(a, n, 12); }
 
 // cache, k, v, lens, ntok
 PyObject* py_cache_write(PyObject*, PyObject* const* a, Py_ssize_t n)
@@ -392,7 +403,7 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n)
     void** to[] = {reinterpret_cast<void**>(&norm_rope), reinterpret_cast<void**>(&norm_rope_bwd),
                    reinterpret_cast<void**>(&norm_rope_bwd_workspace), reinterpret_cast<void**>(&write_cache),
                    reinterpret_cast<void**>(&read_cache), reinterpret_cast<void**>(&tree), reinterpret_cast<void**>(&tree_workspace),
-                   reinterpret_cast<void**>(&rope_axes)};
+                   reinterpret_cast<void**>(&rope_axes), reinterpret_cast<void**>(&tree_window)};
     if (n != (Py_ssize_t)(sizeof(to) / sizeof(to[0]))) {
         PyErr_SetString(PyExc_TypeError, "one address for each function");
         return nullptr;
@@ -411,6 +422,7 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL
 PyMethodDef methods[] = {{"bind", FAST(py_bind), nullptr},
                          {"tree_fwd", FAST(py_tree_fwd), nullptr},
+                         {"tree_window_fwd", FAST(py_tree_window_fwd), nullptr},
                          {"cache_write", FAST(py_cache_write), nullptr},
                          {"cache_read", FAST(py_cache_read), nullptr},
                          {"qk_norm_rope", FAST(py_norm_rope), nullptr},

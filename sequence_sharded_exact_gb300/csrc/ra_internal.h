@@ -134,6 +134,8 @@ struct Tree {
     float* lse;                 // [B][H][T]
     void* workspace;
     unsigned int* status;
+    int window, sinks;          // 0: no window
+    const int* positions;       // [B][T], through a window; may be null
 };
 size_t tree_workspace_size(const Cache& c, int H, int T, int dtype);
 cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s);

@@ -23,6 +23,11 @@
 // slot 1 otherwise, and a second launch joins the partials in CTA order: the result does not vary
 // from run to run.  That launch takes the items that go over a border between CTAs from a list that
 // the first one leaves, whatever the batch, and also writes the rows of sequences that have no tokens.
+//
+// Through a window (kWin): token t, at position p_t in [len, len + T), sees the prefix's rows j < sinks and those with
+// p_t - j < window.  The rows between the sinks and the first one that a token's window reaches are left out of the list,
+// by whole tiles: list tile x is the cache's tile x among the sinks', and gap tiles further on behind them.  Rows that some
+// tokens see and others do not are treated as drafted tokens' are.
 #pragma once
 
 #include <math.h>
@@ -54,11 +59,27 @@ struct TreeArgs {
                      // head * nrt + row tile, its last CTA, its slot here + 2 * its sequence's drafted tokens
     unsigned int* status;
     float scale_log2;  // log2(e) / sqrt(d)
+    int window, sinks; // kWin
+    const int* pos;    // kWin: [B][T] positions of the tokens, or null: lens + t
 };
 
 struct TreeSeq {
     int len, cnt, end;  // prefix rows, drafted tokens, rows in all (0: no queries)
     bool bad;           // a length outside its range was clamped
+};
+// Through a window: the prefix's rows [lo, len) are in reach, those of [all, len) and [0, sinks) seen by every token; of the
+// list's tiles the first `front` are the cache's, the others lie `gap` tiles further on.
+struct TreeWinSeq : TreeSeq {
+    int lo, all, sinks, front, gap;
+};
+
+template <bool kWin>
+struct TreeSeqOf {
+    using type = TreeSeq;
+};
+template <>
+struct TreeSeqOf<true> {
+    using type = TreeWinSeq;
 };
 
 __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b)
@@ -73,6 +94,60 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b)
     return s;
 }
 
+template <bool kWin>
+__device__ __forceinline__ typename TreeSeqOf<kWin>::type tree_sequence(const TreeArgs& a, int b)
+{
+    if constexpr (!kWin) {
+        return tree_seq(a, b);
+    } else {
+        TreeWinSeq s;
+        static_cast<TreeSeq&>(s) = tree_seq(a, b);
+        s.lo = s.len - a.window + 1 > 0 ? s.len - a.window + 1 : 0;
+        s.all = s.len + a.T - a.window > 0 ? s.len + a.T - a.window : 0;
+        s.sinks = a.sinks < s.len ? a.sinks : s.len;
+        s.front = (s.sinks + a.tile - 1) / a.tile;
+        s.gap = s.lo / a.tile > s.front ? s.lo / a.tile - s.front : 0;
+        return s;
+    }
+}
+
+// Row of the cache that row x of the list is.
+__device__ __forceinline__ int tree_row(const TreeSeq&, int x, int) { return x; }
+__device__ __forceinline__ int tree_row(const TreeWinSeq& s, int x, int tile) { return x >= s.front * tile ? x + s.gap * tile : x; }
+__device__ __forceinline__ int tree_list_row(const TreeSeq&, int key, int) { return key; }  // and back
+__device__ __forceinline__ int tree_list_row(const TreeWinSeq& s, int key, int tile) { return key >= s.front * tile ? key - s.gap * tile : key; }
+__device__ __forceinline__ int tree_sinks(const TreeSeq&) { return 0; }
+__device__ __forceinline__ int tree_sinks(const TreeWinSeq& s) { return s.sinks; }
+// The sequence's end in the list.
+__device__ __forceinline__ int tree_list_end(const TreeSeq& s, int) { return s.end; }
+__device__ __forceinline__ int tree_list_end(const TreeWinSeq& s, int tile) { return s.end ? s.end - s.gap * tile : 0; }
+// Rows that no query sees, and rows that some may not see (the former among them).
+__device__ __forceinline__ bool tree_dead(const TreeSeq& s, int key) { return key >= s.end; }
+__device__ __forceinline__ bool tree_dead(const TreeWinSeq& s, int key) { return key >= s.end || (key >= s.sinks && key < s.lo); }
+__device__ __forceinline__ bool tree_partly(const TreeSeq& s, int key) { return key >= s.len; }
+__device__ __forceinline__ bool tree_partly(const TreeWinSeq& s, int key) { return key >= s.len || (key >= s.sinks && key < s.all); }
+// The first of those that some may not see and some see.
+__device__ __forceinline__ int tree_first_partly(const TreeSeq& s) { return s.len; }
+__device__ __forceinline__ int tree_first_partly(const TreeWinSeq& s) { return s.lo < s.sinks ? s.sinks : s.lo; }
+// Does one of the rows [k0, k0 + n) belong to them?
+__device__ __forceinline__ bool tree_masked(const TreeSeq& s, int k0, int n) { return k0 + n > s.len; }
+__device__ __forceinline__ bool tree_masked(const TreeWinSeq& s, int k0, int n) { return k0 + n > s.len || (k0 < s.all && k0 + n > s.sinks); }
+
+// First row of the prefix in the window of token t of sequence b (below 0: all are).
+__device__ __forceinline__ int tree_reach(const TreeArgs& a, const TreeSeq& s, int b, int t)
+{
+    int p = s.len + t;
+    if (a.pos) {
+        p = a.pos[(long long)b * a.T + t];
+        p = p < s.len ? s.len : (p > s.len + a.T - 1 ? s.len + a.T - 1 : p);
+    }
+    return p - a.window + 1;
+}
+
+__device__ __forceinline__ int tree_tiles(const TreeArgs& a, const TreeWinSeq& s)
+{
+    return s.end ? (s.end + a.tile - 1) / a.tile - s.gap : 0;
+}
 __device__ __forceinline__ int tree_tiles(const TreeArgs& a, const TreeSeq& s)
 {
     return a.tile == kTreeTile ? (s.end + kTreeTile - 1) / kTreeTile : (s.end + kTreeSimtTile - 1) / kTreeSimtTile;
@@ -92,12 +167,13 @@ __device__ __forceinline__ int tree_owner(const TreeArgs& a, long long total, lo
 }
 
 // A CTA's walk over its items: (b, kv head g, row tile r) and the tiles [t0, t1) of it.
-struct TreeWalk {
+template <bool kWin>
+struct TreeWalkOf {
     long long left;  // tiles still to do, the current item's included
     long long total; // of all CTAs
     int b, g, r, t0, t1, nt;
     bool first;
-    TreeSeq s;
+    typename TreeSeqOf<kWin>::type s;
 
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
     // Starts here and goes on in the next CTA.
@@ -130,10 +206,10 @@ struct TreeWalk {
     __device__ __forceinline__ int lengths(const TreeArgs& a)
     {
         const int lane = threadIdx.x & 31;
-        const int mine = lane < a.B ? tree_tiles(a, tree_seq(a, lane)) : 0;
+        const int mine = lane < a.B ? tree_tiles(a, tree_sequence<kWin>(a, lane)) : 0;
         long long all = 0;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
-            int n = b0 == 0 ? mine : b0 + lane < a.B ? tree_tiles(a, tree_seq(a, b0 + lane)) : 0;
+            int n = b0 == 0 ? mine : b0 + lane < a.B ? tree_tiles(a, tree_sequence<kWin>(a, b0 + lane)) : 0;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
             all += n;
@@ -147,7 +223,7 @@ struct TreeWalk {
         const int lane = threadIdx.x & 31;
         const long long items = (long long)a.Hkv * a.nrt;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
-            const long long mine = (b0 == 0 ? mine32 : b0 + lane < a.B ? tree_tiles(a, tree_seq(a, b0 + lane)) : 0) * items;
+            const long long mine = (b0 == 0 ? mine32 : b0 + lane < a.B ? tree_tiles(a, tree_sequence<kWin>(a, b0 + lane)) : 0) * items;
             long long upto = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -163,7 +239,7 @@ struct TreeWalk {
             }
             at -= __shfl_sync(0xffffffffu, upto, 31);
         }
-        s = tree_seq(a, b);
+        s = tree_sequence<kWin>(a, b);
         nt = tree_tiles(a, s);
         const int item = (int)(at / nt);
         t0 = (int)(at % nt);
@@ -181,7 +257,7 @@ struct TreeWalk {
             if (++g == a.Hkv) {
                 g = 0;
                 do {
-                    s = tree_seq(a, ++b);
+                    s = tree_sequence<kWin>(a, ++b);
                     nt = tree_tiles(a, s);
                 } while (nt == 0);  // `left` says that a later sequence has tiles
             }
@@ -190,11 +266,13 @@ struct TreeWalk {
         return true;
     }
 };
+using TreeWalk = TreeWalkOf<false>;
 
 // Does query token t see drafted token j (both < cnt)?
+template <bool kWin = false>
 __device__ __forceinline__ bool tree_sees(const TreeArgs& a, int b, int t, int j)
 {
-    if (!a.mask) return j <= t;
+    if (!a.mask) return j <= t && (!kWin || t - j < a.window);
     return a.mask[((a.mask_batched ? (long long)b * a.T : 0) + t) * a.T + j] != 0;
 }
 
@@ -229,5 +307,7 @@ cudaError_t launch_tree_mma_bf16(const TreeArgs& a, int d, cudaStream_t s);
 // Tensor-core path: bf16 queries, bf16 or e4m3 cache (tree_tc_body.cuh).
 cudaError_t launch_tree_tc_d128(const TreeArgs& a, bool e4m3, cudaStream_t s);
 cudaError_t launch_tree_tc_d64(const TreeArgs& a, bool e4m3, cudaStream_t s);
+cudaError_t launch_tree_window_tc_d128(const TreeArgs& a, bool e4m3, cudaStream_t s);
+cudaError_t launch_tree_window_tc_d64(const TreeArgs& a, bool e4m3, cudaStream_t s);
 
 }  // namespace ra

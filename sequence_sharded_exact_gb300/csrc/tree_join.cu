@@ -246,6 +246,14 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
     a.lse = t.lse;
     a.status = t.status;
     a.scale_log2 = kLog2e / sqrtf((float)c.d);
+    a.window = t.window;
+    a.sinks = t.sinks;
+    a.pos = t.positions;
+    if (a.window) {  // no more CTAs than tiles that can be in reach
+        const long long reach = (long long)t.window + t.T, sinks = t.sinks < c.cap ? t.sinks : c.cap;
+        const long long most = (long long)c.B * c.Hkv * u.nrt * (reach / u.tile + 2 + (sinks + u.tile - 1) / u.tile);
+        if (a.ctas > most) a.ctas = (int)most;
+    }
     char* ws = static_cast<char*>(t.workspace);
     a.border = reinterpret_cast<int4*>(ws);
     a.part_ml = reinterpret_cast<float*>(ws + border_bytes(u));
@@ -254,7 +262,8 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
     if (u.path == Path::kMma)
         e = e4m3 ? launch_tree_mma(a, c.d, many ? 4 : 8, s) : launch_tree_mma_bf16(a, c.d, s);
     else if (u.path == Path::kTc)
-        e = c.d == 128 ? launch_tree_tc_d128(a, e4m3, s) : launch_tree_tc_d64(a, e4m3, s);
+        e = a.window ? (c.d == 128 ? launch_tree_window_tc_d128(a, e4m3, s) : launch_tree_window_tc_d64(a, e4m3, s))
+            : c.d == 128 ? launch_tree_tc_d128(a, e4m3, s) : launch_tree_tc_d64(a, e4m3, s);
     else
         e = launch_tree_simt(a, c.d, c.dtype, s);
     return e != cudaSuccess ? e : launch_tree_join(a, c.d, s);

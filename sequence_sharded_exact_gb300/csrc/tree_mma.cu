@@ -124,7 +124,7 @@ __device__ __forceinline__ float convert_query(const TreeArgs& a, uint32_t (&f)[
     return finite ? pow2(e) * a.scale_log2 : __uint_as_float(0x7fc00000u);
 }
 
-template <int D, int kWarps, int N>
+template <int D, int kWarps, int N, bool kWin>
 __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_mma_kernel(const __grid_constant__ Maps maps, const TreeArgs a)
 {
     using C = Cfg<D, kWarps, N>;
@@ -141,7 +141,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
         fence_barrier_init();
     }
     __syncthreads();
-    TreeWalk w;
+    using Walk = TreeWalkOf<kWin>;
+    Walk w;
     if (!w.begin(a, blockIdx.x)) {  // the same for every warp
         if (threadIdx.x == 0) a.border[blockIdx.x] = make_int4(-1, 0, 0, 0);
         return;
@@ -154,28 +155,29 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
     uint32_t bytes = 0, coming[4], qr[N][D / 8], item = 0;
     // An item's first rows, scales and queries set out.
     constexpr int kStep = kWarps * kKeys;  // the warp's 16-row groups of an item: from group_row on, every kWarps-th
-    auto group_row = [&](const TreeWalk& w) { return w.t0 * kTreeTile + warp * kKeys; };
-    auto groups = [&](const TreeWalk& w) {
-        const int end = w.t1 * kTreeTile < w.s.end ? w.t1 * kTreeTile : w.s.end, all = (end - w.t0 * kTreeTile + kKeys - 1) / kKeys;
+    auto group_row = [&](const Walk& w) { return w.t0 * kTreeTile + warp * kKeys; };
+    auto groups = [&](const Walk& w) {
+        const int last = tree_list_end(w.s, kTreeTile), end = w.t1 * kTreeTile < last ? w.t1 * kTreeTile : last, all = (end - w.t0 * kTreeTile + kKeys - 1) / kKeys;
         return all > warp ? (all - warp + kWarps - 1) / kWarps : 0;
     };
-    auto send = [&](const TreeWalk& w, int i) {  // rows of the warp's i-th group
+    auto send = [&](const Walk& w, int i) {  // rows of the warp's i-th group
         if (lane == 0 && !*abort_flag) {
             const uint32_t slot = sent % kStages, bar = bars + 8u * slot, dst = sbase + ring_at + slot * 2 * C::kHalf;
             mbar_arrive_expect_tx(bar, 2 * C::kHalf);
-            tma_load_3d(dst, &maps.k, bar, 0, group_row(w) + i * kStep, w.b * a.Hkv + w.g);
-            tma_load_3d(dst + C::kHalf, &maps.v, bar, 0, group_row(w) + i * kStep, w.b * a.Hkv + w.g);
+            const int row = tree_row(w.s, group_row(w) + i * kStep, kTreeTile);
+            tma_load_3d(dst, &maps.k, bar, 0, row, w.b * a.Hkv + w.g);
+            tma_load_3d(dst + C::kHalf, &maps.v, bar, 0, row, w.b * a.Hkv + w.g);
             ++sent;
         }
     };
     // lane's key's scale byte of group i: K's of key lane, V's of key lane - 16; four groups' in use, four on their
     // way (a register that is moved on is waited for)
-    auto scale_byte = [&](const TreeWalk& w, int i) {
-        const int row = group_row(w) + i * kStep + (lane & 15);
+    auto scale_byte = [&](const Walk& w, int i) {
+        const int row = tree_row(w.s, group_row(w) + i * kStep, kTreeTile) + (lane & 15);
         const uint8_t* exps = (lane < kKeys ? a.k_exp : a.v_exp) + ((long long)w.b * a.Hkv + w.g) * a.cap;
-        return i < groups(w) && row < w.s.end ? (uint32_t)exps[row] : (uint32_t)kHuge - 1;  // (of no row: never far below)
+        return i < groups(w) && !tree_dead(w.s, row) ? (uint32_t)exps[row] : (uint32_t)kHuge - 1;  // (of no row: never far below)
     };
-    auto set_out = [&](const TreeWalk& w) {
+    auto set_out = [&](const Walk& w) {
         for (int i = 0; i < kStages && i < groups(w); ++i) send(w, i);
 #pragma unroll
         for (int e = 0; e < 4; ++e) coming[e] = scale_byte(w, e);
@@ -192,6 +194,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
         float top[N][2];                                    // M
         int low = 0;                                        // V's scale bytes below this are far from M's
         uint32_t live = 0;                                  // bit 2 c + u
+        int reach[N][2];
 #pragma unroll
         for (int c = 0; c < N; ++c) {
             const float scale = convert_query<D>(a, qr[c]);
@@ -203,6 +206,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
                 l[c][u] = 0.f;
                 top[c][u] = -INFINITY;
                 if (x < a.R && x % a.T < w.s.cnt) live |= 1u << (2 * c + u);
+                if constexpr (kWin) reach[c][u] = x < a.R && x % a.T < w.s.cnt ? tree_reach(a, w.s, w.b, x % a.T) : 0;
             }
 #pragma unroll
             for (int j = 0; j < kTiles; ++j)
@@ -210,8 +214,10 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
                 for (int e = 0; e < 4; ++e) o[c][j][e] = 0.f;
         }
         auto sees = [&](int c, int u, int key) {
+            if constexpr (kWin)
+                if (key < w.s.len) return key >= reach[c][u] || key < w.s.sinks;
             return key < w.s.len ||
-                   (key < w.s.end && (live >> (2 * c + u) & 1) && tree_sees(a, w.b, (8 * c + 2 * t4 + u) % a.T, key - w.s.len));
+                   (key < w.s.end && (live >> (2 * c + u) & 1) && tree_sees<kWin>(a, w.b, (8 * c + 2 * t4 + u) % a.T, key - w.s.len));
         };
 
 #pragma unroll 1
@@ -253,8 +259,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
                 }
             }
 
-            const int k0 = row0 + i * kStep;
-            const bool masked = k0 + kKeys > w.s.len;
+            const int k0 = tree_row(w.s, row0 + i * kStep, kTreeTile);
+            const bool masked = tree_masked(w.s, k0, kKeys);
             bool raise = false;
             float y[N][2][2];  // scores: [query][key]
 #pragma unroll
@@ -375,7 +381,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            if (k0 + 2 * t4 + (e & 1) + 8 * (e >> 1) >= w.s.end) vw[e][q] = 0;
+                            if (tree_dead(w.s, k0 + 2 * t4 + (e & 1) + 8 * (e >> 1))) vw[e][q] = 0;
                             odd |= (((vw[e][q] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;  // a byte of NaN
                         }
                     if (__any_sync(0xffffffffu, odd)) {
@@ -391,7 +397,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
 #pragma unroll 1
                         for (int r = 0; r < kKeys; ++r) {
                             const int er = (int)__shfl_sync(0xffffffffu, byte, r + 16);
-                            if (k0 + r >= w.s.end) continue;
+                            if (tree_dead(w.s, k0 + r)) continue;
 #pragma unroll
                             for (int c = 0; c < N; ++c) {
                                 const bool s0 = sees(c, 0, k0 + r), s1 = sees(c, 1, k0 + r);
@@ -528,8 +534,8 @@ bool make_map(CUtensorMap* map, const void* base, long long rows, long long head
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int kWarps, int N>
-cudaError_t launch(const TreeArgs& a, cudaStream_t s)
+template <int D, int kWarps, int N, bool kWin>
+cudaError_t launch_as(const TreeArgs& a, cudaStream_t s)
 {
     using C = Cfg<D, kWarps, N>;
     Maps maps;
@@ -537,10 +543,16 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t s)
     if (!make_map<D>(&maps.k, a.k, a.cap, heads) || !make_map<D>(&maps.v, a.v, a.cap, heads)) return cudaErrorInvalidValue;
     static std::mutex mu;
     static bool done[64];
-    const cudaError_t e = allow_smem(tree_mma_kernel<D, kWarps, N>, (int)C::kSmem, mu, done);
+    const cudaError_t e = allow_smem(tree_mma_kernel<D, kWarps, N, kWin>, (int)C::kSmem, mu, done);
     if (e != cudaSuccess) return e;
-    tree_mma_kernel<D, kWarps, N><<<a.ctas, 32 * kWarps, C::kSmem, s>>>(maps, a);
+    tree_mma_kernel<D, kWarps, N, kWin><<<a.ctas, 32 * kWarps, C::kSmem, s>>>(maps, a);
     return cudaGetLastError();
+}
+
+template <int D, int kWarps, int N>
+cudaError_t launch(const TreeArgs& a, cudaStream_t s)
+{
+    return a.window ? launch_as<D, kWarps, N, true>(a, s) : launch_as<D, kWarps, N, false>(a, s);
 }
 
 }  // namespace

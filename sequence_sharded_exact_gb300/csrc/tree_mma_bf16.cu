@@ -63,7 +63,7 @@ __device__ __forceinline__ uint32_t at16(int r, int c) { return (uint32_t)((c >>
 
 __device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7f80u) == 0x7f80u; }
 
-template <int D>
+template <int D, bool kWin>
 __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid_constant__ Maps maps, const TreeArgs a)
 {
     using C = Cfg<D>;
@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
         fence_barrier_init();
     }
     __syncthreads();
-    TreeWalk w;
+    using Walk = TreeWalkOf<kWin>;
+    Walk w;
     if (!w.begin(a, blockIdx.x)) {  // the same for every warp
         if (threadIdx.x == 0) a.border[blockIdx.x] = make_int4(-1, 0, 0, 0);
         return;
@@ -91,15 +92,15 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
     uint32_t used = 0, sent = 0;  // of the ring (sent: lane 0's)
     uint32_t qr[2 * kTiles], item = 0;
     // the warp's 16-row groups of an item: from group_row on, every kWarps-th
-    auto group_row = [&](const TreeWalk& w) { return w.t0 * kTreeTile + warp * kKeys; };
-    auto groups = [&](const TreeWalk& w) {
-        const int end = w.t1 * kTreeTile < w.s.end ? w.t1 * kTreeTile : w.s.end, all = (end - w.t0 * kTreeTile + kKeys - 1) / kKeys;
+    auto group_row = [&](const Walk& w) { return w.t0 * kTreeTile + warp * kKeys; };
+    auto groups = [&](const Walk& w) {
+        const int last = tree_list_end(w.s, kTreeTile), end = w.t1 * kTreeTile < last ? w.t1 * kTreeTile : last, all = (end - w.t0 * kTreeTile + kKeys - 1) / kKeys;
         return all > warp ? (all - warp + kWarps - 1) / kWarps : 0;
     };
-    auto send = [&](const TreeWalk& w, int i) {
+    auto send = [&](const Walk& w, int i) {
         if (lane == 0 && !*abort_flag) {
             const uint32_t slot = sent % kStages, bar = bars + 8u * slot, dst = sbase + ring_at + slot * 2 * C::kHalf;
-            const int row = group_row(w) + i * kWarps * kKeys, z = w.b * a.Hkv + w.g;
+            const int row = tree_row(w.s, group_row(w) + i * kWarps * kKeys, kTreeTile), z = w.b * a.Hkv + w.g;
             mbar_arrive_expect_tx(bar, 2 * C::kHalf);
             for (int h = 0; h < D / 64; ++h) {
                 tma_load_3d(dst + (uint32_t)h * 2048u, &maps.k, bar, h * 64, row, z);
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
         }
     };
     // An item's first rows, and its queries as the operand of S^T's k steps (columns 16 s + 2t, + 1, + 8, + 9 of row g).
-    auto set_out = [&](const TreeWalk& w) {
+    auto set_out = [&](const Walk& w) {
         for (int i = 0; i < kStages && i < groups(w); ++i) send(w, i);
         const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) +
                                                              (((long long)w.b * a.Hkv + w.g) * a.R + g8) * D) + t4;
@@ -129,19 +130,23 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
         const int row0 = group_row(w), n = groups(w);
         float o[kTiles][4], m[2], l[2];  // queries 2t + u
         bool live[2];
+        int reach[2] = {0, 0};
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int x = 2 * t4 + u;
             m[u] = -INFINITY;
             l[u] = 0.f;
             live[u] = x < a.R && x % a.T < w.s.cnt;
+            if constexpr (kWin) reach[u] = live[u] ? tree_reach(a, w.s, w.b, x % a.T) : 0;
         }
 #pragma unroll
         for (int j = 0; j < kTiles; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
         auto sees = [&](int u, int key) {
-            return key < w.s.len || (key < w.s.end && live[u] && tree_sees(a, w.b, (2 * t4 + u) % a.T, key - w.s.len));
+            if constexpr (kWin)
+                if (key < w.s.len) return key >= reach[u] || key < w.s.sinks;
+            return key < w.s.len || (key < w.s.end && live[u] && tree_sees<kWin>(a, w.b, (2 * t4 + u) % a.T, key - w.s.len));
         };
 
 #pragma unroll 1
@@ -156,8 +161,8 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
                 load_matrices(k, k_at + at16(kr, 2 * st + kc));
                 mma16(s, k, qr[2 * st], qr[2 * st + 1]);
             }
-            const int k0 = row0 + i * kWarps * kKeys;
-            const bool masked = k0 + kKeys > w.s.len;
+            const int k0 = tree_row(w.s, row0 + i * kWarps * kKeys, kTreeTile);
+            const bool masked = tree_masked(w.s, k0, kKeys);
             bool raise = false;
             float y[2][2];  // scores: [query][key]
 #pragma unroll
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
                 uint8_t* v = smem + ring_at + slot * 2 * C::kHalf + C::kHalf;
                 const int r = lane >> 1, key = k0 + r;
                 bool odd = false;
-                if (key >= w.s.len) {
+                if (tree_partly(w.s, key)) {
 #pragma unroll 1
                     for (int c = lane & 1; c < D / 8; c += 2) {
                         uint4* at = reinterpret_cast<uint4*>(v + at16(r, c));
@@ -218,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
                         uint32_t* px = &x.x;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            if (key >= w.s.end) {
+                            if (tree_dead(w.s, key)) {
                                 px[e] = 0;
                                 continue;
                             }
@@ -233,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
                     const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.v) + (((long long)w.b * a.Hkv + w.g) * a.cap + k0) * D + g8;
 #pragma unroll 1
                     for (int r = 0; r < kKeys; ++r) {
-                        if (k0 + r < w.s.len || k0 + r >= w.s.end) continue;
+                        if (!tree_partly(w.s, k0 + r) || tree_dead(w.s, k0 + r)) continue;
                         const bool s0 = sees(0, k0 + r), s1 = sees(1, k0 + r);
 #pragma unroll
                         for (int j = 0; j < 2 * kTiles; ++j) {
@@ -355,7 +360,7 @@ bool make_map(CUtensorMap* map, const void* base, long long rows, long long head
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool kWin>
 cudaError_t launch(const TreeArgs& a, cudaStream_t s)
 {
     using C = Cfg<D>;
@@ -364,9 +369,9 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t s)
     if (!make_map<D>(&maps.k, a.k, a.cap, heads) || !make_map<D>(&maps.v, a.v, a.cap, heads)) return cudaErrorInvalidValue;
     static std::mutex mu;
     static bool done[64];
-    const cudaError_t e = allow_smem(tree_mma_bf16_kernel<D>, (int)C::kSmem, mu, done);
+    const cudaError_t e = allow_smem(tree_mma_bf16_kernel<D, kWin>, (int)C::kSmem, mu, done);
     if (e != cudaSuccess) return e;
-    tree_mma_bf16_kernel<D><<<a.ctas, kThreads, C::kSmem, s>>>(maps, a);
+    tree_mma_bf16_kernel<D, kWin><<<a.ctas, kThreads, C::kSmem, s>>>(maps, a);
     return cudaGetLastError();
 }
 
@@ -374,7 +379,8 @@ cudaError_t launch(const TreeArgs& a, cudaStream_t s)
 
 cudaError_t launch_tree_mma_bf16(const TreeArgs& a, int d, cudaStream_t s)
 {
-    return d == 128 ? launch<128>(a, s) : launch<64>(a, s);
+    if (a.window) return d == 128 ? launch<128, true>(a, s) : launch<64, true>(a, s);
+    return d == 128 ? launch<128, false>(a, s) : launch<64, false>(a, s);
 }
 
 }  // namespace ra

@@ -89,7 +89,7 @@ struct Chunk {
     }
 };
 
-template <typename TC, int D, int ROWS>
+template <typename TC, int D, int ROWS, bool kWin>
 __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel(const TreeArgs a)
 {
     constexpr int RW = ROWS / 4;            // query rows per warp in the scores
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
     __shared__ float ml[ROWS][2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int col = tid % D, part = tid / D;
-    TreeWalk w;
+    TreeWalkOf<kWin> w;
     int4 border = make_int4(-1, 0, 0, 0);
     if (!w.begin(a, blockIdx.x)) {
         if (tid == 0) a.border[blockIdx.x] = border;
@@ -128,13 +128,14 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
         }
 #pragma unroll
         for (int i = 0; i < RC; ++i) acc[i] = 0.f;
-        const int end = w.t1 * kTreeSimtTile < w.s.end ? w.t1 * kTreeSimtTile : w.s.end;
+        const int last = tree_list_end(w.s, kTreeSimtTile), end = w.t1 * kTreeSimtTile < last ? w.t1 * kTreeSimtTile : last;
         Chunk<TC, D> next;
-        next.load(a, head * a.cap, w.t0 * kTreeSimtTile, end);
-        for (int k0 = w.t0 * kTreeSimtTile; k0 < end; k0 += kChunk) {
+        next.load(a, head * a.cap, tree_row(w.s, w.t0 * kTreeSimtTile, kTreeSimtTile), w.s.end);
+        for (int x0 = w.t0 * kTreeSimtTile; x0 < end; x0 += kChunk) {
+            const int k0 = tree_row(w.s, x0, kTreeSimtTile);
             __syncthreads();
             next.store(ks, vs);
-            if (k0 + kChunk < end) next.load(a, head * a.cap, k0 + kChunk, end);
+            if (x0 + kChunk < end) next.load(a, head * a.cap, tree_row(w.s, x0 + kChunk, kTreeSimtTile), w.s.end);
             __syncthreads();
             float sc[RW];
 #pragma unroll
@@ -152,12 +153,15 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
                 }
             }
             const int key = k0 + lane;
-            const bool drafted = k0 + kChunk > w.s.len;  // the chunk holds drafted tokens, or rows past the end
+            const bool drafted = tree_masked(w.s, k0, kChunk);  // the chunk holds rows that not every token sees
 #pragma unroll
             for (int i = 0; i < RW; ++i) {
                 const int x = w.r * a.rt + warp * RW + i, t = x % a.T;
-                bool sees = key < end;
-                if (drafted && key >= w.s.len && sees) sees = t < w.s.cnt && x < a.R && tree_sees(a, w.b, t, key - w.s.len);
+                bool sees = key < w.s.end;
+                if (drafted && key >= w.s.len && sees) sees = t < w.s.cnt && x < a.R && tree_sees<kWin>(a, w.b, t, key - w.s.len);
+                if constexpr (kWin)
+                    if (drafted && key < w.s.len && key >= w.s.sinks)
+                        sees = t < w.s.cnt && x < a.R && key >= tree_reach(a, w.s, w.b, t);
                 float mx = sees ? sc[i] : -INFINITY;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -228,14 +232,14 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
     if (tid == 0) a.border[blockIdx.x] = border;
 }
 
-template <typename TC, int D>
+template <typename TC, int D, bool kWin>
 cudaError_t launch_rows(const TreeArgs& a, cudaStream_t s)
 {
     switch (a.rt) {
-        case 4: tree_simt_kernel<TC, D, 4><<<a.ctas, kThreads, 0, s>>>(a); break;
-        case 8: tree_simt_kernel<TC, D, 8><<<a.ctas, kThreads, 0, s>>>(a); break;
-        case 12: tree_simt_kernel<TC, D, 12><<<a.ctas, kThreads, 0, s>>>(a); break;
-        default: tree_simt_kernel<TC, D, 16><<<a.ctas, kThreads, 0, s>>>(a);
+        case 4: tree_simt_kernel<TC, D, 4, kWin><<<a.ctas, kThreads, 0, s>>>(a); break;
+        case 8: tree_simt_kernel<TC, D, 8, kWin><<<a.ctas, kThreads, 0, s>>>(a); break;
+        case 12: tree_simt_kernel<TC, D, 12, kWin><<<a.ctas, kThreads, 0, s>>>(a); break;
+        default: tree_simt_kernel<TC, D, 16, kWin><<<a.ctas, kThreads, 0, s>>>(a);
     }
     return cudaGetLastError();
 }
@@ -243,7 +247,8 @@ cudaError_t launch_rows(const TreeArgs& a, cudaStream_t s)
 template <typename TC>
 cudaError_t launch_d(const TreeArgs& a, int d, cudaStream_t s)
 {
-    return d == 128 ? launch_rows<TC, 128>(a, s) : launch_rows<TC, 64>(a, s);
+    if (a.window) return d == 128 ? launch_rows<TC, 128, true>(a, s) : launch_rows<TC, 64, true>(a, s);
+    return d == 128 ? launch_rows<TC, 128, false>(a, s) : launch_rows<TC, 64, false>(a, s);
 }
 
 }  // namespace

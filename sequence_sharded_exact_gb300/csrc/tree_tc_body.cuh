@@ -1,6 +1,7 @@
 // tree_tc_body.cuh -- tensor-core path of the attention over a cache (tree.cuh) for bf16 queries and a bf16
 // or e4m3 cache, head dim RA_TREE_HD (128 or 64).  Compiled once per head dim (tree_tc.cu: 128,
-// tree_tc_d64.cu: 64); the including file names the host entry point through RA_TREE_LAUNCH.
+// tree_tc_d64.cu: 64), and again through a window (RA_TREE_WINDOW 1: tree_window_tc.cu, tree_window_tc_d64.cu); the
+// including file names the host entry point through RA_TREE_LAUNCH.
 //
 // One CTA per SM walks its items (tree.cuh): one kv head's tile of query rows against its cached rows, 128
 // at a time.  For query rows X and cached rows K, V of a tile:
@@ -65,6 +66,9 @@ namespace {
 
 constexpr int kHd = RA_TREE_HD;
 static_assert(kHd == 128 || kHd == 64, "head dim");
+constexpr bool kWin = RA_TREE_WINDOW;
+using Walk = TreeWalkOf<kWin>;
+using Seq = TreeSeqOf<kWin>::type;
 constexpr int kThreads = 512;
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;  // S_w at 128 w, O_w at 256 + 128 w
 constexpr long long kWaitLimit = 10000000000ll;
@@ -258,7 +262,7 @@ __device__ __forceinline__ void issue_pv(uint32_t lead, uint32_t v_addr, uint32_
 // loads
 // ------------------------------------------------------------------------------------------------
 template <bool kE4, int kNq>
-__device__ __forceinline__ void load_qk_role(const TreeArgs& a, uint32_t sbase, const Maps& maps, TreeWalk w, const WaitCtl& ctl)
+__device__ __forceinline__ void load_qk_role(const TreeArgs& a, uint32_t sbase, const Maps& maps, Walk w, const WaitCtl& ctl)
 {
     using C = Cfg<kE4, kNq>;
     auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
@@ -283,10 +287,10 @@ __device__ __forceinline__ void load_qk_role(const TreeArgs& a, uint32_t sbase, 
             mbar_arrive_expect_tx(bar(C::bKFull + slot), C::kBytesK);
             const uint32_t dst = sbase + C::kK + (uint32_t)slot * C::kBytesK;
             if constexpr (kE4) {
-                tma_load_3d(dst, &maps.k, bar(C::bKFull + slot), 0, t * kTreeTile, z);
+                tma_load_3d(dst, &maps.k, bar(C::bKFull + slot), 0, tree_row(w.s, t * kTreeTile, kTreeTile), z);
             } else {
                 for (int h = 0; h < kHd / 64; ++h)
-                    tma_load_3d(dst + (uint32_t)h * 16384u, &maps.k, bar(C::bKFull + slot), h * 64, t * kTreeTile, z);
+                    tma_load_3d(dst + (uint32_t)h * 16384u, &maps.k, bar(C::bKFull + slot), h * 64, tree_row(w.s, t * kTreeTile, kTreeTile), z);
             }
         }
     } while (ok && w.next(a));
@@ -296,7 +300,7 @@ __device__ __forceinline__ void load_qk_role(const TreeArgs& a, uint32_t sbase, 
 }
 
 template <bool kE4, int kNq>
-__device__ __forceinline__ void load_v_role(const TreeArgs& a, uint32_t sbase, const Maps& maps, TreeWalk w, const WaitCtl& ctl)
+__device__ __forceinline__ void load_v_role(const TreeArgs& a, uint32_t sbase, const Maps& maps, Walk w, const WaitCtl& ctl)
 {
     using C = Cfg<kE4, kNq>;
     auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
@@ -311,14 +315,14 @@ __device__ __forceinline__ void load_v_role(const TreeArgs& a, uint32_t sbase, c
             const uint32_t dst = sbase + C::kL + (uint32_t)slot * C::kBytesK;
             if constexpr (kE4) {
                 // rows are contiguous and V is not a product's operand here: one untiled copy, no row past the cache
-                const int rows = a.cap - t * kTreeTile < kTreeTile ? a.cap - t * kTreeTile : kTreeTile;
+                const int row0 = tree_row(w.s, t * kTreeTile, kTreeTile), rows = a.cap - row0 < kTreeTile ? a.cap - row0 : kTreeTile;
                 mbar_arrive_expect_tx(bar(C::bLFull + slot), (uint32_t)rows * kHd);
-                bulk_load_1d(dst, static_cast<const uint8_t*>(a.v) + ((long long)z * a.cap + (long long)t * kTreeTile) * kHd,
+                bulk_load_1d(dst, static_cast<const uint8_t*>(a.v) + ((long long)z * a.cap + row0) * kHd,
                              (uint32_t)rows * kHd, bar(C::bLFull + slot));
             } else {
                 mbar_arrive_expect_tx(bar(C::bLFull + slot), C::kBytesK);
                 for (int h = 0; h < kHd / 64; ++h)
-                    tma_load_3d(dst + (uint32_t)h * 16384u, &maps.v, bar(C::bLFull + slot), h * 64, t * kTreeTile, z);
+                    tma_load_3d(dst + (uint32_t)h * 16384u, &maps.v, bar(C::bLFull + slot), h * 64, tree_row(w.s, t * kTreeTile, kTreeTile), z);
             }
         }
     } while (ok && w.next(a));
@@ -328,7 +332,7 @@ __device__ __forceinline__ void load_v_role(const TreeArgs& a, uint32_t sbase, c
 
 // The scales of a tile's rows, 2^e as float32, k's then v's; four tiles' bytes are in flight at a time.
 template <int kNq>
-__device__ __forceinline__ void scale_role(const TreeArgs& a, uint32_t sbase, uint8_t* smem, TreeWalk w, const WaitCtl& ctl)
+__device__ __forceinline__ void scale_role(const TreeArgs& a, uint32_t sbase, uint8_t* smem, Walk w, const WaitCtl& ctl)
 {
     using C = Cfg<true, kNq>;
     auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
@@ -343,7 +347,7 @@ __device__ __forceinline__ void scale_role(const TreeArgs& a, uint32_t sbase, ui
             for (int u = 0; u < 4; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int row = (t + u) * kTreeTile + i * 32 + lane;
+                    const int row = tree_row(w.s, (t + u) * kTreeTile, kTreeTile) + i * 32 + lane;
                     raw[u][i] = 0;
                     if (u < n && row < w.s.end)
                         raw[u][i] = (uint32_t)a.k_exp[row0 + row] | (uint32_t)a.v_exp[row0 + row] << 8;
@@ -390,7 +394,7 @@ __device__ __forceinline__ bool clear_nonfinite(uint32_t& w)
 // bf16: only the tiles that reach past the prefix are touched, in place; the others are passed on (a warp that
 // skipped a tile's phase could take the slot's previous phase for the one it waits for).
 template <int kNq>
-__device__ __forceinline__ void prep_bf16_role(const TreeArgs& a, uint32_t sbase, uint8_t* smem, TreeWalk w, const WaitCtl& ctl)
+__device__ __forceinline__ void prep_bf16_role(const TreeArgs& a, uint32_t sbase, uint8_t* smem, Walk w, const WaitCtl& ctl)
 {
     using C = Cfg<false, kNq>;
     auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
@@ -400,14 +404,15 @@ __device__ __forceinline__ void prep_bf16_role(const TreeArgs& a, uint32_t sbase
         for (int t = w.t0; t < w.t1; ++t, ++vc) {
             const int slot = (int)(vc % C::kSlotsL);
             if (!warp_wait(bar(C::bLFull + slot), (vc / C::kSlotsL) & 1, ctl)) return;
-            if ((t + 1) * kTreeTile > w.s.len) {
+            const int k0 = tree_row(w.s, t * kTreeTile, kTreeTile);
+            if (tree_masked(w.s, k0, kTreeTile)) {
                 uint8_t* v = smem + C::kL + (uint32_t)slot * C::kBytesK;
-                const int key = t * kTreeTile + row;
-                if (key >= w.s.len) {
+                const int key = k0 + row;
+                if (tree_partly(w.s, key)) {
                     bool hit = false;
                     for (int c = 0; c < kHd / 8; ++c) {
                         uint4* p = reinterpret_cast<uint4*>(v + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-                        if (key >= w.s.end) {
+                        if (tree_dead(w.s, key)) {
                             *p = make_uint4(0, 0, 0, 0);
                             continue;
                         }
@@ -492,7 +497,7 @@ __device__ __forceinline__ void split_queries(const TreeArgs& a, uint8_t* smem, 
 }
 
 template <int kNq>
-__device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase, uint8_t* smem, TreeWalk w, const WaitCtl& ctl)
+__device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase, uint8_t* smem, Walk w, const WaitCtl& ctl)
 {
     using C = Cfg<true, kNq>;
     auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
@@ -512,8 +517,8 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
             const __nv_bfloat162 up = __float2bfloat162_rn(reinterpret_cast<const float*>(smem + C::kX + sx * 1024)[128 + row]);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::bXEmpty + sx));
-            const int key = t * kTreeTile + row;
-            const bool past = key >= w.s.end, drafted = key >= w.s.len;
+            const int k0 = tree_row(w.s, t * kTreeTile, kTreeTile), key = k0 + row;
+            const bool past = tree_dead(w.s, key), drafted = tree_partly(w.s, key);
             bool hit = false;
             // a thread has a row; starting each at another chunk keeps a warp's accesses in different banks
             auto at = [&](int i) { return (i + row) & (kHd / 16 - 1); };
@@ -533,7 +538,7 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
                 *reinterpret_cast<uint4*>(p + ((((2 * c) & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 *reinterpret_cast<uint4*>(p + ((((2 * c + 1) & 7) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
             };
-            if ((t + 1) * kTreeTile <= w.s.len) {  // no branch inside: the chunks' conversions overlap
+            if (!tree_masked(w.s, k0, kTreeTile)) {  // no branch inside: the chunks' conversions overlap
                 uint4 x0 = *reinterpret_cast<const uint4*>(src + row * kHd + at(0) * 16);
                 uint4 x1 = *reinterpret_cast<const uint4*>(src + row * kHd + at(1) * 16);
 #pragma unroll 1
@@ -586,7 +591,7 @@ __device__ __forceinline__ void prep_e4m3_role(const TreeArgs& a, uint32_t sbase
 // commit costs the issuing warp 50 to 180 cycles, so there are two per job: S is ready (which also says that P V
 // of job j - 2 is done, and that K has been read), and V has been read.
 template <bool kE4, int kNq, bool kExact>
-__device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint32_t tmem, TreeWalk w, const WaitCtl& ctl)
+__device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint32_t tmem, Walk w, const WaitCtl& ctl)
 {
     using C = Cfg<kE4, kNq>;
     auto bar = [&](int i) { return sbase + C::kBar + 8u * (uint32_t)i; };
@@ -636,15 +641,19 @@ __device__ __forceinline__ void mma_role(const TreeArgs& a, uint32_t sbase, uint
 // softmax warpgroups
 // ------------------------------------------------------------------------------------------------
 // Which of the 64 rows from k0 query token t sees, one bit each; for tiles that reach past the prefix.
-__device__ __forceinline__ unsigned long long seen_bits(const TreeArgs& a, const TreeSeq& s, int b, int t, int k0)
+// reach: the first row of the prefix in the token's window.
+__device__ __forceinline__ unsigned long long low_bits(int n) { return n >= 64 ? ~0ull : (n > 0 ? (1ull << n) - 1 : 0ull); }
+__device__ __forceinline__ unsigned long long seen_bits(const TreeArgs& a, const Seq& s, int b, int t, int k0, int reach)
 {
     const int p = s.len - k0;  // rows of the prefix among them
-    unsigned long long bits = p >= 64 ? ~0ull : (p > 0 ? (1ull << p) - 1 : 0ull);
+    unsigned long long bits = low_bits(p);
+    if constexpr (kWin) bits &= ~low_bits(reach - k0) | low_bits(tree_sinks(s) - k0);
     if (t >= s.cnt) return bits;
     const int j0 = p < 0 ? -p : 0, j1 = 64 - p < s.cnt ? 64 - p : s.cnt;
     if (!a.mask) {
-        const int n = (j1 < t + 1 ? j1 : t + 1) - j0;  // drafted tokens up to t
-        return n > 0 ? bits | (n >= 64 ? ~0ull : (1ull << n) - 1) << (p + j0) : bits;
+        const int from = kWin && t - a.window + 1 > j0 ? t - a.window + 1 : j0;
+        const int n = (j1 < t + 1 ? j1 : t + 1) - from;  // drafted tokens up to t
+        return n > 0 ? bits | (n >= 64 ? ~0ull : (1ull << n) - 1) << (p + from) : bits;
     }
     const uint8_t* m = a.mask + ((a.mask_batched ? (long long)b * a.T : 0) + t) * a.T;
     const bool wide = (reinterpret_cast<uintptr_t>(a.mask) & 15) == 0 && a.T % 16 == 0;  // rows of whole 16-byte words
@@ -675,7 +684,7 @@ __device__ __forceinline__ unsigned long long seen_bits(const TreeArgs& a, const
 }
 
 template <bool kE4, int kNq, bool kExact>
-__device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, uint8_t* smem, uint32_t tmem, TreeWalk w,
+__device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, uint8_t* smem, uint32_t tmem, Walk w,
                                              const WaitCtl& ctl)
 {
     using C = Cfg<kE4, kNq>;
@@ -704,14 +713,16 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
         const int n = w.t1 - w.t0;
         float m_run = -INFINITY, l_run = 0.f, den_run = 0.f, sl2 = a.scale_log2;
         bool first = true;
+        int reach = 0;
+        if constexpr (kWin) reach = live ? tree_reach(a, w.s, w.b, tq) : 0;
         for (int i = kNq == 1 ? wg : 0; i < n; i += kNq == 1 ? 2 : 1) {
-            const int k0 = (w.t0 + i) * kTreeTile;
-            const bool masked = k0 + kTreeTile > w.s.len;
+            const int k0 = tree_row(w.s, (w.t0 + i) * kTreeTile, kTreeTile);
+            const bool masked = tree_masked(w.s, k0, kTreeTile);
             unsigned long long seen[2] = {~0ull, ~0ull};
             if (masked && any_live) {
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
-                    const unsigned long long v = seen_bits(a, w.s, w.b, tq, k0 + 64 * h);
+                    const unsigned long long v = seen_bits(a, w.s, w.b, tq, k0 + 64 * h, reach);
                     seen[0] = h ? seen[0] : v;
                     seen[1] = v;
                 }
@@ -846,7 +857,7 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
         }
 
         if constexpr (kE4) {  // the next item's queries, while the last products run
-            TreeWalk next = w;
+            Walk next = w;
             if (next.next(a)) {
                 if (!warp_wait(bar(C::bQEmpty), item & 1, ctl)) return;
                 split(next.b, next.g, next.r, item + 1);
@@ -904,9 +915,15 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
                     }
                 }
                 if (poison && live) {
-                    for (int j = 0; j < w.s.cnt; ++j) {
+                    // (through a window the prefix's rows that some tokens do not see come first)
+                    for (int j = tree_first_partly(w.s) - w.s.len; j < w.s.cnt; ++j) {
                         const int key = w.s.len + j;
-                        if (key < w.t0 * kTreeTile || key >= w.t1 * kTreeTile || !tree_sees(a, w.b, tq, j)) continue;
+                        if (j < 0 && !tree_partly(w.s, key)) {
+                            j = -1;  // on to the drafted tokens
+                            continue;
+                        }
+                        const int x = tree_list_row(w.s, key, kTreeTile);
+                        if (x < w.t0 * kTreeTile || x >= w.t1 * kTreeTile || !(j < 0 ? key >= reach : tree_sees<kWin>(a, w.b, tq, j))) continue;
                         const long long src = ((long long)w.b * a.Hkv + w.g) * a.cap + key;
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
@@ -997,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
     }
-    TreeWalk w;
+    Walk w;
     const bool work = w.begin(a, blockIdx.x);  // the same for every warp
     tc_fence_before_sync();
     __syncthreads();

@@ -70,3 +70,38 @@ def check_bwd(got, ref, what=""):
         tol = e + EPS2[g.dtype] * 1.01 * (r.abs() + e) + 1e-30
         d = (g.detach().cpu().double() - r).abs() - tol
         assert float(d.max()) <= 0, f"{what}: {name} off by {float(d.max()):.3e} beyond its bound"
+
+
+def tree(q, k, v, lens, mask, ntok, window, sinks, positions):
+    """cache_util.tree through a window: the same four results."""
+    q = q.float().cpu().double()
+    B, H, T, d = q.shape
+    Hkv = k.shape[1]
+    out = torch.zeros((B, H, T, d), dtype=torch.float64)
+    mag = torch.zeros_like(out)
+    lse = torch.full((B, H, T), -math.inf, dtype=torch.float64)
+    big = torch.zeros_like(lse)
+    for b in range(B):
+        n = int(lens[b])
+        cnt = T if ntok is None else int(ntok[b])
+        for t in range(cnt):
+            p = n + t if positions is None else min(max(int(positions[b, t]), n), n + T - 1)
+            prefix = [j for j in range(n) if j < sinks or p - j < window]
+            if mask is None:
+                step = [n + j for j in range(t + 1) if t - j < window]
+            else:
+                row = (mask[b, t] if mask.dim() == 3 else mask[t]).cpu()
+                step = [n + j for j in range(cnt) if row[j]]
+            rows = torch.tensor(prefix + step, dtype=torch.long)
+            if rows.numel() == 0:
+                continue
+            for g in range(Hkv):
+                kk, vv = k[b, g, rows], v[b, g, rows]
+                h = slice(g * (H // Hkv), (g + 1) * (H // Hkv))
+                s = q[b, h, t] @ kk.T / math.sqrt(d)
+                big[b, h, t] = s.abs().amax(-1)
+                lse[b, h, t] = torch.logsumexp(s, -1)
+                w = torch.exp(s - lse[b, h, t].unsqueeze(-1))
+                out[b, h, t] = w @ vv
+                mag[b, h, t] = w @ vv.abs()
+    return out, lse, mag, big
