@@ -198,7 +198,8 @@ def _load_calls(lib):
         loader.exec_module(module)
         module.bind(*(ctypes.cast(getattr(lib, "ring_attn_" + f), ctypes.c_void_p).value for f in (
             "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size", "cache_write", "cache_read", "tree_fwd",
-            "tree_fwd_workspace_size", "qk_rope_axes", "tree_window_fwd")))
+            "tree_fwd_workspace_size", "qk_rope_axes", "tree_window_fwd", "window_fwd", "window_fwd_workspace_size",
+            "window_bwd", "window_bwd_workspace_size")))
     except (ImportError, OSError, AttributeError, TypeError, ValueError) as e:
         warnings.warn(f"the compiled calls in {path} do not load, calls go through Python: {e}", RuntimeWarning)
         return
@@ -1039,6 +1040,10 @@ def window_fwd(q, k, v, n_shards, window, sinks=0, causal=True, layout="zigzag",
     the token at natural position p sees the tokens j <= p with p - j < window, and the first `sinks` ones (causal=False:
     |p - j| < window, and the first ones).  Returns (out [B,H,L,d] in out_dtype -- q's, or float32 -- and lse [B,H,L]
     float32)."""
+    if _calls is not None and stream is None:
+        done = _calls.window_fwd(q, k, v, n_shards, window, sinks, causal, layout, out_dtype, out, lse, workspace)
+        if done is not None:
+            return done
     B, H, Hkv, L, d = _need_qkv(q, k, v)
     dev, lib = q.device, library()
     if out_dtype is None:
@@ -1066,6 +1071,10 @@ def window_bwd(q, k, v, out, lse, dout, n_shards, window, sinks=0, causal=True, 
                dq=None, dk=None, dv=None, workspace=None, stream=None):
     """ring_attn_window_bwd: the gradients of window_fwd's inputs from that of its output, dout (q's dtype), with the
     forward's out (q's dtype or float32) and lse.  Returns (dq, dk, dv) in grad_dtype."""
+    if _calls is not None and stream is None:
+        done = _calls.window_bwd(q, k, v, out, lse, dout, n_shards, window, sinks, causal, layout, grad_dtype, dq, dk, dv, workspace)
+        if done is not None:
+            return done
     B, H, Hkv, L, d = _need_qkv(q, k, v)
     dev, lib = q.device, library()
     _need(out, "out", dev, q.shape)

@@ -16,7 +16,7 @@ ra_status check_window(const Problem& p, int window, int sinks)
     if (st != RA_OK) return st;
     if (window < 1) return fail(RA_ERR_INVALID_ARG, "window must be >= 1 (got %d)", window);
     if (sinks < 0) return fail(RA_ERR_INVALID_ARG, "sinks must be >= 0 (got %d)", sinks);
-    if (p.L >= (1 << 30) || (long long)p.B * p.H * ((p.L + 63) / 64) >= (1LL << 31))
+    if (p.L >= (1 << 30) || (long long)p.B * p.H * ((p.L + 63) / 64) >= (1LL << 30))
         return fail(RA_ERR_UNSUPPORTED, "problem too large");
     return RA_OK;
 }
@@ -122,7 +122,7 @@ size_t ring_attn_window_bwd_workspace_size(int B, int H, int Hkv, int L, int d, 
 {
     const Problem p{B, H, Hkv, L, d, n_shards, causal, layout, dtype};
     if (check_window(p, window, sinks) != RA_OK) return 0;
-    if (dtype == RA_F32) return up256((size_t)B * H * L * sizeof(float));  // D
+    if (dtype == RA_F32) return window_simt_plan(args_of(p, window, sinks).band, B, H, Hkv, d).bytes;
     return window_bwd_plan(args_of(p, window, sinks).band, B, H, Hkv, d).bytes +
            (copies(p) ? 2 * copy_bytes(p, H) + 2 * copy_bytes(p, Hkv) : 0);
 }
@@ -177,7 +177,7 @@ ra_status ring_attn_window_bwd(const void* q, const void* k, const void* v, cons
         if (e == cudaSuccess) e = d == 128 ? launch_window_bwd_tc_d128(a, plan, sw, s) : launch_window_bwd_tc_d64(a, plan, sw, s);
         if (e == cudaSuccess) e = launch_window_bwd_after(a, plan, d, s);
     } else {
-        e = launch_window_bwd_simt(a, static_cast<float*>(workspace), d, s);
+        e = launch_window_bwd_simt(a, window_simt_plan(a.band, B, H, Hkv, d), workspace, d, s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "ring_attn_window_bwd launch");
     return RA_OK;

@@ -28,6 +28,10 @@ decltype(&ring_attn_tree_fwd) tree = nullptr;
 decltype(&ring_attn_tree_fwd_workspace_size) tree_workspace = nullptr;
 decltype(&ring_attn_qk_rope_axes) rope_axes = nullptr;
 decltype(&ring_attn_tree_window_fwd) tree_window = nullptr;
+decltype(&ring_attn_window_fwd) window_forward = nullptr;
+decltype(&ring_attn_window_fwd_workspace_size) window_forward_workspace = nullptr;
+decltype(&ring_attn_window_bwd) window_backward = nullptr;
+decltype(&ring_attn_window_bwd_workspace_size) window_backward_workspace = nullptr;
 
 using at::ScalarType;
 using at::Tensor;
@@ -397,13 +401,90 @@ PyObject* py_rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// What window_fwd and window_bwd share: q, k, v, and n_shards, window, sinks, causal, layout.
+struct WindowCall {
+    int B, H, Hkv, L, d, n, window, sinks, causal, layout, code;
+    ScalarType dt;
+    const void *q, *k, *v;
+    WindowCall(const Call& c, PyObject* const* a, PyObject* const* how)
+    {
+        const Tensor &tq = tensor(a[0]), &tk = tensor(a[1]);
+        four(tk);
+        B = small(tq.size(0)), H = small(tq.size(1)), L = small(tq.size(2)), d = small(tq.size(3)), Hkv = small(tk.size(1));
+        dt = tq.scalar_type();
+        code = code_of(dt);
+        q = c.dense(a[0], {B, H, L, d}, dt);
+        k = c.dense(a[1], {B, Hkv, L, d}, dt);
+        v = c.dense(a[2], {B, Hkv, L, d}, dt);
+        n = whole_number(how[0]);
+        window = whole_number(how[1]);
+        sinks = whole_number(how[2]);
+        if (!PyBool_Check(how[3])) throw Misfit{};
+        causal = how[3] == Py_True;
+        layout = layout_code(how[4]);
+    }
+};
+
+// q, k, v, n_shards, window, sinks, causal, layout, out_dtype, out, lse, workspace
+PyObject* py_window_fwd(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return answer(n, 12, [&]() -> PyObject* {
+        const Tensor& q = tensor(a[0]);
+        four(q);
+        const Call c(q);
+        const WindowCall w(c, a, a + 3);
+        ScalarType odt = w.dt;
+        if (a[8] != Py_None) {
+            if (!THPDtype_Check(a[8])) throw Misfit{};
+            odt = reinterpret_cast<THPDtype*>(a[8])->scalar_type;
+            if (odt != w.dt && odt != at::kFloat) throw Misfit{};
+        }
+        Tensor out = c.output(a[9], {w.B, w.H, w.L, w.d}, odt), lse = c.output(a[10], {w.B, w.H, w.L}, at::kFloat);
+        const Tensor ws = c.workspace(a[11], (int64_t)window_forward_workspace(w.B, w.H, w.Hkv, w.L, w.d, w.n, w.layout, w.code));
+        accept(window_forward(w.q, w.k, w.v, out.data_ptr(), static_cast<float*>(lse.data_ptr()), ws.data_ptr(), (size_t)ws.numel(), w.B, w.H,
+                              w.Hkv, w.L, w.d, w.n, w.window, w.sinks, w.causal, w.layout, w.code, code_of(odt), c.stream()));
+        return pair_of(std::move(out), std::move(lse));
+    });
+}
+
+// q, k, v, out, lse, dout, n_shards, window, sinks, causal, layout, grad_dtype, dq, dk, dv, workspace
+PyObject* py_window_bwd(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return answer(n, 16, [&]() -> PyObject* {
+        const Tensor& q = tensor(a[0]);
+        four(q);
+        const Call c(q);
+        const WindowCall w(c, a, a + 6);
+        const int64_t qs[4] = {w.B, w.H, w.L, w.d}, ks[4] = {w.B, w.Hkv, w.L, w.d};
+        const ScalarType odt = tensor(a[3]).scalar_type();
+        if (odt != w.dt && odt != at::kFloat) throw Misfit{};
+        const void *out = c.dense(a[3], qs, odt), *dout = c.dense(a[5], qs, w.dt);
+        const auto* lse = static_cast<const float*>(c.dense(a[4], {w.B, w.H, w.L}, at::kFloat));
+        if (!THPDtype_Check(a[11])) throw Misfit{};
+        const ScalarType gdt = reinterpret_cast<THPDtype*>(a[11])->scalar_type;
+        const int grad = code_of(gdt);
+        Tensor dq = c.output(a[12], qs, gdt), dk = c.output(a[13], ks, gdt), dv = c.output(a[14], ks, gdt);
+        const size_t need = window_backward_workspace(w.B, w.H, w.Hkv, w.L, w.d, w.n, w.window, w.sinks, w.causal, w.layout, w.code);
+        if (need == 0) throw Misfit{};
+        const Tensor ws = c.workspace(a[15], (int64_t)need);
+        accept(window_backward(w.q, w.k, w.v, out, lse, dout, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), (size_t)ws.numel(), w.B,
+                               w.H, w.Hkv, w.L, w.d, w.n, w.window, w.sinks, w.causal, w.layout, w.code, code_of(odt), grad, c.stream()));
+        PyObject* t[3] = {THPVariable_Wrap(std::move(dq)), THPVariable_Wrap(std::move(dk)), THPVariable_Wrap(std::move(dv))};
+        PyObject* r = t[0] && t[1] && t[2] ? PyTuple_Pack(3, t[0], t[1], t[2]) : nullptr;
+        for (PyObject* o : t) Py_XDECREF(o);
+        return r;
+    });
+}
+
 // bind(address, ...): the library's functions, in the order of the pointers above.
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     void** to[] = {reinterpret_cast<void**>(&norm_rope), reinterpret_cast<void**>(&norm_rope_bwd),
                    reinterpret_cast<void**>(&norm_rope_bwd_workspace), reinterpret_cast<void**>(&write_cache),
                    reinterpret_cast<void**>(&read_cache), reinterpret_cast<void**>(&tree), reinterpret_cast<void**>(&tree_workspace),
-                   reinterpret_cast<void**>(&rope_axes), reinterpret_cast<void**>(&tree_window)};
+                   reinterpret_cast<void**>(&rope_axes), reinterpret_cast<void**>(&tree_window),
+                   reinterpret_cast<void**>(&window_forward), reinterpret_cast<void**>(&window_forward_workspace),
+                   reinterpret_cast<void**>(&window_backward), reinterpret_cast<void**>(&window_backward_workspace)};
     if (n != (Py_ssize_t)(sizeof(to) / sizeof(to[0]))) {
         PyErr_SetString(PyExc_TypeError, "one address for each function");
         return nullptr;
@@ -428,6 +509,8 @@ PyMethodDef methods[] = {{"bind", FAST(py_bind), nullptr},
                          {"qk_norm_rope", FAST(py_norm_rope), nullptr},
                          {"qk_norm_rope_bwd", FAST(py_norm_rope_bwd), nullptr},
                          {"qk_rope_axes", FAST(py_rope_axes), nullptr},
+                         {"window_fwd", FAST(py_window_fwd), nullptr},
+                         {"window_bwd", FAST(py_window_bwd), nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -101,7 +101,14 @@ struct WindowArgs {
 
 // CUDA-core path: float32 (window_simt.cu).
 cudaError_t launch_window_fwd_simt(const WindowArgs& a, int d, cudaStream_t s);
-cudaError_t launch_window_bwd_simt(const WindowArgs& a, float* D, int d, cudaStream_t s);
+struct WindowSimtPlan {
+    int tiles, sink_tiles, segs;  // of 64 positions
+    bool parts;                   // dK and dV are joined from parts
+    long long key_blocks;
+    size_t D_bytes, bytes;        // workspace: D, then the parts
+};
+WindowSimtPlan window_simt_plan(const Band& b, int B, int H, int Hkv, int d);
+cudaError_t launch_window_bwd_simt(const WindowArgs& a, const WindowSimtPlan& p, void* workspace, int d, cudaStream_t s);
 
 
 // Tensor-core path, bf16, layouts that window_tma_reads (window_tc.cuh).

@@ -486,7 +486,7 @@ __device__ __forceinline__ void producer_role(const BwdArgs& a, uint32_t sbase, 
 }
 
 // ------------------------------------------------------------------------------------------------
-// MMA issuer (one thread)
+// MMA issue (one warp, one lane of it)
 // ------------------------------------------------------------------------------------------------
 // Operand descriptors, as the low words of their shared-memory descriptors (query-tile operands
 // at stage 0): K-major views have LBO 16, N- or M-major views LBO = the distance between their
@@ -525,57 +525,45 @@ __device__ __forceinline__ BwdDesc make_desc(uint32_t sbase)
 // pairs of warpgroup w's columns [64w, 64w+64) sit at [64w, 64w+32) of the region.
 __device__ __forceinline__ uint32_t a_col(int kk) { return (uint32_t)(kk >> 2) * 64u + (uint32_t)(kk & 3) * 8u; }
 
-// The issue helpers take their descriptor words through this, so that the compiler rebuilds the
-// eight k-step descriptors at each call (eight 32-bit adds) instead of keeping every product's
-// descriptors live across the tile loop, which would not fit the issuing warp's registers.
-__device__ __forceinline__ uint32_t opaque(uint32_t x)
-{
-    asm volatile("" : "+r"(x));
-    return x;
-}
-
 // D (tmem) = A B over the head dimension, both K-major in shared memory (S^T = K Q^T, dP^T = V dO^T)
-__device__ __forceinline__ void issue_kmajor(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo)
+__device__ __forceinline__ void issue_kmajor(uint32_t lead, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo)
 {
-    a_lo = opaque(a_lo);
-    b_lo = opaque(b_lo);
 #pragma unroll
     for (int kk = 0; kk < kHd / 16; ++kk) {
         const uint32_t off = (uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u;
-        mma_ss(d_tmem, sdesc_at(a_lo, off, kDescHi), sdesc_at(b_lo, off, kDescHi), kId, kk > 0);
+        lead_mma_ss(lead, d_tmem, sdesc_at(a_lo, off, kDescHi), sdesc_at(b_lo, off, kDescHi), kId, kk > 0);
     }
 }
 
 // acc (tmem) += A (tmem, bf16 pairs) B over the 128 query rows, B N-major in shared memory
 // (dV += P^T dO)
-__device__ __forceinline__ void issue_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, bool accumulate)
+__device__ __forceinline__ void issue_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, bool accumulate)
 {
     const uint32_t acc0 = accumulate ? 1u : 0u;
-    b_lo = opaque(b_lo);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
-        mma_ts(d_tmem, a_tmem + a_col(kk), sdesc_at(b_lo, (uint32_t)kk * 2048u, kDescHi), kIdTs, kk > 0 ? 1u : acc0);
+        lead_mma_ts(lead, d_tmem, a_tmem + a_col(kk), sdesc_at(b_lo, (uint32_t)kk * 2048u, kDescHi), kIdTs, kk > 0 ? 1u : acc0);
 }
 
 // dK += dS^T Q over the 128 query rows: A = dS^T K-major (query block kk / 4, 16 queries = 32 bytes
 // of each 128-byte key row), B = Q N-major
-__device__ __forceinline__ void issue_dk(uint32_t tmem, const BwdDesc& dsc, uint32_t q_lo, bool accumulate)
+__device__ __forceinline__ void issue_dk(uint32_t lead, uint32_t tmem, const BwdDesc& dsc, uint32_t q_lo, bool accumulate)
 {
-    const uint32_t a_lo = opaque(dsc.ds_k), b_lo = opaque(q_lo);
+    const uint32_t a_lo = dsc.ds_k, b_lo = q_lo;
     const uint32_t acc0 = accumulate ? 1u : 0u;
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
-        mma_ss(tmem + kColDK, sdesc_at(a_lo, (uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u, kDescHi),
+        lead_mma_ss(lead, tmem + kColDK, sdesc_at(a_lo, (uint32_t)(kk >> 2) * kHalf + (uint32_t)(kk & 3) * 32u, kDescHi),
                sdesc_at(b_lo, (uint32_t)kk * 2048u, kDescHi), kIdTs, kk > 0 ? 1u : acc0);
 }
 
 // dQ^T = K^T dS^T over the 128 key rows
-__device__ __forceinline__ void issue_dq(uint32_t tmem, const BwdDesc& dsc)
+__device__ __forceinline__ void issue_dq(uint32_t lead, uint32_t tmem, const BwdDesc& dsc)
 {
-    const uint32_t a_lo = opaque(dsc.k_m), b_lo = opaque(dsc.ds_n);
+    const uint32_t a_lo = dsc.k_m, b_lo = dsc.ds_n;
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
-        mma_ss(tmem + kColDQ, sdesc_at(a_lo, (uint32_t)kk * 2048u, kDescHi), sdesc_at(b_lo, (uint32_t)kk * 2048u, kDescHi),
+        lead_mma_ss(lead, tmem + kColDQ, sdesc_at(a_lo, (uint32_t)kk * 2048u, kDescHi), sdesc_at(b_lo, (uint32_t)kk * 2048u, kDescHi),
                kIdDQ, kk > 0);
 }
 
@@ -585,71 +573,73 @@ __device__ __forceinline__ void mma_role(const BwdArgs& a, uint32_t sbase, uint3
     constexpr uint32_t kStageLo = kTileBytes >> 4;  // one query-tile stage, in descriptor units
     uint32_t gt = 0, uc = 0;
     bool issued = false;
+    const uint32_t lead = elect();
+    tmem = __shfl_sync(0xffffffffu, tmem, 0);
     const BwdDesc dsc = make_desc(sbase);
     for (long long item = blockIdx.x; item < a.items; item += gridDim.x) {
         {
             const KvUnit u = unit_of(a, item);
             if (u.ntiles == 0) continue;
-            if (!mbar_wait(bar(BAR_KV_FULL), uc & 1, ctl)) goto drain;
+            if (!warp_wait(bar(BAR_KV_FULL), uc & 1, ctl)) goto drain;
             issued = true;
             tc_fence_after_sync();
             // the unit's first S^T and dP^T; later ones are issued one tile ahead (below)
             {
                 const uint32_t st = stage_of(gt), sp = phase_of(gt);
-                if (!mbar_wait(bar(BAR_Q_FULL + (int)st), sp, ctl)) goto drain;
+                if (!warp_wait(bar(BAR_Q_FULL + (int)st), sp, ctl)) goto drain;
                 tc_fence_after_sync();
-                issue_kmajor(tmem + kColX, dsc.k_k, dsc.q_k + st * kStageLo);
-                tc_commit(bar(BAR_ST_FULL));
+                issue_kmajor(lead, tmem + kColX, dsc.k_k, dsc.q_k + st * kStageLo);
+                lead_commit(lead, bar(BAR_ST_FULL));
                 // Y: the previous tile's dQ^T must have been read out (d = 128, where it shares Y)
-                if (!kD64 && gt > 0 && !mbar_wait(bar(BAR_DQ_FREE), (gt - 1) & 1, ctl)) goto drain;
-                if (!mbar_wait(bar(BAR_DO_FULL + (int)st), sp, ctl)) goto drain;
+                if (!kD64 && gt > 0 && !warp_wait(bar(BAR_DQ_FREE), (gt - 1) & 1, ctl)) goto drain;
+                if (!warp_wait(bar(BAR_DO_FULL + (int)st), sp, ctl)) goto drain;
                 tc_fence_after_sync();
-                issue_kmajor(tmem + kColY, dsc.v_k, dsc.do_k + st * kStageLo);
-                tc_commit(bar(BAR_DPT_FULL));
+                issue_kmajor(lead, tmem + kColY, dsc.v_k, dsc.do_k + st * kStageLo);
+                lead_commit(lead, bar(BAR_DPT_FULL));
             }
             for (int t = 0; t < u.ntiles; ++t, ++gt) {
                 const uint32_t st = stage_of(gt);
                 // dV += P^T dO (P^T in X); the accumulators must have been written out at a unit's start
-                if (!mbar_wait(bar(BAR_P_READY), gt & 1, ctl)) goto drain;
-                if (t == 0 && uc > 0 && !mbar_wait(bar(BAR_ACC_FREE), (uc - 1) & 1, ctl)) goto drain;
+                if (!warp_wait(bar(BAR_P_READY), gt & 1, ctl)) goto drain;
+                if (t == 0 && uc > 0 && !warp_wait(bar(BAR_ACC_FREE), (uc - 1) & 1, ctl)) goto drain;
                 tc_fence_after_sync();
-                issue_ts(tmem + kColDV, tmem + kColX, dsc.do_n + st * kStageLo, t > 0);
-                tc_commit(bar(BAR_DO_EMPTY + (int)st));
+                issue_ts(lead, tmem + kColDV, tmem + kColX, dsc.do_n + st * kStageLo, t > 0);
+                lead_commit(lead, bar(BAR_DO_EMPTY + (int)st));
                 const bool more = t + 1 < u.ntiles;
                 const uint32_t nst = stage_of(gt + 1), nsp = phase_of(gt + 1);
                 // next S^T into X, which dV above has read; it runs while phase B computes dS^T
                 if (more) {
-                    if (!mbar_wait(bar(BAR_Q_FULL + (int)nst), nsp, ctl)) goto drain;
+                    if (!warp_wait(bar(BAR_Q_FULL + (int)nst), nsp, ctl)) goto drain;
                     tc_fence_after_sync();
-                    issue_kmajor(tmem + kColX, dsc.k_k, dsc.q_k + nst * kStageLo);
-                    tc_commit(bar(BAR_ST_FULL));
+                    issue_kmajor(lead, tmem + kColX, dsc.k_k, dsc.q_k + nst * kStageLo);
+                    lead_commit(lead, bar(BAR_ST_FULL));
                 }
                 // dQ^T = K^T dS^T (d = 128: into Y, whose dP^T phase B has read; d = 64: into its own
                 // columns, once the previous tile's dQ^T is out), then dK += dS^T Q
-                if (!mbar_wait(bar(BAR_DS_READY), gt & 1, ctl)) goto drain;
-                if (kD64 && gt > 0 && !mbar_wait(bar(BAR_DQ_FREE), (gt - 1) & 1, ctl)) goto drain;
+                if (!warp_wait(bar(BAR_DS_READY), gt & 1, ctl)) goto drain;
+                if (kD64 && gt > 0 && !warp_wait(bar(BAR_DQ_FREE), (gt - 1) & 1, ctl)) goto drain;
                 tc_fence_after_sync();
-                issue_dq(tmem, dsc);
-                tc_commit(bar(BAR_DQ_FULL));
-                issue_dk(tmem, dsc, dsc.q_n + st * kStageLo, t > 0);
-                tc_commit(bar(BAR_Q_EMPTY + (int)st));
+                issue_dq(lead, tmem, dsc);
+                lead_commit(lead, bar(BAR_DQ_FULL));
+                issue_dk(lead, tmem, dsc, dsc.q_n + st * kStageLo, t > 0);
+                lead_commit(lead, bar(BAR_Q_EMPTY + (int)st));
                 // next dP^T into Y (d = 128: once dQ^T has been read out of it)
                 if (more) {
-                    if (!kD64 && !mbar_wait(bar(BAR_DQ_FREE), gt & 1, ctl)) goto drain;
-                    if (!mbar_wait(bar(BAR_DO_FULL + (int)nst), nsp, ctl)) goto drain;
+                    if (!kD64 && !warp_wait(bar(BAR_DQ_FREE), gt & 1, ctl)) goto drain;
+                    if (!warp_wait(bar(BAR_DO_FULL + (int)nst), nsp, ctl)) goto drain;
                     tc_fence_after_sync();
-                    issue_kmajor(tmem + kColY, dsc.v_k, dsc.do_k + nst * kStageLo);
-                    tc_commit(bar(BAR_DPT_FULL));
+                    issue_kmajor(lead, tmem + kColY, dsc.v_k, dsc.do_k + nst * kStageLo);
+                    lead_commit(lead, bar(BAR_DPT_FULL));
                 }
             }
-            tc_commit(bar(BAR_KV_EMPTY));
-            tc_commit(bar(BAR_ACC_FULL));
+            lead_commit(lead, bar(BAR_KV_EMPTY));
+            lead_commit(lead, bar(BAR_ACC_FULL));
             ++uc;
         }
     }
 drain:
     if (issued) {
-        tc_commit(bar(BAR_DRAIN));
+        lead_commit(lead, bar(BAR_DRAIN));
         drain_wait(bar(BAR_DRAIN), 0);
     }
 }
@@ -659,7 +649,7 @@ drain:
 // ------------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(kThreads, 1)
 window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO, const BwdArgs a)
+              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO, const __grid_constant__ BwdArgs a)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -703,7 +693,7 @@ window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     } else if (warp == 12) {
         if ((threadIdx.x & 31) == 0) producer_role(a, sbase, &tmQ, &tmK, &tmV, &tmDO, ctl);
     } else if (warp == 13) {
-        if ((threadIdx.x & 31) == 0) mma_role(a, sbase, tmem, ctl);
+        mma_role(a, sbase, tmem, ctl);
     }
     tc_fence_before_sync();
     __syncthreads();

@@ -4,8 +4,9 @@
 // tiles of 64 that they meet.  Every operand lies transposed in shared memory, [d][64], as float32: the products over the
 // head dimension (scores, dout . v) read four values of both operands with two 16-byte loads for 16 multiply-adds, and
 // the products over positions (P V, dS K, P^T dO, dS^T Q) read four consecutive positions of a column likewise.
-// Backward: one kernel over query tiles for dQ, one over key tiles for dK and dV, both recompute P = exp(s - lse): seven
-// products in place of five, and no sum whose order varies.
+// Backward: blocks over query tiles for dQ, and over key tiles and query heads for dK and dV, both recompute P =
+// exp(s - lse): seven products in place of five, and no sum whose order varies.  The heads' parts of dK and dV, and the
+// segments' of the sinks' tiles, which all later queries see, are added in order by a last launch.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -202,14 +203,12 @@ __device__ __forceinline__ void weights(const WindowArgs& a, int r0, int c0, con
         }
 }
 
+// dQ of 64 queries.
 template <int D>
-__global__ void __launch_bounds__(kThreads) window_bwd_dq_simt_kernel(const WindowArgs a)
+__device__ __forceinline__ void bwd_queries(const WindowArgs& a, float* sm, int zq, int q0)
 {
-    extern __shared__ __align__(16) float sm[];
     float *sq = sm, *sd = sq + D * kStride, *sk = sd + D * kStride, *sv = sk + D * kStride, *sp = sv + D * kStride;
-    const int tiles = (a.band.L + kT - 1) / kT;
-    const int q0 = (int)(blockIdx.x % tiles) * kT, zq = (int)(blockIdx.x / tiles), zk = zq / a.G;
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int zk = zq / a.G, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const long long per = (long long)a.band.L * D;
     load_tile<D>(a.geo, static_cast<const float*>(a.q) + zq * per, q0, sq, a.scale_log2);
     load_tile<D>(a.geo, static_cast<const float*>(a.dout) + zq * per, q0, sd);
@@ -246,57 +245,108 @@ __global__ void __launch_bounds__(kThreads) window_bwd_dq_simt_kernel(const Wind
     }
 }
 
+// dK and dV of 64 keys from one query head and the query tiles [t0, t1): to the gradients, or to `part` [2][64][D].
 template <int D>
-__global__ void __launch_bounds__(kThreads) window_bwd_dkv_simt_kernel(const WindowArgs a)
+__device__ __forceinline__ void bwd_keys(const WindowArgs& a, float* sm, int zq, int k0, int t0, int t1, float* part)
 {
-    extern __shared__ __align__(16) float sm[];
     float *sk = sm, *sv = sk + D * kStride, *sq = sv + D * kStride, *sd = sq + D * kStride, *sp = sd + D * kStride, *ss = sp + kT * kStride;
-    const int tiles = (a.band.L + kT - 1) / kT;
-    const int k0 = (int)(blockIdx.x % tiles) * kT, zk = (int)(blockIdx.x / tiles);
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int zk = zq / a.G, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const long long per = (long long)a.band.L * D;
     load_tile<D>(a.geo, static_cast<const float*>(a.k) + zk * per, k0, sk, a.scale_log2);
     load_tile<D>(a.geo, static_cast<const float*>(a.v) + zk * per, k0, sv);
     float dk[4][D / 16] = {}, dv[4][D / 16] = {};
-    const QueryRun run = query_tiles(a.band, k0, kT, kT);
-    for (int h = 0; h < a.G; ++h) {
-        const int zq = zk * a.G + h;
-        for (int t = run.first; t < run.last; ++t) {
-            const int q0 = t * kT;
-            __syncthreads();
-            load_tile<D>(a.geo, static_cast<const float*>(a.q) + zq * per, q0, sq);
-            load_tile<D>(a.geo, static_cast<const float*>(a.dout) + zq * per, q0, sd);
-            float lse2[4], Dv[4];
+    for (int t = t0; t < t1; ++t) {
+        const int q0 = t * kT;
+        __syncthreads();
+        load_tile<D>(a.geo, static_cast<const float*>(a.q) + zq * per, q0, sq);
+        load_tile<D>(a.geo, static_cast<const float*>(a.dout) + zq * per, q0, sd);
+        float lse2[4], Dv[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int p = q0 + 4 * tx + j;
-                const bool has = p < a.band.L;
-                lse2[j] = has ? a.lse[(long long)zq * a.band.L + buffer_row(a.geo, p)] * kLog2e : 0.f;
-                Dv[j] = has ? a.D[(long long)zq * a.band.L + p] : 0.f;
-            }
-            __syncthreads();
-            float s[4][4] = {}, dp[4][4] = {};
-            dot_tile<D>(sk, sq, s);
-            dot_tile<D>(sv, sd, dp);
-            weights<true>(a, k0, q0, lse2, Dv, s, dp);
-            put4(sp, s);
-            put4(ss, dp);
-            __syncthreads();
-            const bool whole = band_tile_whole(a.band, q0, kT, k0, kT);
-            apply_tile<D, kNegative>(whole, sp, sd, dv);
-            apply_tile<D, kZero>(whole, ss, sq, dk);
+        for (int j = 0; j < 4; ++j) {
+            const int p = q0 + 4 * tx + j;
+            const bool has = p < a.band.L;
+            lse2[j] = has ? a.lse[(long long)zq * a.band.L + buffer_row(a.geo, p)] * kLog2e : 0.f;
+            Dv[j] = has ? a.D[(long long)zq * a.band.L + p] : 0.f;
         }
+        __syncthreads();
+        float s[4][4] = {}, dp[4][4] = {};
+        dot_tile<D>(sk, sq, s);
+        dot_tile<D>(sv, sd, dp);
+        weights<true>(a, k0, q0, lse2, Dv, s, dp);
+        put4(sp, s);
+        put4(ss, dp);
+        __syncthreads();
+        const bool whole = band_tile_whole(a.band, q0, kT, k0, kT);
+        apply_tile<D, kNegative>(whole, sp, sd, dv);
+        apply_tile<D, kZero>(whole, ss, sq, dk);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int p = k0 + 4 * ty + i;
-        if (p >= a.band.L) continue;
-        const long long row = (long long)zk * a.band.L + buffer_row(a.geo, p);
+        const int r = 4 * ty + i;
+        if (k0 + r >= a.band.L) continue;
+        const long long row = (long long)zk * a.band.L + buffer_row(a.geo, k0 + r);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-            store1(a.dk, row * D + tx + 16 * k, dk[i][k], a.grad_dtype);
-            store1(a.dv, row * D + tx + 16 * k, dv[i][k], a.grad_dtype);
+            const int c = tx + 16 * k;
+            if (part) {
+                part[r * D + c] = dk[i][k];
+                part[(kT + r) * D + c] = dv[i][k];
+            } else {
+                store1(a.dk, row * D + c, dk[i][k], a.grad_dtype);
+                store1(a.dv, row * D + c, dv[i][k], a.grad_dtype);
+            }
         }
+    }
+}
+
+// One launch for both, so that the blocks of each fill the SMs beside the other's.  The sinks' tiles come first, in
+// segments: they are the longest.
+template <int D>
+__global__ void __launch_bounds__(kThreads) window_bwd_simt_kernel(const WindowArgs a, const WindowSimtPlan p, float* parts)
+{
+    extern __shared__ __align__(16) float sm[];
+    long long x = blockIdx.x;
+    if (x < p.key_blocks) {
+        const int zq = (int)(x % ((long long)a.B * a.H));
+        int tile = (int)(x / ((long long)a.B * a.H)), seg = 0, segs = 1;
+        if (tile < p.sink_tiles * p.segs) {
+            seg = tile % p.segs;
+            tile /= p.segs;
+            segs = p.segs;
+        } else {
+            tile -= p.sink_tiles * (p.segs - 1);
+        }
+        const QueryRun run = query_tiles(a.band, tile * kT, kT, kT);
+        const int n = run.last - run.first;
+        bwd_keys<D>(a, sm, zq, tile * kT, run.first + (int)((long long)n * seg / segs), run.first + (int)((long long)n * (seg + 1) / segs),
+                    p.parts ? parts + x * 2 * kT * D : nullptr);
+    } else {
+        x -= p.key_blocks;
+        bwd_queries<D>(a, sm, (int)(x / p.tiles), (int)(x % p.tiles) * kT);
+    }
+}
+
+// dK and dV: the parts of a tile's query heads and segments, added in order.
+template <int D>
+__global__ void __launch_bounds__(kThreads) window_join_simt_kernel(const WindowArgs a, const WindowSimtPlan p, const float* parts)
+{
+    const long long total = (long long)a.B * a.Hkv * a.band.L * D, heads = (long long)a.B * a.H;
+    for (long long e = (long long)blockIdx.x * kThreads + threadIdx.x; e < total; e += (long long)gridDim.x * kThreads) {
+        const int c = (int)(e % D), zk = (int)(e / D / a.band.L), pos = (int)(e / D - (long long)zk * a.band.L);
+        const int tile = pos / kT, r = pos % kT;
+        const bool sink = tile < p.sink_tiles;
+        const int segs = sink ? p.segs : 1;
+        const long long slot = sink ? (long long)tile * p.segs : tile + (long long)p.sink_tiles * (p.segs - 1);
+        float dk = 0.f, dv = 0.f;
+        for (int h = 0; h < a.G; ++h)
+            for (int s = 0; s < segs; ++s) {
+                const float* x = parts + ((slot + s) * heads + (long long)zk * a.G + h) * 2 * kT * D + r * D + c;
+                dk += x[0];
+                dv += x[kT * D];
+            }
+        const long long row = (long long)zk * a.band.L + buffer_row(a.geo, pos);
+        store1(a.dk, row * D + c, dk, a.grad_dtype);
+        store1(a.dv, row * D + c, dv, a.grad_dtype);
     }
 }
 
@@ -351,22 +401,21 @@ cudaError_t fwd(const WindowArgs& a, cudaStream_t s)
 }
 
 template <int D>
-cudaError_t bwd(const WindowArgs& a, float* Dv, cudaStream_t s)
+cudaError_t bwd(const WindowArgs& a, const WindowSimtPlan& p, float* Dv, float* parts, cudaStream_t s)
 {
     static std::mutex mu;
-    static bool done_q[64], done_k[64];
-    constexpr size_t smem_q = 4 * tile_bytes(D) + kWeightBytes, smem_k = 4 * tile_bytes(D) + 2 * kWeightBytes;
-    cudaError_t e = allow(window_bwd_dq_simt_kernel<D>, smem_q, mu, done_q);
-    if (e == cudaSuccess) e = allow(window_bwd_dkv_simt_kernel<D>, smem_k, mu, done_k);
+    static bool done[64];
+    constexpr size_t smem = 4 * tile_bytes(D) + 2 * kWeightBytes;
+    cudaError_t e = allow(window_bwd_simt_kernel<D>, smem, mu, done);
     if (e != cudaSuccess) return e;
     const long long rows = (long long)a.B * a.H * a.band.L, need = (rows + kThreads / 32 - 1) / (kThreads / 32);
     const long long most = (long long)device_sm_count() * 8;
     window_rowdot_kernel<D><<<(unsigned)(need < most ? need : most), kThreads, 0, s>>>(a, Dv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const long long tiles = (a.band.L + kT - 1) / kT;
-    window_bwd_dq_simt_kernel<D><<<(unsigned)(a.B * (long long)a.H * tiles), kThreads, smem_q, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    window_bwd_dkv_simt_kernel<D><<<(unsigned)(a.B * (long long)a.Hkv * tiles), kThreads, smem_k, s>>>(a);
+    window_bwd_simt_kernel<D><<<(unsigned)(p.key_blocks + a.B * (long long)a.H * p.tiles), kThreads, smem, s>>>(a, p, parts);
+    if ((e = cudaGetLastError()) != cudaSuccess || !p.parts) return e;
+    const long long blocks = ((long long)a.B * a.Hkv * a.band.L * D + kThreads - 1) / kThreads;
+    window_join_simt_kernel<D><<<(unsigned)(blocks < most ? blocks : most), kThreads, 0, s>>>(a, p, parts);
     return cudaGetLastError();
 }
 
@@ -377,11 +426,32 @@ cudaError_t launch_window_fwd_simt(const WindowArgs& a, int d, cudaStream_t s)
     return d == 128 ? fwd<128>(a, s) : fwd<64>(a, s);
 }
 
-cudaError_t launch_window_bwd_simt(const WindowArgs& args, float* D, int d, cudaStream_t s)
+WindowSimtPlan window_simt_plan(const Band& b, int B, int H, int Hkv, int d)
+{
+    WindowSimtPlan p = {};
+    p.tiles = (b.L + kT - 1) / kT;
+    p.sink_tiles = (b.S + kT - 1) / kT;
+    p.segs = 1;
+    if (p.sink_tiles > 0) {  // segments about as long as the other tiles' runs, but no more than a few for every SM in all
+        const long long near = ((long long)b.W + kT - 1) / kT + 1, unit = b.causal ? near : 2 * near - 1;
+        const long long most = 1024 / ((long long)B * H * p.sink_tiles);
+        long long segs = (p.tiles + unit - 1) / unit;
+        if (segs > most) segs = most;
+        p.segs = segs < 1 ? 1 : (int)segs;
+    }
+    p.key_blocks = (long long)B * H * (p.tiles + (long long)p.sink_tiles * (p.segs - 1));
+    p.parts = H != Hkv || p.segs > 1;
+    p.D_bytes = ((size_t)B * H * b.L * sizeof(float) + 255) & ~size_t(255);
+    p.bytes = p.D_bytes + (p.parts ? (size_t)p.key_blocks * 2 * kT * d * sizeof(float) : 0);
+    return p;
+}
+
+cudaError_t launch_window_bwd_simt(const WindowArgs& args, const WindowSimtPlan& p, void* workspace, int d, cudaStream_t s)
 {
     WindowArgs a = args;
+    float *D = static_cast<float*>(workspace), *parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.D_bytes);
     a.D = D;
-    return d == 128 ? bwd<128>(a, D, s) : bwd<64>(a, D, s);
+    return d == 128 ? bwd<128>(a, p, D, parts, s) : bwd<64>(a, p, D, parts, s);
 }
 
 }  // namespace ra

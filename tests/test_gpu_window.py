@@ -107,12 +107,15 @@ def test_no_window_is_ring_attention(causal, d, dtype):
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("layout,n", [("contiguous", 1), ("striped", 4), ("zigzag", 2)])
 def test_what_is_hidden_has_no_part(layout, n, dtype):
-    """NaN and infinities in keys and values that most rows do not see."""
+    """NaN and infinities in keys and values that most rows do not see.  In float32 those rows keep every bit.  With bf16
+    inputs the rows that share a tile with such a value are computed once more, with unrounded weights: to the bounds of any
+    row, and lse, which has no value in it, to the last bit."""
     B, H, Hkv, L, d, W, S = 1, 4, 2, 640, 128, 70, 3
     q, k, v, _ = _inputs(B, H, Hkv, L, d, dtype, seed=9)
     order = cu.natural(L, n, layout)
     at = torch.argsort(order)
     out, lse = ra.window_fwd(q, k, v, n, W, S, True, layout)
+    ref = wu.fwd(q, k, v, n, layout, W, S, True)
     for j, (kx, vx) in {200: (math.nan, 1.0), 301: (1.0, math.nan), 383: (1.0, math.inf), 384: (1.0, -math.inf), 511: (math.inf, math.nan)}.items():
         k2, v2 = k.clone(), v.clone()
         k2[:, :, at[j], 5] *= kx
@@ -121,7 +124,10 @@ def test_what_is_hidden_has_no_part(layout, n, dtype):
         hidden = torch.ones(L, dtype=torch.bool)
         hidden[j:j + W] = False
         rows = hidden[order].to(DEV)
-        assert torch.equal(o2[:, :, rows], out[:, :, rows]) and torch.equal(l2[:, :, rows], lse[:, :, rows]), j
+        assert torch.equal(l2[:, :, rows], lse[:, :, rows]), j
+        if dtype == F32 or math.isfinite(vx):
+            assert torch.equal(o2[:, :, rows], out[:, :, rows]), j
+        cu.check_tree((o2[:, :, rows], l2[:, :, rows]), [x[:, :, rows.cpu()] for x in ref], WEIGHT_EPS[dtype], dtype, str(j))
         if not math.isfinite(vx):  # who sees it has it
             assert not bool(torch.isfinite(o2[:, :, ~rows][..., 7]).any())
             if math.isfinite(kx):
