@@ -45,23 +45,30 @@ WindowArgs args_of(const Problem& p, int window, int sinks)
     return a;
 }
 
-// bf16 inputs that TMA cannot read in natural order are copied into it, one after another from `at` in the workspace.
+// bf16 inputs that TMA cannot read in natural order are copied into it, one after another in the workspace.
 bool copies(const Problem& p) { return p.dtype == RA_BF16 && !window_tma_reads(p.geo()); }
 size_t copy_bytes(const Problem& p, int heads) { return up256((size_t)p.B * heads * p.L * p.d * 2); }
 
-struct Copier {
-    const Problem& p;
-    char* at;
-    cudaStream_t s;
-    cudaError_t e = cudaSuccess;
-    const void* operator()(const void* src, int heads)
-    {
-        void* dst = at;
-        at += copy_bytes(p, heads);
-        if (e == cudaSuccess) e = launch_window_gather(p.geo(), src, dst, (long long)p.B * heads, p.d, s);
-        return dst;
-    }
-};
+WindowCopies copies_at(const Problem& p, void* at, bool backward)
+{
+    char* x = static_cast<char*>(at);
+    WindowCopies w;
+    w.q = x;
+    w.k = x + copy_bytes(p, p.H);
+    w.v = x + copy_bytes(p, p.H) + copy_bytes(p, p.Hkv);
+    w.dout = backward ? x + copy_bytes(p, p.H) + 2 * copy_bytes(p, p.Hkv) : nullptr;
+    return w;
+}
+
+// The products read the copies.
+void read_copies(WindowArgs& a, const WindowCopies& w)
+{
+    a.q = w.q;
+    a.k = w.k;
+    a.v = w.v;
+    if (w.dout) a.dout = w.dout;
+    a.geo = make_geometry(a.band.L, 1, RA_LAYOUT_CONTIGUOUS, a.band.causal);
+}
 
 }  // namespace
 }  // namespace ra
@@ -102,12 +109,9 @@ ra_status ring_attn_window_fwd(const void* q, const void* k, const void* v, void
         unsigned int* sw = status_word(&e);
         if (!sw) return cuda_fail(e, "status word");
         if (copies(p)) {
-            Copier copy{p, static_cast<char*>(workspace), s};
-            a.q = copy(q, H);
-            a.k = copy(k, Hkv);
-            a.v = copy(v, Hkv);
-            if (copy.e != cudaSuccess) return cuda_fail(copy.e, "ring_attn_window_fwd copies");
-            a.geo = make_geometry(L, 1, RA_LAYOUT_CONTIGUOUS, causal);
+            const WindowCopies w = copies_at(p, workspace, false);
+            if ((e = launch_window_copies(a, w, d, s)) != cudaSuccess) return cuda_fail(e, "ring_attn_window_fwd copies");
+            read_copies(a, w);
         }
         e = d == 128 ? launch_window_fwd_tc_d128(a, sw, s) : launch_window_fwd_tc_d64(a, sw, s);
     } else {
@@ -164,16 +168,9 @@ ra_status ring_attn_window_bwd(const void* q, const void* k, const void* v, cons
         plan.D = reinterpret_cast<float*>(ws + plan.D_at);
         plan.dq = reinterpret_cast<float*>(ws + plan.dq_at);
         plan.part = reinterpret_cast<float*>(ws + plan.part_at);
-        if (copies(p)) {
-            Copier copy{p, ws + plan.bytes, s};
-            a.q = copy(q, H);
-            a.k = copy(k, Hkv);
-            a.v = copy(v, Hkv);
-            a.dout = copy(dout, H);
-            if (copy.e != cudaSuccess) return cuda_fail(copy.e, "ring_attn_window_bwd copies");
-            a.geo = make_geometry(L, 1, RA_LAYOUT_CONTIGUOUS, causal);
-        }
-        e = launch_window_bwd_before(a, plan, d, s);
+        const WindowCopies w = copies(p) ? copies_at(p, ws + plan.bytes, true) : WindowCopies{};
+        e = launch_window_bwd_before(a, plan, w, d, s);
+        if (w.dout) read_copies(a, w);
         if (e == cudaSuccess) e = d == 128 ? launch_window_bwd_tc_d128(a, plan, sw, s) : launch_window_bwd_tc_d64(a, plan, sw, s);
         if (e == cudaSuccess) e = launch_window_bwd_after(a, plan, d, s);
     } else {

@@ -61,6 +61,7 @@ struct TreeArgs {
     float scale_log2;  // log2(e) / sqrt(d)
     int window, sinks; // kWin
     const int* pos;    // kWin: [B][T] positions of the tokens, or null: lens + t
+    int whole;         // kWin: CTA c takes item c alone; no item is shared and there is no second launch
 };
 
 struct TreeSeq {
@@ -193,6 +194,20 @@ struct TreeWalkOf {
     // One warp calls these.  The walk of CTA `cta`; false if it has no tiles.
     __device__ __forceinline__ bool begin(const TreeArgs& a, int cta)
     {
+        if constexpr (kWin) {
+            if (a.whole) {
+                const int per = a.Hkv * a.nrt, item = cta % per;
+                b = cta / per;
+                g = item / a.nrt;
+                r = item % a.nrt;
+                s = tree_sequence<kWin>(a, b);
+                if (s.bad && threadIdx.x == 0) atomicOr(a.status, kStatusRange);
+                t0 = 0;
+                total = left = t1 = nt = tree_tiles(a, s);
+                first = true;
+                return nt > 0;
+            }
+        }
         const int mine = lengths(a);
         const long long at = tree_first(a, total, cta);
         left = tree_first(a, total, cta + 1) - at;
@@ -267,6 +282,21 @@ struct TreeWalkOf {
     }
 };
 using TreeWalk = TreeWalkOf<false>;
+
+// Zeros and -infinity for the rows of CTA `cta`'s item, whose sequence has no tokens (TreeArgs::whole); all its threads.
+template <int D>
+__device__ __forceinline__ void tree_clear_item(const TreeArgs& a, int cta)
+{
+    const int r = cta % a.nrt, rows = a.R - r * a.rt < a.rt ? a.R - r * a.rt : a.rt;
+    const long long row0 = (long long)(cta / a.nrt) * a.R + (long long)r * a.rt;  // cta / nrt: b Hkv + g
+    for (int e = threadIdx.x; e < rows * (D / 2); e += blockDim.x) {
+        if (a.bf16_out)
+            static_cast<uint32_t*>(a.out)[row0 * (D / 2) + e] = 0u;
+        else
+            static_cast<float2*>(a.out)[row0 * (D / 2) + e] = make_float2(0.f, 0.f);
+    }
+    for (int e = threadIdx.x; e < rows; e += blockDim.x) a.lse[row0 + e] = -INFINITY;
+}
 
 // Does query token t see drafted token j (both < cnt)?
 template <bool kWin = false>

@@ -249,10 +249,18 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
     a.window = t.window;
     a.sinks = t.sinks;
     a.pos = t.positions;
+    a.whole = 0;
     if (a.window) {  // no more CTAs than tiles that can be in reach
         const long long reach = (long long)t.window + t.T, sinks = t.sinks < c.cap ? t.sinks : c.cap;
         const long long most = (long long)c.B * c.Hkv * u.nrt * (reach / u.tile + 2 + (sinks + u.tile - 1) / u.tile);
         if (a.ctas > most) a.ctas = (int)most;
+        const long long items = (long long)c.B * c.Hkv * u.nrt;
+        // With one item for most CTAs each takes one alone: an end, a start and the second launch saved count for more than
+        // an even split (windows of 1024 rows: 16 sequences of 8 drafted tokens, 128 items on 152 CTAs, 30 us in place of 38
+        // over e4m3, 22 in place of 31 over bf16; one token each of 32 sequences, 256 items on 304, 32 in place of 38; of 4096
+        // rows, 63 in place of 71 and 81 in place of 87).  Below half as many items as CTAs the split wins.
+        a.whole = items <= a.ctas && 2 * items > a.ctas;
+        if (a.whole) a.ctas = (int)items;
     }
     char* ws = static_cast<char*>(t.workspace);
     a.border = reinterpret_cast<int4*>(ws);
@@ -266,7 +274,7 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
             : c.d == 128 ? launch_tree_tc_d128(a, e4m3, s) : launch_tree_tc_d64(a, e4m3, s);
     else
         e = launch_tree_simt(a, c.d, c.dtype, s);
-    return e != cudaSuccess ? e : launch_tree_join(a, c.d, s);
+    return e != cudaSuccess || a.whole ? e : launch_tree_join(a, c.d, s);
 }
 
 cudaError_t launch_tree_join(const TreeArgs& a, int d, cudaStream_t s)

@@ -145,6 +145,9 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
     Walk w;
     if (!w.begin(a, blockIdx.x)) {  // the same for every warp
         if (threadIdx.x == 0) a.border[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        if constexpr (kWin) {
+            if (a.whole) tree_clear_item<D>(a, blockIdx.x);
+        }
         return;
     }
     const WaitCtl ctl{abort_flag, a.status, 0};
@@ -206,7 +209,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
                 l[c][u] = 0.f;
                 top[c][u] = -INFINITY;
                 if (x < a.R && x % a.T < w.s.cnt) live |= 1u << (2 * c + u);
-                if constexpr (kWin) reach[c][u] = x < a.R && x % a.T < w.s.cnt ? tree_reach(a, w.s, w.b, x % a.T) : 0;
+                // (a column without a query sees no row that is dead: those have no scale of their own)
+                if constexpr (kWin) reach[c][u] = x < a.R && x % a.T < w.s.cnt ? tree_reach(a, w.s, w.b, x % a.T) : w.s.len;
             }
 #pragma unroll
             for (int j = 0; j < kTiles; ++j)

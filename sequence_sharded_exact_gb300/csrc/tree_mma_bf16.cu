@@ -84,6 +84,9 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
     Walk w;
     if (!w.begin(a, blockIdx.x)) {  // the same for every warp
         if (threadIdx.x == 0) a.border[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        if constexpr (kWin) {
+            if (a.whole) tree_clear_item<D>(a, blockIdx.x);
+        }
         return;
     }
     const WaitCtl ctl{abort_flag, a.status, 0};
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
             m[u] = -INFINITY;
             l[u] = 0.f;
             live[u] = x < a.R && x % a.T < w.s.cnt;
-            if constexpr (kWin) reach[u] = live[u] ? tree_reach(a, w.s, w.b, x % a.T) : 0;
+            if constexpr (kWin) reach[u] = live[u] ? tree_reach(a, w.s, w.b, x % a.T) : w.s.len;
         }
 #pragma unroll
         for (int j = 0; j < kTiles; ++j)

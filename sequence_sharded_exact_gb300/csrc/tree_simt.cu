@@ -108,6 +108,9 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
     int4 border = make_int4(-1, 0, 0, 0);
     if (!w.begin(a, blockIdx.x)) {
         if (tid == 0) a.border[blockIdx.x] = border;
+        if constexpr (kWin) {
+            if (a.whole) tree_clear_item<D>(a, blockIdx.x);
+        }
         return;
     }
     do {

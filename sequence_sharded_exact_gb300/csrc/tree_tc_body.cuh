@@ -1042,6 +1042,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
         }
     }
     if (!work && threadIdx.x == 0) a.border[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if constexpr (kWin) {
+        if (!work && a.whole) tree_clear_item<kHd>(a, blockIdx.x);
+    }
     tc_fence_before_sync();
     __syncthreads();
     if (warp == 9) {

@@ -126,10 +126,13 @@ struct WindowBwdPlan {
 WindowBwdPlan window_bwd_plan(const Band& b, int B, int H, int Hkv, int d);
 cudaError_t launch_window_bwd_tc_d128(const WindowArgs& a, const WindowBwdPlan& p, unsigned int* status, cudaStream_t s);
 cudaError_t launch_window_bwd_tc_d64(const WindowArgs& a, const WindowBwdPlan& p, unsigned int* status, cudaStream_t s);
-// What comes before and after them (window_aux.cu): D, lse2 and a cleared dq; dq and the sinks' dk and dv.
-cudaError_t launch_window_bwd_before(const WindowArgs& a, const WindowBwdPlan& p, int d, cudaStream_t s);
+// Copies in natural order, where TMA cannot read the inputs so (dout null: none, but for the forward's).
+struct WindowCopies {
+    void *q, *k, *v, *dout;
+};
+cudaError_t launch_window_copies(const WindowArgs& a, const WindowCopies& w, int d, cudaStream_t s);
+// What comes before and after the backward (window_aux.cu): D, lse2, a cleared dq and the copies; dq and the sinks' dk, dv.
+cudaError_t launch_window_bwd_before(const WindowArgs& a, const WindowBwdPlan& p, const WindowCopies& w, int d, cudaStream_t s);
 cudaError_t launch_window_bwd_after(const WindowArgs& a, const WindowBwdPlan& p, int d, cudaStream_t s);
-// Rows of [heads][L][d] bf16 in natural order.
-cudaError_t launch_window_gather(const Geometry& g, const void* src, void* dst, long long heads, int d, cudaStream_t s);
 
 }  // namespace ra

@@ -3,7 +3,7 @@
 // Before the backward: D = dout . out per row, lse in log2 units and the float32 accumulator of dQ cleared, all in natural
 // order and padded to whole tiles of 128 positions (rows behind the sequence: -lse2 = -infinity, which makes their P 0).
 // After it: dQ from the accumulator to the layout's rows, and the sinks' dK and dV, added over their segments in order.
-// Layouts that TMA cannot read in natural order with one box (window_tc.cuh) are copied into it first.
+// Layouts that TMA cannot read in natural order with one box (window_tc.cuh) are copied into it first, in the same launch.
 // A group of d / 8 lanes has a row, 8 elements (16 bytes of bf16) each.
 #include <cuda_bf16.h>
 #include <math.h>
@@ -17,16 +17,19 @@ namespace {
 
 constexpr int kThreads = 256;
 
+__device__ __forceinline__ void spread8(const uint4& v, float (&f)[8])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f[2 * e] = __uint_as_float(w[e] << 16);
+        f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+}
 __device__ __forceinline__ void load8(const void* p, long long i, bool bf16, float (&f)[8])
 {
     if (bf16) {
-        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            f[2 * e] = __uint_as_float(w[e] << 16);
-            f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-        }
+        spread8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i), f);
     } else {
         const float4* v = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
         const float4 a = v[0], b = v[1];
@@ -61,21 +64,61 @@ __device__ __forceinline__ Row row_of(const Geometry& g, int padded, long long x
     return r;
 }
 
+// One row in natural order: copied from src (copies in natural order), in one launch with the others.
+struct Copies {
+    const uint4* src[3];
+    uint4* dst[3];
+    long long rows[3];  // 0: no copy
+};
 template <int D>
-__global__ void __launch_bounds__(kThreads) before_kernel(const Geometry og, const Geometry dg, const void* out, bool out_bf16, const void* dout,
-                                                          const float* lse, float* lse2, float* Dv, float* dq, int padded, long long rows)
+__device__ __forceinline__ void copy_rows(const Geometry& g, const uint4* src, uint4* dst, long long rows, long long x0, long long step)
+{
+    constexpr int kLanes = D / 8, U = 4;  // four loads on their way
+    const int c = threadIdx.x % kLanes;
+    for (long long x = x0; x < rows; x += U * step) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long y = x + u * step;
+            if (y >= rows) break;
+            const long long z = y / g.L;
+            v[u] = src[(z * g.L + buffer_row(g, (int)(y - z * g.L))) * kLanes + c];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (x + u * step < rows) dst[(x + u * step) * kLanes + c] = v[u];
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) copy_kernel(const Geometry g, const Copies copies)
+{
+    constexpr int kLanes = D / 8;
+    const long long x0 = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes, step = (long long)gridDim.x * (kThreads / kLanes);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) copy_rows<D>(g, copies.src[i], copies.dst[i], copies.rows[i], x0, step);
+}
+
+// kCopies: dout's rows in natural order too (dout_copy), and the others.
+template <int D, bool kCopies>
+__global__ void __launch_bounds__(kThreads) before_kernel(const Geometry g, const void* out, bool out_bf16, const void* dout, uint4* dout_copy,
+                                                          const float* lse, float* lse2, float* Dv, float* dq, int padded, long long rows,
+                                                          const Copies copies)
 {
     constexpr int kLanes = D / 8;
     const int c = threadIdx.x % kLanes * 8;
-    const long long step = (long long)gridDim.x * (kThreads / kLanes), up = (rows + 31) / 32 * 32;
-    for (long long x = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes; x < up; x += step) {
+    const long long x0 = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes, step = (long long)gridDim.x * (kThreads / kLanes);
+    const long long up = (rows + 31) / 32 * 32;
+    for (long long x = x0; x < up; x += step) {
         const bool has = x < rows;
-        const Row o = row_of(og, padded, has ? x : 0), g = row_of(dg, padded, has ? x : 0);
+        const Row r = row_of(g, padded, has ? x : 0);
         float sum = 0.f;
-        if (has && o.in) {
+        if (has && r.in) {
             float a[8], b[8];
-            load8(out, o.at * D + c, out_bf16, a);
-            load8(dout, g.at * D + c, true, b);
+            const uint4 raw = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(dout) + r.at * D + c);
+            load8(out, r.at * D + c, out_bf16, a);
+            spread8(raw, b);
+            if constexpr (kCopies) dout_copy[((long long)r.z * g.L + r.p) * kLanes + c / 8] = raw;
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum = fmaf(a[e], b[e], sum);
         }
@@ -86,8 +129,12 @@ __global__ void __launch_bounds__(kThreads) before_kernel(const Geometry og, con
         store8(dq, x * D + c, false, zero);
         if (c == 0) {
             Dv[x] = sum;
-            lse2[x] = o.in ? -kLog2e * lse[o.at] : -INFINITY;
+            lse2[x] = r.in ? -kLog2e * lse[r.at] : -INFINITY;
         }
+    }
+    if constexpr (kCopies) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) copy_rows<D>(g, copies.src[i], copies.dst[i], copies.rows[i], x0, step);
     }
 }
 
@@ -132,18 +179,6 @@ __global__ void __launch_bounds__(kThreads) sinks_kernel(const Geometry g, const
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) gather_kernel(const Geometry g, const uint4* src, uint4* dst, long long rows)
-{
-    constexpr int kLanes = D / 8;
-    const int c = threadIdx.x % kLanes;
-    const long long step = (long long)gridDim.x * (kThreads / kLanes);
-    for (long long x = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes; x < rows; x += step) {
-        const long long z = x / g.L;
-        dst[x * kLanes + c] = src[(z * g.L + buffer_row(g, (int)(x - z * g.L))) * kLanes + c];
-    }
-}
-
 unsigned blocks(long long rows, int d)
 {
     const long long per = kThreads / (d / 8), want = (rows + per - 1) / per, most = (long long)device_sm_count() * 16;
@@ -178,14 +213,43 @@ WindowBwdPlan window_bwd_plan(const Band& b, int B, int H, int Hkv, int d)
     return p;
 }
 
-cudaError_t launch_window_bwd_before(const WindowArgs& a, const WindowBwdPlan& p, int d, cudaStream_t s)
+namespace {
+
+Copies copies_of(const WindowArgs& a, const WindowCopies& w)
+{
+    Copies c;
+    const long long L = a.band.L, q = (long long)a.B * a.H * L, kv = (long long)a.B * a.Hkv * L;
+    const void* src[3] = {a.q, a.k, a.v};
+    void* dst[3] = {w.q, w.k, w.v};
+    for (int i = 0; i < 3; ++i) {
+        c.src[i] = static_cast<const uint4*>(src[i]);
+        c.dst[i] = static_cast<uint4*>(dst[i]);
+        c.rows[i] = i ? kv : q;
+    }
+    return c;
+}
+
+}  // namespace
+
+cudaError_t launch_window_copies(const WindowArgs& a, const WindowCopies& w, int d, cudaStream_t s)
+{
+    const Copies c = copies_of(a, w);
+    if (d == 128)
+        copy_kernel<128><<<blocks(c.rows[0], d), kThreads, 0, s>>>(a.store_geo, c);
+    else
+        copy_kernel<64><<<blocks(c.rows[0], d), kThreads, 0, s>>>(a.store_geo, c);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_window_bwd_before(const WindowArgs& a, const WindowBwdPlan& p, const WindowCopies& w, int d, cudaStream_t s)
 {
     const int padded = p.tiles * kWindowTile;
     const long long rows = (long long)a.B * a.H * padded;
-    if (d == 128)
-        before_kernel<128><<<blocks(rows, d), kThreads, 0, s>>>(a.store_geo, a.geo, a.out, a.saved_dtype == 1, a.dout, a.lse, p.lse2, p.D, p.dq, padded, rows);
-    else
-        before_kernel<64><<<blocks(rows, d), kThreads, 0, s>>>(a.store_geo, a.geo, a.out, a.saved_dtype == 1, a.dout, a.lse, p.lse2, p.D, p.dq, padded, rows);
+    const Copies c = copies_of(a, w);
+    const auto kernel = d == 128 ? (w.dout ? before_kernel<128, true> : before_kernel<128, false>)
+                                 : (w.dout ? before_kernel<64, true> : before_kernel<64, false>);
+    kernel<<<blocks(rows, d), kThreads, 0, s>>>(a.store_geo, a.out, a.saved_dtype == 1, a.dout, static_cast<uint4*>(w.dout), a.lse, p.lse2, p.D,
+                                                p.dq, padded, rows, c);
     return cudaGetLastError();
 }
 
@@ -205,16 +269,6 @@ cudaError_t launch_window_bwd_after(const WindowArgs& a, const WindowBwdPlan& p,
         sinks_kernel<128><<<blocks(sinks, d), kThreads, 0, s>>>(a.store_geo, a.band, p.part, a.dk, a.dv, bf16, p.sink_tiles, p.segs, sinks);
     else
         sinks_kernel<64><<<blocks(sinks, d), kThreads, 0, s>>>(a.store_geo, a.band, p.part, a.dk, a.dv, bf16, p.sink_tiles, p.segs, sinks);
-    return cudaGetLastError();
-}
-
-cudaError_t launch_window_gather(const Geometry& g, const void* src, void* dst, long long heads, int d, cudaStream_t s)
-{
-    const long long rows = heads * g.L;
-    if (d == 128)
-        gather_kernel<128><<<blocks(rows, d), kThreads, 0, s>>>(g, static_cast<const uint4*>(src), static_cast<uint4*>(dst), rows);
-    else
-        gather_kernel<64><<<blocks(rows, d), kThreads, 0, s>>>(g, static_cast<const uint4*>(src), static_cast<uint4*>(dst), rows);
     return cudaGetLastError();
 }
 

@@ -94,7 +94,7 @@ struct BwdArgs {
     Band band;
     int G, T;          // query heads of a kv head; tiles of the sequence
     int sink_tiles, segs;  // tiles that hold sinks; segments of each of them (1: none is cut)
-    long long sink_items, items;
+    unsigned sink_items, items;
     const float* lse2;  // -lse log2(e), [B H][T 128]
     const float* Dv;    // [B H][T 128]
     float* dq_acc;      // [B H][T 128][d]
@@ -115,19 +115,18 @@ struct KvUnit {
 };
 
 // Items: the segments of the sinks' tiles, then the other tiles.
-__device__ __forceinline__ KvUnit unit_of(const BwdArgs& a, long long item)
+__device__ __forceinline__ KvUnit unit_of(const BwdArgs& a, unsigned item)
 {
     KvUnit u;
     const bool sink = item < a.sink_items;
     int tile, seg = 0;
     if (sink) {
-        const int per = a.sink_tiles * a.segs, x = (int)(item % per);
+        const unsigned per = (unsigned)(a.sink_tiles * a.segs), x = item % per;
         u.zk = (int)(item / per);
-        tile = x / a.segs;
-        seg = x % a.segs;
+        tile = (int)(x / (unsigned)a.segs);
+        seg = (int)(x % (unsigned)a.segs);
     } else {
-        const int per = a.T - a.sink_tiles;
-        const long long x = item - a.sink_items;
+        const unsigned per = (unsigned)(a.T - a.sink_tiles), x = item - a.sink_items;
         u.zk = (int)(x / per);
         tile = a.sink_tiles + (int)(x % per);
     }
@@ -138,7 +137,7 @@ __device__ __forceinline__ KvUnit unit_of(const BwdArgs& a, long long item)
     u.t0 = r.first + from;
     u.nt = to - from;
     u.ntiles = u.nt * a.G;
-    u.slot = sink && a.segs > 1 ? item : -1;
+    u.slot = sink && a.segs > 1 ? (long long)item : -1LL;
     return u;
 }
 
@@ -259,7 +258,7 @@ __device__ __forceinline__ void math_role(const BwdArgs& a, uint32_t sbase, uint
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     auto bar = [&](int i) { return sbase + kSmemBar + 8u * (uint32_t)i; };
     uint32_t gt = 0, uc = 0;
-    for (long long item = blockIdx.x; item < a.items; item += gridDim.x) {
+    for (unsigned item = blockIdx.x; item < a.items; item += gridDim.x) {
         {
             const KvUnit u = unit_of(a, item);
             if (u.ntiles == 0) continue;
@@ -353,12 +352,13 @@ __device__ __forceinline__ void red_add_f32(float* addr, float v)
     asm volatile("red.global.add.f32 [%0], %1;" ::"l"(addr), "f"(v) : "memory");
 }
 
-// The reductions go out in 16 groups of 8 per thread with an 80 ns pause between groups: issued at
-// once they fill the SM's memory-instruction queue, and every other warp's shared-memory and
-// barrier traffic then waits behind them (64K training backward: ~78 ms unpaced, ~71 paced).
-// Pauses of 80-115 ns per group all give the same time; from ~130 ns on, the reductions fall
-// behind the tiles (90 ms and worse), so 80 ns keeps a wide margin on boxes that run the tiles
-// faster.  A tile whose successor is already waiting goes out without pauses.
+// The reductions go out in 16 groups of 8 per thread with a pause between groups: issued at once they fill the SM's
+// memory-instruction queue, and every other warp's shared-memory and barrier traffic waits behind them (64K tokens, window
+// 4096: 9.44 ms without pauses, 9.16 with 60 ns, 8.93 with 80, 8.84 with 100 and 40 where the next tile is already
+// waiting; at d = 64 80 and none then are better: 16K tokens, 512 on both sides 530 us in place of 540).
+// They are what bounds the kernel: without them it takes 6.95.  Bulk reductions out of shared memory (16 KB at a time) took
+// 8.54 there, but need dO's second stage for their room (8.14 without the reductions themselves) and made head dim 64 a
+// fifth slower (530 -> 652 us), since the products' operands take most of what shared memory serves.
 __device__ __forceinline__ void red_group(float* dst, const uint32_t (&x)[64], int c0, uint32_t gap_ns)
 {
 #pragma unroll
@@ -377,7 +377,7 @@ __device__ __forceinline__ void dq_role(const BwdArgs& a, uint32_t sbase, uint32
     const uint32_t dq_c0 = kD64 && (warp & 3) >= 2 ? 64u : 0u;  // d = 64: this warp's query columns
     auto bar = [&](int i) { return sbase + kSmemBar + 8u * (uint32_t)i; };
     uint32_t gt = 0;
-    for (long long item = blockIdx.x; item < a.items; item += gridDim.x) {
+    for (unsigned item = blockIdx.x; item < a.items; item += gridDim.x) {
         {
             const KvUnit u = unit_of(a, item);
             if (u.ntiles == 0) continue;
@@ -386,7 +386,7 @@ __device__ __forceinline__ void dq_role(const BwdArgs& a, uint32_t sbase, uint32
                 int hh, q0;
                 walk.next(u, hh, q0);
                 const bool behind = __shfl_sync(0xffffffffu, mbar_test_wait(bar(BAR_DQ_FULL), gt & 1), 0) != 0;
-                const uint32_t gap_ns = behind ? 0u : 80u;
+                const uint32_t gap_ns = kD64 ? (behind ? 0u : 80u) : (behind ? 40u : 100u);
                 if (!mbar_wait(bar(BAR_DQ_FULL), gt & 1, ctl)) return;
                 tc_fence_after_sync();
                 __syncwarp();
@@ -440,7 +440,7 @@ __device__ __forceinline__ void producer_role(const BwdArgs& a, uint32_t sbase, 
     tma_prefetch_desc(tmDO);
     uint32_t uc = 0, qc = 0, nq = 0, nd = 0;  // units, query tiles; loads sent of Q and dO
     bool ok = true;
-    for (long long item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
+    for (unsigned item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
         const KvUnit u = unit_of(a, item);
         if (u.ntiles == 0) continue;
         if (uc > 0 && !mbar_wait(bar(BAR_KV_EMPTY), (uc - 1) & 1, ctl)) break;
@@ -576,7 +576,7 @@ __device__ __forceinline__ void mma_role(const BwdArgs& a, uint32_t sbase, uint3
     const uint32_t lead = elect();
     tmem = __shfl_sync(0xffffffffu, tmem, 0);
     const BwdDesc dsc = make_desc(sbase);
-    for (long long item = blockIdx.x; item < a.items; item += gridDim.x) {
+    for (unsigned item = blockIdx.x; item < a.items; item += gridDim.x) {
         {
             const KvUnit u = unit_of(a, item);
             if (u.ntiles == 0) continue;
@@ -719,8 +719,8 @@ cudaError_t RA_WIN_BWD_LAUNCH(const WindowArgs& w, const WindowBwdPlan& p, unsig
     a.T = p.tiles;
     a.sink_tiles = p.sink_tiles;
     a.segs = p.segs;
-    a.sink_items = p.sink_items;
-    a.items = p.sink_items + (long long)w.B * w.Hkv * (p.tiles - p.sink_tiles);
+    a.sink_items = (unsigned)p.sink_items;  // (below 2^31: the call's check)
+    a.items = (unsigned)(p.sink_items + (long long)w.B * w.Hkv * (p.tiles - p.sink_tiles));
     a.lse2 = p.lse2;
     a.Dv = p.D;
     a.dq_acc = p.dq;

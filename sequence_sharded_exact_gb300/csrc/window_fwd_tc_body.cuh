@@ -70,7 +70,7 @@ struct FwdArgs {
     int pair;         // 1: a unit is two heads at 128 positions; 0: 256 positions of one head
     int blocks;       // blocks of 128 or 256 positions
     int rows;         // heads, or pairs of them, of a kv head
-    long long units;  // B * Hkv * blocks * rows
+    unsigned units;   // B * Hkv * blocks * rows
     const __nv_bfloat16 *q, *k, *v;
     void* out;
     float* lse;
@@ -86,14 +86,13 @@ struct Unit {
     TileRun run;   // key tiles
 };
 
-__device__ __forceinline__ Unit unit_of(const FwdArgs& a, long long item)
+__device__ __forceinline__ Unit unit_of(const FwdArgs& a, unsigned item)
 {
     Unit u;
-    const int row = (int)(item % a.rows);
-    long long rest = item / a.rows;
-    const int blk = (int)(rest % a.blocks);
-    u.zk = (int)(rest / a.blocks);
-    u.zq = u.zk * a.G + row * (a.pair ? 2 : 1);
+    const unsigned rest = item / (unsigned)a.rows, row = item - rest * (unsigned)a.rows;
+    u.zk = (int)(rest / (unsigned)a.blocks);
+    const int blk = (int)(rest - (unsigned)u.zk * (unsigned)a.blocks);
+    u.zq = u.zk * a.G + (int)row * (a.pair ? 2 : 1);
     u.zq1 = a.pair ? u.zq + 1 : u.zq;
     u.p = blk * (a.pair ? kTile : 2 * kTile);
     u.p1 = a.pair ? u.p : u.p + kTile;
@@ -120,7 +119,7 @@ __device__ __forceinline__ void store32(void* p, bool wide, const uint32_t* v)
 // ------------------------------------------------------------------------------------------------
 // The row at position p, whose output came out with elements that are not finite: those that it gets from the keys that it
 // sees stay (their sum takes the element's place), the others are computed from these keys alone.
-__device__ __noinline__ void mend_row(const FwdArgs& a, long long item, long long zq, int p, long long row_g, float lse)
+__device__ __noinline__ void mend_row(const FwdArgs& a, unsigned item, long long zq, int p, long long row_g, float lse)
 {
     const Unit u = unit_of(a, item);
     if (!(fabsf(lse) <= 3.4028234e38f)) return;  // so are its scores
@@ -274,7 +273,7 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, uint32_t sbase, u
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
     uint32_t tcount = 0, ucount = 0;
 
-    for (long long item = blockIdx.x; item < a.units; item += gridDim.x, ++ucount) {
+    for (unsigned item = blockIdx.x; item < a.units; item += gridDim.x, ++ucount) {
         const Unit u = unit_of(a, item);
         const int q0 = w ? u.p1 : u.p, p = q0 + rw, ntiles = u.run.count();
         Sums row;
@@ -339,7 +338,7 @@ __device__ __forceinline__ void load_role(const FwdArgs& a, uint32_t sbase, cons
     tma_prefetch_desc(tmV);
     uint32_t kc = 0, qc = 0, nk = 0, nv = 0;  // tiles; loads sent of Q, K and V
     bool ok = true;
-    for (long long item = blockIdx.x; ok && item < a.units; item += gridDim.x) {
+    for (unsigned item = blockIdx.x; ok && item < a.units; item += gridDim.x) {
         const Unit u = unit_of(a, item);
         if (qc > 0 && !mbar_wait(bar(BAR_Q_EMPTY), (qc - 1) & 1, ctl)) break;
         mbar_arrive_expect_tx(bar(BAR_Q_FULL), 2 * kTileBytes);
@@ -417,7 +416,7 @@ __device__ __forceinline__ void mma_role(const FwdArgs& a, uint32_t sbase, uint3
     dsc.q = sdesc_sw128_lo(sbase + kSmemQ, 16);
     dsc.k = sdesc_sw128_lo(sbase + kSmemK, 16);
     dsc.v = sdesc_sw128_lo(sbase + kSmemV, kHalfBytes);
-    long long item = blockIdx.x;
+    unsigned item = blockIdx.x;
     uint32_t kc = 0, qc = 0;
     int jj = 0, ntiles = unit_of(a, item).run.count();
     if (!warp_wait(bar(BAR_Q_FULL), 0, ctl)) goto drain;
@@ -539,7 +538,7 @@ cudaError_t RA_WIN_FWD_LAUNCH(const WindowArgs& w, unsigned int* status, cudaStr
     const int block = a.pair ? kTile : 2 * kTile;
     a.blocks = (w.band.L + block - 1) / block;
     a.rows = a.pair ? w.G / 2 : w.G;
-    a.units = (long long)w.B * w.Hkv * a.blocks * a.rows;
+    a.units = (unsigned)((long long)w.B * w.Hkv * a.blocks * a.rows);  // below 2^30: the call's check
     a.q = static_cast<const __nv_bfloat16*>(w.q);
     a.k = static_cast<const __nv_bfloat16*>(w.k);
     a.v = static_cast<const __nv_bfloat16*>(w.v);
