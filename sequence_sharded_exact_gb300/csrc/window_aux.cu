@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kThreads) before_kernel(const Geometry g, cons
 {
     constexpr int kLanes = D / 8;
     const int c = threadIdx.x % kLanes * 8;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long x0 = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes, step = (long long)gridDim.x * (kThreads / kLanes);
     const long long up = (rows + 31) / 32 * 32;
     for (long long x = x0; x < up; x += step) {
@@ -138,44 +139,46 @@ __global__ void __launch_bounds__(kThreads) before_kernel(const Geometry g, cons
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) dq_kernel(const Geometry g, const float* acc, void* dq, bool bf16, long long rows, int padded)
+// dQ's rows, in the buffers' order, and behind them dK and dV of the sinks' tiles: segments [2][128][D] added in order.
+struct After {
+    Geometry g;
+    Band band;
+    const float *acc, *part;
+    void *dq, *dk, *dv;
+    int bf16, padded, sink_tiles, segs;
+    long long rows, sink_rows;
+};
+template <int D, bool kSinks>
+__global__ void __launch_bounds__(kThreads) after_kernel(const After a)
 {
     constexpr int kLanes = D / 8;
     const int c = threadIdx.x % kLanes * 8;
-    const long long step = (long long)gridDim.x * (kThreads / kLanes);
-    for (long long x = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes; x < rows; x += step) {
-        const int z = (int)(x / g.L), r = (int)(x - (long long)z * g.L);  // the buffers' rows in their order
+    const long long x0 = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes, step = (long long)gridDim.x * (kThreads / kLanes);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for the backward's sums
+    for (long long x = x0; x < a.rows; x += step) {
+        const int z = (int)(x / a.g.L), r = (int)(x - (long long)z * a.g.L);
         float f[8];
-        load8(acc, ((long long)z * padded + natural_position(g, r)) * D + c, false, f);
-        store8(dq, x * D + c, bf16, f);
+        load8(a.acc, ((long long)z * a.padded + natural_position(a.g, r)) * D + c, false, f);
+        store8(a.dq, x * D + c, a.bf16, f);
     }
-}
-
-// dK and dV of the sinks' tiles: segments [2][128][D] added in order.
-template <int D>
-__global__ void __launch_bounds__(kThreads) sinks_kernel(const Geometry g, const Band band, const float* part, void* dk, void* dv, bool bf16,
-                                                         int sink_tiles, int segs, long long rows)
-{
-    constexpr int kLanes = D / 8;
-    const int c = threadIdx.x % kLanes * 8;
-    const long long step = (long long)gridDim.x * (kThreads / kLanes);
-    for (long long x = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes; x < rows; x += step) {
-        const int r = (int)(x % kWindowTile), which = (int)(x / kWindowTile % 2);
-        const long long rest = x / (2 * kWindowTile);
-        const int tile = (int)(rest % sink_tiles), z = (int)(rest / sink_tiles), p = tile * kWindowTile + r;
-        if (p >= g.L) continue;
-        const QueryRun q = query_tiles(band, tile * kWindowTile, kWindowTile, kWindowTile);
-        const int n = q.last - q.first;
-        float sum[8] = {};
-        for (int s = 0; s < segs; ++s) {
-            if ((long long)n * s / segs == (long long)n * (s + 1) / segs) continue;  // an empty segment leaves nothing
-            float f[8];
-            load8(part, ((((long long)z * sink_tiles + tile) * segs + s) * 2 * kWindowTile + which * kWindowTile + r) * D + c, false, f);
+    if constexpr (kSinks) {
+        for (long long x = x0; x < a.sink_rows; x += step) {
+            const int r = (int)(x % kWindowTile), which = (int)(x / kWindowTile % 2);
+            const long long rest = x / (2 * kWindowTile);
+            const int tile = (int)(rest % a.sink_tiles), z = (int)(rest / a.sink_tiles), p = tile * kWindowTile + r;
+            if (p >= a.g.L) continue;
+            const QueryRun q = query_tiles(a.band, tile * kWindowTile, kWindowTile, kWindowTile);
+            const int n = q.last - q.first;
+            float sum[8] = {};
+            for (int s = 0; s < a.segs; ++s) {
+                if ((long long)n * s / a.segs == (long long)n * (s + 1) / a.segs) continue;  // an empty segment leaves nothing
+                float f[8];
+                load8(a.part, ((((long long)z * a.sink_tiles + tile) * a.segs + s) * 2 * kWindowTile + which * kWindowTile + r) * D + c, false, f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += f[e];
+                for (int e = 0; e < 8; ++e) sum[e] += f[e];
+            }
+            store8(which ? a.dv : a.dk, ((long long)z * a.g.L + buffer_row(a.g, p)) * D + c, a.bf16, sum);
         }
-        store8(which ? dv : dk, ((long long)z * g.L + buffer_row(g, p)) * D + c, bf16, sum);
     }
 }
 
@@ -205,6 +208,7 @@ WindowBwdPlan window_bwd_plan(const Band& b, int B, int H, int Hkv, int d)
         p.sink_items = (long long)B * Hkv * p.sink_tiles * p.segs;
     }
     const size_t rows = (size_t)B * H * p.tiles * kWindowTile;
+    p.early = rows * d * sizeof(float) <= (size_t)128 << 20;
     p.lse_at = 0;
     p.D_at = p.lse_at + up256(rows * sizeof(float));
     p.dq_at = p.D_at + up256(rows * sizeof(float));
@@ -253,23 +257,25 @@ cudaError_t launch_window_bwd_before(const WindowArgs& a, const WindowBwdPlan& p
     return cudaGetLastError();
 }
 
-cudaError_t launch_window_bwd_after(const WindowArgs& a, const WindowBwdPlan& p, int d, cudaStream_t s)
+cudaError_t launch_window_bwd_after(const WindowArgs& w, const WindowBwdPlan& p, int d, cudaStream_t s)
 {
-    const long long rows = (long long)a.B * a.H * a.band.L;
-    const bool bf16 = a.grad_dtype == 1;
-    const int padded = p.tiles * kWindowTile;
-    if (d == 128)
-        dq_kernel<128><<<blocks(rows, d), kThreads, 0, s>>>(a.store_geo, p.dq, a.dq, bf16, rows, padded);
-    else
-        dq_kernel<64><<<blocks(rows, d), kThreads, 0, s>>>(a.store_geo, p.dq, a.dq, bf16, rows, padded);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.segs == 1) return e;
-    const long long sinks = (long long)a.B * a.Hkv * p.sink_tiles * 2 * kWindowTile;
-    if (d == 128)
-        sinks_kernel<128><<<blocks(sinks, d), kThreads, 0, s>>>(a.store_geo, a.band, p.part, a.dk, a.dv, bf16, p.sink_tiles, p.segs, sinks);
-    else
-        sinks_kernel<64><<<blocks(sinks, d), kThreads, 0, s>>>(a.store_geo, a.band, p.part, a.dk, a.dv, bf16, p.sink_tiles, p.segs, sinks);
-    return cudaGetLastError();
+    After a;
+    a.g = w.store_geo;
+    a.band = w.band;
+    a.acc = p.dq;
+    a.part = p.part;
+    a.dq = w.dq;
+    a.dk = w.dk;
+    a.dv = w.dv;
+    a.bf16 = w.grad_dtype == 1;
+    a.padded = p.tiles * kWindowTile;
+    a.sink_tiles = p.sink_tiles;
+    a.segs = p.segs;
+    a.rows = (long long)w.B * w.H * w.band.L;
+    a.sink_rows = p.segs > 1 ? (long long)w.B * w.Hkv * p.sink_tiles * 2 * kWindowTile : 0;
+    const auto kernel = d == 128 ? (a.sink_rows ? after_kernel<128, true> : after_kernel<128, false>)
+                                 : (a.sink_rows ? after_kernel<64, true> : after_kernel<64, false>);
+    return launch_next(p.early, kernel, blocks(a.rows + a.sink_rows, d), kThreads, 0, s, a);
 }
 
 }  // namespace ra

@@ -672,9 +672,11 @@ window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for D, lse, the cleared dQ and the copies
     const uint32_t tmem = *tmem_slot;
     const WaitCtl ctl{abort_flag, a.status, kWaitLimitNs};
     // Register split: launched with 512 x 128 = 65536 registers; math warpgroups 2 x 128 x 144, the
@@ -736,8 +738,7 @@ cudaError_t RA_WIN_BWD_LAUNCH(const WindowArgs& w, const WindowBwdPlan& p, unsig
     const cudaError_t e = allow_smem(window_bwd_tc_kernel, (int)kSmemBytes, mu, done);
     if (e != cudaSuccess) return e;
     const long long sms = device_sm_count();
-    window_bwd_tc_kernel<<<(unsigned)(a.items < sms ? a.items : sms), kThreads, kSmemBytes, s>>>(tq, tk, tv, tdo, a);
-    return cudaGetLastError();
+    return launch_next(p.early, window_bwd_tc_kernel, (unsigned)(a.items < sms ? a.items : sms), kThreads, kSmemBytes, s, tq, tk, tv, tdo, a);
 }
 
 }  // namespace ra
