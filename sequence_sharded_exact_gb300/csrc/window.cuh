@@ -35,11 +35,19 @@ RA_HD bool band_tile_whole(const Band& b, int q0, int nq, int k0, int nk)
     return k1 < b.S || (q1 - k0 < b.W && (b.causal || k1 - q0 < b.W));
 }
 
-// The key tiles (of `tile` positions) that queries [q0, q0 + rows) meet: [0, sinks) and [first, last).
+// The key tiles (of `tile` positions) that queries [q0, q0 + rows) meet: [first, last) and [0, sinks), those inside the window
+// before the sinks' and its two ends: a maximum over a whole tile seldom has to be raised afterwards, one over the few keys
+// that a row sees of the others often.
 struct TileRun {
     int sinks, first, last;
     RA_HD int count() const { return sinks + last - first; }
-    RA_HD int at(int i) const { return i < sinks ? i : first + (i - sinks); }
+    RA_HD int at(int i) const
+    {
+        const int inside = last - first > 2 ? last - first - 2 : 0;
+        if (i < inside) return first + 1 + i;
+        i -= inside;
+        return i < sinks ? i : i == sinks ? first : last - 1;
+    }
 };
 
 RA_HD TileRun key_tiles(const Band& b, int q0, int rows, int tile)
@@ -62,8 +70,7 @@ RA_HD TileRun key_tiles(const Band& b, int q0, int rows, int tile)
     return r;
 }
 
-// The query tiles that keys [k0, k0 + rows) meet through the window, and from which of them on (causal: any; otherwise
-// those before too) they are met as sinks alone.
+// The query tiles [first, last) that keys [k0, k0 + rows) meet, through the window or as sinks.
 struct QueryRun {
     int first, last;
 };

@@ -64,11 +64,11 @@ __device__ __forceinline__ Row row_of(const Geometry& g, int padded, long long x
     return r;
 }
 
-// One row in natural order: copied from src (copies in natural order), in one launch with the others.
+// q, k and v, whose rows are copied into natural order.
 struct Copies {
     const uint4* src[3];
     uint4* dst[3];
-    long long rows[3];  // 0: no copy
+    long long rows[3];
 };
 template <int D>
 __device__ __forceinline__ void copy_rows(const Geometry& g, const uint4* src, uint4* dst, long long rows, long long x0, long long step)
