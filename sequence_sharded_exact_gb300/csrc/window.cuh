@@ -124,16 +124,23 @@ cudaError_t launch_window_fwd_tc_d64(const WindowArgs& a, unsigned int* status, 
 
 // The backward's cut and its workspace.
 constexpr int kWindowTile = 128;
+constexpr int kWindowCtas = 152;  // a round of units: the SMs of the whole GPU (with fewer the results are the same)
 struct WindowBwdPlan {
     int tiles, sink_tiles, segs;  // tiles of the sequence and with sinks; segments of each of the latter
     // The launches start while the one before them runs, where dQ's accumulator is at most 128 MB: two sequences of 1000 tokens
     // of 8 heads of 64 take 25.4 us in place of 28.2, but 64K tokens of 32 heads of 128 (1 GB) 8.92 ms in place of 8.80.
     bool early;
     long long sink_items;         // segments in all (0: no sinks)
+    // The other tiles: `whole` of them have a unit each, the `tail` behind these, which would fill a last round of CTAs in part,
+    // are cut into tail_segs units each (1: none is): 5005 tokens in 7 stripes, 368 units in 3 rounds of 152, 216 -> 203 us;
+    // 2048 tokens of 8 : 2 heads of 128, window 512, 32 units, 57 -> 32 us.
+    long long whole, tail;
+    int tail_segs;
+    long long parts() const { return (segs > 1 ? sink_items : 0) + (tail_segs > 1 ? tail * tail_segs : 0); }
     size_t lse_at, D_at, dq_at, part_at, bytes;
     float *lse2, *D, *dq, *part;
 };
-WindowBwdPlan window_bwd_plan(const Band& b, int B, int H, int Hkv, int d);
+WindowBwdPlan window_bwd_plan(const Band& b, int B, int H, int Hkv, int d);  // (no CUDA call)
 cudaError_t launch_window_bwd_tc_d128(const WindowArgs& a, const WindowBwdPlan& p, unsigned int* status, cudaStream_t s);
 cudaError_t launch_window_bwd_tc_d64(const WindowArgs& a, const WindowBwdPlan& p, unsigned int* status, cudaStream_t s);
 // Copies in natural order, where TMA cannot read the inputs so (dout null: none, but for the forward's).

@@ -2,7 +2,8 @@
 //
 // Before the backward: D = dout . out per row, lse in log2 units and the float32 accumulator of dQ cleared, all in natural
 // order and padded to whole tiles of 128 positions (rows behind the sequence: -lse2 = -infinity, which makes their P 0).
-// After it: dQ from the accumulator to the layout's rows, and the sinks' dK and dV, added over their segments in order.
+// After it: dQ from the accumulator to the layout's rows, and dK and dV of the tiles that were cut, added over their segments in
+// order.
 // Layouts that TMA cannot read in natural order with one box (window_tc.cuh) are copied into it first, in the same launch.
 // A group of d / 8 lanes has a row, 8 elements (16 bytes of bf16) each.
 #include <cuda_bf16.h>
@@ -139,16 +140,17 @@ __global__ void __launch_bounds__(kThreads) before_kernel(const Geometry g, cons
     }
 }
 
-// dQ's rows, in the buffers' order, and behind them dK and dV of the sinks' tiles: segments [2][128][D] added in order.
+// dQ's rows, in the buffers' order, and behind them dK and dV of the tiles that were cut: segments [2][128][D] added in order.
 struct After {
     Geometry g;
     Band band;
     const float *acc, *part;
     void *dq, *dk, *dv;
-    int bf16, padded, sink_tiles, segs;
-    long long rows, sink_rows;
+    int bf16, padded, sink_tiles, segs, tiles, G, tail_segs;
+    long long rows, cut_rows;        // of dQ; of dK and dV, 2 * 128 for each tile that was cut
+    long long sink_cut, whole;       // the sinks' tiles of all heads, if they were; then those behind the first `whole` others
 };
-template <int D, bool kSinks>
+template <int D, bool kCut>
 __global__ void __launch_bounds__(kThreads) after_kernel(const After a)
 {
     constexpr int kLanes = D / 8;
@@ -161,19 +163,33 @@ __global__ void __launch_bounds__(kThreads) after_kernel(const After a)
         load8(a.acc, ((long long)z * a.padded + natural_position(a.g, r)) * D + c, false, f);
         store8(a.dq, x * D + c, a.bf16, f);
     }
-    if constexpr (kSinks) {
-        for (long long x = x0; x < a.sink_rows; x += step) {
+    if constexpr (kCut) {
+        for (long long x = x0; x < a.cut_rows; x += step) {
             const int r = (int)(x % kWindowTile), which = (int)(x / kWindowTile % 2);
-            const long long rest = x / (2 * kWindowTile);
-            const int tile = (int)(rest % a.sink_tiles), z = (int)(rest / a.sink_tiles), p = tile * kWindowTile + r;
+            const long long at = x / (2 * kWindowTile), item = at < a.sink_cut ? at : at - a.sink_cut;
+            long long slot;
+            int z, tile, segs;
+            if (at < a.sink_cut) {
+                z = (int)(item / a.sink_tiles);
+                tile = (int)(item % a.sink_tiles);
+                segs = a.segs;
+                slot = item * segs;
+            } else {
+                const int per = a.tiles - a.sink_tiles;
+                z = (int)((a.whole + item) / per);
+                tile = a.sink_tiles + (int)((a.whole + item) % per);
+                segs = a.tail_segs;
+                slot = a.sink_cut * a.segs + item * segs;
+            }
+            const int p = tile * kWindowTile + r;
             if (p >= a.g.L) continue;
             const QueryRun q = query_tiles(a.band, tile * kWindowTile, kWindowTile, kWindowTile);
-            const int n = q.last - q.first;
+            const long long n = (long long)(q.last - q.first) * (at < a.sink_cut ? 1 : a.G);
             float sum[8] = {};
-            for (int s = 0; s < a.segs; ++s) {
-                if ((long long)n * s / a.segs == (long long)n * (s + 1) / a.segs) continue;  // an empty segment leaves nothing
+            for (int s = 0; s < segs; ++s) {
+                if (n * s / segs == n * (s + 1) / segs) continue;  // an empty segment leaves nothing
                 float f[8];
-                load8(a.part, ((((long long)z * a.sink_tiles + tile) * a.segs + s) * 2 * kWindowTile + which * kWindowTile + r) * D + c, false, f);
+                load8(a.part, (((slot + s) * 2 + which) * kWindowTile + r) * D + c, false, f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum[e] += f[e];
             }
@@ -190,6 +206,11 @@ unsigned blocks(long long rows, int d)
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// Units of a tile of the last round, and pairs of tiles that each has at least.  (Two sequences of 1000 tokens, units of 8 pairs:
+// 25.2 us uncut, 26.2 cut in two, 27.4 in four.)  Of all units the kernel with them costs up to 1 us, a pair takes 1.35: no cut
+// where the rounds are more than half the pairs of a unit.
+constexpr int kTailSegs = 4, kTailRun = 5;
+
 }  // namespace
 
 WindowBwdPlan window_bwd_plan(const Band& b, int B, int H, int Hkv, int d)
@@ -197,23 +218,33 @@ WindowBwdPlan window_bwd_plan(const Band& b, int B, int H, int Hkv, int d)
     WindowBwdPlan p = {};
     p.tiles = (b.L + kWindowTile - 1) / kWindowTile;
     p.sink_tiles = (b.S + kWindowTile - 1) / kWindowTile;
-    p.segs = 1;
+    p.segs = p.tail_segs = 1;
+    const long long near = ((long long)b.W + kWindowTile - 1) / kWindowTile + 1, unit = b.causal ? near : 2 * near - 1;  // query tiles
     if (p.sink_tiles > 0) {
         // segments about as long as the other units, but no more than a few for every SM of any GPU in all
-        const long long near = ((long long)b.W + kWindowTile - 1) / kWindowTile + 1, unit = b.causal ? near : 2 * near - 1;
         const long long most = 640 / ((long long)B * Hkv * p.sink_tiles);
         long long segs = (p.tiles + unit - 1) / unit;
         if (segs > most) segs = most;
         p.segs = segs < 1 ? 1 : (int)segs;
         p.sink_items = (long long)B * Hkv * p.sink_tiles * p.segs;
     }
+    p.whole = (long long)B * Hkv * (p.tiles - p.sink_tiles);
+    const long long last = (p.sink_items + p.whole) % kWindowCtas, cut = last < p.whole ? last : p.whole;
+    const long long run = (unit < p.tiles ? unit : p.tiles) * (H / Hkv);  // pairs of tiles of a unit
+    if (cut > 0 && 2 * ((p.sink_items + p.whole) / kWindowCtas) <= run) {
+        const long long room = (kWindowCtas - (last - cut)) / cut, most = run / kTailRun;
+        const long long segs = room < most ? room : most;
+        p.tail_segs = segs < 1 ? 1 : segs > kTailSegs ? kTailSegs : (int)segs;
+    }
+    p.tail = p.tail_segs > 1 ? cut : 0;
+    p.whole -= p.tail;
     const size_t rows = (size_t)B * H * p.tiles * kWindowTile;
     p.early = rows * d * sizeof(float) <= (size_t)128 << 20;
     p.lse_at = 0;
     p.D_at = p.lse_at + up256(rows * sizeof(float));
     p.dq_at = p.D_at + up256(rows * sizeof(float));
     p.part_at = p.dq_at + up256(rows * d * sizeof(float));
-    p.bytes = p.part_at + (p.segs > 1 ? up256((size_t)p.sink_items * 2 * kWindowTile * d * sizeof(float)) : 0);
+    p.bytes = p.part_at + up256((size_t)p.parts() * 2 * kWindowTile * d * sizeof(float));
     return p;
 }
 
@@ -271,11 +302,16 @@ cudaError_t launch_window_bwd_after(const WindowArgs& w, const WindowBwdPlan& p,
     a.padded = p.tiles * kWindowTile;
     a.sink_tiles = p.sink_tiles;
     a.segs = p.segs;
+    a.tiles = p.tiles;
+    a.G = w.G;
+    a.tail_segs = p.tail_segs;
     a.rows = (long long)w.B * w.H * w.band.L;
-    a.sink_rows = p.segs > 1 ? (long long)w.B * w.Hkv * p.sink_tiles * 2 * kWindowTile : 0;
-    const auto kernel = d == 128 ? (a.sink_rows ? after_kernel<128, true> : after_kernel<128, false>)
-                                 : (a.sink_rows ? after_kernel<64, true> : after_kernel<64, false>);
-    return launch_next(p.early, kernel, blocks(a.rows + a.sink_rows, d), kThreads, 0, s, a);
+    a.sink_cut = p.segs > 1 ? (long long)w.B * w.Hkv * p.sink_tiles : 0;
+    a.whole = p.whole;
+    a.cut_rows = (a.sink_cut + p.tail) * 2 * kWindowTile;
+    const auto kernel = d == 128 ? (a.cut_rows ? after_kernel<128, true> : after_kernel<128, false>)
+                                 : (a.cut_rows ? after_kernel<64, true> : after_kernel<64, false>);
+    return launch_next(p.early, kernel, blocks(a.rows + a.cut_rows, d), kThreads, 0, s, a);
 }
 
 }  // namespace ra

@@ -8,7 +8,7 @@
 // head: W / 128 + 1 of them, so that units are alike in every layout (the tiles are runs of natural positions).  A tile with
 // sinks is seen by all (later) queries: it is cut into segments about as long as the other units, taken first, each of which
 // leaves its dK and dV in the workspace; a last kernel adds them in order.  Without that one CTA would walk the whole
-// sequence for them.
+// sequence for them.  The tiles of a last round that would leave half of the SMs idle are cut likewise.
 //   * warp 12: TMA loads of the unit's K and V and, through 2 stages, of each query tile's Q (with its lse) and dO (with its
 //     D); the vectors, in natural order and padded to whole tiles (lse with +infinity: those rows' P is 0), by bulk copy.
 //   * warp 13: tcgen05.mma issue, per query tile t: dV += P^T_t dO_t (P^T from TMEM), S^T_{t+1} = K Q_{t+1}^T, dQ^T_t = K^T
@@ -95,12 +95,14 @@ struct BwdArgs {
     int G, T;          // query heads of a kv head; tiles of the sequence
     int sink_tiles, segs;  // tiles that hold sinks; segments of each of them (1: none is cut)
     unsigned sink_items, items;
+    unsigned whole;    // of the other tiles, those with a unit of their own; the rest have tail_segs
+    int tail_segs;
     const float* lse2;  // -lse log2(e), [B H][T 128]
     const float* Dv;    // [B H][T 128]
     float* dq_acc;      // [B H][T 128][d]
     void* dk;
     void* dv;
-    float* part;        // [sink items][2][128][d]: dK, dV of the segments
+    float* part;        // [segments][2][128][d]: their dK, dV
     int grad_bf16;
     unsigned int* status;
     float scale, scale_log2;
@@ -110,23 +112,31 @@ struct KvUnit {
     int zk;         // b * Hkv + kv head
     int k0;         // first key's position
     int t0, nt;     // query tiles [t0, t0 + nt) of every head
-    int ntiles;     // G * nt
+    int from;       // kTail: the unit's first of these G * nt, head by head
+    int ntiles;     // and how many it has (otherwise all)
     long long slot; // segment's place in `part`, or -1
 };
 
-// Items: the segments of the sinks' tiles, then the other tiles.
+// Items: the segments of the sinks' tiles, then the other tiles, and (kTail) the segments of those of the last round.
+// (A kernel without these is compiled apart: their code in it costs a unit 0.5 to 1 us.)
+template <bool kTail>
 __device__ __forceinline__ KvUnit unit_of(const BwdArgs& a, unsigned item)
 {
     KvUnit u;
     const bool sink = item < a.sink_items;
-    int tile, seg = 0;
+    int tile, seg = 0, cut = 0;
     if (sink) {
         const unsigned per = (unsigned)(a.sink_tiles * a.segs), x = item % per;
         u.zk = (int)(item / per);
         tile = (int)(x / (unsigned)a.segs);
         seg = (int)(x % (unsigned)a.segs);
     } else {
-        const unsigned per = (unsigned)(a.T - a.sink_tiles), x = item - a.sink_items;
+        const unsigned per = (unsigned)(a.T - a.sink_tiles);
+        unsigned x = item - a.sink_items;
+        if (kTail && x >= a.whole) {
+            cut = 1 + (int)((x - a.whole) % (unsigned)a.tail_segs);
+            x = a.whole + (x - a.whole) / (unsigned)a.tail_segs;
+        }
         u.zk = (int)(x / per);
         tile = a.sink_tiles + (int)(x % per);
     }
@@ -136,14 +146,29 @@ __device__ __forceinline__ KvUnit unit_of(const BwdArgs& a, unsigned item)
     const int from = (int)((long long)n * seg / segs), to = (int)((long long)n * (seg + 1) / segs);
     u.t0 = r.first + from;
     u.nt = to - from;
+    u.from = 0;
     u.ntiles = u.nt * a.G;
     u.slot = sink && a.segs > 1 ? (long long)item : -1LL;
+    if (kTail && cut) {
+        const long long all = u.ntiles;
+        u.from = (int)(all * (cut - 1) / a.tail_segs);
+        u.ntiles = (int)(all * cut / a.tail_segs) - u.from;
+        u.slot = (a.segs > 1 ? (long long)a.sink_items : 0) + (item - a.sink_items - a.whole);
+    }
     return u;
 }
 
 // The t-th query tile of a unit: head within the group, and first position.
+template <bool kTail>
 struct QWalk {
     int hh = 0, t = 0;
+    __device__ __forceinline__ explicit QWalk(const KvUnit& u)
+    {
+        if (kTail && u.from > 0) {
+            hh = u.from / u.nt;
+            t = u.from % u.nt;
+        }
+    }
     __device__ __forceinline__ void next(const KvUnit& u, int& head, int& q0)
     {
         head = hh;
@@ -250,6 +275,7 @@ __device__ __forceinline__ void phase_b(const BwdArgs& a, uint32_t sbase, uint32
 }
 
 // Per query tile t the warpgroups run phase A then phase B; dQ^T is the dQ warps' business.
+template <bool kTail>
 __device__ __forceinline__ void math_role(const BwdArgs& a, uint32_t sbase, uint32_t tmem, const WaitCtl& ctl)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -260,9 +286,9 @@ __device__ __forceinline__ void math_role(const BwdArgs& a, uint32_t sbase, uint
     uint32_t gt = 0, uc = 0;
     for (unsigned item = blockIdx.x; item < a.items; item += gridDim.x) {
         {
-            const KvUnit u = unit_of(a, item);
+            const KvUnit u = unit_of<kTail>(a, item);
             if (u.ntiles == 0) continue;
-            QWalk walk;
+            QWalk<kTail> walk(u);
             for (int t = 0; t < u.ntiles; ++t, ++gt) {
                 int hh, q0;
                 walk.next(u, hh, q0);
@@ -369,6 +395,7 @@ __device__ __forceinline__ void red_group(float* dst, const uint32_t (&x)[64], i
     }
 }
 
+template <bool kTail>
 __device__ __forceinline__ void dq_role(const BwdArgs& a, uint32_t sbase, uint32_t tmem, const WaitCtl& ctl)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -379,9 +406,9 @@ __device__ __forceinline__ void dq_role(const BwdArgs& a, uint32_t sbase, uint32
     uint32_t gt = 0;
     for (unsigned item = blockIdx.x; item < a.items; item += gridDim.x) {
         {
-            const KvUnit u = unit_of(a, item);
+            const KvUnit u = unit_of<kTail>(a, item);
             if (u.ntiles == 0) continue;
-            QWalk walk;
+            QWalk<kTail> walk(u);
             for (int t = 0; t < u.ntiles; ++t, ++gt) {
                 int hh, q0;
                 walk.next(u, hh, q0);
@@ -429,6 +456,7 @@ __device__ __forceinline__ void dq_role(const BwdArgs& a, uint32_t sbase, uint32
 // ------------------------------------------------------------------------------------------------
 // TMA producer (one thread)
 // ------------------------------------------------------------------------------------------------
+template <bool kTail>
 __device__ __forceinline__ void producer_role(const BwdArgs& a, uint32_t sbase, const CUtensorMap* tmQ,
                                               const CUtensorMap* tmK, const CUtensorMap* tmV,
                                               const CUtensorMap* tmDO, const WaitCtl& ctl)
@@ -441,7 +469,7 @@ __device__ __forceinline__ void producer_role(const BwdArgs& a, uint32_t sbase, 
     uint32_t uc = 0, qc = 0, nq = 0, nd = 0;  // units, query tiles; loads sent of Q and dO
     bool ok = true;
     for (unsigned item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
-        const KvUnit u = unit_of(a, item);
+        const KvUnit u = unit_of<kTail>(a, item);
         if (u.ntiles == 0) continue;
         if (uc > 0 && !mbar_wait(bar(BAR_KV_EMPTY), (uc - 1) & 1, ctl)) break;
         const int krow = window_tma_row(a.geo, u.k0);
@@ -453,7 +481,7 @@ __device__ __forceinline__ void producer_role(const BwdArgs& a, uint32_t sbase, 
         }
         if constexpr (kD64) tma_load_4d(sbase + kSmemK + kTileBytes, tmK, bar(BAR_KV_FULL), 0, krow, u.zk);
         ++uc;
-        QWalk walk;
+        QWalk<kTail> walk(u);
         for (int t = 0; t < u.ntiles; ++t, ++qc) {
             int hh, q0;
             walk.next(u, hh, q0);
@@ -567,6 +595,7 @@ __device__ __forceinline__ void issue_dq(uint32_t lead, uint32_t tmem, const Bwd
                kIdDQ, kk > 0);
 }
 
+template <bool kTail>
 __device__ __forceinline__ void mma_role(const BwdArgs& a, uint32_t sbase, uint32_t tmem, const WaitCtl& ctl)
 {
     auto bar = [&](int i) { return sbase + kSmemBar + 8u * (uint32_t)i; };
@@ -578,7 +607,7 @@ __device__ __forceinline__ void mma_role(const BwdArgs& a, uint32_t sbase, uint3
     const BwdDesc dsc = make_desc(sbase);
     for (unsigned item = blockIdx.x; item < a.items; item += gridDim.x) {
         {
-            const KvUnit u = unit_of(a, item);
+            const KvUnit u = unit_of<kTail>(a, item);
             if (u.ntiles == 0) continue;
             if (!warp_wait(bar(BAR_KV_FULL), uc & 1, ctl)) goto drain;
             issued = true;
@@ -647,6 +676,7 @@ drain:
 // ------------------------------------------------------------------------------------------------
 // kernel
 // ------------------------------------------------------------------------------------------------
+template <bool kTail>
 __global__ void __launch_bounds__(kThreads, 1)
 window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO, const __grid_constant__ BwdArgs a)
@@ -689,13 +719,13 @@ window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     else
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;" ::: "memory");
     if (warp < 8) {
-        math_role(a, sbase, tmem, ctl);
+        math_role<kTail>(a, sbase, tmem, ctl);
     } else if (warp < 12) {
-        dq_role(a, sbase, tmem, ctl);
+        dq_role<kTail>(a, sbase, tmem, ctl);
     } else if (warp == 12) {
-        if ((threadIdx.x & 31) == 0) producer_role(a, sbase, &tmQ, &tmK, &tmV, &tmDO, ctl);
+        if ((threadIdx.x & 31) == 0) producer_role<kTail>(a, sbase, &tmQ, &tmK, &tmV, &tmDO, ctl);
     } else if (warp == 13) {
-        mma_role(a, sbase, tmem, ctl);
+        mma_role<kTail>(a, sbase, tmem, ctl);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -703,6 +733,18 @@ window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         tc_fence_after_sync();
         tmem_dealloc(tmem, 512);
     }
+}
+
+template <bool kTail>
+cudaError_t launch(const WindowBwdPlan& p, const BwdArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                   const CUtensorMap& tdo, cudaStream_t s)
+{
+    static std::mutex mu;
+    static bool done[64];
+    const cudaError_t e = allow_smem(window_bwd_tc_kernel<kTail>, (int)kSmemBytes, mu, done);
+    if (e != cudaSuccess) return e;
+    const long long sms = device_sm_count();
+    return launch_next(p.early, window_bwd_tc_kernel<kTail>, (unsigned)(a.items < sms ? a.items : sms), kThreads, kSmemBytes, s, tq, tk, tv, tdo, a);
 }
 
 }  // namespace
@@ -722,7 +764,9 @@ cudaError_t RA_WIN_BWD_LAUNCH(const WindowArgs& w, const WindowBwdPlan& p, unsig
     a.sink_tiles = p.sink_tiles;
     a.segs = p.segs;
     a.sink_items = (unsigned)p.sink_items;  // (below 2^31: the call's check)
-    a.items = (unsigned)(p.sink_items + (long long)w.B * w.Hkv * (p.tiles - p.sink_tiles));
+    a.whole = (unsigned)p.whole;
+    a.tail_segs = p.tail_segs;
+    a.items = (unsigned)(p.sink_items + p.whole + p.tail * p.tail_segs);
     a.lse2 = p.lse2;
     a.Dv = p.D;
     a.dq_acc = p.dq;
@@ -733,12 +777,7 @@ cudaError_t RA_WIN_BWD_LAUNCH(const WindowArgs& w, const WindowBwdPlan& p, unsig
     a.status = status;
     a.scale = w.scale;
     a.scale_log2 = w.scale_log2;
-    static std::mutex mu;
-    static bool done[64];
-    const cudaError_t e = allow_smem(window_bwd_tc_kernel, (int)kSmemBytes, mu, done);
-    if (e != cudaSuccess) return e;
-    const long long sms = device_sm_count();
-    return launch_next(p.early, window_bwd_tc_kernel, (unsigned)(a.items < sms ? a.items : sms), kThreads, kSmemBytes, s, tq, tk, tv, tdo, a);
+    return a.tail_segs > 1 ? launch<true>(p, a, tq, tk, tv, tdo, s) : launch<false>(p, a, tq, tk, tv, tdo, s);
 }
 
 }  // namespace ra

@@ -184,6 +184,23 @@ def test_a_batch_is_its_sequences(W, S):
         _same([t[b:b + 1] for t in got], ra.window_bwd(*y[:3], o, l, y[3], 4, W, S, True, "zigzag"), BF)
 
 
+@pytest.mark.parametrize("B,H,Hkv,L,d,n,layout,W,S,causal", [
+    (1, 8, 2, 640, 64, 1, "contiguous", 600, 3, True),     # one round: every tile but the sinks' in several units
+    (1, 8, 2, 640, 128, 1, "contiguous", 600, 0, True),
+    (2, 6, 2, 700, 128, 7, "striped", 300, 200, True),     # of the last tile only a part is in the sequence
+    (1, 14, 14, 1410, 64, 5, "zigzag", 1400, 0, True),     # 168 units: a whole round, and 16 in pieces
+    (1, 14, 14, 1410, 128, 1, "contiguous", 700, 100, False),
+])
+def test_backward_units_in_pieces(B, H, Hkv, L, d, n, layout, W, S, causal):
+    """Batches whose last round of units is cut."""
+    x = _inputs(B, H, Hkv, L, d, BF, seed=L + d)
+    out, lse = ra.window_fwd(*x[:3], n, W, S, causal, layout)
+    got = ra.window_bwd(*x[:3], out, lse, x[3], n, W, S, causal, layout)
+    wu.check_bwd(got, wu.bwd(*x[:3], out, lse, x[3], n, layout, W, S, causal, 2.0 ** -8))
+    again = ra.window_bwd(*x[:3], out, lse, x[3], n, W, S, causal, layout)
+    _same(again, got, BF)
+
+
 @pytest.mark.parametrize("layout,n", [("contiguous", 1), ("striped", 5)])
 @pytest.mark.parametrize("out_dtype", [BF, F32])
 def test_rows_beside_values_that_are_not_finite(out_dtype, layout, n):
