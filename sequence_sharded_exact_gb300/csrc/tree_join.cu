@@ -251,15 +251,18 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
     a.pos = t.positions;
     a.whole = 0;
     if (a.window) {  // no more CTAs than tiles that can be in reach
-        const long long reach = (long long)t.window + t.T, sinks = t.sinks < c.cap ? t.sinks : c.cap;
-        const long long most = (long long)c.B * c.Hkv * u.nrt * (reach / u.tile + 2 + (sinks + u.tile - 1) / u.tile);
-        if (a.ctas > most) a.ctas = (int)most;
-        const long long items = (long long)c.B * c.Hkv * u.nrt;
+        const long long reach = (long long)t.window + t.T < c.cap ? (long long)t.window + t.T : c.cap, sinks = t.sinks < c.cap ? t.sinks : c.cap;
+        const long long items = (long long)c.B * c.Hkv * u.nrt, tiles = reach / u.tile + 2 + (sinks + u.tile - 1) / u.tile;  // of an item
+        if (a.ctas > items * tiles) a.ctas = (int)(items * tiles);
         // With one item for most CTAs each takes one alone: an end, a start and the second launch saved count for more than
         // an even split (windows of 1024 rows: 16 sequences of 8 drafted tokens, 128 items on 152 CTAs, 30 us in place of 38
         // over e4m3, 22 in place of 31 over bf16; one token each of 32 sequences, 256 items on 304, 32 in place of 38; of 4096
-        // rows, 63 in place of 71 and 81 in place of 87).  Below half as many items as CTAs the split wins.
-        a.whole = items <= a.ctas && 2 * items > a.ctas;
+        // rows, 63 in place of 71 and 81 in place of 87).  Below half as many items as CTAs the split wins, and where the CTAs
+        // without an item would do more than 8 tiles' work for each of the others (10 sequences of 8 tokens over e4m3, 80 items on
+        // 152: 1024 rows 29 in place of 33 us, 2048 rows 40 and 39, 4096 rows 61 and 52); on the CUDA cores more than one's
+        // (1024 rows, one token each of 76 sequences, 608 items on 608: 137 in place of 148 us; of 60, 480 items, 135 and 122).
+        const long long spare = u.path == Path::kSimt ? 1 : 8;
+        a.whole = items <= a.ctas && 2 * items > a.ctas && tiles * (a.ctas - items) <= spare * a.ctas;
         if (a.whole) a.ctas = (int)items;
     }
     char* ws = static_cast<char*>(t.workspace);
