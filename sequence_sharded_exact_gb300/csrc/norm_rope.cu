@@ -19,7 +19,9 @@
 //
 // Positions with several axes (time, height, width of images and video): each pair of a head takes the position along
 // its axis, read once per group; everything else is as above.  Without weights the rotation alone, whose gradient is
-// the rotation back.
+// the rotation back.  Measured, 48K tokens of 32 + 8 heads of 128 in bf16 with three axes and the norm: forward 166 us (6.05 TB/s,
+// 0.89 of the copy rate; one position 163), backward 249 us (0.90).  The rows fetched into L2 ahead of the positions: 162 us,
+// but 61 in place of 58 at 16K tokens.
 //
 // With few tokens one group per position would leave most SMs idle, so the heads of a position are
 // then split over several groups, which repeat the angles.

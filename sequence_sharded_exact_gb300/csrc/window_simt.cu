@@ -7,6 +7,11 @@
 // Backward: blocks over query tiles for dQ, and over key tiles and query heads for dK and dV, both recompute P =
 // exp(s - lse): seven products in place of five, and no sum whose order varies.  The heads' parts of dK and dV, and the
 // segments' of the sinks' tiles, which all later queries see, are added in order by a last launch.
+//
+// What bounds it: the 16-byte loads from shared memory, two for 16 multiply-adds, and what the few warps of a block leave of
+// their latency.  4096 tokens of 8 : 2 heads of 128, window 1024: forward 679 us (22 TFLOP/s), backward 1.85 ms; 1235
+// tokens of 6 : 2 heads of 64, window 200: 49 and 97 us.  Eight rows a thread in place of four: head dim 64 as fast, 128 a tenth
+// slower (too few warps).
 #include <cuda_bf16.h>
 #include <math.h>
 
