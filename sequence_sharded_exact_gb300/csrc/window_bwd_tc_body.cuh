@@ -6,7 +6,7 @@
 //
 // One CTA per SM, persistent.  A work unit is one tile of 128 keys of one kv head and the query tiles that see it, head by
 // head: W / 128 + 1 of them, so that units are alike in every layout (the tiles are runs of natural positions).  A tile with
-// sinks is seen by all (later) queries: it is cut into segments about as long as the other units, taken first, each of which
+// sinks is seen by all (later) queries: it is cut into segments about as long as the other units, each of which
 // leaves its dK and dV in the workspace; a last kernel adds them in order.  Without that one CTA would walk the whole
 // sequence for them.  The tiles of a last round that would leave half of the SMs idle are cut likewise.
 //   * warp 12: TMA loads of the unit's K and V and, through 2 stages, of each query tile's Q (with its lse) and dO (with its
@@ -25,8 +25,8 @@
 // dP^T waits for dQ^T's read-out where they share Y; the order in which dQ's sums arrive varies.
 //
 // Measured with what comes before and after it (window_aux.cu), 32 : 8 heads of 128: 32K tokens, window 4096 4.8 ms (1.06 PFLOP/s;
-// this kernel 4.3), 64K tokens 8.8 ms, window 1024 2.90 ms without sinks and 3.45 with 4 (its tile is seen by all 512 query tiles
-// of a head: 9 % more pairs, of which few count).  dQ's reductions bound it.
+// this kernel 4.3), 64K tokens 8.8 ms, window 1024 2.92 ms without sinks and 3.25 with 4 (whose tile is seen by all 512 query
+// tiles of a head: 11 % more pairs, of which few count).  dQ's reductions bound it.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -99,6 +99,8 @@ struct BwdArgs {
     int G, T;          // query heads of a kv head; tiles of the sequence
     int sink_tiles, segs;  // tiles that hold sinks; segments of each of them (1: none is cut)
     unsigned sink_items, items;
+    unsigned per;      // items of a kv head, and the sinks' segments of all items, 2^-32 (not kTail)
+    unsigned long long share;
     unsigned whole;    // of the other tiles, those with a unit of their own; the rest have tail_segs
     int tail_segs;
     const float* lse2;  // -lse log2(e), [B H][T 128]
@@ -121,15 +123,29 @@ struct KvUnit {
     long long slot; // segment's place in `part`, or -1
 };
 
-// Items: the segments of the sinks' tiles, then the other tiles, and (kTail) the segments of those of the last round.
-// (A kernel without these is compiled apart: their code in it costs a unit 0.5 to 1 us.)
+// Items, kTail: the segments of the sinks' tiles, then the other tiles, and the segments of those of the last round.  (A kernel
+// without these is compiled apart: their code in it costs a unit 0.5 to 1 us.)  Otherwise, kv head by kv head, the tiles in
+// order, with the segments of the sinks' spread evenly among them: segment s meets the query tiles that its neighbours do, which
+// are then in L2 (64K tokens of 32 : 8 heads of 128, 4 sinks: all segments first, Q, dO and dQ came from memory once more:
+// window 1024 3.50 ms in place of 3.25, window 128 1.85 in place of 1.75).
 template <bool kTail>
 __device__ __forceinline__ KvUnit unit_of(const BwdArgs& a, unsigned item)
 {
     KvUnit u;
-    const bool sink = item < a.sink_items;
+    bool sink;
     int tile, seg = 0, cut = 0;
-    if (sink) {
+    if constexpr (!kTail) {
+        u.zk = (int)(item / a.per);
+        const unsigned x = item - (unsigned)u.zk * a.per;
+        const unsigned before = (unsigned)(x * a.share >> 32);  // segments before it
+        sink = (unsigned)((x + 1) * a.share >> 32) > before;
+        if (sink) {
+            seg = (int)(before / (unsigned)a.sink_tiles);
+            tile = (int)(before - (unsigned)(seg * a.sink_tiles));
+        } else {
+            tile = a.sink_tiles + (int)(x - before);
+        }
+    } else if (sink = item < a.sink_items; sink) {
         const unsigned per = (unsigned)(a.sink_tiles * a.segs), x = item % per;
         u.zk = (int)(item / per);
         tile = (int)(x / (unsigned)a.segs);
@@ -137,7 +153,7 @@ __device__ __forceinline__ KvUnit unit_of(const BwdArgs& a, unsigned item)
     } else {
         const unsigned per = (unsigned)(a.T - a.sink_tiles);
         unsigned x = item - a.sink_items;
-        if (kTail && x >= a.whole) {
+        if (x >= a.whole) {
             cut = 1 + (int)((x - a.whole) % (unsigned)a.tail_segs);
             x = a.whole + (x - a.whole) / (unsigned)a.tail_segs;
         }
@@ -152,7 +168,7 @@ __device__ __forceinline__ KvUnit unit_of(const BwdArgs& a, unsigned item)
     u.nt = to - from;
     u.from = 0;
     u.ntiles = u.nt * a.G;
-    u.slot = sink && a.segs > 1 ? (long long)item : -1LL;
+    u.slot = sink && a.segs > 1 ? ((long long)u.zk * a.sink_tiles + tile) * a.segs + seg : -1LL;
     if (kTail && cut) {
         const long long all = u.ntiles;
         u.from = (int)(all * (cut - 1) / a.tail_segs);
@@ -768,6 +784,9 @@ cudaError_t RA_WIN_BWD_LAUNCH(const WindowArgs& w, const WindowBwdPlan& p, unsig
     a.sink_tiles = p.sink_tiles;
     a.segs = p.segs;
     a.sink_items = (unsigned)p.sink_items;  // (below 2^31: the call's check)
+    const unsigned segments = (unsigned)(p.sink_tiles * p.segs);  // of a kv head
+    a.per = segments + (unsigned)(p.tiles - p.sink_tiles);
+    a.share = (((unsigned long long)segments << 32) + a.per - 1) / a.per;  // rounded up: the last one comes too
     a.whole = (unsigned)p.whole;
     a.tail_segs = p.tail_segs;
     a.items = (unsigned)(p.sink_items + p.whole + p.tail * p.tail_segs);
