@@ -9,8 +9,8 @@
 // segments' of the sinks' tiles, which all later queries see, are added in order by a last launch.
 //
 // What bounds it: the 16-byte loads from shared memory, two for 16 multiply-adds, and what the few warps of a block leave of
-// their latency.  4096 tokens of 8 : 2 heads of 128, window 1024: forward 679 us (22 TFLOP/s), backward 1.85 ms; 1235
-// tokens of 6 : 2 heads of 64, window 200: 49 and 97 us.  Eight rows a thread in place of four: head dim 64 as fast, 128 a tenth
+// their latency.  4096 tokens of 8 : 2 heads of 128, window 1024: forward 661 us (23 TFLOP/s), backward 1.81 ms; 1235
+// tokens of 6 : 2 heads of 64, window 200: 43 and 94 us.  Eight rows a thread in place of four: head dim 64 as fast, 128 a tenth
 // slower (too few warps).
 #include <cuda_bf16.h>
 #include <math.h>
@@ -37,19 +37,48 @@ __device__ __forceinline__ void store1(void* p, long long i, float v, int dtype)
         static_cast<float*>(p)[i] = v;
 }
 
-// 64 positions from p0 of one head's rows, transposed to [D][kStride]; positions past the sequence are zeros.
+// 64 positions from p0 of one head's rows: fetched into registers, and put into shared memory, transposed to [D][kStride];
+// positions past the sequence are zeros.  Both tiles of a step are fetched before the barrier that frees their room: all
+// loads are then on their way at once, beside the other warps' last products (1235 tokens of 6 heads of 64, forward 43 us in
+// place of 48).  Fetched a whole tile ahead: no faster with one block on an SM, head dim 128, and a block fewer at head dim 64
+// (4096 tokens of 32 heads 848 us in place of 716).
+template <int D>
+struct Tile {
+    float f[D / 16][4];
+    __device__ __forceinline__ void fetch(const Geometry& g, const float* head, int p0)
+    {
+        const int p = p0 + threadIdx.x % kT;
+        const float* src = p < g.L ? head + (long long)buffer_row(g, p) * D + threadIdx.x / kT * 4 : nullptr;
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[u][i] = 0.f;
+            if (src) load4(src + 16 * u, f[u]);
+        }
+    }
+    // Is a value that this thread has not finite?
+    __device__ __forceinline__ bool put(float* dst, float scale = 1.f) const
+    {
+        dst += threadIdx.x / kT * 4 * kStride + threadIdx.x % kT;
+        float odd = 0.f;  // NaN if one is
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                dst[(16 * u + i) * kStride] = f[u][i] * scale;
+                odd = fmaf(f[u][i], 0.f, odd);
+            }
+        return odd != 0.f;
+    }
+};
+static_assert(kThreads / kT * 4 == 16, "a thread's columns");
+
 template <int D>
 __device__ __forceinline__ void load_tile(const Geometry& g, const float* head, int p0, float* dst, float scale = 1.f)
 {
-    const int row = threadIdx.x % kT, p = p0 + row;
-    const float* src = p < g.L ? head + (long long)buffer_row(g, p) * D : nullptr;
-#pragma unroll 4
-    for (int c = threadIdx.x / kT * 4; c < D; c += kThreads / kT * 4) {
-        float f[4] = {0.f, 0.f, 0.f, 0.f};
-        if (src) load4(src + c, f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dst[(c + i) * kStride + row] = f[i] * scale;
-    }
+    Tile<D> t;
+    t.fetch(g, head, p0);
+    t.put(dst, scale);
 }
 
 // acc[i][j] += sum_c a[c][4 ty + i] b[c][4 tx + j].
@@ -70,8 +99,8 @@ __device__ __forceinline__ void dot_tile(const float* a, const float* b, float (
     }
 }
 
-// acc[i][k] += sum_j w[4 ty + i][j] b[tx + 16 k][j].  Hidden terms, marked by a weight below 0 (kNegative: P) or of 0
-// (kZero: dS), are left out, so that what is not finite in a hidden row stays out of the sums.
+// acc[i][k] += sum_j w[4 ty + i][j] b[tx + 16 k][j].  Hidden terms have a weight of 0.  Where b holds what is not finite they
+// are left out, so that it stays out of the sums: they are then marked by a weight below 0 (kNegative: P) or by the 0 (kZero: dS).
 enum Hidden { kNone, kNegative, kZero };
 template <int D, Hidden kHow>
 __device__ __forceinline__ void apply_rows(const float* w, const float* b, float (&acc)[4][D / 16])
@@ -96,9 +125,9 @@ __device__ __forceinline__ void apply_rows(const float* w, const float* b, float
     }
 }
 template <int D, Hidden kHow>
-__device__ __forceinline__ void apply_tile(bool whole, const float* w, const float* b, float (&acc)[4][D / 16])
+__device__ __forceinline__ void apply_tile(bool plain, const float* w, const float* b, float (&acc)[4][D / 16])
 {
-    if (whole)
+    if (plain)
         apply_rows<D, kNone>(w, b, acc);
     else
         apply_rows<D, kHow>(w, b, acc);
@@ -146,10 +175,12 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(const WindowA
     const TileRun run = key_tiles(a.band, q0, kT, kT);
     for (int t = 0; t < run.count(); ++t) {
         const int k0 = run.at(t) * kT;
+        Tile<D> tk, tv;
+        tk.fetch(a.geo, static_cast<const float*>(a.k) + zk * per, k0);
+        tv.fetch(a.geo, static_cast<const float*>(a.v) + zk * per, k0);
         __syncthreads();
-        load_tile<D>(a.geo, static_cast<const float*>(a.k) + zk * per, k0, sk);
-        load_tile<D>(a.geo, static_cast<const float*>(a.v) + zk * per, k0, sv);
-        __syncthreads();
+        tk.put(sk);
+        const bool odd = __syncthreads_or(tv.put(sv));
         float s[4][4] = {};
         dot_tile<D>(sq, sk, s);
         const bool whole = band_tile_whole(a.band, q0, kT, k0, kT);
@@ -167,8 +198,10 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(const WindowA
             const float mn = fmaxf(m[i], max16(mx)), ref = mn == -INFINITY ? 0.f : mn, alpha = exp2f(m[i] - ref);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                s[i][j] = hidden >> j & 1u ? -1.f : exp2f(s[i][j] - ref);
-                if (!(hidden >> j & 1u)) sum += s[i][j];
+                const bool hides = hidden >> j & 1u;
+                s[i][j] = hides ? 0.f : exp2f(s[i][j] - ref);
+                sum += s[i][j];
+                if (odd && hides) s[i][j] = -1.f;
             }
             l[i] = l[i] * alpha + sum16(sum);
             m[i] = mn;
@@ -177,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(const WindowA
         }
         put4(sp, s);
         __syncthreads();
-        apply_tile<D, kNegative>(whole, sp, sv, o);
+        apply_tile<D, kNegative>(whole || !odd, sp, sv, o);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -191,9 +224,9 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(const WindowA
     }
 }
 
-// P (-1 where hidden) and dS (0) of a tile whose rows are queries, or keys, from the scores and dout . v.
+// P (`hides` where hidden) and dS (0) of a tile whose rows are queries, or keys, from the scores and dout . v.
 template <bool kKeyRows>
-__device__ __forceinline__ void weights(const WindowArgs& a, int r0, int c0, const float (&lse2)[4], const float (&Dv)[4], float (&s)[4][4],
+__device__ __forceinline__ void weights(const WindowArgs& a, int r0, int c0, float hides, const float (&lse2)[4], const float (&Dv)[4], float (&s)[4][4],
                                         float (&dp)[4][4])
 {
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
@@ -203,7 +236,7 @@ __device__ __forceinline__ void weights(const WindowArgs& a, int r0, int c0, con
         for (int j = 0; j < 4; ++j) {
             const int r = r0 + 4 * ty + i, c = c0 + 4 * tx + j, p = kKeyRows ? c : r, key = kKeyRows ? r : c;
             const bool sees = p < a.band.L && key < a.band.L && band_sees(a.band, p, key);
-            s[i][j] = sees ? exp2f(s[i][j] - lse2[kKeyRows ? j : i]) : -1.f;
+            s[i][j] = sees ? exp2f(s[i][j] - lse2[kKeyRows ? j : i]) : hides;
             dp[i][j] = sees ? s[i][j] * (dp[i][j] - Dv[kKeyRows ? j : i]) * a.scale : 0.f;
         }
 }
@@ -228,17 +261,19 @@ __device__ __forceinline__ void bwd_queries(const WindowArgs& a, float* sm, int 
     const TileRun run = key_tiles(a.band, q0, kT, kT);
     for (int t = 0; t < run.count(); ++t) {
         const int k0 = run.at(t) * kT;
+        Tile<D> tk, tv;
+        tk.fetch(a.geo, static_cast<const float*>(a.k) + zk * per, k0);
+        tv.fetch(a.geo, static_cast<const float*>(a.v) + zk * per, k0);
         __syncthreads();
-        load_tile<D>(a.geo, static_cast<const float*>(a.k) + zk * per, k0, sk);
-        load_tile<D>(a.geo, static_cast<const float*>(a.v) + zk * per, k0, sv);
-        __syncthreads();
+        tv.put(sv);
+        const bool odd = __syncthreads_or(tk.put(sk));
         float s[4][4] = {}, dp[4][4] = {};
         dot_tile<D>(sq, sk, s);
         dot_tile<D>(sd, sv, dp);
-        weights<false>(a, q0, k0, lse2, Dv, s, dp);
+        weights<false>(a, q0, k0, 0.f, lse2, Dv, s, dp);
         put4(sp, dp);
         __syncthreads();
-        apply_tile<D, kZero>(band_tile_whole(a.band, q0, kT, k0, kT), sp, sk, acc);
+        apply_tile<D, kZero>(!odd || band_tile_whole(a.band, q0, kT, k0, kT), sp, sk, acc);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -262,9 +297,12 @@ __device__ __forceinline__ void bwd_keys(const WindowArgs& a, float* sm, int zq,
     float dk[4][D / 16] = {}, dv[4][D / 16] = {};
     for (int t = t0; t < t1; ++t) {
         const int q0 = t * kT;
+        Tile<D> tq, td;
+        tq.fetch(a.geo, static_cast<const float*>(a.q) + zq * per, q0);
+        td.fetch(a.geo, static_cast<const float*>(a.dout) + zq * per, q0);
         __syncthreads();
-        load_tile<D>(a.geo, static_cast<const float*>(a.q) + zq * per, q0, sq);
-        load_tile<D>(a.geo, static_cast<const float*>(a.dout) + zq * per, q0, sd);
+        bool odd = tq.put(sq);
+        odd |= td.put(sd);
         float lse2[4], Dv[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -273,17 +311,17 @@ __device__ __forceinline__ void bwd_keys(const WindowArgs& a, float* sm, int zq,
             lse2[j] = has ? a.lse[(long long)zq * a.band.L + buffer_row(a.geo, p)] * kLog2e : 0.f;
             Dv[j] = has ? a.D[(long long)zq * a.band.L + p] : 0.f;
         }
-        __syncthreads();
+        odd = __syncthreads_or(odd);
         float s[4][4] = {}, dp[4][4] = {};
         dot_tile<D>(sk, sq, s);
         dot_tile<D>(sv, sd, dp);
-        weights<true>(a, k0, q0, lse2, Dv, s, dp);
+        weights<true>(a, k0, q0, odd ? -1.f : 0.f, lse2, Dv, s, dp);
         put4(sp, s);
         put4(ss, dp);
         __syncthreads();
-        const bool whole = band_tile_whole(a.band, q0, kT, k0, kT);
-        apply_tile<D, kNegative>(whole, sp, sd, dv);
-        apply_tile<D, kZero>(whole, ss, sq, dk);
+        const bool plain = !odd || band_tile_whole(a.band, q0, kT, k0, kT);
+        apply_tile<D, kNegative>(plain, sp, sd, dv);
+        apply_tile<D, kZero>(plain, ss, sq, dk);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
