@@ -229,6 +229,22 @@ def test_rows_beside_values_that_are_not_finite(out_dtype, layout, n):
     cu.check_tree((o, got[1].cpu()), (out, lse, mag, big), 2.0 ** -8, out_dtype, "the rest")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_sink_of_infinities(d):
+    """A value that every row sees, infinite in all columns: every output is, lse is what it was, and the call ends without a wait
+    that ran out (the fixture's status) although every row is looked at again."""
+    q, k, v, _ = _inputs(1, 4, 2, 4096, d, BF, seed=d)
+    out, lse = ra.window_fwd(q, k, v, 1, 1024, 2, True, "contiguous")
+    v2 = v.clone()
+    v2[:, :, 1] = math.inf
+    v2[:, :, 1, 5] = -math.inf
+    o2, l2 = ra.window_fwd(q, k, v2, 1, 1024, 2, True, "contiguous")
+    assert torch.equal(l2, lse) and torch.equal(o2[:, :, :1], out[:, :, :1])
+    sign = torch.ones(d, device=DEV)
+    sign[5] = -1
+    assert bool((o2[:, :, 1:] == sign * math.inf).all())
+
+
 def test_the_smallest_and_odd_stripes():
     """A row per shard, shards of a row each in a tile of 128, and heads that pair up or do not."""
     for L, n, layout in ((2, 2, "striped"), (64, 64, "striped"), (256, 64, "striped"), (384, 128, "striped"), (6, 3, "zigzag"), (128, 1, "zigzag")):
