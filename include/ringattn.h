@@ -571,8 +571,9 @@ RA_API size_t ring_attn_tree_fwd_workspace_size(int B, int H, int Hkv, int T, in
  *   window >= 1, sinks >= 0 (any values: past the cache they reach all of it).
  *   With a mask it says which of the step's tokens t sees, whatever their distance, and positions, DEVICE int32 [B][T],
  *   4-byte aligned, gives p_t (for a tree of drafted tokens lens[b] + t's depth; a value outside [lens[b], lens[b] + T) counts
- *   as the nearer end).  Without positions p_t = lens[b] + t.  Without a mask t sees the step's tokens j <= t with t - j < window,
- *   and positions have to be NULL.
+ *   as the nearer end).  Without positions p_t = lens[b] + t.  Without a mask positions have to be NULL, and t sees the step's
+ *   tokens j <= t with t - j < window or lens[b] + j < sinks: every row is what ring_attn_window_fwd gives it over the whole
+ *   sequence, wherever a prompt is cut into steps.
  *   The prefix is the whole one: parts of a cache that is sharded over devices do not fold together through a window.
  *   Everything else as ring_attn_tree_fwd, its workspace and its accuracy among it.
  */

@@ -1209,7 +1209,7 @@ def tree_fwd(q, cache, lens, mask=None, ntok=None, out_dtype=None, out=None, lse
     window, sinks (ring_attn_tree_window_fwd): of the prefix a token at position p sees the rows j > p - window and the
     first `sinks` ones alone.  positions [B, T] int32: the tokens' positions where a mask says which of the step's tokens
     they see (lens[b] + depth in a tree); without them, and without a mask, token t is at lens[b] + t, and without a mask
-    it sees the step's tokens j <= t with t - j < window."""
+    it sees the step's tokens j <= t with t - j < window and those among the first `sinks` of the sequence."""
     if _calls is not None and stream is None:
         if window is None and not sinks and positions is None:
             done = _calls.tree_fwd(q, cache, lens, mask, ntok, out_dtype, out, lse, workspace)

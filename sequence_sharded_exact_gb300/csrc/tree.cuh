@@ -25,7 +25,8 @@
 // the first one leaves, whatever the batch, and also writes the rows of sequences that have no tokens.
 //
 // Through a window (kWin): token t, at position p_t in [len, len + T), sees the prefix's rows j < sinks and those with
-// p_t - j < window.  The rows between the sinks and the first one that a token's window reaches are left out of the list,
+// p_t - j < window; without a mask the same holds of the step's rows up to its own, so that a prompt may go in by
+// chunks of any size.  The rows between the sinks and the first one that a token's window reaches are left out of the list,
 // by whole tiles: list tile x is the cache's tile x among the sinks', and gap tiles further on behind them.  Rows that some
 // tokens see and others do not are treated as drafted tokens' are.
 #pragma once
@@ -300,9 +301,9 @@ __device__ __forceinline__ void tree_clear_item(const TreeArgs& a, int cta)
 
 // Does query token t see drafted token j (both < cnt)?
 template <bool kWin = false>
-__device__ __forceinline__ bool tree_sees(const TreeArgs& a, int b, int t, int j)
+__device__ __forceinline__ bool tree_sees(const TreeArgs& a, const TreeSeq& s, int b, int t, int j)
 {
-    if (!a.mask) return j <= t && (!kWin || t - j < a.window);
+    if (!a.mask) return j <= t && (!kWin || t - j < a.window || s.len + j < a.sinks);
     return a.mask[((a.mask_batched ? (long long)b * a.T : 0) + t) * a.T + j] != 0;
 }
 

@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, kWarps, N>::kPerSm) tree_m
             if constexpr (kWin)
                 if (key < w.s.len) return key >= reach[c][u] || key < w.s.sinks;
             return key < w.s.len ||
-                   (key < w.s.end && (live >> (2 * c + u) & 1) && tree_sees<kWin>(a, w.b, (8 * c + 2 * t4 + u) % a.T, key - w.s.len));
+                   (key < w.s.end && (live >> (2 * c + u) & 1) && tree_sees<kWin>(a, w.s, w.b, (8 * c + 2 * t4 + u) % a.T, key - w.s.len));
         };
 
 #pragma unroll 1

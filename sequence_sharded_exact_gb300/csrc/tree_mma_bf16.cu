@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_mma_bf16_kernel(const __grid
         auto sees = [&](int u, int key) {
             if constexpr (kWin)
                 if (key < w.s.len) return key >= reach[u] || key < w.s.sinks;
-            return key < w.s.len || (key < w.s.end && live[u] && tree_sees<kWin>(a, w.b, (2 * t4 + u) % a.T, key - w.s.len));
+            return key < w.s.len || (key < w.s.end && live[u] && tree_sees<kWin>(a, w.s, w.b, (2 * t4 + u) % a.T, key - w.s.len));
         };
 
 #pragma unroll 1

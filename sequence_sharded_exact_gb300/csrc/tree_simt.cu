@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, kTreeSimtCtasPerSm) tree_simt_kernel
             for (int i = 0; i < RW; ++i) {
                 const int x = w.r * a.rt + warp * RW + i, t = x % a.T;
                 bool sees = key < w.s.end;
-                if (drafted && key >= w.s.len && sees) sees = t < w.s.cnt && x < a.R && tree_sees<kWin>(a, w.b, t, key - w.s.len);
+                if (drafted && key >= w.s.len && sees) sees = t < w.s.cnt && x < a.R && tree_sees<kWin>(a, w.s, w.b, t, key - w.s.len);
                 if constexpr (kWin)
                     if (drafted && key < w.s.len && key >= w.s.sinks)
                         sees = t < w.s.cnt && x < a.R && key >= tree_reach(a, w.s, w.b, t);

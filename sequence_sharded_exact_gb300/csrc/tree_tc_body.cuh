@@ -651,9 +651,14 @@ __device__ __forceinline__ unsigned long long seen_bits(const TreeArgs& a, const
     if (t >= s.cnt) return bits;
     const int j0 = p < 0 ? -p : 0, j1 = 64 - p < s.cnt ? 64 - p : s.cnt;
     if (!a.mask) {
-        const int from = kWin && t - a.window + 1 > j0 ? t - a.window + 1 : j0;
-        const int n = (j1 < t + 1 ? j1 : t + 1) - from;  // drafted tokens up to t
-        return n > 0 ? bits | (n >= 64 ? ~0ull : (1ull << n) - 1) << (p + from) : bits;
+        const int to = j1 < t + 1 ? j1 : t + 1;  // one past the last drafted token up to t
+        if constexpr (kWin) {
+            const int from = t - a.window + 1 > j0 ? t - a.window + 1 : j0, first = a.sinks - s.len < to ? a.sinks - s.len : to;
+            return bits | (low_bits(p + to) & ~low_bits(p + from)) | (low_bits(p + first) & ~low_bits(p + j0));
+        } else {
+            const int n = to - j0;
+            return n > 0 ? bits | (n >= 64 ? ~0ull : (1ull << n) - 1) << (p + j0) : bits;
+        }
     }
     const uint8_t* m = a.mask + ((a.mask_batched ? (long long)b * a.T : 0) + t) * a.T;
     const bool wide = (reinterpret_cast<uintptr_t>(a.mask) & 15) == 0 && a.T % 16 == 0;  // rows of whole 16-byte words
@@ -923,7 +928,7 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
                             continue;
                         }
                         const int x = tree_list_row(w.s, key, kTreeTile);
-                        if (x < w.t0 * kTreeTile || x >= w.t1 * kTreeTile || !(j < 0 ? key >= reach : tree_sees<kWin>(a, w.b, tq, j))) continue;
+                        if (x < w.t0 * kTreeTile || x >= w.t1 * kTreeTile || !(j < 0 ? key >= reach : tree_sees<kWin>(a, w.s, w.b, tq, j))) continue;
                         const long long src = ((long long)w.b * a.Hkv + w.g) * a.cap + key;
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
