@@ -13,8 +13,8 @@
 //     m follows the maximum only when that grows by more than 2^8 (O / l does not depend on the reference).  Hidden scores are
 //     set to -infinity by a bit each, in the tiles that are not wholly visible: one at each end of the window, and the
 //     sinks'.  The other tiles' code knows nothing of masks (with both in one, 64K tokens without sinks took 2.83 ms in place of 2.64).
-//   * A weight of 0 does not hide a value that is not finite: a row whose O comes out so is looked at again, element by
-//     element, by its thread (rare).
+//   * A weight of 0 does not hide a value that is not finite: the rows whose O comes out so are looked at again (rare), once
+//     the CTA's units are done: no wait of the pipeline, all of which have limits, then depends on how long that takes.
 //   * TMEM: S0 columns [0,128), S1 [128,256), O0 from 256, O1 from 384.
 // The weights go into P V as one bf16 value each; the row is divided by the sum of the unrounded weights, but for the
 // tile's largest, which counts as rounded: a row that one key dominates gets that key's value exactly.
@@ -62,8 +62,10 @@ enum : int {
 
 constexpr uint32_t kSmemTmemSlot = kSmemBar + BAR_COUNT * 8;
 constexpr uint32_t kSmemAbort = kSmemTmemSlot + 8;
-constexpr uint32_t kSmemBytes = kSmemAbort + 8 + 1024;  // slack for the 1024-byte alignment of the base
+constexpr uint32_t kSmemOdd = kSmemAbort + 8;  // are there rows to mend; and behind it mend_rows' words
+constexpr uint32_t kSmemBytes = kSmemOdd + 8 + (kTile + 2) * (kHd / 16) * 4 + 1024;  // slack for the 1024-byte alignment of the base
 static_assert(kSmemBytes <= 232448, "shared memory");
+static_assert(kSmemK - kSmemQ >= 256 * kHd * 2 && kStages * kTileBytes >= kTile * kHd * 2, "mend_rows' rows");
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS0 = 0, kColO0 = 256;
@@ -123,71 +125,200 @@ __device__ __forceinline__ void store32(void* p, bool wide, const uint32_t* v)
 // ------------------------------------------------------------------------------------------------
 // softmax warpgroups
 // ------------------------------------------------------------------------------------------------
-// The row at position p, whose output came out with elements that are not finite: those that it gets from the keys that it
-// sees stay (their sum takes the element's place), the others are computed from these keys alone.
-__device__ __noinline__ void mend_row(const FwdArgs& a, unsigned item, long long zq, int p, long long row_g, float lse)
+// x of any of the 256 softmax threads; all of them call it.
+__device__ __forceinline__ bool any_softmax_thread(bool x)
 {
-    const Unit u = unit_of(a, item);
-    if (!(fabsf(lse) <= 3.4028234e38f)) return;  // so are its scores
-    const __nv_bfloat16* q = a.q + (zq * a.band.L + buffer_row(a.geo, p)) * kHd;
-    const long long base = (long long)u.zk * a.band.L;
-    float sum[kHd];
-    unsigned long long odd[2] = {0, 0}, lost[2] = {0, 0};  // columns that are not finite; those of them that the row has from no key
-    for (int c = 0; c < kHd; ++c) {
-        const float o = a.out_f32 ? static_cast<float*>(a.out)[row_g * kHd + c] : __bfloat162float(static_cast<__nv_bfloat16*>(a.out)[row_g * kHd + c]);
-        sum[c] = 0.f;
-        if (fabsf(o) <= 3.4028234e38f) continue;
-        odd[c >> 6] |= 1ull << (c & 63);
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
+constexpr float kMaxF32 = 3.4028234e38f;
+constexpr int kWords = kHd / 32;   // a bit per column
+constexpr int kSigns = 2 * kWords; // columns with +infinity (or NaN), then those with -infinity (or NaN)
+
+// Which of 64 columns (32 at head dim 64) of a row of V are not finite.
+__device__ __forceinline__ void signs_of(const uint4* v, uint32_t (&plus)[kWords / 2], uint32_t (&minus)[kWords / 2])
+{
+#pragma unroll
+    for (int w = 0; w < kWords / 2; ++w) plus[w] = minus[w] = 0;
+#pragma unroll
+    for (int g = 0; g < kHd / 16; ++g) {
+        const uint4 x = v[g];
+        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+        uint32_t any = 0;  // an exponent of ones
+#pragma unroll
+        for (int i = 0; i < 4; ++i) any |= (y[i] & 0x7f807f80u) + 0x00800080u;
+        if (!(any & 0x80008000u)) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t f = y[e >> 1] >> 16 * (e & 1) & 0xffffu;
+            if ((f & 0x7f80u) != 0x7f80u) continue;
+            const bool nan = (f & 0x7fu) != 0;
+            if (nan || !(f & 0x8000u)) plus[g >> 2] |= 1u << ((8 * g + e) & 31);
+            if (nan || (f & 0x8000u)) minus[g >> 2] |= 1u << ((8 * g + e) & 31);
+        }
     }
-    // key by key, 64 columns at a time, of which an exponent of ones tells those that are looked at (64K tokens, window 4096, a sink
-    // of infinities that every row sees: 157 ms; with eight columns at a time 972; a window of a million keys stays below the limit of the waits)
-    for (int jj = 0; jj < u.run.count(); ++jj)
-        for (int j = u.run.at(jj) * kTile, e = j + kTile < a.band.L ? j + kTile : a.band.L; j < e; ++j) {
-            if (!band_sees(a.band, p, j)) continue;
-            const __nv_bfloat16* v = a.v + (base + buffer_row(a.geo, j)) * kHd;
+}
+
+// Which of the 8 elements of the output from number `at` on are not finite.
+__device__ __forceinline__ uint32_t odd_columns(const FwdArgs& a, long long at)
+{
+    uint32_t bits = 0;
+    if (a.out_f32) {
+        const uint4* x = reinterpret_cast<const uint4*>(static_cast<float*>(a.out) + at);
+        const uint4 y = x[0], z = x[1];
+        const uint32_t f[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
 #pragma unroll
-            for (int half = 0; half < kHalves; ++half) {
-                uint32_t any = 0;
+        for (int e = 0; e < 8; ++e) bits |= (uint32_t)((f[e] & 0x7f800000u) == 0x7f800000u) << e;
+    } else {
+        const uint4 x = *reinterpret_cast<const uint4*>(static_cast<__nv_bfloat16*>(a.out) + at);
+        const uint32_t f[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const uint4 x = reinterpret_cast<const uint4*>(v)[8 * half + g];
-                    any |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) | ((x.z & 0x7f807f80u) + 0x00800080u) |
-                           ((x.w & 0x7f807f80u) + 0x00800080u);
-                }
-                if (!(any & 0x80008000u)) continue;
+        for (int e = 0; e < 8; ++e) bits |= (uint32_t)((f[e >> 1] >> 16 * (e & 1) & 0x7f80u) == 0x7f80u) << e;
+    }
+    return bits;
+}
+
+// A row's columns `lost`, from the keys [k0, e) that it sees, which lie in shared memory: q by 16 bytes from every thread in turns.
+__device__ __forceinline__ void sum_tile(const FwdArgs& a, const uint4* q, const uint4* k, const uint4* v, int p, int k0, int e, float lse2,
+                                         const uint32_t (&lost)[kWords], float (&sum)[kHd])
+{
+    for (int j = k0; j < e; ++j, k += kHd / 8, v += kHd / 8) {
+        if (!band_sees(a.band, p, j)) continue;
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int g = 0; g < kHd / 8; ++g) {
+            const uint4 x = q[g * 256], y = k[g];
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w}, z[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[i] = fmaf(__uint_as_float(w[i] << 16), __uint_as_float(z[i] << 16), s[i]);
+                s[i] = fmaf(__uint_as_float(w[i] & 0xffff0000u), __uint_as_float(z[i] & 0xffff0000u), s[i]);
+            }
+        }
+        const float weight = ex2_approx(fmaf((s[0] + s[1]) + (s[2] + s[3]), a.scale_log2, lse2));
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            if (!lost[w]) continue;
 #pragma unroll 1
-                for (int c = 64 * half; c < 64 * half + 64; ++c) {
-                    const float f = __bfloat162float(v[c]);
-                    if (!(fabsf(f) <= 3.3895314e38f)) sum[c] += f;  // past bf16's largest
-                }
-            }
-        }
-    for (int c = 0; c < kHd; ++c)
-        if ((odd[c >> 6] >> (c & 63) & 1) && sum[c] == 0.f) lost[c >> 6] |= 1ull << (c & 63);
-    for (int jj = 0; (lost[0] | lost[1]) != 0 && jj < u.run.count(); ++jj)
-        for (int j = u.run.at(jj) * kTile, e = j + kTile < a.band.L ? j + kTile : a.band.L; j < e; ++j) {
-            if (!band_sees(a.band, p, j)) continue;
-            const long long at = (base + buffer_row(a.geo, j)) * kHd;
-            float s = 0.f;
-            for (int g = 0; g < kHd / 8; ++g) {
-                const uint4 x = reinterpret_cast<const uint4*>(q)[g], y = reinterpret_cast<const uint4*>(a.k + at)[g];
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w}, z[4] = {y.x, y.y, y.z, y.w};
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t cols = lost[w] >> 8 * g & 0xffu;
+                if (!cols) continue;
+                const uint4 x = v[4 * w + g];
+                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+                float* to = sum + 32 * w + 8 * g;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s = fmaf(__uint_as_float(w[i] << 16), __uint_as_float(z[i] << 16), s);
-                    s = fmaf(__uint_as_float(w[i] & 0xffff0000u), __uint_as_float(z[i] & 0xffff0000u), s);
+                for (int i = 0; i < 8; ++i)
+                    if (cols >> i & 1) to[i] = fmaf(weight, __uint_as_float(i & 1 ? y[i >> 1] & 0xffff0000u : y[i >> 1] << 16), to[i]);
+            }
+        }
+    }
+}
+
+// After the CTA's last unit, where no wait depends on how long this takes: the rows whose output came out with elements that are
+// not finite.  Such an element becomes the sum of what is not finite among the values that its row sees in its column (a bit per
+// sign is all of that sum), whatever their weights; one that sees none there, and so has it from a hidden value or from a sum past
+// float32, is summed once more from the visible keys alone.  The softmax warps read V by tiles, each thread half a row, and a
+// row takes a tile that it sees whole at once; for such sums K and V go through the room of the rings and Q's tiles, which
+// nothing else uses by then.  16K tokens of 8 : 2 heads of 128, window 8192 (0.31 ms without such values): a value that every row
+// sees 1.1 ms, none of V finite 1.8, one NaN, beside which 254 rows of each head are summed once more, 10 (key by key for each row,
+// inside the pipeline: 18, 708 and 73).  It costs calls without such values up to 1.5 % (64K tokens, window 128: 338 -> 343 us).
+__device__ __noinline__ void mend_rows(const FwdArgs& a, uint8_t* smem)
+{
+    uint32_t *all = reinterpret_cast<uint32_t*>(smem + kSmemOdd + 8), *keys = all + 2 * kSigns;  // of a tile, two in turns; of each of its keys
+    const int t = threadIdx.x, w = t >> 7, rw = t & 127;
+    if (t < 2 * kSigns) all[t] = 0;
+    for (unsigned item = blockIdx.x; item < a.units; item += gridDim.x) {
+        const Unit u = unit_of(a, item);
+        const int q0 = w ? u.p1 : u.p, p = q0 + rw;
+        const bool in = p < a.band.L;
+        const long long zq = w ? u.zq1 : u.zq, row = zq * a.band.L + (in ? buffer_row(a.store_geo, p) : 0);
+        const float lse = in ? a.lse[row] : 0.f;
+        uint32_t odd[kWords], seen[kSigns];
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            odd[i] = seen[i] = seen[kWords + i] = 0;
+            if (in && fabsf(lse) <= kMaxF32)  // (else so are the row's scores)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) odd[i] |= odd_columns(a, row * kHd + 32 * i + 8 * g) << 8 * g;
+            any |= odd[i] != 0;
+        }
+        if (!any_softmax_thread(any)) continue;
+        for (int jj = 0; jj < u.run.count(); ++jj) {
+            const int k0 = u.run.at(jj) * kTile, key = t >> 1, half = t & 1;
+            uint32_t plus[kWords / 2] = {}, minus[kWords / 2] = {}, *now = all + (jj & 1) * kSigns;
+            if (k0 + key < a.band.L)
+                signs_of(reinterpret_cast<const uint4*>(a.v + ((long long)u.zk * a.band.L + buffer_row(a.geo, k0 + key)) * kHd + half * (kHd / 2)), plus, minus);
+            bool found = false;
+#pragma unroll
+            for (int i = 0; i < kWords / 2; ++i) {
+                const int at = half * (kWords / 2) + i;
+                keys[key * kSigns + at] = plus[i];
+                keys[key * kSigns + kWords + at] = minus[i];
+                if (plus[i]) atomicOr(now + at, plus[i]);
+                if (minus[i]) atomicOr(now + kWords + at, minus[i]);
+                found |= (plus[i] | minus[i]) != 0;
+            }
+            if (any_softmax_thread(found)) {
+                if (any && band_tile_whole(a.band, q0, kTile, k0, kTile)) {
+#pragma unroll
+                    for (int i = 0; i < kSigns; ++i) seen[i] |= now[i];
+                } else if (any) {
+                    const Seen s = seen_keys(a.band, p, k0);
+#pragma unroll 1
+                    for (int c = 0; c < kTile; ++c)
+                        if (s.word(c & ~31) >> (c & 31) & 1) {
+#pragma unroll
+                            for (int i = 0; i < kSigns; ++i) seen[i] |= keys[c * kSigns + i];
+                        }
                 }
             }
-            const float weight = ex2_approx(fmaf(s, a.scale_log2, -lse * kLog2e));
-            for (int c = 0; c < kHd; ++c)
-                if (lost[c >> 6] >> (c & 63) & 1) sum[c] = fmaf(weight, __bfloat162float(a.v[at + c]), sum[c]);
+            if (t < kSigns) all[((jj + 1) & 1) * kSigns + t] = 0;  // the next tile's, last read before the barrier above
+            any_softmax_thread(false);                             // the tile has been read
         }
-    for (int c = 0; c < kHd; ++c) {
-        if (!(odd[c >> 6] >> (c & 63) & 1)) continue;
-        if (a.out_f32)
-            static_cast<float*>(a.out)[row_g * kHd + c] = sum[c];
-        else
-            static_cast<__nv_bfloat16*>(a.out)[row_g * kHd + c] = __float2bfloat16_rn(sum[c]);
+        if (t < 2 * kSigns) all[t] = 0;
+        uint32_t lost[kWords], none = 0;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) none |= lost[i] = odd[i] & ~(seen[i] | seen[kWords + i]);
+        float sum[kHd];
+        if (any_softmax_thread(none != 0)) {
+            uint4 *q = reinterpret_cast<uint4*>(smem + kSmemQ) + t, *k = reinterpret_cast<uint4*>(smem + kSmemK), *v = reinterpret_cast<uint4*>(smem + kSmemV);
+            if (none) {
+                const uint4* x = reinterpret_cast<const uint4*>(a.q + (zq * a.band.L + buffer_row(a.geo, p)) * kHd);
+                for (int g = 0; g < kHd / 8; ++g) q[g * 256] = x[g];
+                for (int c = 0; c < kHd; ++c) sum[c] = 0.f;
+            }
+            for (int jj = 0; jj < u.run.count(); ++jj) {
+                const int k0 = u.run.at(jj) * kTile, e = k0 + kTile < a.band.L ? k0 + kTile : a.band.L;
+                any_softmax_thread(false);  // the tile before this has been read
+#pragma unroll 4
+                for (int x = t; x < (e - k0) * (kHd / 8); x += 256) {
+                    const long long at = ((long long)u.zk * a.band.L + buffer_row(a.geo, k0 + x / (kHd / 8))) * (kHd / 8) + x % (kHd / 8);
+                    k[x] = reinterpret_cast<const uint4*>(a.k)[at];
+                    v[x] = reinterpret_cast<const uint4*>(a.v)[at];
+                }
+                any_softmax_thread(false);
+                if (none) sum_tile(a, q, k, v, p, k0, e, -lse * kLog2e, lost, sum);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+#pragma unroll 1
+            for (uint32_t left = odd[i]; left; left &= left - 1) {
+                const uint32_t bit = left & (0u - left);
+                const int c = 32 * i + __ffs(left) - 1;
+                const float x = lost[i] & bit ? sum[c] : seen[i] & bit ? (seen[kWords + i] & bit ? __uint_as_float(0x7fffffffu) : INFINITY) : -INFINITY;
+                if (a.out_f32)
+                    static_cast<float*>(a.out)[row * kHd + c] = x;
+                else
+                    static_cast<__nv_bfloat16*>(a.out)[row * kHd + c] = __float2bfloat16_rn(x);
+            }
     }
 }
 
@@ -294,7 +425,8 @@ __device__ __forceinline__ bool softmax_tile(const Seen& seen, const Place& x, b
     return true;
 }
 
-__device__ __forceinline__ void softmax_role(const FwdArgs& a, uint32_t sbase, uint32_t tmem, const WaitCtl& ctl)
+// False if a wait ran out.
+__device__ __forceinline__ bool softmax_role(const FwdArgs& a, uint32_t sbase, uint32_t tmem, const WaitCtl& ctl)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w = warp >> 2;                // query tile of this warpgroup
@@ -313,13 +445,13 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, uint32_t sbase, u
         for (int jj = 0; jj < ntiles; ++jj, ++tcount) {
             const int k0 = u.run.at(jj) * kTile;
             if (band_tile_whole(a.band, q0, kTile, k0, kTile)) {
-                if (!softmax_tile<false>(Seen{}, x, jj > 0, tcount, row, ctl)) return;
+                if (!softmax_tile<false>(Seen{}, x, jj > 0, tcount, row, ctl)) return false;
             } else {
-                if (!softmax_tile<true>(seen_keys(a.band, p, k0), x, jj > 0, tcount, row, ctl)) return;
+                if (!softmax_tile<true>(seen_keys(a.band, p, k0), x, jj > 0, tcount, row, ctl)) return false;
             }
         }
         // the unit's rows
-        if (!mbar_wait(bar_o, (tcount - 1) & 1, ctl)) return;
+        if (!mbar_wait(bar_o, (tcount - 1) & 1, ctl)) return false;
         tc_fence_after_sync();
         __syncwarp();
         const float inv = 1.0f / (row.l + row.c), lse = (row.m + log2f(row.l)) * kLn2;
@@ -355,8 +487,9 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, uint32_t sbase, u
             }
         }
         if (in) a.lse[row_g] = lse;
-        if (odd.x + odd.y != 0.f) mend_row(a, item, zq, p, row_g, lse);
+        if (odd.x + odd.y != 0.f) asm volatile("st.shared.u32 [%0], 1;" ::"r"(sbase + kSmemOdd) : "memory");
     }
+    return true;
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -518,6 +651,7 @@ window_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             mbar_init(sbase + kSmemBar + 8u * (uint32_t)i, cnt);
         }
         *abort_flag = 0;
+        *reinterpret_cast<uint32_t*>(smem + kSmemOdd) = 0;
         fence_barrier_init();
     }
     if (warp == 9) {
@@ -537,7 +671,10 @@ window_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;" ::: "memory");
 
     if (warp < 8) {
-        softmax_role(a, sbase, tmem, ctl);
+        const bool done = softmax_role(a, sbase, tmem, ctl);
+        __syncwarp();
+        if (!any_softmax_thread(!done) && *reinterpret_cast<volatile uint32_t*>(smem + kSmemOdd))
+            mend_rows(a, smem);
     } else if (warp == 8) {
         if ((threadIdx.x & 31) == 0) load_role(a, sbase, &tmQ, &tmK, &tmV, ctl);
     } else if (warp == 9) {
