@@ -487,7 +487,8 @@ RA_API ra_status ring_attn_qk_rope_axes_bwd(const void* q, const long long* q_st
  *   bf16 inputs dq is summed by float32 atomics, in an order that varies.
  * What a row of the forward does not see has no part in its result, whatever it holds (NaN, infinities); with bf16 inputs a
  * row that shares a tile of 128 positions with a value that is not finite, or whose sums pass float32's largest, is looked at
- * again after the others, slowly (some microseconds for each of its keys at worst).  The backward takes
+ * again after the others, slowly (about a microsecond for each of its keys at worst).  A value that is not finite reaches every
+ * row that sees it, in its column, whatever its weight (also one that is 0 in float32).  The backward takes
  * finite inputs: what is not may reach the gradients of all positions within 127 of those that see it.
  */
 RA_API ra_status ring_attn_window_fwd(const void* q, const void* k, const void* v, void* out, float* lse, void* workspace,

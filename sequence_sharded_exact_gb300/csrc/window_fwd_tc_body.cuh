@@ -226,7 +226,7 @@ __device__ __forceinline__ void sum_tile(const FwdArgs& a, const uint4* q, const
 // float32, is summed once more from the visible keys alone.  The softmax warps read V by tiles, each thread half a row, and a
 // row takes a tile that it sees whole at once; for such sums K and V go through the room of the rings and Q's tiles, which
 // nothing else uses by then.  16K tokens of 8 : 2 heads of 128, window 8192 (0.31 ms without such values): a value that every row
-// sees 1.1 ms, none of V finite 1.8, one NaN, beside which 254 rows of each head are summed once more, 10 (key by key for each row,
+// sees 1.1 ms, none of V finite 1.8, one NaN, beside which 127 rows of each head are summed once more, 10 (key by key for each row,
 // inside the pipeline: 18, 708 and 73).  It costs calls without such values up to 1.5 % (64K tokens, window 128: 338 -> 343 us).
 __device__ __noinline__ void mend_rows(const FwdArgs& a, uint8_t* smem)
 {

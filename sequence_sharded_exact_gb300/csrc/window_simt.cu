@@ -99,9 +99,12 @@ __device__ __forceinline__ void dot_tile(const float* a, const float* b, float (
     }
 }
 
+constexpr float kMaxF32 = 3.4028234e38f;
+
 // acc[i][k] += sum_j w[4 ty + i][j] b[tx + 16 k][j].  Hidden terms have a weight of 0.  Where b holds what is not finite they
 // are left out, so that it stays out of the sums: they are then marked by a weight below 0 (kNegative: P) or by the 0 (kZero: dS).
-enum Hidden { kNone, kNegative, kZero };
+// kValues: as kNegative, and what is not finite and seen counts whole, also with a weight that is 0 in float32 only.
+enum Hidden { kNone, kNegative, kZero, kValues };
 template <int D, Hidden kHow>
 __device__ __forceinline__ void apply_rows(const float* w, const float* b, float (&acc)[4][D / 16])
 {
@@ -119,8 +122,12 @@ __device__ __forceinline__ void apply_rows(const float* w, const float* b, float
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (kHow == kNone || (kHow == kNegative ? !(x[i][e] < 0.f) : x[i][e] != 0.f)) acc[i][k] = fmaf(x[i][e], y[e], acc[i][k]);
+                for (int e = 0; e < 4; ++e) {
+                    if (kHow == kValues && x[i][e] == 0.f && !(fabsf(y[e]) <= kMaxF32))
+                        acc[i][k] += y[e];
+                    else if (kHow == kNone || (kHow == kZero ? x[i][e] != 0.f : !(x[i][e] < 0.f)))
+                        acc[i][k] = fmaf(x[i][e], y[e], acc[i][k]);
+                }
         }
     }
 }
@@ -205,12 +212,18 @@ __global__ void __launch_bounds__(kThreads) window_fwd_simt_kernel(const WindowA
             }
             l[i] = l[i] * alpha + sum16(sum);
             m[i] = mn;
+            if (alpha != 0.f) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) o[i][k] *= alpha;
+                for (int k = 0; k < D / 16; ++k) o[i][k] *= alpha;
+            } else {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    if (fabsf(o[i][k]) <= kMaxF32) o[i][k] = 0.f;  // (what is not finite stays)
+            }
         }
         put4(sp, s);
         __syncthreads();
-        apply_tile<D, kNegative>(whole || !odd, sp, sv, o);
+        apply_tile<D, kValues>(!odd, sp, sv, o);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

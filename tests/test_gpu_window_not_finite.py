@@ -72,6 +72,25 @@ def test_where_values_go(dtype, out_dtype, H, Hkv, d, n, layout, W, S, causal, w
     _check(q, k, v, v2, n, layout, W, S, causal, out_dtype)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("later", [False, True])
+def test_a_weight_that_underflows(later, d, dtype):
+    """A visible value that is not finite reaches the row although its weight, e^-400 and less, is 0 in float32: met before the
+    row's largest score and behind it."""
+    L, W, at, top = 400, 300, 150, 260
+    if later:
+        at, top = top, at
+    q, k, v = _inputs(1, 2, 1, L, d, dtype, seed=d)
+    q[:] = 1.0
+    k *= 2.0 ** -6
+    k[:, :, at] = -400 / math.sqrt(d)
+    k[:, :, top] = 400 / math.sqrt(d)
+    v2 = v.clone()
+    v2[:, :, at, 3], v2[:, :, at, 9], v2[:, :, at, 20] = math.inf, -math.inf, math.nan
+    _check(q, k, v, v2, 1, "contiguous", W, 0, True)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("what,times", [("sink", 12), ("all", 12), ("all NaN", 12), ("one hidden", 60)])
 def test_how_long_it_takes(what, times, d):
