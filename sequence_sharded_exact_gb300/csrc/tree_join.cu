@@ -256,13 +256,17 @@ cudaError_t launch_tree(const Cache& c, const Tree& t, cudaStream_t s)
         if (a.ctas > items * tiles) a.ctas = (int)(items * tiles);
         // With one item for most CTAs each takes one alone: an end, a start and the second launch saved count for more than
         // an even split (windows of 1024 rows: 16 sequences of 8 drafted tokens, 128 items on 152 CTAs, 30 us in place of 38
-        // over e4m3, 22 in place of 31 over bf16; one token each of 32 sequences, 256 items on 304, 32 in place of 38; of 4096
-        // rows, 63 in place of 71 and 81 in place of 87).  Below half as many items as CTAs the split wins, and where the CTAs
-        // without an item would do more than 8 tiles' work for each of the others (10 sequences of 8 tokens over e4m3, 80 items on
-        // 152: 1024 rows 29 in place of 33 us, 2048 rows 40 and 39, 4096 rows 61 and 52); on the CUDA cores more than one's
-        // (1024 rows, one token each of 76 sequences, 608 items on 608: 137 in place of 148 us; of 60, 480 items, 135 and 122).
+        // over e4m3, 22 in place of 31 over bf16; one token each of 38 sequences, 304 items on 304, 34 in place of 37).  Below half as
+        // many items as CTAs the split wins, and where the CTAs without an item would do more than 8 tiles' work for each of the
+        // others (10 sequences of 8 tokens over e4m3, 80 items on 152: 1024 rows 29 in place of 33 us); on the CUDA cores more
+        // than one's.
+        // The lengths are not known here, and with one long sequence among short ones its CTAs walk their items while the rest
+        // have finished: the more tiles, the more that costs, while what is saved stays 3 us.  304 items on 304 CTAs, alike
+        // and with one long sequence: 1024 rows, 11 tiles, 34 in place of 37 and 21 in place of 17; 2048, 19 tiles, 56
+        // in place of 59 and 32 in place of 17; 16K 355 in place of 358 and 187 in place of 30; on the CUDA cores, 608 items,
+        // 256 rows, 11 tiles, 47 in place of 51 and 27 in place of 25, 1024 rows 136 in place of 140 and 72 in place of 29.
         const long long spare = u.path == Path::kSimt ? 1 : 8;
-        a.whole = items <= a.ctas && 2 * items > a.ctas && tiles * (a.ctas - items) <= spare * a.ctas;
+        a.whole = tiles <= 12 && items <= a.ctas && 2 * items > a.ctas && tiles * (a.ctas - items) <= spare * a.ctas;
         if (a.whole) a.ctas = (int)items;
     }
     char* ws = static_cast<char*>(t.workspace);
