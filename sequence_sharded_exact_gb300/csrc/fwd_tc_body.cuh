@@ -331,6 +331,7 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, uint32_t sbase, u
                     // O of the previous tile must be complete before it is rescaled.
                     if (!mbar_wait(bar_o, (tcount - 1) & 1, ctl)) return;
                     tc_fence_after_sync();
+                    __syncwarp();
 #pragma unroll 1
                     for (int c4 = 0; c4 < kHd / 32; ++c4) {
                         uint32_t o[32];
@@ -390,6 +391,7 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, uint32_t sbase, u
 #pragma unroll 1
                 for (int c4 = 0; c4 < kHd / 32; ++c4) {
                     uint32_t o[32];
+                    __syncwarp();  // the lanes of rows that saw no key have gone ahead
                     tmem_ld_32x32b_x32(tO + c4 * 32, o);
                     tmem_ld_wait(o);
                     if (!any) continue;

@@ -906,6 +906,7 @@ __device__ __forceinline__ void softmax_role(const TreeArgs& a, uint32_t sbase, 
 #pragma unroll 1
             for (int c = col0; c < col0 + kCols; c += 32) {
                 uint32_t o[32];
+                __syncwarp();  // the lanes without a row have gone ahead
                 tmem_ld_32x32b_x32(tmem + lanes + kColO + (kNq == 2 ? (uint32_t)wg * 128u : 0u) + c, o);
                 tmem_ld_wait(o);
                 if constexpr (kNq == 1) {

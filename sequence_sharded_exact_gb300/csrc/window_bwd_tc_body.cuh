@@ -355,6 +355,7 @@ __device__ __forceinline__ void math_role(const BwdArgs& a, uint32_t sbase, uint
 #pragma unroll 1
                 for (int c = 0; c < kHd / 64; ++c) {
                     uint32_t x[32];
+                    __syncwarp();  // the lanes of keys behind the sequence have gone ahead
                     tmem_ld_32x32b_x32(tmem + lane_off + col + c * 32, x);
                     tmem_ld_wait(x);
                     const int at = w * (kHd / 2) + c * 32;

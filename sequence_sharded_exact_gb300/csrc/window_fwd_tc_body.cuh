@@ -403,6 +403,7 @@ __device__ __forceinline__ bool softmax_tile(const Seen& seen, const Place& x, b
     if (__any_sync(0xffffffffu, rescales && alpha != 1.0f)) {
         if (!mbar_wait(x.bar_o, (tcount - 1) & 1, ctl)) return false;  // O of the previous tile is complete
         tc_fence_after_sync();
+        __syncwarp();
 #pragma unroll 1
         for (int c4 = 0; c4 < kHd / 32; ++c4) {
             uint32_t o[32];
@@ -461,6 +462,7 @@ __device__ __forceinline__ bool softmax_role(const FwdArgs& a, uint32_t sbase, u
 #pragma unroll 1
         for (int c = 0; c < kHd; c += 32) {
             uint32_t o[32];
+            __syncwarp();  // the lanes of rows behind the sequence have gone ahead
             tmem_ld_32x32b_x32(tO + c, o);
             tmem_ld_wait(o);
             if (!in) continue;
