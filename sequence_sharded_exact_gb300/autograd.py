@@ -3,7 +3,8 @@
 ``ring_attention`` runs the library's forward and, when a gradient is needed, its backward: the
 same ``ring_attn_fwd`` / ``ring_attn_bwd`` entry points as ``fwd`` and ``bwd`` in the binding.  The
 forward saves its output and log-sum-exp; the backward recomputes the attention weights from them
-(nothing quadratic is stored).  Gradients come back in the dtype of the inputs.
+(nothing quadratic is stored).  Gradients come back in the dtype of the inputs; they have no graph of their
+own, and a second differentiation through them raises an error.
 
 With ``f32_out=True`` (bf16 inputs) the forward keeps its output in float32 for the backward
 (``ring_attn_fwd_f32out``, then ``ring_attn_f32_convert`` for the returned bf16 output) and the
@@ -11,9 +12,37 @@ backward takes D = rowsum(dout * out) from it (``ring_attn_bwd_f32out``) instead
 output: twice the saved output's memory, and gradients closer to the exact ones where a gradient is
 a short sum of large, cancelling terms (the first positions of a causal sequence).
 """
+import functools
+
 import torch
 
 from . import binding
+
+
+class _Refuse(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, *grads):
+        return tuple(g.view_as(g) for g in grads)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the attention's and the rotations' gradients come out of kernels: they cannot be differentiated again")
+
+
+def first_order(backward):
+    """A Function's backward whose gradients have no graph of their own.  Where one is asked for (create_graph=True) they may
+    still be used, but a differentiation through them raises an error in place of leaving those terms out.  (PyTorch's
+    once_differentiable does so only where the output's gradient needs one: not for that of a plain sum.)"""
+    @functools.wraps(backward)
+    def run(ctx, *douts):
+        with torch.no_grad():
+            grads = backward(ctx, *douts)
+        if not torch.is_grad_enabled():
+            return grads
+        marked = iter(_Refuse.apply(*(g.detach().requires_grad_() for g in grads if g is not None)))
+        return tuple(None if g is None else next(marked) for g in grads)
+
+    return run
 
 
 class _RingAttention(torch.autograd.Function):
@@ -37,6 +66,7 @@ class _RingAttention(torch.autograd.Function):
         return out
 
     @staticmethod
+    @first_order
     def backward(ctx, dout):
         q, k, v, saved, lse = ctx.saved_tensors
         n_shards, causal, layout, f32_out, window, sinks = ctx.cfg
@@ -76,7 +106,7 @@ class _QkNormRope(torch.autograd.Function):
         return q_out, k_out
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @first_order
     def backward(ctx, dq_out, dk_out):
         q, k, wq, wk, positions = ctx.saved_tensors
         dq, dk, dwq, dwk = binding.qk_norm_rope_bwd(q, k, _dense(wq.float()), _dense(wk.float()),
@@ -104,7 +134,7 @@ class _QkRopeAxes(torch.autograd.Function):
         return q_out, k_out
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @first_order
     def backward(ctx, dq_out, dk_out):
         positions, *saved = ctx.saved_tensors
         how = dict(ctx.cfg)

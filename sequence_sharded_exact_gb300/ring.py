@@ -27,6 +27,8 @@ import contextlib
 import torch
 import torch.distributed as dist
 
+from .autograd import first_order
+
 
 @contextlib.contextmanager
 def _range(name):
@@ -360,6 +362,7 @@ class _DistributedRingAttention(torch.autograd.Function):
         return out
 
     @staticmethod
+    @first_order
     def backward(ctx, dout):
         q, k, v, saved, lse = ctx.saved_tensors
         comm, groups, causal, layout, ops = ctx.cfg
