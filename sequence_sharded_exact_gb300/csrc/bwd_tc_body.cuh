@@ -531,7 +531,8 @@ done:
 
 // ------------------------------------------------------------------------------------------------
 // dQ warpgroup (warps 8-11, thread = head-dim index): dQ^T of each query tile out of TMEM, then
-// added into the float32 accumulator [heads][L][d] (at d = 64 by warps 8-9 only).  Its columns are freed as soon as they are
+// added into the float32 accumulator [heads][L][d].  All four warps reduce: at d = 64, where rows 64-127 repeat rows 0-63 (K lies
+// twice), warps 8-9 the query columns 0-63 and warps 10-11 the columns 64-127.  Its columns are freed as soon as they are
 // in registers, so the next dP^T does not wait for the reductions.
 // ------------------------------------------------------------------------------------------------
 __device__ __forceinline__ void red_add_f32(float* addr, float v)
@@ -687,8 +688,8 @@ __device__ __forceinline__ void producer_role(const BwdArgs& a, uint32_t sbase, 
 // Operand descriptors, as the low words of their shared-memory descriptors (query-tile operands
 // at stage 0): K-major views have LBO 16, N- or M-major views LBO = the distance between their
 // 64-element column blocks (16 KB everywhere here).  A stage or a k-step is a constant added.
-// At d = 64 the M-major K view's second block (rows 64-127 of dQ^T) is the V tile, which follows
-// K in shared memory: those rows are computed and never read.
+// At d = 64 the M-major K view's second block (rows 64-127 of dQ^T) is K's second copy, which follows the first in shared
+// memory: rows 64-127 are rows 0-63 again, and warps 10-11 read them for the query columns 64-127.
 struct BwdDesc {
     uint32_t k_k, v_k;    // K and V tiles, K-major (A of S^T and dP^T)
     uint32_t k_m;         // K tile, M-major (A of dQ^T = K^T dS^T)

@@ -23,6 +23,8 @@
 //     loaded twice, so that dQ^T's rows 64-127 repeat rows 0-63 and all four dQ warps have 64 columns each to add.
 //   * every wait is bounded; a wait that runs out sets the device status word and the CTA stops.
 // dP^T waits for dQ^T's read-out where they share Y; the order in which dQ's sums arrive varies.
+// P and dS go into the products as one bf16 value each (off by at most 2^-8, of either sign, so that it averages over a sum's
+// terms); scores, P, D and all sums are float32.  What the rounding leaves as a second value would be three more products beside five.
 //
 // Measured with what comes before and after it (window_aux.cu), 32 : 8 heads of 128: 32K tokens, window 4096 4.8 ms (1.06 PFLOP/s;
 // this kernel 4.3), 64K tokens 8.8 ms, window 1024 2.92 ms without sinks and 3.25 with 4 (whose tile is seen by all 512 query
@@ -391,8 +393,9 @@ done:
 
 // ------------------------------------------------------------------------------------------------
 // dQ warpgroup (warps 8-11, thread = head-dim index): dQ^T of each query tile out of TMEM, then
-// added into the float32 accumulator [heads][L][d] (at d = 64 by warps 8-9 only).  Its columns are freed as soon as they are
-// in registers, so the next dP^T does not wait for the reductions.
+// added into the float32 accumulator, [B H][T 128][d] in natural order.  All four warps reduce: at d = 64, where rows 64-127
+// repeat rows 0-63 (K lies twice), warps 8-9 the query columns 0-63 and warps 10-11 the columns 64-127.  Its columns are freed
+// as soon as they are in registers, so the next dP^T does not wait for the reductions.
 // ------------------------------------------------------------------------------------------------
 __device__ __forceinline__ void red_add_f32(float* addr, float v)
 {
@@ -540,8 +543,8 @@ __device__ __forceinline__ void producer_role(const BwdArgs& a, uint32_t sbase, 
 // Operand descriptors, as the low words of their shared-memory descriptors (query-tile operands
 // at stage 0): K-major views have LBO 16, N- or M-major views LBO = the distance between their
 // 64-element column blocks (16 KB everywhere here).  A stage or a k-step is a constant added.
-// At d = 64 the M-major K view's second block (rows 64-127 of dQ^T) is the V tile, which follows
-// K in shared memory: those rows are computed and never read.
+// At d = 64 the M-major K view's second block (rows 64-127 of dQ^T) is K's second copy, which follows the first in shared
+// memory: rows 64-127 are rows 0-63 again, and warps 10-11 read them for the query columns 64-127.
 struct BwdDesc {
     uint32_t k_k, v_k;    // K and V tiles, K-major (A of S^T and dP^T)
     uint32_t k_m;         // K tile, M-major (A of dQ^T = K^T dS^T)

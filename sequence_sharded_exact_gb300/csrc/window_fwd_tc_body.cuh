@@ -16,8 +16,10 @@
 //   * A weight of 0 does not hide a value that is not finite: the rows whose O comes out so are looked at again (rare), once
 //     the CTA's units are done: no wait of the pipeline, all of which have limits, then depends on how long that takes.
 //   * TMEM: S0 columns [0,128), S1 [128,256), O0 from 256, O1 from 384.
-// The weights go into P V as one bf16 value each; the row is divided by the sum of the unrounded weights, but for the
-// tile's largest, which counts as rounded: a row that one key dominates gets that key's value exactly.
+// The weights go into P V as one bf16 value each (off by at most 2^-8, of either sign, so that it averages over a row's keys; what
+// the rounding leaves as a second value would be a third product beside two, of a kernel that the products bound); the row is
+// divided by the sum of the unrounded weights, but for the tile's largest, which counts as rounded: a row that one key dominates gets
+// that key's value exactly.
 //
 // Measured, 64K tokens of 32 : 8 heads of 128: window 4096 2.55 to 2.69 ms (1590 to 1670 TFLOP/s over the visible pairs: the power
 // cap), window 1024 870 us (1250), window 128 370 us (two masked tiles a unit: the chain from a unit's first S to its output, 3.5 us
