@@ -22,9 +22,9 @@
 // that key's value exactly.
 //
 // Measured, 64K tokens of 32 : 8 heads of 128: window 4096 2.55 to 2.69 ms (1590 to 1670 TFLOP/s over the visible pairs: the power
-// cap), window 1024 870 us (1250), window 128 370 us (two masked tiles a unit: the chain from a unit's first S to its output, 3.5 us
+// cap), window 1024 870 us (1250), window 128 345 us (two masked tiles a unit: the chain from a unit's first S to its output, 3.5 us
 // beside its tiles, bounds it).  A tile of sinks costs what any tile does: window 1024 with 4 sinks 960 us.  Head dim 64, 16K
-// tokens of 2 x 16 heads, 512 on both sides: 219 us; dense 1010 TFLOP/s: issue slots, exponentials and products of 64
+// tokens of 2 x 16 heads, 512 on both sides: 223 us; dense 1010 TFLOP/s: issue slots, exponentials and products of 64
 // columns are each near half of the time (half of the exponentials left out: 5 % faster).
 #include <cuda_bf16.h>
 #include <math.h>
